@@ -13,7 +13,11 @@
  *   ppo_config.adv_mode), the Muon optimizer (ppo_muon_step,
  *   ppo_config.optimizer), the rollout-side policy step with sampling
  *   (ppo_policy_act), and the loss and gradient of the recurrent MinGRU
- *   policy (ppo_rnn_loss_grad).
+ *   policy (ppo_rnn_loss_grad);
+ * and the operators of a deeper recurrent trunk, forward and backward: layer
+ * norm (ppo_layernorm_*), the gated linear recurrence over any length and
+ * width (ppo_gated_scan_*), matrix products with bias, activation and residual
+ * (ppo_linear_*).
  *
  * Conventions shared by every entry point
  *  - Pointers named d_* are DEVICE pointers on the current CUDA device;
@@ -555,6 +559,120 @@ typedef int (*ppo_collective_fn)(void *user, int32_t op, void *d_buf, int64_t co
                                  cudaStream_t stream);
 ppo_status ppo_set_collective(ppo_ctx *ctx, int32_t world, int32_t rank, ppo_collective_fn fn,
                               void *user);
+
+/* ---- Operators of a pre-norm residual recurrent trunk --------------------------
+ * The pieces of a deeper recurrent policy than ppo_rnn_config's: blocks
+ *   x <- x + W_o . scan(W_p . layernorm(x) + b_p) + b_o,
+ *   x <- x + W_2 . act(W_1 . layernorm(x) + b_1) + b_2
+ * over the rows t*N + n of a rollout (or the N rows of one acting step).
+ * They take no context.  Matrices are row-major with a row pitch given in
+ * elements (ld*, at least the row's length); dtype is the type of the matrix
+ * arguments declared void*: sums, statistics, states, biases and the
+ * parameters' gradients are fp32 whatever it is, and each result is rounded
+ * to bf16 once.  NULL is allowed where "nullable" is said.  Outputs overlap
+ * no input unless said.  Lengths below 1 are PPO_ERR_INVALID.  NaN and
+ * infinities pass through as the formulas give them. */
+typedef enum { PPO_DTYPE_F32 = 0, PPO_DTYPE_BF16 = 1 } ppo_dtype;
+
+/* Layer norm of the M rows of d_x: mean and 1/sqrt(var + eps) of each row
+ * (var: the mean square deviation, from the deviations themselves),
+ *   y = (x - mean) * rstd * gamma + beta.
+ * d_gamma, d_beta fp32 [D], nullable (1 and 0).  d_stats fp32 [M][2], nullable:
+ * {mean, rstd}.  d_y may be d_x (same pitch). */
+ppo_status ppo_layernorm_forward(int32_t dtype, const void *d_x, int64_t ldx, int64_t M, int64_t D,
+                                 const float *d_gamma, const float *d_beta, float eps, void *d_y,
+                                 int64_t ldy, float *d_stats, cudaStream_t stream);
+/* Its backward pass, from d_stats of the forward call: with xh = (x - mean) *
+ * rstd and q = dy * gamma,
+ *   dx = rstd * (q - mean(q) - xh * mean(q * xh)) + dres,
+ *   dgamma = sum over rows of dy * xh,  dbeta = sum over rows of dy.
+ * d_dres (nullable) is the gradient that reaches x along the residual path.
+ * d_gamma, d_dgamma, d_dbeta nullable.  d_dx may be d_dy or d_dres (same
+ * pitch).  d_work: ppo_layernorm_backward_workspace_bytes; unused, and
+ * nullable, when d_dgamma and d_dbeta are NULL. */
+ppo_status ppo_layernorm_backward_workspace_bytes(int64_t M, int64_t D, size_t *bytes);
+ppo_status ppo_layernorm_backward(int32_t dtype, const void *d_dy, int64_t lddy, const void *d_x,
+                                  int64_t ldx, int64_t M, int64_t D, const float *d_gamma,
+                                  const float *d_stats, const void *d_dres, int64_t lddres,
+                                  void *d_dx, int64_t lddx, float *d_dgamma, float *d_dbeta,
+                                  void *d_work, size_t work_bytes, cudaStream_t stream);
+
+/* The gated linear recurrence of a MinGRU layer (see ppo_rnn_config) over T
+ * steps of N environments, H channels wide, from its pre-activations: row
+ * t*N + n of d_p holds pz (columns 0..H-1) and ph (columns H..2H-1),
+ *   z = sigmoid(pz),   h_t = (1 - z) * h_{t-1} + z * ph.
+ * The state entering step t is cleared where d_done[t-1][n] != 0, and the
+ * state entering step 0 where d_done0[n] != 0 (both nullable: never; NaN
+ * counts as done).  Pointers need only their elements' alignment here, so that
+ * one step of a rollout of odd width can be passed as it lies.  A cleared state does not reach the result, whatever it
+ * holds.  d_h0 fp32 [N][H], nullable (0).  Outputs: d_h, row t*N + n; d_hT
+ * fp32 [N][H], nullable: the state after the last step (may be d_h0, so that
+ * T = 1 advances a carried state by one acting step); d_carry nullable, kept
+ * for the backward pass: fp32 [ceil(T / PPO_SCAN_BLOCK)][N][H], the state
+ * entering steps 0, PPO_SCAN_BLOCK, 2 PPO_SCAN_BLOCK, .. (after clearing). */
+enum { PPO_SCAN_BLOCK = 128 };
+ppo_status ppo_gated_scan_forward(int32_t dtype, const void *d_p, int64_t ldp, const float *d_done,
+                                  const float *d_done0, const float *d_h0, int64_t T, int64_t N,
+                                  int64_t H, void *d_h, int64_t ldh, float *d_hT, float *d_carry,
+                                  cudaStream_t stream);
+/* Its backward pass: with g_t the gradient that reaches h_t (d_dh row t*N + n,
+ * plus d_dhT at the last step, nullable, plus what later steps pass back),
+ *   dph = g z,  dpz = g (ph - h_{t-1}) z (1 - z),  dL/dh_{t-1} += g (1 - z),
+ * the last cut where the state was cleared.  d_dp has d_p's layout; d_dh0
+ * fp32 [N][H], nullable (may be d_dhT).  The states are recomputed in fp32
+ * from d_carry. */
+ppo_status ppo_gated_scan_backward(int32_t dtype, const void *d_dh, int64_t lddh, const void *d_p,
+                                   int64_t ldp, const float *d_done, const float *d_done0,
+                                   const float *d_carry, const float *d_dhT, int64_t T, int64_t N,
+                                   int64_t H, void *d_dp, int64_t lddp, float *d_dh0,
+                                   cudaStream_t stream);
+
+/* Activations of ppo_linear_*: those of ppo_config.act, and
+ *   silu(x) = x sigmoid(x),
+ *   gelu(x) = 0.5 x (1 + tanh(sqrt(2/pi) (x + 0.044715 x^3))). */
+typedef enum {
+    PPO_ACT_NONE = -1, PPO_ACT_TANH = 0, PPO_ACT_RELU = 1, PPO_ACT_SILU = 2, PPO_ACT_GELU = 3
+} ppo_activation;
+
+/* Matrix product with its epilogue: x [M][K], W [N][K],
+ *   pre = x W^T + bias,   y = act(pre) + res.
+ * d_bias fp32 [N], d_res [M][N], d_pre [M][N] (an output) nullable.  d_y may
+ * be d_res (same pitch).  bf16 products run on the tensor cores with fp32
+ * accumulation; fp32 ones in fp32 on the CUDA cores.  d_work:
+ * ppo_linear_workspace_bytes of the same dtype, sizes and pitches (ldz: the
+ * pitch of the [M][N] gradient of ppo_linear_backward_*; a pitch <= 0 stands
+ * for the row's length).  Rows of bf16 operands that do not start on 16-byte
+ * boundaries (a pitch that is no multiple of 8) are copied there first, so the
+ * size covers the given pitches.  The caller zeroes the workspace once; it may
+ * serve any number of later calls in one stream's order.  Its first int32 is
+ * set nonzero if a bounded device wait of a call gave up (the outputs of that
+ * call are then unspecified): ppo_work_status synchronises `stream`, returns
+ * PPO_ERR_TIMEOUT if it is set, and clears it. */
+ppo_status ppo_linear_workspace_bytes(int32_t dtype, int64_t M, int64_t N, int64_t K, int64_t ldx,
+                                      int64_t ldw, int64_t ldz, size_t *bytes);
+ppo_status ppo_linear_forward(int32_t dtype, const void *d_x, int64_t ldx, const void *d_w,
+                              int64_t ldw, const float *d_bias, int32_t act, const void *d_res,
+                              int64_t ldres, int64_t M, int64_t N, int64_t K, void *d_y,
+                              int64_t ldy, void *d_pre, int64_t ldpre, void *d_work,
+                              size_t work_bytes, cudaStream_t stream);
+/* Gradient with respect to the input, from dz [M][N], the gradient with
+ * respect to pre:   dx = (dz W) * act'(pre_in) + res,   [M][K].
+ * d_pre_in [M][K] (nullable with act PPO_ACT_NONE) is the pre-activation that
+ * x came from, so that dx is the previous layer's dz; d_res [M][K], nullable,
+ * the gradient along a residual path.  d_dx may be d_res (same pitch). */
+ppo_status ppo_linear_backward_data(int32_t dtype, const void *d_dz, int64_t lddz, const void *d_w,
+                                    int64_t ldw, const void *d_pre_in, int64_t ldpre, int32_t act,
+                                    const void *d_res, int64_t ldres, int64_t M, int64_t N,
+                                    int64_t K, void *d_dx, int64_t lddx, void *d_work,
+                                    size_t work_bytes, cudaStream_t stream);
+/* Gradients with respect to the weight and the bias:
+ *   dW = dz^T x (fp32 [N][K], pitch K),   db = sum over rows of dz (fp32 [N], nullable);
+ * accumulate != 0 adds them to what d_dw and d_db hold. */
+ppo_status ppo_linear_backward_weight(int32_t dtype, const void *d_dz, int64_t lddz,
+                                      const void *d_x, int64_t ldx, int64_t M, int64_t N, int64_t K,
+                                      float *d_dw, float *d_db, int32_t accumulate, void *d_work,
+                                      size_t work_bytes, cudaStream_t stream);
+ppo_status ppo_work_status(void *d_work, cudaStream_t stream);
 
 /* ---- Inspection and failure handling ----------------------------------------
  * Step trace of the whole update ("Teaching Mario to speedrun", sec. 6 "The

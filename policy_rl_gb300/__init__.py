@@ -25,6 +25,10 @@ __all__ = [
     "ppo_update_host_async", "ppo_host_wait",
     "ppo_sync_status", "ppo_stage_name", "ppo_update_profile", "ppo_set_step_trace",
     "ppo_set_wait_limit", "ppo_set_collective", "TorchCollective", "RnnContext",
+    "ppo_layernorm_forward", "ppo_layernorm_backward_workspace_bytes", "ppo_layernorm_backward",
+    "ppo_gated_scan_forward", "ppo_gated_scan_backward", "ppo_scan_blocks",
+    "ppo_linear_workspace_bytes", "ppo_linear_forward", "ppo_linear_backward_data",
+    "ppo_linear_backward_weight", "ppo_work_status",
     "library_path",
 ]
 
@@ -224,6 +228,192 @@ class RnnContext:
             self.close()
         except Exception:
             pass
+
+
+# ---- operators of a recurrent trunk ---------------------------------------------
+# Matrices may be strided row by row (unit stride within a row); the other
+# arguments are contiguous fp32.  Results go to the tensors the caller passes.
+_DTYPES = None
+
+
+def _dtype(t) -> int:
+    global _DTYPES
+    if _DTYPES is None:
+        import torch
+        _DTYPES = {torch.float32: _abi.DTYPE_F32, torch.bfloat16: _abi.DTYPE_BF16}
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        raise ValueError(f"dtype must be float32 or bfloat16, got {t.dtype}")
+    return code
+
+
+def _mat(t, like, shape, name):
+    """(address, row pitch) of a matrix argument of like's dtype: the last
+    dimension is a row, the others flatten to rows of one pitch."""
+    if t is None:
+        return None, 0
+    if t.dtype != like.dtype or tuple(t.shape) != shape or not t.is_cuda:
+        raise ValueError(f"{name}: a CUDA tensor {shape} of {like.dtype} is wanted, got "
+                         f"{tuple(t.shape)} of {t.dtype} on {t.device}")
+    if t.is_contiguous():
+        return t.data_ptr(), shape[-1]
+    st = t.stride()
+    if (st[-1] != 1 and shape[-1] > 1) or st[-2] < shape[-1] or (
+            len(shape) == 3 and shape[0] > 1 and st[0] != shape[1] * st[1]):
+        raise ValueError(f"{name}: rows must be contiguous and of one pitch")
+    return t.data_ptr(), st[-2]
+
+
+def _vec(t, shape, name):
+    """Address of a contiguous fp32 argument."""
+    if t is None:
+        return None
+    if str(t.dtype) != "torch.float32" or tuple(t.shape) != shape or not t.is_cuda:
+        raise ValueError(f"{name}: a CUDA tensor {shape} of float32 is wanted, got "
+                         f"{tuple(t.shape)} of {t.dtype} on {t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: tensor must be contiguous")
+    return t.data_ptr()
+
+
+def _work_of(work):
+    if work is None:
+        return None, 0
+    if not work.is_cuda or not work.is_contiguous():
+        raise ValueError("work: a contiguous CUDA tensor is wanted")
+    return work.data_ptr(), work.numel() * work.element_size()
+
+
+def ppo_layernorm_forward(x, gamma, beta, y, stats=None, eps=1e-5, stream=None) -> None:
+    """y = layer norm of the rows of x [M, D] (see ppo.h); gamma, beta fp32 [D]
+    or None; stats fp32 [M, 2], kept for the backward pass."""
+    M, D = shape = tuple(x.shape)
+    px, ldx = _mat(x, x, shape, "x")
+    py, ldy = _mat(y, x, shape, "y")
+    _abi.check(_lib().ppo_layernorm_forward(
+        _dtype(x), px, ldx, M, D, _vec(gamma, (D,), "gamma"), _vec(beta, (D,), "beta"), eps, py,
+        ldy, _vec(stats, (M, 2), "stats"), _stream(stream)), "ppo_layernorm_forward")
+
+
+def ppo_layernorm_backward_workspace_bytes(M: int, D: int) -> int:
+    n = ctypes.c_size_t()
+    _abi.check(_lib().ppo_layernorm_backward_workspace_bytes(M, D, ctypes.byref(n)),
+               "ppo_layernorm_backward_workspace_bytes")
+    return n.value
+
+
+def ppo_layernorm_backward(dy, x, gamma, stats, dx, dgamma=None, dbeta=None, dres=None, work=None,
+                           stream=None) -> None:
+    """dx (+ dres, the residual path's gradient), dgamma, dbeta of the layer norm (see ppo.h)."""
+    M, D = shape = tuple(x.shape)
+    px, ldx = _mat(x, x, shape, "x")
+    pdy, lddy = _mat(dy, x, shape, "dy")
+    pr, ldr = _mat(dres, x, shape, "dres")
+    pdx, lddx = _mat(dx, x, shape, "dx")
+    pw, wb = _work_of(work)
+    _abi.check(_lib().ppo_layernorm_backward(
+        _dtype(x), pdy, lddy, px, ldx, M, D, _vec(gamma, (D,), "gamma"),
+        _vec(stats, (M, 2), "stats"), pr, ldr, pdx, lddx, _vec(dgamma, (D,), "dgamma"),
+        _vec(dbeta, (D,), "dbeta"), pw, wb, _stream(stream)), "ppo_layernorm_backward")
+
+
+def ppo_scan_blocks(T: int) -> int:
+    """Rows of the gated scan's carry: the states entering every 128th step."""
+    return -(-T // _abi.SCAN_BLOCK)
+
+
+def ppo_gated_scan_forward(p, h, h0=None, done=None, done0=None, hT=None, carry=None,
+                           stream=None) -> None:
+    """h [T, N, H] from the pre-activations p [T, N, 2H] (see ppo.h); h0, hT
+    fp32 [N, H], done fp32 [T, N], done0 fp32 [N], carry fp32
+    [ppo_scan_blocks(T), N, H].  hT may be h0."""
+    T, N, H = shape = tuple(h.shape)
+    pp, ldp = _mat(p, h, (T, N, 2 * H), "p")
+    ph, ldh = _mat(h, h, shape, "h")
+    _abi.check(_lib().ppo_gated_scan_forward(
+        _dtype(h), pp, ldp, _vec(done, (T, N), "done"), _vec(done0, (N,), "done0"),
+        _vec(h0, (N, H), "h0"), T, N, H, ph, ldh, _vec(hT, (N, H), "hT"),
+        _vec(carry, (ppo_scan_blocks(T), N, H), "carry"), _stream(stream)),
+        "ppo_gated_scan_forward")
+
+
+def ppo_gated_scan_backward(dh, p, carry, dp, done=None, done0=None, dhT=None, dh0=None,
+                            stream=None) -> None:
+    """dp [T, N, 2H] and dh0 from dh [T, N, H] and dhT (see ppo.h)."""
+    T, N, H = shape = tuple(dh.shape)
+    pd, ldd = _mat(dh, dh, shape, "dh")
+    pp, ldp = _mat(p, dh, (T, N, 2 * H), "p")
+    po, ldo = _mat(dp, dh, (T, N, 2 * H), "dp")
+    _abi.check(_lib().ppo_gated_scan_backward(
+        _dtype(dh), pd, ldd, pp, ldp, _vec(done, (T, N), "done"), _vec(done0, (N,), "done0"),
+        _vec(carry, (ppo_scan_blocks(T), N, H), "carry"), _vec(dhT, (N, H), "dhT"), T, N, H, po,
+        ldo, _vec(dh0, (N, H), "dh0"), _stream(stream)), "ppo_gated_scan_backward")
+
+
+def ppo_linear_workspace_bytes(M: int, N: int, K: int, dtype, ldx: int = 0, ldw: int = 0,
+                               ldz: int = 0) -> int:
+    """Bytes of workspace for the three products of x [M, K], w [N, K] and
+    dz [M, N] (allocate it zeroed; pitches only where the rows are strided)."""
+    import torch
+    code = {torch.float32: _abi.DTYPE_F32, torch.bfloat16: _abi.DTYPE_BF16}.get(dtype, -1)
+    n = ctypes.c_size_t()
+    _abi.check(_lib().ppo_linear_workspace_bytes(code, M, N, K, ldx, ldw, ldz, ctypes.byref(n)),
+               "ppo_linear_workspace_bytes")
+    return n.value
+
+
+def ppo_linear_forward(x, w, y, bias=None, act=_abi.ACT_NONE, res=None, pre=None, work=None,
+                       stream=None) -> None:
+    """y [M, N] = act(x w^T + bias) + res, x [M, K], w [N, K], bias fp32 [N];
+    pre [M, N] takes the pre-activation (see ppo.h)."""
+    M, K = tuple(x.shape)
+    N = w.shape[0]
+    px, ldx = _mat(x, x, (M, K), "x")
+    pw, ldw = _mat(w, x, (N, K), "w")
+    pr, ldr = _mat(res, x, (M, N), "res")
+    py, ldy = _mat(y, x, (M, N), "y")
+    pp, ldp = _mat(pre, x, (M, N), "pre")
+    pk, wb = _work_of(work)
+    _abi.check(_lib().ppo_linear_forward(
+        _dtype(x), px, ldx, pw, ldw, _vec(bias, (N,), "bias"), act, pr, ldr, M, N, K, py, ldy, pp,
+        ldp, pk, wb, _stream(stream)), "ppo_linear_forward")
+
+
+def ppo_linear_backward_data(dz, w, dx, pre=None, act=_abi.ACT_NONE, res=None, work=None,
+                             stream=None) -> None:
+    """dx [M, K] = (dz w) * act'(pre) + res; pre [M, K] is the pre-activation
+    that the layer's input came from (see ppo.h)."""
+    M, N = tuple(dz.shape)
+    K = w.shape[1]
+    pd, ldd = _mat(dz, dz, (M, N), "dz")
+    pw, ldw = _mat(w, dz, (N, K), "w")
+    pp, ldp = _mat(pre, dz, (M, K), "pre")
+    pr, ldr = _mat(res, dz, (M, K), "res")
+    po, ldo = _mat(dx, dz, (M, K), "dx")
+    pk, wb = _work_of(work)
+    _abi.check(_lib().ppo_linear_backward_data(
+        _dtype(dz), pd, ldd, pw, ldw, pp, ldp, act, pr, ldr, M, N, K, po, ldo, pk, wb,
+        _stream(stream)), "ppo_linear_backward_data")
+
+
+def ppo_linear_backward_weight(dz, x, dw, db=None, accumulate=False, work=None,
+                               stream=None) -> None:
+    """dw fp32 [N, K] = dz^T x and db fp32 [N] = column sums of dz, or their
+    sums with what dw and db hold (see ppo.h)."""
+    M, N = tuple(dz.shape)
+    K = x.shape[1]
+    pd, ldd = _mat(dz, dz, (M, N), "dz")
+    px, ldx = _mat(x, dz, (M, K), "x")
+    pk, wb = _work_of(work)
+    _abi.check(_lib().ppo_linear_backward_weight(
+        _dtype(dz), pd, ldd, px, ldx, M, N, K, _vec(dw, (N, K), "dw"), _vec(db, (N,), "db"),
+        1 if accumulate else 0, pk, wb, _stream(stream)), "ppo_linear_backward_weight")
+
+
+def ppo_work_status(work, stream=None) -> None:
+    """Synchronises the stream; raises PPO_ERR_TIMEOUT if a bounded device wait
+    of a ppo_linear_* call on this workspace gave up."""
+    _abi.check(_lib().ppo_work_status(_ptr(work), _stream(stream)), "ppo_work_status")
 
 
 # ---- context ------------------------------------------------------------------

@@ -24,8 +24,14 @@ SYMBOLS = (
     "ppo_rnn_destroy", "ppo_rnn_buffers", "ppo_rnn_update", "ppo_rnn_sync_status", "ppo_update",
     "ppo_update_host", "ppo_update_host_async", "ppo_host_wait", "ppo_stage_name",
     "ppo_update_profile", "ppo_sync_status", "ppo_set_collective", "ppo_set_step_trace",
-    "ppo_set_wait_limit",
+    "ppo_set_wait_limit", "ppo_layernorm_forward", "ppo_layernorm_backward_workspace_bytes",
+    "ppo_layernorm_backward", "ppo_gated_scan_forward", "ppo_gated_scan_backward",
+    "ppo_linear_workspace_bytes", "ppo_linear_forward", "ppo_linear_backward_data",
+    "ppo_linear_backward_weight", "ppo_work_status",
 )
+DTYPE_F32, DTYPE_BF16 = 0, 1
+ACT_NONE, ACT_TANH, ACT_RELU, ACT_SILU, ACT_GELU = -1, 0, 1, 2, 3
+SCAN_BLOCK = 128
 NUM_STAGES = 34
 NUM_KERNEL_STAGES = 25
 
@@ -145,6 +151,25 @@ def load(path: str = LIB_PATH):
         "ppo_set_collective": ([_P, i32, i32, COLLECTIVE_FN, _P], ctypes.c_int),
         "ppo_set_step_trace": ([_P, _P, _I64], ctypes.c_int),
         "ppo_set_wait_limit": ([_P, ctypes.c_uint64], ctypes.c_int),
+        "ppo_layernorm_forward": ([i32, _P, _I64, _I64, _I64, _P, _P, _F, _P, _I64, _P, _P],
+                                  ctypes.c_int),
+        "ppo_layernorm_backward_workspace_bytes": ([_I64, _I64, ctypes.POINTER(_SZ)],
+                                                   ctypes.c_int),
+        "ppo_layernorm_backward": ([i32, _P, _I64, _P, _I64, _I64, _I64, _P, _P, _P, _I64, _P,
+                                    _I64, _P, _P, _P, _SZ, _P], ctypes.c_int),
+        "ppo_gated_scan_forward": ([i32, _P, _I64, _P, _P, _P, _I64, _I64, _I64, _P, _I64, _P, _P,
+                                    _P], ctypes.c_int),
+        "ppo_gated_scan_backward": ([i32, _P, _I64, _P, _I64, _P, _P, _P, _P, _I64, _I64, _I64, _P,
+                                     _I64, _P, _P], ctypes.c_int),
+        "ppo_linear_workspace_bytes": ([i32, _I64, _I64, _I64, _I64, _I64, _I64,
+                                        ctypes.POINTER(_SZ)], ctypes.c_int),
+        "ppo_linear_forward": ([i32, _P, _I64, _P, _I64, _P, i32, _P, _I64, _I64, _I64, _I64, _P,
+                                _I64, _P, _I64, _P, _SZ, _P], ctypes.c_int),
+        "ppo_linear_backward_data": ([i32, _P, _I64, _P, _I64, _P, _I64, i32, _P, _I64, _I64, _I64,
+                                      _I64, _P, _I64, _P, _SZ, _P], ctypes.c_int),
+        "ppo_linear_backward_weight": ([i32, _P, _I64, _P, _I64, _I64, _I64, _I64, _P, _P, i32, _P,
+                                        _SZ, _P], ctypes.c_int),
+        "ppo_work_status": ([_P, _P], ctypes.c_int),
     }
     for name, (args, res) in sig.items():
         fn = getattr(L, name)

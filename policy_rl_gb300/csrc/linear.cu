@@ -1,0 +1,357 @@
+// linear.cu -- matrix products with bias, activation and residual: entry
+// points, the fp32 CUDA-core products, and what every product shares (the
+// epilogue of split products, column sums).
+//
+//   forward          y  = act(x W^T + b) + res          [M][N], sum over K
+//   backward data    dx = (dz W) act'(pre_in) + res     [M][K], sum over N
+//   backward weight  dW = dz^T x, db = sum_rows dz      [N][K], sum over M
+//
+// Each is out(i, j) = sum_r A(i, r) B(j, r) with A and B read through a row
+// and a reduction stride.  A product with too few output tiles for the GPU's
+// SMs is cut along the sum; the partial products are added in order by
+// finish_kernel, which then applies the epilogue, so that results do not
+// depend on timing.
+#include "linear.h"
+
+#include <algorithm>
+
+#include "ops.cuh"
+
+namespace ppo {
+namespace lin {
+namespace {
+
+using namespace ops;
+
+// ---- epilogue -------------------------------------------------------------------
+template <typename T>
+__device__ __forceinline__ float at(const void* p, int64_t i) {
+  return (float)static_cast<const T*>(p)[i];
+}
+
+// One output element from its finished sum.
+template <typename T>
+__device__ __forceinline__ void finish_one(const Epilogue& e, float v, int64_t i, int64_t j) {
+  if (e.mode == kWeight) {
+    float* d = static_cast<float*>(e.out) + i * e.ldo + j;
+    *d = e.accumulate ? *d + v : v;
+    return;
+  }
+  if (e.mode == kForward) {
+    if (e.bias) v += __ldg(e.bias + j);
+    if (e.pre) round_to(v, static_cast<T*>(e.pre)[i * e.ldpre + j]);
+    v = act_value<false>(e.act, v);
+  } else if (e.act != PPO_ACT_NONE) {
+    v *= act_slope<false>(e.act, at<T>(e.pre, i * e.ldpre + j));
+  }
+  if (e.res) v += at<T>(e.res, i * e.ldres + j);
+  round_to(v, static_cast<T*>(e.out)[i * e.ldo + j]);
+}
+
+// out = epilogue of the sum of the partial products, in split order
+constexpr int kFinishThreads = 256;
+template <typename T>
+__global__ void __launch_bounds__(kFinishThreads)
+finish_kernel(const float* __restrict__ part, int splits, int64_t I, int64_t J, const Epilogue e) {
+  pdl_wait();
+  const int64_t n = I * J;
+  for (int64_t k = (int64_t)blockIdx.x * kFinishThreads + threadIdx.x; k < n;
+       k += (int64_t)gridDim.x * kFinishThreads) {
+    float v = 0.f;
+#pragma unroll 4
+    for (int s = 0; s < splits; ++s) v += __ldcg(part + s * n + k);
+    finish_one<T>(e, v, k / J, k % J);
+  }
+}
+
+// ---- fp32 products ----------------------------------------------------------------
+// 64 x 64 output tiles, 16 of the sum at a time, 4 x 4 outputs a thread; the
+// next k-tile's loads are in flight while this one is multiplied.
+constexpr int kTile = 64, kStep = 16, kSimtThreads = 256;
+constexpr int kPer = kTile * kStep / kSimtThreads;
+
+// AR (BR): the reduction index is the contiguous one of A (B)
+template <typename T, bool AR, bool BR>
+__global__ void __launch_bounds__(kSimtThreads)
+simt_kernel(const Product g, const Epilogue e, float* __restrict__ part, int64_t r_per_split) {
+  __shared__ float As[kStep][kTile + 4], Bs[kStep][kTile + 4];
+  const int64_t i0 = (int64_t)blockIdx.y * kTile, j0 = (int64_t)blockIdx.x * kTile;
+  const int64_t r0 = (int64_t)blockIdx.z * r_per_split, r1 = min(g.R, r0 + r_per_split);
+  const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
+  const T* A = static_cast<const T*>(g.A);
+  const T* B = static_cast<const T*>(g.B);
+  float ra[kPer], rb[kPer];
+  auto fetch = [&](int64_t rb0) {
+#pragma unroll
+    for (int q = 0; q < kPer; ++q) {
+      const int idx = threadIdx.x + q * kSimtThreads;
+      const int ka = AR ? idx % kStep : idx / kTile, ia = AR ? idx / kStep : idx % kTile;
+      const int kb = BR ? idx % kStep : idx / kTile, jb = BR ? idx / kStep : idx % kTile;
+      ra[q] = rb0 + ka < r1 && i0 + ia < g.I ? (float)A[(i0 + ia) * g.sai + (rb0 + ka) * g.sar] : 0.f;
+      rb[q] = rb0 + kb < r1 && j0 + jb < g.J ? (float)B[(j0 + jb) * g.sbj + (rb0 + kb) * g.sbr] : 0.f;
+    }
+  };
+  float acc[4][4] = {};
+  fetch(r0);
+  for (int64_t r = r0; r < r1; r += kStep) {
+#pragma unroll
+    for (int q = 0; q < kPer; ++q) {
+      const int idx = threadIdx.x + q * kSimtThreads;
+      As[AR ? idx % kStep : idx / kTile][AR ? idx / kStep : idx % kTile] = ra[q];
+      Bs[BR ? idx % kStep : idx / kTile][BR ? idx / kStep : idx % kTile] = rb[q];
+    }
+    __syncthreads();
+    if (r + kStep < r1) fetch(r + kStep);
+#pragma unroll
+    for (int k = 0; k < kStep; ++k) {
+      const float4 a4 = *reinterpret_cast<const float4*>(&As[k][ty * 4]);
+      const float4 b4 = *reinterpret_cast<const float4*>(&Bs[k][tx * 4]);
+      const float a[4] = {a4.x, a4.y, a4.z, a4.w}, b[4] = {b4.x, b4.y, b4.z, b4.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(a[i], b[j], acc[i][j]);
+    }
+    __syncthreads();
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int64_t oi = i0 + ty * 4 + i, oj = j0 + tx * 4 + j;
+      if (oi >= g.I || oj >= g.J) continue;
+      if (part) part[(blockIdx.z * g.I + oi) * g.J + oj] = acc[i][j];
+      else finish_one<T>(e, acc[i][j], oi, oj);
+    }
+}
+
+// ---- column sums --------------------------------------------------------------------
+// db: a block sums kSumCols columns over a chunk of rows, its warps taking
+// every eighth row; the chunks are added by finish_kernel.
+constexpr int kSumThreads = 256, kSumCols = 32;
+template <typename T>
+__global__ void __launch_bounds__(kSumThreads)
+colsum_kernel(const void* a, int64_t ld, int64_t rows, int64_t cols, int64_t rows_per_chunk,
+              float* __restrict__ part) {
+  __shared__ float s[kSumThreads / kWarp][kWarp];
+  const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp;
+  const int64_t c = (int64_t)blockIdx.x * kSumCols + lane;
+  const int64_t r0 = (int64_t)blockIdx.y * rows_per_chunk, r1 = min(rows, r0 + rows_per_chunk);
+  float t = 0.f;
+  if (c < cols) {
+#pragma unroll 8
+    for (int64_t r = r0 + warp; r < r1; r += kSumThreads / kWarp) t += at<T>(a, r * ld + c);
+  }
+  s[warp][lane] = t;
+  __syncthreads();
+  if (warp == 0 && c < cols) {
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < kSumThreads / kWarp; ++w) v += s[w][lane];
+    part[blockIdx.y * cols + c] = v;
+  }
+}
+
+// ---- plan ---------------------------------------------------------------------------
+constexpr int kSms = 152;               // the plans are made for a whole GB300
+constexpr int64_t kMinSplitR = 128;     // of the sum per split at least
+constexpr int64_t kMaxSplits = 64;
+
+int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+int64_t simt_splits(int64_t I, int64_t J, int64_t R) {
+  const int64_t tiles = cdiv(I, kTile) * cdiv(J, kTile);
+  return std::max<int64_t>(1, std::min({(2 * kSms) / tiles, cdiv(R, kMinSplitR), kMaxSplits}));
+}
+int64_t sum_chunks(int64_t M, int64_t N) {
+  return std::max<int64_t>(1, std::min({cdiv(4 * kSms, cdiv(N, kSumCols)), cdiv(M, 64), (int64_t)256}));
+}
+size_t split_bytes(int64_t I, int64_t J, int64_t R) {
+  const int64_t s = simt_splits(I, J, R);
+  return s > 1 ? (size_t)(s * I * J) * 4 : 0;
+}
+
+template <typename T>
+cudaError_t launch_finish(const float* part, int64_t splits, int64_t I, int64_t J,
+                          const Epilogue& e, cudaStream_t st) {
+  const int64_t blocks = std::min<int64_t>(cdiv(I * J, kFinishThreads), 8 * kSms);
+  return launch_pdl(finish_kernel<T>, dim3((unsigned)blocks), dim3(kFinishThreads), 0, st, part,
+                    (int)splits, I, J, e);
+}
+
+template <typename T>
+cudaError_t simt_product(const Product& g, const Epilogue& e, float* part, cudaStream_t st) {
+  const int64_t splits = simt_splits(g.I, g.J, g.R);
+  const int64_t per = cdiv(cdiv(g.R, splits), kStep) * kStep;
+  const int64_t used = cdiv(g.R, per);
+  if (cdiv(g.I, kTile) > 65535) return cudaErrorInvalidValue;
+  const dim3 grid((unsigned)cdiv(g.J, kTile), (unsigned)cdiv(g.I, kTile), (unsigned)used);
+  float* pp = used > 1 ? part : nullptr;
+  const bool ar = g.sar == 1, br = g.sbr == 1;
+  if (ar && br) simt_kernel<T, true, true><<<grid, kSimtThreads, 0, st>>>(g, e, pp, per);
+  else if (ar) simt_kernel<T, true, false><<<grid, kSimtThreads, 0, st>>>(g, e, pp, per);
+  else simt_kernel<T, false, false><<<grid, kSimtThreads, 0, st>>>(g, e, pp, per);
+  const cudaError_t err = cudaGetLastError();
+  if (err != cudaSuccess || used == 1) return err;
+  return launch_finish<T>(pp, used, g.I, g.J, e, st);
+}
+
+cudaError_t product(int32_t dtype, const Product& g, const Epilogue& e, float* part,
+                    cudaStream_t st) {
+  return dtype == PPO_DTYPE_F32 ? simt_product<float>(g, e, part, st)
+                                : simt_product<__nv_bfloat16>(g, e, part, st);
+}
+
+template <typename T>
+cudaError_t column_sums(const void* dz, int64_t ld, int64_t M, int64_t N, float* db,
+                        int accumulate, float* part, cudaStream_t st) {
+  const int64_t chunks = sum_chunks(M, N), per = cdiv(M, chunks), used = cdiv(M, per);
+  const dim3 grid((unsigned)cdiv(N, kSumCols), (unsigned)used);
+  colsum_kernel<T><<<grid, kSumThreads, 0, st>>>(dz, ld, M, N, per, part);
+  const cudaError_t err = cudaGetLastError();
+  if (err != cudaSuccess) return err;
+  Epilogue e{};
+  e.mode = kWeight;
+  e.out = db;
+  e.ldo = N;
+  e.accumulate = accumulate;
+  return launch_finish<T>(part, used, 1, N, e, st);
+}
+
+bool sizes_ok(int64_t M, int64_t N, int64_t K) {
+  constexpr int64_t top = 1ll << 31;
+  return M >= 1 && N >= 1 && K >= 1 && M < top && N < top && K < top && M <= (1ll << 40) / N &&
+         M <= (1ll << 40) / K && N <= (1ll << 40) / K;
+}
+
+}  // namespace
+}  // namespace lin
+}  // namespace ppo
+
+using namespace ppo;
+using ppo::ops::al16;
+
+namespace {
+
+constexpr size_t kCtrl = 256;   // the error word and its padding
+
+ppo_status checked(std::initializer_list<const void*> ptrs, const void* work, size_t work_bytes,
+                   size_t need) {
+  for (const void* p : ptrs)
+    if (!al16(p)) return PPO_ERR_ALIGN;
+  if (!work || work_bytes < need) return PPO_ERR_INVALID;
+  if (!al16(work)) return PPO_ERR_ALIGN;
+  return ops::num_sms() > 0 ? PPO_OK : PPO_ERR_CUDA;
+}
+ppo_status status_of(cudaError_t e) { return e == cudaSuccess ? PPO_OK : PPO_ERR_CUDA; }
+float* parts(void* work) { return reinterpret_cast<float*>(static_cast<char*>(work) + kCtrl); }
+
+}  // namespace
+
+extern "C" {
+
+ppo_status ppo_linear_workspace_bytes(int32_t dtype, int64_t M, int64_t N, int64_t K, int64_t ldx,
+                                      int64_t ldw, int64_t ldz, size_t* bytes) {
+  if (!bytes || !ops::dtype_ok(dtype) || !lin::sizes_ok(M, N, K)) return PPO_ERR_INVALID;
+  (void)ldx;
+  (void)ldw;
+  (void)ldz;
+  const size_t sums = (size_t)(lin::sum_chunks(M, N) * N) * 4;
+  *bytes = kCtrl + std::max({lin::split_bytes(M, N, K), lin::split_bytes(M, K, N),
+                             lin::split_bytes(N, K, M), sums});
+  return PPO_OK;
+}
+
+ppo_status ppo_linear_forward(int32_t dtype, const void* x, int64_t ldx, const void* w, int64_t ldw,
+                              const float* bias, int32_t act, const void* res, int64_t ldres,
+                              int64_t M, int64_t N, int64_t K, void* y, int64_t ldy, void* pre,
+                              int64_t ldpre, void* work, size_t work_bytes, cudaStream_t st) {
+  size_t need = 0;
+  if (!x || !w || !y || !ops::act_ok(act)) return PPO_ERR_INVALID;
+  if (ppo_linear_workspace_bytes(dtype, M, N, K, ldx, ldw, 0, &need) != PPO_OK ||
+      !ops::extent_ok(M, ldx, K) || !ops::extent_ok(N, ldw, K) || !ops::extent_ok(M, ldy, N) ||
+      (res && !ops::extent_ok(M, ldres, N)) || (pre && !ops::extent_ok(M, ldpre, N)) ||
+      (y == res && ldy != ldres))
+    return PPO_ERR_INVALID;
+  const ppo_status s = checked({x, w, bias, res, y, pre}, work, work_bytes, need);
+  if (s != PPO_OK) return s;
+  const lin::Product g{x, ldx, 1, w, ldw, 1, M, N, K};
+  lin::Epilogue e{};
+  e.mode = lin::kForward;
+  e.act = act;
+  e.bias = bias;
+  e.res = res;
+  e.ldres = ldres;
+  e.pre = pre;
+  e.ldpre = ldpre;
+  e.out = y;
+  e.ldo = ldy;
+  return status_of(lin::product(dtype, g, e, parts(work), st));
+}
+
+ppo_status ppo_linear_backward_data(int32_t dtype, const void* dz, int64_t lddz, const void* w,
+                                    int64_t ldw, const void* pre_in, int64_t ldpre, int32_t act,
+                                    const void* res, int64_t ldres, int64_t M, int64_t N,
+                                    int64_t K, void* dx, int64_t lddx, void* work,
+                                    size_t work_bytes, cudaStream_t st) {
+  size_t need = 0;
+  if (!dz || !w || !dx || !ops::act_ok(act) || (act != PPO_ACT_NONE && !pre_in))
+    return PPO_ERR_INVALID;
+  if (ppo_linear_workspace_bytes(dtype, M, N, K, 0, ldw, lddz, &need) != PPO_OK ||
+      !ops::extent_ok(M, lddz, N) || !ops::extent_ok(N, ldw, K) || !ops::extent_ok(M, lddx, K) ||
+      (res && !ops::extent_ok(M, ldres, K)) ||
+      (act != PPO_ACT_NONE && !ops::extent_ok(M, ldpre, K)) || (dx == res && lddx != ldres))
+    return PPO_ERR_INVALID;
+  const ppo_status s = checked({dz, w, pre_in, res, dx}, work, work_bytes, need);
+  if (s != PPO_OK) return s;
+  const lin::Product g{dz, lddz, 1, w, 1, ldw, M, K, N};
+  lin::Epilogue e{};
+  e.mode = lin::kData;
+  e.act = act;
+  e.pre = const_cast<void*>(pre_in);
+  e.ldpre = ldpre;
+  e.res = res;
+  e.ldres = ldres;
+  e.out = dx;
+  e.ldo = lddx;
+  return status_of(lin::product(dtype, g, e, parts(work), st));
+}
+
+ppo_status ppo_linear_backward_weight(int32_t dtype, const void* dz, int64_t lddz, const void* x,
+                                      int64_t ldx, int64_t M, int64_t N, int64_t K, float* dw,
+                                      float* db, int32_t accumulate, void* work,
+                                      size_t work_bytes, cudaStream_t st) {
+  size_t need = 0;
+  if (!dz || !x || !dw) return PPO_ERR_INVALID;
+  if (ppo_linear_workspace_bytes(dtype, M, N, K, ldx, 0, lddz, &need) != PPO_OK ||
+      !ops::extent_ok(M, lddz, N) || !ops::extent_ok(M, ldx, K))
+    return PPO_ERR_INVALID;
+  const ppo_status s = checked({dz, x, dw, db}, work, work_bytes, need);
+  if (s != PPO_OK) return s;
+  const lin::Product g{dz, 1, lddz, x, 1, ldx, N, K, M};
+  lin::Epilogue e{};
+  e.mode = lin::kWeight;
+  e.out = dw;
+  e.ldo = K;
+  e.accumulate = accumulate != 0;
+  cudaError_t err = lin::product(dtype, g, e, parts(work), st);
+  if (err == cudaSuccess && db)
+    err = dtype == PPO_DTYPE_F32
+              ? lin::column_sums<float>(dz, lddz, M, N, db, e.accumulate, parts(work), st)
+              : lin::column_sums<__nv_bfloat16>(dz, lddz, M, N, db, e.accumulate, parts(work), st);
+  return status_of(err);
+}
+
+ppo_status ppo_work_status(void* work, cudaStream_t st) {
+  if (!work) return PPO_ERR_INVALID;
+  if (!al16(work)) return PPO_ERR_ALIGN;
+  int32_t word = 0;
+  if (cudaMemcpyAsync(&word, work, sizeof(word), cudaMemcpyDeviceToHost, st) != cudaSuccess ||
+      cudaStreamSynchronize(st) != cudaSuccess)
+    return PPO_ERR_CUDA;
+  if (word == 0) return PPO_OK;
+  if (cudaMemsetAsync(work, 0, sizeof(word), st) != cudaSuccess) return PPO_ERR_CUDA;
+  return PPO_ERR_TIMEOUT;
+}
+
+}  // extern "C"
