@@ -7,7 +7,8 @@
 //   backward weight  dW = dz^T x, db = sum_rows dz      [N][K], sum over M
 //
 // Each is out(i, j) = sum_r A(i, r) B(j, r) with A and B read through a row
-// and a reduction stride.  A product with too few output tiles for the GPU's
+// and a reduction stride; bf16 products run on the tensor cores (linear_tc.cu),
+// fp32 ones here, so that every product and sum keeps fp32's digits.  A product with too few output tiles for the GPU's
 // SMs is cut along the sum; the partial products are added in order by
 // finish_kernel, which then applies the epilogue, so that results do not
 // depend on timing.
@@ -52,15 +53,18 @@ __device__ __forceinline__ void finish_one(const Epilogue& e, float v, int64_t i
 constexpr int kFinishThreads = 256;
 template <typename T>
 __global__ void __launch_bounds__(kFinishThreads)
-finish_kernel(const float* __restrict__ part, int splits, int64_t I, int64_t J, const Epilogue e) {
+finish_kernel(const float* __restrict__ part, int splits, int64_t I, int64_t J, int64_t ldp,
+              const Epilogue e) {
   pdl_wait();
-  const int64_t n = I * J;
+  const int64_t n = I * ldp;
   for (int64_t k = (int64_t)blockIdx.x * kFinishThreads + threadIdx.x; k < n;
        k += (int64_t)gridDim.x * kFinishThreads) {
+    const int64_t i = k / ldp, j = k - i * ldp;
+    if (j >= J) continue;
     float v = 0.f;
 #pragma unroll 4
     for (int s = 0; s < splits; ++s) v += __ldcg(part + s * n + k);
-    finish_one<T>(e, v, k / J, k % J);
+    finish_one<T>(e, v, i, j);
   }
 }
 
@@ -172,11 +176,11 @@ size_t split_bytes(int64_t I, int64_t J, int64_t R) {
 }
 
 template <typename T>
-cudaError_t launch_finish(const float* part, int64_t splits, int64_t I, int64_t J,
+cudaError_t launch_finish(const float* part, int64_t splits, int64_t I, int64_t J, int64_t ldp,
                           const Epilogue& e, cudaStream_t st) {
-  const int64_t blocks = std::min<int64_t>(cdiv(I * J, kFinishThreads), 8 * kSms);
+  const int64_t blocks = std::min<int64_t>(cdiv(I * ldp, kFinishThreads), 8 * kSms);
   return launch_pdl(finish_kernel<T>, dim3((unsigned)blocks), dim3(kFinishThreads), 0, st, part,
-                    (int)splits, I, J, e);
+                    (int)splits, I, J, ldp, e);
 }
 
 template <typename T>
@@ -193,14 +197,62 @@ cudaError_t simt_product(const Product& g, const Epilogue& e, float* part, cudaS
   else simt_kernel<T, false, false><<<grid, kSimtThreads, 0, st>>>(g, e, pp, per);
   const cudaError_t err = cudaGetLastError();
   if (err != cudaSuccess || used == 1) return err;
-  return launch_finish<T>(pp, used, g.I, g.J, e, st);
+  return launch_finish<T>(pp, used, g.I, g.J, g.J, e, st);
 }
 
-cudaError_t product(int32_t dtype, const Product& g, const Epilogue& e, float* part,
-                    cudaStream_t st) {
-  return dtype == PPO_DTYPE_F32 ? simt_product<float>(g, e, part, st)
-                                : simt_product<__nv_bfloat16>(g, e, part, st);
+// ---- bf16 operands on 16-byte rows ---------------------------------------------------
+// TMA reads rows that start on 16-byte boundaries: others are copied once, with
+// a pitch rounded up to 8 elements.
+int64_t pitch8(int64_t cols) { return (cols + 7) / 8 * 8; }
+size_t packed_bytes(int64_t rows, int64_t cols, int64_t ld) {
+  if (ld <= 0) ld = cols;
+  return ld % 8 ? (size_t)(rows * pitch8(cols) * 2 + 255) / 256 * 256 : 0;
 }
+constexpr int kPackThreads = 256;
+__global__ void __launch_bounds__(kPackThreads)
+pack_rows_kernel(const __nv_bfloat16* __restrict__ src, int64_t ld, int64_t rows, int64_t cols,
+                 int64_t pitch, uint4* __restrict__ dst) {
+  const int64_t n = rows * (pitch / 8);
+  for (int64_t k = (int64_t)blockIdx.x * kPackThreads + threadIdx.x; k < n;
+       k += (int64_t)gridDim.x * kPackThreads) {
+    const int64_t r = k / (pitch / 8), c = (k - r * (pitch / 8)) * 8;
+    float f[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = c + i < cols ? (float)src[r * ld + c + i] : 0.f;
+    dst[k] = from_f32<__nv_bfloat16, 8>(f);
+  }
+}
+// the operand itself, or its copy in the workspace (advanced past it)
+cudaError_t on_16_bytes(const void*& a, int64_t& ld, int64_t rows, int64_t cols, char*& work,
+                        cudaStream_t st) {
+  if (ld % 8 == 0) return cudaSuccess;
+  const int64_t pitch = pitch8(cols);
+  const int64_t blocks = std::min<int64_t>(cdiv(rows * (pitch / 8), kPackThreads), 16 * kSms);
+  pack_rows_kernel<<<(unsigned)blocks, kPackThreads, 0, st>>>(
+      static_cast<const __nv_bfloat16*>(a), ld, rows, cols, pitch, reinterpret_cast<uint4*>(work));
+  a = work;
+  ld = pitch;
+  work += (rows * pitch * 2 + 255) / 256 * 256;
+  return cudaGetLastError();
+}
+
+size_t tc_part_bytes(int64_t I, int64_t J, int64_t R, bool must_split) {
+  const TcPlan p = tc_plan(I, J, R, must_split);
+  return p.splits > 1 || must_split ? (size_t)p.splits * I * ((J + 3) / 4 * 4) * 4 : 0;
+}
+
+cudaError_t tc_run(const Product& g, const Epilogue& e, char* work, int* err, cudaStream_t st) {
+  if (!tc_fits(g)) return cudaErrorInvalidValue;
+  // a gradient that is added to, or whose rows TMA cannot store, is finished from partials
+  const bool must = e.mode == kWeight && (e.accumulate || g.J % 4);
+  const TcPlan plan = tc_plan(g.I, g.J, g.R, must);
+  const bool split = plan.splits > 1 || must;
+  float* part = split ? reinterpret_cast<float*>(work) : nullptr;
+  const cudaError_t x = tc_product(g, e, plan, part, err, num_sms(), st);
+  if (x != cudaSuccess || !split) return x;
+  return launch_finish<__nv_bfloat16>(part, plan.splits, g.I, g.J, (g.J + 3) / 4 * 4, e, st);
+}
+
 
 template <typename T>
 cudaError_t column_sums(const void* dz, int64_t ld, int64_t M, int64_t N, float* db,
@@ -215,7 +267,7 @@ cudaError_t column_sums(const void* dz, int64_t ld, int64_t M, int64_t N, float*
   e.out = db;
   e.ldo = N;
   e.accumulate = accumulate;
-  return launch_finish<T>(part, used, 1, N, e, st);
+  return launch_finish<T>(part, used, 1, N, N, e, st);
 }
 
 bool sizes_ok(int64_t M, int64_t N, int64_t K) {
@@ -244,6 +296,27 @@ ppo_status checked(std::initializer_list<const void*> ptrs, const void* work, si
   return ops::num_sms() > 0 ? PPO_OK : PPO_ERR_CUDA;
 }
 ppo_status status_of(cudaError_t e) { return e == cudaSuccess ? PPO_OK : PPO_ERR_CUDA; }
+// Workspace of one direction: the copies of its two operands (pitches lda,
+// ldb) and the partial products or column sums behind them.
+size_t need(int32_t dtype, int mode, int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb) {
+  const size_t sums = mode == lin::kWeight ? (size_t)(lin::sum_chunks(M, N) * N) * 4 : 0;
+  if (dtype == PPO_DTYPE_F32) {
+    const size_t part = mode == lin::kForward ? lin::split_bytes(M, N, K)
+                        : mode == lin::kData  ? lin::split_bytes(M, K, N)
+                                              : lin::split_bytes(N, K, M);
+    return kCtrl + std::max(part, sums);
+  }
+  switch (mode) {
+    case lin::kForward:
+      return kCtrl + lin::packed_bytes(M, K, lda) + lin::packed_bytes(N, K, ldb) +
+             lin::tc_part_bytes(M, N, K, false);
+    case lin::kData:
+      return kCtrl + lin::packed_bytes(M, N, lda) + lin::packed_bytes(N, K, ldb) +
+             lin::tc_part_bytes(M, K, N, false);
+  }
+  return kCtrl + lin::packed_bytes(M, N, lda) + lin::packed_bytes(M, K, ldb) +
+         std::max({lin::tc_part_bytes(N, K, M, false), lin::tc_part_bytes(N, K, M, true), sums});
+}
 float* parts(void* work) { return reinterpret_cast<float*>(static_cast<char*>(work) + kCtrl); }
 
 }  // namespace
@@ -253,12 +326,9 @@ extern "C" {
 ppo_status ppo_linear_workspace_bytes(int32_t dtype, int64_t M, int64_t N, int64_t K, int64_t ldx,
                                       int64_t ldw, int64_t ldz, size_t* bytes) {
   if (!bytes || !ops::dtype_ok(dtype) || !lin::sizes_ok(M, N, K)) return PPO_ERR_INVALID;
-  (void)ldx;
-  (void)ldw;
-  (void)ldz;
-  const size_t sums = (size_t)(lin::sum_chunks(M, N) * N) * 4;
-  *bytes = kCtrl + std::max({lin::split_bytes(M, N, K), lin::split_bytes(M, K, N),
-                             lin::split_bytes(N, K, M), sums});
+  *bytes = std::max({need(dtype, lin::kForward, M, N, K, ldx, ldw),
+                     need(dtype, lin::kData, M, N, K, ldz, ldw),
+                     need(dtype, lin::kWeight, M, N, K, ldz, ldx)});
   return PPO_OK;
 }
 
@@ -266,16 +336,14 @@ ppo_status ppo_linear_forward(int32_t dtype, const void* x, int64_t ldx, const v
                               const float* bias, int32_t act, const void* res, int64_t ldres,
                               int64_t M, int64_t N, int64_t K, void* y, int64_t ldy, void* pre,
                               int64_t ldpre, void* work, size_t work_bytes, cudaStream_t st) {
-  size_t need = 0;
   if (!x || !w || !y || !ops::act_ok(act)) return PPO_ERR_INVALID;
-  if (ppo_linear_workspace_bytes(dtype, M, N, K, ldx, ldw, 0, &need) != PPO_OK ||
-      !ops::extent_ok(M, ldx, K) || !ops::extent_ok(N, ldw, K) || !ops::extent_ok(M, ldy, N) ||
+  if (!ops::dtype_ok(dtype) || !lin::sizes_ok(M, N, K) || !ops::extent_ok(M, ldx, K) || !ops::extent_ok(N, ldw, K) || !ops::extent_ok(M, ldy, N) ||
       (res && !ops::extent_ok(M, ldres, N)) || (pre && !ops::extent_ok(M, ldpre, N)) ||
       (y == res && ldy != ldres))
     return PPO_ERR_INVALID;
-  const ppo_status s = checked({x, w, bias, res, y, pre}, work, work_bytes, need);
+  const ppo_status s = checked({x, w, bias, res, y, pre}, work, work_bytes,
+                               need(dtype, lin::kForward, M, N, K, ldx, ldw));
   if (s != PPO_OK) return s;
-  const lin::Product g{x, ldx, 1, w, ldw, 1, M, N, K};
   lin::Epilogue e{};
   e.mode = lin::kForward;
   e.act = act;
@@ -286,7 +354,14 @@ ppo_status ppo_linear_forward(int32_t dtype, const void* x, int64_t ldx, const v
   e.ldpre = ldpre;
   e.out = y;
   e.ldo = ldy;
-  return status_of(lin::product(dtype, g, e, parts(work), st));
+  if (dtype == PPO_DTYPE_F32)
+    return status_of(lin::simt_product<float>({x, ldx, 1, w, ldw, 1, M, N, K}, e, parts(work), st));
+  char* free = reinterpret_cast<char*>(parts(work));
+  cudaError_t err = lin::on_16_bytes(x, ldx, M, K, free, st);
+  if (err == cudaSuccess) err = lin::on_16_bytes(w, ldw, N, K, free, st);
+  if (err == cudaSuccess)
+    err = lin::tc_run({x, ldx, 1, w, ldw, 1, M, N, K}, e, free, static_cast<int*>(work), st);
+  return status_of(err);
 }
 
 ppo_status ppo_linear_backward_data(int32_t dtype, const void* dz, int64_t lddz, const void* w,
@@ -294,17 +369,15 @@ ppo_status ppo_linear_backward_data(int32_t dtype, const void* dz, int64_t lddz,
                                     const void* res, int64_t ldres, int64_t M, int64_t N,
                                     int64_t K, void* dx, int64_t lddx, void* work,
                                     size_t work_bytes, cudaStream_t st) {
-  size_t need = 0;
   if (!dz || !w || !dx || !ops::act_ok(act) || (act != PPO_ACT_NONE && !pre_in))
     return PPO_ERR_INVALID;
-  if (ppo_linear_workspace_bytes(dtype, M, N, K, 0, ldw, lddz, &need) != PPO_OK ||
-      !ops::extent_ok(M, lddz, N) || !ops::extent_ok(N, ldw, K) || !ops::extent_ok(M, lddx, K) ||
+  if (!ops::dtype_ok(dtype) || !lin::sizes_ok(M, N, K) || !ops::extent_ok(M, lddz, N) || !ops::extent_ok(N, ldw, K) || !ops::extent_ok(M, lddx, K) ||
       (res && !ops::extent_ok(M, ldres, K)) ||
       (act != PPO_ACT_NONE && !ops::extent_ok(M, ldpre, K)) || (dx == res && lddx != ldres))
     return PPO_ERR_INVALID;
-  const ppo_status s = checked({dz, w, pre_in, res, dx}, work, work_bytes, need);
+  const ppo_status s = checked({dz, w, pre_in, res, dx}, work, work_bytes,
+                               need(dtype, lin::kData, M, N, K, lddz, ldw));
   if (s != PPO_OK) return s;
-  const lin::Product g{dz, lddz, 1, w, 1, ldw, M, K, N};
   lin::Epilogue e{};
   e.mode = lin::kData;
   e.act = act;
@@ -314,31 +387,46 @@ ppo_status ppo_linear_backward_data(int32_t dtype, const void* dz, int64_t lddz,
   e.ldres = ldres;
   e.out = dx;
   e.ldo = lddx;
-  return status_of(lin::product(dtype, g, e, parts(work), st));
+  if (dtype == PPO_DTYPE_F32)
+    return status_of(lin::simt_product<float>({dz, lddz, 1, w, 1, ldw, M, K, N}, e, parts(work), st));
+  char* free = reinterpret_cast<char*>(parts(work));
+  cudaError_t err = lin::on_16_bytes(dz, lddz, M, N, free, st);
+  if (err == cudaSuccess) err = lin::on_16_bytes(w, ldw, N, K, free, st);
+  if (err == cudaSuccess)
+    err = lin::tc_run({dz, lddz, 1, w, 1, ldw, M, K, N}, e, free, static_cast<int*>(work), st);
+  return status_of(err);
 }
 
 ppo_status ppo_linear_backward_weight(int32_t dtype, const void* dz, int64_t lddz, const void* x,
                                       int64_t ldx, int64_t M, int64_t N, int64_t K, float* dw,
                                       float* db, int32_t accumulate, void* work,
                                       size_t work_bytes, cudaStream_t st) {
-  size_t need = 0;
   if (!dz || !x || !dw) return PPO_ERR_INVALID;
-  if (ppo_linear_workspace_bytes(dtype, M, N, K, ldx, 0, lddz, &need) != PPO_OK ||
-      !ops::extent_ok(M, lddz, N) || !ops::extent_ok(M, ldx, K))
+  if (!ops::dtype_ok(dtype) || !lin::sizes_ok(M, N, K) || !ops::extent_ok(M, lddz, N) || !ops::extent_ok(M, ldx, K))
     return PPO_ERR_INVALID;
-  const ppo_status s = checked({dz, x, dw, db}, work, work_bytes, need);
+  const ppo_status s = checked({dz, x, dw, db}, work, work_bytes,
+                               need(dtype, lin::kWeight, M, N, K, lddz, ldx));
   if (s != PPO_OK) return s;
-  const lin::Product g{dz, 1, lddz, x, 1, ldx, N, K, M};
   lin::Epilogue e{};
   e.mode = lin::kWeight;
   e.out = dw;
   e.ldo = K;
   e.accumulate = accumulate != 0;
-  cudaError_t err = lin::product(dtype, g, e, parts(work), st);
+  if (dtype == PPO_DTYPE_F32) {
+    cudaError_t err =
+        lin::simt_product<float>({dz, 1, lddz, x, 1, ldx, N, K, M}, e, parts(work), st);
+    if (err == cudaSuccess && db)
+      err = lin::column_sums<float>(dz, lddz, M, N, db, e.accumulate, parts(work), st);
+    return status_of(err);
+  }
+  char* free = reinterpret_cast<char*>(parts(work));
+  cudaError_t err = lin::on_16_bytes(dz, lddz, M, N, free, st);
+  if (err == cudaSuccess) err = lin::on_16_bytes(x, ldx, M, K, free, st);
+  if (err == cudaSuccess)
+    err = lin::tc_run({dz, 1, lddz, x, 1, ldx, N, K, M}, e, free, static_cast<int*>(work), st);
   if (err == cudaSuccess && db)
-    err = dtype == PPO_DTYPE_F32
-              ? lin::column_sums<float>(dz, lddz, M, N, db, e.accumulate, parts(work), st)
-              : lin::column_sums<__nv_bfloat16>(dz, lddz, M, N, db, e.accumulate, parts(work), st);
+    err = lin::column_sums<__nv_bfloat16>(dz, lddz, M, N, db, e.accumulate,
+                                          reinterpret_cast<float*>(free), st);
   return status_of(err);
 }
 

@@ -33,5 +33,25 @@ struct Epilogue {
   int64_t ldo;
 };
 
+// ---- tensor-core products (bf16, linear_tc.cu) ------------------------------------
+// A product whose rows (A(i, .), B(j, .), or for the weight gradient A(., r),
+// B(., r)) start on 16-byte boundaries.
+struct TcPlan {
+  int cg;              // CTAs of an output tile: 1 (128 x 128) or 2 (256 x 256)
+  int kt_per_split;    // 64-deep steps of the sum per split
+  int splits;
+};
+TcPlan tc_plan(int64_t I, int64_t J, int64_t R, bool must_split);
+bool tc_fits(const Product& g);
+// part: [splits][I][J rounded up to 4] for split products (the epilogue is
+// then finish_kernel's), else nullptr
+cudaError_t tc_product(const Product& g, const Epilogue& e, const TcPlan& plan, float* part,
+                       int* err, int sms, cudaStream_t st);
+
 }  // namespace lin
+
+// fp32 [splits][rows][cols] with row pitch ld (a multiple of 4) as 32-column x
+// 32-row x 1-split boxes, 128-byte swizzle (gemm_tc.cu)
+cudaError_t tc_make_tmap_f32(CUtensorMap* m, float* base, int64_t cols, int64_t rows,
+                             int64_t splits, int64_t ld);
 }  // namespace ppo
