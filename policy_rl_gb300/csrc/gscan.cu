@@ -7,32 +7,37 @@
 // (a1 a2, a2 b1 + b2), so a channel's steps can be cut into blocks that are
 // reduced to one map each, joined, and run again from their entering state.
 // The backward recurrence g_t = dh_t + u_t, u_{t-1} = a_t g_t (0 where the
-// state was cleared) has the same form from the other end.
+// state was cleared) has the same form from the other end, with the same a.
 //
 // Bound by memory (6 bytes per channel and step forward, 10 backward, in
-// bf16), so every pre-activation is read once: a thread keeps kSteps steps of
-// its channels in registers, reduces them, meets the other warps of its
-// block (consecutive steps of the same channels) in shared memory and runs the
-// steps again from registers.  A block of WT warps so covers a tile of
-// kSteps * WT steps and walks along the time axis tile by tile; with few
-// channels, a cluster of CS blocks takes CS consecutive tiles at a time and
-// joins them through distributed shared memory.  The forward pass leaves the
-// state that enters every 128th step for the backward pass, which walks the
-// same tiles from the end and recomputes the states in between.
+// bf16), so an input is read from DRAM once: warps fetch their steps into
+// shared memory two tiles ahead, reduce L steps of 32 channels (pairs) to maps
+// in registers, and run the steps after the maps of the block's warps
+// (consecutive steps of the same channels) were joined in shared memory.  A
+// block of WT warps so covers a tile of L * WT steps and walks over tiles.
+// The forward pass leaves the state that enters every 128th step for the
+// backward pass, which walks the same tiles from the end and recomputes the
+// states in between.  Three shapes of work:
+//   - many channels, forward: a warp alone walks its channels, nothing to join;
+//   - enough channels for every SM: a block walks along its channels' tiles;
+//   - few channels and a long sequence ("split"): one launch reduces every tile
+//     to its maps, a second joins them along the sequence, a third runs all
+//     tiles at once from their entering states.  This reads the gates (and ph
+//     or dh) twice, and leaves no tile waiting for another.  The maps lie in
+//     rows of the output that the third launch overwrites.
 // Compositions happen in an order fixed by the sizes: results are
 // deterministic.  A cleared state is dropped by a select, never multiplied by
 // 0, so that infinities and NaN do not cross it.
-#include <cooperative_groups.h>
-
 #include <algorithm>
+#include <type_traits>
 
 #include "ops.cuh"
+#include "tc_ptx.cuh"
 
 namespace ppo {
 namespace {
 
 using namespace ops;
-namespace cg = cooperative_groups;
 
 struct ScanArgs {
   const void *p, *dh;
@@ -43,393 +48,897 @@ struct ScanArgs {
   int64_t ldo;
   float *last;             // hT, or dh0 (nullable)
   float* carry;            // [ceil(T / 128)][C]: written (nullable), or read
+  int64_t groups;          // of channels, one block (warp) each
+  int wide;                // rows are read in 16-byte pieces
+  int split;               // tiles start from stored entering states (see above)
 };
 
-__device__ __forceinline__ float sigmoid(float x) {
-  // 1 / (1 + e^-x): e^-x overflows to inf below -88, whose reciprocal is 0
-  return __fdividef(1.f, 1.f + __expf(-x));
+// V channels at once; pairs go through the packed fp32 instructions (each half
+// rounded as the scalar instruction would).
+template <int V>
+__device__ __forceinline__ void vfma(const float (&a)[V], const float (&b)[V], const float (&c)[V],
+                                     float (&o)[V]) {
+  if constexpr (V == 2) {
+    const float2 r = ptx::ffma2(make_float2(a[0], a[1]), make_float2(b[0], b[1]),
+                                make_float2(c[0], c[1]));
+    o[0] = r.x;
+    o[1] = r.y;
+  } else {
+#pragma unroll
+    for (int v = 0; v < V; ++v) o[v] = fmaf(a[v], b[v], c[v]);
+  }
+}
+template <int V>
+__device__ __forceinline__ void vmul(const float (&a)[V], const float (&b)[V], float (&o)[V]) {
+  if constexpr (V == 2) {
+    const float2 r = ptx::fmul2(make_float2(a[0], a[1]), make_float2(b[0], b[1]));
+    o[0] = r.x;
+    o[1] = r.y;
+  } else {
+#pragma unroll
+    for (int v = 0; v < V; ++v) o[v] = a[v] * b[v];
+  }
+}
+template <int V>
+__device__ __forceinline__ void vset(float (&o)[V], float x) {
+#pragma unroll
+  for (int v = 0; v < V; ++v) o[v] = x;
+}
+template <int V>
+__device__ __forceinline__ void one_minus(const float (&z)[V], float (&a)[V]) {
+  float m[V], one[V];
+  vset<V>(m, -1.f);
+  vset<V>(one, 1.f);
+  vfma<V>(z, m, one, a);
+}
+// z = 1 / (1 + 2^(-x log2 e)): the power is inf below -88, its reciprocal 0
+template <int V>
+__device__ __forceinline__ void sigmoid(const float (&x)[V], float (&z)[V]) {
+  float k[V], one[V], e[V];
+  vset<V>(k, -1.4426950408889634f);
+  vset<V>(one, 1.f);
+  vmul<V>(x, k, e);
+#pragma unroll
+  for (int v = 0; v < V; ++v) asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e[v]) : "f"(e[v]));
+  vfma<V>(e, one, one, e);
+#pragma unroll
+  for (int v = 0; v < V; ++v) asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(z[v]) : "f"(e[v]));
 }
 
 // The affine map of a block of steps.  a < 0 stands for "the state was cleared
 // inside": what enters does not matter (products of 1 - z are never negative).
-struct Map {
-  float a, b;
-};
-__device__ __forceinline__ float apply(const Map& m, float h) {
-  return m.a < 0.f ? m.b : fmaf(m.a, h, m.b);
+__device__ __forceinline__ float apply(float a, float b, float h) {
+  return a < 0.f ? b : fmaf(a, h, b);
+}
+__device__ __forceinline__ float joined(float a1, float a2) {
+  return a1 < 0.f || a2 < 0.f ? -1.f : a1 * a2;
 }
 
-// Bit i: the state entering step t0 + i is cleared (steps beyond T: clear no
-// state).  `same`: all lanes of the warp belong to one environment.
+// Where the state entering a step is cleared (steps outside [0, T): nowhere).
+__device__ __forceinline__ float reset_flag(const ScanArgs& s, int64_t t, int n) {
+  if (t < 0 || t >= s.T) return 0.f;
+  if (t == 0) return s.done0 ? __ldg(s.done0 + n) : 0.f;
+  return s.done ? __ldg(s.done + (t - 1) * s.N + n) : 0.f;
+}
+
+// A channel's environment and its place within it.
+struct Channel {
+  int n, j;
+};
+__device__ __forceinline__ Channel channel(const ScanArgs& s, unsigned c) {
+  const unsigned n = c / (unsigned)s.H;
+  return {(int)n, (int)(c - n * (unsigned)s.H)};
+}
+// A lane's channels: V consecutive ones of one environment.
+struct Place {
+  unsigned c;
+  int n, j;
+  bool ok, same;   // same: the warp's channels belong to one environment
+};
+template <int V>
+__device__ __forceinline__ Place place_of(const ScanArgs& s, int group, int lane) {
+  Place p;
+  const unsigned first = (unsigned)group * kWarp * V, C = (unsigned)s.C;
+  p.c = first + lane * V;
+  p.ok = p.c < C;
+  const int n0 = channel(s, first < C ? first : 0).n;
+  const unsigned lastc = first + kWarp * V <= C ? first + kWarp * V - 1 : C - 1;
+  p.same = first < C && channel(s, lastc).n == n0;
+  const Channel x = channel(s, p.ok ? p.c : 0);
+  p.n = p.same ? n0 : x.n;   // lanes past the end read the warp's flags too
+  p.j = x.j;
+  return p;
+}
+
+// Bit i: the state entering step t0 + i is cleared.  Where all lanes of the
+// warp belong to one environment, lane i has loaded step i's flag beforehand.
 template <int L>
-__device__ __forceinline__ uint32_t reset_mask(const ScanArgs& s, int64_t t0, int64_t n, bool ok,
-                                               bool same, int lane) {
-  auto flag = [&](int64_t t) {
-    if (t < 0 || t >= s.T) return false;
-    if (t == 0) return s.done0 && __ldg(s.done0 + n) != 0.f;
-    return s.done && __ldg(s.done + (t - 1) * s.N + n) != 0.f;
-  };
-  if (L > 1 && same) return __ballot_sync(0xffffffffu, lane < L && flag(t0 + lane)) & ((1ull << L) - 1);
+__device__ __forceinline__ uint32_t reset_mask(const ScanArgs& s, float mine, int64_t t0,
+                                               const Place& pl) {
+  if (L > 1 && pl.same) return __ballot_sync(0xffffffffu, mine != 0.f);
   uint32_t m = 0;
-  if (ok) {
+  if (pl.ok) {
 #pragma unroll
-    for (int i = 0; i < L; ++i) m |= flag(t0 + i) ? 1u << i : 0u;
+    for (int i = 0; i < L; ++i) m |= reset_flag(s, t0 + i, pl.n) != 0.f ? 1u << i : 0u;
   }
   return m;
 }
 
-// A thread's place: V consecutive channels of one environment, L steps.
-struct Place {
-  int64_t c, n, j;
-  bool ok, same;
-};
-template <int V>
-__device__ __forceinline__ Place place_of(const ScanArgs& s, int64_t group, int lane) {
-  Place p;
-  const int64_t first = group * kWarp * V;
-  p.c = first + lane * V;
-  p.ok = p.c < s.C;
-  p.n = p.ok ? p.c / s.H : 0;
-  p.j = p.ok ? p.c - p.n * s.H : 0;
-  const int64_t lastc = min(first + kWarp * V, s.C) - 1;
-  p.same = first < s.C && first / s.H == lastc / s.H;
-  // lanes past the end share the warp's environment where all others do
-  if (p.same) p.n = first / s.H;
-  return p;
+// Keeps a row step out of the compiler's reach, so that it does not carry its
+// multiples from tile to tile in registers (measured with 16 steps: 128
+// registers and 500 to 1,200 bytes of spills a thread).
+__device__ __forceinline__ int64_t opaque(int64_t v) {
+  asm volatile("" : "+l"(v));
+  return v;
+}
+// The steps of a thread's block of L in [t0, T): their count.
+template <int L>
+__device__ __forceinline__ int steps_in(int64_t t0, int64_t T) {
+  const int64_t n = T - t0;
+  return n <= 0 ? 0 : n < L ? (int)n : L;
 }
 
-// ---- forward --------------------------------------------------------------------
-// WT warps along time, WC along channels; CS blocks of a cluster along time.
-template <typename T, int V, int L, int WT, int WC, bool CLUSTER>
-__global__ void __launch_bounds__(WT* WC* kWarp)
-scan_fwd_kernel(const ScanArgs s) {
-  __shared__ Map maps[2][WC][WT][V][kWarp];
-  __shared__ Map total[2][WC][V][kWarp];
-  const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp;
-  const int wt = warp % WT, wc = warp / WT;
-  int rank = 0, cs = 1;
-  if constexpr (CLUSTER) {
-    rank = (int)cg::this_cluster().block_rank();
-    cs = (int)cg::this_cluster().num_blocks();
+// One input's L steps of a warp: 2-byte elements in registers ..
+template <typename T, int V, int L>
+struct RegColumn {
+  Raw<T, V> r[L];
+  __device__ __forceinline__ void load(const ScanArgs&, const void* base, int64_t ld, int64_t off,
+                                       int64_t t0, int n, const Place& pl, int64_t N, int) {
+    const int64_t step = opaque(N * ld);
+    const T* p = static_cast<const T*>(base) + pl.n * ld + pl.j + off + t0 * step;
+#pragma unroll
+    for (int i = 0; i < L; ++i) {
+      r[i] = pl.ok && i < n ? __ldg(reinterpret_cast<const Raw<T, V>*>(p)) : Raw<T, V>{};
+      p += step;
+    }
   }
-  const Place pl = place_of<V>(s, (int64_t)(blockIdx.x / cs) * WC + wc, lane);
-  const int64_t tiles = (s.T + L * WT - 1) / (L * WT);
-  const T* pz = static_cast<const T*>(s.p) + pl.n * s.ldp + pl.j;
-  const T* ph = pz + s.H;
-  const int64_t pstep = s.N * s.ldp;
-  T* out = static_cast<T*>(s.out) + pl.n * s.ldo + pl.j;
-  float h[V];
+  __device__ __forceinline__ void get(int i, int, float (&f)[V]) const { to_f32<T, V>(r[i], f); }
+};
+// .. others in the warp's [L][32] words of shared memory, filled asynchronously
+// two tiles ahead (steps past n keep what was there): in 16-byte pieces, eight
+// of a row, where the rows are so aligned, else word by word.
+template <typename T, int V, int L>
+struct SharedColumn {
+  uint32_t* w;
+  __device__ __forceinline__ void load(const ScanArgs& s, const void* base, int64_t ld, int64_t off,
+                                       int64_t t0, int n, const Place& pl, int64_t N,
+                                       int lane) const {
+    const int64_t step = opaque(N * ld);
+    if (s.wide) {
+      const int r0 = lane >> 3;
+      const unsigned c = pl.c - lane * V + (lane & 7) * (16 / (int)sizeof(T));
+      const bool ok = c < (unsigned)s.C;
+      const Channel x = channel(s, ok ? c : 0);
+      const T* p = static_cast<const T*>(base) + x.n * ld + x.j + off + (t0 + r0) * step;
+      uint32_t dst = ptx::smem_u32(w) + r0 * 128 + (lane & 7) * 16;
 #pragma unroll
-  for (int v = 0; v < V; ++v) h[v] = pl.ok && s.h0 ? s.h0[pl.c + v] : 0.f;
-  int buf = 0;
-  for (int64_t base = 0; base < tiles; base += cs, buf ^= 1) {
-    const int64_t t0 = ((base + rank) * WT + wt) * L;
-    Raw<T, V> rz[L], rh[L];
-#pragma unroll
-    for (int i = 0; i < L; ++i) {
-      const bool in = pl.ok && t0 + i < s.T;
-      rz[i] = in ? __ldg(reinterpret_cast<const Raw<T, V>*>(pz + (t0 + i) * pstep)) : Raw<T, V>{};
-      rh[i] = in ? __ldg(reinterpret_cast<const Raw<T, V>*>(ph + (t0 + i) * pstep)) : Raw<T, V>{};
-    }
-    const uint32_t clear = reset_mask<L>(s, t0, pl.n, pl.ok, pl.same, lane);
-    float z[L][V];
-    Map m[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) m[v] = Map{1.f, 0.f};
-#pragma unroll
-    for (int i = 0; i < L; ++i) {
-      const bool in = t0 + i < s.T;
-      float x[V], c[V];
-      to_f32<T, V>(rz[i], x);
-      to_f32<T, V>(rh[i], c);
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        z[i][v] = sigmoid(x[v]);
-        if (in) {
-          const float a = 1.f - z[i][v], b = z[i][v] * c[v];
-          m[v].b = (clear >> i) & 1u ? b : fmaf(a, m[v].b, b);
-          m[v].a *= a;
-        }
-      }
-    }
-    if constexpr (WT > 1) {
-#pragma unroll
-      for (int v = 0; v < V; ++v)
-        maps[buf][wc][wt][v][lane] = Map{clear ? -1.f : m[v].a, m[v].b};
-      __syncthreads();
-    }
-    // hin: the state entering this thread's steps; h moves past the tiles
-    float hin[V];
-    if constexpr (CLUSTER) {
-      if (wt == 0) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          Map t{1.f, 0.f};
-#pragma unroll
-          for (int w = 0; w < WT; ++w) {
-            const Map k = maps[buf][wc][w][v][lane];
-            t.b = k.a < 0.f ? k.b : fmaf(k.a, t.b, k.b);
-            t.a = k.a < 0.f || t.a < 0.f ? -1.f : t.a * k.a;
-          }
-          total[buf][wc][v][lane] = t;
-        }
-      }
-      cg::this_cluster().sync();
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        for (int r = 0; r < cs; ++r) {
-          if (r == rank) hin[v] = h[v];
-          const Map* remote = cg::this_cluster().map_shared_rank(&total[buf][wc][v][lane], r);
-          h[v] = apply(*remote, h[v]);
-        }
-#pragma unroll
-        for (int w = 0; w < WT; ++w)
-          if (w < wt) hin[v] = apply(maps[buf][wc][w][v][lane], hin[v]);
+      for (int i = 0; i < L; i += 4) {
+        if (ok && r0 + i < n)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + i * 128), "l"(p)
+                       : "memory");
+        p += 4 * step;
       }
     } else {
+      const T* p = static_cast<const T*>(base) + pl.n * ld + pl.j + off + t0 * step;
+      const uint32_t dst = ptx::smem_u32(w) + lane * 4;
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        if constexpr (WT > 1) {
-#pragma unroll
-          for (int w = 0; w < WT; ++w) {
-            if (w == wt) hin[v] = h[v];
-            h[v] = apply(maps[buf][wc][w][v][lane], h[v]);
-          }
-        } else {
-          hin[v] = h[v];
-        }
+      for (int i = 0; i < L; ++i) {
+        if (pl.ok && i < n)
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst + i * 128), "l"(p)
+                       : "memory");
+        p += step;
       }
     }
-    if (s.carry && pl.ok && t0 % PPO_SCAN_BLOCK == 0 && t0 < s.T) {
-#pragma unroll
-      for (int v = 0; v < V; ++v)
-        s.carry[(t0 / PPO_SCAN_BLOCK) * s.C + pl.c + v] = clear & 1u ? 0.f : hin[v];
-    }
-#pragma unroll
-    for (int i = 0; i < L; ++i) {
-      float c[V];
-      to_f32<T, V>(rh[i], c);
-      if (t0 + i < s.T) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          const float b = z[i][v] * c[v];
-          hin[v] = (clear >> i) & 1u ? b : fmaf(1.f - z[i][v], hin[v], b);
-        }
-        if (pl.ok)
-          *reinterpret_cast<Raw<T, V>*>(out + (t0 + i) * s.N * s.ldo) = from_f32<T, V>(hin);
-      }
-    }
-    if constexpr (WT == 1) {
-#pragma unroll
-      for (int v = 0; v < V; ++v) h[v] = hin[v];
-    }
   }
-  if (s.last && wt == 0 && rank == 0 && pl.ok) {
-#pragma unroll
-    for (int v = 0; v < V; ++v) s.last[pl.c + v] = h[v];
+  __device__ __forceinline__ void get(int i, int lane, float (&f)[V]) const {
+    static_assert(sizeof(Raw<T, V>) == 4, "one word");
+    const uint32_t x = w[i * kWarp + lane];
+    Raw<T, V> r;
+    memcpy(&r, &x, 4);
+    to_f32<T, V>(r, f);
   }
-  if constexpr (CLUSTER) cg::this_cluster().sync();   // no block leaves while its maps are read
+};
+template <typename T, int V> constexpr bool kFetch = sizeof(T) * V == 4;
+constexpr int kStages = 2;
+__device__ __forceinline__ void fetch_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void fetch_wait() {   // all but the newest kStages - 1 groups
+  asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
 }
 
-// ---- backward ---------------------------------------------------------------------
-template <typename T, int V, int L, int WT, int WC, bool CLUSTER>
-__global__ void __launch_bounds__(WT* WC* kWarp)
-scan_bwd_kernel(const ScanArgs s) {
-  // fwd maps of the blocks of steps, and the maps of what they pass back
-  // (same a; the states of a tile start from the stored carry)
-  __shared__ Map maps[2][WC][WT][V][kWarp];
-  __shared__ float back[2][WC][WT][V][kWarp];
-  __shared__ Map total[2][WC][V][kWarp];
-  static_assert(PPO_SCAN_BLOCK % (L * WT) == 0, "tiles start at stored states or inside a block");
+// ---- steps in registers ----------------------------------------------------------
+// PLAIN: all L steps exist and none clears a state.
+template <int V, int L, bool PLAIN, typename Col>
+__device__ __forceinline__ void block_map(const float (&z)[L][V], const Col& rh, int n,
+                                          uint32_t clear, int lane, float (&ma)[V],
+                                          float (&mb)[V]) {
+  vset<V>(ma, 1.f);
+  vset<V>(mb, 0.f);
+#pragma unroll
+  for (int i = 0; i < L; ++i) {
+    float c[V], a[V], b[V];
+    rh.get(i, lane, c);
+    if (PLAIN || i < n) {
+      one_minus<V>(z[i], a);
+      vmul<V>(z[i], c, b);
+      if (!PLAIN && ((clear >> i) & 1u)) vset<V>(mb, 0.f);
+      vfma<V>(a, mb, b, mb);
+      vmul<V>(ma, a, ma);
+    }
+  }
+  if (!PLAIN && clear) vset<V>(ma, -1.f);
+}
+
+// The steps themselves, from the entering state h to the last one.
+template <typename T, int V, int L, bool PLAIN, typename Col>
+__device__ __forceinline__ void run_steps(const float (&z)[L][V], const Col& rh, int n,
+                                          uint32_t clear, int lane, bool ok, float (&h)[V], T* o,
+                                          int64_t ostep) {
+#pragma unroll
+  for (int i = 0; i < L; ++i) {
+    float c[V], a[V], b[V];
+    rh.get(i, lane, c);
+    if (PLAIN || i < n) {
+      one_minus<V>(z[i], a);
+      vmul<V>(z[i], c, b);
+      if (!PLAIN && ((clear >> i) & 1u)) vset<V>(h, 0.f);
+      vfma<V>(a, h, b, h);
+      if (ok) *reinterpret_cast<Raw<T, V>*>(o) = from_f32<T, V>(h);
+    }
+    o += ostep;
+  }
+}
+
+// What n steps pass back from their own dh, in reverse order (and, with MAP,
+// the factor of what reaches them from later steps).
+template <int V, int L, bool PLAIN, bool MAP, typename Col>
+__device__ __forceinline__ void block_back(const float (&z)[L][V], const Col& rg, int n,
+                                           uint32_t clear, int lane, float (&ma)[V],
+                                           float (&g)[V]) {
+  vset<V>(g, 0.f);
+  if (MAP) vset<V>(ma, 1.f);
+  float one[V];
+  vset<V>(one, 1.f);
+#pragma unroll
+  for (int i = L - 1; i >= 0; --i) {
+    float d[V], a[V];
+    rg.get(i, lane, d);
+    if (PLAIN || i < n) {
+      one_minus<V>(z[i], a);
+      vfma<V>(d, one, g, g);
+      vmul<V>(a, g, g);
+      if (MAP) vmul<V>(ma, a, ma);
+      if (!PLAIN && ((clear >> i) & 1u)) vset<V>(g, 0.f);
+    }
+  }
+  if (MAP && !PLAIN && clear) vset<V>(ma, -1.f);
+}
+
+// The steps from the last to the first, given the state h entering the first
+// and u, what reaches the last state from later steps.
+template <typename T, int V, int L, bool PLAIN, typename Col>
+__device__ __forceinline__ void run_back(const float (&z)[L][V], const Col& rh, const Col& rg,
+                                         int n, uint32_t clear, int lane, bool ok, float (&h)[V],
+                                         float (&u)[V], T* o, int64_t ostep, int64_t H) {
+  float w[L][V];   // dpz / g of each step
+  float one[V], minus[V];
+  vset<V>(one, 1.f);
+  vset<V>(minus, -1.f);
+#pragma unroll
+  for (int i = 0; i < L; ++i) {
+    float c[V], a[V], k[V];
+    rh.get(i, lane, c);
+    if (!PLAIN && ((clear >> i) & 1u)) vset<V>(h, 0.f);
+    one_minus<V>(z[i], a);
+    vmul<V>(z[i], a, k);
+    vfma<V>(h, minus, c, w[i]);
+    vmul<V>(w[i], k, w[i]);
+    vmul<V>(z[i], c, k);
+    vfma<V>(a, h, k, h);
+  }
+  o += (L - 1) * ostep;
+#pragma unroll
+  for (int i = L - 1; i >= 0; --i) {
+    float d[V], dz[V], dc[V], a[V];
+    rg.get(i, lane, d);
+    if (PLAIN || i < n) {
+      vfma<V>(d, one, u, d);
+      vmul<V>(d, z[i], dc);
+      vmul<V>(d, w[i], dz);
+      one_minus<V>(z[i], a);
+      vmul<V>(a, d, u);
+      if (!PLAIN && ((clear >> i) & 1u)) vset<V>(u, 0.f);
+      if (ok) {
+        *reinterpret_cast<Raw<T, V>*>(o) = from_f32<T, V>(dz);
+        *reinterpret_cast<Raw<T, V>*>(o + H) = from_f32<T, V>(dc);
+      }
+    }
+    o -= ostep;
+  }
+}
+
+// ---- maps kept in the output's rows (split) -----------------------------------------
+// Value k (0, 1, 2) of a tile and channel: fp32 outputs hold it in the tile's
+// row k, bf16 outputs its upper and lower halves in rows 2k and 2k + 1.  (dp
+// uses its pz columns.)
+template <typename T>
+__device__ __forceinline__ void put_value(T* row, int64_t step, int k, float v) {
+  if constexpr (sizeof(T) == 4) {
+    row[k * step] = v;
+  } else {
+    const uint32_t u = __float_as_uint(v);
+    row[2 * k * step] = __ushort_as_bfloat16((uint16_t)(u >> 16));
+    row[(2 * k + 1) * step] = __ushort_as_bfloat16((uint16_t)u);
+  }
+}
+template <typename T>
+__device__ __forceinline__ float get_value(const T* row, int64_t step, int k) {
+  if constexpr (sizeof(T) == 4) {
+    return row[k * step];
+  } else {
+    const uint32_t hi = __bfloat16_as_ushort(row[2 * k * step]);
+    return __uint_as_float(hi << 16 | __bfloat16_as_ushort(row[(2 * k + 1) * step]));
+  }
+}
+// rows that values 0..k need
+template <typename T>
+__host__ __device__ constexpr int value_rows(int k) { return sizeof(T) == 4 ? k + 1 : 2 * k + 2; }
+
+// ---- the kernels ----------------------------------------------------------------------
+// A block's walk over (group of channels, tile) pairs, tiles fastest.
+struct Walk {
+  int group, tile;
+};
+
+#ifndef TPS
+#define TPS 1024
+#endif
+// threads that the registers of L steps leave room for on an SM
+__host__ __device__ constexpr int threads_per_sm(int L) { return L > 8 ? 512 : TPS; }
+
+enum Phase : int { kWhole = 0, kMaps = 1 };
+
+// WT warps along time, WC along channels.  PHASE kMaps writes each tile's map
+// and runs nothing.
+template <typename T, int V, int L, int WT, int WC, int PHASE>
+__global__ void __launch_bounds__(WT* WC* kWarp, L > 1 ? threads_per_sm(L) / (WT * WC * kWarp) : 1)
+scan_fwd_kernel(const ScanArgs s) {
+  constexpr int CH = WC * kWarp * V, NT = WT * WC * kWarp;
+  __shared__ float sa[WT > 1 ? WT : 1][WT > 1 ? CH : 1], sb[WT > 1 ? WT : 1][WT > 1 ? CH : 1];
+  constexpr bool FETCH = L > 1 && kFetch<T, V>;
+  extern __shared__ __align__(128) uint32_t ring[];   // FETCH: [kStages][pz, ph][warp][L][32]
   const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp;
   const int wt = warp % WT, wc = warp / WT;
-  int rank = 0, cs = 1;
-  if constexpr (CLUSTER) {
-    rank = (int)cg::this_cluster().block_rank();
-    cs = (int)cg::this_cluster().num_blocks();
+  const int tiles = (int)((s.T + L * WT - 1) / (L * WT)), groups = (int)s.groups;
+  // units: the pairs of a block, dealt out round by round; unsplit, a group's
+  // tiles stay with one block
+  const int first = s.split ? blockIdx.x / groups : 0;
+  using Col = std::conditional_t<FETCH, SharedColumn<T, V, L>, RegColumn<T, V, L>>;
+  auto column = [&](int stage, int k) {
+    Col c;
+    if constexpr (FETCH) c.w = ring + ((stage * 2 + k) * (WT * WC) + warp) * (L * kWarp);
+    return c;
+  };
+  auto place = [&](int group) { return place_of<V>(s, group * WC + wc, lane); };
+  auto load = [&](const Place& pl, int tile, Col& cz, Col& ch, float& flag) {
+    const int64_t t0 = ((int64_t)tile * WT + wt) * L;
+    const int n = steps_in<L>(t0, s.T);
+    cz.load(s, s.p, s.ldp, 0, t0, n, pl, s.N, lane);
+    ch.load(s, s.p, s.ldp, s.H, t0, n, pl, s.N, lane);
+    flag = L > 1 && pl.same && lane < L ? reset_flag(s, t0 + lane, pl.n) : 0.f;
+  };
+  const int stride = s.split ? gridDim.x / groups : 1;   // tiles from one to the next
+  Walk at{(int)(s.split ? blockIdx.x % groups : blockIdx.x), first}, ahead = at;
+  auto more = [&](const Walk& w) { return s.split ? w.tile < tiles : w.group < groups; };
+  auto advance = [&](Walk& w) {
+    w.tile += stride;
+    if (!s.split && w.tile >= tiles) {
+      w.tile = 0;
+      w.group += gridDim.x;
+    }
+  };
+  float flags[kStages] = {};
+  if constexpr (FETCH) {
+#pragma unroll
+    for (int i = 0; i < kStages; ++i) {
+      Col cz = column(i, 0), ch = column(i, 1);
+      if (more(ahead)) {
+        load(place(ahead.group), ahead.tile, cz, ch, flags[i]);
+        advance(ahead);
+      }
+      fetch_commit();
+    }
   }
-  const Place pl = place_of<V>(s, (int64_t)(blockIdx.x / cs) * WC + wc, lane);
-  const int64_t tiles = (s.T + L * WT - 1) / (L * WT);
-  const T* pz = static_cast<const T*>(s.p) + pl.n * s.ldp + pl.j;
-  const T* ph = pz + s.H;
-  const T* gh = static_cast<const T*>(s.dh) + pl.n * s.lddh + pl.j;
-  const int64_t pstep = s.N * s.ldp, gstep = s.N * s.lddh, ostep = s.N * s.ldo;
-  T* oz = static_cast<T*>(s.out) + pl.n * s.ldo + pl.j;
-  T* oh = oz + s.H;
-  float u[V];
+  // the running state: each thread's own (WT == 1), or that of the channel
+  // thread x joins (block channel x, below CH)
+  float h[V];
+  float hj[(CH + NT - 1) / NT];
+  int stage = 0;
+  while (more(at)) {
+    const Place pl = place(at.group);
+    const int64_t t0 = ((int64_t)at.tile * WT + wt) * L;
+    const int n = steps_in<L>(t0, s.T);
+    const int64_t ostep = opaque(s.N * s.ldo);
+    T* out = static_cast<T*>(s.out) + pl.n * s.ldo + pl.j + t0 * ostep;
+    if constexpr (PHASE == kWhole) {
+      if (at.tile == 0 || s.split) {
+        // (split, not h0 itself, which the last tile's block may be replacing)
+        const float* from = s.split ? s.carry + (int64_t)at.tile * s.C : s.h0;
+        if constexpr (WT == 1) {
 #pragma unroll
-  for (int v = 0; v < V; ++v) u[v] = pl.ok && s.dhT ? s.dhT[pl.c + v] : 0.f;
-  int buf = 0;
-  const int64_t rounds = (tiles + cs - 1) / cs;
-  for (int64_t r0 = rounds - 1; r0 >= 0; --r0, buf ^= 1) {
-    const int64_t t0 = ((r0 * cs + rank) * WT + wt) * L;
-    Raw<T, V> rz[L], rh[L], rg[L];
+          for (int v = 0; v < V; ++v) h[v] = pl.ok && from ? from[pl.c + v] : 0.f;
+        } else {
 #pragma unroll
-    for (int i = 0; i < L; ++i) {
-      const bool in = pl.ok && t0 + i < s.T;
-      rz[i] = in ? __ldg(reinterpret_cast<const Raw<T, V>*>(pz + (t0 + i) * pstep)) : Raw<T, V>{};
-      rh[i] = in ? __ldg(reinterpret_cast<const Raw<T, V>*>(ph + (t0 + i) * pstep)) : Raw<T, V>{};
-      rg[i] = in ? __ldg(reinterpret_cast<const Raw<T, V>*>(gh + (t0 + i) * gstep)) : Raw<T, V>{};
+          for (int k = 0; k < (CH + NT - 1) / NT; ++k) {
+            const int x = threadIdx.x + k * NT;
+            const unsigned c = (unsigned)at.group * CH + x;
+            hj[k] = x < CH && c < s.C && from ? from[c] : 0.f;
+          }
+        }
+      }
     }
-    const int64_t tile0 = (r0 * cs + rank) * WT * L;
-    float hin[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-      hin[v] = pl.ok && tile0 < s.T ? __ldg(s.carry + (tile0 / PPO_SCAN_BLOCK) * s.C + pl.c + v) : 0.f;
-    const uint32_t clear = reset_mask<L>(s, t0, pl.n, pl.ok, pl.same, lane);
+    Col cz = column(stage, 0), rh = column(stage, 1);
+    float flag;
+    if constexpr (FETCH) {
+      fetch_wait();
+      __syncwarp();   // pieces that other lanes fetched
+      flag = stage == 0 ? flags[0] : flags[1];
+    } else {
+      load(pl, at.tile, cz, rh, flag);
+    }
     float z[L][V];
-    Map m[V];
-    float g[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      m[v] = Map{1.f, 0.f};
-      g[v] = 0.f;
-    }
 #pragma unroll
     for (int i = 0; i < L; ++i) {
-      float x[V], c[V];
-      to_f32<T, V>(rz[i], x);
-      to_f32<T, V>(rh[i], c);
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        z[i][v] = sigmoid(x[v]);
-        if (t0 + i < s.T) {
-          const float a = 1.f - z[i][v], b = z[i][v] * c[v];
-          m[v].b = (clear >> i) & 1u ? b : fmaf(a, m[v].b, b);
-          m[v].a *= a;
-        }
-      }
+      cz.get(i, lane, z[i]);
+      sigmoid<V>(z[i], z[i]);
     }
+    const uint32_t clear = reset_mask<L>(s, flag, t0, pl);
+    const bool plain = __all_sync(0xffffffffu, n == L && clear == 0);
+    float hin[V];   // the state entering this thread's steps
     if constexpr (WT > 1) {
-#pragma unroll
-      for (int i = L - 1; i >= 0; --i) {
-        float d[V];
-        to_f32<T, V>(rg[i], d);
-        if (t0 + i < s.T) {
-#pragma unroll
-          for (int v = 0; v < V; ++v)
-            g[v] = (clear >> i) & 1u ? 0.f : (1.f - z[i][v]) * (d[v] + g[v]);
-        }
-      }
+      float ma[V], mb[V];
+      if (plain) block_map<V, L, true>(z, rh, n, clear, lane, ma, mb);
+      else block_map<V, L, false>(z, rh, n, clear, lane, ma, mb);
+      const int x0 = (wc * kWarp + lane) * V;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        maps[buf][wc][wt][v][lane] = Map{clear ? -1.f : m[v].a, m[v].b};
-        back[buf][wc][wt][v][lane] = g[v];
+        sa[wt][x0 + v] = ma[v];
+        sb[wt][x0 + v] = mb[v];
       }
       __syncthreads();
-      // the state entering this thread's steps, from the tile's
+      // a channel's thread replaces each block's map by the state entering it
 #pragma unroll
-      for (int v = 0; v < V; ++v)
+      for (int k = 0; k < (CH + NT - 1) / NT; ++k) {
+        const int x = threadIdx.x + k * NT;
+        if (x < CH) {
+          if constexpr (PHASE == kWhole) {
 #pragma unroll
-        for (int w = 0; w < WT - 1; ++w)
-          if (w < wt) hin[v] = apply(maps[buf][wc][w][v][lane], hin[v]);
+            for (int w = 0; w < WT; ++w) {
+              const float a = sa[w][x], b = sb[w][x];
+              sb[w][x] = hj[k];
+              hj[k] = apply(a, b, hj[k]);
+            }
+          } else {
+            float a = 1.f, b = 0.f;
+#pragma unroll
+            for (int w = 0; w < WT; ++w) {
+              b = apply(sa[w][x], sb[w][x], b);
+              a = joined(a, sa[w][x]);
+            }
+            const unsigned c = (unsigned)at.group * CH + x;
+            if (c < s.C && at.tile < tiles - 1) {   // (the last one's is not needed)
+              const Channel e = channel(s, c);
+              T* row = static_cast<T*>(s.out) + e.n * s.ldo + e.j + (int64_t)at.tile * (L * WT) * ostep;
+              put_value<T>(row, ostep, 0, a);
+              put_value<T>(row, ostep, 1, b);
+            }
+          }
+        }
+      }
+      __syncthreads();
+#pragma unroll
+      for (int v = 0; v < V; ++v) hin[v] = sb[wt][x0 + v];
+    } else {
+#pragma unroll
+      for (int v = 0; v < V; ++v) hin[v] = h[v];
     }
-    // uin: what reaches this thread's last state from later steps
-    float uin[V];
-    auto pass_back = [&](int w, int v, float x) {
-      const float a = maps[buf][wc][w][v][lane].a, b = back[buf][wc][w][v][lane];
-      return a < 0.f ? b : fmaf(a, x, b);
-    };
-    if constexpr (CLUSTER) {
-      if (wt == 0) {
+    if constexpr (PHASE == kWhole) {
+      if (s.carry && !s.split && pl.ok && n > 0 && t0 % PPO_SCAN_BLOCK == 0) {
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+          s.carry[(t0 / PPO_SCAN_BLOCK) * s.C + pl.c + v] = clear & 1u ? 0.f : hin[v];
+      }
+      if (plain) run_steps<T, V, L, true>(z, rh, n, clear, lane, pl.ok, hin, out, ostep);
+      else run_steps<T, V, L, false>(z, rh, n, clear, lane, pl.ok, hin, out, ostep);
+      // the thread of the last step has the last state
+      if (s.last && pl.ok && n > 0 && t0 + n == s.T) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) s.last[pl.c + v] = hin[v];
+      }
+      if constexpr (WT == 1) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) h[v] = hin[v];
+      }
+    }
+    if constexpr (FETCH) {
+      __syncwarp();   // the warp has read its words: they may be refilled
+      if (more(ahead)) {
+        float f;
+        load(place(ahead.group), ahead.tile, cz, rh, f);
+        if (stage == 0) flags[0] = f;
+        else flags[1] = f;
+        advance(ahead);
+      }
+      fetch_commit();
+      stage ^= 1;
+    }
+    advance(at);
+  }
+}
+
+// A tile of fewer than PPO_SCAN_BLOCK steps has to hold the whole sequence.
+template <typename T, int V, int L, int WT, int WC, int PHASE>
+__global__ void __launch_bounds__(WT* WC* kWarp, L > 1 ? threads_per_sm(L) / (WT * WC * kWarp) : 1)
+scan_bwd_kernel(const ScanArgs s) {
+  constexpr int CH = WC * kWarp * V, NT = WT * WC * kWarp;
+  // maps of the blocks of steps (factor, state), and what they pass back
+  __shared__ float sa[WT > 1 ? WT : 1][WT > 1 ? CH : 1], sb[WT > 1 ? WT : 1][WT > 1 ? CH : 1],
+      sg[WT > 1 ? WT : 1][WT > 1 ? CH : 1];
+  constexpr bool FETCH = L > 1 && kFetch<T, V>;
+  constexpr int IN = PHASE == kMaps ? 2 : 3;
+  extern __shared__ __align__(128) uint32_t ring[];   // FETCH: [kStages][pz, dh (, ph)][warp][L][32]
+  const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp;
+  const int wt = warp % WT, wc = warp / WT;
+  const int tiles = (int)((s.T + L * WT - 1) / (L * WT)), groups = (int)s.groups;
+  using Col = std::conditional_t<FETCH, SharedColumn<T, V, L>, RegColumn<T, V, L>>;
+  auto column = [&](int stage, int k) {
+    Col c;
+    if constexpr (FETCH) c.w = ring + ((stage * IN + k) * (WT * WC) + warp) * (L * kWarp);
+    return c;
+  };
+  auto place = [&](int group) { return place_of<V>(s, group * WC + wc, lane); };
+  auto load = [&](const Place& pl, int tile, Col& cz, Col& cd, Col& ch, float& flag) {
+    const int64_t t0 = ((int64_t)tile * WT + wt) * L;
+    const int n = steps_in<L>(t0, s.T);
+    cz.load(s, s.p, s.ldp, 0, t0, n, pl, s.N, lane);
+    cd.load(s, s.dh, s.lddh, 0, t0, n, pl, s.N, lane);
+    if constexpr (PHASE == kWhole) ch.load(s, s.p, s.ldp, s.H, t0, n, pl, s.N, lane);
+    flag = L > 1 && pl.same && lane < L ? reset_flag(s, t0 + lane, pl.n) : 0.f;
+  };
+  // tiles run from the last to the first
+  const int stride = s.split ? gridDim.x / groups : 1;
+  Walk at{(int)(s.split ? blockIdx.x % groups : blockIdx.x),
+          tiles - 1 - (int)(s.split ? blockIdx.x / groups : 0)},
+      ahead = at;
+  auto more = [&](const Walk& w) { return s.split ? w.tile >= 0 : w.group < groups; };
+  auto advance = [&](Walk& w) {
+    w.tile -= stride;
+    if (!s.split && w.tile < 0) {
+      w.tile = tiles - 1;
+      w.group += gridDim.x;
+    }
+  };
+  float flags[kStages] = {};
+  if constexpr (FETCH) {
+#pragma unroll
+    for (int i = 0; i < kStages; ++i) {
+      Col a = column(i, 0), b = column(i, 1), c = column(i, IN - 1);
+      if (more(ahead)) {
+        load(place(ahead.group), ahead.tile, a, b, c, flags[i]);
+        advance(ahead);
+      }
+      fetch_commit();
+    }
+  }
+  float u[V];
+  float uj[(CH + NT - 1) / NT], hj[(CH + NT - 1) / NT];
+  int stage = 0;
+  while (more(at)) {
+    const Place pl = place(at.group);
+    const int64_t t0 = ((int64_t)at.tile * WT + wt) * L;
+    const int n = steps_in<L>(t0, s.T);
+    const int64_t ostep = opaque(s.N * s.ldo);
+    T* out = static_cast<T*>(s.out) + pl.n * s.ldo + pl.j + t0 * ostep;
+    float hin[V], uin[V];   // the state entering this thread's steps, what reaches the last of them
+    if constexpr (PHASE == kWhole) {
+      const float* from = s.carry + ((int64_t)at.tile * L * WT / PPO_SCAN_BLOCK) * s.C;
+      if constexpr (WT == 1) {
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-          Map t{1.f, 0.f};
+          hin[v] = pl.ok ? __ldg(from + pl.c + v) : 0.f;
+          if (at.tile == tiles - 1) u[v] = pl.ok && s.dhT ? s.dhT[pl.c + v] : 0.f;
+        }
+      } else {
 #pragma unroll
-          for (int w = WT - 1; w >= 0; --w) {
-            const float a = maps[buf][wc][w][v][lane].a;
-            t.b = pass_back(w, v, t.b);
-            t.a = a < 0.f || t.a < 0.f ? -1.f : t.a * a;
+        for (int k = 0; k < (CH + NT - 1) / NT; ++k) {
+          const int x = threadIdx.x + k * NT;
+          const unsigned c = (unsigned)at.group * CH + x;
+          const bool in = x < CH && c < s.C;
+          hj[k] = in ? __ldg(from + c) : 0.f;
+          if (at.tile == tiles - 1) {
+            uj[k] = in && s.dhT ? s.dhT[c] : 0.f;
+          } else if (s.split && in) {
+            const Channel e = channel(s, c);
+            uj[k] = get_value<T>(static_cast<const T*>(s.out) + e.n * s.ldo + e.j +
+                                     (int64_t)at.tile * (L * WT) * ostep, ostep, 2);
           }
-          total[buf][wc][v][lane] = t;
         }
       }
-      cg::this_cluster().sync();
+    }
+    Col cz = column(stage, 0), rg = column(stage, 1), rh = column(stage, IN - 1);
+    float flag;
+    if constexpr (FETCH) {
+      fetch_wait();
+      __syncwarp();
+      flag = stage == 0 ? flags[0] : flags[1];
+    } else {
+      load(pl, at.tile, cz, rg, rh, flag);
+    }
+    float z[L][V];
+#pragma unroll
+    for (int i = 0; i < L; ++i) {
+      cz.get(i, lane, z[i]);
+      sigmoid<V>(z[i], z[i]);
+    }
+    const uint32_t clear = reset_mask<L>(s, flag, t0, pl);
+    const bool plain = __all_sync(0xffffffffu, n == L && clear == 0);
+    if constexpr (WT > 1) {
+      const int x0 = (wc * kWarp + lane) * V;
+      float ma[V], mb[V], g[V];
+      if constexpr (PHASE == kWhole) {
+        if (plain) {
+          block_map<V, L, true>(z, rh, n, clear, lane, ma, mb);
+          block_back<V, L, true, false>(z, rg, n, clear, lane, ma, g);
+        } else {
+          block_map<V, L, false>(z, rh, n, clear, lane, ma, mb);
+          block_back<V, L, false, false>(z, rg, n, clear, lane, ma, g);
+        }
+#pragma unroll
+        for (int v = 0; v < V; ++v) sb[wt][x0 + v] = mb[v];
+      } else {
+        if (plain) block_back<V, L, true, true>(z, rg, n, clear, lane, ma, g);
+        else block_back<V, L, false, true>(z, rg, n, clear, lane, ma, g);
+      }
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        for (int r = cs - 1; r >= 0; --r) {
-          if (r == rank) uin[v] = u[v];
-          const Map* remote = cg::this_cluster().map_shared_rank(&total[buf][wc][v][lane], r);
-          u[v] = apply(*remote, u[v]);
-        }
-#pragma unroll
-        for (int w = WT - 1; w > 0; --w)
-          if (w > wt) uin[v] = pass_back(w, v, uin[v]);
+        sa[wt][x0 + v] = ma[v];
+        sg[wt][x0 + v] = g[v];
       }
-    } else if constexpr (WT > 1) {
+      __syncthreads();
 #pragma unroll
-      for (int v = 0; v < V; ++v)
+      for (int k = 0; k < (CH + NT - 1) / NT; ++k) {
+        const int x = threadIdx.x + k * NT;
+        if (x < CH) {
+          if constexpr (PHASE == kWhole) {
 #pragma unroll
-        for (int w = WT - 1; w >= 0; --w) {
-          if (w == wt) uin[v] = u[v];
-          u[v] = pass_back(w, v, u[v]);
+            for (int w = 0; w < WT; ++w) {
+              const float b = sb[w][x];
+              sb[w][x] = hj[k];
+              hj[k] = apply(sa[w][x], b, hj[k]);
+            }
+#pragma unroll
+            for (int w = WT - 1; w >= 0; --w) {
+              const float b = sg[w][x];
+              sg[w][x] = uj[k];
+              uj[k] = apply(sa[w][x], b, uj[k]);
+            }
+          } else {
+            float a = 1.f, b = 0.f;
+#pragma unroll
+            for (int w = WT - 1; w >= 0; --w) {
+              b = apply(sa[w][x], sg[w][x], b);
+              a = joined(a, sa[w][x]);
+            }
+            const unsigned c = (unsigned)at.group * CH + x;
+            // (a last tile too short for them is joined from its steps)
+            if (c < s.C && s.T - (int64_t)at.tile * (L * WT) >= value_rows<T>(1)) {
+              const Channel e = channel(s, c);
+              T* row = static_cast<T*>(s.out) + e.n * s.ldo + e.j + (int64_t)at.tile * (L * WT) * ostep;
+              put_value<T>(row, ostep, 0, a);
+              put_value<T>(row, ostep, 1, b);
+            }
+          }
         }
+      }
+      __syncthreads();
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        if constexpr (PHASE == kWhole) hin[v] = sb[wt][x0 + v];
+        uin[v] = sg[wt][x0 + v];
+      }
     } else {
 #pragma unroll
       for (int v = 0; v < V; ++v) uin[v] = u[v];
     }
-    // the states entering the steps, then the steps from the last to the first
-    float hp[L][V];
+    if constexpr (PHASE == kWhole) {
+      if (plain) run_back<T, V, L, true>(z, rh, rg, n, clear, lane, pl.ok, hin, uin, out, ostep, s.H);
+      else run_back<T, V, L, false>(z, rh, rg, n, clear, lane, pl.ok, hin, uin, out, ostep, s.H);
+      if (s.last && pl.ok && t0 == 0) {   // the thread of the first step
 #pragma unroll
-    for (int i = 0; i < L; ++i) {
-      float c[V];
-      to_f32<T, V>(rh[i], c);
+        for (int v = 0; v < V; ++v) s.last[pl.c + v] = uin[v];
+      }
+      if constexpr (WT == 1) {
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        if ((clear >> i) & 1u) hin[v] = 0.f;
-        hp[i][v] = hin[v];
-        hin[v] = fmaf(1.f - z[i][v], hin[v], z[i][v] * c[v]);
+        for (int v = 0; v < V; ++v) u[v] = uin[v];
+      }
+    }
+    if constexpr (FETCH) {
+      __syncwarp();
+      if (more(ahead)) {
+        float f;
+        load(place(ahead.group), ahead.tile, cz, rg, rh, f);
+        if (stage == 0) flags[0] = f;
+        else flags[1] = f;
+        advance(ahead);
+      }
+      fetch_commit();
+      stage ^= 1;
+    }
+    advance(at);
+  }
+}
+
+// Joins the tiles' maps along the sequence: a block takes 32 channels, its
+// warps consecutive runs of kRun tiles, round after round.  Forward it leaves
+// the state entering each tile in carry; backward, what reaches each tile's last
+// state from later tiles as value 2 of the tile.
+constexpr int kRun = 8, kJoinWarps = 16;
+template <typename T, bool BACK>
+__global__ void __launch_bounds__(kJoinWarps* kWarp) scan_join_kernel(const ScanArgs s) {
+  __shared__ float sa[kJoinWarps][kWarp], sb[kJoinWarps][kWarp];
+  pdl_wait();
+  const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp;
+  const int64_t c = (int64_t)blockIdx.x * kWarp + lane;
+  const bool ok = c < s.C;
+  const Channel e = channel(s, ok ? (unsigned)c : 0);
+  const int n = e.n, j = e.j;
+  const int64_t tiles = (s.T + PPO_SCAN_BLOCK - 1) / PPO_SCAN_BLOCK;
+  T* out = static_cast<T*>(s.out) + n * s.ldo + j;
+  const int64_t need = value_rows<T>(1);
+  // maps 0 .. tiles - 2 forward (what enters tile 0 is h0); tiles - 1 .. 1 backward
+  const int64_t maps = tiles - 1;
+  float x = 0.f;
+  if (ok) {
+    if (!BACK) {
+      x = s.h0 ? s.h0[c] : 0.f;
+      if (warp == 0) s.carry[c] = reset_flag(s, 0, n) != 0.f ? 0.f : x;
+    } else {
+      x = s.dhT ? s.dhT[c] : 0.f;
+    }
+  }
+  for (int64_t m0 = 0; m0 < maps; m0 += kJoinWarps * kRun) {
+    float a[kRun], b[kRun];
+    float ta = 1.f, tb = 0.f;
+    const int64_t ostep = opaque(s.N * s.ldo);
+#pragma unroll
+    for (int i = 0; i < kRun; ++i) {
+      const int64_t m = m0 + warp * kRun + i;
+      a[i] = 1.f;
+      b[i] = 0.f;
+      if (ok && m < maps) {
+        const int64_t tile = BACK ? tiles - 1 - m : m, t0 = tile * PPO_SCAN_BLOCK;
+        if (BACK && s.T - t0 < need) {
+          // a last tile too short to hold its map: from its steps
+          for (int64_t t = s.T - 1; t >= t0; --t) {
+            const float pz = (float)static_cast<const T*>(s.p)[(t * s.N + n) * s.ldp + j];
+            const float d = (float)static_cast<const T*>(s.dh)[(t * s.N + n) * s.lddh + j];
+            float z[1], q[1] = {pz};
+            sigmoid<1>(q, z);
+            const bool cut = reset_flag(s, t, n) != 0.f;
+            b[i] = cut ? 0.f : (1.f - z[0]) * (d + b[i]);
+            a[i] = cut ? -1.f : joined(a[i], 1.f - z[0]);
+          }
+        } else {
+          a[i] = get_value<T>(out + t0 * ostep, ostep, 0);
+          b[i] = get_value<T>(out + t0 * ostep, ostep, 1);
+        }
       }
     }
 #pragma unroll
-    for (int i = L - 1; i >= 0; --i) {
-      float c[V], d[V], dz[V], dc[V];
-      to_f32<T, V>(rh[i], c);
-      to_f32<T, V>(rg[i], d);
-      if (t0 + i < s.T) {
+    for (int i = 0; i < kRun; ++i) {
+      tb = apply(a[i], b[i], tb);
+      ta = joined(ta, a[i]);
+    }
+    __syncthreads();
+    sa[warp][lane] = ta;
+    sb[warp][lane] = tb;
+    __syncthreads();
+    float y = x;
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-          const float gg = d[v] + uin[v], a = 1.f - z[i][v];
-          dc[v] = gg * z[i][v];
-          dz[v] = dc[v] * (c[v] - hp[i][v]) * a;
-          uin[v] = (clear >> i) & 1u ? 0.f : a * gg;
-        }
-        if (pl.ok) {
-          *reinterpret_cast<Raw<T, V>*>(oz + (t0 + i) * ostep) = from_f32<T, V>(dz);
-          *reinterpret_cast<Raw<T, V>*>(oh + (t0 + i) * ostep) = from_f32<T, V>(dc);
-        }
+    for (int w = 0; w < kJoinWarps; ++w) {
+      if (w == warp) y = x;
+      x = apply(sa[w][lane], sb[w][lane], x);
+    }
+#pragma unroll
+    for (int i = 0; i < kRun; ++i) {
+      const int64_t m = m0 + warp * kRun + i;
+      y = apply(a[i], b[i], y);
+      if (ok && m < maps) {
+        const int64_t tile = BACK ? tiles - 2 - m : m + 1, t0 = tile * PPO_SCAN_BLOCK;
+        if (BACK) put_value<T>(out + t0 * ostep, ostep, 2, y);
+        else s.carry[tile * s.C + c] = reset_flag(s, t0, n) != 0.f ? 0.f : y;
       }
     }
-    if constexpr (WT == 1) {
-#pragma unroll
-      for (int v = 0; v < V; ++v) u[v] = uin[v];
-    }
   }
-  if (s.last && wt == 0 && rank == 0 && pl.ok) {
-#pragma unroll
-    for (int v = 0; v < V; ++v) s.last[pl.c + v] = u[v];
-  }
-  if constexpr (CLUSTER) cg::this_cluster().sync();
 }
 
 // ---- plan -------------------------------------------------------------------------
-template <typename T, int V, int L, int WT, int WC>
-cudaError_t launch(const ScanArgs& s, bool backward, cudaStream_t st) {
-  const int64_t groups = (s.C + (int64_t)kWarp * V * WC - 1) / ((int64_t)kWarp * V * WC);
-  if (groups > (1ll << 30)) return cudaErrorInvalidValue;
-  const dim3 grid((unsigned)groups), block(WT * WC * kWarp);
-  if (backward) scan_bwd_kernel<T, V, L, WT, WC, false><<<grid, block, 0, st>>>(s);
-  else scan_fwd_kernel<T, V, L, WT, WC, false><<<grid, block, 0, st>>>(s);
+constexpr int kSteps = 8;    // of a warp's block; 16 blocks are a tile of PPO_SCAN_BLOCK
+constexpr int kTileWarps = PPO_SCAN_BLOCK / kSteps;
+constexpr int kWalkSteps = 16, kWalkWarps = 8;
+constexpr int kSms = 152;
+#ifndef WALK
+#define WALK 16
+#endif
+#ifndef SPLIT_GROUPS
+#define SPLIT_GROUPS 304
+#endif
+#ifndef SPLIT_TILES
+#define SPLIT_TILES 4
+#endif
+
+template <typename T, int V, int L, int WT, int WC, int PHASE>
+cudaError_t launch(ScanArgs s, bool backward, cudaStream_t st) {
+  constexpr int per = kWarp * V * WC, threads = WT * WC * kWarp;
+  s.groups = (s.C + per - 1) / per;
+  const auto kernel = backward ? scan_bwd_kernel<T, V, L, WT, WC, PHASE>
+                               : scan_fwd_kernel<T, V, L, WT, WC, PHASE>;
+  const int inputs = backward && PHASE == kWhole ? 3 : 2;
+  const size_t ring = L > 1 && kFetch<T, V> ? (size_t)kStages * inputs * L * threads * 4 : 0;
+  if (ring) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ring);
+    if (e != cudaSuccess) return e;
+  }
+  // with fetched columns the blocks that fit an SM together stay on it and walk
+  const int64_t resident = (int64_t)kSms * std::max(1, threads_per_sm(L) / threads);
+  int64_t grid = ring ? std::min(s.groups, resident) : s.groups;
+  if (s.split) {
+    const int64_t tiles = (s.T + L * WT - 1) / (L * WT);
+    grid = s.groups * std::min(tiles, std::max<int64_t>(1, resident / s.groups));
+  }
+  if (grid > (1ll << 30)) return cudaErrorInvalidValue;
+  kernel<<<(unsigned)grid, threads, ring, st>>>(s);
   return cudaGetLastError();
 }
 
-template <typename T, int V>
-cudaError_t dispatch(const ScanArgs& s, bool backward, cudaStream_t st) {
-  if (s.T == 1) return launch<T, V, 1, 1, 4>(s, backward, st);
-  return launch<T, V, 16, 8, 1>(s, backward, st);
+// Few channels and a long sequence: fewer than one group of channels for every
+// block that the SMs hold, and tiles enough to deal out.  Forward it needs the
+// carry to leave the entering states in.
+template <int V>
+bool splits(const ScanArgs& s, bool backward) {
+  // (the first tile's block may replace dhT while the last one's reads it)
+  if (backward && s.last && s.last == s.dhT) return false;
+  const int64_t groups = (s.C + kWarp * V - 1) / (kWarp * V);
+  return s.carry && groups < SPLIT_GROUPS && s.T >= SPLIT_TILES * PPO_SCAN_BLOCK;
 }
 
-ppo_status run(int32_t dtype, const ScanArgs& s, bool backward, bool pairs, cudaStream_t st) {
+template <typename T, int V>
+cudaError_t dispatch(ScanArgs s, bool backward, cudaStream_t st) {
+  // one step: a thread per channel (pair), nothing to join
+  if (s.T == 1) return launch<T, V, 1, 1, 4, kWhole>(s, backward, st);
+  // enough channels to fill the GPU: forward, a warp walks its channels alone
+  if (!backward && s.C >= (int64_t)kSms * WALK * V * kWarp)
+    return launch<T, V, kWalkSteps, 1, kWalkWarps, kWhole>(s, backward, st);
+  // short sequences: as many warps along time as there are blocks of steps, the
+  // others take more channels
+  if (s.T <= kSteps) return launch<T, V, kSteps, 1, 8, kWhole>(s, backward, st);
+  if (s.T <= 2 * kSteps) return launch<T, V, kSteps, 2, 8, kWhole>(s, backward, st);
+  if (s.T <= 4 * kSteps) return launch<T, V, kSteps, 4, 4, kWhole>(s, backward, st);
+  if (s.T <= 8 * kSteps) return launch<T, V, kSteps, 8, 2, kWhole>(s, backward, st);
+  if (splits<V>(s, backward)) {
+    s.split = 1;
+    cudaError_t e = launch<T, V, kSteps, kTileWarps, 1, kMaps>(s, backward, st);
+    if (e != cudaSuccess) return e;
+    const dim3 grid((unsigned)((s.C + kWarp - 1) / kWarp)), block(kJoinWarps * kWarp);
+    e = backward ? launch_pdl(scan_join_kernel<T, true>, grid, block, 0, st, s)
+                 : launch_pdl(scan_join_kernel<T, false>, grid, block, 0, st, s);
+    if (e != cudaSuccess) return e;
+  }
+  return launch<T, V, kSteps, kTileWarps, 1, kWhole>(s, backward, st);
+}
+
+ppo_status run(int32_t dtype, ScanArgs s, bool backward, bool pairs, bool wide, cudaStream_t st) {
+  s.wide = wide;
   cudaError_t e;
   if (dtype == PPO_DTYPE_F32) e = dispatch<float, 1>(s, backward, st);
   else if (pairs) e = dispatch<__nv_bfloat16, 2>(s, backward, st);
@@ -445,7 +954,7 @@ bool aligned(std::initializer_list<const void*> ptrs, int bytes) {
 
 bool sizes_ok(int64_t T, int64_t N, int64_t H) {
   return T >= 1 && N >= 1 && H >= 1 && H < (1ll << 30) && N < (1ll << 31) && T < (1ll << 31) &&
-         N * H < (1ll << 34);
+         N * H < (1ll << 31) - 4096;
 }
 
 }  // namespace
@@ -476,7 +985,9 @@ ppo_status ppo_gated_scan_forward(int32_t dtype, const void* p, int64_t ldp, con
   s.ldo = ldh;
   s.last = hT;
   s.carry = carry;
-  return run(dtype, s, false, H % 2 == 0 && ldp % 2 == 0 && ldh % 2 == 0 && aligned({p, h}, 4), st);
+  const int piece = 16 / ops::esize(dtype);
+  return run(dtype, s, false, H % 2 == 0 && ldp % 2 == 0 && ldh % 2 == 0 && aligned({p, h}, 4),
+             H % piece == 0 && ldp % piece == 0 && aligned({p}, 16), st);
 }
 
 ppo_status ppo_gated_scan_backward(int32_t dtype, const void* dh, int64_t lddh, const void* p,
@@ -508,8 +1019,9 @@ ppo_status ppo_gated_scan_backward(int32_t dtype, const void* dh, int64_t lddh, 
   s.ldo = lddp;
   s.last = dh0;
   s.carry = const_cast<float*>(carry);
+  const int piece = 16 / ops::esize(dtype);
   return run(dtype, s, true, H % 2 == 0 && ldp % 2 == 0 && lddh % 2 == 0 && lddp % 2 == 0 && aligned({dh, p, dp}, 4),
-             st);
+             H % piece == 0 && ldp % piece == 0 && lddh % piece == 0 && aligned({p, dh}, 16), st);
 }
 
 }  // extern "C"

@@ -50,7 +50,7 @@ constexpr int kThreads = (2 + kEpiWarps) * kWarp;
 // and added in registers, rounded to nearest, while the next window's MMAs fill
 // the other accumulator.
 #ifndef KWIN
-#define KWIN 2
+#define KWIN 8
 #endif
 constexpr int kWindow = KWIN;
 constexpr int kStg = 8192;             // staging of an epilogue warp: two 32-row x 128-byte boxes
