@@ -49,6 +49,8 @@ struct ScanArgs {
   float *last;             // hT, or dh0 (nullable)
   float* carry;            // [ceil(T / 128)][C]: written (nullable), or read
   int64_t groups;          // of channels, one block (warp) each
+  unsigned div_m;          // c / H = c * div_m >> div_s for c < 2^31
+  int div_s;
   int wide;                // rows are read in 16-byte pieces
   int split;               // tiles start from stored entering states (see above)
 };
@@ -126,7 +128,7 @@ struct Channel {
   int n, j;
 };
 __device__ __forceinline__ Channel channel(const ScanArgs& s, unsigned c) {
-  const unsigned n = c / (unsigned)s.H;
+  const unsigned n = (unsigned)((uint64_t)c * s.div_m >> s.div_s);
   return {(int)n, (int)(c - n * (unsigned)s.H)};
 }
 // A lane's channels: V consecutive ones of one environment.
@@ -781,7 +783,7 @@ scan_bwd_kernel(const ScanArgs s) {
 // warps consecutive runs of kRun tiles, round after round.  Forward it leaves
 // the state entering each tile in carry; backward, what reaches each tile's last
 // state from later tiles as value 2 of the tile.
-constexpr int kRun = 8, kJoinWarps = 16;
+constexpr int kRun = 8, kJoinWarps = 32;
 template <typename T, bool BACK>
 __global__ void __launch_bounds__(kJoinWarps* kWarp) scan_join_kernel(const ScanArgs s) {
   __shared__ float sa[kJoinWarps][kWarp], sb[kJoinWarps][kWarp];
@@ -809,6 +811,12 @@ __global__ void __launch_bounds__(kJoinWarps* kWarp) scan_join_kernel(const Scan
     float a[kRun], b[kRun];
     float ta = 1.f, tb = 0.f;
     const int64_t ostep = opaque(s.N * s.ldo);
+    uint32_t cut = 0;   // forward: the state entering the tile after map i is cleared
+    if (!BACK && ok) {
+#pragma unroll
+      for (int i = 0; i < kRun; ++i)
+        cut |= reset_flag(s, (m0 + warp * kRun + i + 1) * PPO_SCAN_BLOCK, n) != 0.f ? 1u << i : 0u;
+    }
 #pragma unroll
     for (int i = 0; i < kRun; ++i) {
       const int64_t m = m0 + warp * kRun + i;
@@ -823,9 +831,9 @@ __global__ void __launch_bounds__(kJoinWarps* kWarp) scan_join_kernel(const Scan
             const float d = (float)static_cast<const T*>(s.dh)[(t * s.N + n) * s.lddh + j];
             float z[1], q[1] = {pz};
             sigmoid<1>(q, z);
-            const bool cut = reset_flag(s, t, n) != 0.f;
-            b[i] = cut ? 0.f : (1.f - z[0]) * (d + b[i]);
-            a[i] = cut ? -1.f : joined(a[i], 1.f - z[0]);
+            const bool gone = reset_flag(s, t, n) != 0.f;
+            b[i] = gone ? 0.f : (1.f - z[0]) * (d + b[i]);
+            a[i] = gone ? -1.f : joined(a[i], 1.f - z[0]);
           }
         } else {
           a[i] = get_value<T>(out + t0 * ostep, ostep, 0);
@@ -855,7 +863,7 @@ __global__ void __launch_bounds__(kJoinWarps* kWarp) scan_join_kernel(const Scan
       if (ok && m < maps) {
         const int64_t tile = BACK ? tiles - 2 - m : m + 1, t0 = tile * PPO_SCAN_BLOCK;
         if (BACK) put_value<T>(out + t0 * ostep, ostep, 2, y);
-        else s.carry[tile * s.C + c] = reset_flag(s, t0, n) != 0.f ? 0.f : y;
+        else s.carry[tile * s.C + c] = (cut >> i) & 1u ? 0.f : y;
       }
     }
   }
@@ -939,6 +947,10 @@ cudaError_t dispatch(ScanArgs s, bool backward, cudaStream_t st) {
 
 ppo_status run(int32_t dtype, ScanArgs s, bool backward, bool pairs, bool wide, cudaStream_t st) {
   s.wide = wide;
+  // ceil(log2 H) + 31 bits: exact for every c of 31 bits
+  s.div_s = 31;
+  while ((1ll << (s.div_s - 31)) < s.H) ++s.div_s;
+  s.div_m = (unsigned)((1ull << s.div_s) / (uint64_t)s.H + 1);
   cudaError_t e;
   if (dtype == PPO_DTYPE_F32) e = dispatch<float, 1>(s, backward, st);
   else if (pairs) e = dispatch<__nv_bfloat16, 2>(s, backward, st);
