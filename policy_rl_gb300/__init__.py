@@ -38,7 +38,7 @@ def library_path() -> str:
 
 
 def _lib():
-    return _abi.load()
+    return _abi._lib or _abi.load()
 
 
 def _ptr(t):
@@ -233,18 +233,36 @@ class RnnContext:
 # ---- operators of a recurrent trunk ---------------------------------------------
 # Matrices may be strided row by row (unit stride within a row); the other
 # arguments are contiguous fp32.  Results go to the tensors the caller passes.
-_DTYPES = None
+# A call on a few rows takes the GPU some 3 us, so these wrappers are written
+# for little work per argument.
+_F32 = None        # torch.float32 (torch is imported by the caller's tensors)
+_DTYPES: dict = {}
+_raw_stream = None
+
+
+def _bind_torch():
+    global _F32, _raw_stream
+    import torch
+    _F32 = torch.float32
+    _DTYPES.update({torch.float32: _abi.DTYPE_F32, torch.bfloat16: _abi.DTYPE_BF16})
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    _raw_stream = raw or (lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
 def _dtype(t) -> int:
-    global _DTYPES
-    if _DTYPES is None:
-        import torch
-        _DTYPES = {torch.float32: _abi.DTYPE_F32, torch.bfloat16: _abi.DTYPE_BF16}
+    if _F32 is None:
+        _bind_torch()
     code = _DTYPES.get(t.dtype)
     if code is None:
         raise ValueError(f"dtype must be float32 or bfloat16, got {t.dtype}")
     return code
+
+
+def _on(stream, t):
+    """The stream's handle: the given one, or the current one of t's device."""
+    if stream is None:
+        return _raw_stream(t.get_device())
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _mat(t, like, shape, name):
@@ -252,8 +270,8 @@ def _mat(t, like, shape, name):
     dimension is a row, the others flatten to rows of one pitch."""
     if t is None:
         return None, 0
-    if t.dtype != like.dtype or tuple(t.shape) != shape or not t.is_cuda:
-        raise ValueError(f"{name}: a CUDA tensor {shape} of {like.dtype} is wanted, got "
+    if t.dtype is not like.dtype or t.shape != shape or not t.is_cuda:
+        raise ValueError(f"{name}: a CUDA tensor {tuple(shape)} of {like.dtype} is wanted, got "
                          f"{tuple(t.shape)} of {t.dtype} on {t.device}")
     if t.is_contiguous():
         return t.data_ptr(), shape[-1]
@@ -268,8 +286,8 @@ def _vec(t, shape, name):
     """Address of a contiguous fp32 argument."""
     if t is None:
         return None
-    if str(t.dtype) != "torch.float32" or tuple(t.shape) != shape or not t.is_cuda:
-        raise ValueError(f"{name}: a CUDA tensor {shape} of float32 is wanted, got "
+    if t.dtype is not _F32 or t.shape != shape or not t.is_cuda:
+        raise ValueError(f"{name}: a CUDA tensor {tuple(shape)} of float32 is wanted, got "
                          f"{tuple(t.shape)} of {t.dtype} on {t.device}")
     if not t.is_contiguous():
         raise ValueError(f"{name}: tensor must be contiguous")
@@ -281,18 +299,24 @@ def _work_of(work):
         return None, 0
     if not work.is_cuda or not work.is_contiguous():
         raise ValueError("work: a contiguous CUDA tensor is wanted")
-    return work.data_ptr(), work.numel() * work.element_size()
+    return work.data_ptr(), work.nbytes
+
+
+def _check(status: int, what: str) -> None:
+    if status:
+        _abi.check(status, what)
 
 
 def ppo_layernorm_forward(x, gamma, beta, y, stats=None, eps=1e-5, stream=None) -> None:
     """y = layer norm of the rows of x [M, D] (see ppo.h); gamma, beta fp32 [D]
     or None; stats fp32 [M, 2], kept for the backward pass."""
-    M, D = shape = tuple(x.shape)
+    code = _dtype(x)
+    M, D = shape = x.shape
     px, ldx = _mat(x, x, shape, "x")
     py, ldy = _mat(y, x, shape, "y")
-    _abi.check(_lib().ppo_layernorm_forward(
-        _dtype(x), px, ldx, M, D, _vec(gamma, (D,), "gamma"), _vec(beta, (D,), "beta"), eps, py,
-        ldy, _vec(stats, (M, 2), "stats"), _stream(stream)), "ppo_layernorm_forward")
+    _check(_lib().ppo_layernorm_forward(
+        code, px, ldx, M, D, _vec(gamma, (D,), "gamma"), _vec(beta, (D,), "beta"), eps, py,
+        ldy, _vec(stats, (M, 2), "stats"), _on(stream, x)), "ppo_layernorm_forward")
 
 
 def ppo_layernorm_backward_workspace_bytes(M: int, D: int) -> int:
@@ -305,16 +329,17 @@ def ppo_layernorm_backward_workspace_bytes(M: int, D: int) -> int:
 def ppo_layernorm_backward(dy, x, gamma, stats, dx, dgamma=None, dbeta=None, dres=None, work=None,
                            stream=None) -> None:
     """dx (+ dres, the residual path's gradient), dgamma, dbeta of the layer norm (see ppo.h)."""
-    M, D = shape = tuple(x.shape)
+    code = _dtype(x)
+    M, D = shape = x.shape
     px, ldx = _mat(x, x, shape, "x")
     pdy, lddy = _mat(dy, x, shape, "dy")
     pr, ldr = _mat(dres, x, shape, "dres")
     pdx, lddx = _mat(dx, x, shape, "dx")
     pw, wb = _work_of(work)
-    _abi.check(_lib().ppo_layernorm_backward(
-        _dtype(x), pdy, lddy, px, ldx, M, D, _vec(gamma, (D,), "gamma"),
+    _check(_lib().ppo_layernorm_backward(
+        code, pdy, lddy, px, ldx, M, D, _vec(gamma, (D,), "gamma"),
         _vec(stats, (M, 2), "stats"), pr, ldr, pdx, lddx, _vec(dgamma, (D,), "dgamma"),
-        _vec(dbeta, (D,), "dbeta"), pw, wb, _stream(stream)), "ppo_layernorm_backward")
+        _vec(dbeta, (D,), "dbeta"), pw, wb, _on(stream, x)), "ppo_layernorm_backward")
 
 
 def ppo_scan_blocks(T: int) -> int:
@@ -327,37 +352,40 @@ def ppo_gated_scan_forward(p, h, h0=None, done=None, done0=None, hT=None, carry=
     """h [T, N, H] from the pre-activations p [T, N, 2H] (see ppo.h); h0, hT
     fp32 [N, H], done fp32 [T, N], done0 fp32 [N], carry fp32
     [ppo_scan_blocks(T), N, H].  hT may be h0."""
-    T, N, H = shape = tuple(h.shape)
+    code = _dtype(h)
+    T, N, H = shape = h.shape
     pp, ldp = _mat(p, h, (T, N, 2 * H), "p")
     ph, ldh = _mat(h, h, shape, "h")
-    _abi.check(_lib().ppo_gated_scan_forward(
-        _dtype(h), pp, ldp, _vec(done, (T, N), "done"), _vec(done0, (N,), "done0"),
+    _check(_lib().ppo_gated_scan_forward(
+        code, pp, ldp, _vec(done, (T, N), "done"), _vec(done0, (N,), "done0"),
         _vec(h0, (N, H), "h0"), T, N, H, ph, ldh, _vec(hT, (N, H), "hT"),
-        _vec(carry, (ppo_scan_blocks(T), N, H), "carry"), _stream(stream)),
+        _vec(carry, (ppo_scan_blocks(T), N, H), "carry"), _on(stream, h)),
         "ppo_gated_scan_forward")
 
 
 def ppo_gated_scan_backward(dh, p, carry, dp, done=None, done0=None, dhT=None, dh0=None,
                             stream=None) -> None:
     """dp [T, N, 2H] and dh0 from dh [T, N, H] and dhT (see ppo.h)."""
-    T, N, H = shape = tuple(dh.shape)
+    code = _dtype(dh)
+    T, N, H = shape = dh.shape
     pd, ldd = _mat(dh, dh, shape, "dh")
     pp, ldp = _mat(p, dh, (T, N, 2 * H), "p")
     po, ldo = _mat(dp, dh, (T, N, 2 * H), "dp")
-    _abi.check(_lib().ppo_gated_scan_backward(
-        _dtype(dh), pd, ldd, pp, ldp, _vec(done, (T, N), "done"), _vec(done0, (N,), "done0"),
+    _check(_lib().ppo_gated_scan_backward(
+        code, pd, ldd, pp, ldp, _vec(done, (T, N), "done"), _vec(done0, (N,), "done0"),
         _vec(carry, (ppo_scan_blocks(T), N, H), "carry"), _vec(dhT, (N, H), "dhT"), T, N, H, po,
-        ldo, _vec(dh0, (N, H), "dh0"), _stream(stream)), "ppo_gated_scan_backward")
+        ldo, _vec(dh0, (N, H), "dh0"), _on(stream, dh)), "ppo_gated_scan_backward")
 
 
 def ppo_linear_workspace_bytes(M: int, N: int, K: int, dtype, ldx: int = 0, ldw: int = 0,
                                ldz: int = 0) -> int:
     """Bytes of workspace for the three products of x [M, K], w [N, K] and
     dz [M, N] (allocate it zeroed; pitches only where the rows are strided)."""
-    import torch
-    code = {torch.float32: _abi.DTYPE_F32, torch.bfloat16: _abi.DTYPE_BF16}.get(dtype, -1)
+    if _F32 is None:
+        _bind_torch()
     n = ctypes.c_size_t()
-    _abi.check(_lib().ppo_linear_workspace_bytes(code, M, N, K, ldx, ldw, ldz, ctypes.byref(n)),
+    _abi.check(_lib().ppo_linear_workspace_bytes(_DTYPES.get(dtype, -1), M, N, K, ldx, ldw,
+                                                 ldz, ctypes.byref(n)),
                "ppo_linear_workspace_bytes")
     return n.value
 
@@ -366,7 +394,8 @@ def ppo_linear_forward(x, w, y, bias=None, act=_abi.ACT_NONE, res=None, pre=None
                        stream=None) -> None:
     """y [M, N] = act(x w^T + bias) + res, x [M, K], w [N, K], bias fp32 [N];
     pre [M, N] takes the pre-activation (see ppo.h)."""
-    M, K = tuple(x.shape)
+    code = _dtype(x)
+    M, K = x.shape
     N = w.shape[0]
     px, ldx = _mat(x, x, (M, K), "x")
     pw, ldw = _mat(w, x, (N, K), "w")
@@ -374,16 +403,17 @@ def ppo_linear_forward(x, w, y, bias=None, act=_abi.ACT_NONE, res=None, pre=None
     py, ldy = _mat(y, x, (M, N), "y")
     pp, ldp = _mat(pre, x, (M, N), "pre")
     pk, wb = _work_of(work)
-    _abi.check(_lib().ppo_linear_forward(
-        _dtype(x), px, ldx, pw, ldw, _vec(bias, (N,), "bias"), act, pr, ldr, M, N, K, py, ldy, pp,
-        ldp, pk, wb, _stream(stream)), "ppo_linear_forward")
+    _check(_lib().ppo_linear_forward(
+        code, px, ldx, pw, ldw, _vec(bias, (N,), "bias"), act, pr, ldr, M, N, K, py, ldy, pp,
+        ldp, pk, wb, _on(stream, x)), "ppo_linear_forward")
 
 
 def ppo_linear_backward_data(dz, w, dx, pre=None, act=_abi.ACT_NONE, res=None, work=None,
                              stream=None) -> None:
     """dx [M, K] = (dz w) * act'(pre) + res; pre [M, K] is the pre-activation
     that the layer's input came from (see ppo.h)."""
-    M, N = tuple(dz.shape)
+    code = _dtype(dz)
+    M, N = dz.shape
     K = w.shape[1]
     pd, ldd = _mat(dz, dz, (M, N), "dz")
     pw, ldw = _mat(w, dz, (N, K), "w")
@@ -391,23 +421,24 @@ def ppo_linear_backward_data(dz, w, dx, pre=None, act=_abi.ACT_NONE, res=None, w
     pr, ldr = _mat(res, dz, (M, K), "res")
     po, ldo = _mat(dx, dz, (M, K), "dx")
     pk, wb = _work_of(work)
-    _abi.check(_lib().ppo_linear_backward_data(
-        _dtype(dz), pd, ldd, pw, ldw, pp, ldp, act, pr, ldr, M, N, K, po, ldo, pk, wb,
-        _stream(stream)), "ppo_linear_backward_data")
+    _check(_lib().ppo_linear_backward_data(
+        code, pd, ldd, pw, ldw, pp, ldp, act, pr, ldr, M, N, K, po, ldo, pk, wb,
+        _on(stream, dz)), "ppo_linear_backward_data")
 
 
 def ppo_linear_backward_weight(dz, x, dw, db=None, accumulate=False, work=None,
                                stream=None) -> None:
     """dw fp32 [N, K] = dz^T x and db fp32 [N] = column sums of dz, or their
     sums with what dw and db hold (see ppo.h)."""
-    M, N = tuple(dz.shape)
+    code = _dtype(dz)
+    M, N = dz.shape
     K = x.shape[1]
     pd, ldd = _mat(dz, dz, (M, N), "dz")
     px, ldx = _mat(x, dz, (M, K), "x")
     pk, wb = _work_of(work)
-    _abi.check(_lib().ppo_linear_backward_weight(
-        _dtype(dz), pd, ldd, px, ldx, M, N, K, _vec(dw, (N, K), "dw"), _vec(db, (N,), "db"),
-        1 if accumulate else 0, pk, wb, _stream(stream)), "ppo_linear_backward_weight")
+    _check(_lib().ppo_linear_backward_weight(
+        code, pd, ldd, px, ldx, M, N, K, _vec(dw, (N, K), "dw"), _vec(db, (N,), "db"),
+        1 if accumulate else 0, pk, wb, _on(stream, dz)), "ppo_linear_backward_weight")
 
 
 def ppo_work_status(work, stream=None) -> None:
