@@ -241,18 +241,92 @@ size_t tc_part_bytes(int64_t I, int64_t J, int64_t R, bool must_split) {
   return p.splits > 1 || must_split ? (size_t)p.splits * I * ((J + 3) / 4 * 4) * 4 : 0;
 }
 
+// dW from its partial products, four columns a thread, and db from the partial
+// column sums (the blocks after the first `wblocks`), all in a fixed order
+__global__ void __launch_bounds__(kFinishThreads)
+finish_weight_kernel(const float* __restrict__ part, int splits, int64_t I, int64_t J, int64_t ldp,
+                     float* __restrict__ dw, const float* __restrict__ sums, int64_t sum_rows,
+                     float* __restrict__ db, int accumulate, int wblocks) {
+  pdl_wait();
+  if ((int)blockIdx.x < wblocks) {
+    const int64_t n4 = I * ldp / 4, n = I * ldp;
+    for (int64_t k = (int64_t)blockIdx.x * kFinishThreads + threadIdx.x; k < n4;
+         k += (int64_t)wblocks * kFinishThreads) {
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+      for (int s = 0; s < splits; ++s) {
+        const float4 x = __ldcg(reinterpret_cast<const float4*>(part + s * n) + k);
+        v.x += x.x;
+        v.y += x.y;
+        v.z += x.z;
+        v.w += x.w;
+      }
+      const int64_t i = 4 * k / ldp, j = 4 * k - i * ldp;
+      float* o = dw + i * J + j;
+      const float vv[4] = {v.x, v.y, v.z, v.w};
+      if (J % 4 == 0 && !accumulate) {
+        *reinterpret_cast<float4*>(o) = v;
+      } else {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (j + q < J) o[q] = accumulate ? o[q] + vv[q] : vv[q];
+      }
+    }
+    return;
+  }
+  __shared__ float part_sum[kFinishThreads / kWarp][kWarp];
+  const int lane = threadIdx.x % kWarp, w = threadIdx.x / kWarp;
+  const int64_t c = (int64_t)(blockIdx.x - wblocks) * kWarp + lane;
+  float t = 0.f;
+  if (c < I) {
+#pragma unroll 4
+    for (int64_t r = w; r < sum_rows; r += kFinishThreads / kWarp) t += __ldcg(sums + r * I + c);
+  }
+  part_sum[w][lane] = t;
+  __syncthreads();
+  if (w == 0 && c < I) {
+    float v = 0.f;
+#pragma unroll
+    for (int q = 0; q < kFinishThreads / kWarp; ++q) v += part_sum[q][lane];
+    db[c] = accumulate ? db[c] + v : v;
+  }
+}
+
 cudaError_t tc_run(const Product& g, const Epilogue& e, char* work, int* err, cudaStream_t st) {
   if (!tc_fits(g)) return cudaErrorInvalidValue;
-  // a gradient that is added to, or whose rows TMA cannot store, is finished from partials
-  const bool must = e.mode == kWeight && (e.accumulate || g.J % 4);
-  const TcPlan plan = tc_plan(g.I, g.J, g.R, must);
-  const bool split = plan.splits > 1 || must;
-  float* part = split ? reinterpret_cast<float*>(work) : nullptr;
-  const cudaError_t x = tc_product(g, e, plan, part, err, num_sms(), st);
-  if (x != cudaSuccess || !split) return x;
+  const TcPlan plan = tc_plan(g.I, g.J, g.R, false);
+  float* part = plan.splits > 1 ? reinterpret_cast<float*>(work) : nullptr;
+  const cudaError_t x = tc_product(g, e, plan, part, nullptr, err, num_sms(), st);
+  if (x != cudaSuccess || !part) return x;
   return launch_finish<__nv_bfloat16>(part, plan.splits, g.I, g.J, (g.J + 3) / 4 * 4, e, st);
 }
 
+// A gradient that is added to, or whose rows TMA cannot store, is finished from
+// partial products even where the sum is not split.
+bool must_finish(int64_t J, int accumulate) { return accumulate || J % 4; }
+size_t tc_sum_bytes(int64_t N, int64_t K, int64_t M, bool must) {
+  const Product g{nullptr, 0, 0, nullptr, 0, 0, N, K, M};
+  return (size_t)(tc_sum_rows(g, tc_plan(N, K, M, must)) * N * 4 + 255) / 256 * 256;
+}
+cudaError_t tc_run_weight(const Product& g, const Epilogue& e, float* db, char* work, int* err,
+                          cudaStream_t st) {
+  if (!tc_fits(g)) return cudaErrorInvalidValue;
+  const bool must = must_finish(g.J, e.accumulate);
+  const TcPlan plan = tc_plan(g.I, g.J, g.R, must);
+  const int64_t rows = tc_sum_rows(g, plan);
+  float* sums = db ? reinterpret_cast<float*>(work) : nullptr;
+  float* part = plan.splits > 1 || must
+                    ? reinterpret_cast<float*>(work + tc_sum_bytes(g.I, g.J, g.R, must))
+                    : nullptr;
+  const cudaError_t x = tc_product(g, e, plan, part, sums, err, num_sms(), st);
+  if (x != cudaSuccess || (!part && !db)) return x;
+  const int64_t ldp = (g.J + 3) / 4 * 4;
+  const int wb = part ? (int)std::min<int64_t>(cdiv(g.I * ldp / 4, kFinishThreads), 8 * kSms) : 0;
+  const int sb = db ? (int)cdiv(g.I, kWarp) : 0;
+  return launch_pdl(finish_weight_kernel, dim3((unsigned)(wb + sb)), dim3(kFinishThreads), 0, st,
+                    (const float*)part, plan.splits, g.I, g.J, ldp, static_cast<float*>(e.out),
+                    (const float*)sums, rows, db, e.accumulate, wb);
+}
 
 template <typename T>
 cudaError_t column_sums(const void* dz, int64_t ld, int64_t M, int64_t N, float* db,
@@ -299,8 +373,8 @@ ppo_status status_of(cudaError_t e) { return e == cudaSuccess ? PPO_OK : PPO_ERR
 // Workspace of one direction: the copies of its two operands (pitches lda,
 // ldb) and the partial products or column sums behind them.
 size_t need(int32_t dtype, int mode, int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb) {
-  const size_t sums = mode == lin::kWeight ? (size_t)(lin::sum_chunks(M, N) * N) * 4 : 0;
   if (dtype == PPO_DTYPE_F32) {
+    const size_t sums = mode == lin::kWeight ? (size_t)(lin::sum_chunks(M, N) * N) * 4 : 0;
     const size_t part = mode == lin::kForward ? lin::split_bytes(M, N, K)
                         : mode == lin::kData  ? lin::split_bytes(M, K, N)
                                               : lin::split_bytes(N, K, M);
@@ -315,7 +389,8 @@ size_t need(int32_t dtype, int mode, int64_t M, int64_t N, int64_t K, int64_t ld
              lin::tc_part_bytes(M, K, N, false);
   }
   return kCtrl + lin::packed_bytes(M, N, lda) + lin::packed_bytes(M, K, ldb) +
-         std::max({lin::tc_part_bytes(N, K, M, false), lin::tc_part_bytes(N, K, M, true), sums});
+         std::max(lin::tc_sum_bytes(N, K, M, false) + lin::tc_part_bytes(N, K, M, false),
+                  lin::tc_sum_bytes(N, K, M, true) + lin::tc_part_bytes(N, K, M, true));
 }
 float* parts(void* work) { return reinterpret_cast<float*>(static_cast<char*>(work) + kCtrl); }
 
@@ -423,10 +498,8 @@ ppo_status ppo_linear_backward_weight(int32_t dtype, const void* dz, int64_t ldd
   cudaError_t err = lin::on_16_bytes(dz, lddz, M, N, free, st);
   if (err == cudaSuccess) err = lin::on_16_bytes(x, ldx, M, K, free, st);
   if (err == cudaSuccess)
-    err = lin::tc_run({dz, 1, lddz, x, 1, ldx, N, K, M}, e, free, static_cast<int*>(work), st);
-  if (err == cudaSuccess && db)
-    err = lin::column_sums<__nv_bfloat16>(dz, lddz, M, N, db, e.accumulate,
-                                          reinterpret_cast<float*>(free), st);
+    err = lin::tc_run_weight({dz, 1, lddz, x, 1, ldx, N, K, M}, e, db, free,
+                             static_cast<int*>(work), st);
   return status_of(err);
 }
 

@@ -43,10 +43,13 @@ struct TcPlan {
 };
 TcPlan tc_plan(int64_t I, int64_t J, int64_t R, bool must_split);
 bool tc_fits(const Product& g);
+// Rows of partial column sums that the weight gradient's kernel leaves.
+int64_t tc_sum_rows(const Product& g, const TcPlan& plan);
 // part: [splits][I][J rounded up to 4] for split products (the epilogue is
-// then finish_kernel's), else nullptr
+// then finish_kernel's), else nullptr; db_part (kWeight, nullable):
+// [tc_sum_rows][I], sums over r of A
 cudaError_t tc_product(const Product& g, const Epilogue& e, const TcPlan& plan, float* part,
-                       int* err, int sms, cudaStream_t st);
+                       float* db_part, int* err, int sms, cudaStream_t st);
 
 }  // namespace lin
 

@@ -11,8 +11,11 @@
 // pair of CTAs, walks over units.  Warp 0 issues TMA loads into a ring of
 // 64-deep stages, warp 1 issues the MMAs into one of two TMEM accumulators,
 // and eight warps drain the other accumulator through the epilogue meanwhile:
-// bias, pre-activation, activation, residual, rounding, and stores through
-// swizzled staging by TMA.
+// bias, pre-activation, activation, residual, rounding.  An epilogue warp works
+// on boxes of 32 rows x 64 columns: the residual or pre_in box comes by TMA two
+// boxes ahead, is overwritten by the result, and leaves by TMA.  In the weight
+// gradient warps 2 and 3 add up the columns of dz from the stages that the MMAs
+// have read, so that db costs no pass of its own.
 //
 // Why pairs: at the full MMA rate a CTA with a 128 x 256 tile would have to
 // take in 48 KB of operands every 512 clocks, more than an SM receives (about
@@ -43,27 +46,28 @@ using ppo::tc::wait_bar;
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr int BM = 128, BK = 64;
 constexpr int kEpiWarps = 8;
-constexpr int kThreads = (2 + kEpiWarps) * kWarp;
+constexpr int kFirstEpi = 4;           // warps 0..3: producer, MMA, column sums
+constexpr int kThreads = (kFirstEpi + kEpiWarps) * kWarp;
+constexpr int kSlots = 3;              // boxes of an epilogue warp
+constexpr int kBox = 4096;             // 32 rows x 128 bytes, 128-byte swizzle
 // The tensor cores truncate their fp32 sums: measured, 7.6e-5 relative after
 // 1,000 16-deep steps.  Sums that stay fp32 (the weight gradient over many
 // thousand rows) are therefore taken out of TMEM every kWindow 64-deep steps
 // and added in registers, rounded to nearest, while the next window's MMAs fill
 // the other accumulator.
-#ifndef KWIN
-#define KWIN 8
-#endif
-constexpr int kWindow = KWIN;
-constexpr int kStg = 8192;             // staging of an epilogue warp: two 32-row x 128-byte boxes
-
+// (Measured at 32,768 rows: error 1.9e-7 and 108 us with windows of 2 steps,
+// 4.8e-7 and 60 us with 8, 4.4e-6 and 58 us with 64.)
+constexpr int kWindow = 8;
 template <int CG, int BN>
 struct TileCfg {
   static constexpr int A_BYTES = BM * BK * 2;
   static constexpr int B_ROWS = BN / CG;
   static constexpr int B_BYTES = B_ROWS * BK * 2;
   static constexpr int STAGE = A_BYTES + B_BYTES;
-  static constexpr int S = 5;
+  static constexpr int S = 4;
   static constexpr int TMEM = 2 * BN;
-  static constexpr size_t SMEM = 1024 + (size_t)S * STAGE + kEpiWarps * (size_t)kStg + 512;
+  static constexpr size_t SMEM =
+      1024 + (size_t)S * STAGE + kEpiWarps * (size_t)(kSlots * kBox) + 512;
   static_assert(SMEM <= 232448, "shared memory per CTA");
 };
 
@@ -76,7 +80,9 @@ struct TcArgs {
   float* part;                   // [splits][I][ldp] partial products (nullable)
   int64_t ldp;
   int tma_out, tma_pre;          // the result (pre) leaves by TMA
+  int tma_in;                    // comes by TMA: 1 the residual, 2 pre_in (0: neither)
   int vec_res, vec_aux;          // residual (pre_in) rows are 16-byte aligned
+  float* db_part;                // [splits * tiles_j][I] column sums of A (nullable)
   int* err;
 };
 
@@ -184,21 +190,70 @@ __device__ __forceinline__ float2 pair_of(const uint4 (&o)[4], int k) {   // ele
   return unpack_bf16x2(w);
 }
 __device__ __forceinline__ void store_plain(void* base, int64_t ld, int64_t row, int64_t c0,
-                                            int64_t cols, bool ok, const float (&v)[32]) {
+                                            int64_t cols, bool ok, const float2 (&v)[16]) {
   if (!ok) return;
   __nv_bfloat16* p = static_cast<__nv_bfloat16*>(base) + row * ld + c0;
 #pragma unroll
-  for (int j = 0; j < 32; ++j)
-    if (c0 + j < cols) p[j] = __float2bfloat16_rn(v[j]);
+  for (int k = 0; k < 16; ++k) {
+    if (c0 + 2 * k < cols) p[2 * k] = __float2bfloat16_rn(v[k].x);
+    if (c0 + 2 * k + 1 < cols) p[2 * k + 1] = __float2bfloat16_rn(v[k].y);
+  }
 }
 
-// The activation with its code known outside the loop over a chunk's values
-template <int ACT>
-__device__ __forceinline__ void act_chunk(float (&v)[32]) {
-#pragma unroll
-  for (int j = 0; j < 32; ++j) v[j] = ops::act_value<true>(ACT, v[j]);
+// Activations of a pair of values, the multiplications and additions packed.
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+__device__ __forceinline__ float2 ex2_pair(float2 u) {
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(u.x) : "f"(u.x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(u.y) : "f"(u.y));
+  return u;
 }
-__device__ __forceinline__ void act_chunk(int act, float (&v)[32]) {
+__device__ __forceinline__ float2 rcp_pair(float2 u) {
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(u.x) : "f"(u.x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(u.y) : "f"(u.y));
+  return u;
+}
+constexpr float kLog2e = 1.4426950408889634f;
+// q = sigmoid(u), u = x (silu) or 2 sqrt(2/pi) (x + 0.044715 x^3) (gelu); e = 2^(-u log2 e)
+template <int ACT>
+__device__ __forceinline__ void gate_pair(float2 x, float2& q, float2& e, float2& x2) {
+  float2 u;
+  if constexpr (ACT == PPO_ACT_GELU) {
+    x2 = fmul2(x, x);
+    u = fmul2(x, ffma2(x2, both(-kLog2e * ops::kGeluU * ops::kGeluA), both(-kLog2e * ops::kGeluU)));
+  } else {
+    u = fmul2(x, both(-kLog2e));
+  }
+  e = ex2_pair(u);
+  q = rcp_pair(ffma2(e, both(1.f), both(1.f)));
+}
+template <int ACT>
+__device__ __forceinline__ float2 act_pair(float2 x) {
+  if constexpr (ACT == PPO_ACT_SILU || ACT == PPO_ACT_GELU) {
+    float2 q, e, x2;
+    gate_pair<ACT>(x, q, e, x2);
+    return fmul2(x, q);
+  }
+  return make_float2(ops::act_value<true>(ACT, x.x), ops::act_value<true>(ACT, x.y));
+}
+template <int ACT>
+__device__ __forceinline__ float2 slope_pair(float2 x) {
+  if constexpr (ACT == PPO_ACT_SILU || ACT == PPO_ACT_GELU) {
+    // q + x q (1 - q) u'
+    float2 q, e, x2;
+    gate_pair<ACT>(x, q, e, x2);
+    float2 t = ffma2(q, both(-1.f), both(1.f));
+    if constexpr (ACT == PPO_ACT_GELU)
+      t = fmul2(t, ffma2(x2, both(3.f * ops::kGeluU * ops::kGeluA), both(ops::kGeluU)));
+    return ffma2(fmul2(x, t), q, q);
+  }
+  return make_float2(ops::act_slope<true>(ACT, x.x), ops::act_slope<true>(ACT, x.y));
+}
+template <int ACT>
+__device__ __forceinline__ void act_chunk(float2 (&v)[16]) {
+#pragma unroll
+  for (int k = 0; k < 16; ++k) v[k] = act_pair<ACT>(v[k]);
+}
+__device__ __forceinline__ void act_chunk(int act, float2 (&v)[16]) {
   switch (act) {
     case PPO_ACT_TANH: act_chunk<PPO_ACT_TANH>(v); break;
     case PPO_ACT_RELU: act_chunk<PPO_ACT_RELU>(v); break;
@@ -208,15 +263,11 @@ __device__ __forceinline__ void act_chunk(int act, float (&v)[32]) {
   }
 }
 template <int ACT>
-__device__ __forceinline__ void slope_chunk(const uint4 (&aux)[4], float (&v)[32]) {
+__device__ __forceinline__ void slope_chunk(const uint4 (&aux)[4], float2 (&v)[16]) {
 #pragma unroll
-  for (int k = 0; k < 16; ++k) {
-    const float2 x = pair_of(aux, k);
-    v[2 * k] *= ops::act_slope<true>(ACT, x.x);
-    v[2 * k + 1] *= ops::act_slope<true>(ACT, x.y);
-  }
+  for (int k = 0; k < 16; ++k) v[k] = fmul2(v[k], slope_pair<ACT>(pair_of(aux, k)));
 }
-__device__ __forceinline__ void slope_chunk(int act, const uint4 (&aux)[4], float (&v)[32]) {
+__device__ __forceinline__ void slope_chunk(int act, const uint4 (&aux)[4], float2 (&v)[16]) {
   switch (act) {
     case PPO_ACT_TANH: slope_chunk<PPO_ACT_TANH>(aux, v); break;
     case PPO_ACT_RELU: slope_chunk<PPO_ACT_RELU>(aux, v); break;
@@ -225,27 +276,61 @@ __device__ __forceinline__ void slope_chunk(int act, const uint4 (&aux)[4], floa
     default: break;
   }
 }
+// 32 values as the four 16-byte pieces c16.. of row r of a 128-byte-swizzled box
+__device__ __forceinline__ void box_put(uint8_t* box, int r, int c16, const float2 (&v)[16]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint4 o;
+    o.x = pack_bf16x2(v[4 * i].x, v[4 * i].y);
+    o.y = pack_bf16x2(v[4 * i + 1].x, v[4 * i + 1].y);
+    o.z = pack_bf16x2(v[4 * i + 2].x, v[4 * i + 2].y);
+    o.w = pack_bf16x2(v[4 * i + 3].x, v[4 * i + 3].y);
+    *reinterpret_cast<uint4*>(box + r * 128 + (((c16 + i) ^ (r & 7)) << 4)) = o;
+  }
+}
+__device__ __forceinline__ void box_get(const uint8_t* box, int r, int c16, uint4 (&o)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    o[i] = *reinterpret_cast<const uint4*>(box + r * 128 + (((c16 + i) ^ (r & 7)) << 4));
+}
+template <int N>
+__device__ __forceinline__ void bulk_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
 
 template <int CG, int BN, int MODE, bool AMN, bool BMN>
 __global__ void __launch_bounds__(kThreads, 1)
 lin_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
               const __grid_constant__ CUtensorMap tmO, const __grid_constant__ CUtensorMap tmP,
-              const TcArgs p) {
+              const __grid_constant__ CUtensorMap tmI, const TcArgs p) {
   using C = TileCfg<CG, BN>;
   constexpr int S = C::S;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* gbase = smem_raw + (base - raw);
-  uint8_t* stg = gbase + (size_t)S * C::STAGE;
-  uint8_t* ctrl = stg + kEpiWarps * (size_t)kStg;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(ctrl);   // full[S] empty[S] tfull[2] tempty[2] drain
+  uint8_t* boxes = gbase + (size_t)S * C::STAGE;
+  uint8_t* ctrl = boxes + kEpiWarps * (size_t)(kSlots * kBox);
+  // full[S] empty[S] tfull[2] tempty[2] drain summed[S] box[kEpiWarps][kSlots]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(ctrl);
   auto full = [&](int s) { return smem_u32(&bars[s]); };
   auto empty = [&](int s) { return smem_u32(&bars[S + s]); };
   auto tfull = [&](int a) { return smem_u32(&bars[2 * S + a]); };
   auto tempty = [&](int a) { return smem_u32(&bars[2 * S + 2 + a]); };
   const uint32_t drain = smem_u32(&bars[2 * S + 4]);
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(&bars[2 * S + 5]);
+  auto summed = [&](int i) { return smem_u32(&bars[2 * S + 5 + i]); };
+  auto box_bar = [&](int w, int i) { return smem_u32(&bars[3 * S + 5 + w * kSlots + i]); };
+  constexpr int kBars = 3 * S + 5 + kEpiWarps * kSlots;
+  static_assert(kBars * 8 + 16 <= 512, "control block");
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(&bars[kBars]);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
   volatile uint32_t* cnt = reinterpret_cast<volatile uint32_t*>(tslot + 2);   // issued, consumed
 
@@ -261,6 +346,8 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
       mbar_init(tempty(a), CG * kEpiWarps);
     }
     mbar_init(drain, 1);
+    for (int s = 0; s < S; ++s) mbar_init(summed(s), 2);
+    for (int i = 0; i < kEpiWarps * kSlots; ++i) mbar_init(box_bar(0, i), 1);
     *abort_flag = 0;
     cnt[0] = cnt[1] = 0;
     fence_mbar_init();
@@ -291,6 +378,11 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
     kt1 = min(p.k_tiles, kt0 + p.kt_per_split);
   };
 
+  // 128 fp32 sums a thread: the epilogue's two warpgroups take registers from
+  // the first one (56 + 2 x 224 = 3 x 168, the launch's registers a thread)
+  constexpr bool kShift = MODE == kWeight && CG == 2;
+  if (warp < kFirstEpi) {
+  if constexpr (kShift) regs_dec<56>();
   if (warp == 0) {
     if (lane == 0) {
       uint32_t it = 0, ph = 0;
@@ -302,6 +394,7 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
         const int i0 = (ti * CG + (int)rank) * BM, j0 = tj * BN + (int)rank * C::B_ROWS;
         for (int kt = kt0; kt < kt1; ++kt) {
           if (!wait_bar(empty(s), ph ^ 1, g)) { ok = false; break; }
+          if (MODE == kWeight && p.db_part && !wait_bar(summed(s), ph ^ 1, g)) { ok = false; break; }
           if (rank == 0) mbar_arrive_expect_tx(full(s), CG * C::STAGE);
           const uint32_t bar = CG == 2 ? map_rank(full(s), 0) : full(s);
           if constexpr (AMN) {
@@ -363,10 +456,67 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
       }
     }
   } else {
-    const int q = warp & 3, half = (warp - 2) / 4;
+    // column sums of A (MN-major: [2 blocks of 64 columns][64 of the sum][64]):
+    // a warp takes a block, a lane 8 columns of every fourth row.  A tile row's
+    // stages are shared out among its tiles_j tiles.
+    if (MODE == kWeight && p.db_part) {
+      uint32_t ph = 0;
+      int s = 0;
+      bool ok = true;
+      for (int64_t u = group; u < p.units && ok; u += groups) {
+        int ti, tj, kt0, kt1, split;
+        unit_of(u, ti, tj, kt0, kt1, split);
+        float sum[8] = {};
+        int turn = kt0 % p.tiles_j;
+        for (int kt = kt0; kt < kt1; ++kt) {
+          if (!wait_bar(empty(s), ph, g)) { ok = false; break; }
+          if (turn == tj) {
+            const uint8_t* blk = gbase + (size_t)s * C::STAGE + (warp - 2) * 8192;
+            float t[8] = {};
+#pragma unroll
+            for (int r = 0; r < BK; r += 4) {
+              const int k = r + (lane >> 3);
+              const uint4 w = *reinterpret_cast<const uint4*>(
+                  blk + k * 128 + (((lane & 7) ^ (k & 7)) << 4));
+              const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const float2 f = unpack_bf16x2(ww[i]);
+                t[2 * i] += f.x;
+                t[2 * i + 1] += f.y;
+              }
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum[i] += t[i];
+          }
+          if (++turn == p.tiles_j) turn = 0;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(summed(s));
+          if (++s == S) { s = 0; ph ^= 1; }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 8);
+          sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 16);
+        }
+        const int64_t col = (int64_t)(ti * CG + (int)rank) * BM + (warp - 2) * 64 + lane * 8;
+        if (ok && lane < 8) {
+          float* d = p.db_part + ((int64_t)split * p.tiles_j + tj) * p.I;
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (col + i < p.I) d[col + i] = sum[i];
+        }
+      }
+    }
+  }
+  } else {
+    if constexpr (kShift) regs_inc<224>();
+    const int q = warp & 3, we = warp - kFirstEpi, half = we / 4;
     constexpr int PART = BN / 2;                  // columns of an epilogue warp
-    uint8_t* mine = stg + (warp - 2) * kStg;
-    uint32_t n = 0, sc = 0;
+    constexpr int BOXES = PART / 64;              // bf16 boxes of a unit
+    uint8_t* mine = boxes + we * (kSlots * kBox);
+    uint32_t n = 0;      // accumulators read
+    uint32_t sc = 0;     // stores (fp32 boxes, or bf16 boxes without an input) committed
     // one window: TMEM columns of this warp, or false when a wait gave up
     auto window = [&](uint32_t& taddr) {
       const int acc = n & 1;
@@ -386,6 +536,38 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
       }
       ++n;
     };
+    // the next slot of the ring, once the store that used it last has read it
+    auto slot = [&]() {
+      if (lane == 0) bulk_wait_read<kSlots - 1>();
+      __syncwarp();
+      return mine + (sc++ % kSlots) * kBox;
+    };
+    // input boxes: lane 0 keeps two of them in flight
+    int64_t in_u = group;
+    int in_box = 0;
+    uint32_t in_sent = 0, in_used = 0;
+    auto send = [&]() {
+      while (in_u < p.units) {
+        int ti, tj, kt0, kt1, split;
+        unit_of(in_u, ti, tj, kt0, kt1, split);
+        const int64_t r0 = (int64_t)(ti * CG + (int)rank) * BM + q * 32;
+        const int64_t c0 = (int64_t)tj * BN + half * PART + 64 * in_box;
+        if (++in_box == BOXES) {
+          in_box = 0;
+          in_u += groups;
+        }
+        if (r0 >= p.I || c0 >= p.J) continue;   // (nothing there: not awaited either)
+        const int i = in_sent % kSlots;
+        mbar_arrive_expect_tx(box_bar(we, i), kBox);
+        tma_load_2d(smem_u32(mine + i * kBox), &tmI, (int)c0, (int)r0, box_bar(we, i));
+        ++in_sent;
+        return;
+      }
+    };
+    if (MODE != kWeight && p.tma_in && lane == 0) {
+      send();
+      send();
+    }
     for (int64_t u = group; u < p.units; u += groups) {
       int ti, tj, kt0, kt1, split;
       unit_of(u, ti, tj, kt0, kt1, split);
@@ -399,39 +581,37 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
         bool ok = true;
         for (int w0 = kt0; w0 < kt1; w0 += p.window) {
           if (!window(taddr)) { ok = false; break; }
-          uint32_t r[32];
-          tmem_ld32_async(taddr, r);
+          uint32_t r[2][32];
+          tmem_ld32_async(taddr, r[0]);
 #pragma unroll
           for (int c = 0; c < PART / 32; ++c) {
-            tmem_wait_ld(r);
+            tmem_wait_ld(r[c & 1]);
+            if (c + 1 < PART / 32) tmem_ld32_async(taddr + (uint32_t)(32 * (c + 1)), r[(c + 1) & 1]);
             if (w0 == kt0) {
 #pragma unroll
-              for (int j = 0; j < 32; ++j) v[c][j] = __uint_as_float(r[j]);
+              for (int j = 0; j < 32; ++j) v[c][j] = __uint_as_float(r[c & 1][j]);
             } else {
 #pragma unroll
-              for (int j = 0; j < 32; ++j) v[c][j] += __uint_as_float(r[j]);
+              for (int j = 0; j < 32; ++j) v[c][j] += __uint_as_float(r[c & 1][j]);
             }
-            if (c + 1 < PART / 32) tmem_ld32_async(taddr + (uint32_t)(32 * (c + 1)), r);
           }
           release();
         }
         if (!ok) break;
-        // 32 columns (128 bytes) at a time through two boxes
+        // 32 columns (128 bytes) at a time
 #pragma unroll
-        for (int c = 0; c < PART / 32; ++c, ++sc) {
+        for (int c = 0; c < PART / 32; ++c) {
           const int64_t cc = col0 + 32 * c;
           if (p.tma_out) {
-            uint8_t* buf = mine + (sc & 1) * 4096;
-            if (lane == 0) bulk_wait_read1();
-            __syncwarp();
+            uint8_t* buf = slot();
 #pragma unroll
             for (int i = 0; i < 8; ++i)
               *reinterpret_cast<float4*>(buf + lane * 128 + ((i ^ (lane & 7)) << 4)) =
                   make_float4(v[c][4 * i], v[c][4 * i + 1], v[c][4 * i + 2], v[c][4 * i + 3]);
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0 && any && cc < p.J) {
-              tma_store_3d(&tmO, smem_u32(buf), (int)cc, (int)row0, split);
+            if (lane == 0) {
+              if (any && cc < p.J) tma_store_3d(&tmO, smem_u32(buf), (int)cc, (int)row0, split);
               bulk_commit();
             }
           } else if (rok) {
@@ -447,50 +627,76 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
         const bool use_res = p.e.res != nullptr;
         const bool use_aux = MODE == kData && p.e.act != PPO_ACT_NONE;
         const bool use_pre = MODE == kForward && p.e.pre != nullptr;
+        bool ok = true;
 #pragma unroll 1
-        for (int c = 0; c < PART; c += 64, ++sc) {
+        for (int c = 0; c < PART; c += 64) {
           const int64_t c64 = col0 + c;
-          uint8_t* yb = mine + (use_pre ? 4096 : (sc & 1) * 4096);
-          uint8_t* pb = mine;
-          const bool cols = c64 < p.J;
-          if (lane == 0) {      // the buffers' last stores have read them
-            if (use_pre) bulk_wait_read0();
-            else bulk_wait_read1();
+          if (!any || c64 >= p.J) break;
+          uint32_t r[2][32];
+          tmem_ld32_async(taddr + (uint32_t)c, r[0]);
+          // this box's buffer: the input's, or the next of the ring
+          uint8_t* box;
+          if (p.tma_in) {
+            const int i = in_used % kSlots;
+            if (!wait_bar(box_bar(we, i), (in_used / kSlots) & 1, g)) ok = false;
+            ++in_used;
+            box = mine + i * kBox;
+          } else {
+            box = slot();
           }
-          __syncwarp();
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) {
+            tmem_wait_ld(r[0]);
+            break;
+          }
 #pragma unroll
           for (int hh = 0; hh < 2; ++hh) {
             const int64_t cc = c64 + 32 * hh;
-            uint32_t r[32];
-            tmem_ld32_async(taddr + (uint32_t)(c + 32 * hh), r);
             uint4 rs[4], ax[4];
-            if (use_res) load_row32(p.e.res, p.e.ldres, row, cc, p.J, rok, p.vec_res, rs);
-            if (use_aux) load_row32(p.e.pre, p.e.ldpre, row, cc, p.J, rok, p.vec_aux, ax);
-            float v[32];
-            tmem_wait_ld(r);
-#pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
+            if (use_res) {
+              if (p.tma_in == 1) box_get(box, lane, 4 * hh, rs);
+              else load_row32(p.e.res, p.e.ldres, row, cc, p.J, rok, p.vec_res, rs);
+            }
+            if (use_aux) {
+              if (p.tma_in == 2) box_get(box, lane, 4 * hh, ax);
+              else load_row32(p.e.pre, p.e.ldpre, row, cc, p.J, rok, p.vec_aux, ax);
+            }
+            float2 bi[16];
             if constexpr (MODE == kForward) {
-              if (p.e.bias) {
-                if (cc + 32 <= p.J) {
-                  const float4* b4 = reinterpret_cast<const float4*>(p.e.bias + cc);
+              if (p.e.bias && cc + 32 <= p.J) {
+                const float4* b4 = reinterpret_cast<const float4*>(p.e.bias + cc);
 #pragma unroll
-                  for (int j = 0; j < 8; ++j) {
-                    const float4 b = __ldg(b4 + j);
-                    v[4 * j] += b.x;
-                    v[4 * j + 1] += b.y;
-                    v[4 * j + 2] += b.z;
-                    v[4 * j + 3] += b.w;
-                  }
-                } else {
-#pragma unroll
-                  for (int j = 0; j < 32; ++j)
-                    if (cc + j < p.J) v[j] += __ldg(p.e.bias + cc + j);
+                for (int j = 0; j < 8; ++j) {
+                  const float4 b = __ldg(b4 + j);
+                  bi[2 * j] = make_float2(b.x, b.y);
+                  bi[2 * j + 1] = make_float2(b.z, b.w);
                 }
+              } else {
+#pragma unroll
+                for (int k = 0; k < 16; ++k)
+                  bi[k] = make_float2(
+                      p.e.bias && cc + 2 * k < p.J ? __ldg(p.e.bias + cc + 2 * k) : 0.f,
+                      p.e.bias && cc + 2 * k + 1 < p.J ? __ldg(p.e.bias + cc + 2 * k + 1) : 0.f);
               }
+            }
+            tmem_wait_ld(r[hh]);
+            if (hh == 0) tmem_ld32_async(taddr + (uint32_t)(c + 32), r[1]);
+            float2 v[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+              v[k] = make_float2(__uint_as_float(r[hh][2 * k]), __uint_as_float(r[hh][2 * k + 1]));
+            if constexpr (MODE == kForward) {
+#pragma unroll
+              for (int k = 0; k < 16; ++k) v[k] = ffma2(v[k], both(1.f), bi[k]);
               if (use_pre) {
-                if (p.tma_pre) put_row_chunks(pb + lane * 128, lane, 4 * hh, v);
-                else store_plain(p.e.pre, p.e.ldpre, row, cc, p.J, rok, v);
+                if (p.tma_pre) {
+                  // pre goes out from a box of its own, both halves of it
+                  uint32_t* keep = r[0];
+#pragma unroll
+                  for (int k = 0; k < 16; ++k) keep[16 * hh + k] = pack_bf16x2(v[k].x, v[k].y);
+                } else {
+                  store_plain(p.e.pre, p.e.ldpre, row, cc, p.J, rok, v);
+                }
               }
               act_chunk(p.e.act, v);
             } else {
@@ -498,26 +704,45 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
             }
             if (use_res) {
 #pragma unroll
-              for (int k = 0; k < 16; ++k) {
-                const float2 x = pair_of(rs, k);
-                v[2 * k] += x.x;
-                v[2 * k + 1] += x.y;
-              }
+              for (int k = 0; k < 16; ++k) v[k] = ffma2(v[k], both(1.f), pair_of(rs, k));
             }
-            if (p.tma_out) put_row_chunks(yb + lane * 128, lane, 4 * hh, v);
+            if (p.tma_out) box_put(box, lane, 4 * hh, v);
             else store_plain(p.e.out, p.e.ldo, row, cc, p.J, rok, v);
           }
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0 && any && cols) {
-            if (use_pre && p.tma_pre) tma_store_2d(&tmP, smem_u32(pb), (int)c64, (int)row0);
-            if (p.tma_out) tma_store_2d(&tmO, smem_u32(yb), (int)c64, (int)row0);
+          if (lane == 0) {
+            if (p.tma_out) tma_store_2d(&tmO, smem_u32(box), (int)c64, (int)row0);
             bulk_commit();
+            if (p.tma_in) {
+              bulk_wait_read1();   // the box before this one has left: its slot takes the next input
+              send();
+            }
+          }
+          if (use_pre && p.tma_pre) {
+            uint8_t* pb = p.tma_in ? nullptr : slot();
+            if (pb) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                *reinterpret_cast<uint4*>(pb + lane * 128 + ((i ^ (lane & 7)) << 4)) =
+                    make_uint4(r[0][4 * i], r[0][4 * i + 1], r[0][4 * i + 2], r[0][4 * i + 3]);
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) {
+                tma_store_2d(&tmP, smem_u32(pb), (int)c64, (int)row0);
+                bulk_commit();
+              }
+            }
           }
         }
+        if (!ok) break;
+        release();
       }
-      if constexpr (MODE != kWeight) release();
     }
+    // input boxes that were sent but not used (after an abort)
+    if (MODE != kWeight && p.tma_in && lane == 0)
+      for (; in_used < in_sent; ++in_used)
+        drain_wait(box_bar(we, in_used % kSlots), (in_used / kSlots) & 1, kWaitNs);
     if (lane == 0) bulk_wait0();   // this warp's stores are complete before the CTA exits
   }
 
@@ -561,7 +786,7 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
 template <int CG, int BN, int MODE, bool AMN, bool BMN>
 cudaError_t launch(const Product& g, TcArgs p, int sms, cudaStream_t st) {
   using C = TileCfg<CG, BN>;
-  CUtensorMap ta, tb, to, tp;
+  CUtensorMap ta, tb, to, tp, ti;
   cudaError_t e;
   if (AMN) e = tc_make_tmap(&ta, g.A, g.I, g.R, g.sar, 64, BK);
   else e = tc_make_tmap(&ta, g.A, g.R, g.I, g.sai, BK, BM);
@@ -571,6 +796,12 @@ cudaError_t launch(const Product& g, TcArgs p, int sms, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   to = ta;
   tp = ta;
+  ti = ta;
+  if (p.tma_in) {
+    e = p.tma_in == 1 ? tc_make_tmap(&ti, p.e.res, p.J, p.I, p.e.ldres, 64, 32)
+                      : tc_make_tmap(&ti, p.e.pre, p.J, p.I, p.e.ldpre, 64, 32);
+    if (e != cudaSuccess) return e;
+  }
   if (p.tma_out) {
     if (MODE == kWeight) {
       const int64_t splits = (p.k_tiles + p.kt_per_split - 1) / p.kt_per_split;
@@ -610,7 +841,7 @@ cudaError_t launch(const Product& g, TcArgs p, int sms, cudaStream_t st) {
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = CG == 2 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kernel, ta, tb, to, tp, p);
+  return cudaLaunchKernelEx(&cfg, kernel, ta, tb, to, tp, ti, p);
 }
 
 template <int CG, int BN>
@@ -667,8 +898,12 @@ bool tc_fits(const Product& g) {
          cdiv(g.I, BM) * cdiv(g.J, 128) < (1ll << 31);
 }
 
+int64_t tc_sum_rows(const Product& g, const TcPlan& plan) {
+  return (int64_t)plan.splits * cdiv(g.J, plan.cg == 2 ? 256 : 128);
+}
+
 cudaError_t tc_product(const Product& g, const Epilogue& e, const TcPlan& plan, float* part,
-                       int* err, int sms, cudaStream_t st) {
+                       float* db_part, int* err, int sms, cudaStream_t st) {
   TcArgs p{};
   p.I = g.I;
   p.J = g.J;
@@ -688,6 +923,13 @@ cudaError_t tc_product(const Product& g, const Epilogue& e, const TcPlan& plan, 
   p.tma_pre = !part && e.mode == kForward && e.pre && al(e.pre, e.ldpre, 8);
   p.vec_res = al(e.res, e.ldres, 8);
   p.vec_aux = al(e.pre, e.ldpre, 8);
+  p.db_part = db_part;
+  // one input box at a time: pre_in before the residual, and the residual only
+  // where pre does not need the ring
+  if (!part && p.tma_out) {
+    if (e.mode == kData && e.act != PPO_ACT_NONE && p.vec_aux) p.tma_in = 2;
+    else if (e.mode != kWeight && e.res && p.vec_res && !(e.mode == kForward && e.pre)) p.tma_in = 1;
+  }
   if (plan.cg == 2) return launch_mode<2, 256>(g, p, e.mode, sms, st);
   return launch_mode<1, 128>(g, p, e.mode, sms, st);
 }
