@@ -9,13 +9,23 @@
 //
 // A unit of work is one output tile (and one slice of the sum); a CTA, or a
 // pair of CTAs, walks over units.  Warp 0 issues TMA loads into a ring of
-// 64-deep stages, warp 1 issues the MMAs into one of two TMEM accumulators,
-// and eight warps drain the other accumulator through the epilogue meanwhile:
-// bias, pre-activation, activation, residual, rounding.  An epilogue warp works
-// on boxes of 32 rows x 64 columns: the residual or pre_in box comes by TMA two
-// boxes ahead, is overwritten by the result, and leaves by TMA.  In the weight
-// gradient warps 2 and 3 add up the columns of dz from the stages that the MMAs
-// have read, so that db costs no pass of its own.
+// 64-deep stages, warp 1 issues the MMAs into one of two TMEM accumulators, and
+// 16 warps (8 for single CTAs) drain the other accumulator through the epilogue
+// meanwhile: bias, pre-activation, activation, residual, rounding.  An epilogue
+// warp owns a box of 32 rows x 64 columns of the tile: the residual or pre_in
+// box comes by TMA while the MMAs run, is overwritten by the result, and leaves
+// by TMA.  In the weight gradient warps 2 and 3 add up the columns of dz from
+// the stages that the MMAs have read, so that db costs no pass of its own.
+//
+// What bounds it: an SM takes in 47 bytes of operands a clock by TMA (measured
+// with and without an epilogue, for long and short sums alike; the full MMA rate
+// would want 64), and the epilogue's boxes share that path and shared memory.
+// 8,192 x 8,192 x 8,192 runs at 1.76 PFLOP/s, 32,768 x 512 -> 2,048 forward in
+// 60 us (41 without an epilogue), with gelu and pre in 83.  Measured and left:
+// stores by the warps themselves, straight from rows in registers (78 us) or
+// through shared memory in whole lines (69); the accumulator held in 64
+// registers so that TMEM is free at once (72: spills); L2 prefetches of the
+// operands by TMA (67: they take the same unit's time).
 //
 // Why pairs: at the full MMA rate a CTA with a 128 x 256 tile would have to
 // take in 48 KB of operands every 512 clocks, more than an SM receives (about
@@ -40,15 +50,11 @@ namespace {
 using namespace ptx;
 using ppo::tc::Guard;
 using ppo::tc::drain_wait;
-using ppo::tc::put_row_chunks;
 using ppo::tc::wait_bar;
 
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr int BM = 128, BK = 64;
-constexpr int kEpiWarps = 8;
 constexpr int kFirstEpi = 4;           // warps 0..3: producer, MMA, column sums
-constexpr int kThreads = (kFirstEpi + kEpiWarps) * kWarp;
-constexpr int kSlots = 3;              // boxes of an epilogue warp
 constexpr int kBox = 4096;             // 32 rows x 128 bytes, 128-byte swizzle
 // The tensor cores truncate their fp32 sums: measured, 7.6e-5 relative after
 // 1,000 16-deep steps.  Sums that stay fp32 (the weight gradient over many
@@ -58,16 +64,22 @@ constexpr int kBox = 4096;             // 32 rows x 128 bytes, 128-byte swizzle
 // (Measured at 32,768 rows: error 1.9e-7 and 108 us with windows of 2 steps,
 // 4.8e-7 and 60 us with 8, 4.4e-6 and 58 us with 64.)
 constexpr int kWindow = 8;
-template <int CG, int BN>
+template <int CG, int BN, int MODE>
 struct TileCfg {
   static constexpr int A_BYTES = BM * BK * 2;
   static constexpr int B_ROWS = BN / CG;
   static constexpr int B_BYTES = B_ROWS * BK * 2;
   static constexpr int STAGE = A_BYTES + B_BYTES;
-  static constexpr int S = 4;
+  // the weight gradient stages no results: its boxes' room goes to the ring
+  // (weight and bias gradient of 32,768 x 512 -> 2,048: 68 us with 5 stages, 60
+  // with 7)
+  static constexpr int S = MODE == kWeight ? 7 : 5;
+  static constexpr int EW = 4 * (BN / 64);   // epilogue warps: 32 rows x 64 columns each
+  static constexpr int THREADS = (kFirstEpi + EW) * kWarp;
+  static constexpr int BOXES = MODE == kWeight ? 0 : EW * kBox;
   static constexpr int TMEM = 2 * BN;
-  static constexpr size_t SMEM =
-      1024 + (size_t)S * STAGE + kEpiWarps * (size_t)(kSlots * kBox) + 512;
+  static constexpr int CTRL = 512;
+  static constexpr size_t SMEM = 1024 + (size_t)S * STAGE + BOXES + CTRL;
   static_assert(SMEM <= 232448, "shared memory per CTA");
 };
 
@@ -75,13 +87,13 @@ struct TcArgs {
   int64_t I, J, R;
   int tiles_i, tiles_j, k_tiles, kt_per_split;
   int window;                    // 64-deep steps that the tensor cores sum before a rounded add
-  int64_t units;                 // tiles * splits
+  int units;                     // tiles * splits
   Epilogue e;
   float* part;                   // [splits][I][ldp] partial products (nullable)
   int64_t ldp;
-  int tma_out, tma_pre;          // the result (pre) leaves by TMA
-  int tma_in;                    // comes by TMA: 1 the residual, 2 pre_in (0: neither)
-  int vec_res, vec_aux;          // residual (pre_in) rows are 16-byte aligned
+  int in;                        // matrix read a unit ahead: 0 none, 1 the residual, 2 pre_in
+  int res_late;                  // the residual is read when it is added
+  int tma_in, tma_out, tma_pre;  // it (the result, pre) moves by TMA
   float* db_part;                // [splits * tiles_j][I] column sums of A (nullable)
   int* err;
 };
@@ -164,40 +176,87 @@ __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t
   }
 }
 
-// 32 consecutive bf16 of a row, zeros from column `cols` on
-__device__ __forceinline__ void load_row32(const void* base, int64_t ld, int64_t row, int64_t c0,
-                                           int64_t cols, bool ok, bool vec, uint4 (&o)[4]) {
-  const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(base) + row * ld + c0;
-  if (vec && c0 + 32 <= cols) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      o[i] = ok ? *reinterpret_cast<const uint4*>(p + 8 * i) : make_uint4(0, 0, 0, 0);
-  } else {
-    uint32_t w[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const uint32_t lo = ok && c0 + 2 * i < cols ? __bfloat16_as_ushort(p[2 * i]) : 0;
-      const uint32_t hi = ok && c0 + 2 * i + 1 < cols ? __bfloat16_as_ushort(p[2 * i + 1]) : 0;
-      w[i] = lo | (hi << 16);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+// Piece c (16 bytes) of row r of a box.
+__device__ __forceinline__ uint8_t* box_piece(uint8_t* box, int r, int c) {
+  return box + r * 128 + ((c ^ (r & 7)) << 4);
+}
+// Boxes that TMA cannot move (rows off 16-byte boundaries): lane l of a warp
+// takes the 16-byte piece l % 8 of rows l / 8, l / 8 + 4, .., element by element.
+// (Not inlined: rare, and the code would only be in the way.)
+__device__ __noinline__ void box_load_slow(uint8_t* box, int lane, const void* base, int64_t ld,
+                                           int64_t row0, int64_t col0, int64_t I, int64_t J) {
+  const int64_t col = col0 + (lane & 7) * 8;
+  for (int r = lane >> 3; r < 32; r += 4) {
+    uint32_t w[4] = {0, 0, 0, 0};
+    const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(base) + (row0 + r) * ld + col;
+    for (int i = 0; i < 8; ++i)
+      if (row0 + r < I && col + i < J)
+        w[i >> 1] |= (uint32_t)__bfloat16_as_ushort(p[i]) << (16 * (i & 1));
+    *reinterpret_cast<uint4*>(box_piece(box, r, lane & 7)) = make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
-__device__ __forceinline__ float2 pair_of(const uint4 (&o)[4], int k) {   // elements 2k, 2k + 1
-  const uint4 q = o[k / 4];
-  const uint32_t w = (k & 3) == 0 ? q.x : (k & 3) == 1 ? q.y : (k & 3) == 2 ? q.z : q.w;
-  return unpack_bf16x2(w);
-}
-__device__ __forceinline__ void store_plain(void* base, int64_t ld, int64_t row, int64_t c0,
-                                            int64_t cols, bool ok, const float2 (&v)[16]) {
-  if (!ok) return;
-  __nv_bfloat16* p = static_cast<__nv_bfloat16*>(base) + row * ld + c0;
-#pragma unroll
-  for (int k = 0; k < 16; ++k) {
-    if (c0 + 2 * k < cols) p[2 * k] = __float2bfloat16_rn(v[k].x);
-    if (c0 + 2 * k + 1 < cols) p[2 * k + 1] = __float2bfloat16_rn(v[k].y);
+// half a box: 16 rows
+__device__ __noinline__ void box_store_slow(uint8_t* half, int lane, void* base, int64_t ld,
+                                            int64_t row0, int64_t col0, int64_t I, int64_t J) {
+  const int64_t col = col0 + (lane & 7) * 8;
+  for (int r = lane >> 3; r < 16; r += 4) {
+    const uint4 v = *reinterpret_cast<const uint4*>(box_piece(half, r, lane & 7));
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    __nv_bfloat16* p = static_cast<__nv_bfloat16*>(base) + (row0 + r) * ld + col;
+    for (int i = 0; i < 8; ++i)
+      if (row0 + r < I && col + i < J)
+        p[i] = __ushort_as_bfloat16((uint16_t)(w[i >> 1] >> (16 * (i & 1))));
   }
+}
+// two consecutive elements of a row, or what there is of them
+__device__ __noinline__ float2 load_pair_slow(const __nv_bfloat16* p, int n) {
+  return make_float2(n > 0 ? (float)p[0] : 0.f, n > 1 ? (float)p[1] : 0.f);
+}
+
+// 16 TMEM lanes x 64 fp32 columns: thread t gets, of every group i of 8 columns,
+// columns 2 (t % 4) and + 1 of rows t / 4 (r[4 i], r[4 i + 1]) and t / 4 + 8
+// (r[4 i + 2], r[4 i + 3]) -- the layout of 8 x 8 matrices of stmatrix, and one
+// in which a thread meets 16 of the 64 columns, so that it needs 16 biases (in
+// rows of 64 columns a thread, the broadcast loads of 64 cost 12 % of the
+// forward product: shared memory and L1 are busy with the operands).
+__device__ __forceinline__ void tmem_ld_16x64(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+  tmem_wait_ld(r);
+}
+// Four 8 x 8 matrices: rows 0..7 and 8..15 of column groups i and i + 1 of half
+// a box (16 rows of 128 bytes).
+__device__ __forceinline__ uint32_t quad_addr(uint8_t* half, int lane, int i) {
+  const int m = lane >> 3;
+  return smem_u32(box_piece(half, (m & 1) * 8 + (lane & 7), i + (m >> 1)));
+}
+__device__ __forceinline__ void quad_put(uint8_t* half, int lane, int i, const uint32_t* w) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(
+                   quad_addr(half, lane, i)),
+               "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+               : "memory");
+}
+__device__ __forceinline__ void quad_get(uint8_t* half, int lane, int i, uint32_t* w) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+               : "r"(quad_addr(half, lane, i))
+               : "memory");
+}
+template <int N>
+__device__ __forceinline__ void bulk_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+// bias[c], bias[c + 1], zeros past J
+__device__ __noinline__ float2 bias_slow(const float* b, int64_t c, int64_t J) {
+  return make_float2(c < J ? b[c] : 0.f, c + 1 < J ? b[c + 1] : 0.f);
 }
 
 // Activations of a pair of values, the multiplications and additions packed.
@@ -263,11 +322,11 @@ __device__ __forceinline__ void act_chunk(int act, float2 (&v)[16]) {
   }
 }
 template <int ACT>
-__device__ __forceinline__ void slope_chunk(const uint4 (&aux)[4], float2 (&v)[16]) {
+__device__ __forceinline__ void slope_chunk(const uint32_t (&aux)[16], float2 (&v)[16]) {
 #pragma unroll
-  for (int k = 0; k < 16; ++k) v[k] = fmul2(v[k], slope_pair<ACT>(pair_of(aux, k)));
+  for (int k = 0; k < 16; ++k) v[k] = fmul2(v[k], slope_pair<ACT>(unpack_bf16x2(aux[k])));
 }
-__device__ __forceinline__ void slope_chunk(int act, const uint4 (&aux)[4], float2 (&v)[16]) {
+__device__ __forceinline__ void slope_chunk(int act, const uint32_t (&aux)[16], float2 (&v)[16]) {
   switch (act) {
     case PPO_ACT_TANH: slope_chunk<PPO_ACT_TANH>(aux, v); break;
     case PPO_ACT_RELU: slope_chunk<PPO_ACT_RELU>(aux, v); break;
@@ -276,26 +335,8 @@ __device__ __forceinline__ void slope_chunk(int act, const uint4 (&aux)[4], floa
     default: break;
   }
 }
-// 32 values as the four 16-byte pieces c16.. of row r of a 128-byte-swizzled box
-__device__ __forceinline__ void box_put(uint8_t* box, int r, int c16, const float2 (&v)[16]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    uint4 o;
-    o.x = pack_bf16x2(v[4 * i].x, v[4 * i].y);
-    o.y = pack_bf16x2(v[4 * i + 1].x, v[4 * i + 1].y);
-    o.z = pack_bf16x2(v[4 * i + 2].x, v[4 * i + 2].y);
-    o.w = pack_bf16x2(v[4 * i + 3].x, v[4 * i + 3].y);
-    *reinterpret_cast<uint4*>(box + r * 128 + (((c16 + i) ^ (r & 7)) << 4)) = o;
-  }
-}
-__device__ __forceinline__ void box_get(const uint8_t* box, int r, int c16, uint4 (&o)[4]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    o[i] = *reinterpret_cast<const uint4*>(box + r * 128 + (((c16 + i) ^ (r & 7)) << 4));
-}
-template <int N>
-__device__ __forceinline__ void bulk_wait_read() {
-  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+__device__ __forceinline__ void prefetch_l2(const void* p) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
 }
 template <int N>
 __device__ __forceinline__ void regs_inc() {
@@ -307,19 +348,19 @@ __device__ __forceinline__ void regs_dec() {
 }
 
 template <int CG, int BN, int MODE, bool AMN, bool BMN>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(TileCfg<CG, BN, MODE>::THREADS, 1)
 lin_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
               const __grid_constant__ CUtensorMap tmO, const __grid_constant__ CUtensorMap tmP,
               const __grid_constant__ CUtensorMap tmI, const TcArgs p) {
-  using C = TileCfg<CG, BN>;
+  using C = TileCfg<CG, BN, MODE>;
   constexpr int S = C::S;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* gbase = smem_raw + (base - raw);
   uint8_t* boxes = gbase + (size_t)S * C::STAGE;
-  uint8_t* ctrl = boxes + kEpiWarps * (size_t)(kSlots * kBox);
-  // full[S] empty[S] tfull[2] tempty[2] drain summed[S] box[kEpiWarps][kSlots]
+  uint8_t* ctrl = boxes + C::BOXES;
+  // full[S] empty[S] tfull[2] tempty[2] drain summed[S] box[EW]
   uint64_t* bars = reinterpret_cast<uint64_t*>(ctrl);
   auto full = [&](int s) { return smem_u32(&bars[s]); };
   auto empty = [&](int s) { return smem_u32(&bars[S + s]); };
@@ -327,9 +368,9 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
   auto tempty = [&](int a) { return smem_u32(&bars[2 * S + 2 + a]); };
   const uint32_t drain = smem_u32(&bars[2 * S + 4]);
   auto summed = [&](int i) { return smem_u32(&bars[2 * S + 5 + i]); };
-  auto box_bar = [&](int w, int i) { return smem_u32(&bars[3 * S + 5 + w * kSlots + i]); };
-  constexpr int kBars = 3 * S + 5 + kEpiWarps * kSlots;
-  static_assert(kBars * 8 + 16 <= 512, "control block");
+  auto box_bar = [&](int w) { return smem_u32(&bars[3 * S + 5 + w]); };
+  constexpr int kBars = 3 * S + 5 + C::EW;
+  static_assert(kBars * 8 + 16 <= C::CTRL, "control block");
   uint32_t* tslot = reinterpret_cast<uint32_t*>(&bars[kBars]);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
   volatile uint32_t* cnt = reinterpret_cast<volatile uint32_t*>(tslot + 2);   // issued, consumed
@@ -343,11 +384,11 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(tfull(a), 1);
-      mbar_init(tempty(a), CG * kEpiWarps);
+      mbar_init(tempty(a), CG * C::EW);
     }
     mbar_init(drain, 1);
     for (int s = 0; s < S; ++s) mbar_init(summed(s), 2);
-    for (int i = 0; i < kEpiWarps * kSlots; ++i) mbar_init(box_bar(0, i), 1);
+    for (int w = 0; w < C::EW; ++w) mbar_init(box_bar(w), 1);
     *abort_flag = 0;
     cnt[0] = cnt[1] = 0;
     fence_mbar_init();
@@ -363,32 +404,31 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
   tc_fence_after();
   const uint32_t tmem = *tslot;
   const Guard g{abort_flag, p.err, kWaitNs};
-  const int64_t group = blockIdx.x / CG, groups = gridDim.x / CG;
-  const int64_t tiles = (int64_t)p.tiles_i * p.tiles_j;
+  const int group = blockIdx.x / CG, groups = gridDim.x / CG;
   pdl_wait();
   pdl_trigger();
   auto sA = [&](int s) { return base + (uint32_t)(s * C::STAGE); };
   auto sB = [&](int s) { return base + (uint32_t)(s * C::STAGE + C::A_BYTES); };
-  auto unit_of = [&](int64_t u, int& ti, int& tj, int& kt0, int& kt1, int& split) {
-    split = (int)(u / tiles);
-    const int64_t t = u - (int64_t)split * tiles;
-    ti = (int)(t / p.tiles_j);
-    tj = (int)(t - (int64_t)ti * p.tiles_j);
+  auto unit_of = [&](int u, int& ti, int& tj, int& kt0, int& kt1, int& split) {
+    const int row = u / p.tiles_j;
+    tj = u - row * p.tiles_j;
+    split = row / p.tiles_i;
+    ti = row - split * p.tiles_i;
     kt0 = split * p.kt_per_split;
     kt1 = min(p.k_tiles, kt0 + p.kt_per_split);
   };
 
-  // 128 fp32 sums a thread: the epilogue's two warpgroups take registers from
-  // the first one (56 + 2 x 224 = 3 x 168, the launch's registers a thread)
-  constexpr bool kShift = MODE == kWeight && CG == 2;
+  // 16 epilogue warps leave 96 registers a thread: their four warpgroups take
+  // some from the first one (64 + 4 x 104 = 5 x 96, the launch's registers)
+  constexpr bool kShift = C::EW == 16;
   if (warp < kFirstEpi) {
-  if constexpr (kShift) regs_dec<56>();
+  if constexpr (kShift) regs_dec<64>();
   if (warp == 0) {
     if (lane == 0) {
       uint32_t it = 0, ph = 0;
       int s = 0;
       bool ok = true;
-      for (int64_t u = group; u < p.units && ok; u += groups) {
+      for (int u = group; u < p.units && ok; u += groups) {
         int ti, tj, kt0, kt1, split;
         unit_of(u, ti, tj, kt0, kt1, split);
         const int i0 = (ti * CG + (int)rank) * BM, j0 = tj * BN + (int)rank * C::B_ROWS;
@@ -428,7 +468,7 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
       uint32_t it = 0, ph = 0, n = 0;
       int s = 0;
       bool ok = true;
-      for (int64_t u = group; u < p.units && ok; u += groups) {
+      for (int u = group; u < p.units && ok; u += groups) {
         int ti, tj, kt0, kt1, split;
         unit_of(u, ti, tj, kt0, kt1, split);
         for (int w0 = kt0; w0 < kt1 && ok; w0 += p.window, ++n) {
@@ -463,7 +503,7 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
       uint32_t ph = 0;
       int s = 0;
       bool ok = true;
-      for (int64_t u = group; u < p.units && ok; u += groups) {
+      for (int u = group; u < p.units && ok; u += groups) {
         int ti, tj, kt0, kt1, split;
         unit_of(u, ti, tj, kt0, kt1, split);
         float sum[8] = {};
@@ -510,19 +550,18 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
     }
   }
   } else {
-    if constexpr (kShift) regs_inc<224>();
-    const int q = warp & 3, we = warp - kFirstEpi, half = we / 4;
-    constexpr int PART = BN / 2;                  // columns of an epilogue warp
-    constexpr int BOXES = PART / 64;              // bf16 boxes of a unit
-    uint8_t* mine = boxes + we * (kSlots * kBox);
+    if constexpr (kShift) regs_inc<104>();
+    const int q = warp & 3, we = warp - kFirstEpi, part = we / 4;
+    constexpr int PART = 64;                      // columns of an epilogue warp
+    uint8_t* box = boxes + we * kBox;
     uint32_t n = 0;      // accumulators read
-    uint32_t sc = 0;     // stores (fp32 boxes, or bf16 boxes without an input) committed
+    uint32_t boxes_in = 0;
     // one window: TMEM columns of this warp, or false when a wait gave up
     auto window = [&](uint32_t& taddr) {
       const int acc = n & 1;
       if (!wait_bar(tfull(acc), (n >> 1) & 1, g)) return false;
       tc_fence_after();
-      taddr = tmem + (uint32_t)(acc * BN + half * PART) + ((uint32_t)(q * 32) << 16);
+      taddr = tmem + (uint32_t)(acc * BN + part * PART) + ((uint32_t)(q * 32) << 16);
       return true;
     };
     // the window's columns are read: the MMAs may overwrite them
@@ -536,44 +575,38 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
       }
       ++n;
     };
-    // the next slot of the ring, once the store that used it last has read it
-    auto slot = [&]() {
-      if (lane == 0) bulk_wait_read<kSlots - 1>();
-      __syncwarp();
-      return mine + (sc++ % kSlots) * kBox;
+    // the input box of unit u (lane 0; nothing where the box is off the matrix)
+    auto send = [&](int u) {
+      if (u >= p.units) return;
+      int ti, tj, kt0, kt1, split;
+      unit_of(u, ti, tj, kt0, kt1, split);
+      const int64_t r0 = (int64_t)(ti * CG + (int)rank) * BM + q * 32;
+      const int64_t c0 = (int64_t)tj * BN + part * PART;
+      if (r0 >= p.I || c0 >= p.J) return;
+      mbar_arrive_expect_tx(box_bar(we), kBox);
+      tma_load_2d(smem_u32(box), &tmI, (int)c0, (int)r0, box_bar(we));
     };
-    // input boxes: lane 0 keeps two of them in flight
-    int64_t in_u = group;
-    int in_box = 0;
-    uint32_t in_sent = 0, in_used = 0;
-    auto send = [&]() {
-      while (in_u < p.units) {
-        int ti, tj, kt0, kt1, split;
-        unit_of(in_u, ti, tj, kt0, kt1, split);
-        const int64_t r0 = (int64_t)(ti * CG + (int)rank) * BM + q * 32;
-        const int64_t c0 = (int64_t)tj * BN + half * PART + 64 * in_box;
-        if (++in_box == BOXES) {
-          in_box = 0;
-          in_u += groups;
-        }
-        if (r0 >= p.I || c0 >= p.J) continue;   // (nothing there: not awaited either)
-        const int i = in_sent % kSlots;
-        mbar_arrive_expect_tx(box_bar(we, i), kBox);
-        tma_load_2d(smem_u32(mine + i * kBox), &tmI, (int)c0, (int)r0, box_bar(we, i));
-        ++in_sent;
-        return;
-      }
+    // this thread's row of unit u's box (nullptr off the matrix)
+    auto ahead = [&](int u) -> const void* {
+      if (u >= p.units) return nullptr;
+      int ti, tj, kt0, kt1, split;
+      unit_of(u, ti, tj, kt0, kt1, split);
+      const int64_t r = (int64_t)(ti * CG + (int)rank) * BM + q * 32 + lane;
+      const int64_t c = (int64_t)tj * BN + part * PART;
+      if (r >= p.I || c >= p.J) return nullptr;
+      return static_cast<const __nv_bfloat16*>(p.in == 1 ? p.e.res : p.e.pre) +
+             r * (p.in == 1 ? p.e.ldres : p.e.ldpre) + c;
     };
-    if (MODE != kWeight && p.tma_in && lane == 0) {
-      send();
-      send();
+    if (MODE != kWeight && p.tma_in) {
+      if (lane == 0) send(group);
+      if (const void* f = ahead(group + groups)) prefetch_l2(f);
     }
-    for (int64_t u = group; u < p.units; u += groups) {
+    for (int u = group; u < p.units; u += groups) {
       int ti, tj, kt0, kt1, split;
       unit_of(u, ti, tj, kt0, kt1, split);
       const int64_t row0 = (int64_t)(ti * CG + (int)rank) * BM + q * 32, row = row0 + lane;
       const bool rok = row < p.I, any = row0 < p.I;
-      const int64_t col0 = (int64_t)tj * BN + half * PART;
+      const int64_t col0 = (int64_t)tj * BN + part * PART;
       uint32_t taddr;
       if constexpr (MODE == kWeight) {
         // the windows' sums are added here, in fp32 with rounding to nearest
@@ -581,168 +614,164 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
         bool ok = true;
         for (int w0 = kt0; w0 < kt1; w0 += p.window) {
           if (!window(taddr)) { ok = false; break; }
-          uint32_t r[2][32];
-          tmem_ld32_async(taddr, r[0]);
 #pragma unroll
           for (int c = 0; c < PART / 32; ++c) {
-            tmem_wait_ld(r[c & 1]);
-            if (c + 1 < PART / 32) tmem_ld32_async(taddr + (uint32_t)(32 * (c + 1)), r[(c + 1) & 1]);
+            uint32_t r[32];
+            tmem_ld32_async(taddr + (uint32_t)(32 * c), r);
+            tmem_wait_ld(r);
             if (w0 == kt0) {
 #pragma unroll
-              for (int j = 0; j < 32; ++j) v[c][j] = __uint_as_float(r[c & 1][j]);
+              for (int j = 0; j < 32; ++j) v[c][j] = __uint_as_float(r[j]);
             } else {
 #pragma unroll
-              for (int j = 0; j < 32; ++j) v[c][j] += __uint_as_float(r[c & 1][j]);
+              for (int j = 0; j < 32; ++j) v[c][j] += __uint_as_float(r[j]);
             }
           }
           release();
         }
         if (!ok) break;
-        // 32 columns (128 bytes) at a time
+        if (row < p.I) {
+          float* o = p.part ? p.part + ((int64_t)split * p.I + row) * p.ldp
+                            : static_cast<float*>(p.e.out) + row * p.e.ldo;
 #pragma unroll
-        for (int c = 0; c < PART / 32; ++c) {
-          const int64_t cc = col0 + 32 * c;
-          if (p.tma_out) {
-            uint8_t* buf = slot();
+          for (int c = 0; c < PART / 32; ++c) {
+            const int64_t cc = col0 + 32 * c;
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              *reinterpret_cast<float4*>(buf + lane * 128 + ((i ^ (lane & 7)) << 4)) =
-                  make_float4(v[c][4 * i], v[c][4 * i + 1], v[c][4 * i + 2], v[c][4 * i + 3]);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-              if (any && cc < p.J) tma_store_3d(&tmO, smem_u32(buf), (int)cc, (int)row0, split);
-              bulk_commit();
+            for (int i = 0; i < 8; ++i) {      // (rows of partials and of dW start on 16 bytes)
+              if (cc + 4 * i + 4 <= p.J) {
+                *reinterpret_cast<float4*>(o + cc + 4 * i) =
+                    make_float4(v[c][4 * i], v[c][4 * i + 1], v[c][4 * i + 2], v[c][4 * i + 3]);
+              } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                  if (cc + 4 * i + j < p.J) o[cc + 4 * i + j] = v[c][4 * i + j];
+              }
             }
-          } else if (rok) {
-            float* o = p.part ? p.part + ((int64_t)split * p.I + row) * p.ldp
-                              : static_cast<float*>(p.e.out) + row * p.e.ldo;
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (cc + j < p.J) o[cc + j] = v[c][j];
           }
         }
       } else {
         if (!window(taddr)) break;
-        const bool use_res = p.e.res != nullptr;
-        const bool use_aux = MODE == kData && p.e.act != PPO_ACT_NONE;
-        const bool use_pre = MODE == kForward && p.e.pre != nullptr;
-        bool ok = true;
-#pragma unroll 1
-        for (int c = 0; c < PART; c += 64) {
-          const int64_t c64 = col0 + c;
-          if (!any || c64 >= p.J) break;
-          uint32_t r[2][32];
-          tmem_ld32_async(taddr + (uint32_t)c, r[0]);
-          // this box's buffer: the input's, or the next of the ring
-          uint8_t* box;
+        const bool there = any && col0 < p.J;
+        if (there && p.in) {
+          bool ok = true;
           if (p.tma_in) {
-            const int i = in_used % kSlots;
-            if (!wait_bar(box_bar(we, i), (in_used / kSlots) & 1, g)) ok = false;
-            ++in_used;
-            box = mine + i * kBox;
+            ok = wait_bar(box_bar(we), boxes_in & 1, g);
+            ++boxes_in;
+            // the rows of the box after the next, towards L2
+            if (const void* f = ahead(u + 2 * groups)) prefetch_l2(f);
           } else {
-            box = slot();
+            if (lane == 0) bulk_wait_read0();
+            __syncwarp();
+            box_load_slow(box, lane, p.in == 1 ? p.e.res : p.e.pre,
+                          p.in == 1 ? p.e.ldres : p.e.ldpre, row0, col0, p.I, p.J);
+            __syncwarp();
           }
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) {
-            tmem_wait_ld(r[0]);
-            break;
-          }
+          if (!__all_sync(0xffffffffu, ok)) break;
+        }
+        float2 bi[8];      // this thread's columns: c8 + 8 i, + 1
+        const int64_t c8 = col0 + 2 * (lane & 3);
+        if constexpr (MODE == kForward) {
 #pragma unroll
-          for (int hh = 0; hh < 2; ++hh) {
-            const int64_t cc = c64 + 32 * hh;
-            uint4 rs[4], ax[4];
-            if (use_res) {
-              if (p.tma_in == 1) box_get(box, lane, 4 * hh, rs);
-              else load_row32(p.e.res, p.e.ldres, row, cc, p.J, rok, p.vec_res, rs);
-            }
-            if (use_aux) {
-              if (p.tma_in == 2) box_get(box, lane, 4 * hh, ax);
-              else load_row32(p.e.pre, p.e.ldpre, row, cc, p.J, rok, p.vec_aux, ax);
-            }
-            float2 bi[16];
-            if constexpr (MODE == kForward) {
-              if (p.e.bias && cc + 32 <= p.J) {
-                const float4* b4 = reinterpret_cast<const float4*>(p.e.bias + cc);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                  const float4 b = __ldg(b4 + j);
-                  bi[2 * j] = make_float2(b.x, b.y);
-                  bi[2 * j + 1] = make_float2(b.z, b.w);
-                }
-              } else {
-#pragma unroll
-                for (int k = 0; k < 16; ++k)
-                  bi[k] = make_float2(
-                      p.e.bias && cc + 2 * k < p.J ? __ldg(p.e.bias + cc + 2 * k) : 0.f,
-                      p.e.bias && cc + 2 * k + 1 < p.J ? __ldg(p.e.bias + cc + 2 * k + 1) : 0.f);
-              }
-            }
-            tmem_wait_ld(r[hh]);
-            if (hh == 0) tmem_ld32_async(taddr + (uint32_t)(c + 32), r[1]);
-            float2 v[16];
-#pragma unroll
-            for (int k = 0; k < 16; ++k)
-              v[k] = make_float2(__uint_as_float(r[hh][2 * k]), __uint_as_float(r[hh][2 * k + 1]));
-            if constexpr (MODE == kForward) {
-#pragma unroll
-              for (int k = 0; k < 16; ++k) v[k] = ffma2(v[k], both(1.f), bi[k]);
-              if (use_pre) {
-                if (p.tma_pre) {
-                  // pre goes out from a box of its own, both halves of it
-                  uint32_t* keep = r[0];
-#pragma unroll
-                  for (int k = 0; k < 16; ++k) keep[16 * hh + k] = pack_bf16x2(v[k].x, v[k].y);
-                } else {
-                  store_plain(p.e.pre, p.e.ldpre, row, cc, p.J, rok, v);
-                }
-              }
-              act_chunk(p.e.act, v);
-            } else {
-              if (use_aux) slope_chunk(p.e.act, ax, v);
-            }
-            if (use_res) {
-#pragma unroll
-              for (int k = 0; k < 16; ++k) v[k] = ffma2(v[k], both(1.f), pair_of(rs, k));
-            }
-            if (p.tma_out) box_put(box, lane, 4 * hh, v);
-            else store_plain(p.e.out, p.e.ldo, row, cc, p.J, rok, v);
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            if (p.tma_out) tma_store_2d(&tmO, smem_u32(box), (int)c64, (int)row0);
-            bulk_commit();
-            if (p.tma_in) {
-              bulk_wait_read1();   // the box before this one has left: its slot takes the next input
-              send();
-            }
-          }
-          if (use_pre && p.tma_pre) {
-            uint8_t* pb = p.tma_in ? nullptr : slot();
-            if (pb) {
-#pragma unroll
-              for (int i = 0; i < 8; ++i)
-                *reinterpret_cast<uint4*>(pb + lane * 128 + ((i ^ (lane & 7)) << 4)) =
-                    make_uint4(r[0][4 * i], r[0][4 * i + 1], r[0][4 * i + 2], r[0][4 * i + 3]);
-              fence_proxy_async_smem();
-              __syncwarp();
-              if (lane == 0) {
-                tma_store_2d(&tmP, smem_u32(pb), (int)c64, (int)row0);
-                bulk_commit();
-              }
-            }
+          for (int i = 0; i < 8; ++i) {
+            bi[i] = make_float2(0.f, 0.f);
+            if (p.e.bias && there)
+              bi[i] = col0 + PART <= p.J
+                          ? __ldg(reinterpret_cast<const float2*>(p.e.bias + c8 + 8 * i))
+                          : bias_slow(p.e.bias, c8 + 8 * i, p.J);
           }
         }
-        if (!ok) break;
-        release();
+        // a half of the box to where it belongs
+        auto leave = [&](uint8_t* half, const CUtensorMap* tm, bool tma, void* base, int64_t ld,
+                         int64_t r0) {
+          if (tma) {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0 && r0 < p.I) tma_store_2d(tm, smem_u32(half), (int)col0, (int)r0);
+          } else {
+            __syncwarp();
+            box_store_slow(half, lane, base, ld, r0, col0, p.I, p.J);
+            __syncwarp();
+          }
+          if (lane == 0) bulk_commit();
+        };
+        // before a half is written: its last store has read it
+        auto vacate = [&]() {
+          if (lane == 0) bulk_wait_read1();
+          __syncwarp();
+        };
+#pragma unroll 1
+        for (int hr = 0; hr < 2; ++hr) {      // 16 rows at a time
+          uint32_t r[32];
+          tmem_ld_16x64(taddr + ((uint32_t)(16 * hr) << 16), r);
+          if (hr == 1) release();
+          if (!there) continue;
+          const int64_t r0 = row0 + 16 * hr;
+          float2 v[16];      // v[2 i + b]: column group i, row lane / 4 + 8 b
+#pragma unroll
+          for (int k = 0; k < 16; ++k)
+            v[k] = make_float2(__uint_as_float(r[2 * k]), __uint_as_float(r[2 * k + 1]));
+          if constexpr (MODE == kForward) {
+#pragma unroll
+            for (int k = 0; k < 16; ++k) v[k] = ffma2(v[k], both(1.f), bi[k / 2]);
+            if (p.e.pre) {
+              vacate();
+#pragma unroll
+              for (int i = 0; i < 8; i += 2) {
+                uint32_t w[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) w[j] = pack_bf16x2(v[2 * i + j].x, v[2 * i + j].y);
+                quad_put(box, lane, i, w);
+              }
+              leave(box, &tmP, p.tma_pre, p.e.pre, p.e.ldpre, r0);
+            }
+            act_chunk(p.e.act, v);
+          }
+          uint8_t* half = p.e.pre && MODE == kForward ? box + 2048 : box + 2048 * hr;
+          if (p.in) {
+            uint32_t x[16];
+#pragma unroll
+            for (int i = 0; i < 8; i += 2) quad_get(half, lane, i, x + 2 * i);
+            if (MODE == kData && p.in == 2) {
+              slope_chunk(p.e.act, x, v);
+            } else {
+#pragma unroll
+              for (int k = 0; k < 16; ++k) v[k] = ffma2(v[k], both(1.f), unpack_bf16x2(x[k]));
+            }
+            __syncwarp();   // all have read the half
+          } else {
+            vacate();
+          }
+          if (p.res_late) {
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              const int64_t rr = r0 + (lane >> 2) + 8 * (k & 1), cc = c8 + 8 * (k / 2);
+              const int left = rr < p.I ? (int)max((int64_t)0, min((int64_t)2, p.J - cc)) : 0;
+              const __nv_bfloat16* rp =
+                  static_cast<const __nv_bfloat16*>(p.e.res) + rr * p.e.ldres + cc;
+              const float2 x = left == 2 && (reinterpret_cast<uintptr_t>(rp) & 3u) == 0
+                                   ? unpack_bf16x2(*reinterpret_cast<const uint32_t*>(rp))
+                                   : load_pair_slow(rp, left);
+              v[k] = ffma2(v[k], both(1.f), x);
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 8; i += 2) {
+            uint32_t w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w[j] = pack_bf16x2(v[2 * i + j].x, v[2 * i + j].y);
+            quad_put(half, lane, i, w);
+          }
+          leave(half, &tmO, p.tma_out, p.e.out, p.e.ldo, r0);
+        }
+        if (p.tma_in && lane == 0) {      // the box takes the next unit's input
+          bulk_wait_read0();
+          send(u + groups);
+        }
       }
     }
-    // input boxes that were sent but not used (after an abort)
-    if (MODE != kWeight && p.tma_in && lane == 0)
-      for (; in_used < in_sent; ++in_used)
-        drain_wait(box_bar(we, in_used % kSlots), (in_used / kSlots) & 1, kWaitNs);
+    // a box that was sent for but not used (after an abort)
+    if (MODE != kWeight && p.tma_in && lane == 0 && *abort_flag)
+      drain_wait(box_bar(we), boxes_in & 1, 1000000ull);
     if (lane == 0) bulk_wait0();   // this warp's stores are complete before the CTA exits
   }
 
@@ -785,7 +814,7 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
 // 64 (sum) x 128 rows, an MN-major one in boxes of 64 (own index) x 64.
 template <int CG, int BN, int MODE, bool AMN, bool BMN>
 cudaError_t launch(const Product& g, TcArgs p, int sms, cudaStream_t st) {
-  using C = TileCfg<CG, BN>;
+  using C = TileCfg<CG, BN, MODE>;
   CUtensorMap ta, tb, to, tp, ti;
   cudaError_t e;
   if (AMN) e = tc_make_tmap(&ta, g.A, g.I, g.R, g.sar, 64, BK);
@@ -797,23 +826,17 @@ cudaError_t launch(const Product& g, TcArgs p, int sms, cudaStream_t st) {
   to = ta;
   tp = ta;
   ti = ta;
-  if (p.tma_in) {
-    e = p.tma_in == 1 ? tc_make_tmap(&ti, p.e.res, p.J, p.I, p.e.ldres, 64, 32)
-                      : tc_make_tmap(&ti, p.e.pre, p.J, p.I, p.e.ldpre, 64, 32);
+  if (MODE != kWeight && p.tma_out) {
+    e = tc_make_tmap(&to, p.e.out, p.J, p.I, p.e.ldo, 64, 16);
     if (e != cudaSuccess) return e;
   }
-  if (p.tma_out) {
-    if (MODE == kWeight) {
-      const int64_t splits = (p.k_tiles + p.kt_per_split - 1) / p.kt_per_split;
-      e = tc_make_tmap_f32(&to, p.part ? p.part : static_cast<float*>(p.e.out), p.J, p.I,
-                           p.part ? splits : 1, p.part ? p.ldp : p.e.ldo);
-    } else {
-      e = tc_make_tmap(&to, p.e.out, p.J, p.I, p.e.ldo, 64, 32);
-    }
+  if (MODE != kWeight && p.tma_pre) {
+    e = tc_make_tmap(&tp, p.e.pre, p.J, p.I, p.e.ldpre, 64, 16);
     if (e != cudaSuccess) return e;
   }
-  if (p.tma_pre) {
-    e = tc_make_tmap(&tp, p.e.pre, p.J, p.I, p.e.ldpre, 64, 32);
+  if (MODE != kWeight && p.tma_in) {
+    e = p.in == 1 ? tc_make_tmap(&ti, p.e.res, p.J, p.I, p.e.ldres, 64, 32)
+                  : tc_make_tmap(&ti, p.e.pre, p.J, p.I, p.e.ldpre, 64, 32);
     if (e != cudaSuccess) return e;
   }
   const auto kernel = lin_tc_kernel<CG, BN, MODE, AMN, BMN>;
@@ -829,7 +852,7 @@ cudaError_t launch(const Product& g, TcArgs p, int sms, cudaStream_t st) {
   const int64_t groups = std::min<int64_t>(p.units, sms / CG);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(groups * CG));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(C::THREADS);
   cfg.dynamicSmemBytes = C::SMEM;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
@@ -895,7 +918,7 @@ bool tc_fits(const Product& g) {
   // TMA coordinates and tile counts are 32-bit
   constexpr int64_t top = (1ll << 31) - 512;
   return g.I < top && g.J < top && g.R < top &&
-         cdiv(g.I, BM) * cdiv(g.J, 128) < (1ll << 31);
+         cdiv(g.I, BM) * cdiv(g.J, 128) < (1ll << 30);
 }
 
 int64_t tc_sum_rows(const Product& g, const TcPlan& plan) {
@@ -913,23 +936,22 @@ cudaError_t tc_product(const Product& g, const Epilogue& e, const TcPlan& plan, 
   p.k_tiles = (int)cdiv(g.R, BK);
   p.kt_per_split = plan.kt_per_split;
   p.window = e.mode == kWeight ? kWindow : p.k_tiles;
-  p.units = (int64_t)p.tiles_i * p.tiles_j * plan.splits;
+  const int64_t units = (int64_t)p.tiles_i * p.tiles_j * plan.splits;
+  if (units > (1ll << 30)) return cudaErrorInvalidValue;
+  p.units = (int)units;
   p.e = e;
   p.part = part;
   p.ldp = (g.J + 3) / 4 * 4;
   p.err = err;
   auto al = [](const void* q, int64_t ld, int m) { return ops::al16(q) && ld % m == 0; };
-  p.tma_out = part ? 1 : e.mode == kWeight ? al(e.out, e.ldo, 4) : al(e.out, e.ldo, 8);
-  p.tma_pre = !part && e.mode == kForward && e.pre && al(e.pre, e.ldpre, 8);
-  p.vec_res = al(e.res, e.ldres, 8);
-  p.vec_aux = al(e.pre, e.ldpre, 8);
-  p.db_part = db_part;
-  // one input box at a time: pre_in before the residual, and the residual only
-  // where pre does not need the ring
-  if (!part && p.tma_out) {
-    if (e.mode == kData && e.act != PPO_ACT_NONE && p.vec_aux) p.tma_in = 2;
-    else if (e.mode != kWeight && e.res && p.vec_res && !(e.mode == kForward && e.pre)) p.tma_in = 1;
+  p.tma_out = al(e.out, e.ldo, 8);
+  p.tma_pre = e.mode == kForward && e.pre && al(e.pre, e.ldpre, 8);
+  if (!part && e.mode != kWeight) {
+    p.in = e.mode == kData && e.act != PPO_ACT_NONE ? 2 : e.res && !e.pre ? 1 : 0;
+    p.tma_in = p.in == 1 ? al(e.res, e.ldres, 8) : p.in == 2 && al(e.pre, e.ldpre, 8);
+    p.res_late = e.res && p.in != 1;
   }
+  p.db_part = db_part;
   if (plan.cg == 2) return launch_mode<2, 256>(g, p, e.mode, sms, st);
   return launch_mode<1, 128>(g, p, e.mode, sms, st);
 }
