@@ -30,41 +30,107 @@ __device__ __forceinline__ float at(const void* p, int64_t i) {
   return (float)static_cast<const T*>(p)[i];
 }
 
-// One output element from its finished sum.
+// n (<= 4) consecutive elements of a row, in one piece where rows allow it
 template <typename T>
-__device__ __forceinline__ void finish_one(const Epilogue& e, float v, int64_t i, int64_t j) {
+__device__ __forceinline__ void get4(const void* p, int64_t at, int n, bool vec, float (&f)[4]) {
+  const T* q = static_cast<const T*>(p) + at;
+  if (vec && n == 4) {
+    to_f32<T, 4>(*reinterpret_cast<const Raw<T, 4>*>(q), f);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = i < n ? (float)q[i] : 0.f;
+  }
+}
+template <typename T>
+__device__ __forceinline__ void put4(void* p, int64_t at, int n, bool vec, const float (&f)[4]) {
+  T* q = static_cast<T*>(p) + at;
+  if (vec && n == 4) {
+    *reinterpret_cast<Raw<T, 4>*>(q) = from_f32<T, 4>(f);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < n) round_to(f[i], q[i]);
+  }
+}
+
+// n (<= 4) output elements of row i from column j on, from their finished sums.
+// vec: pieces of four elements are aligned in every matrix.
+template <typename T>
+__device__ __forceinline__ void finish4(const Epilogue& e, float (&v)[4], int64_t i, int64_t j,
+                                        int n, bool vec) {
+  float x[4];
   if (e.mode == kWeight) {
-    float* d = static_cast<float*>(e.out) + i * e.ldo + j;
-    *d = e.accumulate ? *d + v : v;
+    if (e.accumulate) {
+      get4<float>(e.out, i * e.ldo + j, n, vec, x);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) v[q] += x[q];
+    }
+    put4<float>(e.out, i * e.ldo + j, n, vec, v);
     return;
   }
   if (e.mode == kForward) {
-    if (e.bias) v += __ldg(e.bias + j);
-    if (e.pre) round_to(v, static_cast<T*>(e.pre)[i * e.ldpre + j]);
-    v = act_value<false>(e.act, v);
+    if (e.bias) {
+      get4<float>(e.bias, j, n, j % 4 == 0, x);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) v[q] += x[q];
+    }
+    if (e.pre) put4<T>(e.pre, i * e.ldpre + j, n, vec, v);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) v[q] = act_value<false>(e.act, v[q]);
   } else if (e.act != PPO_ACT_NONE) {
-    v *= act_slope<false>(e.act, at<T>(e.pre, i * e.ldpre + j));
+    get4<T>(e.pre, i * e.ldpre + j, n, vec, x);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) v[q] *= act_slope<false>(e.act, x[q]);
   }
-  if (e.res) v += at<T>(e.res, i * e.ldres + j);
-  round_to(v, static_cast<T*>(e.out)[i * e.ldo + j]);
+  if (e.res) {
+    get4<T>(e.res, i * e.ldres + j, n, vec, x);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) v[q] += x[q];
+  }
+  put4<T>(e.out, i * e.ldo + j, n, vec, v);
 }
 
-// out = epilogue of the sum of the partial products, in split order
+// An fp32 product straight from its operands.  (The planes of an infinity, or of
+// what rounds to one in bf16, do not add up: their products hold NaN where the
+// product may not.)
+__device__ __noinline__ float dot_again(const Product& g, int64_t i, int64_t j) {
+  const float* A = static_cast<const float*>(g.A) + i * g.sai;
+  const float* B = static_cast<const float*>(g.B) + j * g.sbj;
+  float v = 0.f;
+  for (int64_t r = 0; r < g.R; ++r) v = fmaf(A[r * g.sar], B[r * g.sbr], v);
+  return v;
+}
+
+// out = epilogue of the sum of the partial products, in split order, four columns
+// a thread.  g: the fp32 operands of a product of planes (A nullptr: no planes).
 constexpr int kFinishThreads = 256;
 template <typename T>
 __global__ void __launch_bounds__(kFinishThreads)
 finish_kernel(const float* __restrict__ part, int splits, int64_t I, int64_t J, int64_t ldp,
-              const Epilogue e) {
+              const Epilogue e, int vec, const Product g) {
   pdl_wait();
-  const int64_t n = I * ldp;
-  for (int64_t k = (int64_t)blockIdx.x * kFinishThreads + threadIdx.x; k < n;
+  const int64_t n = I * ldp, per = ldp / 4, n4 = I * per;
+  for (int64_t k = (int64_t)blockIdx.x * kFinishThreads + threadIdx.x; k < n4;
        k += (int64_t)gridDim.x * kFinishThreads) {
-    const int64_t i = k / ldp, j = k - i * ldp;
-    if (j >= J) continue;
-    float v = 0.f;
-#pragma unroll 4
-    for (int s = 0; s < splits; ++s) v += __ldcg(part + s * n + k);
-    finish_one<T>(e, v, i, j);
+    // (a 64-bit division costs as much as the rest)
+    const int64_t i = n4 < (1ll << 32) ? (int64_t)((uint32_t)k / (uint32_t)per) : k / per;
+    const int64_t j = 4 * (k - i * per);
+    const int cols = (int)min((int64_t)4, J - j);
+    float v[4] = {};
+#pragma unroll 8
+    for (int s = 0; s < splits; ++s) {
+      const float4 x = __ldcg(reinterpret_cast<const float4*>(part + s * n) + k);
+      v[0] += x.x;
+      v[1] += x.y;
+      v[2] += x.z;
+      v[3] += x.w;
+    }
+    if (g.A && !(isfinite(v[0]) && isfinite(v[1]) && isfinite(v[2]) && isfinite(v[3]))) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (q < cols && !isfinite(v[q])) v[q] = dot_again(g, i, j + q);
+    }
+    if (cols > 0) finish4<T>(e, v, i, j, cols, vec);
   }
 }
 
@@ -77,7 +143,8 @@ constexpr int kPer = kTile * kStep / kSimtThreads;
 // AR (BR): the reduction index is the contiguous one of A (B)
 template <typename T, bool AR, bool BR>
 __global__ void __launch_bounds__(kSimtThreads)
-simt_kernel(const Product g, const Epilogue e, float* __restrict__ part, int64_t r_per_split) {
+simt_kernel(const Product g, const Epilogue e, int vec, float* __restrict__ part,
+            int64_t r_per_split) {
   __shared__ float As[kStep][kTile + 4], Bs[kStep][kTile + 4];
   const int64_t i0 = (int64_t)blockIdx.y * kTile, j0 = (int64_t)blockIdx.x * kTile;
   const int64_t r0 = (int64_t)blockIdx.z * r_per_split, r1 = min(g.R, r0 + r_per_split);
@@ -118,15 +185,18 @@ simt_kernel(const Product g, const Epilogue e, float* __restrict__ part, int64_t
     }
     __syncthreads();
   }
+  const int64_t ldp = part_pitch(g.J), oj = j0 + tx * 4;
+  if (oj >= g.J) return;
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int64_t oi = i0 + ty * 4 + i, oj = j0 + tx * 4 + j;
-      if (oi >= g.I || oj >= g.J) continue;
-      if (part) part[(blockIdx.z * g.I + oi) * g.J + oj] = acc[i][j];
-      else finish_one<T>(e, acc[i][j], oi, oj);
-    }
+  for (int i = 0; i < 4; ++i) {
+    const int64_t oi = i0 + ty * 4 + i;
+    if (oi >= g.I) return;
+    if (part)
+      *reinterpret_cast<float4*>(part + (blockIdx.z * g.I + oi) * ldp + oj) =
+          make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+    else
+      finish4<T>(e, acc[i], oi, oj, (int)min((int64_t)4, g.J - oj), vec);
+  }
 }
 
 // ---- column sums --------------------------------------------------------------------
@@ -152,7 +222,7 @@ colsum_kernel(const void* a, int64_t ld, int64_t rows, int64_t cols, int64_t row
     float v = 0.f;
 #pragma unroll
     for (int w = 0; w < kSumThreads / kWarp; ++w) v += s[w][lane];
-    part[blockIdx.y * cols + c] = v;
+    part[blockIdx.y * part_pitch(cols) + c] = v;
   }
 }
 
@@ -172,15 +242,22 @@ int64_t sum_chunks(int64_t M, int64_t N) {
 }
 size_t split_bytes(int64_t I, int64_t J, int64_t R) {
   const int64_t s = simt_splits(I, J, R);
-  return s > 1 ? (size_t)(s * I * J) * 4 : 0;
+  return s > 1 ? (size_t)(s * I * part_pitch(J)) * 4 : 0;
+}
+
+// Whether pieces of four elements are aligned in all matrices of an epilogue
+// (bases are on 16 bytes).
+template <typename T>
+int fours(const Epilogue& e) {
+  return e.ldo % 4 == 0 && (!e.res || e.ldres % 4 == 0) && (!e.pre || e.ldpre % 4 == 0);
 }
 
 template <typename T>
 cudaError_t launch_finish(const float* part, int64_t splits, int64_t I, int64_t J, int64_t ldp,
-                          const Epilogue& e, cudaStream_t st) {
-  const int64_t blocks = std::min<int64_t>(cdiv(I * ldp, kFinishThreads), 8 * kSms);
+                          const Epilogue& e, cudaStream_t st, const Product& g = {}) {
+  const int64_t blocks = std::min<int64_t>(cdiv(I * ldp / 4, kFinishThreads), 16 * kSms);
   return launch_pdl(finish_kernel<T>, dim3((unsigned)blocks), dim3(kFinishThreads), 0, st, part,
-                    (int)splits, I, J, ldp, e);
+                    (int)splits, I, J, ldp, e, fours<T>(e), g);
 }
 
 template <typename T>
@@ -192,12 +269,13 @@ cudaError_t simt_product(const Product& g, const Epilogue& e, float* part, cudaS
   const dim3 grid((unsigned)cdiv(g.J, kTile), (unsigned)cdiv(g.I, kTile), (unsigned)used);
   float* pp = used > 1 ? part : nullptr;
   const bool ar = g.sar == 1, br = g.sbr == 1;
-  if (ar && br) simt_kernel<T, true, true><<<grid, kSimtThreads, 0, st>>>(g, e, pp, per);
-  else if (ar) simt_kernel<T, true, false><<<grid, kSimtThreads, 0, st>>>(g, e, pp, per);
-  else simt_kernel<T, false, false><<<grid, kSimtThreads, 0, st>>>(g, e, pp, per);
+  const int vec = fours<T>(e);
+  if (ar && br) simt_kernel<T, true, true><<<grid, kSimtThreads, 0, st>>>(g, e, vec, pp, per);
+  else if (ar) simt_kernel<T, true, false><<<grid, kSimtThreads, 0, st>>>(g, e, vec, pp, per);
+  else simt_kernel<T, false, false><<<grid, kSimtThreads, 0, st>>>(g, e, vec, pp, per);
   const cudaError_t err = cudaGetLastError();
   if (err != cudaSuccess || used == 1) return err;
-  return launch_finish<T>(pp, used, g.I, g.J, g.J, e, st);
+  return launch_finish<T>(pp, used, g.I, g.J, part_pitch(g.J), e, st);
 }
 
 // ---- bf16 operands on 16-byte rows ---------------------------------------------------
@@ -208,6 +286,9 @@ size_t packed_bytes(int64_t rows, int64_t cols, int64_t ld) {
   if (ld <= 0) ld = cols;
   return ld % 8 ? (size_t)(rows * pitch8(cols) * 2 + 255) / 256 * 256 : 0;
 }
+#ifndef PLANES
+#define PLANES (1ll << 28)
+#endif
 constexpr int kPackThreads = 256;
 __global__ void __launch_bounds__(kPackThreads)
 pack_rows_kernel(const __nv_bfloat16* __restrict__ src, int64_t ld, int64_t rows, int64_t cols,
@@ -236,9 +317,54 @@ cudaError_t on_16_bytes(const void*& a, int64_t& ld, int64_t rows, int64_t cols,
   return cudaGetLastError();
 }
 
-size_t tc_part_bytes(int64_t I, int64_t J, int64_t R, bool must_split) {
-  const TcPlan p = tc_plan(I, J, R, must_split);
-  return p.splits > 1 || must_split ? (size_t)p.splits * I * ((J + 3) / 4 * 4) * 4 : 0;
+// ---- fp32 operands as three bf16 planes ------------------------------------------------
+// x = x1 + x2 + x3 with bf16 x1 (x rounded), x2 (the rest rounded), x3: 24 bits
+// together.  Of the nine products of two such operands the six of 2^-16 and more
+// are kept; what is left out is below fp32's own rounding.  On the tensor cores
+// that is twelve times the CUDA cores' rate for a sixth of the products each.
+int64_t plane_rows(int64_t rows) { return (rows + 63) / 64 * 64; }
+size_t planes_bytes(int64_t rows, int64_t cols) {
+  return (size_t)(3 * plane_rows(rows) * pitch8(cols)) * 2;
+}
+__global__ void __launch_bounds__(kPackThreads)
+split_planes_kernel(const float* __restrict__ src, int64_t ld, int64_t rows, int64_t cols,
+                    int64_t pitch, int64_t rows_pad, int vec, uint4* __restrict__ dst) {
+  const int64_t per = pitch / 8, n = rows_pad * per;
+  for (int64_t k = (int64_t)blockIdx.x * kPackThreads + threadIdx.x; k < n;
+       k += (int64_t)gridDim.x * kPackThreads) {
+    const int64_t r = k / per, c = (k - r * per) * 8;
+    float f[8] = {}, p1[8], p2[8], p3[8];
+    if (r < rows) {
+      const float* q = src + r * ld + c;
+      if (vec && c + 8 <= cols) {
+        const float4 x = reinterpret_cast<const float4*>(q)[0], y = reinterpret_cast<const float4*>(q)[1];
+        f[0] = x.x; f[1] = x.y; f[2] = x.z; f[3] = x.w;
+        f[4] = y.x; f[5] = y.y; f[6] = y.z; f[7] = y.w;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (c + i < cols) f[i] = q[i];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      p1[i] = (float)__float2bfloat16_rn(f[i]);
+      const float rest = f[i] - p1[i];      // exact
+      p2[i] = (float)__float2bfloat16_rn(rest);
+      p3[i] = rest - p2[i];
+    }
+    dst[k] = from_f32<__nv_bfloat16, 8>(p1);
+    dst[n + k] = from_f32<__nv_bfloat16, 8>(p2);
+    dst[2 * n + k] = from_f32<__nv_bfloat16, 8>(p3);
+  }
+}
+// Fewer multiplications than this take the CUDA cores: one launch instead of
+// four (measured: XXX)
+bool takes_planes(int64_t M, int64_t N, int64_t K) { return M * N * K >= PLANES; }
+
+size_t tc_part_bytes(int64_t I, int64_t J, int64_t R, bool must_split, int terms = 1) {
+  const TcPlan p = tc_plan(I, J, R, must_split, terms);
+  return p.splits > 1 || must_split ? (size_t)p.splits * I * part_pitch(J) * 4 : 0;
 }
 
 // dW from its partial products, four columns a thread, and db from the partial
@@ -298,7 +424,45 @@ cudaError_t tc_run(const Product& g, const Epilogue& e, char* work, int* err, cu
   float* part = plan.splits > 1 ? reinterpret_cast<float*>(work) : nullptr;
   const cudaError_t x = tc_product(g, e, plan, part, nullptr, err, num_sms(), st);
   if (x != cudaSuccess || !part) return x;
-  return launch_finish<__nv_bfloat16>(part, plan.splits, g.I, g.J, (g.J + 3) / 4 * 4, e, st);
+  return launch_finish<__nv_bfloat16>(part, plan.splits, g.I, g.J, part_pitch(g.J), e, st);
+}
+
+// out = epilogue of an fp32 product, by planes.  A lies as rows of `ca`
+// elements (its own row or the sum's index), so does B.
+cudaError_t planes_run(const Product& g, const Epilogue& e, char* work, int* err, cudaStream_t st) {
+  const bool amn = g.sai == 1 && e.mode == kWeight, bmn = e.mode != kForward;
+  Product t = g;
+  auto split = [&](const void*& a, int64_t ld, int64_t rows, int64_t cols, int64_t& pitch) {
+    pitch = pitch8(cols);
+    const int64_t pad = plane_rows(rows);
+    const int vec = ld % 4 == 0;
+    const int64_t blocks = std::min<int64_t>(cdiv(pad * (pitch / 8), kPackThreads), 16 * kSms);
+    split_planes_kernel<<<(unsigned)blocks, kPackThreads, 0, st>>>(
+        static_cast<const float*>(a), ld, rows, cols, pitch, pad, vec, reinterpret_cast<uint4*>(work));
+    a = work;
+    work += (planes_bytes(rows, cols) + 255) / 256 * 256;
+    return cudaGetLastError();
+  };
+  cudaError_t x = amn ? split(t.A, g.sar, g.R, g.I, t.sar) : split(t.A, g.sai, g.I, g.R, t.sai);
+  if (x == cudaSuccess)
+    x = bmn ? split(t.B, g.sbr, g.R, g.J, t.sbr) : split(t.B, g.sbj, g.J, g.R, t.sbj);
+  if (x != cudaSuccess) return x;
+  const TcPlan plan = tc_plan(g.I, g.J, g.R, true, kTerms);
+  x = tc_product(t, e, plan, reinterpret_cast<float*>(work), nullptr, err, num_sms(), st,
+                 plane_rows(amn ? g.R : g.I), plane_rows(bmn ? g.R : g.J));
+  if (x != cudaSuccess) return x;
+  return launch_finish<float>(reinterpret_cast<float*>(work), plan.splits, g.I, g.J,
+                              part_pitch(g.J), e, st, g);
+}
+size_t planes_need(int64_t ra, int64_t ca, int64_t rb, int64_t cb, int64_t I, int64_t J, int64_t R) {
+  return planes_bytes(ra, ca) + planes_bytes(rb, cb) + 512 + tc_part_bytes(I, J, R, true, kTerms);
+}
+// The fp32 product on the units that suit its size.
+cudaError_t run_f32(const Product& g, const Epilogue& e, int64_t M, int64_t N, int64_t K, void* work,
+                    float* part, cudaStream_t st) {
+  if (takes_planes(M, N, K) && tc_fits(g))
+    return planes_run(g, e, reinterpret_cast<char*>(part), static_cast<int*>(work), st);
+  return simt_product<float>(g, e, part, st);
 }
 
 // A gradient that is added to, or whose rows TMA cannot store, is finished from
@@ -320,7 +484,7 @@ cudaError_t tc_run_weight(const Product& g, const Epilogue& e, float* db, char* 
                     : nullptr;
   const cudaError_t x = tc_product(g, e, plan, part, sums, err, num_sms(), st);
   if (x != cudaSuccess || (!part && !db)) return x;
-  const int64_t ldp = (g.J + 3) / 4 * 4;
+  const int64_t ldp = part_pitch(g.J);
   const int wb = part ? (int)std::min<int64_t>(cdiv(g.I * ldp / 4, kFinishThreads), 8 * kSms) : 0;
   const int sb = db ? (int)cdiv(g.I, kWarp) : 0;
   return launch_pdl(finish_weight_kernel, dim3((unsigned)(wb + sb)), dim3(kFinishThreads), 0, st,
@@ -341,7 +505,7 @@ cudaError_t column_sums(const void* dz, int64_t ld, int64_t M, int64_t N, float*
   e.out = db;
   e.ldo = N;
   e.accumulate = accumulate;
-  return launch_finish<T>(part, used, 1, N, N, e, st);
+  return launch_finish<T>(part, used, 1, N, part_pitch(N), e, st);
 }
 
 bool sizes_ok(int64_t M, int64_t N, int64_t K) {
@@ -374,10 +538,14 @@ ppo_status status_of(cudaError_t e) { return e == cudaSuccess ? PPO_OK : PPO_ERR
 // ldb) and the partial products or column sums behind them.
 size_t need(int32_t dtype, int mode, int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb) {
   if (dtype == PPO_DTYPE_F32) {
-    const size_t sums = mode == lin::kWeight ? (size_t)(lin::sum_chunks(M, N) * N) * 4 : 0;
-    const size_t part = mode == lin::kForward ? lin::split_bytes(M, N, K)
-                        : mode == lin::kData  ? lin::split_bytes(M, K, N)
-                                              : lin::split_bytes(N, K, M);
+    const size_t sums = mode == lin::kWeight ? (size_t)(lin::sum_chunks(M, N) * lin::part_pitch(N)) * 4 : 0;
+    size_t part = mode == lin::kForward ? lin::split_bytes(M, N, K)
+                  : mode == lin::kData  ? lin::split_bytes(M, K, N)
+                                        : lin::split_bytes(N, K, M);
+    if (lin::takes_planes(M, N, K))
+      part = std::max(part, mode == lin::kForward ? lin::planes_need(M, K, N, K, M, N, K)
+                            : mode == lin::kData  ? lin::planes_need(M, N, N, K, M, K, N)
+                                                  : lin::planes_need(M, N, M, K, N, K, M));
     return kCtrl + std::max(part, sums);
   }
   switch (mode) {
@@ -430,7 +598,8 @@ ppo_status ppo_linear_forward(int32_t dtype, const void* x, int64_t ldx, const v
   e.out = y;
   e.ldo = ldy;
   if (dtype == PPO_DTYPE_F32)
-    return status_of(lin::simt_product<float>({x, ldx, 1, w, ldw, 1, M, N, K}, e, parts(work), st));
+    return status_of(
+        lin::run_f32({x, ldx, 1, w, ldw, 1, M, N, K}, e, M, N, K, work, parts(work), st));
   char* free = reinterpret_cast<char*>(parts(work));
   cudaError_t err = lin::on_16_bytes(x, ldx, M, K, free, st);
   if (err == cudaSuccess) err = lin::on_16_bytes(w, ldw, N, K, free, st);
@@ -463,7 +632,8 @@ ppo_status ppo_linear_backward_data(int32_t dtype, const void* dz, int64_t lddz,
   e.out = dx;
   e.ldo = lddx;
   if (dtype == PPO_DTYPE_F32)
-    return status_of(lin::simt_product<float>({dz, lddz, 1, w, 1, ldw, M, K, N}, e, parts(work), st));
+    return status_of(
+        lin::run_f32({dz, lddz, 1, w, 1, ldw, M, K, N}, e, M, N, K, work, parts(work), st));
   char* free = reinterpret_cast<char*>(parts(work));
   cudaError_t err = lin::on_16_bytes(dz, lddz, M, N, free, st);
   if (err == cudaSuccess) err = lin::on_16_bytes(w, ldw, N, K, free, st);
@@ -489,7 +659,7 @@ ppo_status ppo_linear_backward_weight(int32_t dtype, const void* dz, int64_t ldd
   e.accumulate = accumulate != 0;
   if (dtype == PPO_DTYPE_F32) {
     cudaError_t err =
-        lin::simt_product<float>({dz, 1, lddz, x, 1, ldx, N, K, M}, e, parts(work), st);
+        lin::run_f32({dz, 1, lddz, x, 1, ldx, N, K, M}, e, M, N, K, work, parts(work), st);
     if (err == cudaSuccess && db)
       err = lin::column_sums<float>(dz, lddz, M, N, db, e.accumulate, parts(work), st);
     return status_of(err);

@@ -41,15 +41,22 @@ struct TcPlan {
   int kt_per_split;    // 64-deep steps of the sum per split
   int splits;
 };
-TcPlan tc_plan(int64_t I, int64_t J, int64_t R, bool must_split);
+// terms: products of bf16 planes that make one product (fp32 operands: kTerms)
+constexpr int kTerms = 6;
+TcPlan tc_plan(int64_t I, int64_t J, int64_t R, bool must_split, int terms = 1);
 bool tc_fits(const Product& g);
+// Row pitch of partial products: rows start on 32-byte boundaries.
+__host__ __device__ constexpr int64_t part_pitch(int64_t J) { return (J + 7) / 8 * 8; }
 // Rows of partial column sums that the weight gradient's kernel leaves.
 int64_t tc_sum_rows(const Product& g, const TcPlan& plan);
-// part: [splits][I][J rounded up to 4] for split products (the epilogue is
+// part: [splits][I][part_pitch(J)] for split products (the epilogue is
 // then finish_kernel's), else nullptr; db_part (kWeight, nullable):
-// [tc_sum_rows][I], sums over r of A
+// [tc_sum_rows][I], sums over r of A.  plane_a, plane_b: the operands are three
+// planes of that many rows each (a multiple of 64, zeros past the operand's),
+// one below the other, whose sum is the fp32 operand; part is then required.
 cudaError_t tc_product(const Product& g, const Epilogue& e, const TcPlan& plan, float* part,
-                       float* db_part, int* err, int sms, cudaStream_t st);
+                       float* db_part, int* err, int sms, cudaStream_t st, int64_t plane_a = 0,
+                       int64_t plane_b = 0);
 
 }  // namespace lin
 

@@ -89,10 +89,12 @@ struct TcArgs {
   int window;                    // 64-deep steps that the tensor cores sum before a rounded add
   int units;                     // tiles * splits
   Epilogue e;
+  int64_t plane_a, plane_b;      // fp32 operands as three bf16 planes: their rows (0: bf16)
   float* part;                   // [splits][I][ldp] partial products (nullable)
   int64_t ldp;
   int in;                        // matrix read a unit ahead: 0 none, 1 the residual, 2 pre_in
   int res_late;                  // the residual is read when it is added
+  int wide_out;                  // fp32 rows start on 32-byte boundaries
   int tma_in, tma_out, tma_pre;  // it (the result, pre) moves by TMA
   float* db_part;                // [splits * tiles_j][I] column sums of A (nullable)
   int* err;
@@ -335,6 +337,11 @@ __device__ __forceinline__ void slope_chunk(int act, const uint32_t (&aux)[16], 
     default: break;
   }
 }
+__device__ __forceinline__ void store_32b(void* p, const uint32_t* v) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]),
+               "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
 __device__ __forceinline__ void prefetch_l2(const void* p) {
   asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
 }
@@ -435,21 +442,31 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
         for (int kt = kt0; kt < kt1; ++kt) {
           if (!wait_bar(empty(s), ph ^ 1, g)) { ok = false; break; }
           if (MODE == kWeight && p.db_part && !wait_bar(summed(s), ph ^ 1, g)) { ok = false; break; }
+          // the sum's step, and the rows that the operands' planes start at: of
+          // three planes the six products of 2^-16 and more, the small ones first
+          // (the accumulator is truncated at its own size)
+          int k = kt, pa = 0, pb = 0;
+          if (MODE == kWeight && p.plane_a) {
+            k = kt / kTerms;
+            const int t = kt - k * kTerms;
+            pa = (int)p.plane_a * (t == 0 ? 2 : t == 2 || t == 3 ? 1 : 0);
+            pb = (int)p.plane_b * (t == 1 ? 2 : t == 2 || t == 4 ? 1 : 0);
+          }
           if (rank == 0) mbar_arrive_expect_tx(full(s), CG * C::STAGE);
           const uint32_t bar = CG == 2 ? map_rank(full(s), 0) : full(s);
           if constexpr (AMN) {
 #pragma unroll
             for (int b = 0; b < BM / 64; ++b)
-              load_2d<CG>(sA(s) + b * 8192, &tmA, i0 + 64 * b, kt * BK, bar);
+              load_2d<CG>(sA(s) + b * 8192, &tmA, i0 + 64 * b, k * BK + pa, bar);
           } else {
-            load_2d<CG>(sA(s), &tmA, kt * BK, i0, bar);
+            load_2d<CG>(sA(s), &tmA, k * BK, i0 + pa, bar);
           }
           if constexpr (BMN) {
 #pragma unroll
             for (int b = 0; b < C::B_ROWS / 64; ++b)
-              load_2d<CG>(sB(s) + b * 8192, &tmB, j0 + 64 * b, kt * BK, bar);
+              load_2d<CG>(sB(s) + b * 8192, &tmB, j0 + 64 * b, k * BK + pb, bar);
           } else {
-            load_2d<CG>(sB(s), &tmB, kt * BK, j0, bar);
+            load_2d<CG>(sB(s), &tmB, k * BK, j0 + pb, bar);
           }
           cnt[0] = ++it;
           if (++s == S) { s = 0; ph ^= 1; }
@@ -637,14 +654,17 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
           for (int c = 0; c < PART / 32; ++c) {
             const int64_t cc = col0 + 32 * c;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {      // (rows of partials and of dW start on 16 bytes)
-              if (cc + 4 * i + 4 <= p.J) {
-                *reinterpret_cast<float4*>(o + cc + 4 * i) =
-                    make_float4(v[c][4 * i], v[c][4 * i + 1], v[c][4 * i + 2], v[c][4 * i + 3]);
+            for (int i = 0; i < 4; ++i) {      // 32-byte pieces: whole sectors
+              const int64_t c8 = cc + 8 * i;
+              if (p.wide_out && c8 + 8 <= p.J) {
+                uint32_t w[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(v[c][8 * i + j]);
+                store_32b(o + c8, w);
               } else {
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                  if (cc + 4 * i + j < p.J) o[cc + 4 * i + j] = v[c][4 * i + j];
+                for (int j = 0; j < 8; ++j)
+                  if (c8 + j < p.J) o[c8 + j] = v[c][8 * i + j];
               }
             }
           }
@@ -817,11 +837,12 @@ cudaError_t launch(const Product& g, TcArgs p, int sms, cudaStream_t st) {
   using C = TileCfg<CG, BN, MODE>;
   CUtensorMap ta, tb, to, tp, ti;
   cudaError_t e;
-  if (AMN) e = tc_make_tmap(&ta, g.A, g.I, g.R, g.sar, 64, BK);
-  else e = tc_make_tmap(&ta, g.A, g.R, g.I, g.sai, BK, BM);
+  const int64_t pa = 3 * p.plane_a, pb = 3 * p.plane_b;   // all rows of planes
+  if (AMN) e = tc_make_tmap(&ta, g.A, g.I, pa ? pa : g.R, g.sar, 64, BK);
+  else e = tc_make_tmap(&ta, g.A, g.R, pa ? pa : g.I, g.sai, BK, BM);
   if (e != cudaSuccess) return e;
-  if (BMN) e = tc_make_tmap(&tb, g.B, g.J, g.R, g.sbr, 64, BK);
-  else e = tc_make_tmap(&tb, g.B, g.R, g.J, g.sbj, BK, C::B_ROWS);
+  if (BMN) e = tc_make_tmap(&tb, g.B, g.J, pb ? pb : g.R, g.sbr, 64, BK);
+  else e = tc_make_tmap(&tb, g.B, g.R, pb ? pb : g.J, g.sbj, BK, C::B_ROWS);
   if (e != cudaSuccess) return e;
   to = ta;
   tp = ta;
@@ -886,17 +907,17 @@ int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // its units take: a 64-deep step of a unit costs a pair of CTAs and a single
 // CTA (128 x 128) about 300 and 200 ns, a unit's start and epilogue 2 us, and
 // a split product writes and re-reads its partial products.
-TcPlan tc_plan(int64_t I, int64_t J, int64_t R, bool must_split) {
+TcPlan tc_plan(int64_t I, int64_t J, int64_t R, bool must_split, int terms) {
   constexpr int kSms = 152;
   TcPlan best{};
   double best_cost = 0;
-  const int64_t kt = cdiv(R, BK);
+  const int64_t kt = cdiv(R, BK) * terms;
   for (int cg = 1; cg <= 2; ++cg) {
     const int64_t ti = cdiv(I, cg * BM), tj = cdiv(J, cg == 2 ? 256 : 128);
     const double step = cg == 2 ? 0.30 : 0.20;
     int64_t last = -1;
     for (int64_t s = 1; s <= 32 && s <= kt; ++s) {
-      const int64_t per = cdiv(kt, s), used = cdiv(kt, per);
+      const int64_t per = cdiv(cdiv(kt, s), terms) * terms, used = cdiv(kt, per);
       if (used == last) continue;
       last = used;
       const int64_t rounds = cdiv(ti * tj * used, kSms / cg);
@@ -915,8 +936,8 @@ TcPlan tc_plan(int64_t I, int64_t J, int64_t R, bool must_split) {
 }
 
 bool tc_fits(const Product& g) {
-  // TMA coordinates and tile counts are 32-bit
-  constexpr int64_t top = (1ll << 31) - 512;
+  // TMA coordinates (of planes too) and tile counts are 32-bit
+  constexpr int64_t top = (1ll << 29);
   return g.I < top && g.J < top && g.R < top &&
          cdiv(g.I, BM) * cdiv(g.J, 128) < (1ll << 30);
 }
@@ -926,22 +947,25 @@ int64_t tc_sum_rows(const Product& g, const TcPlan& plan) {
 }
 
 cudaError_t tc_product(const Product& g, const Epilogue& e, const TcPlan& plan, float* part,
-                       float* db_part, int* err, int sms, cudaStream_t st) {
+                       float* db_part, int* err, int sms, cudaStream_t st, int64_t plane_a,
+                       int64_t plane_b) {
   TcArgs p{};
   p.I = g.I;
   p.J = g.J;
   p.R = g.R;
   p.tiles_i = (int)cdiv(g.I, plan.cg * BM);
   p.tiles_j = (int)cdiv(g.J, plan.cg == 2 ? 256 : 128);
-  p.k_tiles = (int)cdiv(g.R, BK);
+  p.plane_a = plane_a;
+  p.plane_b = plane_b;
+  p.k_tiles = (int)cdiv(g.R, BK) * (plane_a ? kTerms : 1);
   p.kt_per_split = plan.kt_per_split;
-  p.window = e.mode == kWeight ? kWindow : p.k_tiles;
+  p.window = plane_a ? kTerms : e.mode == kWeight || part ? kWindow : p.k_tiles;
   const int64_t units = (int64_t)p.tiles_i * p.tiles_j * plan.splits;
   if (units > (1ll << 30)) return cudaErrorInvalidValue;
   p.units = (int)units;
   p.e = e;
   p.part = part;
-  p.ldp = (g.J + 3) / 4 * 4;
+  p.ldp = part_pitch(g.J);
   p.err = err;
   auto al = [](const void* q, int64_t ld, int m) { return ops::al16(q) && ld % m == 0; };
   p.tma_out = al(e.out, e.ldo, 8);
@@ -952,6 +976,8 @@ cudaError_t tc_product(const Product& g, const Epilogue& e, const TcPlan& plan, 
     p.res_late = e.res && p.in != 1;
   }
   p.db_part = db_part;
+  const void* f32_out = part ? part : e.out;
+  p.wide_out = ((reinterpret_cast<uintptr_t>(f32_out) | (uintptr_t)((part ? p.ldp : e.ldo) * 4)) & 31) == 0;
   if (plan.cg == 2) return launch_mode<2, 256>(g, p, e.mode, sms, st);
   return launch_mode<1, 128>(g, p, e.mode, sms, st);
 }
