@@ -6,14 +6,22 @@
 //   q = dy gamma, dx = rstd (q - mean(q) - xh mean(q xh)) + dres,
 //   dgamma = sum_rows dy xh, dbeta = sum_rows dy.
 // Both are bound by memory: 2 and 3 (4 with dres) row lengths per row.  A row
-// is therefore read once and kept in registers (at most 16 elements a thread, 8
-// where rows are not 16-byte aligned) between the reductions and the result; a
-// row that fits a warp so belongs to 1..32 of its lanes (short rows share a
-// warp), a longer one to a block of up to 512 threads.  Every warp (block) walks over many
-// rows with the next row's loads in flight, and keeps its columns of gamma,
-// beta and their gradient sums in registers meanwhile: the parameters are read
-// once per warp instead of once per row.  Rows beyond 8,192 elements (4,096 unaligned)
+// is therefore read once and kept in registers (16 or 32 elements a thread)
+// between the reductions and the result; a row that fits a warp so belongs to
+// 1..32 of its lanes (short rows share a warp), a longer one to a block of up to
+// 512 threads.  Every warp (block) walks over many rows and keeps its columns of
+// gamma, beta and their gradient sums in registers meanwhile: the parameters are
+// read once per warp instead of once per row.  The rows ahead are fetched into
+// the thread's own places of a ring in shared memory by 16-byte copies that need
+// neither registers nor barriers.
+// Rows off 16-byte boundaries (1,397 floats) are read in aligned pieces all the
+// same: rows that start equally far from a boundary are dealt to the same block,
+// so that a thread's columns, shifted by that distance, stay its own.  Only
+// matrices whose pitches disagree go element by element.  Rows that 512 threads
+// cannot keep (8,192 elements; 16,384 forward in bf16; 4,096 element by element)
 // take the kernels that read the row once per reduction.
+// Measured (of the copy rate): 262,144 x 512 bf16 forward 88 us (90 %), backward
+// with dres 184 us (86 %); 48,000 x 1,397 fp32 95 us (84 %) and 149 us (80 %).
 // The parameter gradients leave each block as one partial row; a second kernel
 // adds the partial rows in a fixed order, so results do not depend on timing.
 #include <algorithm>
@@ -26,10 +34,17 @@ namespace {
 using namespace ops;
 
 constexpr int kWarpRowThreads = 256;   // block of the rows-per-warp kernels
+constexpr int64_t kTall = 16384;       // rows from which they are many
 constexpr int kMaxBlock = 512;
-// elements of a row that a thread keeps: with the next row's loads in flight,
-// twice as many single loads would spill at a block's 128 registers a thread
-__host__ __device__ constexpr int max_kept(int vec) { return vec == 1 ? 8 : 16; }
+constexpr int kMaxWarps = kMaxBlock / kWarp;
+// elements of a row that a thread of a block keeps: what its 128 registers hold
+// beside the parameters (32,768 x 4,096 bf16 forward: 120 us with 16, 99 with 32)
+__host__ __device__ constexpr int max_kept(int vec, bool backward) {
+  return vec == 1 ? 8 : vec == 8 && !backward ? 32 : 16;
+}
+// a warp keeps twice as many before a row goes to a block and its barriers
+// (131,072 x 1,024 bf16: forward 121 us with blocks of two warps, 89 with warps)
+__host__ __device__ constexpr int max_kept_warp(int vec) { return vec == 1 ? 8 : 32; }
 constexpr int kLongThreads = 512;
 
 struct LnArgs {
@@ -43,6 +58,7 @@ struct LnArgs {
   float eps;
   float* part;                // backward: [blocks][2][D] (nullable)
   int lanes;                  // rows-per-warp kernels: lanes of a row (power of two)
+  int classes;                // rows r, r + classes, .. start equally far from a boundary
 };
 
 __device__ __forceinline__ float group_sum(float v, int lanes) {
@@ -52,185 +68,290 @@ __device__ __forceinline__ float group_sum(float v, int lanes) {
   return v;
 }
 
-// Sum over the row's threads: lanes of a warp, or the block (N values at once;
-// `red` has room for one set per warp and is free again at the next sync).
+// Sum over the row's threads: lanes of a warp, or the block (N values at once).
+// Successive sums of a block alternate between two sets of `red`, so that one
+// barrier each is enough: a set is written again only after the next sum's.
 template <bool BLOCK, int N>
-__device__ __forceinline__ void row_sum(float (&v)[N], int lanes, float* red) {
+__device__ __forceinline__ void row_sum(float (&v)[N], int lanes, float* red, int& set) {
 #pragma unroll
   for (int i = 0; i < N; ++i) v[i] = group_sum(v[i], lanes);
   if constexpr (BLOCK) {
     const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp, nw = blockDim.x / kWarp;
+    float* r = red + set * (N * kMaxWarps);
+    set ^= 1;
     if (lane == 0)
 #pragma unroll
-      for (int i = 0; i < N; ++i) red[i * 32 + warp] = v[i];
+      for (int i = 0; i < N; ++i) r[i * kMaxWarps + warp] = v[i];
     __syncthreads();
+    const int from = lane & (kMaxWarps - 1);   // (both halves of the warp)
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = group_sum(lane < nw ? red[i * 32 + lane] : 0.f, 32);
-    __syncthreads();
+    for (int i = 0; i < N; ++i)
+      v[i] = group_sum(from < nw ? r[i * kMaxWarps + from] : 0.f, kMaxWarps);
   }
 }
 
-// What a thread holds of a row: NV vectors of V elements, vector j at column
-// (j * threads_of_row + rank) * V.
-template <typename T, int V, int NV>
-struct RowLoader {
-  Raw<T, V> r[NV];
-  __device__ __forceinline__ void load(const void* base, int64_t ld, int64_t row, bool ok, int rank,
-                                       int tpr, int D) {
-    const T* p = static_cast<const T*>(base) + row * ld;
+// A thread's columns: NV pieces of V, piece j at column at[j] (below 0 where the
+// row starts inside it), of which the elements of mask[j] exist.
+template <int V, int NV>
+struct Columns {
+  int at[NV];
+  unsigned mask[NV];
+  static constexpr unsigned kFull = (1u << V) - 1;
+  __device__ __forceinline__ Columns(int rank, int tpr, int shift, int D) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int c = (j * tpr + rank) * V;
-      r[j] = Raw<T, V>{};
-      // (plain loads: the result may be written in place)
-      if (ok && c < D) r[j] = *reinterpret_cast<const Raw<T, V>*>(p + c);
+      at[j] = (j * tpr + rank) * V - shift;
+      mask[j] = 0;
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (at[j] + i >= 0 && at[j] + i < D) mask[j] |= 1u << i;
     }
   }
 };
 
-// BLOCK: a block per row; else `lanes` lanes per row, kWarpRowThreads / lanes
-// rows a block.  VECTOR loads need D, the pitches and the base aligned to V.
-template <typename T, int V, int NV, bool BLOCK>
-__global__ void __launch_bounds__(BLOCK ? kMaxBlock : kWarpRowThreads)
-ln_fwd_kernel(const LnArgs a) {
-  __shared__ float red[BLOCK ? 32 : 1];
-  const int tpr = BLOCK ? (int)blockDim.x : a.lanes;
-  const int rank = BLOCK ? (int)threadIdx.x : (int)(threadIdx.x & (a.lanes - 1));
+// Rows on their way: IN matrices, DEEP rows, each thread's pieces at places of
+// its own.  (V == 1: elements are loaded when they are needed.)
+// (as deep as 512 threads of an SM find room for)
+__host__ __device__ constexpr int ring_depth(int inputs, int size) {
+  return inputs == 1 ? 5 : inputs * size == 12 ? 2 : 3;
+}
+template <typename T, int V, int NV, int IN>
+struct Ring {
+  static constexpr bool kFetch = sizeof(T) * V == 16;
+  static constexpr int kDeep = ring_depth(IN, (int)sizeof(T));
+  uint4* mine;
+  int threads;
+  __device__ __forceinline__ uint4* place(int slot, int m, int j) const {
+    return mine + ((slot * IN + m) * NV + j) * threads;
+  }
+  __device__ __forceinline__ void fetch(int slot, int m, const void* base, int64_t ld, int64_t row,
+                                        const LnArgs& a, const Columns<V, NV>& c) const {
+    const T* p = static_cast<const T*>(base) + row * ld;
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+      if (c.mask[j]) {
+        // (a piece may reach into the next rows, but not past the matrix)
+        int n = 16;
+        if (row + V >= a.M)
+          n = (int)min((int64_t)V, (a.M - 1 - row) * ld + a.D - c.at[j]) * (int)sizeof(T);
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                         (uint32_t)__cvta_generic_to_shared(place(slot, m, j))),
+                     "l"(p + c.at[j]), "r"(n)
+                     : "memory");
+      }
+  }
+  __device__ __forceinline__ void get(int slot, int m, const void* base, int64_t ld, int64_t row,
+                                      const Columns<V, NV>& c, float (&f)[NV][V]) const {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      if constexpr (kFetch) {
+        to_f32<T, V>(*place(slot, m, j), f[j]);
+        if (c.mask[j] != c.kFull) {
+#pragma unroll
+          for (int i = 0; i < V; ++i) f[j][i] = (c.mask[j] >> i) & 1u ? f[j][i] : 0.f;
+        }
+      } else {
+        const T* p = static_cast<const T*>(base) + row * ld + c.at[j];
+#pragma unroll
+        for (int i = 0; i < V; ++i) f[j][i] = (c.mask[j] >> i) & 1u ? (float)p[i] : 0.f;
+      }
+    }
+  }
+};
+template <typename T, int V, int NV>
+__device__ __forceinline__ void put_row(void* base, int64_t ld, int64_t row,
+                                        const Columns<V, NV>& c, const float (&f)[NV][V]) {
+  T* p = static_cast<T*>(base) + row * ld;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    if (c.mask[j] == c.kFull) {
+      *reinterpret_cast<Raw<T, V>*>(p + c.at[j]) = from_f32<T, V>(f[j]);
+    } else if (c.mask[j]) {
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if ((c.mask[j] >> i) & 1u) round_to(f[j][i], p[c.at[j] + i]);
+    }
+  }
+}
+__device__ __forceinline__ void ring_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int DEEP>
+__device__ __forceinline__ void ring_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(DEEP - 2) : "memory");
+}
+
+// blocks of rows-per-warp kernels on an SM, by the elements a thread keeps
+__host__ __device__ constexpr int fwd_blocks(int kept) { return kept > 16 ? 2 : 3; }
+__host__ __device__ constexpr int bwd_blocks(int kept) { return kept > 16 ? 1 : 2; }
+
+// A thread's walk: rows of its block's class, `step` apart.
+struct RowWalk {
+  int64_t row, step, rounds;
+  int rank, tpr, lanes, shift;
+};
+template <typename T, int V, bool BLOCK>
+__device__ __forceinline__ RowWalk row_walk(const LnArgs& a) {
+  RowWalk w;
+  w.tpr = BLOCK ? (int)blockDim.x : a.lanes;
+  w.rank = BLOCK ? (int)threadIdx.x : (int)(threadIdx.x & (a.lanes - 1));
+  w.lanes = BLOCK ? 32 : a.lanes;
   const int rpb = BLOCK ? 1 : kWarpRowThreads / a.lanes;
-  const int lanes = BLOCK ? 32 : a.lanes;
-  const int64_t step = (int64_t)gridDim.x * rpb;
-  int64_t row = (int64_t)blockIdx.x * rpb + (BLOCK ? 0 : (int)threadIdx.x / a.lanes);
+  const int cls = (int)(blockIdx.x % a.classes), b = (int)(blockIdx.x / a.classes);
+  const int nb = (int)(gridDim.x / a.classes);
+  w.shift = (int)((int64_t)cls * a.ldx % V);
+  const int64_t mine = (a.M - cls + a.classes - 1) / a.classes;   // rows of the class
+  const int64_t first = (int64_t)b * rpb;
+  w.step = (int64_t)nb * rpb * a.classes;
+  // every thread of a block makes the same number of rounds (the sums use whole
+  // warps); rows past the end are computed on what the ring holds and not stored
+  w.rounds = mine > first ? (mine - first + (int64_t)nb * rpb - 1) / ((int64_t)nb * rpb) : 0;
+  w.row = cls + (first + (BLOCK ? 0 : (int)threadIdx.x / a.lanes)) * a.classes;
+  return w;
+}
+
+// BLOCK: a block per row; else `lanes` lanes per row, kWarpRowThreads / lanes
+// rows a block.
+template <typename T, int V, int NV, bool BLOCK>
+__global__ void __launch_bounds__(BLOCK ? kMaxBlock : kWarpRowThreads, BLOCK ? 1 : fwd_blocks(V * NV))
+ln_fwd_kernel(const LnArgs a) {
+  __shared__ float red[BLOCK ? 2 * kMaxWarps : 1];
+  int set = 0;
+  extern __shared__ uint4 ring_mem[];
+  RowWalk w = row_walk<T, V, BLOCK>(a);
+  const Columns<V, NV> c(w.rank, w.tpr, w.shift, a.D);
+  using R = Ring<T, V, NV, 1>;
+  const R ring{ring_mem + threadIdx.x, (int)blockDim.x};
   float ga[NV][V], be[NV][V];
 #pragma unroll
   for (int j = 0; j < NV; ++j)
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int c = (j * tpr + rank) * V + i;
-      ga[j][i] = c < a.D && a.gamma ? __ldg(a.gamma + c) : 1.f;
-      be[j][i] = c < a.D && a.beta ? __ldg(a.beta + c) : 0.f;
+      const bool in = (c.mask[j] >> i) & 1u;
+      ga[j][i] = in && a.gamma ? __ldg(a.gamma + c.at[j] + i) : 1.f;
+      be[j][i] = in && a.beta ? __ldg(a.beta + c.at[j] + i) : 0.f;
     }
   const float inv = 1.f / (float)a.D;
-  RowLoader<T, V, NV> cur, nxt;
-  // every thread of a block makes the same number of rounds (the sums use
-  // whole warps); rows past the end are computed on zeros and not stored
-  int64_t rounds = ((a.M - (int64_t)blockIdx.x * rpb) + step - 1) / step;
-  cur.load(a.x, a.ldx, row, row < a.M, rank, tpr, a.D);
-  for (; rounds > 0; --rounds, row += step) {
-    nxt.load(a.x, a.ldx, row + step, row + step < a.M, rank, tpr, a.D);
-    float x[NV][V];
+  auto fetch = [&](int slot, int64_t row) {
+    if constexpr (R::kFetch) {
+      if (row < a.M) ring.fetch(slot, 0, a.x, a.ldx, row, a, c);
+      ring_commit();
+    }
+  };
+  for (int i = 0; i < R::kDeep - 1; ++i) fetch(i, w.row + i * w.step);
+  int slot = 0;
+  for (; w.rounds > 0; --w.rounds, w.row += w.step) {
+    if constexpr (R::kFetch) ring_wait<R::kDeep>();
+    // the slot that was read a round ago takes the farthest row
+    fetch(slot == 0 ? R::kDeep - 1 : slot - 1, w.row + (R::kDeep - 1) * w.step);
+    float x[NV][V] = {};
+    if (w.row < a.M) ring.get(slot, 0, a.x, a.ldx, w.row, c, x);
+    slot = slot == R::kDeep - 1 ? 0 : slot + 1;
     float s[1] = {0.f};
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      to_f32<T, V>(cur.r[j], x[j]);
+    for (int j = 0; j < NV; ++j)
 #pragma unroll
       for (int i = 0; i < V; ++i) s[0] += x[j][i];
-    }
-    row_sum<BLOCK>(s, lanes, red);
+    row_sum<BLOCK>(s, w.lanes, red, set);
     const float mean = s[0] * inv;
     float q[1] = {0.f};
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const bool in = (j * tpr + rank) * V < a.D;
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        x[j][i] -= mean;
-        q[0] += in ? x[j][i] * x[j][i] : 0.f;
+      for (int i = 0; i < V; ++i) x[j][i] -= mean;
+      if (c.mask[j] != c.kFull) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) x[j][i] = (c.mask[j] >> i) & 1u ? x[j][i] : 0.f;
       }
+#pragma unroll
+      for (int i = 0; i < V; ++i) q[0] += x[j][i] * x[j][i];
     }
-    row_sum<BLOCK>(q, lanes, red);
+    row_sum<BLOCK>(q, w.lanes, red, set);
     const float rstd = rsqrtf(q[0] * inv + a.eps);
-    if (row < a.M) {
-      T* y = static_cast<T*>(a.out) + row * a.ldo;
+    if (w.row < a.M) {
 #pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        const int c = (j * tpr + rank) * V;
-        float o[V];
+      for (int j = 0; j < NV; ++j)
 #pragma unroll
-        for (int i = 0; i < V; ++i) o[i] = x[j][i] * rstd * ga[j][i] + be[j][i];
-        if (c < a.D) *reinterpret_cast<Raw<T, V>*>(y + c) = from_f32<T, V>(o);
-      }
-      if (a.stats && rank == 0)
-        *reinterpret_cast<float2*>(a.stats + 2 * row) = make_float2(mean, rstd);
+        for (int i = 0; i < V; ++i) x[j][i] = x[j][i] * rstd * ga[j][i] + be[j][i];
+      put_row<T, V, NV>(a.out, a.ldo, w.row, c, x);
+      if (a.stats && w.rank == 0)
+        *reinterpret_cast<float2*>(a.stats + 2 * w.row) = make_float2(mean, rstd);
     }
-    cur = nxt;
   }
 }
 
 template <typename T, int V, int NV, bool BLOCK, bool RES>
-__global__ void __launch_bounds__(BLOCK ? kMaxBlock : kWarpRowThreads)
+__global__ void __launch_bounds__(BLOCK ? kMaxBlock : kWarpRowThreads, BLOCK ? 1 : bwd_blocks(V * NV))
 ln_bwd_kernel(const LnArgs a) {
-  __shared__ float red[BLOCK ? 64 : 1];
-  // the parameter gradients of a block's warps, 512 columns at most
-  __shared__ float acc[BLOCK ? 1 : kWarpRowThreads / kWarp][BLOCK ? 1 : 2][BLOCK ? 1 : 512];
-  const int tpr = BLOCK ? (int)blockDim.x : a.lanes;
-  const int rank = BLOCK ? (int)threadIdx.x : (int)(threadIdx.x & (a.lanes - 1));
-  const int rpb = BLOCK ? 1 : kWarpRowThreads / a.lanes;
-  const int lanes = BLOCK ? 32 : a.lanes;
-  const int64_t step = (int64_t)gridDim.x * rpb;
-  int64_t row = (int64_t)blockIdx.x * rpb + (BLOCK ? 0 : (int)threadIdx.x / a.lanes);
+  __shared__ float red[BLOCK ? 4 * kMaxWarps : 1];
+  int set = 0;
+  extern __shared__ uint4 ring_mem[];
+  RowWalk w = row_walk<T, V, BLOCK>(a);
+  const Columns<V, NV> c(w.rank, w.tpr, w.shift, a.D);
+  using R = Ring<T, V, NV, RES ? 3 : 2>;
+  const R ring{ring_mem + threadIdx.x, (int)blockDim.x};
   float ga[NV][V], dg[NV][V], db[NV][V];
 #pragma unroll
   for (int j = 0; j < NV; ++j)
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int c = (j * tpr + rank) * V + i;
-      ga[j][i] = c < a.D && a.gamma ? __ldg(a.gamma + c) : 1.f;
+      ga[j][i] = ((c.mask[j] >> i) & 1u) && a.gamma ? __ldg(a.gamma + c.at[j] + i) : 1.f;
       dg[j][i] = db[j][i] = 0.f;
     }
   const float inv = 1.f / (float)a.D;
-  RowLoader<T, V, NV> cx, cy, cr, nx, ny, nr;
   auto stat = [&](int64_t r) {
     return r < a.M ? __ldg(reinterpret_cast<const float2*>(a.stats + 2 * r)) : make_float2(0.f, 0.f);
   };
-  auto fetch = [&](RowLoader<T, V, NV>& x, RowLoader<T, V, NV>& y, RowLoader<T, V, NV>& r,
-                   int64_t at) {
-    x.load(a.x, a.ldx, at, at < a.M, rank, tpr, a.D);
-    y.load(a.dy, a.lddy, at, at < a.M, rank, tpr, a.D);
-    if constexpr (RES) r.load(a.res, a.ldres, at, at < a.M, rank, tpr, a.D);
+  auto fetch = [&](int slot, int64_t row) {
+    if constexpr (R::kFetch) {
+      if (row < a.M) {
+        ring.fetch(slot, 0, a.x, a.ldx, row, a, c);
+        ring.fetch(slot, 1, a.dy, a.lddy, row, a, c);
+        if constexpr (RES) ring.fetch(slot, 2, a.res, a.ldres, row, a, c);
+      }
+      ring_commit();
+    }
   };
-  int64_t rounds = ((a.M - (int64_t)blockIdx.x * rpb) + step - 1) / step;
-  fetch(cx, cy, cr, row);
-  float2 st = stat(row), nst;
-  for (; rounds > 0; --rounds, row += step) {
-    fetch(nx, ny, nr, row + step);
-    nst = stat(row + step);
-    float xh[NV][V], q[NV][V];
+  for (int i = 0; i < R::kDeep - 1; ++i) fetch(i, w.row + i * w.step);
+  float2 st = stat(w.row), nst;
+  int slot = 0;
+  for (; w.rounds > 0; --w.rounds, w.row += w.step) {
+    nst = stat(w.row + w.step);
+    if constexpr (R::kFetch) ring_wait<R::kDeep>();
+    fetch(slot == 0 ? R::kDeep - 1 : slot - 1, w.row + (R::kDeep - 1) * w.step);
+    float xh[NV][V] = {}, q[NV][V] = {};
+    if (w.row < a.M) {
+      ring.get(slot, 0, a.x, a.ldx, w.row, c, xh);
+      ring.get(slot, 1, a.dy, a.lddy, w.row, c, q);
+    }
     float s[2] = {0.f, 0.f};
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const bool in = (j * tpr + rank) * V < a.D;
-      to_f32<T, V>(cx.r[j], xh[j]);
-      to_f32<T, V>(cy.r[j], q[j]);
+    for (int j = 0; j < NV; ++j)
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        xh[j][i] = in ? (xh[j][i] - st.x) * st.y : 0.f;
+        // (where no element is, q = 0 and xh reaches nothing that is stored)
+        xh[j][i] = (xh[j][i] - st.x) * st.y;
         dg[j][i] += q[j][i] * xh[j][i];
         db[j][i] += q[j][i];
         q[j][i] *= ga[j][i];
         s[0] += q[j][i];
         s[1] += q[j][i] * xh[j][i];
       }
-    }
-    row_sum<BLOCK>(s, lanes, red);
+    row_sum<BLOCK>(s, w.lanes, red, set);
     const float m1 = s[0] * inv, m2 = s[1] * inv;
-    if (row < a.M) {
-      T* o = static_cast<T*>(a.out) + row * a.ldo;
+    if (w.row < a.M) {
 #pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        const int c = (j * tpr + rank) * V;
-        float d[V], rr[V];
-        if constexpr (RES) to_f32<T, V>(cr.r[j], rr);
+      for (int j = 0; j < NV; ++j)
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          d[i] = st.y * (q[j][i] - m1 - xh[j][i] * m2);
-          if constexpr (RES) d[i] += rr[i];
-        }
-        if (c < a.D) *reinterpret_cast<Raw<T, V>*>(o + c) = from_f32<T, V>(d);
+        for (int i = 0; i < V; ++i) q[j][i] = st.y * (q[j][i] - m1 - xh[j][i] * m2);
+      if constexpr (RES) {
+        ring.get(slot, 2, a.res, a.ldres, w.row, c, xh);
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+          for (int i = 0; i < V; ++i) q[j][i] += xh[j][i];
       }
+      put_row<T, V, NV>(a.out, a.ldo, w.row, c, q);
     }
-    cx = nx;
-    cy = ny;
-    if constexpr (RES) cr = nr;
+    slot = slot == R::kDeep - 1 ? 0 : slot + 1;
     st = nst;
   }
   if (!a.part) return;
@@ -239,14 +360,16 @@ ln_bwd_kernel(const LnArgs a) {
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const int c = (j * tpr + rank) * V + i;
-        if (c < a.D) {
-          part[c] = dg[j][i];
-          part[a.D + c] = db[j][i];
+      for (int i = 0; i < V; ++i)
+        if ((c.mask[j] >> i) & 1u) {
+          part[c.at[j] + i] = dg[j][i];
+          part[a.D + c.at[j] + i] = db[j][i];
         }
-      }
   } else {
+    // the warps' sums meet in the ring's place: [warp][2][D], D <= 1,024
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncthreads();
+    float* acc = reinterpret_cast<float*>(ring_mem);
     const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp;
 #pragma unroll
     for (int j = 0; j < NV; ++j)
@@ -259,18 +382,16 @@ ln_bwd_kernel(const LnArgs a) {
             dg[j][i] += __shfl_xor_sync(0xffffffffu, dg[j][i], o);
             db[j][i] += __shfl_xor_sync(0xffffffffu, db[j][i], o);
           }
-        const int c = (j * tpr + rank) * V + i;
-        if (lane < a.lanes && c < a.D) {
-          acc[warp][0][c] = dg[j][i];
-          acc[warp][1][c] = db[j][i];
+        if (lane < a.lanes && ((c.mask[j] >> i) & 1u)) {
+          acc[(2 * warp) * a.D + c.at[j] + i] = dg[j][i];
+          acc[(2 * warp + 1) * a.D + c.at[j] + i] = db[j][i];
         }
       }
     __syncthreads();
     for (int e = threadIdx.x; e < 2 * a.D; e += kWarpRowThreads) {
-      const int k = e >= a.D, c = e - k * a.D;
       float t = 0.f;
 #pragma unroll
-      for (int w = 0; w < kWarpRowThreads / kWarp; ++w) t += acc[w][k][c];
+      for (int k = 0; k < kWarpRowThreads / kWarp; ++k) t += acc[2 * k * a.D + e];
       part[e] = t;
     }
   }
@@ -280,21 +401,22 @@ ln_bwd_kernel(const LnArgs a) {
 // result; the parameter gradients accumulate in the block's own partial row.
 template <typename T>
 __global__ void __launch_bounds__(kLongThreads) ln_fwd_long_kernel(const LnArgs a) {
-  __shared__ float red[32];
+  __shared__ float red[2 * kMaxWarps];
+  int set = 0;
   const float inv = 1.f / (float)a.D;
   for (int64_t row = blockIdx.x; row < a.M; row += gridDim.x) {
     const T* x = static_cast<const T*>(a.x) + row * a.ldx;
     T* y = static_cast<T*>(a.out) + row * a.ldo;
     float s[1] = {0.f};
     for (int c = threadIdx.x; c < a.D; c += kLongThreads) s[0] += (float)x[c];
-    row_sum<true>(s, 32, red);
+    row_sum<true>(s, 32, red, set);
     const float mean = s[0] * inv;
     float q[1] = {0.f};
     for (int c = threadIdx.x; c < a.D; c += kLongThreads) {
       const float d = (float)x[c] - mean;
       q[0] += d * d;
     }
-    row_sum<true>(q, 32, red);
+    row_sum<true>(q, 32, red, set);
     const float rstd = rsqrtf(q[0] * inv + a.eps);
     for (int c = threadIdx.x; c < a.D; c += kLongThreads) {
       const float g = a.gamma ? __ldg(a.gamma + c) : 1.f, b = a.beta ? __ldg(a.beta + c) : 0.f;
@@ -307,7 +429,8 @@ __global__ void __launch_bounds__(kLongThreads) ln_fwd_long_kernel(const LnArgs 
 
 template <typename T>
 __global__ void __launch_bounds__(kLongThreads) ln_bwd_long_kernel(const LnArgs a) {
-  __shared__ float red[64];
+  __shared__ float red[4 * kMaxWarps];
+  int set = 0;
   const float inv = 1.f / (float)a.D;
   float* part = a.part ? a.part + (int64_t)blockIdx.x * 2 * a.D : nullptr;
   for (int64_t row = blockIdx.x; row < a.M; row += gridDim.x) {
@@ -328,7 +451,7 @@ __global__ void __launch_bounds__(kLongThreads) ln_bwd_long_kernel(const LnArgs 
         part[a.D + c] = (first ? 0.f : part[a.D + c]) + d;
       }
     }
-    row_sum<true>(s, 32, red);
+    row_sum<true>(s, 32, red, set);
     const float m1 = s[0] * inv, m2 = s[1] * inv;
     for (int c = threadIdx.x; c < a.D; c += kLongThreads) {
       const float xh = ((float)x[c] - st.x) * st.y;
@@ -373,62 +496,87 @@ ln_param_grad_kernel(const float* __restrict__ part, int nparts, int D, float* _
 // ---- plan ---------------------------------------------------------------------
 constexpr int kGridCap = 1216;   // partial rows at most: 8 blocks on each of 152 SMs
 
-// The widest vector whose alignment the row length and every pitch keep
-int vec_of(int32_t dtype, int64_t D, std::initializer_list<int64_t> lds) {
+// Elements of a piece: 16 bytes where every matrix's rows start equally far from
+// a boundary, else one; and how many rows on they do so again.
+int vec_of(int32_t dtype, std::initializer_list<int64_t> lds) {
   const int v = 16 / esize(dtype);
-  if (D % v) return 1;
   for (int64_t l : lds)
-    if (l % v) return 1;
+    if (l % v != *lds.begin() % v) return 1;
   return v;
+}
+int classes_of(int vec, int64_t ld) {
+  int c = 1;
+  while (c * ld % vec) c *= 2;
+  return c;
 }
 
 struct Plan {
   int vec, nv, lanes, threads;   // lanes: 0 for a block per row; threads: 0 for the long kernels
-  int grid;
+  int grid, classes;
+  size_t smem;
 };
 
-Plan plan_of(int64_t M, int64_t D, int vec, int sms, bool backward) {
+Plan plan_of(int64_t M, int64_t D, int vec, int64_t ld, int sms, bool backward, bool res) {
   Plan p{};
   p.vec = vec;
-  if (D > (int64_t)kMaxBlock * max_kept(vec)) {
+  p.classes = classes_of(vec, ld);
+  if (p.classes > M) p.classes = 1, p.vec = vec = 1;   // too few rows to deal out
+  const int64_t span = D + (p.classes > 1 ? vec - 1 : 0);   // shifted columns
+  if (span > (int64_t)kMaxBlock * max_kept(vec, backward)) {
+    p.classes = 1;
     p.grid = (int)std::min<int64_t>(M, 2 * sms);
     return p;
   }
   int64_t per_sm;
-  if (D <= (int64_t)kWarp * max_kept(vec)) {
+  const int inputs = !backward ? 1 : res ? 3 : 2;
+  if (span <= (int64_t)kWarp * max_kept_warp(vec)) {
     // fewest elements a thread with which the row fits a warp, so that a short
     // row keeps its lanes busy
-    p.nv = vec == 1 ? 4 : 1;
-    while (p.nv * vec * kWarp < D) p.nv *= 2;
+    // (many rows: rather many elements a thread, so that a warp's reductions
+    // serve more rows; 262,144 x 512 bf16 forward 99 us with 16 elements, 89 with
+    // 32; 1,000,000 x 64 58 us with 8, 48 with 16, 54 with 32)
+    p.nv = vec == 1 ? 4 : M < kTall ? 1 : (backward || vec == 4 || span <= 128 ? 16 : 32) / vec;
+    while (p.nv * vec * kWarp < span) p.nv *= 2;
     p.lanes = 1;
-    while (p.lanes * p.nv * vec < D) p.lanes *= 2;
+    while (p.lanes * p.nv * vec < span) p.lanes *= 2;
     p.threads = kWarpRowThreads;
-    per_sm = backward ? 3 : 6;
+    per_sm = backward ? bwd_blocks(p.nv * vec) : fwd_blocks(p.nv * vec);
   } else {
-    p.nv = max_kept(vec) / vec;
+    p.nv = max_kept(vec, backward) / vec;
     const int64_t per = (int64_t)p.nv * vec;
-    p.threads = (int)(((D + per - 1) / per + kWarp - 1) / kWarp) * kWarp;
-    per_sm = std::max<int64_t>(1, std::min<int64_t>(8, (backward ? 768 : 1536) / p.threads));
+    p.threads = (int)(((span + per - 1) / per + kWarp - 1) / kWarp) * kWarp;
+    per_sm = std::max<int64_t>(1, std::min<int64_t>(8, 512 / p.threads));
   }
+  if (vec > 1) p.smem = (size_t)ring_depth(inputs, 16 / vec) * inputs * p.nv * 16 * p.threads;
+  if (backward && p.lanes)   // room for the warps' parameter gradients
+    p.smem = std::max(p.smem, (size_t)(kWarpRowThreads / kWarp) * 2 * D * sizeof(float));
   const int64_t rpb = p.lanes ? kWarpRowThreads / p.lanes : 1;
-  p.grid = (int)std::min<int64_t>({(M + rpb - 1) / rpb, per_sm * sms, (int64_t)kGridCap});
+  const int64_t rows = (M + p.classes - 1) / p.classes;   // of a class
+  const int64_t most = std::min<int64_t>(per_sm * sms, kGridCap) / p.classes;
+  p.grid = (int)(std::min((rows + rpb - 1) / rpb, std::max<int64_t>(1, most)) * p.classes);
   return p;
 }
 
 template <typename T, int V, int NV>
 cudaError_t go(const LnArgs& a, const Plan& p, bool backward, cudaStream_t st) {
-  const dim3 g(p.grid), b(p.threads);
+  void (*kernel)(const LnArgs) = nullptr;
   if (p.lanes) {
-    if (!backward) ln_fwd_kernel<T, V, NV, false><<<g, b, 0, st>>>(a);
-    else if (a.res) ln_bwd_kernel<T, V, NV, false, true><<<g, b, 0, st>>>(a);
-    else ln_bwd_kernel<T, V, NV, false, false><<<g, b, 0, st>>>(a);
-  } else if constexpr (V * NV == max_kept(V)) {   // (the one count that blocks use)
-    if (!backward) ln_fwd_kernel<T, V, NV, true><<<g, b, 0, st>>>(a);
-    else if (a.res) ln_bwd_kernel<T, V, NV, true, true><<<g, b, 0, st>>>(a);
-    else ln_bwd_kernel<T, V, NV, true, false><<<g, b, 0, st>>>(a);
+    kernel = !backward ? ln_fwd_kernel<T, V, NV, false>
+             : a.res   ? ln_bwd_kernel<T, V, NV, false, true>
+                       : ln_bwd_kernel<T, V, NV, false, false>;
+  } else if (!backward) {      // (blocks use one count of elements each way)
+    if constexpr (V * NV == max_kept(V, false)) kernel = ln_fwd_kernel<T, V, NV, true>;
   } else {
-    return cudaErrorInvalidValue;
+    if constexpr (V * NV == max_kept(V, true))
+      kernel = a.res ? ln_bwd_kernel<T, V, NV, true, true> : ln_bwd_kernel<T, V, NV, true, false>;
   }
+  if (!kernel) return cudaErrorInvalidValue;
+  if (p.smem > 48 * 1024) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)p.smem);
+    if (e != cudaSuccess) return e;
+  }
+  kernel<<<p.grid, p.threads, p.smem, st>>>(a);
   return cudaGetLastError();
 }
 
@@ -443,8 +591,9 @@ cudaError_t dispatch(const LnArgs& a, const Plan& p, bool backward, cudaStream_t
   if (p.vec == V) {
     if (p.nv == 1) return go<T, V, 1>(a, p, backward, st);
     if (p.nv == 2) return go<T, V, 2>(a, p, backward, st);
+    if (p.nv == 4) return go<T, V, 4>(a, p, backward, st);
     if constexpr (V == 4)
-      if (p.nv == 4) return go<T, V, 4>(a, p, backward, st);
+      if (p.nv == 8) return go<T, V, 8>(a, p, backward, st);
     return cudaErrorInvalidValue;
   }
   if (p.nv == 4) return go<T, 1, 4>(a, p, backward, st);
@@ -482,8 +631,9 @@ ppo_status ppo_layernorm_forward(int32_t dtype, const void* x, int64_t ldx, int6
   a.beta = beta;
   a.eps = eps;
   a.stats = stats;
-  const Plan p = plan_of(M, D, vec_of(dtype, D, {ldx, ldy}), sms, false);
+  const Plan p = plan_of(M, D, vec_of(dtype, {ldx, ldy}), ldx, sms, false, false);
   a.lanes = p.lanes;
+  a.classes = p.classes;
   const cudaError_t e = dtype == PPO_DTYPE_F32 ? dispatch<float>(a, p, false, st)
                                                : dispatch<__nv_bfloat16>(a, p, false, st);
   return e == cudaSuccess ? PPO_OK : PPO_ERR_CUDA;
@@ -491,8 +641,9 @@ ppo_status ppo_layernorm_forward(int32_t dtype, const void* x, int64_t ldx, int6
 
 ppo_status ppo_layernorm_backward_workspace_bytes(int64_t M, int64_t D, size_t* bytes) {
   if (!bytes || M < 1 || D < 1 || D >= (1ll << 30)) return PPO_ERR_INVALID;
-  // one partial row (gamma's and beta's gradient) per block
-  *bytes = (size_t)std::min<int64_t>(M, ppo::kGridCap) * 2 * (size_t)D * sizeof(float);
+  // one partial row (gamma's and beta's gradient) per block: a row's, rounded up
+  // to the at most 8 classes of rows
+  *bytes = (size_t)std::min<int64_t>(M + 8, ppo::kGridCap) * 2 * (size_t)D * sizeof(float);
   return PPO_OK;
 }
 
@@ -530,9 +681,10 @@ ppo_status ppo_layernorm_backward(int32_t dtype, const void* dy, int64_t lddy, c
   a.gamma = gamma;
   a.stats = const_cast<float*>(stats);
   a.part = params ? static_cast<float*>(work) : nullptr;
-  const Plan p =
-      plan_of(M, D, vec_of(dtype, D, {ldx, lddy, lddx, dres ? lddres : ldx}), sms, true);
+  const Plan p = plan_of(M, D, vec_of(dtype, {ldx, lddy, lddx, dres ? lddres : ldx}), ldx, sms,
+                         true, dres != nullptr);
   a.lanes = p.lanes;
+  a.classes = p.classes;
   cudaError_t e = dtype == PPO_DTYPE_F32 ? dispatch<float>(a, p, true, st)
                                          : dispatch<__nv_bfloat16>(a, p, true, st);
   if (e == cudaSuccess && params)
