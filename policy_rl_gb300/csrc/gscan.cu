@@ -25,6 +25,10 @@
 //     tiles at once from their entering states.  This reads the gates (and ph
 //     or dh) twice, and leaves no tile waiting for another.  The maps lie in
 //     rows of the output that the third launch overwrites.
+// Measured, forward and backward, bf16: 128 x 2,048 x 256 72 us (5.6 TB/s) and
+// 146 us (4.6 TB/s: limited by the instructions of the walk back, two blocks of
+// 128 registers a thread on an SM); 65,537 x 1 x 1,024 157 and 220 us, of which
+// the maps take 56 and 55, the join 18, the run 79 and 143.
 // Compositions happen in an order fixed by the sizes: results are
 // deterministic.  A cleared state is dropped by a select, never multiplied by
 // 0, so that infinities and NaN do not cross it.
@@ -39,16 +43,19 @@ namespace {
 
 using namespace ops;
 
+// Rows (t * N + n) and row pitches in bytes fit 32 bits, so that an address is one
+// wide multiplication.
 struct ScanArgs {
   const void *p, *dh;
-  int64_t ldp, lddh;
+  uint32_t ldp, lddh, ldo; // bytes
   const float *done, *done0, *h0, *dhT;
-  int64_t T, N, H, C;      // C = N * H channels
+  int T, N, H;
+  int64_t C;               // N * H channels
   void* out;               // h, or dp
-  int64_t ldo;
   float *last;             // hT, or dh0 (nullable)
   float* carry;            // [ceil(T / 128)][C]: written (nullable), or read
-  int64_t groups;          // of channels, one block (warp) each
+  int groups;              // of channels, one block each
+  int whole;               // a warp's channels always belong to one environment
   unsigned div_m;          // c / H = c * div_m >> div_s for c < 2^31
   int div_s;
   int wide;                // rows are read in 16-byte pieces
@@ -116,11 +123,30 @@ __device__ __forceinline__ float joined(float a1, float a2) {
   return a1 < 0.f || a2 < 0.f ? -1.f : a1 * a2;
 }
 
+// Keeps a row step out of the compiler's reach, so that it does not carry its
+// multiples from tile to tile in registers (measured with 16 steps: 128
+// registers and 500 to 1,200 bytes of spills a thread).
+__device__ __forceinline__ int64_t opaque(int64_t v) {
+  asm volatile("" : "+l"(v));
+  return v;
+}
 // Where the state entering a step is cleared (steps outside [0, T): nowhere).
-__device__ __forceinline__ float reset_flag(const ScanArgs& s, int64_t t, int n) {
+__device__ __forceinline__ float reset_flag(const ScanArgs& s, int t, int n) {
   if (t < 0 || t >= s.T) return 0.f;
   if (t == 0) return s.done0 ? __ldg(s.done0 + n) : 0.f;
-  return s.done ? __ldg(s.done + (t - 1) * s.N + n) : 0.f;
+  return s.done ? __ldg(s.done + ((unsigned)(t - 1) * (unsigned)s.N + (unsigned)n)) : 0.f;
+}
+// element j of row t * N + n of a matrix of pitch ld bytes
+template <typename T>
+__device__ __forceinline__ T* element(const ScanArgs& s, const void* base, uint32_t ld, int t, int n,
+                                      int j) {
+  const uint32_t row = (uint32_t)t * (uint32_t)s.N + (uint32_t)n;
+  return reinterpret_cast<T*>(reinterpret_cast<char*>(const_cast<void*>(base)) + (uint64_t)row * ld) +
+         j;
+}
+// rows of one step, in bytes
+__device__ __forceinline__ int64_t step_of(const ScanArgs& s, uint32_t ld) {
+  return opaque((int64_t)((uint64_t)(uint32_t)s.N * ld));
 }
 
 // A channel's environment and its place within it.
@@ -135,7 +161,8 @@ __device__ __forceinline__ Channel channel(const ScanArgs& s, unsigned c) {
 struct Place {
   unsigned c;
   int n, j;
-  bool ok, same;   // same: the warp's channels belong to one environment
+  bool ok, two;   // two: the warp's channels belong to environment n0 or n0 and n1
+  int n0, n1;
 };
 template <int V>
 __device__ __forceinline__ Place place_of(const ScanArgs& s, int group, int lane) {
@@ -143,21 +170,37 @@ __device__ __forceinline__ Place place_of(const ScanArgs& s, int group, int lane
   const unsigned first = (unsigned)group * kWarp * V, C = (unsigned)s.C;
   p.c = first + lane * V;
   p.ok = p.c < C;
-  const int n0 = channel(s, first < C ? first : 0).n;
-  const unsigned lastc = first + kWarp * V <= C ? first + kWarp * V - 1 : C - 1;
-  p.same = first < C && channel(s, lastc).n == n0;
+  const Channel x0 = channel(s, first < C ? first : 0);
+  p.n0 = p.n1 = p.n = x0.n;
+  p.two = true;
+  p.j = x0.j + lane * V;
+  if (s.whole) return p;
   const Channel x = channel(s, p.ok ? p.c : 0);
-  p.n = p.same ? n0 : x.n;   // lanes past the end read the warp's flags too
+  const unsigned lastc = first + kWarp * V <= C ? first + kWarp * V - 1 : C - 1;
+  p.n1 = first < C ? channel(s, lastc).n : x0.n;
+  p.two = p.n1 - p.n0 <= 1;
+  if (p.ok) p.n = x.n;   // lanes past the end read flags of n0
   p.j = x.j;
   return p;
 }
 
-// Bit i: the state entering step t0 + i is cleared.  Where all lanes of the
-// warp belong to one environment, lane i has loaded step i's flag beforehand.
+// Bit i: the state entering step t0 + i is cleared.  Where the warp's channels
+// belong to two environments at most, lanes i and L + i have loaded their flags
+// of step i beforehand (1,023 x 37 x 129 fp32, where a quarter of the warps
+// straddles two: 30 and 44 us; 46 and 60 with every lane's flags loaded here).
 template <int L>
-__device__ __forceinline__ uint32_t reset_mask(const ScanArgs& s, float mine, int64_t t0,
+__device__ __forceinline__ float load_flag(const ScanArgs& s, int t0, const Place& pl, int lane) {
+  if (L == 1 || !pl.two || lane >= 2 * L) return 0.f;
+  return lane < L ? reset_flag(s, t0 + lane, pl.n0) : reset_flag(s, t0 + lane - L, pl.n1);
+}
+template <int L>
+__device__ __forceinline__ uint32_t reset_mask(const ScanArgs& s, float mine, int t0,
                                                const Place& pl) {
-  if (L > 1 && pl.same) return __ballot_sync(0xffffffffu, mine != 0.f);
+  static_assert(2 * L <= kWarp, "a lane for each step and environment");
+  if (L > 1 && pl.two) {
+    const uint32_t all = __ballot_sync(0xffffffffu, mine != 0.f);
+    return (pl.n == pl.n0 ? all : all >> L) & ((1u << L) - 1);
+  }
   uint32_t m = 0;
   if (pl.ok) {
 #pragma unroll
@@ -166,28 +209,18 @@ __device__ __forceinline__ uint32_t reset_mask(const ScanArgs& s, float mine, in
   return m;
 }
 
-// Keeps a row step out of the compiler's reach, so that it does not carry its
-// multiples from tile to tile in registers (measured with 16 steps: 128
-// registers and 500 to 1,200 bytes of spills a thread).
-__device__ __forceinline__ int64_t opaque(int64_t v) {
-  asm volatile("" : "+l"(v));
-  return v;
-}
 // The steps of a thread's block of L in [t0, T): their count.
 template <int L>
-__device__ __forceinline__ int steps_in(int64_t t0, int64_t T) {
-  const int64_t n = T - t0;
-  return n <= 0 ? 0 : n < L ? (int)n : L;
-}
+__device__ __forceinline__ int steps_in(int t0, int T) { return min(max(T - t0, 0), L); }
 
 // One input's L steps of a warp: 2-byte elements in registers ..
 template <typename T, int V, int L>
 struct RegColumn {
   Raw<T, V> r[L];
-  __device__ __forceinline__ void load(const ScanArgs&, const void* base, int64_t ld, int64_t off,
-                                       int64_t t0, int n, const Place& pl, int64_t N, int) {
-    const int64_t step = opaque(N * ld);
-    const T* p = static_cast<const T*>(base) + pl.n * ld + pl.j + off + t0 * step;
+  __device__ __forceinline__ void load(const ScanArgs& s, const void* base, uint32_t ld, int off,
+                                       int t0, int n, const Place& pl, int) {
+    const int64_t step = step_of(s, ld);
+    const char* p = element<const char>(s, base, ld, t0, pl.n, (pl.j + off) * (int)sizeof(T));
 #pragma unroll
     for (int i = 0; i < L; ++i) {
       r[i] = pl.ok && i < n ? __ldg(reinterpret_cast<const Raw<T, V>*>(p)) : Raw<T, V>{};
@@ -202,16 +235,16 @@ struct RegColumn {
 template <typename T, int V, int L>
 struct SharedColumn {
   uint32_t* w;
-  __device__ __forceinline__ void load(const ScanArgs& s, const void* base, int64_t ld, int64_t off,
-                                       int64_t t0, int n, const Place& pl, int64_t N,
-                                       int lane) const {
-    const int64_t step = opaque(N * ld);
+  __device__ __forceinline__ void load(const ScanArgs& s, const void* base, uint32_t ld, int off,
+                                       int t0, int n, const Place& pl, int lane) const {
+    const int64_t step = step_of(s, ld);
     if (s.wide) {
-      const int r0 = lane >> 3;
-      const unsigned c = pl.c - lane * V + (lane & 7) * (16 / (int)sizeof(T));
+      const int r0 = lane >> 3, back = (lane & 7) * (16 / (int)sizeof(T)) - lane * V;
+      const unsigned c = pl.c + back;      // the piece's first channel
       const bool ok = c < (unsigned)s.C;
-      const Channel x = channel(s, ok ? c : 0);
-      const T* p = static_cast<const T*>(base) + x.n * ld + x.j + off + (t0 + r0) * step;
+      Channel x{pl.n, pl.j + back};
+      if (!s.whole) x = channel(s, ok ? c : 0);
+      const char* p = element<const char>(s, base, ld, t0 + r0, x.n, (x.j + off) * (int)sizeof(T));
       uint32_t dst = ptx::smem_u32(w) + r0 * 128 + (lane & 7) * 16;
 #pragma unroll
       for (int i = 0; i < L; i += 4) {
@@ -221,7 +254,7 @@ struct SharedColumn {
         p += 4 * step;
       }
     } else {
-      const T* p = static_cast<const T*>(base) + pl.n * ld + pl.j + off + t0 * step;
+      const char* p = element<const char>(s, base, ld, t0, pl.n, (pl.j + off) * (int)sizeof(T));
       const uint32_t dst = ptx::smem_u32(w) + lane * 4;
 #pragma unroll
       for (int i = 0; i < L; ++i) {
@@ -241,11 +274,27 @@ struct SharedColumn {
   }
 };
 template <typename T, int V> constexpr bool kFetch = sizeof(T) * V == 4;
-constexpr int kStages = 2;
+constexpr int kStages = 2;   // tiles on their way
 __device__ __forceinline__ void fetch_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-__device__ __forceinline__ void fetch_wait() {   // all but the newest kStages - 1 groups
-  asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+template <int STAGES>
+__device__ __forceinline__ void fetch_wait() {   // all but the newest STAGES - 1 groups
+  asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 1) : "memory");
 }
+// what lane i has read of step i's flag, kept with the tile it belongs to
+template <int N>
+struct Flags {
+  float f[N];
+  __device__ __forceinline__ float get(int k) const {
+    float v = f[0];
+#pragma unroll
+    for (int i = 1; i < N; ++i) v = k == i ? f[i] : v;
+    return v;
+  }
+  __device__ __forceinline__ void set(int k, float v) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) f[i] = k == i ? v : f[i];
+  }
+};
 
 // ---- steps in registers ----------------------------------------------------------
 // PLAIN: all L steps exist and none clears a state.
@@ -286,7 +335,7 @@ __device__ __forceinline__ void run_steps(const float (&z)[L][V], const Col& rh,
       vfma<V>(a, h, b, h);
       if (ok) *reinterpret_cast<Raw<T, V>*>(o) = from_f32<T, V>(h);
     }
-    o += ostep;
+    o = reinterpret_cast<T*>(reinterpret_cast<char*>(o) + ostep);
   }
 }
 
@@ -320,7 +369,7 @@ __device__ __forceinline__ void block_back(const float (&z)[L][V], const Col& rg
 template <typename T, int V, int L, bool PLAIN, typename Col>
 __device__ __forceinline__ void run_back(const float (&z)[L][V], const Col& rh, const Col& rg,
                                          int n, uint32_t clear, int lane, bool ok, float (&h)[V],
-                                         float (&u)[V], T* o, int64_t ostep, int64_t H) {
+                                         float (&u)[V], T* o, int64_t ostep, int H) {
   float w[L][V];   // dpz / g of each step
   float one[V], minus[V];
   vset<V>(one, 1.f);
@@ -337,7 +386,7 @@ __device__ __forceinline__ void run_back(const float (&z)[L][V], const Col& rh, 
     vmul<V>(z[i], c, k);
     vfma<V>(a, h, k, h);
   }
-  o += (L - 1) * ostep;
+  o = reinterpret_cast<T*>(reinterpret_cast<char*>(o) + (L - 1) * ostep);
 #pragma unroll
   for (int i = L - 1; i >= 0; --i) {
     float d[V], dz[V], dc[V], a[V];
@@ -354,7 +403,7 @@ __device__ __forceinline__ void run_back(const float (&z)[L][V], const Col& rh, 
         *reinterpret_cast<Raw<T, V>*>(o + H) = from_f32<T, V>(dc);
       }
     }
-    o -= ostep;
+    o = reinterpret_cast<T*>(reinterpret_cast<char*>(o) - ostep);
   }
 }
 
@@ -363,22 +412,26 @@ __device__ __forceinline__ void run_back(const float (&z)[L][V], const Col& rh, 
 // row k, bf16 outputs its upper and lower halves in rows 2k and 2k + 1.  (dp
 // uses its pz columns.)
 template <typename T>
+__device__ __forceinline__ T* below(T* row, int64_t step, int k) {
+  return reinterpret_cast<T*>(reinterpret_cast<char*>(row) + k * step);
+}
+template <typename T>
 __device__ __forceinline__ void put_value(T* row, int64_t step, int k, float v) {
   if constexpr (sizeof(T) == 4) {
-    row[k * step] = v;
+    *below(row, step, k) = v;
   } else {
     const uint32_t u = __float_as_uint(v);
-    row[2 * k * step] = __ushort_as_bfloat16((uint16_t)(u >> 16));
-    row[(2 * k + 1) * step] = __ushort_as_bfloat16((uint16_t)u);
+    *below(row, step, 2 * k) = __ushort_as_bfloat16((uint16_t)(u >> 16));
+    *below(row, step, 2 * k + 1) = __ushort_as_bfloat16((uint16_t)u);
   }
 }
 template <typename T>
-__device__ __forceinline__ float get_value(const T* row, int64_t step, int k) {
+__device__ __forceinline__ float get_value(T* row, int64_t step, int k) {
   if constexpr (sizeof(T) == 4) {
-    return row[k * step];
+    return *below(row, step, k);
   } else {
-    const uint32_t hi = __bfloat16_as_ushort(row[2 * k * step]);
-    return __uint_as_float(hi << 16 | __bfloat16_as_ushort(row[(2 * k + 1) * step]));
+    const uint32_t hi = __bfloat16_as_ushort(*below(row, step, 2 * k));
+    return __uint_as_float(hi << 16 | __bfloat16_as_ushort(*below(row, step, 2 * k + 1)));
   }
 }
 // rows that values 0..k need
@@ -391,18 +444,19 @@ struct Walk {
   int group, tile;
 };
 
-#ifndef TPS
-#define TPS 1024
-#endif
-// threads that the registers of L steps leave room for on an SM
-__host__ __device__ constexpr int threads_per_sm(int L) { return L > 8 ? 512 : TPS; }
-
 enum Phase : int { kWhole = 0, kMaps = 1 };
+
+// Threads of an SM that the registers of L steps leave room for (65,537 x 1 x
+// 1,024 bf16: forward 95 us with 512, 79 with 768; its maps 64 and 56; backward
+// 142 with 512, 249 with 768, which spills).
+__host__ __device__ constexpr int threads_per_sm(int L, int phase, bool backward) {
+  return L <= 8 ? 1024 : phase == kMaps ? 768 : backward ? 512 : 768;
+}
 
 // WT warps along time, WC along channels.  PHASE kMaps writes each tile's map
 // and runs nothing.
 template <typename T, int V, int L, int WT, int WC, int PHASE>
-__global__ void __launch_bounds__(WT* WC* kWarp, L > 1 ? threads_per_sm(L) / (WT * WC * kWarp) : 1)
+__global__ void __launch_bounds__(WT* WC* kWarp, L > 1 ? threads_per_sm(L, PHASE, false) / (WT * WC * kWarp) : 1)
 scan_fwd_kernel(const ScanArgs s) {
   constexpr int CH = WC * kWarp * V, NT = WT * WC * kWarp;
   __shared__ float sa[WT > 1 ? WT : 1][WT > 1 ? CH : 1], sb[WT > 1 ? WT : 1][WT > 1 ? CH : 1];
@@ -410,23 +464,22 @@ scan_fwd_kernel(const ScanArgs s) {
   extern __shared__ __align__(128) uint32_t ring[];   // FETCH: [kStages][pz, ph][warp][L][32]
   const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp;
   const int wt = warp % WT, wc = warp / WT;
-  const int tiles = (int)((s.T + L * WT - 1) / (L * WT)), groups = (int)s.groups;
+  const int tiles = (s.T + L * WT - 1) / (L * WT), groups = s.groups;
   // units: the pairs of a block, dealt out round by round; unsplit, a group's
   // tiles stay with one block
   const int first = s.split ? blockIdx.x / groups : 0;
   using Col = std::conditional_t<FETCH, SharedColumn<T, V, L>, RegColumn<T, V, L>>;
   auto column = [&](int stage, int k) {
-    Col c;
-    if constexpr (FETCH) c.w = ring + ((stage * 2 + k) * (WT * WC) + warp) * (L * kWarp);
-    return c;
+    if constexpr (FETCH) return Col{ring + ((stage * 2 + k) * (WT * WC) + warp) * (L * kWarp)};
+    else return Col{};
   };
   auto place = [&](int group) { return place_of<V>(s, group * WC + wc, lane); };
   auto load = [&](const Place& pl, int tile, Col& cz, Col& ch, float& flag) {
-    const int64_t t0 = ((int64_t)tile * WT + wt) * L;
+    const int t0 = (tile * WT + wt) * L;
     const int n = steps_in<L>(t0, s.T);
-    cz.load(s, s.p, s.ldp, 0, t0, n, pl, s.N, lane);
-    ch.load(s, s.p, s.ldp, s.H, t0, n, pl, s.N, lane);
-    flag = L > 1 && pl.same && lane < L ? reset_flag(s, t0 + lane, pl.n) : 0.f;
+    cz.load(s, s.p, s.ldp, 0, t0, n, pl, lane);
+    ch.load(s, s.p, s.ldp, s.H, t0, n, pl, lane);
+    flag = load_flag<L>(s, t0, pl, lane);
   };
   const int stride = s.split ? gridDim.x / groups : 1;   // tiles from one to the next
   Walk at{(int)(s.split ? blockIdx.x % groups : blockIdx.x), first}, ahead = at;
@@ -438,13 +491,13 @@ scan_fwd_kernel(const ScanArgs s) {
       w.group += gridDim.x;
     }
   };
-  float flags[kStages] = {};
+  Flags<kStages> flags{};
   if constexpr (FETCH) {
 #pragma unroll
     for (int i = 0; i < kStages; ++i) {
       Col cz = column(i, 0), ch = column(i, 1);
       if (more(ahead)) {
-        load(place(ahead.group), ahead.tile, cz, ch, flags[i]);
+        load(place(ahead.group), ahead.tile, cz, ch, flags.f[i]);
         advance(ahead);
       }
       fetch_commit();
@@ -457,10 +510,10 @@ scan_fwd_kernel(const ScanArgs s) {
   int stage = 0;
   while (more(at)) {
     const Place pl = place(at.group);
-    const int64_t t0 = ((int64_t)at.tile * WT + wt) * L;
+    const int t0 = (at.tile * WT + wt) * L;
     const int n = steps_in<L>(t0, s.T);
-    const int64_t ostep = opaque(s.N * s.ldo);
-    T* out = static_cast<T*>(s.out) + pl.n * s.ldo + pl.j + t0 * ostep;
+    const int64_t ostep = step_of(s, s.ldo);
+    T* out = element<T>(s, s.out, s.ldo, t0, pl.n, pl.j);
     if constexpr (PHASE == kWhole) {
       if (at.tile == 0 || s.split) {
         // (split, not h0 itself, which the last tile's block may be replacing)
@@ -481,9 +534,9 @@ scan_fwd_kernel(const ScanArgs s) {
     Col cz = column(stage, 0), rh = column(stage, 1);
     float flag;
     if constexpr (FETCH) {
-      fetch_wait();
+      fetch_wait<kStages>();
       __syncwarp();   // pieces that other lanes fetched
-      flag = stage == 0 ? flags[0] : flags[1];
+      flag = flags.get(stage);
     } else {
       load(pl, at.tile, cz, rh, flag);
     }
@@ -529,7 +582,7 @@ scan_fwd_kernel(const ScanArgs s) {
             const unsigned c = (unsigned)at.group * CH + x;
             if (c < s.C && at.tile < tiles - 1) {   // (the last one's is not needed)
               const Channel e = channel(s, c);
-              T* row = static_cast<T*>(s.out) + e.n * s.ldo + e.j + (int64_t)at.tile * (L * WT) * ostep;
+              T* row = element<T>(s, s.out, s.ldo, at.tile * (L * WT), e.n, e.j);
               put_value<T>(row, ostep, 0, a);
               put_value<T>(row, ostep, 1, b);
             }
@@ -547,7 +600,7 @@ scan_fwd_kernel(const ScanArgs s) {
       if (s.carry && !s.split && pl.ok && n > 0 && t0 % PPO_SCAN_BLOCK == 0) {
 #pragma unroll
         for (int v = 0; v < V; ++v)
-          s.carry[(t0 / PPO_SCAN_BLOCK) * s.C + pl.c + v] = clear & 1u ? 0.f : hin[v];
+          s.carry[(int64_t)(t0 / PPO_SCAN_BLOCK) * s.C + pl.c + v] = clear & 1u ? 0.f : hin[v];
       }
       if (plain) run_steps<T, V, L, true>(z, rh, n, clear, lane, pl.ok, hin, out, ostep);
       else run_steps<T, V, L, false>(z, rh, n, clear, lane, pl.ok, hin, out, ostep);
@@ -566,12 +619,11 @@ scan_fwd_kernel(const ScanArgs s) {
       if (more(ahead)) {
         float f;
         load(place(ahead.group), ahead.tile, cz, rh, f);
-        if (stage == 0) flags[0] = f;
-        else flags[1] = f;
+        flags.set(stage, f);
         advance(ahead);
       }
       fetch_commit();
-      stage ^= 1;
+      stage = stage == kStages - 1 ? 0 : stage + 1;
     }
     advance(at);
   }
@@ -579,7 +631,7 @@ scan_fwd_kernel(const ScanArgs s) {
 
 // A tile of fewer than PPO_SCAN_BLOCK steps has to hold the whole sequence.
 template <typename T, int V, int L, int WT, int WC, int PHASE>
-__global__ void __launch_bounds__(WT* WC* kWarp, L > 1 ? threads_per_sm(L) / (WT * WC * kWarp) : 1)
+__global__ void __launch_bounds__(WT* WC* kWarp, L > 1 ? threads_per_sm(L, PHASE, true) / (WT * WC * kWarp) : 1)
 scan_bwd_kernel(const ScanArgs s) {
   constexpr int CH = WC * kWarp * V, NT = WT * WC * kWarp;
   // maps of the blocks of steps (factor, state), and what they pass back
@@ -590,21 +642,20 @@ scan_bwd_kernel(const ScanArgs s) {
   extern __shared__ __align__(128) uint32_t ring[];   // FETCH: [kStages][pz, dh (, ph)][warp][L][32]
   const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp;
   const int wt = warp % WT, wc = warp / WT;
-  const int tiles = (int)((s.T + L * WT - 1) / (L * WT)), groups = (int)s.groups;
+  const int tiles = (s.T + L * WT - 1) / (L * WT), groups = s.groups;
   using Col = std::conditional_t<FETCH, SharedColumn<T, V, L>, RegColumn<T, V, L>>;
   auto column = [&](int stage, int k) {
-    Col c;
-    if constexpr (FETCH) c.w = ring + ((stage * IN + k) * (WT * WC) + warp) * (L * kWarp);
-    return c;
+    if constexpr (FETCH) return Col{ring + ((stage * IN + k) * (WT * WC) + warp) * (L * kWarp)};
+    else return Col{};
   };
   auto place = [&](int group) { return place_of<V>(s, group * WC + wc, lane); };
   auto load = [&](const Place& pl, int tile, Col& cz, Col& cd, Col& ch, float& flag) {
-    const int64_t t0 = ((int64_t)tile * WT + wt) * L;
+    const int t0 = (tile * WT + wt) * L;
     const int n = steps_in<L>(t0, s.T);
-    cz.load(s, s.p, s.ldp, 0, t0, n, pl, s.N, lane);
-    cd.load(s, s.dh, s.lddh, 0, t0, n, pl, s.N, lane);
-    if constexpr (PHASE == kWhole) ch.load(s, s.p, s.ldp, s.H, t0, n, pl, s.N, lane);
-    flag = L > 1 && pl.same && lane < L ? reset_flag(s, t0 + lane, pl.n) : 0.f;
+    cz.load(s, s.p, s.ldp, 0, t0, n, pl, lane);
+    cd.load(s, s.dh, s.lddh, 0, t0, n, pl, lane);
+    if constexpr (PHASE == kWhole) ch.load(s, s.p, s.ldp, s.H, t0, n, pl, lane);
+    flag = load_flag<L>(s, t0, pl, lane);
   };
   // tiles run from the last to the first
   const int stride = s.split ? gridDim.x / groups : 1;
@@ -619,13 +670,13 @@ scan_bwd_kernel(const ScanArgs s) {
       w.group += gridDim.x;
     }
   };
-  float flags[kStages] = {};
+  Flags<kStages> flags{};
   if constexpr (FETCH) {
 #pragma unroll
     for (int i = 0; i < kStages; ++i) {
       Col a = column(i, 0), b = column(i, 1), c = column(i, IN - 1);
       if (more(ahead)) {
-        load(place(ahead.group), ahead.tile, a, b, c, flags[i]);
+        load(place(ahead.group), ahead.tile, a, b, c, flags.f[i]);
         advance(ahead);
       }
       fetch_commit();
@@ -636,10 +687,10 @@ scan_bwd_kernel(const ScanArgs s) {
   int stage = 0;
   while (more(at)) {
     const Place pl = place(at.group);
-    const int64_t t0 = ((int64_t)at.tile * WT + wt) * L;
+    const int t0 = (at.tile * WT + wt) * L;
     const int n = steps_in<L>(t0, s.T);
-    const int64_t ostep = opaque(s.N * s.ldo);
-    T* out = static_cast<T*>(s.out) + pl.n * s.ldo + pl.j + t0 * ostep;
+    const int64_t ostep = step_of(s, s.ldo);
+    T* out = element<T>(s, s.out, s.ldo, t0, pl.n, pl.j);
     float hin[V], uin[V];   // the state entering this thread's steps, what reaches the last of them
     if constexpr (PHASE == kWhole) {
       const float* from = s.carry + ((int64_t)at.tile * L * WT / PPO_SCAN_BLOCK) * s.C;
@@ -660,8 +711,7 @@ scan_bwd_kernel(const ScanArgs s) {
             uj[k] = in && s.dhT ? s.dhT[c] : 0.f;
           } else if (s.split && in) {
             const Channel e = channel(s, c);
-            uj[k] = get_value<T>(static_cast<const T*>(s.out) + e.n * s.ldo + e.j +
-                                     (int64_t)at.tile * (L * WT) * ostep, ostep, 2);
+            uj[k] = get_value<T>(element<T>(s, s.out, s.ldo, at.tile * (L * WT), e.n, e.j), ostep, 2);
           }
         }
       }
@@ -669,9 +719,9 @@ scan_bwd_kernel(const ScanArgs s) {
     Col cz = column(stage, 0), rg = column(stage, 1), rh = column(stage, IN - 1);
     float flag;
     if constexpr (FETCH) {
-      fetch_wait();
+      fetch_wait<kStages>();
       __syncwarp();
-      flag = stage == 0 ? flags[0] : flags[1];
+      flag = flags.get(stage);
     } else {
       load(pl, at.tile, cz, rg, rh, flag);
     }
@@ -732,9 +782,9 @@ scan_bwd_kernel(const ScanArgs s) {
             }
             const unsigned c = (unsigned)at.group * CH + x;
             // (a last tile too short for them is joined from its steps)
-            if (c < s.C && s.T - (int64_t)at.tile * (L * WT) >= value_rows<T>(1)) {
+            if (c < s.C && s.T - at.tile * (L * WT) >= value_rows<T>(1)) {
               const Channel e = channel(s, c);
-              T* row = static_cast<T*>(s.out) + e.n * s.ldo + e.j + (int64_t)at.tile * (L * WT) * ostep;
+              T* row = element<T>(s, s.out, s.ldo, at.tile * (L * WT), e.n, e.j);
               put_value<T>(row, ostep, 0, a);
               put_value<T>(row, ostep, 1, b);
             }
@@ -768,12 +818,11 @@ scan_bwd_kernel(const ScanArgs s) {
       if (more(ahead)) {
         float f;
         load(place(ahead.group), ahead.tile, cz, rg, rh, f);
-        if (stage == 0) flags[0] = f;
-        else flags[1] = f;
+        flags.set(stage, f);
         advance(ahead);
       }
       fetch_commit();
-      stage ^= 1;
+      stage = stage == kStages - 1 ? 0 : stage + 1;
     }
     advance(at);
   }
@@ -793,11 +842,11 @@ __global__ void __launch_bounds__(kJoinWarps* kWarp) scan_join_kernel(const Scan
   const bool ok = c < s.C;
   const Channel e = channel(s, ok ? (unsigned)c : 0);
   const int n = e.n, j = e.j;
-  const int64_t tiles = (s.T + PPO_SCAN_BLOCK - 1) / PPO_SCAN_BLOCK;
-  T* out = static_cast<T*>(s.out) + n * s.ldo + j;
-  const int64_t need = value_rows<T>(1);
+  const int tiles = (s.T + PPO_SCAN_BLOCK - 1) / PPO_SCAN_BLOCK;
+  const int need = value_rows<T>(1);
+  auto rows_of = [&](int tile) { return element<T>(s, s.out, s.ldo, tile * PPO_SCAN_BLOCK, n, j); };
   // maps 0 .. tiles - 2 forward (what enters tile 0 is h0); tiles - 1 .. 1 backward
-  const int64_t maps = tiles - 1;
+  const int maps = tiles - 1;
   float x = 0.f;
   if (ok) {
     if (!BACK) {
@@ -807,10 +856,10 @@ __global__ void __launch_bounds__(kJoinWarps* kWarp) scan_join_kernel(const Scan
       x = s.dhT ? s.dhT[c] : 0.f;
     }
   }
-  for (int64_t m0 = 0; m0 < maps; m0 += kJoinWarps * kRun) {
+  for (int m0 = 0; m0 < maps; m0 += kJoinWarps * kRun) {
     float a[kRun], b[kRun];
     float ta = 1.f, tb = 0.f;
-    const int64_t ostep = opaque(s.N * s.ldo);
+    const int64_t ostep = step_of(s, s.ldo);
     uint32_t cut = 0;   // forward: the state entering the tile after map i is cleared
     if (!BACK && ok) {
 #pragma unroll
@@ -819,16 +868,16 @@ __global__ void __launch_bounds__(kJoinWarps* kWarp) scan_join_kernel(const Scan
     }
 #pragma unroll
     for (int i = 0; i < kRun; ++i) {
-      const int64_t m = m0 + warp * kRun + i;
+      const int m = m0 + warp * kRun + i;
       a[i] = 1.f;
       b[i] = 0.f;
       if (ok && m < maps) {
-        const int64_t tile = BACK ? tiles - 1 - m : m, t0 = tile * PPO_SCAN_BLOCK;
+        const int tile = BACK ? tiles - 1 - m : m, t0 = tile * PPO_SCAN_BLOCK;
         if (BACK && s.T - t0 < need) {
           // a last tile too short to hold its map: from its steps
-          for (int64_t t = s.T - 1; t >= t0; --t) {
-            const float pz = (float)static_cast<const T*>(s.p)[(t * s.N + n) * s.ldp + j];
-            const float d = (float)static_cast<const T*>(s.dh)[(t * s.N + n) * s.lddh + j];
+          for (int t = s.T - 1; t >= t0; --t) {
+            const float pz = (float)*element<const T>(s, s.p, s.ldp, t, n, j);
+            const float d = (float)*element<const T>(s, s.dh, s.lddh, t, n, j);
             float z[1], q[1] = {pz};
             sigmoid<1>(q, z);
             const bool gone = reset_flag(s, t, n) != 0.f;
@@ -836,8 +885,8 @@ __global__ void __launch_bounds__(kJoinWarps* kWarp) scan_join_kernel(const Scan
             a[i] = gone ? -1.f : joined(a[i], 1.f - z[0]);
           }
         } else {
-          a[i] = get_value<T>(out + t0 * ostep, ostep, 0);
-          b[i] = get_value<T>(out + t0 * ostep, ostep, 1);
+          a[i] = get_value<T>(rows_of(tile), ostep, 0);
+          b[i] = get_value<T>(rows_of(tile), ostep, 1);
         }
       }
     }
@@ -858,36 +907,39 @@ __global__ void __launch_bounds__(kJoinWarps* kWarp) scan_join_kernel(const Scan
     }
 #pragma unroll
     for (int i = 0; i < kRun; ++i) {
-      const int64_t m = m0 + warp * kRun + i;
+      const int m = m0 + warp * kRun + i;
       y = apply(a[i], b[i], y);
       if (ok && m < maps) {
-        const int64_t tile = BACK ? tiles - 2 - m : m + 1, t0 = tile * PPO_SCAN_BLOCK;
-        if (BACK) put_value<T>(out + t0 * ostep, ostep, 2, y);
-        else s.carry[tile * s.C + c] = (cut >> i) & 1u ? 0.f : y;
+        const int tile = BACK ? tiles - 2 - m : m + 1;
+        if (BACK) put_value<T>(rows_of(tile), ostep, 2, y);
+        else s.carry[(int64_t)tile * s.C + c] = (cut >> i) & 1u ? 0.f : y;
       }
     }
   }
 }
 
 // ---- plan -------------------------------------------------------------------------
-constexpr int kSteps = 8;    // of a warp's block; 16 blocks are a tile of PPO_SCAN_BLOCK
+// Steps of a warp's block (with 8, forward 76 us and backward 156 us instead of
+// 72 and 146 at 128 x 2,048 x 256 bf16; 191 and 243 instead of 157 and 220 at
+// 65,537 x 1 x 1,024); 8 blocks are a tile of PPO_SCAN_BLOCK.
+constexpr int kSteps = 16;
 constexpr int kTileWarps = PPO_SCAN_BLOCK / kSteps;
-constexpr int kWalkSteps = 16, kWalkWarps = 8;
 constexpr int kSms = 152;
-#ifndef WALK
-#define WALK 16
-#endif
-#ifndef SPLIT_GROUPS
-#define SPLIT_GROUPS 304
-#endif
-#ifndef SPLIT_TILES
-#define SPLIT_TILES 4
-#endif
+// Channels from which a forward warp walks alone (862 steps of 304 x 512 bf16
+// 151 us so, 167 in blocks; of 152 x 512, below the bound, 214 and 182).
+constexpr int64_t kWalkChannels = kSms * 1024;
+// "split" takes at most this many groups of channels (2,000 steps of 64 groups:
+// 29 and 42 us split, 39 and 58 walked; of 256 groups 125 and 153 split, 57 and
+// 83 walked) and at least this many tiles (600 steps of 64 groups, five tiles:
+// 21 and 22 us split, 13 and 18 walked).
+constexpr int kSplitGroups = 96, kSplitTiles = 8;
 
 template <typename T, int V, int L, int WT, int WC, int PHASE>
 cudaError_t launch(ScanArgs s, bool backward, cudaStream_t st) {
   constexpr int per = kWarp * V * WC, threads = WT * WC * kWarp;
-  s.groups = (s.C + per - 1) / per;
+  if (s.C > (1ll << 31) - per) return cudaErrorInvalidValue;
+  s.groups = (int)((s.C + per - 1) / per);
+  s.whole = s.H % (kWarp * V) == 0;
   const auto kernel = backward ? scan_bwd_kernel<T, V, L, WT, WC, PHASE>
                                : scan_fwd_kernel<T, V, L, WT, WC, PHASE>;
   const int inputs = backward && PHASE == kWhole ? 3 : 2;
@@ -898,8 +950,8 @@ cudaError_t launch(ScanArgs s, bool backward, cudaStream_t st) {
     if (e != cudaSuccess) return e;
   }
   // with fetched columns the blocks that fit an SM together stay on it and walk
-  const int64_t resident = (int64_t)kSms * std::max(1, threads_per_sm(L) / threads);
-  int64_t grid = ring ? std::min(s.groups, resident) : s.groups;
+  const int64_t resident = (int64_t)kSms * std::max(1, threads_per_sm(L, PHASE, backward) / threads);
+  int64_t grid = ring ? std::min<int64_t>(s.groups, resident) : s.groups;
   if (s.split) {
     const int64_t tiles = (s.T + L * WT - 1) / (L * WT);
     grid = s.groups * std::min(tiles, std::max<int64_t>(1, resident / s.groups));
@@ -909,30 +961,28 @@ cudaError_t launch(ScanArgs s, bool backward, cudaStream_t st) {
   return cudaGetLastError();
 }
 
-// Few channels and a long sequence: fewer than one group of channels for every
-// block that the SMs hold, and tiles enough to deal out.  Forward it needs the
-// carry to leave the entering states in.
+// Few channels and a long sequence.  Forward it needs the carry to leave the
+// entering states in.
 template <int V>
 bool splits(const ScanArgs& s, bool backward) {
   // (the first tile's block may replace dhT while the last one's reads it)
   if (backward && s.last && s.last == s.dhT) return false;
   const int64_t groups = (s.C + kWarp * V - 1) / (kWarp * V);
-  return s.carry && groups < SPLIT_GROUPS && s.T >= SPLIT_TILES * PPO_SCAN_BLOCK;
+  return s.carry && groups <= kSplitGroups && s.T >= kSplitTiles * PPO_SCAN_BLOCK;
 }
 
 template <typename T, int V>
 cudaError_t dispatch(ScanArgs s, bool backward, cudaStream_t st) {
   // one step: a thread per channel (pair), nothing to join
   if (s.T == 1) return launch<T, V, 1, 1, 4, kWhole>(s, backward, st);
+  if (s.T <= kSteps / 2) return launch<T, V, kSteps / 2, 1, 8, kWhole>(s, backward, st);
   // enough channels to fill the GPU: forward, a warp walks its channels alone
-  if (!backward && s.C >= (int64_t)kSms * WALK * V * kWarp)
-    return launch<T, V, kWalkSteps, 1, kWalkWarps, kWhole>(s, backward, st);
+  if (s.T <= kSteps || (!backward && s.C >= kWalkChannels))
+    return launch<T, V, kSteps, 1, 8, kWhole>(s, backward, st);
   // short sequences: as many warps along time as there are blocks of steps, the
   // others take more channels
-  if (s.T <= kSteps) return launch<T, V, kSteps, 1, 8, kWhole>(s, backward, st);
-  if (s.T <= 2 * kSteps) return launch<T, V, kSteps, 2, 8, kWhole>(s, backward, st);
-  if (s.T <= 4 * kSteps) return launch<T, V, kSteps, 4, 4, kWhole>(s, backward, st);
-  if (s.T <= 8 * kSteps) return launch<T, V, kSteps, 8, 2, kWhole>(s, backward, st);
+  if (s.T <= 2 * kSteps) return launch<T, V, kSteps, 2, 4, kWhole>(s, backward, st);
+  if (s.T <= 4 * kSteps) return launch<T, V, kSteps, 4, 2, kWhole>(s, backward, st);
   if (splits<V>(s, backward)) {
     s.split = 1;
     cudaError_t e = launch<T, V, kSteps, kTileWarps, 1, kMaps>(s, backward, st);
@@ -965,8 +1015,9 @@ bool aligned(std::initializer_list<const void*> ptrs, int bytes) {
 }
 
 bool sizes_ok(int64_t T, int64_t N, int64_t H) {
-  return T >= 1 && N >= 1 && H >= 1 && H < (1ll << 30) && N < (1ll << 31) && T < (1ll << 31) &&
-         N * H < (1ll << 31) - 4096;
+  constexpr int64_t top = 1ll << 31;
+  return T >= 1 && N >= 1 && H >= 1 && H < (1ll << 28) && N < top && T < top - 4096 && T * N < top &&
+         N * H < top - 4096;
 }
 
 }  // namespace
@@ -980,21 +1031,23 @@ ppo_status ppo_gated_scan_forward(int32_t dtype, const void* p, int64_t ldp, con
                                   cudaStream_t st) {
   using namespace ppo;
   if (!ops::dtype_ok(dtype) || !p || !h || !sizes_ok(T, N, H)) return PPO_ERR_INVALID;
-  if (!ops::extent_ok(T * N, ldp, 2 * H) || !ops::extent_ok(T * N, ldh, H)) return PPO_ERR_INVALID;
+  if (!ops::extent_ok(T * N, ldp, 2 * H) || !ops::extent_ok(T * N, ldh, H) ||
+      ldp >= (1ll << 30) || ldh >= (1ll << 30))
+    return PPO_ERR_INVALID;
   if (!aligned({p, h}, ops::esize(dtype)) || !aligned({done, done0, h0, hT, carry}, 4))
     return PPO_ERR_ALIGN;
   ScanArgs s{};
   s.p = p;
-  s.ldp = ldp;
+  s.ldp = (uint32_t)(ldp * ops::esize(dtype));
   s.done = done;
   s.done0 = done0;
   s.h0 = h0;
-  s.T = T;
-  s.N = N;
-  s.H = H;
+  s.T = (int)T;
+  s.N = (int)N;
+  s.H = (int)H;
   s.C = N * H;
   s.out = h;
-  s.ldo = ldh;
+  s.ldo = (uint32_t)(ldh * ops::esize(dtype));
   s.last = hT;
   s.carry = carry;
   const int piece = 16 / ops::esize(dtype);
@@ -1011,24 +1064,25 @@ ppo_status ppo_gated_scan_backward(int32_t dtype, const void* dh, int64_t lddh, 
   if (!ops::dtype_ok(dtype) || !dh || !p || !carry || !dp || !sizes_ok(T, N, H))
     return PPO_ERR_INVALID;
   if (!ops::extent_ok(T * N, ldp, 2 * H) || !ops::extent_ok(T * N, lddp, 2 * H) ||
-      !ops::extent_ok(T * N, lddh, H))
+      !ops::extent_ok(T * N, lddh, H) || ldp >= (1ll << 30) || lddp >= (1ll << 30) ||
+      lddh >= (1ll << 30))
     return PPO_ERR_INVALID;
   if (!aligned({dh, p, dp}, ops::esize(dtype)) || !aligned({done, done0, carry, dhT, dh0}, 4))
     return PPO_ERR_ALIGN;
   ScanArgs s{};
   s.p = p;
-  s.ldp = ldp;
+  s.ldp = (uint32_t)(ldp * ops::esize(dtype));
   s.dh = dh;
-  s.lddh = lddh;
+  s.lddh = (uint32_t)(lddh * ops::esize(dtype));
   s.done = done;
   s.done0 = done0;
   s.dhT = dhT;
-  s.T = T;
-  s.N = N;
-  s.H = H;
+  s.T = (int)T;
+  s.N = (int)N;
+  s.H = (int)H;
   s.C = N * H;
   s.out = dp;
-  s.ldo = lddp;
+  s.ldo = (uint32_t)(lddp * ops::esize(dtype));
   s.last = dh0;
   s.carry = const_cast<float*>(carry);
   const int piece = 16 / ops::esize(dtype);
