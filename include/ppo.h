@@ -603,9 +603,10 @@ ppo_status ppo_layernorm_backward(int32_t dtype, const void *d_dy, int64_t lddy,
  *   z = sigmoid(pz),   h_t = (1 - z) * h_{t-1} + z * ph.
  * The state entering step t is cleared where d_done[t-1][n] != 0, and the
  * state entering step 0 where d_done0[n] != 0 (both nullable: never; NaN
- * counts as done).  Pointers need only their elements' alignment here, so that
- * one step of a rollout of odd width can be passed as it lies.  A cleared state does not reach the result, whatever it
- * holds.  d_h0 fp32 [N][H], nullable (0).  Outputs: d_h, row t*N + n; d_hT
+ * counts as done).  A cleared state does not reach the result, whatever it
+ * holds.  Pointers need only their elements' alignment here, so that one step
+ * of a rollout of odd width can be passed as it lies; T * N and N * H are below
+ * 2^31 (4,096 less), pitches below 2^30.  d_h0 fp32 [N][H], nullable (0).  Outputs: d_h, row t*N + n; d_hT
  * fp32 [N][H], nullable: the state after the last step (may be d_h0, so that
  * T = 1 advances a carried state by one acting step); d_carry nullable, kept
  * for the backward pass: fp32 [ceil(T / PPO_SCAN_BLOCK)][N][H], the state
@@ -638,7 +639,10 @@ typedef enum {
  *   pre = x W^T + bias,   y = act(pre) + res.
  * d_bias fp32 [N], d_res [M][N], d_pre [M][N] (an output) nullable.  d_y may
  * be d_res (same pitch).  bf16 products run on the tensor cores with fp32
- * accumulation; fp32 ones in fp32 on the CUDA cores.  d_work:
+ * accumulation.  fp32 ones keep fp32's digits: as products of three bf16 planes
+ * of each operand on the tensor cores from M N K = 2^28 on, on the CUDA cores
+ * below.  Forward products of a few rows stream W through the CUDA cores.  M,
+ * N, K are below 2^29, the product of any two at most 2^40.  d_work:
  * ppo_linear_workspace_bytes of the same dtype, sizes and pitches (ldz: the
  * pitch of the [M][N] gradient of ppo_linear_backward_*; a pitch <= 0 stands
  * for the row's length).  Rows of bf16 operands that do not start on 16-byte

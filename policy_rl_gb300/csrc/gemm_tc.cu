@@ -34,7 +34,6 @@
 
 #include "common.cuh"
 #include "gemm.h"
-#include "linear.h"
 #include "reduce.cuh"
 #include "tc_ptx.cuh"
 #include "tc_tile.cuh"
@@ -871,13 +870,12 @@ cudaError_t make_tmap(CUtensorMap* m, const void* base, int64_t cols, int64_t ro
 // box lands in shared memory as box_blk consecutive [box_rows][64] atoms.
 // fp32 split-K partials [splits][rows][cols] as 32-column x 32-row x 1-split boxes
 cudaError_t make_tmap_partials(CUtensorMap* m, const float* base, int64_t cols, int64_t rows,
-                               int64_t splits, int64_t ld) {
-  if (base == nullptr || cols < 1 || rows < 1 || splits < 1 || ld < cols)
-    return cudaErrorInvalidValue;
+                               int64_t splits) {
+  if (base == nullptr || cols < 1 || rows < 1 || splits < 1) return cudaErrorInvalidValue;
   cudaError_t e = get_encode();
   if (e != cudaSuccess) return e;
   cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)splits};
-  cuuint64_t strides[2] = {(cuuint64_t)ld * 4, (cuuint64_t)(ld * rows * 4)};
+  cuuint64_t strides[2] = {(cuuint64_t)cols * 4, (cuuint64_t)(cols * rows * 4)};
   cuuint32_t box[3] = {32, 32, 1};
   cuuint32_t es[3] = {1, 1, 1};
   CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, const_cast<float*>(base), dims,
@@ -981,11 +979,6 @@ cudaError_t tc_make_tmap(CUtensorMap* m, const void* base, int64_t cols, int64_t
 cudaError_t tc_make_tmap_blocks(CUtensorMap* m, const void* base, int64_t rows, int64_t ld,
                                 int nblk, int box_rows, int box_blk) {
   return make_tmap_blocks(m, base, rows, ld, nblk, box_rows, box_blk);
-}
-
-cudaError_t tc_make_tmap_f32(CUtensorMap* m, float* base, int64_t cols, int64_t rows,
-                             int64_t splits, int64_t ld) {
-  return make_tmap_partials(m, base, cols, rows, splits, ld);
 }
 
 int tc_pick_bn(int N) {
@@ -1123,7 +1116,7 @@ cudaError_t tc_wgrad(const WGradRegion* regs, int nreg, int rows, uint32_t mn_lb
     R.k_tiles = (rows + BK - 1) / BK;
     R.kt_per_split = G.kt_per_split;
     R.splits = (R.k_tiles + R.kt_per_split - 1) / R.kt_per_split;
-    e = make_tmap_partials(&tp[r], G.part, G.N, G.M, R.splits, G.N);
+    e = make_tmap_partials(&tp[r], G.part, G.N, G.M, R.splits);
     if (e != cudaSuccess) return e;
     R.unit_begin = unit;
     R.part = G.part;

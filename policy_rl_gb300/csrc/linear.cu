@@ -1,5 +1,5 @@
 // linear.cu -- matrix products with bias, activation and residual: entry
-// points, the fp32 CUDA-core products, and what every product shares (the
+// points, the products on the CUDA cores, and what every product shares (the
 // epilogue of split products, column sums).
 //
 //   forward          y  = act(x W^T + b) + res          [M][N], sum over K
@@ -8,15 +8,18 @@
 //
 // Each is out(i, j) = sum_r A(i, r) B(j, r) with A and B read through a row
 // and a reduction stride; bf16 products run on the tensor cores (linear_tc.cu),
-// fp32 ones here, so that every product and sum keeps fp32's digits.  A product with too few output tiles for the GPU's
-// SMs is cut along the sum; the partial products are added in order by
-// finish_kernel, which then applies the epilogue, so that results do not
-// depend on timing.
+// and so do large fp32 ones, as products of three bf16 planes that together
+// hold fp32's digits; smaller fp32 products run here on the CUDA cores, and so
+// do forward products of a few rows of either type.  A product with too few
+// output tiles for the GPU's SMs is cut along the sum; the partial products are
+// added in order by finish_kernel, which then applies the epilogue, so that
+// results do not depend on timing.
 #include "linear.h"
 
 #include <algorithm>
 
 #include "ops.cuh"
+#include "tc_ptx.cuh"
 
 namespace ppo {
 namespace lin {
@@ -25,11 +28,6 @@ namespace {
 using namespace ops;
 
 // ---- epilogue -------------------------------------------------------------------
-template <typename T>
-__device__ __forceinline__ float at(const void* p, int64_t i) {
-  return (float)static_cast<const T*>(p)[i];
-}
-
 // n (<= 4) consecutive elements of a row, in one piece where rows allow it
 template <typename T>
 __device__ __forceinline__ void get4(const void* p, int64_t at, int n, bool vec, float (&f)[4]) {
@@ -92,12 +90,12 @@ __device__ __forceinline__ void finish4(const Epilogue& e, float (&v)[4], int64_
 
 // An fp32 product straight from its operands.  (The planes of an infinity, or of
 // what rounds to one in bf16, do not add up: their products hold NaN where the
-// product may not.)
+// product may not.)  NaN operands, whose sums are NaN from there on, stop early.
 __device__ __noinline__ float dot_again(const Product& g, int64_t i, int64_t j) {
   const float* A = static_cast<const float*>(g.A) + i * g.sai;
   const float* B = static_cast<const float*>(g.B) + j * g.sbj;
   float v = 0.f;
-  for (int64_t r = 0; r < g.R; ++r) v = fmaf(A[r * g.sar], B[r * g.sbr], v);
+  for (int64_t r = 0; r < g.R && v == v; ++r) v = fmaf(A[r * g.sar], B[r * g.sbr], v);
   return v;
 }
 
@@ -134,6 +132,154 @@ finish_kernel(const float* __restrict__ part, int splits, int64_t I, int64_t J, 
   }
 }
 
+// ---- a few rows ------------------------------------------------------------------------
+// The forward product of few rows: bound by reading W once, and for small W by
+// the launch (one row of 512 -> 2,048 bf16: 2.3 us in a graph, 6.7 on the tensor
+// cores).  A group of wk
+// warps (1, 2 or 4, along the sum) takes CPW columns, every lane 16 bytes of
+// each W row at a time and the same piece of MR rows of x, which stay in L1; the
+// lanes' sums are then folded so that each of MR * CPW lanes holds one.  No
+// tensor maps, no partial products in memory, no copies of rows off 16-byte
+// boundaries: those are read element by element.
+constexpr int kFewGroup = 8, kFewThreads = 256;
+template <typename T, int MR>
+__global__ void __launch_bounds__(kFewThreads)
+few_rows_kernel(const Product g, const Epilogue e, int vec, int wk) {
+  constexpr int CPW = MR >= 4 ? 2 : 1, A = MR * CPW, E = 16 / (int)sizeof(T);
+  constexpr int U = MR >= 4 ? 2 : 4;     // pieces of a W row in flight
+  __shared__ float sums[kFewThreads / kWarp][A];
+  pdl_wait();
+  const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp;
+  const int per = kFewThreads / kWarp / wk;      // groups of a block
+  const int64_t j0 = ((int64_t)blockIdx.x * per + warp / wk) * CPW;
+  const int64_t i0 = (int64_t)blockIdx.y * MR;
+  const int rows = (int)min((int64_t)MR, g.I - i0);
+  // rows and columns past the last one repeat it, so that no load is conditional
+  const T *x[MR], *w[CPW];
+#pragma unroll
+  for (int m = 0; m < MR; ++m) x[m] = static_cast<const T*>(g.A) + (i0 + min(m, rows - 1)) * g.sai;
+#pragma unroll
+  for (int c = 0; c < CPW; ++c)
+    w[c] = static_cast<const T*>(g.B) + min(j0 + c, g.J - 1) * g.sbj;
+  float2 pair[A];      // sums of even and odd elements
+#pragma unroll
+  for (int i = 0; i < A; ++i) pair[i] = make_float2(0.f, 0.f);
+  int64_t k = 0;
+  if (vec) {
+    const int64_t whole = g.R / E * E;
+    const int64_t step = (int64_t)wk * kWarp * E;
+    k = ((int64_t)(warp % wk) * kWarp + lane) * E;
+    for (; k < whole; k += U * step) {
+      Raw<T, E> rw[U][CPW];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int c = 0; c < CPW; ++c)
+          rw[u][c] = k + u * step < whole ? __ldg(reinterpret_cast<const Raw<T, E>*>(w[c] + k + u * step))
+                                          : Raw<T, E>{};
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (k + u * step >= whole) break;
+        Raw<T, E> rx[MR];
+#pragma unroll
+        for (int m = 0; m < MR; ++m) rx[m] = __ldg(reinterpret_cast<const Raw<T, E>*>(x[m] + k + u * step));
+        float fw[CPW][E];
+#pragma unroll
+        for (int c = 0; c < CPW; ++c) to_f32<T, E>(rw[u][c], fw[c]);
+#pragma unroll
+        for (int m = 0; m < MR; ++m) {
+          float fx[E];
+          to_f32<T, E>(rx[m], fx);
+#pragma unroll
+          for (int c = 0; c < CPW; ++c)
+#pragma unroll
+            for (int i = 0; i < E; i += 2)
+              pair[m * CPW + c] = ptx::ffma2(make_float2(fx[i], fx[i + 1]),
+                                             make_float2(fw[c][i], fw[c][i + 1]), pair[m * CPW + c]);
+        }
+      }
+    }
+    k = whole;
+  }
+  float acc[A];
+#pragma unroll
+  for (int i = 0; i < A; ++i) acc[i] = pair[i].x + pair[i].y;
+#pragma unroll 4
+  for (k += (int64_t)(warp % wk) * kWarp + lane; k < g.R; k += (int64_t)wk * kWarp) {
+    float f[CPW];
+#pragma unroll
+    for (int c = 0; c < CPW; ++c) f[c] = (float)w[c][k];
+#pragma unroll
+    for (int m = 0; m < MR; ++m)
+#pragma unroll
+      for (int c = 0; c < CPW; ++c) acc[m * CPW + c] = fmaf((float)x[m][k], f[c], acc[m * CPW + c]);
+  }
+  // lanes fold their sums: each keeps half of them and takes the other lane's
+  // share, until one is left
+  int mine = 0;
+#pragma unroll
+  for (int n = A, off = 16; off >= 1; off >>= 1) {
+    if (n > 1) {
+      n >>= 1;
+      const bool up = lane & off;
+#pragma unroll
+      for (int i = 0; i < n; ++i) {
+        const float give = up ? acc[i] : acc[i + n], keep = up ? acc[i + n] : acc[i];
+        acc[i] = keep + __shfl_xor_sync(0xffffffffu, give, off);
+      }
+      mine += up ? n : 0;
+    } else {
+      acc[0] += __shfl_xor_sync(0xffffffffu, acc[0], off);
+    }
+  }
+  const bool holds = (lane & (kWarp / A - 1)) == 0;
+  float v[4] = {acc[0], 0.f, 0.f, 0.f};
+  if (wk > 1) {
+    if (holds) sums[warp][mine] = acc[0];
+    __syncthreads();
+    if (warp % wk != 0) return;
+    v[0] = 0.f;
+    for (int i = 0; i < wk; ++i) v[0] += sums[warp + i][mine];
+  }
+  const int64_t j = j0 + mine % CPW;
+  if (holds && mine / CPW < rows && j < g.J) finish4<T>(e, v, i0 + mine / CPW, j, 1, false);
+}
+
+// Whether a forward product takes few_rows_kernel, by how often it reads W's
+// elements: two rows always do; a group of up to four rows costs half a group
+// of eight, and rows read element by element would have to be copied otherwise.
+// (Measured in a graph, bf16, 8 rows: 1,024 x 1,024 4.3 us and 8.5 on the tensor
+// cores, 2,048 x 2,048 7.1 and 7.5, 4,096 x 4,096 30 and 14; one row of the last
+// 10.4 and 14.4.  fp32, 8 rows: 46 us at 4,096 x 4,096, 91 in 64 x 64 tiles.)
+template <typename T>
+bool takes_few_rows(const Product& g) {
+  constexpr int E = 16 / (int)sizeof(T);
+  if (g.I <= 2 || (sizeof(T) == 4 && g.I <= kFewGroup)) return true;
+  const bool vec = g.sai % E == 0 && g.sbj % E == 0;
+  const int64_t groups2 = g.I <= 4 ? 1 : 2 * ((g.I + kFewGroup - 1) / kFewGroup);   // halves
+  return groups2 * g.J * g.R <= (vec ? 1ll << 22 : 1ll << 23);
+}
+
+template <typename T>
+cudaError_t few_rows(const Product& g, const Epilogue& e, cudaStream_t st) {
+  constexpr int E = 16 / (int)sizeof(T);
+  const int vec = g.sai % E == 0 && g.sbj % E == 0;
+  auto go = [&](auto kernel, int cpw) {
+    // warps along the sum until there are 4,096 (one row of 1,024 -> 8,192 bf16
+    // 6.9 us with one, 14 with four; 2,048 -> 512 3.5 and 2.5)
+    int wk = 1;
+    while (wk < 4 && g.J / cpw * wk < 4096 && g.R >= 4 * wk * kWarp * E) wk *= 2;
+    const int64_t cols = (int64_t)(kFewThreads / kWarp / wk) * cpw;
+    return launch_pdl(kernel, dim3((unsigned)((g.J + cols - 1) / cols),
+                                   (unsigned)((g.I + kFewGroup - 1) / kFewGroup)),
+                      dim3(kFewThreads), 0, st, g, e, vec, wk);
+  };
+  if (g.I <= 1) return go(few_rows_kernel<T, 1>, 1);
+  if (g.I <= 2) return go(few_rows_kernel<T, 2>, 1);
+  if (g.I <= 4) return go(few_rows_kernel<T, 4>, 2);
+  return go(few_rows_kernel<T, kFewGroup>, 2);
+}
+
 // ---- fp32 products ----------------------------------------------------------------
 // 64 x 64 output tiles, 16 of the sum at a time, 4 x 4 outputs a thread; the
 // next k-tile's loads are in flight while this one is multiplied.
@@ -141,16 +287,17 @@ constexpr int kTile = 64, kStep = 16, kSimtThreads = 256;
 constexpr int kPer = kTile * kStep / kSimtThreads;
 
 // AR (BR): the reduction index is the contiguous one of A (B)
-template <typename T, bool AR, bool BR>
+template <bool AR, bool BR>
 __global__ void __launch_bounds__(kSimtThreads)
-simt_kernel(const Product g, const Epilogue e, int vec, float* __restrict__ part,
-            int64_t r_per_split) {
+simt_kernel(const Product g, const Epilogue e, int vec, float* __restrict__ part, int64_t r_per_split,
+            unsigned tiles_j) {
   __shared__ float As[kStep][kTile + 4], Bs[kStep][kTile + 4];
-  const int64_t i0 = (int64_t)blockIdx.y * kTile, j0 = (int64_t)blockIdx.x * kTile;
+  const unsigned ti = blockIdx.x / tiles_j;
+  const int64_t i0 = (int64_t)ti * kTile, j0 = (int64_t)(blockIdx.x - ti * tiles_j) * kTile;
   const int64_t r0 = (int64_t)blockIdx.z * r_per_split, r1 = min(g.R, r0 + r_per_split);
   const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-  const T* A = static_cast<const T*>(g.A);
-  const T* B = static_cast<const T*>(g.B);
+  const float* A = static_cast<const float*>(g.A);
+  const float* B = static_cast<const float*>(g.B);
   float ra[kPer], rb[kPer];
   auto fetch = [&](int64_t rb0) {
 #pragma unroll
@@ -158,8 +305,8 @@ simt_kernel(const Product g, const Epilogue e, int vec, float* __restrict__ part
       const int idx = threadIdx.x + q * kSimtThreads;
       const int ka = AR ? idx % kStep : idx / kTile, ia = AR ? idx / kStep : idx % kTile;
       const int kb = BR ? idx % kStep : idx / kTile, jb = BR ? idx / kStep : idx % kTile;
-      ra[q] = rb0 + ka < r1 && i0 + ia < g.I ? (float)A[(i0 + ia) * g.sai + (rb0 + ka) * g.sar] : 0.f;
-      rb[q] = rb0 + kb < r1 && j0 + jb < g.J ? (float)B[(j0 + jb) * g.sbj + (rb0 + kb) * g.sbr] : 0.f;
+      ra[q] = rb0 + ka < r1 && i0 + ia < g.I ? A[(i0 + ia) * g.sai + (rb0 + ka) * g.sar] : 0.f;
+      rb[q] = rb0 + kb < r1 && j0 + jb < g.J ? B[(j0 + jb) * g.sbj + (rb0 + kb) * g.sbr] : 0.f;
     }
   };
   float acc[4][4] = {};
@@ -195,7 +342,7 @@ simt_kernel(const Product g, const Epilogue e, int vec, float* __restrict__ part
       *reinterpret_cast<float4*>(part + (blockIdx.z * g.I + oi) * ldp + oj) =
           make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
     else
-      finish4<T>(e, acc[i], oi, oj, (int)min((int64_t)4, g.J - oj), vec);
+      finish4<float>(e, acc[i], oi, oj, (int)min((int64_t)4, g.J - oj), vec);
   }
 }
 
@@ -203,9 +350,8 @@ simt_kernel(const Product g, const Epilogue e, int vec, float* __restrict__ part
 // db: a block sums kSumCols columns over a chunk of rows, its warps taking
 // every eighth row; the chunks are added by finish_kernel.
 constexpr int kSumThreads = 256, kSumCols = 32;
-template <typename T>
 __global__ void __launch_bounds__(kSumThreads)
-colsum_kernel(const void* a, int64_t ld, int64_t rows, int64_t cols, int64_t rows_per_chunk,
+colsum_kernel(const float* a, int64_t ld, int64_t rows, int64_t cols, int64_t rows_per_chunk,
               float* __restrict__ part) {
   __shared__ float s[kSumThreads / kWarp][kWarp];
   const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp;
@@ -214,7 +360,7 @@ colsum_kernel(const void* a, int64_t ld, int64_t rows, int64_t cols, int64_t row
   float t = 0.f;
   if (c < cols) {
 #pragma unroll 8
-    for (int64_t r = r0 + warp; r < r1; r += kSumThreads / kWarp) t += at<T>(a, r * ld + c);
+    for (int64_t r = r0 + warp; r < r1; r += kSumThreads / kWarp) t += a[r * ld + c];
   }
   s[warp][lane] = t;
   __syncthreads();
@@ -247,7 +393,6 @@ size_t split_bytes(int64_t I, int64_t J, int64_t R) {
 
 // Whether pieces of four elements are aligned in all matrices of an epilogue
 // (bases are on 16 bytes).
-template <typename T>
 int fours(const Epilogue& e) {
   return e.ldo % 4 == 0 && (!e.res || e.ldres % 4 == 0) && (!e.pre || e.ldpre % 4 == 0);
 }
@@ -257,25 +402,25 @@ cudaError_t launch_finish(const float* part, int64_t splits, int64_t I, int64_t 
                           const Epilogue& e, cudaStream_t st, const Product& g = {}) {
   const int64_t blocks = std::min<int64_t>(cdiv(I * ldp / 4, kFinishThreads), 16 * kSms);
   return launch_pdl(finish_kernel<T>, dim3((unsigned)blocks), dim3(kFinishThreads), 0, st, part,
-                    (int)splits, I, J, ldp, e, fours<T>(e), g);
+                    (int)splits, I, J, ldp, e, fours(e), g);
 }
 
-template <typename T>
 cudaError_t simt_product(const Product& g, const Epilogue& e, float* part, cudaStream_t st) {
   const int64_t splits = simt_splits(g.I, g.J, g.R);
   const int64_t per = cdiv(cdiv(g.R, splits), kStep) * kStep;
   const int64_t used = cdiv(g.R, per);
-  if (cdiv(g.I, kTile) > 65535) return cudaErrorInvalidValue;
-  const dim3 grid((unsigned)cdiv(g.J, kTile), (unsigned)cdiv(g.I, kTile), (unsigned)used);
+  const int64_t tiles_j = cdiv(g.J, kTile), tiles = cdiv(g.I, kTile) * tiles_j;
+  const dim3 grid((unsigned)tiles, 1, (unsigned)used);
   float* pp = used > 1 ? part : nullptr;
   const bool ar = g.sar == 1, br = g.sbr == 1;
-  const int vec = fours<T>(e);
-  if (ar && br) simt_kernel<T, true, true><<<grid, kSimtThreads, 0, st>>>(g, e, vec, pp, per);
-  else if (ar) simt_kernel<T, true, false><<<grid, kSimtThreads, 0, st>>>(g, e, vec, pp, per);
-  else simt_kernel<T, false, false><<<grid, kSimtThreads, 0, st>>>(g, e, vec, pp, per);
+  const int vec = fours(e);
+  const unsigned tj = (unsigned)tiles_j;
+  if (ar && br) simt_kernel<true, true><<<grid, kSimtThreads, 0, st>>>(g, e, vec, pp, per, tj);
+  else if (ar) simt_kernel<true, false><<<grid, kSimtThreads, 0, st>>>(g, e, vec, pp, per, tj);
+  else simt_kernel<false, false><<<grid, kSimtThreads, 0, st>>>(g, e, vec, pp, per, tj);
   const cudaError_t err = cudaGetLastError();
   if (err != cudaSuccess || used == 1) return err;
-  return launch_finish<T>(pp, used, g.I, g.J, part_pitch(g.J), e, st);
+  return launch_finish<float>(pp, used, g.I, g.J, part_pitch(g.J), e, st);
 }
 
 // ---- bf16 operands on 16-byte rows ---------------------------------------------------
@@ -286,9 +431,6 @@ size_t packed_bytes(int64_t rows, int64_t cols, int64_t ld) {
   if (ld <= 0) ld = cols;
   return ld % 8 ? (size_t)(rows * pitch8(cols) * 2 + 255) / 256 * 256 : 0;
 }
-#ifndef PLANES
-#define PLANES (1ll << 28)
-#endif
 constexpr int kPackThreads = 256;
 __global__ void __launch_bounds__(kPackThreads)
 pack_rows_kernel(const __nv_bfloat16* __restrict__ src, int64_t ld, int64_t rows, int64_t cols,
@@ -358,9 +500,10 @@ split_planes_kernel(const float* __restrict__ src, int64_t ld, int64_t rows, int
     dst[2 * n + k] = from_f32<__nv_bfloat16, 8>(p3);
   }
 }
-// Fewer multiplications than this take the CUDA cores: one launch instead of
-// four (measured: XXX)
-bool takes_planes(int64_t M, int64_t N, int64_t K) { return M * N * K >= PLANES; }
+// Fewer multiplications than this take the CUDA cores, one launch instead of
+// four (at 1.3e8 of them 21 to 23 us a product, 23 to 25 by planes; at 3.6e9 230
+// to 460 us, and 92 to 105 by planes).
+bool takes_planes(int64_t M, int64_t N, int64_t K) { return M * N * K >= 1ll << 28; }
 
 size_t tc_part_bytes(int64_t I, int64_t J, int64_t R, bool must_split, int terms = 1) {
   const TcPlan p = tc_plan(I, J, R, must_split, terms);
@@ -419,7 +562,6 @@ finish_weight_kernel(const float* __restrict__ part, int splits, int64_t I, int6
 }
 
 cudaError_t tc_run(const Product& g, const Epilogue& e, char* work, int* err, cudaStream_t st) {
-  if (!tc_fits(g)) return cudaErrorInvalidValue;
   const TcPlan plan = tc_plan(g.I, g.J, g.R, false);
   float* part = plan.splits > 1 ? reinterpret_cast<float*>(work) : nullptr;
   const cudaError_t x = tc_product(g, e, plan, part, nullptr, err, num_sms(), st);
@@ -460,9 +602,9 @@ size_t planes_need(int64_t ra, int64_t ca, int64_t rb, int64_t cb, int64_t I, in
 // The fp32 product on the units that suit its size.
 cudaError_t run_f32(const Product& g, const Epilogue& e, int64_t M, int64_t N, int64_t K, void* work,
                     float* part, cudaStream_t st) {
-  if (takes_planes(M, N, K) && tc_fits(g))
+  if (takes_planes(M, N, K))
     return planes_run(g, e, reinterpret_cast<char*>(part), static_cast<int*>(work), st);
-  return simt_product<float>(g, e, part, st);
+  return simt_product(g, e, part, st);
 }
 
 // A gradient that is added to, or whose rows TMA cannot store, is finished from
@@ -474,7 +616,6 @@ size_t tc_sum_bytes(int64_t N, int64_t K, int64_t M, bool must) {
 }
 cudaError_t tc_run_weight(const Product& g, const Epilogue& e, float* db, char* work, int* err,
                           cudaStream_t st) {
-  if (!tc_fits(g)) return cudaErrorInvalidValue;
   const bool must = must_finish(g.J, e.accumulate);
   const TcPlan plan = tc_plan(g.I, g.J, g.R, must);
   const int64_t rows = tc_sum_rows(g, plan);
@@ -492,12 +633,11 @@ cudaError_t tc_run_weight(const Product& g, const Epilogue& e, float* db, char* 
                     (const float*)sums, rows, db, e.accumulate, wb);
 }
 
-template <typename T>
-cudaError_t column_sums(const void* dz, int64_t ld, int64_t M, int64_t N, float* db,
+cudaError_t column_sums(const float* dz, int64_t ld, int64_t M, int64_t N, float* db,
                         int accumulate, float* part, cudaStream_t st) {
   const int64_t chunks = sum_chunks(M, N), per = cdiv(M, chunks), used = cdiv(M, per);
   const dim3 grid((unsigned)cdiv(N, kSumCols), (unsigned)used);
-  colsum_kernel<T><<<grid, kSumThreads, 0, st>>>(dz, ld, M, N, per, part);
+  colsum_kernel<<<grid, kSumThreads, 0, st>>>(dz, ld, M, N, per, part);
   const cudaError_t err = cudaGetLastError();
   if (err != cudaSuccess) return err;
   Epilogue e{};
@@ -505,11 +645,12 @@ cudaError_t column_sums(const void* dz, int64_t ld, int64_t M, int64_t N, float*
   e.out = db;
   e.ldo = N;
   e.accumulate = accumulate;
-  return launch_finish<T>(part, used, 1, N, part_pitch(N), e, st);
+  return launch_finish<float>(part, used, 1, N, part_pitch(N), e, st);
 }
 
 bool sizes_ok(int64_t M, int64_t N, int64_t K) {
-  constexpr int64_t top = 1ll << 31;
+  // 32-bit TMA coordinates, of three planes too, and tile counts
+  constexpr int64_t top = 1ll << 29;
   return M >= 1 && N >= 1 && K >= 1 && M < top && N < top && K < top && M <= (1ll << 40) / N &&
          M <= (1ll << 40) / K && N <= (1ll << 40) / K;
 }
@@ -597,9 +738,11 @@ ppo_status ppo_linear_forward(int32_t dtype, const void* x, int64_t ldx, const v
   e.ldpre = ldpre;
   e.out = y;
   e.ldo = ldy;
+  const lin::Product g{x, ldx, 1, w, ldw, 1, M, N, K};
   if (dtype == PPO_DTYPE_F32)
-    return status_of(
-        lin::run_f32({x, ldx, 1, w, ldw, 1, M, N, K}, e, M, N, K, work, parts(work), st));
+    return status_of(lin::takes_few_rows<float>(g) ? lin::few_rows<float>(g, e, st)
+                                                   : lin::run_f32(g, e, M, N, K, work, parts(work), st));
+  if (lin::takes_few_rows<__nv_bfloat16>(g)) return status_of(lin::few_rows<__nv_bfloat16>(g, e, st));
   char* free = reinterpret_cast<char*>(parts(work));
   cudaError_t err = lin::on_16_bytes(x, ldx, M, K, free, st);
   if (err == cudaSuccess) err = lin::on_16_bytes(w, ldw, N, K, free, st);
@@ -661,7 +804,7 @@ ppo_status ppo_linear_backward_weight(int32_t dtype, const void* dz, int64_t ldd
     cudaError_t err =
         lin::run_f32({dz, 1, lddz, x, 1, ldx, N, K, M}, e, M, N, K, work, parts(work), st);
     if (err == cudaSuccess && db)
-      err = lin::column_sums<float>(dz, lddz, M, N, db, e.accumulate, parts(work), st);
+      err = lin::column_sums(static_cast<const float*>(dz), lddz, M, N, db, e.accumulate, parts(work), st);
     return status_of(err);
   }
   char* free = reinterpret_cast<char*>(parts(work));

@@ -44,7 +44,6 @@ struct TcPlan {
 // terms: products of bf16 planes that make one product (fp32 operands: kTerms)
 constexpr int kTerms = 6;
 TcPlan tc_plan(int64_t I, int64_t J, int64_t R, bool must_split, int terms = 1);
-bool tc_fits(const Product& g);
 // Row pitch of partial products: rows start on 32-byte boundaries.
 __host__ __device__ constexpr int64_t part_pitch(int64_t J) { return (J + 7) / 8 * 8; }
 // Rows of partial column sums that the weight gradient's kernel leaves.
@@ -59,9 +58,4 @@ cudaError_t tc_product(const Product& g, const Epilogue& e, const TcPlan& plan, 
                        int64_t plane_b = 0);
 
 }  // namespace lin
-
-// fp32 [splits][rows][cols] with row pitch ld (a multiple of 4) as 32-column x
-// 32-row x 1-split boxes, 128-byte swizzle (gemm_tc.cu)
-cudaError_t tc_make_tmap_f32(CUtensorMap* m, float* base, int64_t cols, int64_t rows,
-                             int64_t splits, int64_t ld);
 }  // namespace ppo

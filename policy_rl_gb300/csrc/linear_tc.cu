@@ -622,7 +622,7 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
       int ti, tj, kt0, kt1, split;
       unit_of(u, ti, tj, kt0, kt1, split);
       const int64_t row0 = (int64_t)(ti * CG + (int)rank) * BM + q * 32, row = row0 + lane;
-      const bool rok = row < p.I, any = row0 < p.I;
+      const bool any = row0 < p.I;
       const int64_t col0 = (int64_t)tj * BN + part * PART;
       uint32_t taddr;
       if constexpr (MODE == kWeight) {
@@ -933,13 +933,6 @@ TcPlan tc_plan(int64_t I, int64_t J, int64_t R, bool must_split, int terms) {
     }
   }
   return best;
-}
-
-bool tc_fits(const Product& g) {
-  // TMA coordinates (of planes too) and tile counts are 32-bit
-  constexpr int64_t top = (1ll << 29);
-  return g.I < top && g.J < top && g.R < top &&
-         cdiv(g.I, BM) * cdiv(g.J, 128) < (1ll << 30);
 }
 
 int64_t tc_sum_rows(const Product& g, const TcPlan& plan) {

@@ -501,6 +501,55 @@ def test_linear_nan_stays_in_its_row(P):
         assert list(np.flatnonzero(~np.isfinite(f64(y)).all(1))) == [7]
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("M,N,K", [(1, 5, 4104), (2, 33, 2056), (3, 16, 7), (4, 1030, 520), (5, 9, 1032), (8, 1001, 300),
+                                   (16, 64, 1024), (23, 40, 2051), (40, 24, 136)])
+def test_linear_few_rows(P, M, N, K, dtype):
+    check_linear(P, M, N, K, dtype, act="gelu", seed=11 + M)
+    check_linear(P, M, N, K, dtype, act="silu", bias=False, res=False, pitch=(K + 3, K + 5, max(N, K) + 1), seed=12 + M)
+
+
+@pytest.mark.parametrize("M", [1, 6, 200])
+def test_linear_one_output_per_row(P, M):
+    check_linear(P, M, 1, 260, "bf16", seed=13)
+    check_linear(P, M, 1, 260, "f32", seed=13)
+
+
+@pytest.mark.parametrize("pitch", [None, (645, 643, 650), (648, 641, 644)])
+def test_linear_f32_in_planes(P, pitch):
+    """Sizes that take the tensor cores: 2^28 multiplications and more."""
+    check_linear(P, 700, 641, 639, "f32", act="tanh", pact="gelu", dres=True, pitch=pitch, seed=14)
+
+
+def test_linear_f32_infinities_nan_and_what_rounds_to_infinity(P):
+    """An element that bf16 rounds to an infinity, an infinity, a NaN, sums past
+    fp32's range: as the fp32 product has them, in their rows alone."""
+    import torch
+    rng = np.random.default_rng(15)
+    M, N, K = 700, 640, 640
+    x, w = dev(rng.normal(size=(M, K))), dev(rng.normal(size=(N, K)) / 25)
+    x[3, 5] = float("inf")
+    x[9, 1] = float("nan")
+    x[20] = 0.0
+    x[20, 7] = 3.4e38           # bf16's largest is 3.39e38
+    x[31] = 3.0e38
+    w[:, 7] = w[:, 7].abs().clamp(max=0.5) + 0.01
+    w[0] = 1.0                  # x[31] w[0] leaves fp32's range
+    w[1, 5] = 0.0               # infinity times zero
+    y = out((M, N))
+    work = torch.zeros(P.ppo_linear_workspace_bytes(M, N, K, x.dtype), dtype=torch.uint8, device="cuda")
+    P.ppo_linear_forward(x, w, y, work=work)
+    P.ppo_work_status(work)
+    Y, X, W = f64(y), f64(x), f64(w)
+    rest = np.setdiff1d(np.arange(M), [3, 9, 31])
+    ref = X[rest] @ W.T
+    within(y[torch.from_numpy(rest).cuda()], ref, prod_bound("f32", X[rest], W.T, K), "rows without special values")
+    sign = np.sign(W[:, 5])
+    assert np.isnan(Y[3, 1]) and (np.delete(Y[3], 1) == np.delete(sign, 1) * np.inf).all()
+    assert np.isnan(Y[9]).all()
+    assert Y[31, 0] == np.inf
+
+
 def test_linear_past_32_bit_offsets(P):
     import torch
     M, N, K = 1100000, 2048, 64             # 2.3e9 outputs
