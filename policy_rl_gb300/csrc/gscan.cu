@@ -27,8 +27,8 @@
 //     rows of the output that the third launch overwrites.
 // Measured, forward and backward, bf16: 128 x 2,048 x 256 72 us (5.6 TB/s) and
 // 146 us (4.6 TB/s: limited by the instructions of the walk back, two blocks of
-// 128 registers a thread on an SM); 65,537 x 1 x 1,024 157 and 220 us, of which
-// the maps take 56 and 55, the join 18, the run 79 and 143.
+// 128 registers a thread on an SM); 65,537 x 1 x 1,024 151 and 214 us, of which
+// the maps take 55, the join 14, the run 78 and 142.
 // Compositions happen in an order fixed by the sizes: results are
 // deterministic.  A cleared state is dropped by a select, never multiplied by
 // 0, so that infinities and NaN do not cross it.
@@ -491,13 +491,16 @@ scan_fwd_kernel(const ScanArgs s) {
       w.group += gridDim.x;
     }
   };
+  // the maps are made from the last tile on, so that the run that follows finds
+  // the first ones' inputs in L2
+  auto tile_of = [&](const Walk& w) { return PHASE == kMaps ? tiles - 1 - w.tile : w.tile; };
   Flags<kStages> flags{};
   if constexpr (FETCH) {
 #pragma unroll
     for (int i = 0; i < kStages; ++i) {
       Col cz = column(i, 0), ch = column(i, 1);
       if (more(ahead)) {
-        load(place(ahead.group), ahead.tile, cz, ch, flags.f[i]);
+        load(place(ahead.group), tile_of(ahead), cz, ch, flags.f[i]);
         advance(ahead);
       }
       fetch_commit();
@@ -510,14 +513,15 @@ scan_fwd_kernel(const ScanArgs s) {
   int stage = 0;
   while (more(at)) {
     const Place pl = place(at.group);
-    const int t0 = (at.tile * WT + wt) * L;
+    const int tile = tile_of(at);
+    const int t0 = (tile * WT + wt) * L;
     const int n = steps_in<L>(t0, s.T);
     const int64_t ostep = step_of(s, s.ldo);
     T* out = element<T>(s, s.out, s.ldo, t0, pl.n, pl.j);
     if constexpr (PHASE == kWhole) {
-      if (at.tile == 0 || s.split) {
+      if (tile == 0 || s.split) {
         // (split, not h0 itself, which the last tile's block may be replacing)
-        const float* from = s.split ? s.carry + (int64_t)at.tile * s.C : s.h0;
+        const float* from = s.split ? s.carry + (int64_t)tile * s.C : s.h0;
         if constexpr (WT == 1) {
 #pragma unroll
           for (int v = 0; v < V; ++v) h[v] = pl.ok && from ? from[pl.c + v] : 0.f;
@@ -538,7 +542,7 @@ scan_fwd_kernel(const ScanArgs s) {
       __syncwarp();   // pieces that other lanes fetched
       flag = flags.get(stage);
     } else {
-      load(pl, at.tile, cz, rh, flag);
+      load(pl, tile, cz, rh, flag);
     }
     float z[L][V];
 #pragma unroll
@@ -580,9 +584,9 @@ scan_fwd_kernel(const ScanArgs s) {
               a = joined(a, sa[w][x]);
             }
             const unsigned c = (unsigned)at.group * CH + x;
-            if (c < s.C && at.tile < tiles - 1) {   // (the last one's is not needed)
+            if (c < s.C && tile < tiles - 1) {   // (the last one's is not needed)
               const Channel e = channel(s, c);
-              T* row = element<T>(s, s.out, s.ldo, at.tile * (L * WT), e.n, e.j);
+              T* row = element<T>(s, s.out, s.ldo, tile * (L * WT), e.n, e.j);
               put_value<T>(row, ostep, 0, a);
               put_value<T>(row, ostep, 1, b);
             }
@@ -618,7 +622,7 @@ scan_fwd_kernel(const ScanArgs s) {
       __syncwarp();   // the warp has read its words: they may be refilled
       if (more(ahead)) {
         float f;
-        load(place(ahead.group), ahead.tile, cz, rh, f);
+        load(place(ahead.group), tile_of(ahead), cz, rh, f);
         flags.set(stage, f);
         advance(ahead);
       }
@@ -670,13 +674,15 @@ scan_bwd_kernel(const ScanArgs s) {
       w.group += gridDim.x;
     }
   };
+  // (the maps from the first tile on: the run finds the last ones in L2)
+  auto tile_of = [&](const Walk& w) { return PHASE == kMaps ? tiles - 1 - w.tile : w.tile; };
   Flags<kStages> flags{};
   if constexpr (FETCH) {
 #pragma unroll
     for (int i = 0; i < kStages; ++i) {
       Col a = column(i, 0), b = column(i, 1), c = column(i, IN - 1);
       if (more(ahead)) {
-        load(place(ahead.group), ahead.tile, a, b, c, flags.f[i]);
+        load(place(ahead.group), tile_of(ahead), a, b, c, flags.f[i]);
         advance(ahead);
       }
       fetch_commit();
@@ -687,18 +693,19 @@ scan_bwd_kernel(const ScanArgs s) {
   int stage = 0;
   while (more(at)) {
     const Place pl = place(at.group);
-    const int t0 = (at.tile * WT + wt) * L;
+    const int tile = tile_of(at);
+    const int t0 = (tile * WT + wt) * L;
     const int n = steps_in<L>(t0, s.T);
     const int64_t ostep = step_of(s, s.ldo);
     T* out = element<T>(s, s.out, s.ldo, t0, pl.n, pl.j);
     float hin[V], uin[V];   // the state entering this thread's steps, what reaches the last of them
     if constexpr (PHASE == kWhole) {
-      const float* from = s.carry + ((int64_t)at.tile * L * WT / PPO_SCAN_BLOCK) * s.C;
+      const float* from = s.carry + ((int64_t)tile * L * WT / PPO_SCAN_BLOCK) * s.C;
       if constexpr (WT == 1) {
 #pragma unroll
         for (int v = 0; v < V; ++v) {
           hin[v] = pl.ok ? __ldg(from + pl.c + v) : 0.f;
-          if (at.tile == tiles - 1) u[v] = pl.ok && s.dhT ? s.dhT[pl.c + v] : 0.f;
+          if (tile == tiles - 1) u[v] = pl.ok && s.dhT ? s.dhT[pl.c + v] : 0.f;
         }
       } else {
 #pragma unroll
@@ -707,11 +714,11 @@ scan_bwd_kernel(const ScanArgs s) {
           const unsigned c = (unsigned)at.group * CH + x;
           const bool in = x < CH && c < s.C;
           hj[k] = in ? __ldg(from + c) : 0.f;
-          if (at.tile == tiles - 1) {
+          if (tile == tiles - 1) {
             uj[k] = in && s.dhT ? s.dhT[c] : 0.f;
           } else if (s.split && in) {
             const Channel e = channel(s, c);
-            uj[k] = get_value<T>(element<T>(s, s.out, s.ldo, at.tile * (L * WT), e.n, e.j), ostep, 2);
+            uj[k] = get_value<T>(element<T>(s, s.out, s.ldo, tile * (L * WT), e.n, e.j), ostep, 2);
           }
         }
       }
@@ -723,7 +730,7 @@ scan_bwd_kernel(const ScanArgs s) {
       __syncwarp();
       flag = flags.get(stage);
     } else {
-      load(pl, at.tile, cz, rg, rh, flag);
+      load(pl, tile, cz, rg, rh, flag);
     }
     float z[L][V];
 #pragma unroll
@@ -782,9 +789,9 @@ scan_bwd_kernel(const ScanArgs s) {
             }
             const unsigned c = (unsigned)at.group * CH + x;
             // (a last tile too short for them is joined from its steps)
-            if (c < s.C && s.T - at.tile * (L * WT) >= value_rows<T>(1)) {
+            if (c < s.C && s.T - tile * (L * WT) >= value_rows<T>(1)) {
               const Channel e = channel(s, c);
-              T* row = element<T>(s, s.out, s.ldo, at.tile * (L * WT), e.n, e.j);
+              T* row = element<T>(s, s.out, s.ldo, tile * (L * WT), e.n, e.j);
               put_value<T>(row, ostep, 0, a);
               put_value<T>(row, ostep, 1, b);
             }
@@ -817,7 +824,7 @@ scan_bwd_kernel(const ScanArgs s) {
       __syncwarp();
       if (more(ahead)) {
         float f;
-        load(place(ahead.group), ahead.tile, cz, rg, rh, f);
+        load(place(ahead.group), tile_of(ahead), cz, rg, rh, f);
         flags.set(stage, f);
         advance(ahead);
       }
@@ -866,28 +873,35 @@ __global__ void __launch_bounds__(kJoinWarps* kWarp) scan_join_kernel(const Scan
       for (int i = 0; i < kRun; ++i)
         cut |= reset_flag(s, (m0 + warp * kRun + i + 1) * PPO_SCAN_BLOCK, n) != 0.f ? 1u << i : 0u;
     }
+    // all of a run's loads at once (off the end: the last map's, not used)
 #pragma unroll
     for (int i = 0; i < kRun; ++i) {
-      const int m = m0 + warp * kRun + i;
-      a[i] = 1.f;
-      b[i] = 0.f;
-      if (ok && m < maps) {
-        const int tile = BACK ? tiles - 1 - m : m, t0 = tile * PPO_SCAN_BLOCK;
-        if (BACK && s.T - t0 < need) {
-          // a last tile too short to hold its map: from its steps
-          for (int t = s.T - 1; t >= t0; --t) {
-            const float pz = (float)*element<const T>(s, s.p, s.ldp, t, n, j);
-            const float d = (float)*element<const T>(s, s.dh, s.lddh, t, n, j);
-            float z[1], q[1] = {pz};
-            sigmoid<1>(q, z);
-            const bool gone = reset_flag(s, t, n) != 0.f;
-            b[i] = gone ? 0.f : (1.f - z[0]) * (d + b[i]);
-            a[i] = gone ? -1.f : joined(a[i], 1.f - z[0]);
-          }
-        } else {
-          a[i] = get_value<T>(rows_of(tile), ostep, 0);
-          b[i] = get_value<T>(rows_of(tile), ostep, 1);
-        }
+      const int m = min(m0 + warp * kRun + i, maps - 1);
+      // (a last tile too short to hold its map: the one before it, not used)
+      const int tile = BACK ? tiles - 1 - m - (s.T - (tiles - 1 - m) * PPO_SCAN_BLOCK < need) : m;
+      T* row = rows_of(tile);
+      a[i] = get_value<T>(row, ostep, 0);
+      b[i] = get_value<T>(row, ostep, 1);
+    }
+#pragma unroll
+    for (int i = 0; i < kRun; ++i) {
+      if (!ok || m0 + warp * kRun + i >= maps) {
+        a[i] = 1.f;
+        b[i] = 0.f;
+      }
+    }
+    if (BACK && m0 + warp == 0 && ok && s.T - (tiles - 1) * PPO_SCAN_BLOCK < need) {
+      // the short last tile: from its steps
+      a[0] = 1.f;
+      b[0] = 0.f;
+      for (int t = s.T - 1; t >= (tiles - 1) * PPO_SCAN_BLOCK; --t) {
+        const float pz = (float)*element<const T>(s, s.p, s.ldp, t, n, j);
+        const float d = (float)*element<const T>(s, s.dh, s.lddh, t, n, j);
+        float z[1], q[1] = {pz};
+        sigmoid<1>(q, z);
+        const bool gone = reset_flag(s, t, n) != 0.f;
+        b[0] = gone ? 0.f : (1.f - z[0]) * (d + b[0]);
+        a[0] = gone ? -1.f : joined(a[0], 1.f - z[0]);
       }
     }
 #pragma unroll
