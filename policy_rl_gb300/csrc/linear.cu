@@ -51,39 +51,53 @@ __device__ __forceinline__ void put4(void* p, int64_t at, int n, bool vec, const
   }
 }
 
-// n (<= 4) output elements of row i from column j on, from their finished sums.
-// vec: pieces of four elements are aligned in every matrix.
+// What the epilogue of n (<= 4) output elements of row i from column j on reads;
+// vec: pieces of four elements are aligned in every matrix.  Read ahead of the
+// sums that it is applied to (nothing here comes from the product's kernel).
+struct Beside {
+  float bias[4], res[4], pre[4], out[4];
+};
 template <typename T>
-__device__ __forceinline__ void finish4(const Epilogue& e, float (&v)[4], int64_t i, int64_t j,
-                                        int n, bool vec) {
-  float x[4];
+__device__ __forceinline__ void beside4(const Epilogue& e, Beside& x, int64_t i, int64_t j, int n,
+                                        bool vec) {
+  if (e.mode == kWeight) {
+    if (e.accumulate) get4<float>(e.out, i * e.ldo + j, n, vec, x.out);
+    return;
+  }
+  if (e.mode == kForward) {
+    if (e.bias) get4<float>(e.bias, j, n, j % 4 == 0, x.bias);
+  } else if (e.act != PPO_ACT_NONE) {
+    get4<T>(e.pre, i * e.ldpre + j, n, vec, x.pre);
+  }
+  if (e.res) get4<T>(e.res, i * e.ldres + j, n, vec, x.res);
+}
+// The elements from their finished sums.
+template <typename T>
+__device__ __forceinline__ void finish4(const Epilogue& e, const Beside& x, float (&v)[4], int64_t i,
+                                        int64_t j, int n, bool vec) {
   if (e.mode == kWeight) {
     if (e.accumulate) {
-      get4<float>(e.out, i * e.ldo + j, n, vec, x);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) v[q] += x[q];
+      for (int q = 0; q < 4; ++q) v[q] += x.out[q];
     }
     put4<float>(e.out, i * e.ldo + j, n, vec, v);
     return;
   }
   if (e.mode == kForward) {
     if (e.bias) {
-      get4<float>(e.bias, j, n, j % 4 == 0, x);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) v[q] += x[q];
+      for (int q = 0; q < 4; ++q) v[q] += x.bias[q];
     }
     if (e.pre) put4<T>(e.pre, i * e.ldpre + j, n, vec, v);
 #pragma unroll
     for (int q = 0; q < 4; ++q) v[q] = act_value<false>(e.act, v[q]);
   } else if (e.act != PPO_ACT_NONE) {
-    get4<T>(e.pre, i * e.ldpre + j, n, vec, x);
 #pragma unroll
-    for (int q = 0; q < 4; ++q) v[q] *= act_slope<false>(e.act, x[q]);
+    for (int q = 0; q < 4; ++q) v[q] *= act_slope<false>(e.act, x.pre[q]);
   }
   if (e.res) {
-    get4<T>(e.res, i * e.ldres + j, n, vec, x);
 #pragma unroll
-    for (int q = 0; q < 4; ++q) v[q] += x[q];
+    for (int q = 0; q < 4; ++q) v[q] += x.res[q];
   }
   put4<T>(e.out, i * e.ldo + j, n, vec, v);
 }
@@ -91,45 +105,56 @@ __device__ __forceinline__ void finish4(const Epilogue& e, float (&v)[4], int64_
 // An fp32 product straight from its operands.  (The planes of an infinity, or of
 // what rounds to one in bf16, do not add up: their products hold NaN where the
 // product may not.)  NaN operands, whose sums are NaN from there on, stop early.
-__device__ __noinline__ float dot_again(const Product& g, int64_t i, int64_t j) {
-  const float* A = static_cast<const float*>(g.A) + i * g.sai;
-  const float* B = static_cast<const float*>(g.B) + j * g.sbj;
+__device__ __noinline__ float sum_again(const float* a, int64_t step, int64_t R) {
   float v = 0.f;
-  for (int64_t r = 0; r < g.R && v == v; ++r) v = fmaf(A[r * g.sar], B[r * g.sbr], v);
+  for (int64_t r = 0; r < R && v == v; ++r) v += a[r * step];
+  return v;
+}
+__device__ __noinline__ float dot_again(const float* a, int64_t sar, const float* b, int64_t sbr,
+                                        int64_t R) {
+  float v = 0.f;
+  for (int64_t r = 0; r < R && v == v; ++r) v = fmaf(a[r * sar], b[r * sbr], v);
   return v;
 }
 
 // out = epilogue of the sum of the partial products, in split order, four columns
-// a thread.  g: the fp32 operands of a product of planes (A nullptr: no planes).
+// a thread.  PLANES: of a product of planes, g its fp32 operands.
 constexpr int kFinishThreads = 256;
-template <typename T>
-__global__ void __launch_bounds__(kFinishThreads)
+template <typename T, bool PLANES>
+__global__ void __launch_bounds__(kFinishThreads, 4)
 finish_kernel(const float* __restrict__ part, int splits, int64_t I, int64_t J, int64_t ldp,
               const Epilogue e, int vec, const Product g) {
-  pdl_wait();
   const int64_t n = I * ldp, per = ldp / 4, n4 = I * per;
+  bool waited = false;
   for (int64_t k = (int64_t)blockIdx.x * kFinishThreads + threadIdx.x; k < n4;
        k += (int64_t)gridDim.x * kFinishThreads) {
     // (a 64-bit division costs as much as the rest)
     const int64_t i = n4 < (1ll << 32) ? (int64_t)((uint32_t)k / (uint32_t)per) : k / per;
     const int64_t j = 4 * (k - i * per);
     const int cols = (int)min((int64_t)4, J - j);
+    Beside x;
+    if (cols > 0) beside4<T>(e, x, i, j, cols, vec);
+    if (!waited) pdl_wait();      // for the partial products
+    waited = true;
     float v[4] = {};
-#pragma unroll 8
+#pragma unroll 4
     for (int s = 0; s < splits; ++s) {
-      const float4 x = __ldcg(reinterpret_cast<const float4*>(part + s * n) + k);
-      v[0] += x.x;
-      v[1] += x.y;
-      v[2] += x.z;
-      v[3] += x.w;
+      const float4 t = __ldcg(reinterpret_cast<const float4*>(part + s * n) + k);
+      v[0] += t.x;
+      v[1] += t.y;
+      v[2] += t.z;
+      v[3] += t.w;
     }
-    if (g.A && !(isfinite(v[0]) && isfinite(v[1]) && isfinite(v[2]) && isfinite(v[3]))) {
+    if (PLANES && !(isfinite(v[0]) && isfinite(v[1]) && isfinite(v[2]) && isfinite(v[3]))) {
 #pragma unroll
       for (int q = 0; q < 4; ++q)
-        if (q < cols && !isfinite(v[q])) v[q] = dot_again(g, i, j + q);
+        if (q < cols && !isfinite(v[q]))
+          v[q] = dot_again(static_cast<const float*>(g.A) + i * g.sai, g.sar,
+                           static_cast<const float*>(g.B) + (j + q) * g.sbj, g.sbr, g.R);
     }
-    if (cols > 0) finish4<T>(e, v, i, j, cols, vec);
+    if (cols > 0) finish4<T>(e, x, v, i, j, cols, vec);
   }
+  if (!waited) pdl_wait();
 }
 
 // ---- a few rows ------------------------------------------------------------------------
@@ -154,6 +179,14 @@ few_rows_kernel(const Product g, const Epilogue e, int vec, int wk) {
   const int64_t j0 = ((int64_t)blockIdx.x * per + warp / wk) * CPW;
   const int64_t i0 = (int64_t)blockIdx.y * MR;
   const int rows = (int)min((int64_t)MR, g.I - i0);
+  // the output that this lane will hold, and whether it does
+  int mine = 0;
+#pragma unroll
+  for (int n = A, off = 16; n > 1; n >>= 1, off >>= 1) mine += lane & off ? n / 2 : 0;
+  const int64_t j = j0 + mine % CPW;
+  const bool holds = (lane & (kWarp / A - 1)) == 0 && mine / CPW < rows && j < g.J && warp % wk == 0;
+  Beside beside;
+  if (holds) beside4<T>(e, beside, i0 + mine / CPW, j, 1, false);
   // rows and columns past the last one repeat it, so that no load is conditional
   const T *x[MR], *w[CPW];
 #pragma unroll
@@ -216,7 +249,6 @@ few_rows_kernel(const Product g, const Epilogue e, int vec, int wk) {
   }
   // lanes fold their sums: each keeps half of them and takes the other lane's
   // share, until one is left
-  int mine = 0;
 #pragma unroll
   for (int n = A, off = 16; off >= 1; off >>= 1) {
     if (n > 1) {
@@ -227,22 +259,20 @@ few_rows_kernel(const Product g, const Epilogue e, int vec, int wk) {
         const float give = up ? acc[i] : acc[i + n], keep = up ? acc[i + n] : acc[i];
         acc[i] = keep + __shfl_xor_sync(0xffffffffu, give, off);
       }
-      mine += up ? n : 0;
     } else {
       acc[0] += __shfl_xor_sync(0xffffffffu, acc[0], off);
     }
   }
-  const bool holds = (lane & (kWarp / A - 1)) == 0;
   float v[4] = {acc[0], 0.f, 0.f, 0.f};
   if (wk > 1) {
-    if (holds) sums[warp][mine] = acc[0];
+    if ((lane & (kWarp / A - 1)) == 0) sums[warp][mine] = acc[0];
     __syncthreads();
-    if (warp % wk != 0) return;
-    v[0] = 0.f;
-    for (int i = 0; i < wk; ++i) v[0] += sums[warp + i][mine];
+    if (holds) {
+      v[0] = 0.f;
+      for (int i = 0; i < wk; ++i) v[0] += sums[warp + i][mine];
+    }
   }
-  const int64_t j = j0 + mine % CPW;
-  if (holds && mine / CPW < rows && j < g.J) finish4<T>(e, v, i0 + mine / CPW, j, 1, false);
+  if (holds) finish4<T>(e, beside, v, i0 + mine / CPW, j, 1, false);
 }
 
 // Whether a forward product takes few_rows_kernel, by how often it reads W's
@@ -341,8 +371,11 @@ simt_kernel(const Product g, const Epilogue e, int vec, float* __restrict__ part
     if (part)
       *reinterpret_cast<float4*>(part + (blockIdx.z * g.I + oi) * ldp + oj) =
           make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
-    else
-      finish4<float>(e, acc[i], oi, oj, (int)min((int64_t)4, g.J - oj), vec);
+    else {
+      Beside x;
+      beside4<float>(e, x, oi, oj, (int)min((int64_t)4, g.J - oj), vec);
+      finish4<float>(e, x, acc[i], oi, oj, (int)min((int64_t)4, g.J - oj), vec);
+    }
   }
 }
 
@@ -397,11 +430,11 @@ int fours(const Epilogue& e) {
   return e.ldo % 4 == 0 && (!e.res || e.ldres % 4 == 0) && (!e.pre || e.ldpre % 4 == 0);
 }
 
-template <typename T>
+template <typename T, bool PLANES = false>
 cudaError_t launch_finish(const float* part, int64_t splits, int64_t I, int64_t J, int64_t ldp,
                           const Epilogue& e, cudaStream_t st, const Product& g = {}) {
   const int64_t blocks = std::min<int64_t>(cdiv(I * ldp / 4, kFinishThreads), 16 * kSms);
-  return launch_pdl(finish_kernel<T>, dim3((unsigned)blocks), dim3(kFinishThreads), 0, st, part,
+  return launch_pdl(finish_kernel<T, PLANES>, dim3((unsigned)blocks), dim3(kFinishThreads), 0, st, part,
                     (int)splits, I, J, ldp, e, fours(e), g);
 }
 
@@ -511,11 +544,13 @@ size_t tc_part_bytes(int64_t I, int64_t J, int64_t R, bool must_split, int terms
 }
 
 // dW from its partial products, four columns a thread, and db from the partial
-// column sums (the blocks after the first `wblocks`), all in a fixed order
+// column sums (the blocks after the first `wblocks`), all in a fixed order.
+// PLANES: of a product of planes, g its fp32 operands.
+template <bool PLANES>
 __global__ void __launch_bounds__(kFinishThreads)
 finish_weight_kernel(const float* __restrict__ part, int splits, int64_t I, int64_t J, int64_t ldp,
                      float* __restrict__ dw, const float* __restrict__ sums, int64_t sum_rows,
-                     float* __restrict__ db, int accumulate, int wblocks) {
+                     float* __restrict__ db, int accumulate, int wblocks, const Product g) {
   pdl_wait();
   if ((int)blockIdx.x < wblocks) {
     const int64_t n4 = I * ldp / 4, n = I * ldp;
@@ -532,9 +567,16 @@ finish_weight_kernel(const float* __restrict__ part, int splits, int64_t I, int6
       }
       const int64_t i = 4 * k / ldp, j = 4 * k - i * ldp;
       float* o = dw + i * J + j;
-      const float vv[4] = {v.x, v.y, v.z, v.w};
+      float vv[4] = {v.x, v.y, v.z, v.w};
+      if (PLANES && !(isfinite(v.x) && isfinite(v.y) && isfinite(v.z) && isfinite(v.w))) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (j + q < J && !isfinite(vv[q]))
+            vv[q] = dot_again(static_cast<const float*>(g.A) + i * g.sai, g.sar,
+                              static_cast<const float*>(g.B) + (j + q) * g.sbj, g.sbr, g.R);
+      }
       if (J % 4 == 0 && !accumulate) {
-        *reinterpret_cast<float4*>(o) = v;
+        *reinterpret_cast<float4*>(o) = make_float4(vv[0], vv[1], vv[2], vv[3]);
       } else {
 #pragma unroll
         for (int q = 0; q < 4; ++q)
@@ -557,8 +599,25 @@ finish_weight_kernel(const float* __restrict__ part, int splits, int64_t I, int6
     float v = 0.f;
 #pragma unroll
     for (int q = 0; q < kFinishThreads / kWarp; ++q) v += part_sum[q][lane];
+    if (PLANES && !isfinite(v)) v = sum_again(static_cast<const float*>(g.A) + c * g.sai, g.sar, g.R);
     db[c] = accumulate ? db[c] + v : v;
   }
+}
+
+// (part nullptr: dW is there already)
+template <bool PLANES>
+cudaError_t launch_finish_weight(const float* part, int splits, const Product& g, const Epilogue& e,
+                                 const float* sums, int64_t sum_rows, float* db, cudaStream_t st) {
+  const int64_t ldp = part_pitch(g.J);
+  const int wb = part ? (int)std::min<int64_t>(cdiv(g.I * ldp / 4, kFinishThreads), 8 * kSms) : 0;
+  const int sb = db ? (int)cdiv(g.I, kWarp) : 0;
+  return launch_pdl(finish_weight_kernel<PLANES>, dim3((unsigned)(wb + sb)), dim3(kFinishThreads), 0, st,
+                    part, splits, g.I, g.J, ldp, static_cast<float*>(e.out), sums, sum_rows, db,
+                    e.accumulate, wb, g);
+}
+size_t sum_bytes(int64_t I, int64_t J, int64_t R, const TcPlan& plan) {
+  const Product g{nullptr, 0, 0, nullptr, 0, 0, I, J, R};
+  return (size_t)(tc_sum_rows(g, plan) * I * 4 + 255) / 256 * 256;
 }
 
 cudaError_t tc_run(const Product& g, const Epilogue& e, char* work, int* err, cudaStream_t st) {
@@ -571,7 +630,8 @@ cudaError_t tc_run(const Product& g, const Epilogue& e, char* work, int* err, cu
 
 // out = epilogue of an fp32 product, by planes.  A lies as rows of `ca`
 // elements (its own row or the sum's index), so does B.
-cudaError_t planes_run(const Product& g, const Epilogue& e, char* work, int* err, cudaStream_t st) {
+cudaError_t planes_run(const Product& g, const Epilogue& e, float* db, char* work, int* err,
+                       cudaStream_t st) {
   const bool amn = g.sai == 1 && e.mode == kWeight, bmn = e.mode != kForward;
   Product t = g;
   auto split = [&](const void*& a, int64_t ld, int64_t rows, int64_t cols, int64_t& pitch) {
@@ -590,29 +650,26 @@ cudaError_t planes_run(const Product& g, const Epilogue& e, char* work, int* err
     x = bmn ? split(t.B, g.sbr, g.R, g.J, t.sbr) : split(t.B, g.sbj, g.J, g.R, t.sbj);
   if (x != cudaSuccess) return x;
   const TcPlan plan = tc_plan(g.I, g.J, g.R, true, kTerms);
-  x = tc_product(t, e, plan, reinterpret_cast<float*>(work), nullptr, err, num_sms(), st,
-                 plane_rows(amn ? g.R : g.I), plane_rows(bmn ? g.R : g.J));
+  float* sums = db ? reinterpret_cast<float*>(work) : nullptr;
+  if (db) work += sum_bytes(g.I, g.J, g.R, plan);
+  float* part = reinterpret_cast<float*>(work);
+  x = tc_product(t, e, plan, part, sums, err, num_sms(), st, plane_rows(amn ? g.R : g.I),
+                 plane_rows(bmn ? g.R : g.J));
   if (x != cudaSuccess) return x;
-  return launch_finish<float>(reinterpret_cast<float*>(work), plan.splits, g.I, g.J,
-                              part_pitch(g.J), e, st, g);
+  if (e.mode == kWeight)
+    return launch_finish_weight<true>(part, plan.splits, g, e, sums, tc_sum_rows(g, plan), db, st);
+  return launch_finish<float, true>(part, plan.splits, g.I, g.J, part_pitch(g.J), e, st, g);
 }
 size_t planes_need(int64_t ra, int64_t ca, int64_t rb, int64_t cb, int64_t I, int64_t J, int64_t R) {
-  return planes_bytes(ra, ca) + planes_bytes(rb, cb) + 512 + tc_part_bytes(I, J, R, true, kTerms);
-}
-// The fp32 product on the units that suit its size.
-cudaError_t run_f32(const Product& g, const Epilogue& e, int64_t M, int64_t N, int64_t K, void* work,
-                    float* part, cudaStream_t st) {
-  if (takes_planes(M, N, K))
-    return planes_run(g, e, reinterpret_cast<char*>(part), static_cast<int*>(work), st);
-  return simt_product(g, e, part, st);
+  return planes_bytes(ra, ca) + planes_bytes(rb, cb) + 512 + tc_part_bytes(I, J, R, true, kTerms) +
+         sum_bytes(I, J, R, tc_plan(I, J, R, true, kTerms));
 }
 
 // A gradient that is added to, or whose rows TMA cannot store, is finished from
 // partial products even where the sum is not split.
 bool must_finish(int64_t J, int accumulate) { return accumulate || J % 4; }
 size_t tc_sum_bytes(int64_t N, int64_t K, int64_t M, bool must) {
-  const Product g{nullptr, 0, 0, nullptr, 0, 0, N, K, M};
-  return (size_t)(tc_sum_rows(g, tc_plan(N, K, M, must)) * N * 4 + 255) / 256 * 256;
+  return sum_bytes(N, K, M, tc_plan(N, K, M, must));
 }
 cudaError_t tc_run_weight(const Product& g, const Epilogue& e, float* db, char* work, int* err,
                           cudaStream_t st) {
@@ -625,12 +682,7 @@ cudaError_t tc_run_weight(const Product& g, const Epilogue& e, float* db, char* 
                     : nullptr;
   const cudaError_t x = tc_product(g, e, plan, part, sums, err, num_sms(), st);
   if (x != cudaSuccess || (!part && !db)) return x;
-  const int64_t ldp = part_pitch(g.J);
-  const int wb = part ? (int)std::min<int64_t>(cdiv(g.I * ldp / 4, kFinishThreads), 8 * kSms) : 0;
-  const int sb = db ? (int)cdiv(g.I, kWarp) : 0;
-  return launch_pdl(finish_weight_kernel, dim3((unsigned)(wb + sb)), dim3(kFinishThreads), 0, st,
-                    (const float*)part, plan.splits, g.I, g.J, ldp, static_cast<float*>(e.out),
-                    (const float*)sums, rows, db, e.accumulate, wb);
+  return launch_finish_weight<false>(part, plan.splits, g, e, sums, rows, db, st);
 }
 
 cudaError_t column_sums(const float* dz, int64_t ld, int64_t M, int64_t N, float* db,
@@ -646,6 +698,16 @@ cudaError_t column_sums(const float* dz, int64_t ld, int64_t M, int64_t N, float
   e.ldo = N;
   e.accumulate = accumulate;
   return launch_finish<float>(part, used, 1, N, part_pitch(N), e, st);
+}
+
+// The fp32 product on the units that suit its size (db: kWeight alone, nullable).
+cudaError_t run_f32(const Product& g, const Epilogue& e, int64_t M, int64_t N, int64_t K, float* db,
+                    void* work, float* part, cudaStream_t st) {
+  if (takes_planes(M, N, K))
+    return planes_run(g, e, db, reinterpret_cast<char*>(part), static_cast<int*>(work), st);
+  const cudaError_t x = simt_product(g, e, part, st);
+  if (x != cudaSuccess || !db) return x;
+  return column_sums(static_cast<const float*>(g.A), g.sar, M, N, db, e.accumulate, part, st);
 }
 
 bool sizes_ok(int64_t M, int64_t N, int64_t K) {
@@ -741,7 +803,7 @@ ppo_status ppo_linear_forward(int32_t dtype, const void* x, int64_t ldx, const v
   const lin::Product g{x, ldx, 1, w, ldw, 1, M, N, K};
   if (dtype == PPO_DTYPE_F32)
     return status_of(lin::takes_few_rows<float>(g) ? lin::few_rows<float>(g, e, st)
-                                                   : lin::run_f32(g, e, M, N, K, work, parts(work), st));
+                                                   : lin::run_f32(g, e, M, N, K, nullptr, work, parts(work), st));
   if (lin::takes_few_rows<__nv_bfloat16>(g)) return status_of(lin::few_rows<__nv_bfloat16>(g, e, st));
   char* free = reinterpret_cast<char*>(parts(work));
   cudaError_t err = lin::on_16_bytes(x, ldx, M, K, free, st);
@@ -776,7 +838,7 @@ ppo_status ppo_linear_backward_data(int32_t dtype, const void* dz, int64_t lddz,
   e.ldo = lddx;
   if (dtype == PPO_DTYPE_F32)
     return status_of(
-        lin::run_f32({dz, lddz, 1, w, 1, ldw, M, K, N}, e, M, N, K, work, parts(work), st));
+        lin::run_f32({dz, lddz, 1, w, 1, ldw, M, K, N}, e, M, N, K, nullptr, work, parts(work), st));
   char* free = reinterpret_cast<char*>(parts(work));
   cudaError_t err = lin::on_16_bytes(dz, lddz, M, N, free, st);
   if (err == cudaSuccess) err = lin::on_16_bytes(w, ldw, N, K, free, st);
@@ -800,13 +862,9 @@ ppo_status ppo_linear_backward_weight(int32_t dtype, const void* dz, int64_t ldd
   e.out = dw;
   e.ldo = K;
   e.accumulate = accumulate != 0;
-  if (dtype == PPO_DTYPE_F32) {
-    cudaError_t err =
-        lin::run_f32({dz, 1, lddz, x, 1, ldx, N, K, M}, e, M, N, K, work, parts(work), st);
-    if (err == cudaSuccess && db)
-      err = lin::column_sums(static_cast<const float*>(dz), lddz, M, N, db, e.accumulate, parts(work), st);
-    return status_of(err);
-  }
+  if (dtype == PPO_DTYPE_F32)
+    return status_of(
+        lin::run_f32({dz, 1, lddz, x, 1, ldx, N, K, M}, e, M, N, K, db, work, parts(work), st));
   char* free = reinterpret_cast<char*>(parts(work));
   cudaError_t err = lin::on_16_bytes(dz, lddz, M, N, free, st);
   if (err == cudaSuccess) err = lin::on_16_bytes(x, ldx, M, K, free, st);

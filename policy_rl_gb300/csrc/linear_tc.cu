@@ -524,10 +524,11 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
         int ti, tj, kt0, kt1, split;
         unit_of(u, ti, tj, kt0, kt1, split);
         float sum[8] = {};
-        int turn = kt0 % p.tiles_j;
+        const int terms = p.plane_a ? kTerms : 1;
+        int turn = kt0 / terms % p.tiles_j, term = 0;
         for (int kt = kt0; kt < kt1; ++kt) {
           if (!wait_bar(empty(s), ph, g)) { ok = false; break; }
-          if (turn == tj) {
+          if (turn == tj && term < 3) {      // (the first three terms meet each plane of A once)
             const uint8_t* blk = gbase + (size_t)s * C::STAGE + (warp - 2) * 8192;
             float t[8] = {};
 #pragma unroll
@@ -546,7 +547,10 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
 #pragma unroll
             for (int i = 0; i < 8; ++i) sum[i] += t[i];
           }
-          if (++turn == p.tiles_j) turn = 0;
+          if (++term == terms) {
+            term = 0;
+            if (++turn == p.tiles_j) turn = 0;
+          }
           __syncwarp();
           if (lane == 0) mbar_arrive(summed(s));
           if (++s == S) { s = 0; ph ^= 1; }

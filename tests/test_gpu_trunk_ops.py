@@ -550,6 +550,27 @@ def test_linear_f32_infinities_nan_and_what_rounds_to_infinity(P):
     assert Y[31, 0] == np.inf
 
 
+def test_linear_f32_weight_gradient_with_infinities_and_nan(P):
+    import torch
+    rng = np.random.default_rng(16)
+    M, N, K = 700, 640, 640
+    dz, x = dev(rng.normal(size=(M, N))), dev(rng.normal(size=(M, K)))
+    dz[3, 5] = float("inf")
+    dz[4, 6] = float("nan")
+    dz[5, 7], x[5] = 3.4e38, x[5].clamp(-0.5, 0.5)
+    dw, db = out((N, K)), out((N,))
+    work = torch.zeros(P.ppo_linear_workspace_bytes(M, N, K, x.dtype), dtype=torch.uint8, device="cuda")
+    P.ppo_linear_backward_weight(dz, x, dw, db=db, work=work)
+    P.ppo_work_status(work)
+    Z, X, W, B = f64(dz), f64(x), f64(dw), f64(db)
+    rest = np.setdiff1d(np.arange(N), [5, 6])
+    bound = prod_bound("f32", Z[:, rest].T, X, M)
+    assert (np.abs(W[rest] - Z[:, rest].T @ X) <= bound).all()
+    assert (np.abs(B[rest] - Z[:, rest].sum(0)) <= 8 * U32 * (np.sqrt(M) + 8) * np.abs(Z[:, rest]).sum(0)).all()
+    assert (W[5] == np.sign(X[3]) * np.inf).all() and B[5] == np.inf
+    assert np.isnan(W[6]).all() and np.isnan(B[6])
+
+
 def test_linear_past_32_bit_offsets(P):
     import torch
     M, N, K = 1100000, 2048, 64             # 2.3e9 outputs
