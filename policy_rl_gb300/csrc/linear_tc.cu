@@ -14,18 +14,27 @@
 // meanwhile: bias, pre-activation, activation, residual, rounding.  An epilogue
 // warp owns a box of 32 rows x 64 columns of the tile: the residual or pre_in
 // box comes by TMA while the MMAs run, is overwritten by the result, and leaves
-// by TMA.  In the weight gradient warps 2 and 3 add up the columns of dz from
-// the stages that the MMAs have read, so that db costs no pass of its own.
+// by TMA.  A residual beside pre or pre_in has a box of 16 rows more, for which
+// the ring gives up a stage.  In the weight gradient warps 2 and 3 add up the
+// columns of dz from the stages that the MMAs have read, so that db costs no
+// pass of its own.
 //
 // What bounds it: an SM takes in 47 bytes of operands a clock by TMA (measured
 // with and without an epilogue, for long and short sums alike; the full MMA rate
-// would want 64), and the epilogue's boxes share that path and shared memory.
-// 8,192 x 8,192 x 8,192 runs at 1.76 PFLOP/s, 32,768 x 512 -> 2,048 forward in
-// 60 us (41 without an epilogue), with gelu and pre in 83.  Measured and left:
-// stores by the warps themselves, straight from rows in registers (78 us) or
-// through shared memory in whole lines (69); the accumulator held in 64
-// registers so that TMEM is free at once (72: spills); L2 prefetches of the
-// operands by TMA (67: they take the same unit's time).
+// would want 64): 0.35 us per 64-deep step of a 256 x 256 tile, 1.76 PFLOP/s at
+// 8,192 x 8,192 x 8,192.  Beside that the epilogue of a tile takes about 2.7 us,
+// 4 with an input box, 5 with gelu' of it, nearly all of it instructions of 16
+// warps in step: with sums of 512 (8 steps) it is the longer part.  32,768 x 512
+// -> 2,048 forward 55 us, with gelu and pre 84 (268 MB written), with a residual
+// too 109; 65,536 x 512 -> 2,048 data gradient 99 us, with gelu' 157.
+// Measured and left, on the last figure or the plain forward's 55 us: a set of
+// eight warps for each accumulator (153; plain 60), inputs fetched 16 rows at a
+// time (+10) or half a unit earlier from a third box (+8: a stage less), inputs
+// by cp.async (+4), one reciprocal for two (+3; none of the four special-function
+// operations of a pair: -8), a fence and store for every 16 rows (plain 62),
+// divisions for each unit's place (plain 58, gelu' 165), stores by the warps
+// themselves (plain 69 and more), the accumulator held in 64 registers so that
+// TMEM is free at once (spills), L2 prefetches of the operands by TMA (67).
 //
 // Why pairs: at the full MMA rate a CTA with a 128 x 256 tile would have to
 // take in 48 KB of operands every 512 clocks, more than an SM receives (about
@@ -64,7 +73,9 @@ constexpr int kBox = 4096;             // 32 rows x 128 bytes, 128-byte swizzle
 // (Measured at 32,768 rows: error 1.9e-7 and 108 us with windows of 2 steps,
 // 4.8e-7 and 60 us with 8, 4.4e-6 and 58 us with 64.)
 constexpr int kWindow = 8;
-template <int CG, int BN, int MODE>
+// LATE: a residual beside another box of input or output; its boxes, of 16
+// rows, take the room of a stage
+template <int CG, int BN, int MODE, bool LATE>
 struct TileCfg {
   static constexpr int A_BYTES = BM * BK * 2;
   static constexpr int B_ROWS = BN / CG;
@@ -73,10 +84,10 @@ struct TileCfg {
   // the weight gradient stages no results: its boxes' room goes to the ring
   // (weight and bias gradient of 32,768 x 512 -> 2,048: 68 us with 5 stages, 60
   // with 7)
-  static constexpr int S = MODE == kWeight ? 7 : 5;
+  static constexpr int S = MODE == kWeight ? 7 : LATE ? 4 : 5;
   static constexpr int EW = 4 * (BN / 64);   // epilogue warps: 32 rows x 64 columns each
   static constexpr int THREADS = (kFirstEpi + EW) * kWarp;
-  static constexpr int BOXES = MODE == kWeight ? 0 : EW * kBox;
+  static constexpr int BOXES = MODE == kWeight ? 0 : EW * kBox + (LATE ? EW * kBox / 2 : 0);
   static constexpr int TMEM = 2 * BN;
   static constexpr int CTRL = 512;
   static constexpr size_t SMEM = 1024 + (size_t)S * STAGE + BOXES + CTRL;
@@ -93,7 +104,7 @@ struct TcArgs {
   float* part;                   // [splits][I][ldp] partial products (nullable)
   int64_t ldp;
   int in;                        // matrix read a unit ahead: 0 none, 1 the residual, 2 pre_in
-  int res_late;                  // the residual is read when it is added
+  int tma_late;                  // the residual beside another box (LATE) moves by TMA
   int wide_out;                  // fp32 rows start on 32-byte boundaries
   int tma_in, tma_out, tma_pre;  // it (the result, pre) moves by TMA
   float* db_part;                // [splits * tiles_j][I] column sums of A (nullable)
@@ -186,9 +197,10 @@ __device__ __forceinline__ uint8_t* box_piece(uint8_t* box, int r, int c) {
 // takes the 16-byte piece l % 8 of rows l / 8, l / 8 + 4, .., element by element.
 // (Not inlined: rare, and the code would only be in the way.)
 __device__ __noinline__ void box_load_slow(uint8_t* box, int lane, const void* base, int64_t ld,
-                                           int64_t row0, int64_t col0, int64_t I, int64_t J) {
+                                           int64_t row0, int64_t col0, int64_t I, int64_t J,
+                                           int rows) {
   const int64_t col = col0 + (lane & 7) * 8;
-  for (int r = lane >> 3; r < 32; r += 4) {
+  for (int r = lane >> 3; r < rows; r += 4) {
     uint32_t w[4] = {0, 0, 0, 0};
     const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(base) + (row0 + r) * ld + col;
     for (int i = 0; i < 8; ++i)
@@ -197,12 +209,12 @@ __device__ __noinline__ void box_load_slow(uint8_t* box, int lane, const void* b
     *reinterpret_cast<uint4*>(box_piece(box, r, lane & 7)) = make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
-// half a box: 16 rows
-__device__ __noinline__ void box_store_slow(uint8_t* half, int lane, void* base, int64_t ld,
-                                            int64_t row0, int64_t col0, int64_t I, int64_t J) {
+__device__ __noinline__ void box_store_slow(uint8_t* box, int lane, void* base, int64_t ld,
+                                            int64_t row0, int64_t col0, int64_t I, int64_t J,
+                                            int rows) {
   const int64_t col = col0 + (lane & 7) * 8;
-  for (int r = lane >> 3; r < 16; r += 4) {
-    const uint4 v = *reinterpret_cast<const uint4*>(box_piece(half, r, lane & 7));
+  for (int r = lane >> 3; r < rows; r += 4) {
+    const uint4 v = *reinterpret_cast<const uint4*>(box_piece(box, r, lane & 7));
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
     __nv_bfloat16* p = static_cast<__nv_bfloat16*>(base) + (row0 + r) * ld + col;
     for (int i = 0; i < 8; ++i)
@@ -210,11 +222,6 @@ __device__ __noinline__ void box_store_slow(uint8_t* half, int lane, void* base,
         p[i] = __ushort_as_bfloat16((uint16_t)(w[i >> 1] >> (16 * (i & 1))));
   }
 }
-// two consecutive elements of a row, or what there is of them
-__device__ __noinline__ float2 load_pair_slow(const __nv_bfloat16* p, int n) {
-  return make_float2(n > 0 ? (float)p[0] : 0.f, n > 1 ? (float)p[1] : 0.f);
-}
-
 // 16 TMEM lanes x 64 fp32 columns: thread t gets, of every group i of 8 columns,
 // columns 2 (t % 4) and + 1 of rows t / 4 (r[4 i], r[4 i + 1]) and t / 4 + 8
 // (r[4 i + 2], r[4 i + 3]) -- the layout of 8 x 8 matrices of stmatrix, and one
@@ -354,12 +361,12 @@ __device__ __forceinline__ void regs_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-template <int CG, int BN, int MODE, bool AMN, bool BMN>
-__global__ void __launch_bounds__(TileCfg<CG, BN, MODE>::THREADS, 1)
+template <int CG, int BN, int MODE, bool AMN, bool BMN, bool LATE>
+__global__ void __launch_bounds__(TileCfg<CG, BN, MODE, LATE>::THREADS, 1)
 lin_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
               const __grid_constant__ CUtensorMap tmO, const __grid_constant__ CUtensorMap tmP,
               const __grid_constant__ CUtensorMap tmI, const TcArgs p) {
-  using C = TileCfg<CG, BN, MODE>;
+  using C = TileCfg<CG, BN, MODE, LATE>;
   constexpr int S = C::S;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
@@ -367,7 +374,7 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
   uint8_t* gbase = smem_raw + (base - raw);
   uint8_t* boxes = gbase + (size_t)S * C::STAGE;
   uint8_t* ctrl = boxes + C::BOXES;
-  // full[S] empty[S] tfull[2] tempty[2] drain summed[S] box[EW]
+  // full[S] empty[S] tfull[2] tempty[2] drain summed[S] box[EW] late[EW]
   uint64_t* bars = reinterpret_cast<uint64_t*>(ctrl);
   auto full = [&](int s) { return smem_u32(&bars[s]); };
   auto empty = [&](int s) { return smem_u32(&bars[S + s]); };
@@ -376,7 +383,8 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
   const uint32_t drain = smem_u32(&bars[2 * S + 4]);
   auto summed = [&](int i) { return smem_u32(&bars[2 * S + 5 + i]); };
   auto box_bar = [&](int w) { return smem_u32(&bars[3 * S + 5 + w]); };
-  constexpr int kBars = 3 * S + 5 + C::EW;
+  auto late_bar = [&](int w) { return smem_u32(&bars[3 * S + 5 + C::EW + w]); };
+  constexpr int kBars = 3 * S + 5 + 2 * C::EW;
   static_assert(kBars * 8 + 16 <= C::CTRL, "control block");
   uint32_t* tslot = reinterpret_cast<uint32_t*>(&bars[kBars]);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
@@ -395,7 +403,7 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
     }
     mbar_init(drain, 1);
     for (int s = 0; s < S; ++s) mbar_init(summed(s), 2);
-    for (int w = 0; w < C::EW; ++w) mbar_init(box_bar(w), 1);
+    for (int w = 0; w < 2 * C::EW; ++w) mbar_init(box_bar(w), 1);
     *abort_flag = 0;
     cnt[0] = cnt[1] = 0;
     fence_mbar_init();
@@ -576,7 +584,7 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
     constexpr int PART = 64;                      // columns of an epilogue warp
     uint8_t* box = boxes + we * kBox;
     uint32_t n = 0;      // accumulators read
-    uint32_t boxes_in = 0;
+    uint32_t boxes_in = 0, late_in = 0;
     // one window: TMEM columns of this warp, or false when a wait gave up
     auto window = [&](uint32_t& taddr) {
       const int acc = n & 1;
@@ -596,40 +604,13 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
       }
       ++n;
     };
-    // the input box of unit u (lane 0; nothing where the box is off the matrix)
-    auto send = [&](int u) {
-      if (u >= p.units) return;
-      int ti, tj, kt0, kt1, split;
-      unit_of(u, ti, tj, kt0, kt1, split);
-      const int64_t r0 = (int64_t)(ti * CG + (int)rank) * BM + q * 32;
-      const int64_t c0 = (int64_t)tj * BN + part * PART;
-      if (r0 >= p.I || c0 >= p.J) return;
-      mbar_arrive_expect_tx(box_bar(we), kBox);
-      tma_load_2d(smem_u32(box), &tmI, (int)c0, (int)r0, box_bar(we));
-    };
-    // this thread's row of unit u's box (nullptr off the matrix)
-    auto ahead = [&](int u) -> const void* {
-      if (u >= p.units) return nullptr;
-      int ti, tj, kt0, kt1, split;
-      unit_of(u, ti, tj, kt0, kt1, split);
-      const int64_t r = (int64_t)(ti * CG + (int)rank) * BM + q * 32 + lane;
-      const int64_t c = (int64_t)tj * BN + part * PART;
-      if (r >= p.I || c >= p.J) return nullptr;
-      return static_cast<const __nv_bfloat16*>(p.in == 1 ? p.e.res : p.e.pre) +
-             r * (p.in == 1 ? p.e.ldres : p.e.ldpre) + c;
-    };
-    if (MODE != kWeight && p.tma_in) {
-      if (lane == 0) send(group);
-      if (const void* f = ahead(group + groups)) prefetch_l2(f);
-    }
-    for (int u = group; u < p.units; u += groups) {
-      int ti, tj, kt0, kt1, split;
-      unit_of(u, ti, tj, kt0, kt1, split);
-      const int64_t row0 = (int64_t)(ti * CG + (int)rank) * BM + q * 32, row = row0 + lane;
-      const bool any = row0 < p.I;
-      const int64_t col0 = (int64_t)tj * BN + part * PART;
-      uint32_t taddr;
-      if constexpr (MODE == kWeight) {
+    if constexpr (MODE == kWeight) {
+      for (int u = group; u < p.units; u += groups) {
+        int ti, tj, kt0, kt1, split;
+        unit_of(u, ti, tj, kt0, kt1, split);
+        const int64_t row = (int64_t)(ti * CG + (int)rank) * BM + q * 32 + lane;
+        const int64_t col0 = (int64_t)tj * BN + part * PART;
+        uint32_t taddr;
         // the windows' sums are added here, in fp32 with rounding to nearest
         float v[PART / 32][32];
         bool ok = true;
@@ -673,63 +654,113 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
             }
           }
         }
-      } else {
+      }
+    } else {
+      const int I = (int)p.I, J = (int)p.J;
+      // the places (row, column) of this unit, the next and the one after, walked
+      // without the divisions of unit_of
+      struct Place {
+        int r, c;
+      };
+      const int first = group / p.tiles_j, step = groups / p.tiles_j;
+      const int dr = step * (CG * BM), dc = (groups - step * p.tiles_j) * BN, wrap = p.tiles_j * BN;
+      Place at{(first * CG + (int)rank) * BM + q * 32, (group - first * p.tiles_j) * BN + part * PART};
+      auto after = [&](Place x) {
+        x.r += dr;
+        x.c += dc;
+        if (x.c >= wrap) {
+          x.c -= wrap;
+          x.r += CG * BM;
+        }
+        return x;
+      };
+      // the input box of a unit (lane 0; nothing where the box is off the matrix;
+      // rows of units past the last are)
+      auto send = [&](const Place& x) {
+        if (x.r >= I || x.c >= J) return;
+        mbar_arrive_expect_tx(box_bar(we), kBox);
+        tma_load_2d(smem_u32(box), &tmI, x.c, x.r, box_bar(we));
+      };
+      // and its residual's rows 16 h ..
+      uint8_t* late = boxes + C::EW * kBox + we * (kBox / 2);
+      const CUtensorMap* tmL = MODE == kForward ? &tmI : &tmP;      // (not used otherwise)
+      auto send_late = [&](const Place& x, int h) {
+        if (x.r + 16 * h >= I || x.c >= J) return;
+        mbar_arrive_expect_tx(late_bar(we), kBox / 2);
+        tma_load_2d(smem_u32(late), tmL, x.c, x.r + 16 * h, late_bar(we));
+      };
+      // this thread's row of a unit's box, towards L2
+      auto fetch = [&](const Place& x) {
+        if (x.r + lane >= I || x.c >= J) return;
+        const int64_t r = x.r + lane;
+        if (p.tma_in && p.in == 2) prefetch_l2(static_cast<const __nv_bfloat16*>(p.e.pre) + r * p.e.ldpre + x.c);
+        if (p.tma_in && p.in == 1 || LATE && p.tma_late)
+          prefetch_l2(static_cast<const __nv_bfloat16*>(p.e.res) + r * p.e.ldres + x.c);
+      };
+      Place soon = after(at), later = after(soon);
+      if (lane == 0 && p.tma_in) send(at);
+      if (LATE && lane == 0 && p.tma_late) send_late(at, 0);
+      if (p.in || LATE) fetch(soon);
+      for (int u = group; u < p.units; u += groups, at = soon, soon = later, later = after(later)) {
+        uint32_t taddr;
         if (!window(taddr)) break;
-        const bool there = any && col0 < p.J;
+        const int row0 = at.r, col0 = at.c;
+        const bool there = row0 < I && col0 < J;
+        bool ok = true;
         if (there && p.in) {
-          bool ok = true;
           if (p.tma_in) {
             ok = wait_bar(box_bar(we), boxes_in & 1, g);
             ++boxes_in;
-            // the rows of the box after the next, towards L2
-            if (const void* f = ahead(u + 2 * groups)) prefetch_l2(f);
           } else {
             if (lane == 0) bulk_wait_read0();
             __syncwarp();
             box_load_slow(box, lane, p.in == 1 ? p.e.res : p.e.pre,
-                          p.in == 1 ? p.e.ldres : p.e.ldpre, row0, col0, p.I, p.J);
+                          p.in == 1 ? p.e.ldres : p.e.ldpre, row0, col0, p.I, p.J, 32);
             __syncwarp();
           }
           if (!__all_sync(0xffffffffu, ok)) break;
         }
+        if (there && (p.in || LATE)) fetch(later);
         float2 bi[8];      // this thread's columns: c8 + 8 i, + 1
-        const int64_t c8 = col0 + 2 * (lane & 3);
+        const int c8 = col0 + 2 * (lane & 3);
         if constexpr (MODE == kForward) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             bi[i] = make_float2(0.f, 0.f);
             if (p.e.bias && there)
-              bi[i] = col0 + PART <= p.J
+              bi[i] = col0 + PART <= J
                           ? __ldg(reinterpret_cast<const float2*>(p.e.bias + c8 + 8 * i))
-                          : bias_slow(p.e.bias, c8 + 8 * i, p.J);
+                          : bias_slow(p.e.bias, c8 + 8 * i, J);
           }
         }
-        // a half of the box to where it belongs
-        auto leave = [&](uint8_t* half, const CUtensorMap* tm, bool tma, void* base, int64_t ld,
-                         int64_t r0) {
+        // `rows` rows of the box to where they belong (by TMA: after a fence)
+        auto leave = [&](uint8_t* from, const CUtensorMap* tm, bool tma, void* base, int64_t ld,
+                         int r0, int rows) {
           if (tma) {
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0 && r0 < p.I) tma_store_2d(tm, smem_u32(half), (int)col0, (int)r0);
+            if (lane == 0 && r0 < I) tma_store_2d(tm, smem_u32(from), col0, r0);
           } else {
-            __syncwarp();
-            box_store_slow(half, lane, base, ld, r0, col0, p.I, p.J);
+            box_store_slow(from, lane, base, ld, r0, col0, p.I, p.J, rows);
             __syncwarp();
           }
-          if (lane == 0) bulk_commit();
         };
-        // before a half is written: its last store has read it
-        auto vacate = [&]() {
-          if (lane == 0) bulk_wait_read1();
-          __syncwarp();
-        };
+        const bool two = MODE == kForward && p.e.pre;   // results: pre as well
 #pragma unroll 1
         for (int hr = 0; hr < 2; ++hr) {      // 16 rows at a time
           uint32_t r[32];
           tmem_ld_16x64(taddr + ((uint32_t)(16 * hr) << 16), r);
           if (hr == 1) release();
-          if (!there) continue;
-          const int64_t r0 = row0 + 16 * hr;
+          const int r0 = row0 + 16 * hr;
+          // the residual's box takes the next rows
+          auto late_next = [&]() {
+            if (LATE && p.tma_late && lane == 0) {
+              if (hr == 0) send_late(at, 1);
+              else send_late(soon, 0);
+            }
+          };
+          if (!there) {
+            late_next();
+            continue;
+          }
           float2 v[16];      // v[2 i + b]: column group i, row lane / 4 + 8 b
 #pragma unroll
           for (int k = 0; k < 16; ++k)
@@ -738,7 +769,9 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
 #pragma unroll
             for (int k = 0; k < 16; ++k) v[k] = ffma2(v[k], both(1.f), bi[k / 2]);
             if (p.e.pre) {
-              vacate();
+              // (halves: the last stores have read them)
+              if (lane == 0) bulk_wait_read0();
+              __syncwarp();
 #pragma unroll
               for (int i = 0; i < 8; i += 2) {
                 uint32_t w[4];
@@ -746,11 +779,10 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                 for (int j = 0; j < 4; ++j) w[j] = pack_bf16x2(v[2 * i + j].x, v[2 * i + j].y);
                 quad_put(box, lane, i, w);
               }
-              leave(box, &tmP, p.tma_pre, p.e.pre, p.e.ldpre, r0);
             }
             act_chunk(p.e.act, v);
           }
-          uint8_t* half = p.e.pre && MODE == kForward ? box + 2048 : box + 2048 * hr;
+          uint8_t* half = two ? box + 2048 : box + 2048 * hr;
           if (p.in) {
             uint32_t x[16];
 #pragma unroll
@@ -762,21 +794,32 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
               for (int k = 0; k < 16; ++k) v[k] = ffma2(v[k], both(1.f), unpack_bf16x2(x[k]));
             }
             __syncwarp();   // all have read the half
-          } else {
-            vacate();
+          } else if (hr == 0 && !two) {
+            if (lane == 0) bulk_wait_read0();
+            __syncwarp();
           }
-          if (p.res_late) {
-#pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              const int64_t rr = r0 + (lane >> 2) + 8 * (k & 1), cc = c8 + 8 * (k / 2);
-              const int left = rr < p.I ? (int)max((int64_t)0, min((int64_t)2, p.J - cc)) : 0;
-              const __nv_bfloat16* rp =
-                  static_cast<const __nv_bfloat16*>(p.e.res) + rr * p.e.ldres + cc;
-              const float2 x = left == 2 && (reinterpret_cast<uintptr_t>(rp) & 3u) == 0
-                                   ? unpack_bf16x2(*reinterpret_cast<const uint32_t*>(rp))
-                                   : load_pair_slow(rp, left);
-              v[k] = ffma2(v[k], both(1.f), x);
+          if constexpr (LATE) {
+            if (p.tma_late) {
+              if (r0 < I) {      // (rows off the matrix are not stored)
+                ok = __all_sync(0xffffffffu, wait_bar(late_bar(we), late_in & 1, g));
+                if (!ok) break;
+                ++late_in;
+              }
+            } else {
+              box_load_slow(late, lane, p.e.res, p.e.ldres, r0, col0, p.I, p.J, 16);
+              __syncwarp();
             }
+#pragma unroll
+            for (int i = 0; i < 8; i += 2) {
+              uint32_t x[4];
+              quad_get(late, lane, i, x);
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                v[2 * i + j] = ffma2(v[2 * i + j], both(1.f), unpack_bf16x2(x[j]));
+            }
+            fence_proxy_async_smem();      // (read by all lanes before it is written again)
+            __syncwarp();
+            late_next();
           }
 #pragma unroll
           for (int i = 0; i < 8; i += 2) {
@@ -785,17 +828,31 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
             for (int j = 0; j < 4; ++j) w[j] = pack_bf16x2(v[2 * i + j].x, v[2 * i + j].y);
             quad_put(half, lane, i, w);
           }
-          leave(half, &tmO, p.tma_out, p.e.out, p.e.ldo, r0);
+          if (two || hr == 1) {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (two) {
+              leave(box, &tmP, p.tma_pre, p.e.pre, p.e.ldpre, r0, 16);
+              leave(half, &tmO, p.tma_out, p.e.out, p.e.ldo, r0, 16);
+            } else {
+              leave(box, &tmO, p.tma_out, p.e.out, p.e.ldo, row0, 32);
+            }
+            if (lane == 0) bulk_commit();
+          }
         }
-        if (p.tma_in && lane == 0) {      // the box takes the next unit's input
+        if (!ok) break;
+        // the box takes the next unit's input
+        if (p.tma_in && lane == 0) {
           bulk_wait_read0();
-          send(u + groups);
+          send(soon);
         }
       }
     }
     // a box that was sent for but not used (after an abort)
     if (MODE != kWeight && p.tma_in && lane == 0 && *abort_flag)
       drain_wait(box_bar(we), boxes_in & 1, 1000000ull);
+    if (LATE && p.tma_late && lane == 0 && *abort_flag)
+      drain_wait(late_bar(we), late_in & 1, 1000000ull);
     if (lane == 0) bulk_wait0();   // this warp's stores are complete before the CTA exits
   }
 
@@ -836,9 +893,9 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
 // ---- launch --------------------------------------------------------------------
 // One launch with its tensor maps.  A K-major operand is read in boxes of
 // 64 (sum) x 128 rows, an MN-major one in boxes of 64 (own index) x 64.
-template <int CG, int BN, int MODE, bool AMN, bool BMN>
+template <int CG, int BN, int MODE, bool AMN, bool BMN, bool LATE = false>
 cudaError_t launch(const Product& g, TcArgs p, int sms, cudaStream_t st) {
-  using C = TileCfg<CG, BN, MODE>;
+  using C = TileCfg<CG, BN, MODE, LATE>;
   CUtensorMap ta, tb, to, tp, ti;
   cudaError_t e;
   const int64_t pa = 3 * p.plane_a, pb = 3 * p.plane_b;   // all rows of planes
@@ -852,7 +909,8 @@ cudaError_t launch(const Product& g, TcArgs p, int sms, cudaStream_t st) {
   tp = ta;
   ti = ta;
   if (MODE != kWeight && p.tma_out) {
-    e = tc_make_tmap(&to, p.e.out, p.J, p.I, p.e.ldo, 64, 16);
+    e = tc_make_tmap(&to, p.e.out, p.J, p.I, p.e.ldo, 64,
+                     MODE == kForward && p.e.pre ? 16 : 32);
     if (e != cudaSuccess) return e;
   }
   if (MODE != kWeight && p.tma_pre) {
@@ -864,7 +922,11 @@ cudaError_t launch(const Product& g, TcArgs p, int sms, cudaStream_t st) {
                   : tc_make_tmap(&ti, p.e.pre, p.J, p.I, p.e.ldpre, 64, 32);
     if (e != cudaSuccess) return e;
   }
-  const auto kernel = lin_tc_kernel<CG, BN, MODE, AMN, BMN>;
+  if (LATE && p.tma_late) {
+    e = tc_make_tmap(MODE == kForward ? &ti : &tp, p.e.res, p.J, p.I, p.e.ldres, 64, 16);
+    if (e != cudaSuccess) return e;
+  }
+  const auto kernel = lin_tc_kernel<CG, BN, MODE, AMN, BMN, LATE>;
   static thread_local int prepared = -1;   // the device whose shared-memory opt-in is made
   int dev = 0;
   e = cudaGetDevice(&dev);
@@ -899,8 +961,12 @@ cudaError_t launch_mode(const Product& g, const TcArgs& p, int mode, int sms, cu
     if (mode == kForward) return launch<CG, BN, kWeight, false, false>(g, p, sms, st);
     return launch<CG, BN, kWeight, false, true>(g, p, sms, st);
   }
-  if (mode == kForward) return launch<CG, BN, kForward, false, false>(g, p, sms, st);
-  return launch<CG, BN, kData, false, true>(g, p, sms, st);
+  const bool late = p.e.res && p.in != 1;
+  if (mode == kForward)
+    return late ? launch<CG, BN, kForward, false, false, true>(g, p, sms, st)
+                : launch<CG, BN, kForward, false, false>(g, p, sms, st);
+  return late ? launch<CG, BN, kData, false, true, true>(g, p, sms, st)
+              : launch<CG, BN, kData, false, true>(g, p, sms, st);
 }
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -970,7 +1036,7 @@ cudaError_t tc_product(const Product& g, const Epilogue& e, const TcPlan& plan, 
   if (!part && e.mode != kWeight) {
     p.in = e.mode == kData && e.act != PPO_ACT_NONE ? 2 : e.res && !e.pre ? 1 : 0;
     p.tma_in = p.in == 1 ? al(e.res, e.ldres, 8) : p.in == 2 && al(e.pre, e.ldpre, 8);
-    p.res_late = e.res && p.in != 1;
+    p.tma_late = e.res && p.in != 1 && al(e.res, e.ldres, 8);
   }
   p.db_part = db_part;
   const void* f32_out = part ? part : e.out;
