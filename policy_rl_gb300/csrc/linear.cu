@@ -468,14 +468,12 @@ constexpr int kPackThreads = 256;
 __global__ void __launch_bounds__(kPackThreads)
 pack_rows_kernel(const __nv_bfloat16* __restrict__ src, int64_t ld, int64_t rows, int64_t cols,
                  int64_t pitch, uint4* __restrict__ dst) {
-  const int64_t n = rows * (pitch / 8);
+  const int64_t per = pitch / 8, n = rows * per, total = (rows - 1) * ld + cols;
   for (int64_t k = (int64_t)blockIdx.x * kPackThreads + threadIdx.x; k < n;
        k += (int64_t)gridDim.x * kPackThreads) {
-    const int64_t r = k / (pitch / 8), c = (k - r * (pitch / 8)) * 8;
-    float f[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = c + i < cols ? (float)src[r * ld + c + i] : 0.f;
-    dst[k] = from_f32<__nv_bfloat16, 8>(f);
+    const int64_t r = n < (1ll << 32) ? (int64_t)((uint32_t)k / (uint32_t)per) : k / per;
+    const int64_t c = (k - r * per) * 8;
+    dst[k] = load8_any(src, r * ld + c, total, (int)min((int64_t)8, cols - c));
   }
 }
 // the operand itself, or its copy in the workspace (advanced past it)

@@ -64,6 +64,39 @@ __device__ __forceinline__ Raw<T, V> from_f32(const float (&f)[V]) {
   return r;
 }
 
+// Elements e .. e + n - 1 (n <= 8) of `base` (on 16 bytes), wherever e lies, zeros
+// after them: the one or two aligned 16-byte pieces that hold them, shifted.
+// Nothing past the first `total` elements is read.
+__device__ __forceinline__ uint4 load8_any(const __nv_bfloat16* base, int64_t e, int64_t total, int n) {
+  if (n <= 0) return make_uint4(0, 0, 0, 0);
+  const int64_t a = e & ~7ll;
+  const int sh = (int)(e & 7);
+  const bool more = sh + n > 8;
+  uint32_t w[8] = {};
+  if (a + (more ? 16 : 8) <= total) {
+    const uint4 x = *reinterpret_cast<const uint4*>(base + a);
+    w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
+    if (more) {
+      const uint4 y = *reinterpret_cast<const uint4*>(base + a + 8);
+      w[4] = y.x; w[5] = y.y; w[6] = y.z; w[7] = y.w;
+    }
+#pragma unroll
+    for (int i = 0; i < 6; ++i) w[i] = sh & 4 ? w[i + 2] : w[i];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) w[i] = sh & 2 ? w[i + 1] : w[i];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = sh & 1 ? __funnelshift_r(w[i], w[i + 1], 16) : w[i];
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) w[i >> 1] |= (uint32_t)__bfloat16_as_ushort(base[e + i]) << (16 * (i & 1));
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    w[i] = 2 * i + 2 <= n ? w[i] : 2 * i < n ? w[i] & 0xffffu : 0u;
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 // Activations and their derivatives at the pre-activation x (codes of
 // ppo_activation).  x sigmoid(u) has no cancellation where it is small, unlike
 // 0.5 x (1 + tanh(u / 2)).
