@@ -21,12 +21,16 @@
 // cannot keep (8,192 elements; 16,384 forward in bf16; 4,096 element by element)
 // take the kernels that read the row once per reduction.
 // Measured (of the copy rate): 262,144 x 512 bf16 forward 88 us (90 %), backward
-// with dres 184 us (86 %); 48,000 x 1,397 fp32 95 us (84 %) and 149 us (80 %).
+// with dres 174 us (91 %); 48,000 x 1,397 fp32 92 us (86 %) and 146 us (81 %).
+// Near that the instructions of a row are the other limit (75 and 80 % of the
+// issue slots before the arithmetic was packed).
 // The parameter gradients leave each block as one partial row; a second kernel
 // adds the partial rows in a fixed order, so results do not depend on timing.
 #include <algorithm>
+#include <type_traits>
 
 #include "ops.cuh"
+#include "tc_ptx.cuh"
 
 namespace ppo {
 namespace {
@@ -90,6 +94,50 @@ __device__ __forceinline__ void row_sum(float (&v)[N], int lanes, float* red, in
   }
 }
 
+// A piece's elements: in pairs, P of a piece, for the packed fp32 instructions
+// (each half rounded as the scalar one would), or one by one.
+template <int V, int P>
+using Pair = std::conditional_t<P == V, float, float2>;
+__device__ __forceinline__ float mul(float a, float b) { return a * b; }
+__device__ __forceinline__ float2 mul(float2 a, float2 b) { return ptx::fmul2(a, b); }
+__device__ __forceinline__ float fma(float a, float b, float c) { return fmaf(a, b, c); }
+__device__ __forceinline__ float2 fma(float2 a, float2 b, float2 c) { return ptx::ffma2(a, b, c); }
+__device__ __forceinline__ void set(float& o, float x) { o = x; }
+__device__ __forceinline__ void set(float2& o, float x) { o = make_float2(x, x); }
+template <typename E>
+__device__ __forceinline__ E all(float x) {
+  E o;
+  set(o, x);
+  return o;
+}
+template <typename E>
+__device__ __forceinline__ E add(E a, E b) { return fma(a, all<E>(1.f), b); }
+__device__ __forceinline__ float total(float a) { return a; }
+__device__ __forceinline__ float total(float2 a) { return a.x + a.y; }
+template <int V, int P>
+__device__ __forceinline__ void to_pairs(const float (&f)[V], Pair<V, P> (&o)[P]) {
+  if constexpr (P == V) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) o[i] = f[i];
+  } else {
+#pragma unroll
+    for (int i = 0; i < P; ++i) o[i] = make_float2(f[2 * i], f[2 * i + 1]);
+  }
+}
+template <int V, int P>
+__device__ __forceinline__ void from_pairs(const Pair<V, P> (&p)[P], float (&f)[V]) {
+  if constexpr (P == V) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) f[i] = p[i];
+  } else {
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      f[2 * i] = p[i].x;
+      f[2 * i + 1] = p[i].y;
+    }
+  }
+}
+
 // A thread's columns: NV pieces of V, piece j at column at[j] (below 0 where the
 // row starts inside it), of which the elements of mask[j] exist.
 template <int V, int NV>
@@ -115,61 +163,65 @@ struct Columns {
 __host__ __device__ constexpr int ring_depth(int inputs, int size) {
   return inputs == 1 ? 5 : inputs * size == 12 ? 2 : 3;
 }
-template <typename T, int V, int NV, int IN>
+template <typename T, int V, int NV, int IN, int THREADS>      // THREADS 0: blockDim.x
 struct Ring {
   static constexpr bool kFetch = sizeof(T) * V == 16;
   static constexpr int kDeep = ring_depth(IN, (int)sizeof(T));
   uint4* mine;
-  int threads;
+  __device__ __forceinline__ int threads() const { return THREADS ? THREADS : (int)blockDim.x; }
   __device__ __forceinline__ uint4* place(int slot, int m, int j) const {
-    return mine + ((slot * IN + m) * NV + j) * threads;
+    return mine + ((slot * IN + m) * NV + j) * threads();
   }
   __device__ __forceinline__ void fetch(int slot, int m, const void* base, int64_t ld, int64_t row,
                                         const LnArgs& a, const Columns<V, NV>& c) const {
     const T* p = static_cast<const T*>(base) + row * ld;
+    // (a piece may reach into the next rows, but not past the matrix)
 #pragma unroll
     for (int j = 0; j < NV; ++j)
       if (c.mask[j]) {
-        // (a piece may reach into the next rows, but not past the matrix)
         int n = 16;
         if (row + V >= a.M)
           n = (int)min((int64_t)V, (a.M - 1 - row) * ld + a.D - c.at[j]) * (int)sizeof(T);
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
-                         (uint32_t)__cvta_generic_to_shared(place(slot, m, j))),
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(ptx::smem_u32(place(slot, m, j))),
                      "l"(p + c.at[j]), "r"(n)
                      : "memory");
       }
   }
+  template <int P>
   __device__ __forceinline__ void get(int slot, int m, const void* base, int64_t ld, int64_t row,
-                                      const Columns<V, NV>& c, float (&f)[NV][V]) const {
+                                      const Columns<V, NV>& c, Pair<V, P> (&o)[NV][P]) const {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
+      float f[V];
       if constexpr (kFetch) {
-        to_f32<T, V>(*place(slot, m, j), f[j]);
+        to_f32<T, V>(*place(slot, m, j), f);
         if (c.mask[j] != c.kFull) {
 #pragma unroll
-          for (int i = 0; i < V; ++i) f[j][i] = (c.mask[j] >> i) & 1u ? f[j][i] : 0.f;
+          for (int i = 0; i < V; ++i) f[i] = (c.mask[j] >> i) & 1u ? f[i] : 0.f;
         }
       } else {
         const T* p = static_cast<const T*>(base) + row * ld + c.at[j];
 #pragma unroll
-        for (int i = 0; i < V; ++i) f[j][i] = (c.mask[j] >> i) & 1u ? (float)p[i] : 0.f;
+        for (int i = 0; i < V; ++i) f[i] = (c.mask[j] >> i) & 1u ? (float)p[i] : 0.f;
       }
+      to_pairs<V, P>(f, o[j]);
     }
   }
 };
-template <typename T, int V, int NV>
+template <typename T, int V, int NV, int P>
 __device__ __forceinline__ void put_row(void* base, int64_t ld, int64_t row,
-                                        const Columns<V, NV>& c, const float (&f)[NV][V]) {
+                                        const Columns<V, NV>& c, const Pair<V, P> (&q)[NV][P]) {
   T* p = static_cast<T*>(base) + row * ld;
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
+    float f[V];
+    from_pairs<V, P>(q[j], f);
     if (c.mask[j] == c.kFull) {
-      *reinterpret_cast<Raw<T, V>*>(p + c.at[j]) = from_f32<T, V>(f[j]);
+      *reinterpret_cast<Raw<T, V>*>(p + c.at[j]) = from_f32<T, V>(f);
     } else if (c.mask[j]) {
 #pragma unroll
       for (int i = 0; i < V; ++i)
-        if ((c.mask[j] >> i) & 1u) round_to(f[j][i], p[c.at[j] + i]);
+        if ((c.mask[j] >> i) & 1u) round_to(f[i], p[c.at[j] + i]);
     }
   }
 }
@@ -218,17 +270,25 @@ ln_fwd_kernel(const LnArgs a) {
   extern __shared__ uint4 ring_mem[];
   RowWalk w = row_walk<T, V, BLOCK>(a);
   const Columns<V, NV> c(w.rank, w.tpr, w.shift, a.D);
-  using R = Ring<T, V, NV, 1>;
-  const R ring{ring_mem + threadIdx.x, (int)blockDim.x};
-  float ga[NV][V], be[NV][V];
+  using R = Ring<T, V, NV, 1, 0>;
+  // packed: 32,768 x 4,096 bf16 93 us, 99 one by one; 48,000 x 1,397 fp32 91 and
+  // 95; but bf16 rows of a warp 97 and 89 (262,144 x 512)
+  constexpr int P = V > 1 && (BLOCK || sizeof(T) == 4) ? V / 2 : V;
+  using E = Pair<V, P>;
+  const R ring{ring_mem + threadIdx.x};
+  E ga[NV][P], be[NV][P];
 #pragma unroll
-  for (int j = 0; j < NV; ++j)
+  for (int j = 0; j < NV; ++j) {
+    float g[V], b[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const bool in = (c.mask[j] >> i) & 1u;
-      ga[j][i] = in && a.gamma ? __ldg(a.gamma + c.at[j] + i) : 1.f;
-      be[j][i] = in && a.beta ? __ldg(a.beta + c.at[j] + i) : 0.f;
+      g[i] = in && a.gamma ? __ldg(a.gamma + c.at[j] + i) : 1.f;
+      b[i] = in && a.beta ? __ldg(a.beta + c.at[j] + i) : 0.f;
     }
+    to_pairs<V, P>(g, ga[j]);
+    to_pairs<V, P>(b, be[j]);
+  }
   const float inv = 1.f / (float)a.D;
   auto fetch = [&](int slot, int64_t row) {
     if constexpr (R::kFetch) {
@@ -242,36 +302,42 @@ ln_fwd_kernel(const LnArgs a) {
     if constexpr (R::kFetch) ring_wait<R::kDeep>();
     // the slot that was read a round ago takes the farthest row
     fetch(slot == 0 ? R::kDeep - 1 : slot - 1, w.row + (R::kDeep - 1) * w.step);
-    float x[NV][V] = {};
-    if (w.row < a.M) ring.get(slot, 0, a.x, a.ldx, w.row, c, x);
+    E x[NV][P] = {};
+    if (w.row < a.M) ring.template get<P>(slot, 0, a.x, a.ldx, w.row, c, x);
     slot = slot == R::kDeep - 1 ? 0 : slot + 1;
-    float s[1] = {0.f};
+    E sum = all<E>(0.f);
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
-      for (int i = 0; i < V; ++i) s[0] += x[j][i];
+      for (int i = 0; i < P; ++i) sum = add<E>(x[j][i], sum);
+    float s[1] = {total(sum)};
     row_sum<BLOCK>(s, w.lanes, red, set);
     const float mean = s[0] * inv;
-    float q[1] = {0.f};
+    sum = all<E>(0.f);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) x[j][i] -= mean;
+      for (int i = 0; i < P; ++i) x[j][i] = add<E>(x[j][i], all<E>(-mean));
       if (c.mask[j] != c.kFull) {
+        float f[V];
+        from_pairs<V, P>(x[j], f);
 #pragma unroll
-        for (int i = 0; i < V; ++i) x[j][i] = (c.mask[j] >> i) & 1u ? x[j][i] : 0.f;
+        for (int i = 0; i < V; ++i) f[i] = (c.mask[j] >> i) & 1u ? f[i] : 0.f;
+        to_pairs<V, P>(f, x[j]);
       }
 #pragma unroll
-      for (int i = 0; i < V; ++i) q[0] += x[j][i] * x[j][i];
+      for (int i = 0; i < P; ++i) sum = fma(x[j][i], x[j][i], sum);
     }
+    float q[1] = {total(sum)};
     row_sum<BLOCK>(q, w.lanes, red, set);
     const float rstd = rsqrtf(q[0] * inv + a.eps);
     if (w.row < a.M) {
 #pragma unroll
       for (int j = 0; j < NV; ++j)
 #pragma unroll
-        for (int i = 0; i < V; ++i) x[j][i] = x[j][i] * rstd * ga[j][i] + be[j][i];
-      put_row<T, V, NV>(a.out, a.ldo, w.row, c, x);
+        for (int i = 0; i < P; ++i)
+          x[j][i] = fma(mul(x[j][i], all<E>(rstd)), ga[j][i], be[j][i]);
+      put_row<T, V, NV, P>(a.out, a.ldo, w.row, c, x);
       if (a.stats && w.rank == 0)
         *reinterpret_cast<float2*>(a.stats + 2 * w.row) = make_float2(mean, rstd);
     }
@@ -286,16 +352,23 @@ ln_bwd_kernel(const LnArgs a) {
   extern __shared__ uint4 ring_mem[];
   RowWalk w = row_walk<T, V, BLOCK>(a);
   const Columns<V, NV> c(w.rank, w.tpr, w.shift, a.D);
-  using R = Ring<T, V, NV, RES ? 3 : 2>;
-  const R ring{ring_mem + threadIdx.x, (int)blockDim.x};
-  float ga[NV][V], dg[NV][V], db[NV][V];
+  using R = Ring<T, V, NV, RES ? 3 : 2, BLOCK ? 0 : kWarpRowThreads>;
+  // packed: 262,144 x 512 bf16 173 us, 184 one by one; 48,000 x 1,397 fp32 146 and
+  // 147; but bf16 rows of a block 230 and 205 (32,768 x 4,096)
+  constexpr int P = V > 1 && (!BLOCK || sizeof(T) == 4) ? V / 2 : V;
+  using E = Pair<V, P>;
+  const R ring{ring_mem + threadIdx.x};
+  E ga[NV][P], dg[NV][P], db[NV][P];
 #pragma unroll
-  for (int j = 0; j < NV; ++j)
+  for (int j = 0; j < NV; ++j) {
+    float g[V];
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      ga[j][i] = ((c.mask[j] >> i) & 1u) && a.gamma ? __ldg(a.gamma + c.at[j] + i) : 1.f;
-      dg[j][i] = db[j][i] = 0.f;
-    }
+    for (int i = 0; i < V; ++i)
+      g[i] = ((c.mask[j] >> i) & 1u) && a.gamma ? __ldg(a.gamma + c.at[j] + i) : 1.f;
+    to_pairs<V, P>(g, ga[j]);
+#pragma unroll
+    for (int i = 0; i < P; ++i) dg[j][i] = db[j][i] = all<E>(0.f);
+  }
   const float inv = 1.f / (float)a.D;
   auto stat = [&](int64_t r) {
     return r < a.M ? __ldg(reinterpret_cast<const float2*>(a.stats + 2 * r)) : make_float2(0.f, 0.f);
@@ -317,39 +390,41 @@ ln_bwd_kernel(const LnArgs a) {
     nst = stat(w.row + w.step);
     if constexpr (R::kFetch) ring_wait<R::kDeep>();
     fetch(slot == 0 ? R::kDeep - 1 : slot - 1, w.row + (R::kDeep - 1) * w.step);
-    float xh[NV][V] = {}, q[NV][V] = {};
+    E xh[NV][P] = {}, q[NV][P] = {};
     if (w.row < a.M) {
-      ring.get(slot, 0, a.x, a.ldx, w.row, c, xh);
-      ring.get(slot, 1, a.dy, a.lddy, w.row, c, q);
+      ring.template get<P>(slot, 0, a.x, a.ldx, w.row, c, xh);
+      ring.template get<P>(slot, 1, a.dy, a.lddy, w.row, c, q);
     }
-    float s[2] = {0.f, 0.f};
+    E s0 = all<E>(0.f), s1 = all<E>(0.f);
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
+      for (int i = 0; i < P; ++i) {
         // (where no element is, q = 0 and xh reaches nothing that is stored)
-        xh[j][i] = (xh[j][i] - st.x) * st.y;
-        dg[j][i] += q[j][i] * xh[j][i];
-        db[j][i] += q[j][i];
-        q[j][i] *= ga[j][i];
-        s[0] += q[j][i];
-        s[1] += q[j][i] * xh[j][i];
+        xh[j][i] = mul(add<E>(xh[j][i], all<E>(-st.x)), all<E>(st.y));
+        dg[j][i] = fma(q[j][i], xh[j][i], dg[j][i]);
+        db[j][i] = add<E>(q[j][i], db[j][i]);
+        q[j][i] = mul(q[j][i], ga[j][i]);
+        s0 = add<E>(q[j][i], s0);
+        s1 = fma(q[j][i], xh[j][i], s1);
       }
+    float s[2] = {total(s0), total(s1)};
     row_sum<BLOCK>(s, w.lanes, red, set);
     const float m1 = s[0] * inv, m2 = s[1] * inv;
     if (w.row < a.M) {
 #pragma unroll
       for (int j = 0; j < NV; ++j)
 #pragma unroll
-        for (int i = 0; i < V; ++i) q[j][i] = st.y * (q[j][i] - m1 - xh[j][i] * m2);
+        for (int i = 0; i < P; ++i)
+          q[j][i] = mul(fma(xh[j][i], all<E>(-m2), add<E>(q[j][i], all<E>(-m1))), all<E>(st.y));
       if constexpr (RES) {
-        ring.get(slot, 2, a.res, a.ldres, w.row, c, xh);
+        ring.template get<P>(slot, 2, a.res, a.ldres, w.row, c, xh);
 #pragma unroll
         for (int j = 0; j < NV; ++j)
 #pragma unroll
-          for (int i = 0; i < V; ++i) q[j][i] += xh[j][i];
+          for (int i = 0; i < P; ++i) q[j][i] = add<E>(q[j][i], xh[j][i]);
       }
-      put_row<T, V, NV>(a.out, a.ldo, w.row, c, q);
+      put_row<T, V, NV, P>(a.out, a.ldo, w.row, c, q);
     }
     slot = slot == R::kDeep - 1 ? 0 : slot + 1;
     st = nst;
@@ -358,13 +433,17 @@ ln_bwd_kernel(const LnArgs a) {
   float* part = a.part + (int64_t)blockIdx.x * 2 * a.D;
   if constexpr (BLOCK) {
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
+    for (int j = 0; j < NV; ++j) {
+      float g[V], b[V];
+      from_pairs<V, P>(dg[j], g);
+      from_pairs<V, P>(db[j], b);
 #pragma unroll
       for (int i = 0; i < V; ++i)
         if ((c.mask[j] >> i) & 1u) {
-          part[c.at[j] + i] = dg[j][i];
-          part[a.D + c.at[j] + i] = db[j][i];
+          part[c.at[j] + i] = g[i];
+          part[a.D + c.at[j] + i] = b[i];
         }
+    }
   } else {
     // the warps' sums meet in the ring's place: [warp][2][D], D <= 1,024
     asm volatile("cp.async.wait_group 0;" ::: "memory");
@@ -372,21 +451,25 @@ ln_bwd_kernel(const LnArgs a) {
     float* acc = reinterpret_cast<float*>(ring_mem);
     const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp;
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
+    for (int j = 0; j < NV; ++j) {
+      float g[V], b[V];
+      from_pairs<V, P>(dg[j], g);
+      from_pairs<V, P>(db[j], b);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         // lanes that hold the same columns of the warp's rows
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
           if (o >= a.lanes) {
-            dg[j][i] += __shfl_xor_sync(0xffffffffu, dg[j][i], o);
-            db[j][i] += __shfl_xor_sync(0xffffffffu, db[j][i], o);
+            g[i] += __shfl_xor_sync(0xffffffffu, g[i], o);
+            b[i] += __shfl_xor_sync(0xffffffffu, b[i], o);
           }
         if (lane < a.lanes && ((c.mask[j] >> i) & 1u)) {
-          acc[(2 * warp) * a.D + c.at[j] + i] = dg[j][i];
-          acc[(2 * warp + 1) * a.D + c.at[j] + i] = db[j][i];
+          acc[(2 * warp) * a.D + c.at[j] + i] = g[i];
+          acc[(2 * warp + 1) * a.D + c.at[j] + i] = b[i];
         }
       }
+    }
     __syncthreads();
     for (int e = threadIdx.x; e < 2 * a.D; e += kWarpRowThreads) {
       float t = 0.f;
