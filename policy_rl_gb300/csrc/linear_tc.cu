@@ -22,19 +22,20 @@
 // What bounds it: an SM takes in 47 bytes of operands a clock by TMA (measured
 // with and without an epilogue, for long and short sums alike; the full MMA rate
 // would want 64): 0.35 us per 64-deep step of a 256 x 256 tile, 1.76 PFLOP/s at
-// 8,192 x 8,192 x 8,192.  Beside that the epilogue of a tile takes about 2.7 us,
-// 4 with an input box, 5 with gelu' of it, nearly all of it instructions of 16
-// warps in step: with sums of 512 (8 steps) it is the longer part.  32,768 x 512
-// -> 2,048 forward 55 us, with gelu and pre 84 (268 MB written), with a residual
-// too 109; 65,536 x 512 -> 2,048 data gradient 99 us, with gelu' 157.
-// Measured and left, on the last figure or the plain forward's 55 us: a set of
-// eight warps for each accumulator (153; plain 60), inputs fetched 16 rows at a
-// time (+10) or half a unit earlier from a third box (+8: a stage less), inputs
-// by cp.async (+4), one reciprocal for two (+3; none of the four special-function
-// operations of a pair: -8), a fence and store for every 16 rows (plain 62),
-// divisions for each unit's place (plain 58, gelu' 165), stores by the warps
-// themselves (plain 69 and more), the accumulator held in 64 registers so that
-// TMEM is free at once (spills), L2 prefetches of the operands by TMA (67).
+// 8,192 x 8,192 x 8,192.  With sums of 512 (8 steps) the epilogue, 16 warps in
+// step, and the memory behind it come to as much.  32,768 x 512 -> 2,048 forward
+// 59 us, with gelu and pre 69 (302 MB), with a residual too 86; 65,536 x 512 ->
+// 2,048 data gradient 105 us, with gelu' 124 (604 MB).
+// What a warp waits for matters more than what it computes: with a releasing
+// arrival for each read accumulator (a memory barrier) the last figure was 157,
+// forward with gelu and pre 84.  Measured and left, on the last figure: a set of
+// eight warps for each accumulator (148; the plain forward 55 instead of 59), a
+// fence and store for every 16 rows (145).  Before the arrival was relaxed, on
+// 157: inputs fetched 16 rows at a time (+10) or half a unit earlier from a third
+// box (+8: a stage less), inputs by cp.async (+4), one reciprocal for two (+3),
+// divisions for each unit's place (+5), stores by the warps themselves, the
+// accumulator held in 64 registers so that TMEM is free at once (spills), L2
+// prefetches of the operands by TMA.
 //
 // Why pairs: at the full MMA rate a CTA with a 128 x 256 tile would have to
 // take in 48 KB of operands every 512 clocks, more than an SM receives (about
@@ -125,8 +126,10 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+// Relaxed: what it tells the other CTA is that this warp's TMEM loads have
+// completed (they have, before it is issued); no memory is handed over.
 __device__ __forceinline__ void arrive_cluster(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 // TMA load whose completion counts on the even CTA's barrier
 template <int CG>
