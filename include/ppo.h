@@ -640,8 +640,8 @@ typedef enum {
  * d_bias fp32 [N], d_res [M][N], d_pre [M][N] (an output) nullable.  d_y may
  * be d_res (same pitch).  bf16 products run on the tensor cores with fp32
  * accumulation.  fp32 ones keep fp32's digits: as products of three bf16 planes
- * of each operand on the tensor cores from M N K = 2^28 on, on the CUDA cores
- * below.  Forward products of a few rows stream W through the CUDA cores.  M,
+ * of each operand on the tensor cores from M N K = 2^26 on (weight gradients
+ * 2^25), on the CUDA cores below.  Forward products of a few rows stream W through the CUDA cores.  M,
  * N, K are below 2^29, the product of any two at most 2^40.  d_work:
  * ppo_linear_workspace_bytes of the same dtype, sizes and pitches (ldz: the
  * pitch of the [M][N] gradient of ppo_linear_backward_*; a pitch <= 0 stands

@@ -465,29 +465,44 @@ size_t packed_bytes(int64_t rows, int64_t cols, int64_t ld) {
   return ld % 8 ? (size_t)(rows * pitch8(cols) * 2 + 255) / 256 * 256 : 0;
 }
 constexpr int kPackThreads = 256;
-__global__ void __launch_bounds__(kPackThreads)
-pack_rows_kernel(const __nv_bfloat16* __restrict__ src, int64_t ld, int64_t rows, int64_t cols,
-                 int64_t pitch, uint4* __restrict__ dst) {
-  const int64_t per = pitch / 8, n = rows * per, total = (rows - 1) * ld + cols;
-  for (int64_t k = (int64_t)blockIdx.x * kPackThreads + threadIdx.x; k < n;
-       k += (int64_t)gridDim.x * kPackThreads) {
+// A matrix that is copied, and the blocks that do it.  A product's two operands
+// take one launch (2,000 x 130 -> 250 forward: 15 us, 21 with a launch each).
+struct Copy {
+  const void* src;
+  int64_t ld, rows, cols, pitch, rows_pad;
+  uint4* dst;
+  int blocks;
+};
+__device__ __forceinline__ void copy_rows(const Copy& m, int block) {
+  const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(m.src);
+  const int64_t per = m.pitch / 8, n = m.rows * per, total = (m.rows - 1) * m.ld + m.cols;
+  for (int64_t k = (int64_t)block * kPackThreads + threadIdx.x; k < n;
+       k += (int64_t)m.blocks * kPackThreads) {
     const int64_t r = n < (1ll << 32) ? (int64_t)((uint32_t)k / (uint32_t)per) : k / per;
     const int64_t c = (k - r * per) * 8;
-    dst[k] = load8_any(src, r * ld + c, total, (int)min((int64_t)8, cols - c));
+    m.dst[k] = load8_any(src, r * m.ld + c, total, (int)min((int64_t)8, m.cols - c));
   }
 }
+__global__ void __launch_bounds__(kPackThreads) pack_rows_kernel(const Copy a, const Copy b) {
+  pdl_wait();
+  pdl_trigger();
+  if ((int)blockIdx.x < a.blocks) copy_rows(a, blockIdx.x);
+  else copy_rows(b, blockIdx.x - a.blocks);
+}
 // the operand itself, or its copy in the workspace (advanced past it)
-cudaError_t on_16_bytes(const void*& a, int64_t& ld, int64_t rows, int64_t cols, char*& work,
-                        cudaStream_t st) {
-  if (ld % 8 == 0) return cudaSuccess;
+Copy on_16_bytes(const void*& a, int64_t& ld, int64_t rows, int64_t cols, char*& work) {
+  if (ld % 8 == 0) return Copy{};
   const int64_t pitch = pitch8(cols);
-  const int64_t blocks = std::min<int64_t>(cdiv(rows * (pitch / 8), kPackThreads), 16 * kSms);
-  pack_rows_kernel<<<(unsigned)blocks, kPackThreads, 0, st>>>(
-      static_cast<const __nv_bfloat16*>(a), ld, rows, cols, pitch, reinterpret_cast<uint4*>(work));
+  const Copy c{a, ld, rows, cols, pitch, rows, reinterpret_cast<uint4*>(work),
+               (int)std::min<int64_t>(cdiv(rows * (pitch / 8), kPackThreads), 16 * kSms)};
   a = work;
   ld = pitch;
   work += (rows * pitch * 2 + 255) / 256 * 256;
-  return cudaGetLastError();
+  return c;
+}
+cudaError_t pack(const Copy& a, const Copy& b, cudaStream_t st) {
+  if (a.blocks + b.blocks == 0) return cudaSuccess;
+  return launch_pdl(pack_rows_kernel, dim3((unsigned)(a.blocks + b.blocks)), dim3(kPackThreads), 0, st, a, b);
 }
 
 // ---- fp32 operands as three bf16 planes ------------------------------------------------
@@ -499,24 +514,25 @@ int64_t plane_rows(int64_t rows) { return (rows + 63) / 64 * 64; }
 size_t planes_bytes(int64_t rows, int64_t cols) {
   return (size_t)(3 * plane_rows(rows) * pitch8(cols)) * 2;
 }
-__global__ void __launch_bounds__(kPackThreads)
-split_planes_kernel(const float* __restrict__ src, int64_t ld, int64_t rows, int64_t cols,
-                    int64_t pitch, int64_t rows_pad, int vec, uint4* __restrict__ dst) {
-  const int64_t per = pitch / 8, n = rows_pad * per;
-  for (int64_t k = (int64_t)blockIdx.x * kPackThreads + threadIdx.x; k < n;
-       k += (int64_t)gridDim.x * kPackThreads) {
-    const int64_t r = k / per, c = (k - r * per) * 8;
+__device__ __forceinline__ void split_rows(const Copy& m, int block) {
+  const float* src = static_cast<const float*>(m.src);
+  const int64_t per = m.pitch / 8, n = m.rows_pad * per;
+  const bool vec = m.ld % 4 == 0;
+  for (int64_t k = (int64_t)block * kPackThreads + threadIdx.x; k < n;
+       k += (int64_t)m.blocks * kPackThreads) {
+    const int64_t r = n < (1ll << 32) ? (int64_t)((uint32_t)k / (uint32_t)per) : k / per;
+    const int64_t c = (k - r * per) * 8;
     float f[8] = {}, p1[8], p2[8], p3[8];
-    if (r < rows) {
-      const float* q = src + r * ld + c;
-      if (vec && c + 8 <= cols) {
+    if (r < m.rows) {
+      const float* q = src + r * m.ld + c;
+      if (vec && c + 8 <= m.cols) {
         const float4 x = reinterpret_cast<const float4*>(q)[0], y = reinterpret_cast<const float4*>(q)[1];
         f[0] = x.x; f[1] = x.y; f[2] = x.z; f[3] = x.w;
         f[4] = y.x; f[5] = y.y; f[6] = y.z; f[7] = y.w;
       } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          if (c + i < cols) f[i] = q[i];
+          if (c + i < m.cols) f[i] = q[i];
       }
     }
 #pragma unroll
@@ -526,15 +542,24 @@ split_planes_kernel(const float* __restrict__ src, int64_t ld, int64_t rows, int
       p2[i] = (float)__float2bfloat16_rn(rest);
       p3[i] = rest - p2[i];
     }
-    dst[k] = from_f32<__nv_bfloat16, 8>(p1);
-    dst[n + k] = from_f32<__nv_bfloat16, 8>(p2);
-    dst[2 * n + k] = from_f32<__nv_bfloat16, 8>(p3);
+    m.dst[k] = from_f32<__nv_bfloat16, 8>(p1);
+    m.dst[n + k] = from_f32<__nv_bfloat16, 8>(p2);
+    m.dst[2 * n + k] = from_f32<__nv_bfloat16, 8>(p3);
   }
 }
-// Fewer multiplications than this take the CUDA cores, one launch instead of
-// four (at 1.3e8 of them 21 to 23 us a product, 23 to 25 by planes; at 3.6e9 230
-// to 460 us, and 92 to 105 by planes).
-bool takes_planes(int64_t M, int64_t N, int64_t K) { return M * N * K >= 1ll << 28; }
+__global__ void __launch_bounds__(kPackThreads) split_planes_kernel(const Copy a, const Copy b) {
+  pdl_wait();
+  pdl_trigger();
+  if ((int)blockIdx.x < a.blocks) split_rows(a, blockIdx.x);
+  else split_rows(b, blockIdx.x - a.blocks);
+}
+// Fewer multiplications than this take the CUDA cores, one or two launches
+// instead of three (1,024 x 256 -> 256, 6.7e7 of them: 14.6 us forward, 12.5 and
+// 18.9 the gradients; 12.1, 11.9 and 12.7 by planes; 256 x 256 -> 256 7.8, 12.5 and
+// 16.9; 8.6, 13.0 and 11.7 by planes; 4,999 x 1,397 -> 512 230 to 460 and 67 to 77).
+bool takes_planes(int mode, int64_t M, int64_t N, int64_t K) {
+  return M * N * K >= (mode == kWeight ? 1ll << 25 : 1ll << 26);
+}
 
 size_t tc_part_bytes(int64_t I, int64_t J, int64_t R, bool must_split, int terms = 1) {
   const TcPlan p = tc_plan(I, J, R, must_split, terms);
@@ -635,17 +660,16 @@ cudaError_t planes_run(const Product& g, const Epilogue& e, float* db, char* wor
   auto split = [&](const void*& a, int64_t ld, int64_t rows, int64_t cols, int64_t& pitch) {
     pitch = pitch8(cols);
     const int64_t pad = plane_rows(rows);
-    const int vec = ld % 4 == 0;
-    const int64_t blocks = std::min<int64_t>(cdiv(pad * (pitch / 8), kPackThreads), 16 * kSms);
-    split_planes_kernel<<<(unsigned)blocks, kPackThreads, 0, st>>>(
-        static_cast<const float*>(a), ld, rows, cols, pitch, pad, vec, reinterpret_cast<uint4*>(work));
+    const Copy c{a, ld, rows, cols, pitch, pad, reinterpret_cast<uint4*>(work),
+                 (int)std::min<int64_t>(cdiv(pad * (pitch / 8), kPackThreads), 16 * kSms)};
     a = work;
     work += (planes_bytes(rows, cols) + 255) / 256 * 256;
-    return cudaGetLastError();
+    return c;
   };
-  cudaError_t x = amn ? split(t.A, g.sar, g.R, g.I, t.sar) : split(t.A, g.sai, g.I, g.R, t.sai);
-  if (x == cudaSuccess)
-    x = bmn ? split(t.B, g.sbr, g.R, g.J, t.sbr) : split(t.B, g.sbj, g.J, g.R, t.sbj);
+  const Copy ca = amn ? split(t.A, g.sar, g.R, g.I, t.sar) : split(t.A, g.sai, g.I, g.R, t.sai);
+  const Copy cb = bmn ? split(t.B, g.sbr, g.R, g.J, t.sbr) : split(t.B, g.sbj, g.J, g.R, t.sbj);
+  cudaError_t x = launch_pdl(split_planes_kernel, dim3((unsigned)(ca.blocks + cb.blocks)), dim3(kPackThreads),
+                             0, st, ca, cb);
   if (x != cudaSuccess) return x;
   const TcPlan plan = tc_plan(g.I, g.J, g.R, true, kTerms);
   float* sums = db ? reinterpret_cast<float*>(work) : nullptr;
@@ -701,7 +725,7 @@ cudaError_t column_sums(const float* dz, int64_t ld, int64_t M, int64_t N, float
 // The fp32 product on the units that suit its size (db: kWeight alone, nullable).
 cudaError_t run_f32(const Product& g, const Epilogue& e, int64_t M, int64_t N, int64_t K, float* db,
                     void* work, float* part, cudaStream_t st) {
-  if (takes_planes(M, N, K))
+  if (takes_planes(e.mode, M, N, K))
     return planes_run(g, e, db, reinterpret_cast<char*>(part), static_cast<int*>(work), st);
   const cudaError_t x = simt_product(g, e, part, st);
   if (x != cudaSuccess || !db) return x;
@@ -743,7 +767,7 @@ size_t need(int32_t dtype, int mode, int64_t M, int64_t N, int64_t K, int64_t ld
     size_t part = mode == lin::kForward ? lin::split_bytes(M, N, K)
                   : mode == lin::kData  ? lin::split_bytes(M, K, N)
                                         : lin::split_bytes(N, K, M);
-    if (lin::takes_planes(M, N, K))
+    if (lin::takes_planes(mode, M, N, K))
       part = std::max(part, mode == lin::kForward ? lin::planes_need(M, K, N, K, M, N, K)
                             : mode == lin::kData  ? lin::planes_need(M, N, N, K, M, K, N)
                                                   : lin::planes_need(M, N, M, K, N, K, M));
@@ -804,8 +828,8 @@ ppo_status ppo_linear_forward(int32_t dtype, const void* x, int64_t ldx, const v
                                                    : lin::run_f32(g, e, M, N, K, nullptr, work, parts(work), st));
   if (lin::takes_few_rows<__nv_bfloat16>(g)) return status_of(lin::few_rows<__nv_bfloat16>(g, e, st));
   char* free = reinterpret_cast<char*>(parts(work));
-  cudaError_t err = lin::on_16_bytes(x, ldx, M, K, free, st);
-  if (err == cudaSuccess) err = lin::on_16_bytes(w, ldw, N, K, free, st);
+  const lin::Copy ca = lin::on_16_bytes(x, ldx, M, K, free), cb = lin::on_16_bytes(w, ldw, N, K, free);
+  cudaError_t err = lin::pack(ca, cb, st);
   if (err == cudaSuccess)
     err = lin::tc_run({x, ldx, 1, w, ldw, 1, M, N, K}, e, free, static_cast<int*>(work), st);
   return status_of(err);
@@ -838,8 +862,8 @@ ppo_status ppo_linear_backward_data(int32_t dtype, const void* dz, int64_t lddz,
     return status_of(
         lin::run_f32({dz, lddz, 1, w, 1, ldw, M, K, N}, e, M, N, K, nullptr, work, parts(work), st));
   char* free = reinterpret_cast<char*>(parts(work));
-  cudaError_t err = lin::on_16_bytes(dz, lddz, M, N, free, st);
-  if (err == cudaSuccess) err = lin::on_16_bytes(w, ldw, N, K, free, st);
+  const lin::Copy ca = lin::on_16_bytes(dz, lddz, M, N, free), cb = lin::on_16_bytes(w, ldw, N, K, free);
+  cudaError_t err = lin::pack(ca, cb, st);
   if (err == cudaSuccess)
     err = lin::tc_run({dz, lddz, 1, w, 1, ldw, M, K, N}, e, free, static_cast<int*>(work), st);
   return status_of(err);
@@ -864,8 +888,8 @@ ppo_status ppo_linear_backward_weight(int32_t dtype, const void* dz, int64_t ldd
     return status_of(
         lin::run_f32({dz, 1, lddz, x, 1, ldx, N, K, M}, e, M, N, K, db, work, parts(work), st));
   char* free = reinterpret_cast<char*>(parts(work));
-  cudaError_t err = lin::on_16_bytes(dz, lddz, M, N, free, st);
-  if (err == cudaSuccess) err = lin::on_16_bytes(x, ldx, M, K, free, st);
+  const lin::Copy ca = lin::on_16_bytes(dz, lddz, M, N, free), cb = lin::on_16_bytes(x, ldx, M, K, free);
+  cudaError_t err = lin::pack(ca, cb, st);
   if (err == cudaSuccess)
     err = lin::tc_run_weight({dz, 1, lddz, x, 1, ldx, N, K, M}, e, db, free,
                              static_cast<int*>(work), st);

@@ -517,7 +517,7 @@ def test_linear_one_output_per_row(P, M):
 
 @pytest.mark.parametrize("pitch", [None, (645, 643, 650), (648, 641, 644)])
 def test_linear_f32_in_planes(P, pitch):
-    """Sizes that take the tensor cores: 2^28 multiplications and more."""
+    """Sizes that take the tensor cores."""
     check_linear(P, 700, 641, 639, "f32", act="tanh", pact="gelu", dres=True, pitch=pitch, seed=14)
 
 
