@@ -24,13 +24,12 @@
 // would want 64): 0.35 us per 64-deep step of a 256 x 256 tile, 1.76 PFLOP/s at
 // 8,192 x 8,192 x 8,192.  With sums of 512 (8 steps) the epilogue, 16 warps in
 // step, and the memory behind it come to as much.  32,768 x 512 -> 2,048 forward
-// 59 us, with gelu and pre 69 (302 MB), with a residual too 86; 65,536 x 512 ->
-// 2,048 data gradient 105 us, with gelu' 124 (604 MB).
+// 53 us, with gelu and pre 68 (302 MB), with a residual too 86; 65,536 x 512 ->
+// 2,048 data gradient 95 us, with gelu' 121 to 124 (604 MB).
 // What a warp waits for matters more than what it computes: with a releasing
 // arrival for each read accumulator (a memory barrier) the last figure was 157,
-// forward with gelu and pre 84.  Measured and left, on the last figure: a set of
-// eight warps for each accumulator (148; the plain forward 55 instead of 59), a
-// fence and store for every 16 rows (145).  Before the arrival was relaxed, on
+// forward with gelu and pre 84.  Measured and left, on the last figure: a fence and
+// store for every 16 rows (145).  Before the arrival was relaxed, on
 // 157: inputs fetched 16 rows at a time (+10) or half a unit earlier from a third
 // box (+8: a stage less), inputs by cp.async (+4), one reciprocal for two (+3),
 // divisions for each unit's place (+5), stores by the warps themselves, the
@@ -369,7 +368,7 @@ __device__ __forceinline__ void regs_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-template <int CG, int BN, int MODE, bool AMN, bool BMN, bool LATE>
+template <int CG, int BN, int MODE, bool AMN, bool BMN, bool LATE, int SETS>
 __global__ void __launch_bounds__(TileCfg<CG, BN, MODE, LATE>::THREADS, 1)
 lin_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
               const __grid_constant__ CUtensorMap tmO, const __grid_constant__ CUtensorMap tmP,
@@ -407,7 +406,7 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(tfull(a), 1);
-      mbar_init(tempty(a), CG * C::EW);
+      mbar_init(tempty(a), CG * C::EW / SETS);
     }
     mbar_init(drain, 1);
     for (int s = 0; s < S; ++s) mbar_init(summed(s), 2);
@@ -588,22 +587,25 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
   }
   } else {
     if constexpr (kShift) regs_inc<104>();
-    const int q = warp & 3, we = warp - kFirstEpi, part = we / 4;
+    const int q = warp & 3, we = warp - kFirstEpi;
+    // one set of warps reads every accumulator, 64 columns a warp, or two sets one
+    // accumulator each, 128 columns a warp in turn
+    const int set = SETS == 2 && we >= C::EW / 2, part = (we - set * (C::EW / 2)) / 4 * SETS;
     constexpr int PART = 64;                      // columns of an epilogue warp
     uint8_t* box = boxes + we * kBox;
     uint32_t n = 0;      // accumulators read
     uint32_t boxes_in = 0, late_in = 0;
     // one window: TMEM columns of this warp, or false when a wait gave up
     auto window = [&](uint32_t& taddr) {
-      const int acc = n & 1;
-      if (!wait_bar(tfull(acc), (n >> 1) & 1, g)) return false;
+      const int acc = SETS == 1 ? n & 1 : set;
+      if (!wait_bar(tfull(acc), (SETS == 1 ? n >> 1 : n) & 1, g)) return false;
       tc_fence_after();
       taddr = tmem + (uint32_t)(acc * BN + part * PART) + ((uint32_t)(q * 32) << 16);
       return true;
     };
     // the window's columns are read: the MMAs may overwrite them
     auto release = [&]() {
-      const int acc = n & 1;
+      const int acc = SETS == 1 ? n & 1 : set;
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
@@ -670,9 +672,9 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
       struct Place {
         int r, c;
       };
-      const int first = group / p.tiles_j, step = groups / p.tiles_j;
-      const int dr = step * (CG * BM), dc = (groups - step * p.tiles_j) * BN, wrap = p.tiles_j * BN;
-      Place at{(first * CG + (int)rank) * BM + q * 32, (group - first * p.tiles_j) * BN + part * PART};
+      const int u0 = group + set * groups, first = u0 / p.tiles_j, step = SETS * groups / p.tiles_j;
+      const int dr = step * (CG * BM), dc = (SETS * groups - step * p.tiles_j) * BN, wrap = p.tiles_j * BN;
+      Place at{(first * CG + (int)rank) * BM + q * 32, (u0 - first * p.tiles_j) * BN + part * PART};
       auto after = [&](Place x) {
         x.r += dr;
         x.c += dc;
@@ -706,15 +708,21 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
           prefetch_l2(static_cast<const __nv_bfloat16*>(p.e.res) + r * p.e.ldres + x.c);
       };
       Place soon = after(at), later = after(soon);
+      // boxes in their order: SETS side by side of each unit
+      auto beside = [&](const Place& x, int sub) { return Place{x.r, x.c + sub * PART}; };
+      auto next_box = [&](int sub) { return sub + 1 < SETS ? beside(at, sub + 1) : soon; };
       if (lane == 0 && p.tma_in) send(at);
       if (LATE && lane == 0 && p.tma_late) send_late(at, 0);
-      if (p.in || LATE) fetch(soon);
-      for (int u = group; u < p.units; u += groups, at = soon, soon = later, later = after(later)) {
+      if (p.in || LATE) fetch(next_box(0));
+      bool ok = true;
+      for (int u = u0; u < p.units && ok;
+           u += SETS * groups, at = soon, soon = later, later = after(later)) {
         uint32_t taddr;
         if (!window(taddr)) break;
-        const int row0 = at.r, col0 = at.c;
+#pragma unroll 1
+        for (int sub = 0; sub < SETS; ++sub) {
+        const int row0 = at.r, col0 = at.c + sub * PART;
         const bool there = row0 < I && col0 < J;
-        bool ok = true;
         if (there && p.in) {
           if (p.tma_in) {
             ok = wait_bar(box_bar(we), boxes_in & 1, g);
@@ -726,9 +734,11 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                           p.in == 1 ? p.e.ldres : p.e.ldpre, row0, col0, p.I, p.J, 32);
             __syncwarp();
           }
-          if (!__all_sync(0xffffffffu, ok)) break;
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
         }
-        if (there && (p.in || LATE)) fetch(later);
+        // towards L2: the box after the next
+        if (there && (p.in || LATE)) fetch(SETS == 2 ? beside(soon, sub) : later);
         float2 bi[8];      // this thread's columns: c8 + 8 i, + 1
         const int c8 = col0 + 2 * (lane & 3);
         if constexpr (MODE == kForward) {
@@ -755,8 +765,8 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
 #pragma unroll 1
         for (int hr = 0; hr < 2; ++hr) {      // 16 rows at a time
           uint32_t r[32];
-          tmem_ld_16x64(taddr + ((uint32_t)(16 * hr) << 16), r);
-          if (hr == 1) release();
+          tmem_ld_16x64(taddr + (uint32_t)(sub * PART) + ((uint32_t)(16 * hr) << 16), r);
+          if (sub == SETS - 1 && hr == 1) release();
           const int r0 = row0 + 16 * hr;
           // the residual's box takes the next rows
           auto late_next = [&]() {
@@ -852,7 +862,8 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
         // the box takes the next unit's input
         if (p.tma_in && lane == 0) {
           bulk_wait_read0();
-          send(soon);
+          send(next_box(sub));
+        }
         }
       }
     }
@@ -901,7 +912,7 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
 // ---- launch --------------------------------------------------------------------
 // One launch with its tensor maps.  A K-major operand is read in boxes of
 // 64 (sum) x 128 rows, an MN-major one in boxes of 64 (own index) x 64.
-template <int CG, int BN, int MODE, bool AMN, bool BMN, bool LATE = false>
+template <int CG, int BN, int MODE, bool AMN, bool BMN, bool LATE = false, int SETS = 1>
 cudaError_t launch(const Product& g, TcArgs p, int sms, cudaStream_t st) {
   using C = TileCfg<CG, BN, MODE, LATE>;
   CUtensorMap ta, tb, to, tp, ti;
@@ -934,7 +945,7 @@ cudaError_t launch(const Product& g, TcArgs p, int sms, cudaStream_t st) {
     e = tc_make_tmap(MODE == kForward ? &ti : &tp, p.e.res, p.J, p.I, p.e.ldres, 64, 16);
     if (e != cudaSuccess) return e;
   }
-  const auto kernel = lin_tc_kernel<CG, BN, MODE, AMN, BMN, LATE>;
+  const auto kernel = lin_tc_kernel<CG, BN, MODE, AMN, BMN, LATE, SETS>;
   static thread_local int prepared = -1;   // the device whose shared-memory opt-in is made
   int dev = 0;
   e = cudaGetDevice(&dev);
@@ -970,6 +981,19 @@ cudaError_t launch_mode(const Product& g, const TcArgs& p, int mode, int sms, cu
     return launch<CG, BN, kWeight, false, true>(g, p, sms, st);
   }
   const bool late = p.e.res && p.in != 1;
+  // Two sets of epilogue warps where there is little to compute and there are
+  // tiles enough: one set computes while the other waits (for TMEM, its input, a
+  // fence, a store).  32,768 x 512 -> 2,048 forward 59 us with one set, 53 with two;
+  // 65,536 x 512 -> 2,048 data gradient 105 and 95, with a residual 121 and 112;
+  // 16,384 x 4,096 -> 2,048 forward with one 163 and 155; but 65 and 68 at 32,768 x
+  // 512 -> 2,048, and 124 and 148 with gelu' of the data gradient.
+  if constexpr (CG == 2) {
+    const bool light = p.e.act == PPO_ACT_NONE || p.e.act == PPO_ACT_RELU;
+    const bool short_in = mode == kForward && p.in && p.R < 1024;
+    if (!late && light && !short_in && p.units >= 4 * (sms / CG))
+      return mode == kForward ? launch<CG, BN, kForward, false, false, false, 2>(g, p, sms, st)
+                              : launch<CG, BN, kData, false, true, false, 2>(g, p, sms, st);
+  }
   if (mode == kForward)
     return late ? launch<CG, BN, kForward, false, false, true>(g, p, sms, st)
                 : launch<CG, BN, kForward, false, false>(g, p, sms, st);
