@@ -721,149 +721,149 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
         if (!window(taddr)) break;
 #pragma unroll 1
         for (int sub = 0; sub < SETS; ++sub) {
-        const int row0 = at.r, col0 = at.c + sub * PART;
-        const bool there = row0 < I && col0 < J;
-        if (there && p.in) {
-          if (p.tma_in) {
-            ok = wait_bar(box_bar(we), boxes_in & 1, g);
-            ++boxes_in;
-          } else {
-            if (lane == 0) bulk_wait_read0();
-            __syncwarp();
-            box_load_slow(box, lane, p.in == 1 ? p.e.res : p.e.pre,
-                          p.in == 1 ? p.e.ldres : p.e.ldpre, row0, col0, p.I, p.J, 32);
-            __syncwarp();
-          }
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-        }
-        // towards L2: the box after the next
-        if (there && (p.in || LATE)) fetch(SETS == 2 ? beside(soon, sub) : later);
-        float2 bi[8];      // this thread's columns: c8 + 8 i, + 1
-        const int c8 = col0 + 2 * (lane & 3);
-        if constexpr (MODE == kForward) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            bi[i] = make_float2(0.f, 0.f);
-            if (p.e.bias && there)
-              bi[i] = col0 + PART <= J
-                          ? __ldg(reinterpret_cast<const float2*>(p.e.bias + c8 + 8 * i))
-                          : bias_slow(p.e.bias, c8 + 8 * i, J);
-          }
-        }
-        // `rows` rows of the box to where they belong (by TMA: after a fence)
-        auto leave = [&](uint8_t* from, const CUtensorMap* tm, bool tma, void* base, int64_t ld,
-                         int r0, int rows) {
-          if (tma) {
-            if (lane == 0 && r0 < I) tma_store_2d(tm, smem_u32(from), col0, r0);
-          } else {
-            box_store_slow(from, lane, base, ld, r0, col0, p.I, p.J, rows);
-            __syncwarp();
-          }
-        };
-        const bool two = MODE == kForward && p.e.pre;   // results: pre as well
-#pragma unroll 1
-        for (int hr = 0; hr < 2; ++hr) {      // 16 rows at a time
-          uint32_t r[32];
-          tmem_ld_16x64(taddr + (uint32_t)(sub * PART) + ((uint32_t)(16 * hr) << 16), r);
-          if (sub == SETS - 1 && hr == 1) release();
-          const int r0 = row0 + 16 * hr;
-          // the residual's box takes the next rows
-          auto late_next = [&]() {
-            if (LATE && p.tma_late && lane == 0) {
-              if (hr == 0) send_late(at, 1);
-              else send_late(soon, 0);
-            }
-          };
-          if (!there) {
-            late_next();
-            continue;
-          }
-          float2 v[16];      // v[2 i + b]: column group i, row lane / 4 + 8 b
-#pragma unroll
-          for (int k = 0; k < 16; ++k)
-            v[k] = make_float2(__uint_as_float(r[2 * k]), __uint_as_float(r[2 * k + 1]));
-          if constexpr (MODE == kForward) {
-#pragma unroll
-            for (int k = 0; k < 16; ++k) v[k] = ffma2(v[k], both(1.f), bi[k / 2]);
-            if (p.e.pre) {
-              // (halves: the last stores have read them)
+          const int row0 = at.r, col0 = at.c + sub * PART;
+          const bool there = row0 < I && col0 < J;
+          if (there && p.in) {
+            if (p.tma_in) {
+              ok = wait_bar(box_bar(we), boxes_in & 1, g);
+              ++boxes_in;
+            } else {
               if (lane == 0) bulk_wait_read0();
               __syncwarp();
+              box_load_slow(box, lane, p.in == 1 ? p.e.res : p.e.pre,
+                            p.in == 1 ? p.e.ldres : p.e.ldpre, row0, col0, p.I, p.J, 32);
+              __syncwarp();
+            }
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+          }
+          // towards L2: the box after the next
+          if (there && (p.in || LATE)) fetch(SETS == 2 ? beside(soon, sub) : later);
+          float2 bi[8];      // this thread's columns: c8 + 8 i, + 1
+          const int c8 = col0 + 2 * (lane & 3);
+          if constexpr (MODE == kForward) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              bi[i] = make_float2(0.f, 0.f);
+              if (p.e.bias && there)
+                bi[i] = col0 + PART <= J
+                            ? __ldg(reinterpret_cast<const float2*>(p.e.bias + c8 + 8 * i))
+                            : bias_slow(p.e.bias, c8 + 8 * i, J);
+            }
+          }
+          // `rows` rows of the box to where they belong (by TMA: after a fence)
+          auto leave = [&](uint8_t* from, const CUtensorMap* tm, bool tma, void* base, int64_t ld,
+                           int r0, int rows) {
+            if (tma) {
+              if (lane == 0 && r0 < I) tma_store_2d(tm, smem_u32(from), col0, r0);
+            } else {
+              box_store_slow(from, lane, base, ld, r0, col0, p.I, p.J, rows);
+              __syncwarp();
+            }
+          };
+          const bool two = MODE == kForward && p.e.pre;   // results: pre as well
+#pragma unroll 1
+          for (int hr = 0; hr < 2; ++hr) {      // 16 rows at a time
+            uint32_t r[32];
+            tmem_ld_16x64(taddr + (uint32_t)(sub * PART) + ((uint32_t)(16 * hr) << 16), r);
+            if (sub == SETS - 1 && hr == 1) release();
+            const int r0 = row0 + 16 * hr;
+            // the residual's box takes the next rows
+            auto late_next = [&]() {
+              if (LATE && p.tma_late && lane == 0) {
+                if (hr == 0) send_late(at, 1);
+                else send_late(soon, 0);
+              }
+            };
+            if (!there) {
+              late_next();
+              continue;
+            }
+            float2 v[16];      // v[2 i + b]: column group i, row lane / 4 + 8 b
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+              v[k] = make_float2(__uint_as_float(r[2 * k]), __uint_as_float(r[2 * k + 1]));
+            if constexpr (MODE == kForward) {
+#pragma unroll
+              for (int k = 0; k < 16; ++k) v[k] = ffma2(v[k], both(1.f), bi[k / 2]);
+              if (p.e.pre) {
+                // (halves: the last stores have read them)
+                if (lane == 0) bulk_wait_read0();
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 8; i += 2) {
+                  uint32_t w[4];
+#pragma unroll
+                  for (int j = 0; j < 4; ++j) w[j] = pack_bf16x2(v[2 * i + j].x, v[2 * i + j].y);
+                  quad_put(box, lane, i, w);
+                }
+              }
+              act_chunk(p.e.act, v);
+            }
+            uint8_t* half = two ? box + 2048 : box + 2048 * hr;
+            if (p.in) {
+              uint32_t x[16];
+#pragma unroll
+              for (int i = 0; i < 8; i += 2) quad_get(half, lane, i, x + 2 * i);
+              if (MODE == kData && p.in == 2) {
+                slope_chunk(p.e.act, x, v);
+              } else {
+#pragma unroll
+                for (int k = 0; k < 16; ++k) v[k] = ffma2(v[k], both(1.f), unpack_bf16x2(x[k]));
+              }
+              __syncwarp();   // all have read the half
+            } else if (hr == 0 && !two) {
+              if (lane == 0) bulk_wait_read0();
+              __syncwarp();
+            }
+            if constexpr (LATE) {
+              if (p.tma_late) {
+                if (r0 < I) {      // (rows off the matrix are not stored)
+                  ok = __all_sync(0xffffffffu, wait_bar(late_bar(we), late_in & 1, g));
+                  if (!ok) break;
+                  ++late_in;
+                }
+              } else {
+                box_load_slow(late, lane, p.e.res, p.e.ldres, r0, col0, p.I, p.J, 16);
+                __syncwarp();
+              }
 #pragma unroll
               for (int i = 0; i < 8; i += 2) {
-                uint32_t w[4];
+                uint32_t x[4];
+                quad_get(late, lane, i, x);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) w[j] = pack_bf16x2(v[2 * i + j].x, v[2 * i + j].y);
-                quad_put(box, lane, i, w);
+                for (int j = 0; j < 4; ++j)
+                  v[2 * i + j] = ffma2(v[2 * i + j], both(1.f), unpack_bf16x2(x[j]));
               }
-            }
-            act_chunk(p.e.act, v);
-          }
-          uint8_t* half = two ? box + 2048 : box + 2048 * hr;
-          if (p.in) {
-            uint32_t x[16];
-#pragma unroll
-            for (int i = 0; i < 8; i += 2) quad_get(half, lane, i, x + 2 * i);
-            if (MODE == kData && p.in == 2) {
-              slope_chunk(p.e.act, x, v);
-            } else {
-#pragma unroll
-              for (int k = 0; k < 16; ++k) v[k] = ffma2(v[k], both(1.f), unpack_bf16x2(x[k]));
-            }
-            __syncwarp();   // all have read the half
-          } else if (hr == 0 && !two) {
-            if (lane == 0) bulk_wait_read0();
-            __syncwarp();
-          }
-          if constexpr (LATE) {
-            if (p.tma_late) {
-              if (r0 < I) {      // (rows off the matrix are not stored)
-                ok = __all_sync(0xffffffffu, wait_bar(late_bar(we), late_in & 1, g));
-                if (!ok) break;
-                ++late_in;
-              }
-            } else {
-              box_load_slow(late, lane, p.e.res, p.e.ldres, r0, col0, p.I, p.J, 16);
+              fence_proxy_async_smem();      // (read by all lanes before it is written again)
               __syncwarp();
+              late_next();
             }
 #pragma unroll
             for (int i = 0; i < 8; i += 2) {
-              uint32_t x[4];
-              quad_get(late, lane, i, x);
+              uint32_t w[4];
 #pragma unroll
-              for (int j = 0; j < 4; ++j)
-                v[2 * i + j] = ffma2(v[2 * i + j], both(1.f), unpack_bf16x2(x[j]));
+              for (int j = 0; j < 4; ++j) w[j] = pack_bf16x2(v[2 * i + j].x, v[2 * i + j].y);
+              quad_put(half, lane, i, w);
             }
-            fence_proxy_async_smem();      // (read by all lanes before it is written again)
-            __syncwarp();
-            late_next();
-          }
-#pragma unroll
-          for (int i = 0; i < 8; i += 2) {
-            uint32_t w[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) w[j] = pack_bf16x2(v[2 * i + j].x, v[2 * i + j].y);
-            quad_put(half, lane, i, w);
-          }
-          if (two || hr == 1) {
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (two) {
-              leave(box, &tmP, p.tma_pre, p.e.pre, p.e.ldpre, r0, 16);
-              leave(half, &tmO, p.tma_out, p.e.out, p.e.ldo, r0, 16);
-            } else {
-              leave(box, &tmO, p.tma_out, p.e.out, p.e.ldo, row0, 32);
+            if (two || hr == 1) {
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (two) {
+                leave(box, &tmP, p.tma_pre, p.e.pre, p.e.ldpre, r0, 16);
+                leave(half, &tmO, p.tma_out, p.e.out, p.e.ldo, r0, 16);
+              } else {
+                leave(box, &tmO, p.tma_out, p.e.out, p.e.ldo, row0, 32);
+              }
+              if (lane == 0) bulk_commit();
             }
-            if (lane == 0) bulk_commit();
           }
-        }
-        if (!ok) break;
-        // the box takes the next unit's input
-        if (p.tma_in && lane == 0) {
-          bulk_wait_read0();
-          send(next_box(sub));
-        }
+          if (!ok) break;
+          // the box takes the next unit's input
+          if (p.tma_in && lane == 0) {
+            bulk_wait_read0();
+            send(next_box(sub));
+          }
         }
       }
     }
