@@ -585,6 +585,8 @@ finish_weight_kernel(const float* __restrict__ part, int splits, int64_t I, int6
     const int64_t n4 = I * ldp / 4, n = I * ldp;
     for (int64_t k = (int64_t)blockIdx.x * kFinishThreads + threadIdx.x; k < n4;
          k += (int64_t)wblocks * kFinishThreads) {
+      const int64_t i = 4 * k / ldp, j = 4 * k - i * ldp;
+      if (j >= J) continue;      // the partial rows' padding (J % 8 <= 4), which dW's rows lack
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
       for (int s = 0; s < splits; ++s) {
@@ -594,7 +596,6 @@ finish_weight_kernel(const float* __restrict__ part, int splits, int64_t I, int6
         v.z += x.z;
         v.w += x.w;
       }
-      const int64_t i = 4 * k / ldp, j = 4 * k - i * ldp;
       float* o = dw + i * J + j;
       float vv[4] = {v.x, v.y, v.z, v.w};
       if (PLANES && !(isfinite(v.x) && isfinite(v.y) && isfinite(v.z) && isfinite(v.w))) {

@@ -1,0 +1,42 @@
+"""The trunk operators at the limits of their plans: widths that fill a shared-
+memory size exactly, very many rows of few columns, rows padded in the
+workspace, values near the ends of the types' ranges, very long sums, and
+shapes that reach the variants for large problems.  Bounds as in
+test_gpu_trunk_ops.py."""
+import os
+import subprocess
+import sys
+
+import numpy as np
+import pytest
+
+import _trunk_ref as R
+from test_gpu_trunk_ops import (P, check_linear, check_ln, check_scan, dev, f64, ln_inputs, out,  # noqa: F401
+                                prod_bound, rounding, scan_inputs, tdt, within)
+
+pytestmark = pytest.mark.gpu
+U32, U16 = R.U32, R.U16
+HERE = os.path.dirname(os.path.abspath(__file__))
+
+
+@pytest.mark.parametrize("dtype,M,N,K", [("bf16", 4096, 512, 100), ("bf16", 65536, 64, 20),
+                                         ("f32", 700, 640, 636), ("f32", 3000, 130, 100)])
+@pytest.mark.parametrize("bias", [True, False])
+def test_weight_gradient_of_widths_four_past_eight(P, dtype, M, N, K, bias):
+    """K % 8 = 4: rows of partial products are padded, rows of dW are not.  The
+    workspace holds what earlier calls may have left, and dW and db lie in larger
+    buffers whose other elements stay."""
+    import torch
+    rng = np.random.default_rng(M + K)
+    dz, x = dev(rng.normal(size=(M, N)), dtype), dev(rng.normal(size=(M, K)), dtype)
+    work = torch.zeros(P.ppo_linear_workspace_bytes(M, N, K, tdt(dtype)), dtype=torch.uint8, device="cuda")
+    work[256:] = 0x7f
+    room, roomb = torch.full((N * K + 64,), 5.0, device="cuda"), torch.full((N + 64,), 5.0, device="cuda")
+    dw, db = room[:N * K].view(N, K), roomb[:N]
+    P.ppo_linear_backward_weight(dz, x, dw, db=db if bias else None, work=work)
+    P.ppo_work_status(work)
+    Z, X = f64(dz), f64(x)
+    within(dw, Z.T @ X, prod_bound(dtype, Z.T, X, M), "dw")
+    if bias:
+        within(db, Z.sum(0), 8 * U32 * (np.sqrt(M) + 8) * np.abs(Z).sum(0), "db")
+    assert bool((room[N * K:] == 5.0).all()) and bool((roomb[N if bias else 0:] == 5.0).all())
