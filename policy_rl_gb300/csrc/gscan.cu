@@ -1019,7 +1019,7 @@ ppo_status run(int32_t dtype, ScanArgs s, bool backward, bool pairs, bool wide, 
   if (dtype == PPO_DTYPE_F32) e = dispatch<float, 1>(s, backward, st);
   else if (pairs) e = dispatch<__nv_bfloat16, 2>(s, backward, st);
   else e = dispatch<__nv_bfloat16, 1>(s, backward, st);
-  return e == cudaSuccess ? PPO_OK : PPO_ERR_CUDA;
+  return status_of(e);
 }
 
 bool aligned(std::initializer_list<const void*> ptrs, int bytes) {

@@ -765,7 +765,7 @@ ppo_status checked(std::initializer_list<const void*> ptrs, const void* work, si
   if (!al16(work)) return PPO_ERR_ALIGN;
   return ops::num_sms() > 0 ? PPO_OK : PPO_ERR_CUDA;
 }
-ppo_status status_of(cudaError_t e) { return e == cudaSuccess ? PPO_OK : PPO_ERR_CUDA; }
+using ops::status_of;
 // Workspace of one direction: the copies of its two operands (pitches lda,
 // ldb) and the partial products or column sums behind them.
 size_t need(int32_t dtype, int mode, int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb) {
@@ -907,12 +907,11 @@ ppo_status ppo_work_status(void* work, cudaStream_t st) {
   if (!work) return PPO_ERR_INVALID;
   if (!al16(work)) return PPO_ERR_ALIGN;
   int32_t word = 0;
-  if (cudaMemcpyAsync(&word, work, sizeof(word), cudaMemcpyDeviceToHost, st) != cudaSuccess ||
-      cudaStreamSynchronize(st) != cudaSuccess)
-    return PPO_ERR_CUDA;
-  if (word == 0) return PPO_OK;
-  if (cudaMemsetAsync(work, 0, sizeof(word), st) != cudaSuccess) return PPO_ERR_CUDA;
-  return PPO_ERR_TIMEOUT;
+  cudaError_t e = cudaMemcpyAsync(&word, work, sizeof(word), cudaMemcpyDeviceToHost, st);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+  if (e != cudaSuccess || word == 0) return status_of(e);
+  e = cudaMemsetAsync(work, 0, sizeof(word), st);
+  return e == cudaSuccess ? PPO_ERR_TIMEOUT : status_of(e);
 }
 
 }  // extern "C"

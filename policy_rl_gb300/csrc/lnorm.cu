@@ -719,7 +719,7 @@ ppo_status ppo_layernorm_forward(int32_t dtype, const void* x, int64_t ldx, int6
   a.classes = p.classes;
   const cudaError_t e = dtype == PPO_DTYPE_F32 ? dispatch<float>(a, p, false, st)
                                                : dispatch<__nv_bfloat16>(a, p, false, st);
-  return e == cudaSuccess ? PPO_OK : PPO_ERR_CUDA;
+  return ops::status_of(e);
 }
 
 ppo_status ppo_layernorm_backward_workspace_bytes(int64_t M, int64_t D, size_t* bytes) {
@@ -773,7 +773,7 @@ ppo_status ppo_layernorm_backward(int32_t dtype, const void* dy, int64_t lddy, c
   if (e == cudaSuccess && params)
     e = launch_pdl(ln_param_grad_kernel, dim3((unsigned)((2 * D + kWarp - 1) / kWarp)),
                    dim3(kFinThreads), 0, st, (const float*)a.part, p.grid, (int)D, dgamma, dbeta);
-  return e == cudaSuccess ? PPO_OK : PPO_ERR_CUDA;
+  return ops::status_of(e);
 }
 
 }  // extern "C"

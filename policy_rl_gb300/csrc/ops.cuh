@@ -17,6 +17,14 @@ inline bool extent_ok(int64_t rows, int64_t ld, int64_t row) {
          rows <= (1ll << 59) / ld;
 }
 
+// A call's status.  The runtime remembers the error of a refused launch or query:
+// it is dropped here, or the next call's launch check would report it.
+inline ppo_status status_of(cudaError_t e) {
+  if (e == cudaSuccess) return PPO_OK;
+  cudaGetLastError();
+  return PPO_ERR_CUDA;
+}
+
 // SM count of the current device (0 without a device); one query per device
 inline int num_sms() {
   static int cached[64] = {};

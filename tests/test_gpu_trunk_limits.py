@@ -40,3 +40,30 @@ def test_weight_gradient_of_widths_four_past_eight(P, dtype, M, N, K, bias):
     if bias:
         within(db, Z.sum(0), 8 * U32 * (np.sqrt(M) + 8) * np.abs(Z).sum(0), "db")
     assert bool((room[N * K:] == 5.0).all()) and bool((roomb[N if bias else 0:] == 5.0).all())
+
+
+def test_a_refused_call_leaves_no_error_behind():
+    """The status word cannot be waited for inside a graph capture: that call says
+    so, and the calls after it are not blamed for it."""
+    code = (f"import sys; sys.path[:0] = [{os.path.dirname(HERE)!r}, {HERE!r}]\n"
+            "import torch\n"
+            "import policy_rl_gb300 as P\n"
+            "from test_gpu_trunk_ops import check_linear, check_ln, check_scan\n"
+            "work, side = torch.zeros(256, dtype=torch.uint8, device='cuda'), torch.cuda.Stream()\n"
+            "def refused():\n"
+            "    try:\n"
+            "        with torch.cuda.graph(torch.cuda.CUDAGraph(), stream=side):\n"
+            "            try:\n"
+            "                P.ppo_work_status(work, stream=side)\n"
+            "            except P.PpoError as e:\n"
+            "                assert 'PPO_ERR_CUDA' in str(e)\n"
+            "                return True\n"
+            "    except RuntimeError:\n"
+            "        return True\n"
+            "for check in (lambda: check_ln(P, 9, 40, 'f32'), lambda: check_scan(P, 3, 2, 8, 'f32', 1),\n"
+            "              lambda: check_linear(P, 20, 24, 16, 'f32')):\n"
+            "    assert refused()\n"
+            "    torch.cuda.synchronize()\n"
+            "    check()\n")
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
