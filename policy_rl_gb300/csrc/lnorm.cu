@@ -640,27 +640,54 @@ Plan plan_of(int64_t M, int64_t D, int vec, int64_t ld, int sms, bool backward, 
   return p;
 }
 
+// Dynamic shared memory that the plans of a kernel ask for at most: its ring in the
+// largest block and, backward with rows per warp, the warps' parameter gradients.
+template <typename T, int V, int NV, bool BLOCK, int IN, bool BACK>
+constexpr int most_smem() {
+  const int ring = V > 1 ? ring_depth(IN, (int)sizeof(T)) * IN * NV * 16 *
+                               (BLOCK ? kMaxBlock : kWarpRowThreads)
+                         : 0;
+  const int sums = BACK && !BLOCK ? kWarpRowThreads / kWarp * 2 * (kWarp * V * NV) * (int)sizeof(float) : 0;
+  return std::max(ring, sums);
+}
+// One launch.  A kernel that may need it is allowed its largest size once per host
+// thread and device, whatever this call's size: static shared memory counts
+// towards the 48 KB that need no allowance, and a call must not take back what
+// another thread's launch relies on.
+template <auto KERNEL, int MOST>
+cudaError_t launch(const LnArgs& a, const Plan& p, cudaStream_t st) {
+  static_assert(MOST + 4 * kMaxWarps * 4 <= 232448, "shared memory per CTA");
+  if (p.smem > (size_t)MOST) return cudaErrorInvalidValue;
+  if constexpr (MOST > 40 * 1024) {
+    static thread_local int prepared = -1;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess && prepared != dev)
+      e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, MOST);
+    if (e != cudaSuccess) return e;
+    prepared = dev;
+  }
+  KERNEL<<<p.grid, p.threads, p.smem, st>>>(a);
+  return cudaGetLastError();
+}
+
 template <typename T, int V, int NV>
 cudaError_t go(const LnArgs& a, const Plan& p, bool backward, cudaStream_t st) {
-  void (*kernel)(const LnArgs) = nullptr;
   if (p.lanes) {
-    kernel = !backward ? ln_fwd_kernel<T, V, NV, false>
-             : a.res   ? ln_bwd_kernel<T, V, NV, false, true>
-                       : ln_bwd_kernel<T, V, NV, false, false>;
-  } else if (!backward) {      // (blocks use one count of elements each way)
-    if constexpr (V * NV == max_kept(V, false)) kernel = ln_fwd_kernel<T, V, NV, true>;
-  } else {
-    if constexpr (V * NV == max_kept(V, true))
-      kernel = a.res ? ln_bwd_kernel<T, V, NV, true, true> : ln_bwd_kernel<T, V, NV, true, false>;
+    if (!backward)
+      return launch<ln_fwd_kernel<T, V, NV, false>, most_smem<T, V, NV, false, 1, false>()>(a, p, st);
+    return a.res ? launch<ln_bwd_kernel<T, V, NV, false, true>, most_smem<T, V, NV, false, 3, true>()>(a, p, st)
+                 : launch<ln_bwd_kernel<T, V, NV, false, false>, most_smem<T, V, NV, false, 2, true>()>(a, p, st);
   }
-  if (!kernel) return cudaErrorInvalidValue;
-  if (p.smem > 48 * 1024) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)p.smem);
-    if (e != cudaSuccess) return e;
-  }
-  kernel<<<p.grid, p.threads, p.smem, st>>>(a);
-  return cudaGetLastError();
+  // (blocks use one count of elements each way)
+  if constexpr (V * NV == max_kept(V, false))
+    if (!backward)
+      return launch<ln_fwd_kernel<T, V, NV, true>, most_smem<T, V, NV, true, 1, false>()>(a, p, st);
+  if constexpr (V * NV == max_kept(V, true))
+    if (backward)
+      return a.res ? launch<ln_bwd_kernel<T, V, NV, true, true>, most_smem<T, V, NV, true, 3, true>()>(a, p, st)
+                   : launch<ln_bwd_kernel<T, V, NV, true, false>, most_smem<T, V, NV, true, 2, true>()>(a, p, st);
+  return cudaErrorInvalidValue;
 }
 
 template <typename T>

@@ -67,3 +67,18 @@ def test_a_refused_call_leaves_no_error_behind():
             "    check()\n")
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("dtype,widths", [("f32", (1532, 1534, 1536, 1537, 1801, 2048)),
+                                          ("bf16", (3576, 3584, 3585, 3847, 4096))])
+def test_layernorm_backward_of_rows_that_fill_48_kb(dtype, widths):
+    """Widths whose rows on their way take 48 KB beside what the kernel holds
+    statically: in a process of their own and in ascending order, so that no wider
+    call has gone before."""
+    code = (f"import sys; sys.path[:0] = [{os.path.dirname(HERE)!r}, {HERE!r}]\n"
+            "import policy_rl_gb300 as P\nfrom test_gpu_trunk_ops import check_ln\n"
+            f"for D in {widths}:\n"
+            "    for res in (False, True):\n"
+            f"        check_ln(P, 40, D, {dtype!r}, res=res, seed=D)\n")
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
