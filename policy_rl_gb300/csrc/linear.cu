@@ -287,6 +287,12 @@ template <typename T>
 bool takes_few_rows(const Product& g) {
   constexpr int E = 16 / (int)sizeof(T);
   if (g.I <= 2 || (sizeof(T) == 4 && g.I <= kFewGroup)) return true;
+  // Many rows of few columns: a block for every eight of them costs more than tiles
+  // do (here / there, bf16, K = 64: 2,048 rows 3.7 / 6.8 us of one column and 3.7 /
+  // 4.3 of eight, 4,096 6.6 / 6.8 and 6.6 / 4.2, 100,000 118 / 29; fp32, one column:
+  // 4,096 rows 5.4 / 7.7 and 8,192 9.4 / 7.9 at K = 64, 16,384 19 / 26 and 50,000
+  // 75 / 66 at 256).  It also keeps the groups of rows below a grid's 65,535.
+  if (g.I > (sizeof(T) == 4 ? std::max<int64_t>(2048, 64 * g.R) : 2048)) return false;
   const bool vec = g.sai % E == 0 && g.sbj % E == 0;
   const int64_t groups2 = g.I <= 4 ? 1 : 2 * ((g.I + kFewGroup - 1) / kFewGroup);   // halves
   return groups2 * g.J * g.R <= (vec ? 1ll << 22 : 1ll << 23);

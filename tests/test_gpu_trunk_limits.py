@@ -82,3 +82,19 @@ def test_layernorm_backward_of_rows_that_fill_48_kb(dtype, widths):
             f"        check_ln(P, 40, D, {dtype!r}, res=res, seed=D)\n")
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("M,N,K", [(600000, 1, 16), (600000, 1, 7), (1000000, 1, 33), (530001, 3, 5), (524281, 2, 8)])
+def test_linear_forward_of_very_many_rows_and_few_columns(P, M, N, K, dtype):
+    """A value head over a large rollout."""
+    import torch
+    rng = np.random.default_rng(K)
+    x, w, b = dev(rng.normal(size=(M, K)), dtype), dev(rng.normal(size=(N, K)), dtype), dev(rng.normal(size=N))
+    y = out((M, N), dtype)
+    work = torch.zeros(P.ppo_linear_workspace_bytes(M, N, K, tdt(dtype)), dtype=torch.uint8, device="cuda")
+    P.ppo_linear_forward(x, w, y, bias=b, work=work)
+    P.ppo_work_status(work)
+    X, W = f64(x), f64(w)
+    ry = X @ W.T + f64(b)
+    within(y, ry, rounding(dtype, ry) + prod_bound(dtype, X, W.T, K) + 2 * U32 * (np.abs(ry) + np.abs(f64(b))), "y")
