@@ -318,8 +318,9 @@ __device__ __forceinline__ float2 slope_pair(float2 x) {
     gate_pair<ACT>(x, q, e, x2);
     float2 t = ffma2(q, both(-1.f), both(1.f));
     if constexpr (ACT == PPO_ACT_GELU)
-      t = fmul2(t, ffma2(x2, both(3.f * ops::kGeluU * ops::kGeluA), both(ops::kGeluU)));
-    return ffma2(fmul2(x, t), q, q);
+      t = fmul2(t, ffma2(make_float2(fminf(x2.x, ops::kGeluTop), fminf(x2.y, ops::kGeluTop)),
+                         both(3.f * ops::kGeluU * ops::kGeluA), both(ops::kGeluU)));
+    return ffma2(fmul2(x, q), t, q);
   }
   return make_float2(ops::act_slope<true>(ACT, x.x), ops::act_slope<true>(ACT, x.y));
 }

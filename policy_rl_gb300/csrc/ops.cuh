@@ -111,6 +111,10 @@ __device__ __forceinline__ uint4 load8_any(const __nv_bfloat16* base, int64_t e,
 __device__ __forceinline__ float sigmoid_f(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
 constexpr float kGeluU = 1.5957691216057308f;   // 2 sqrt(2 / pi)
 constexpr float kGeluA = 0.044715f;
+// From x^2 = 256 on gelu's slope is 0 or 1 to fp32's digits: the polynomial beside
+// q (1 - q) = 0 stays finite there.  (x q comes first, so that -x is not multiplied
+// by it either; a NaN comes through q.)
+constexpr float kGeluTop = 256.f;
 
 // FAST: tanh by the hardware approximation (error 2^-11), for results that are
 // rounded to bf16 (2^-9) next
@@ -139,7 +143,7 @@ __device__ __forceinline__ float act_slope(int act, float x) {
     }
     case PPO_ACT_GELU: {
       const float q = sigmoid_f(kGeluU * (x + kGeluA * x * x * x));
-      return q + x * q * (1.f - q) * kGeluU * (1.f + 3.f * kGeluA * x * x);
+      return q + x * q * (1.f - q) * kGeluU * (1.f + 3.f * kGeluA * fminf(x * x, kGeluTop));
     }
   }
   return 1.f;

@@ -98,3 +98,35 @@ def test_linear_forward_of_very_many_rows_and_few_columns(P, M, N, K, dtype):
     X, W = f64(x), f64(w)
     ry = X @ W.T + f64(b)
     within(y, ry, rounding(dtype, ry) + prod_bound(dtype, X, W.T, K) + 2 * U32 * (np.abs(ry) + np.abs(f64(b))), "y")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("act", ["tanh", "relu", "silu", "gelu"])
+@pytest.mark.parametrize("M,N,K", [(5, 40, 24), (300, 256, 264), (700, 640, 640)])
+def test_slopes_of_large_pre_activations(P, M, N, K, act, dtype):
+    """Finite values whose squares leave fp32's range: the slope is 0 or 1 there,
+    and a NaN stays in its element."""
+    import torch
+    rng = np.random.default_rng(M)
+    code = {"tanh": 0, "relu": 1, "silu": 2, "gelu": 3}[act]
+    dz, w = dev(rng.normal(size=(M, N)), dtype), dev(rng.normal(size=(N, K)) / np.sqrt(K), dtype)
+    pre = 1.5 * rng.normal(size=(M, K))
+    large = [16, 17, 40, 100, 1e4, 1e10, 1.5e19, 2e19, 1e20, 3e38]
+    for i, v in enumerate(large):
+        pre[i % M, 2 * i], pre[i % M, 2 * i + 1] = v, -v
+    pre[M - 1, K - 1] = np.nan
+    pre, dx = dev(pre, dtype), out((M, K), dtype)
+    work = torch.zeros(P.ppo_linear_workspace_bytes(M, N, K, tdt(dtype)), dtype=torch.uint8, device="cuda")
+    P.ppo_linear_backward_data(dz, w, dx, pre=pre, act=code, work=work)
+    P.ppo_work_status(work)
+    Z, W, X = f64(dz), f64(w), f64(pre)
+    rd = Z @ W
+    ref = rd * R.act_grad(act, np.where(np.isnan(X), 0.0, X))
+    bound = rounding(dtype, ref) + 1.2 * prod_bound(dtype, Z, W, N) + 64 * U32 * np.abs(rd) + 4 * U32 * np.abs(ref)
+    bound[M - 1, K - 1] = np.inf
+    got = f64(dx)
+    if act != "relu":
+        assert np.isnan(got[M - 1, K - 1])
+    got[M - 1, K - 1] = 0.0
+    bad = ~(np.abs(got - ref) <= bound)
+    assert not bad.any(), (X[bad], got[bad], ref[bad])
