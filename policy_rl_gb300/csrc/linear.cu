@@ -656,9 +656,16 @@ size_t sum_bytes(int64_t I, int64_t J, int64_t R, const TcPlan& plan) {
   return (size_t)(tc_sum_rows(g, plan) * I * 4 + 255) / 256 * 256;
 }
 
+// A bf16 result straight from the accumulator has the drift of its truncations,
+// 7.6e-8 of the sum's size a 16-deep step.  Sums past 2^16 (3e-4 there, a sixth of
+// bf16's half unit; measured 1.5e-3 at 2^18 and 6.3e-3 at 2^20) are therefore taken
+// out by windows and finished from partial products like split ones (2,048 x
+// 2^18 -> 2,048: 1,173 us from the accumulator, 1,356 so).
+bool long_sum(int64_t R) { return R > 1ll << 16; }
+
 cudaError_t tc_run(const Product& g, const Epilogue& e, char* work, int* err, cudaStream_t st) {
-  const TcPlan plan = tc_plan(g.I, g.J, g.R, false);
-  float* part = plan.splits > 1 ? reinterpret_cast<float*>(work) : nullptr;
+  const TcPlan plan = tc_plan(g.I, g.J, g.R, long_sum(g.R));
+  float* part = plan.splits > 1 || long_sum(g.R) ? reinterpret_cast<float*>(work) : nullptr;
   const cudaError_t x = tc_product(g, e, plan, part, nullptr, err, num_sms(), st);
   if (x != cudaSuccess || !part) return x;
   return launch_finish<__nv_bfloat16>(part, plan.splits, g.I, g.J, part_pitch(g.J), e, st);
@@ -789,10 +796,10 @@ size_t need(int32_t dtype, int mode, int64_t M, int64_t N, int64_t K, int64_t ld
   switch (mode) {
     case lin::kForward:
       return kCtrl + lin::packed_bytes(M, K, lda) + lin::packed_bytes(N, K, ldb) +
-             lin::tc_part_bytes(M, N, K, false);
+             lin::tc_part_bytes(M, N, K, lin::long_sum(K));
     case lin::kData:
       return kCtrl + lin::packed_bytes(M, N, lda) + lin::packed_bytes(N, K, ldb) +
-             lin::tc_part_bytes(M, K, N, false);
+             lin::tc_part_bytes(M, K, N, lin::long_sum(N));
   }
   return kCtrl + lin::packed_bytes(M, N, lda) + lin::packed_bytes(M, K, ldb) +
          std::max(lin::tc_sum_bytes(N, K, M, false) + lin::tc_part_bytes(N, K, M, false),

@@ -130,3 +130,32 @@ def test_slopes_of_large_pre_activations(P, M, N, K, act, dtype):
     got[M - 1, K - 1] = 0.0
     bad = ~(np.abs(got - ref) <= bound)
     assert not bad.any(), (X[bad], got[bad], ref[bad])
+
+
+@pytest.mark.parametrize("K", [1 << 18, 1 << 20])
+def test_bf16_products_of_very_long_sums(P, K):
+    """The tensor cores truncate what they add, which over positive terms is a
+    drift; rounding to nearest has none.  The mean relative error of many results
+    is below six standard errors of a bf16 rounding, (U16 / sqrt 3) / sqrt(count),
+    and what 32 truncated steps of a window and fp32 sums leave, 1e-5."""
+    import torch
+    M = N = 2048
+    g = torch.Generator(device="cuda")
+    g.manual_seed(K)
+    x = torch.rand(M, K, generator=g, device="cuda", dtype=torch.bfloat16)
+    w = torch.rand(N, K, generator=g, device="cuda", dtype=torch.bfloat16)
+    y, work = out((M, N), "bf16"), torch.zeros(P.ppo_linear_workspace_bytes(M, N, K, x.dtype), dtype=torch.uint8,
+                                               device="cuda")
+    rows = torch.arange(0, M, 32, device="cuda")
+    ref = sum(x[rows, k:k + 65536].double() @ w[rows, k:k + 65536].double().t() for k in range(0, K, 65536))
+    limit = 6 * U16 / np.sqrt(3 * ref.numel()) + 1e-5
+    P.ppo_linear_forward(x, w, y, work=work)
+    err = y[rows][:, rows].double() / ref - 1
+    assert abs(float(err.mean())) < limit, float(err.mean())
+    assert float(err.abs().max()) < 1.01 * U16
+    # the data gradient of [M][K] by [K][N] sums over K as well
+    wt = w.t().contiguous()
+    P.ppo_linear_backward_data(x, wt, y, work=work)
+    P.ppo_work_status(work)
+    err = y[rows][:, rows].double() / ref - 1
+    assert abs(float(err.mean())) < limit and float(err.abs().max()) < 1.01 * U16
