@@ -276,10 +276,12 @@ def _mat(t, like, shape, name):
     if t.is_contiguous():
         return t.data_ptr(), shape[-1]
     st = t.stride()
-    if (st[-1] != 1 and shape[-1] > 1) or st[-2] < shape[-1] or (
-            len(shape) == 3 and shape[0] > 1 and st[0] != shape[1] * st[1]):
+    # (one row of each of [T, 1, W]: the pitch is the distance of the first dimension)
+    pitch = st[0] if len(shape) == 3 and shape[1] == 1 else st[-2]
+    if (st[-1] != 1 and shape[-1] > 1) or pitch < shape[-1] or (
+            len(shape) == 3 and shape[0] > 1 and st[0] != shape[1] * pitch):
         raise ValueError(f"{name}: rows must be contiguous and of one pitch")
-    return t.data_ptr(), st[-2]
+    return t.data_ptr(), pitch
 
 
 def _vec(t, shape, name):

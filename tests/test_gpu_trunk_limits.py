@@ -159,3 +159,20 @@ def test_bf16_products_of_very_long_sums(P, K):
     P.ppo_work_status(work)
     err = y[rows][:, rows].double() / ref - 1
     assert abs(float(err.mean())) < limit and float(err.abs().max()) < 1.01 * U16
+
+
+def test_views_of_one_environment(P):
+    """[T, 1, W] slices of a rollout have one pitch and are taken as they lie."""
+    import torch
+    T, N, H = 150, 5, 40
+    rng = np.random.default_rng(3)
+    full, dfull = dev(rng.normal(size=(T, N, 2 * H)), "bf16"), dev(rng.normal(size=(T, N, H)), "bf16")
+    h, dp = torch.zeros(T, N, H, dtype=torch.bfloat16, device="cuda"), torch.zeros_like(full)
+    carry, want_h, want_dp = out((2, 1, H)), out((T, 1, H), "bf16"), out((T, 1, 2 * H), "bf16")
+    for n in (0, 2):
+        P.ppo_gated_scan_forward(full[:, n:n + 1].contiguous(), want_h, carry=carry)
+        P.ppo_gated_scan_forward(full[:, n:n + 1], h[:, n:n + 1], carry=carry)
+        P.ppo_gated_scan_backward(dfull[:, n:n + 1].contiguous(), full[:, n:n + 1].contiguous(), carry, want_dp)
+        P.ppo_gated_scan_backward(dfull[:, n:n + 1], full[:, n:n + 1], carry, dp[:, n:n + 1])
+        assert torch.equal(h[:, n:n + 1], want_h) and torch.equal(dp[:, n:n + 1], want_dp)
+    assert not h[:, [1, 3, 4]].any() and not dp[:, [1, 3, 4]].any()
