@@ -249,29 +249,33 @@ def _bind_torch():
     _raw_stream = raw or (lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
-def _dtype(t) -> int:
+def _kind(t):
+    """(dtype code, GPU index) of the argument that the others have to agree with."""
     if _F32 is None:
         _bind_torch()
     code = _DTYPES.get(t.dtype)
     if code is None:
         raise ValueError(f"dtype must be float32 or bfloat16, got {t.dtype}")
-    return code
+    gpu = t.get_device()
+    if gpu < 0:
+        raise ValueError(f"CUDA tensors are wanted, got one on {t.device}")
+    return code, gpu
 
 
-def _on(stream, t):
-    """The stream's handle: the given one, or the current one of t's device."""
+def _on(stream, gpu):
+    """The stream's handle: the given one, or the current one of the GPU."""
     if stream is None:
-        return _raw_stream(t.get_device())
+        return _raw_stream(gpu)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _mat(t, like, shape, name):
-    """(address, row pitch) of a matrix argument of like's dtype: the last
-    dimension is a row, the others flatten to rows of one pitch."""
+def _mat(t, dtype, gpu, shape, name):
+    """(address, row pitch) of a matrix argument: the last dimension is a row,
+    the others flatten to rows of one pitch."""
     if t is None:
         return None, 0
-    if t.dtype is not like.dtype or t.shape != shape or not t.is_cuda:
-        raise ValueError(f"{name}: a CUDA tensor {tuple(shape)} of {like.dtype} is wanted, got "
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != gpu:
+        raise ValueError(f"{name}: a tensor {tuple(shape)} of {dtype} on cuda:{gpu} is wanted, got "
                          f"{tuple(t.shape)} of {t.dtype} on {t.device}")
     if t.is_contiguous():
         return t.data_ptr(), shape[-1]
@@ -284,23 +288,23 @@ def _mat(t, like, shape, name):
     return t.data_ptr(), pitch
 
 
-def _vec(t, shape, name):
+def _vec(t, gpu, shape, name):
     """Address of a contiguous fp32 argument."""
     if t is None:
         return None
-    if t.dtype is not _F32 or t.shape != shape or not t.is_cuda:
-        raise ValueError(f"{name}: a CUDA tensor {tuple(shape)} of float32 is wanted, got "
+    if t.dtype is not _F32 or t.shape != shape or t.get_device() != gpu:
+        raise ValueError(f"{name}: a tensor {tuple(shape)} of float32 on cuda:{gpu} is wanted, got "
                          f"{tuple(t.shape)} of {t.dtype} on {t.device}")
     if not t.is_contiguous():
         raise ValueError(f"{name}: tensor must be contiguous")
     return t.data_ptr()
 
 
-def _work_of(work):
+def _work_of(work, gpu):
     if work is None:
         return None, 0
-    if not work.is_cuda or not work.is_contiguous():
-        raise ValueError("work: a contiguous CUDA tensor is wanted")
+    if work.get_device() != gpu or not work.is_contiguous():
+        raise ValueError(f"work: a contiguous tensor on cuda:{gpu} is wanted")
     return work.data_ptr(), work.nbytes
 
 
@@ -312,13 +316,14 @@ def _check(status: int, what: str) -> None:
 def ppo_layernorm_forward(x, gamma, beta, y, stats=None, eps=1e-5, stream=None) -> None:
     """y = layer norm of the rows of x [M, D] (see ppo.h); gamma, beta fp32 [D]
     or None; stats fp32 [M, 2], kept for the backward pass."""
-    code = _dtype(x)
+    code, gpu = _kind(x)
+    dt = x.dtype
     M, D = shape = x.shape
-    px, ldx = _mat(x, x, shape, "x")
-    py, ldy = _mat(y, x, shape, "y")
+    px, ldx = _mat(x, dt, gpu, shape, "x")
+    py, ldy = _mat(y, dt, gpu, shape, "y")
     _check(_lib().ppo_layernorm_forward(
-        code, px, ldx, M, D, _vec(gamma, (D,), "gamma"), _vec(beta, (D,), "beta"), eps, py,
-        ldy, _vec(stats, (M, 2), "stats"), _on(stream, x)), "ppo_layernorm_forward")
+        code, px, ldx, M, D, _vec(gamma, gpu, (D,), "gamma"), _vec(beta, gpu, (D,), "beta"), eps, py,
+        ldy, _vec(stats, gpu, (M, 2), "stats"), _on(stream, gpu)), "ppo_layernorm_forward")
 
 
 def ppo_layernorm_backward_workspace_bytes(M: int, D: int) -> int:
@@ -331,17 +336,18 @@ def ppo_layernorm_backward_workspace_bytes(M: int, D: int) -> int:
 def ppo_layernorm_backward(dy, x, gamma, stats, dx, dgamma=None, dbeta=None, dres=None, work=None,
                            stream=None) -> None:
     """dx (+ dres, the residual path's gradient), dgamma, dbeta of the layer norm (see ppo.h)."""
-    code = _dtype(x)
+    code, gpu = _kind(x)
+    dt = x.dtype
     M, D = shape = x.shape
-    px, ldx = _mat(x, x, shape, "x")
-    pdy, lddy = _mat(dy, x, shape, "dy")
-    pr, ldr = _mat(dres, x, shape, "dres")
-    pdx, lddx = _mat(dx, x, shape, "dx")
-    pw, wb = _work_of(work)
+    px, ldx = _mat(x, dt, gpu, shape, "x")
+    pdy, lddy = _mat(dy, dt, gpu, shape, "dy")
+    pr, ldr = _mat(dres, dt, gpu, shape, "dres")
+    pdx, lddx = _mat(dx, dt, gpu, shape, "dx")
+    pw, wb = _work_of(work, gpu)
     _check(_lib().ppo_layernorm_backward(
-        code, pdy, lddy, px, ldx, M, D, _vec(gamma, (D,), "gamma"),
-        _vec(stats, (M, 2), "stats"), pr, ldr, pdx, lddx, _vec(dgamma, (D,), "dgamma"),
-        _vec(dbeta, (D,), "dbeta"), pw, wb, _on(stream, x)), "ppo_layernorm_backward")
+        code, pdy, lddy, px, ldx, M, D, _vec(gamma, gpu, (D,), "gamma"),
+        _vec(stats, gpu, (M, 2), "stats"), pr, ldr, pdx, lddx, _vec(dgamma, gpu, (D,), "dgamma"),
+        _vec(dbeta, gpu, (D,), "dbeta"), pw, wb, _on(stream, gpu)), "ppo_layernorm_backward")
 
 
 def ppo_scan_blocks(T: int) -> int:
@@ -354,29 +360,31 @@ def ppo_gated_scan_forward(p, h, h0=None, done=None, done0=None, hT=None, carry=
     """h [T, N, H] from the pre-activations p [T, N, 2H] (see ppo.h); h0, hT
     fp32 [N, H], done fp32 [T, N], done0 fp32 [N], carry fp32
     [ppo_scan_blocks(T), N, H].  hT may be h0."""
-    code = _dtype(h)
+    code, gpu = _kind(h)
+    dt = h.dtype
     T, N, H = shape = h.shape
-    pp, ldp = _mat(p, h, (T, N, 2 * H), "p")
-    ph, ldh = _mat(h, h, shape, "h")
+    pp, ldp = _mat(p, dt, gpu, (T, N, 2 * H), "p")
+    ph, ldh = _mat(h, dt, gpu, shape, "h")
     _check(_lib().ppo_gated_scan_forward(
-        code, pp, ldp, _vec(done, (T, N), "done"), _vec(done0, (N,), "done0"),
-        _vec(h0, (N, H), "h0"), T, N, H, ph, ldh, _vec(hT, (N, H), "hT"),
-        _vec(carry, (ppo_scan_blocks(T), N, H), "carry"), _on(stream, h)),
+        code, pp, ldp, _vec(done, gpu, (T, N), "done"), _vec(done0, gpu, (N,), "done0"),
+        _vec(h0, gpu, (N, H), "h0"), T, N, H, ph, ldh, _vec(hT, gpu, (N, H), "hT"),
+        _vec(carry, gpu, (ppo_scan_blocks(T), N, H), "carry"), _on(stream, gpu)),
         "ppo_gated_scan_forward")
 
 
 def ppo_gated_scan_backward(dh, p, carry, dp, done=None, done0=None, dhT=None, dh0=None,
                             stream=None) -> None:
     """dp [T, N, 2H] and dh0 from dh [T, N, H] and dhT (see ppo.h)."""
-    code = _dtype(dh)
+    code, gpu = _kind(dh)
+    dt = dh.dtype
     T, N, H = shape = dh.shape
-    pd, ldd = _mat(dh, dh, shape, "dh")
-    pp, ldp = _mat(p, dh, (T, N, 2 * H), "p")
-    po, ldo = _mat(dp, dh, (T, N, 2 * H), "dp")
+    pd, ldd = _mat(dh, dt, gpu, shape, "dh")
+    pp, ldp = _mat(p, dt, gpu, (T, N, 2 * H), "p")
+    po, ldo = _mat(dp, dt, gpu, (T, N, 2 * H), "dp")
     _check(_lib().ppo_gated_scan_backward(
-        code, pd, ldd, pp, ldp, _vec(done, (T, N), "done"), _vec(done0, (N,), "done0"),
-        _vec(carry, (ppo_scan_blocks(T), N, H), "carry"), _vec(dhT, (N, H), "dhT"), T, N, H, po,
-        ldo, _vec(dh0, (N, H), "dh0"), _on(stream, dh)), "ppo_gated_scan_backward")
+        code, pd, ldd, pp, ldp, _vec(done, gpu, (T, N), "done"), _vec(done0, gpu, (N,), "done0"),
+        _vec(carry, gpu, (ppo_scan_blocks(T), N, H), "carry"), _vec(dhT, gpu, (N, H), "dhT"), T, N, H, po,
+        ldo, _vec(dh0, gpu, (N, H), "dh0"), _on(stream, gpu)), "ppo_gated_scan_backward")
 
 
 def ppo_linear_workspace_bytes(M: int, N: int, K: int, dtype, ldx: int = 0, ldw: int = 0,
@@ -396,51 +404,54 @@ def ppo_linear_forward(x, w, y, bias=None, act=_abi.ACT_NONE, res=None, pre=None
                        stream=None) -> None:
     """y [M, N] = act(x w^T + bias) + res, x [M, K], w [N, K], bias fp32 [N];
     pre [M, N] takes the pre-activation (see ppo.h)."""
-    code = _dtype(x)
+    code, gpu = _kind(x)
+    dt = x.dtype
     M, K = x.shape
     N = w.shape[0]
-    px, ldx = _mat(x, x, (M, K), "x")
-    pw, ldw = _mat(w, x, (N, K), "w")
-    pr, ldr = _mat(res, x, (M, N), "res")
-    py, ldy = _mat(y, x, (M, N), "y")
-    pp, ldp = _mat(pre, x, (M, N), "pre")
-    pk, wb = _work_of(work)
+    px, ldx = _mat(x, dt, gpu, (M, K), "x")
+    pw, ldw = _mat(w, dt, gpu, (N, K), "w")
+    pr, ldr = _mat(res, dt, gpu, (M, N), "res")
+    py, ldy = _mat(y, dt, gpu, (M, N), "y")
+    pp, ldp = _mat(pre, dt, gpu, (M, N), "pre")
+    pk, wb = _work_of(work, gpu)
     _check(_lib().ppo_linear_forward(
-        code, px, ldx, pw, ldw, _vec(bias, (N,), "bias"), act, pr, ldr, M, N, K, py, ldy, pp,
-        ldp, pk, wb, _on(stream, x)), "ppo_linear_forward")
+        code, px, ldx, pw, ldw, _vec(bias, gpu, (N,), "bias"), act, pr, ldr, M, N, K, py, ldy, pp,
+        ldp, pk, wb, _on(stream, gpu)), "ppo_linear_forward")
 
 
 def ppo_linear_backward_data(dz, w, dx, pre=None, act=_abi.ACT_NONE, res=None, work=None,
                              stream=None) -> None:
     """dx [M, K] = (dz w) * act'(pre) + res; pre [M, K] is the pre-activation
     that the layer's input came from (see ppo.h)."""
-    code = _dtype(dz)
+    code, gpu = _kind(dz)
+    dt = dz.dtype
     M, N = dz.shape
     K = w.shape[1]
-    pd, ldd = _mat(dz, dz, (M, N), "dz")
-    pw, ldw = _mat(w, dz, (N, K), "w")
-    pp, ldp = _mat(pre, dz, (M, K), "pre")
-    pr, ldr = _mat(res, dz, (M, K), "res")
-    po, ldo = _mat(dx, dz, (M, K), "dx")
-    pk, wb = _work_of(work)
+    pd, ldd = _mat(dz, dt, gpu, (M, N), "dz")
+    pw, ldw = _mat(w, dt, gpu, (N, K), "w")
+    pp, ldp = _mat(pre, dt, gpu, (M, K), "pre")
+    pr, ldr = _mat(res, dt, gpu, (M, K), "res")
+    po, ldo = _mat(dx, dt, gpu, (M, K), "dx")
+    pk, wb = _work_of(work, gpu)
     _check(_lib().ppo_linear_backward_data(
         code, pd, ldd, pw, ldw, pp, ldp, act, pr, ldr, M, N, K, po, ldo, pk, wb,
-        _on(stream, dz)), "ppo_linear_backward_data")
+        _on(stream, gpu)), "ppo_linear_backward_data")
 
 
 def ppo_linear_backward_weight(dz, x, dw, db=None, accumulate=False, work=None,
                                stream=None) -> None:
     """dw fp32 [N, K] = dz^T x and db fp32 [N] = column sums of dz, or their
     sums with what dw and db hold (see ppo.h)."""
-    code = _dtype(dz)
+    code, gpu = _kind(dz)
+    dt = dz.dtype
     M, N = dz.shape
     K = x.shape[1]
-    pd, ldd = _mat(dz, dz, (M, N), "dz")
-    px, ldx = _mat(x, dz, (M, K), "x")
-    pk, wb = _work_of(work)
+    pd, ldd = _mat(dz, dt, gpu, (M, N), "dz")
+    px, ldx = _mat(x, dt, gpu, (M, K), "x")
+    pk, wb = _work_of(work, gpu)
     _check(_lib().ppo_linear_backward_weight(
-        code, pd, ldd, px, ldx, M, N, K, _vec(dw, (N, K), "dw"), _vec(db, (N,), "db"),
-        1 if accumulate else 0, pk, wb, _on(stream, dz)), "ppo_linear_backward_weight")
+        code, pd, ldd, px, ldx, M, N, K, _vec(dw, gpu, (N, K), "dw"), _vec(db, gpu, (N,), "db"),
+        1 if accumulate else 0, pk, wb, _on(stream, gpu)), "ppo_linear_backward_weight")
 
 
 def ppo_work_status(work, stream=None) -> None:

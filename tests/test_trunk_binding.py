@@ -9,10 +9,10 @@ from policy_rl_gb300 import _abi
 
 
 class OnGpu:
-    """A CPU tensor that claims to be on GPU `index`."""
+    """A CPU tensor that claims to be on GPU `index` (-1: on the CPU)."""
 
     def __init__(self, t, index=0):
-        self.t, self.index, self.is_cuda, self.device = t, index, True, f"cuda:{index}"
+        self.t, self.index, self.is_cuda, self.device = t, index, index >= 0, f"cuda:{index}"
 
     def get_device(self):
         return self.index
@@ -66,3 +66,36 @@ def test_views_without_one_pitch_are_refused(lib):
         with pytest.raises(ValueError):
             P.ppo_gated_scan_forward(zeros(*bad.shape[:2], 2 * bad.shape[2]), h)
     assert not lib.calls
+
+
+def calls():
+    """Every operator with every tensor argument: (call, names), arguments by name."""
+    T, N, H, M, D = 3, 2, 4, 6, 8
+    m = lambda *s: dict(shape=s)
+    return {
+        "ppo_layernorm_forward": (dict(x=m(M, D), gamma=m(D), beta=m(D), y=m(M, D), stats=m(M, 2)), {}),
+        "ppo_layernorm_backward": (dict(dy=m(M, D), x=m(M, D), gamma=m(D), stats=m(M, 2), dx=m(M, D), dgamma=m(D),
+                                        dbeta=m(D), dres=m(M, D), work=m(64)), {}),
+        "ppo_gated_scan_forward": (dict(p=m(T, N, 2 * H), h=m(T, N, H), h0=m(N, H), done=m(T, N), done0=m(N),
+                                        hT=m(N, H), carry=m(1, N, H)), {}),
+        "ppo_gated_scan_backward": (dict(dh=m(T, N, H), p=m(T, N, 2 * H), carry=m(1, N, H), dp=m(T, N, 2 * H),
+                                         done=m(T, N), done0=m(N), dhT=m(N, H), dh0=m(N, H)), {}),
+        "ppo_linear_forward": (dict(x=m(M, D), w=m(5, D), y=m(M, 5), bias=m(5), res=m(M, 5), pre=m(M, 5),
+                                    work=m(64)), {}),
+        "ppo_linear_backward_data": (dict(dz=m(M, 5), w=m(5, D), dx=m(M, D), pre=m(M, D), res=m(M, D), work=m(64)),
+                                     dict(act=3)),
+        "ppo_linear_backward_weight": (dict(dz=m(M, 5), x=m(M, D), dw=m(5, D), db=m(5), work=m(64)), {}),
+    }
+
+
+@pytest.mark.parametrize("name", list(calls()))
+def test_tensors_of_two_devices_are_refused(lib, name):
+    tensors, other = calls()[name]
+    given = {k: zeros(*v["shape"], index=1) for k, v in tensors.items()}
+    getattr(P, name)(**given, **other)          # all on one GPU, whichever
+    assert len(lib.calls) == 1
+    for k, v in tensors.items():
+        for index in (0, -1):
+            with pytest.raises(ValueError):
+                getattr(P, name)(**{**given, k: zeros(*v["shape"], index=index)}, **other)
+    assert len(lib.calls) == 1
