@@ -238,15 +238,17 @@ class RnnContext:
 _F32 = None        # torch.float32 (torch is imported by the caller's tensors)
 _DTYPES: dict = {}
 _raw_stream = None
+_current_gpu = None
 
 
 def _bind_torch():
-    global _F32, _raw_stream
+    global _F32, _raw_stream, _current_gpu
     import torch
     _F32 = torch.float32
     _DTYPES.update({torch.float32: _abi.DTYPE_F32, torch.bfloat16: _abi.DTYPE_BF16})
     raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
     _raw_stream = raw or (lambda device: torch.cuda.current_stream(device).cuda_stream)
+    _current_gpu = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _kind(t):
@@ -259,6 +261,8 @@ def _kind(t):
     gpu = t.get_device()
     if gpu < 0:
         raise ValueError(f"CUDA tensors are wanted, got one on {t.device}")
+    if gpu != _current_gpu():
+        raise ValueError(f"tensors are on cuda:{gpu}, the current device is cuda:{_current_gpu()}")
     return code, gpu
 
 

@@ -23,7 +23,7 @@ class OnGpu:
 
 class Recorder:
     def __init__(self):
-        self.calls = []
+        self.calls, self.gpu = [], 0
 
     def __getattr__(self, name):
         def call(*args):
@@ -38,6 +38,7 @@ def lib(monkeypatch):
     monkeypatch.setattr(_abi, "_lib", r)
     P._bind_torch()
     monkeypatch.setattr(P, "_raw_stream", lambda device: 0)
+    monkeypatch.setattr(P, "_current_gpu", lambda: r.gpu)
     return r
 
 
@@ -92,6 +93,7 @@ def calls():
 def test_tensors_of_two_devices_are_refused(lib, name):
     tensors, other = calls()[name]
     given = {k: zeros(*v["shape"], index=1) for k, v in tensors.items()}
+    lib.gpu = 1
     getattr(P, name)(**given, **other)          # all on one GPU, whichever
     assert len(lib.calls) == 1
     for k, v in tensors.items():
@@ -99,3 +101,13 @@ def test_tensors_of_two_devices_are_refused(lib, name):
             with pytest.raises(ValueError):
                 getattr(P, name)(**{**given, k: zeros(*v["shape"], index=index)}, **other)
     assert len(lib.calls) == 1
+
+
+@pytest.mark.parametrize("name", list(calls()))
+def test_another_device_than_the_current_one_is_refused(lib, name):
+    """A launch goes to the current device: its kernel cannot read the other's memory."""
+    tensors, other = calls()[name]
+    lib.gpu = 0
+    with pytest.raises(ValueError):
+        getattr(P, name)(**{k: zeros(*v["shape"], index=1) for k, v in tensors.items()}, **other)
+    assert not lib.calls
