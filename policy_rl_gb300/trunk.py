@@ -69,8 +69,11 @@ class RecurrentTrunk:
         self._one = dict(n=torch.empty(N, D, **own), p=torch.empty(1, N, 2 * H, **own),
                          h=torch.empty(1, N, H, **own), xm=torch.empty(N, D, **own),
                          a=torch.empty(N, F, **own), y=torch.empty(N, D, **own))
-        sizes = [(r, rows, cols) for r in (M, N) for rows, cols in shapes.values()]
-        need = max(ppo_linear_workspace_bytes(r, rows, cols, self.dtype) for r, rows, cols in sizes)
+        # (dy, W2's dz, may come in rows of any pitch: an odd one asks for most)
+        sizes = [(r, rows, cols, D | 1 if name == "W2" else 0) for r in (M, N)
+                 for name, (rows, cols) in shapes.items()]
+        need = max(ppo_linear_workspace_bytes(r, rows, cols, self.dtype, ldz=ldz)
+                   for r, rows, cols, ldz in sizes)
         self._work = torch.zeros(need, dtype=torch.uint8, device=device)
         self._ln_work = torch.empty(ppo_layernorm_backward_workspace_bytes(M, D), dtype=torch.uint8,
                                     device=device)

@@ -176,3 +176,20 @@ def test_views_of_one_environment(P):
         P.ppo_gated_scan_backward(dfull[:, n:n + 1], full[:, n:n + 1], carry, dp[:, n:n + 1])
         assert torch.equal(h[:, n:n + 1], want_h) and torch.equal(dp[:, n:n + 1], want_dp)
     assert not h[:, [1, 3, 4]].any() and not dp[:, [1, 3, 4]].any()
+
+
+def test_trunk_takes_gradients_of_odd_pitch(P):
+    """dy as columns of a wider buffer (logits beside a value), against 64-bit
+    autograd with the bound of test_trunk_in_bf16.  (Not bit for bit what rows of
+    even pitch give: layer norm sums rows of unequal pitches in another order.)"""
+    import torch
+    from test_gpu_trunk import build, reference, run
+    t, made = build(20, 6, 64, 32, 96, torch.bfloat16)
+    ref = reference(t, made)
+    wide = torch.zeros(20, 6, 65, dtype=torch.bfloat16, device="cuda")
+    wide[..., :64] = made["dy"]
+    made["dy"] = wide[..., :64]
+    got = run(t, made)
+    for k, r in ref.items():
+        err = float((got[k].double() - r).norm() / r.norm())
+        assert err <= 3e-2, (k, err)
