@@ -9,7 +9,9 @@ A block takes the residual stream x [T, N, D] of a rollout through a gated scan
 RecurrentTrunk holds the parameters, what the forward pass leaves for the
 backward pass, and the workspaces, all allocated once: forward() and backward()
 run whole rollouts, step() advances carried states by one acting step.  None of
-them allocates or synchronises, so each can be captured in a CUDA graph.
+them allocates or synchronises, so each can be captured in a CUDA graph, and
+step() shares only the parameters with the other two, so that it may run on a
+stream of its own between two load_params().
 """
 import math
 
@@ -69,12 +71,14 @@ class RecurrentTrunk:
         self._one = dict(n=torch.empty(N, D, **own), p=torch.empty(1, N, 2 * H, **own),
                          h=torch.empty(1, N, H, **own), xm=torch.empty(N, D, **own),
                          a=torch.empty(N, F, **own), y=torch.empty(N, D, **own))
-        # (dy, W2's dz, may come in rows of any pitch: an odd one asks for most)
-        sizes = [(r, rows, cols, D | 1 if name == "W2" else 0) for r in (M, N)
-                 for name, (rows, cols) in shapes.items()]
-        need = max(ppo_linear_workspace_bytes(r, rows, cols, self.dtype, ldz=ldz)
-                   for r, rows, cols, ldz in sizes)
-        self._work = torch.zeros(need, dtype=torch.uint8, device=device)
+        # acting may run on another stream than learning: a workspace each.  (dy, W2's
+        # dz, may come in rows of any pitch: an odd one asks for most.)
+        def workspace(rows):
+            need = max(ppo_linear_workspace_bytes(rows, r, c, self.dtype, ldz=D | 1 if name == "W2" else 0)
+                       for name, (r, c) in shapes.items())
+            return torch.zeros(need, dtype=torch.uint8, device=device)
+
+        self._work, self._act_work = workspace(M), workspace(N)
         self._ln_work = torch.empty(ppo_layernorm_backward_workspace_bytes(M, D), dtype=torch.uint8,
                                     device=device)
         self._in = None
@@ -146,7 +150,7 @@ class RecurrentTrunk:
         """One acting step: the output [N, D] for x [N, D], the states [blocks, N,
         H] advanced in place (cleared first where done [N] is not 0).  The
         result is the trunk's own buffer."""
-        P, W, o, work, st = self.params, self._w, self._one, self._work, stream
+        P, W, o, work, st = self.params, self._w, self._one, self._act_work, stream
         for b in range(self.blocks):
             ppo_layernorm_forward(x, P[b, "g1"], P[b, "c1"], o["n"], None, self.eps, st)
             ppo_linear_forward(o["n"], W[b, "Wp"], o["p"][0], P[b, "bp"], work=work, stream=st)
@@ -159,5 +163,13 @@ class RecurrentTrunk:
         return x
 
     def check(self, stream=None):
-        """Synchronises; raises PpoError if a bounded device wait gave up."""
-        ppo_work_status(self._work, stream)
+        """Synchronises the stream; raises PpoError if a bounded device wait of
+        learning or acting gave up (on another stream: wait for that one first)."""
+        failed = []
+        for work in (self._work, self._act_work):
+            try:
+                ppo_work_status(work, stream)
+            except RuntimeError as e:
+                failed.append(e)
+        if failed:
+            raise failed[0]
