@@ -193,3 +193,123 @@ def test_trunk_takes_gradients_of_odd_pitch(P):
     for k, r in ref.items():
         err = float((got[k].double() - r).norm() / r.norm())
         assert err <= 3e-2, (k, err)
+
+
+# ---- variants that only large problems reach ---------------------------------------
+@pytest.mark.parametrize("act,pact,res,dres,pre,K,pitch", [
+    ("relu", "relu", False, False, False, 1000, None),
+    ("none", "none", False, True, False, 1000, None),
+    ("relu", "none", True, False, False, 1032, None),
+    ("none", "relu", True, True, False, 1032, None),
+    ("gelu", "silu", True, True, True, 1000, None),
+    ("relu", "relu", False, False, False, 997, (999, 1001, 1003)),
+    ("none", "none", True, True, False, 1031, (1033, 1035, 1001)),
+    ("gelu", "relu", True, True, True, 997, (1001, 997, 1007))])
+def test_linear_with_many_tiles_a_pair(P, act, pact, res, dres, pre, K, pitch):
+    """308 tiles of 256 x 256 forward (and 308 or 385 backward): four and more for each
+    pair of CTAs, each epilogue with its boxes moved by TMA or, of odd pitch, by hand."""
+    check_linear(P, 19500, 1000, K, "bf16", act=act, pact=pact, res=res, dres=dres, pre=pre, pitch=pitch, seed=K)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,N,H", [(140, 1217, 128), (135, 1207, 129), (300, 2440, 64)])
+def test_scan_walked_by_warps_over_many_tiles(P, T, N, H, dtype):
+    """More than 155,648 channels: forward, each warp walks its channels alone and
+    leaves the carry of every 128th step, which the backward pass starts from."""
+    import torch
+    g = torch.Generator(device="cuda")
+    g.manual_seed(T)
+    rn = lambda *s: torch.randn(*s, generator=g, device="cuda")
+    p = (1.5 * rn(T, N, 2 * H) - 0.5).to(tdt(dtype))
+    done, done0 = (rn(T, N) > 1.6).float(), (rn(N) > 0.5).float()
+    h0, dh, dhT = rn(N, H), rn(T, N, H).to(tdt(dtype)), rn(N, H)
+    h, hT, carry = out((T, N, H), dtype), out((N, H)), out((P.ppo_scan_blocks(T), N, H))
+    dp, dh0 = out((T, N, 2 * H), dtype), out((N, H))
+    P.ppo_gated_scan_forward(p, h, h0=h0, done=done, done0=done0, hT=hT, carry=carry)
+    P.ppo_gated_scan_backward(dh, p, carry, dp, done=done, done0=done0, dhT=dhT, dh0=dh0)
+    # step by step in 64 bits, on the device
+    state, ent, S = h0.double(), [], 0.0
+    for t in range(T):
+        state = torch.where((done0 if t == 0 else done[t - 1])[:, None] != 0, 0.0, state)
+        ent.append(state)
+        S = max(S, float(state.abs().max()), float(p[t, :, H:].abs().max()))
+        if t % 128 == 0:
+            assert float((carry[t // 128].double() - state).abs().max()) <= 1e-5 * S
+        z = torch.sigmoid(p[t, :, :H].double())
+        state = (1 - z) * state + z * p[t, :, H:].double()
+        lost = 2 * U16 * state.abs() if dtype == "bf16" else 0.0
+        assert bool(((h[t].double() - state).abs() <= lost + 1e-5 * max(S, float(state.abs().max()))).all()), t
+    assert float((hT.double() - state).abs().max()) <= 1e-5 * S
+    u, G = dhT.double(), 0.0
+    for t in range(T - 1, -1, -1):
+        z, c = torch.sigmoid(p[t, :, :H].double()), p[t, :, H:].double()
+        q = dh[t].double() + u
+        G = max(G, float(q.abs().max()))
+        want = torch.cat([q * (c - ent[t]) * z * (1 - z), q * z], 1)
+        lost = 2 * U16 * want.abs() if dtype == "bf16" else 0.0
+        assert bool(((dp[t].double() - want).abs() <= lost + 1e-5 * G * (1 + 2 * S)).all()), t
+        u = torch.where((done0 if t == 0 else done[t - 1])[:, None] != 0, 0.0, (1 - z) * q)
+    assert float((dh0.double() - u).abs().max()) <= 1e-5 * G
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("M,D", [(1000, 513), (3001, 33), (700, 1397), (500, 4101), (330, 8201)])
+def test_layernorm_in_place_of_odd_widths(P, M, D, dtype):
+    """Aligned pieces reach into the rows beside: in place, rows that other blocks write."""
+    import torch
+    _, x, ga, be = ln_inputs(M, D, dtype, 5)
+    y, st = torch.empty_like(x), out((M, 2))
+    P.ppo_layernorm_forward(x, ga, be, y, stats=st)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(D)
+    dy, dres = (torch.randn(M, D, generator=g, device="cuda").to(x.dtype) for _ in range(2))
+    dx, dxr = torch.empty_like(x), torch.empty_like(x)
+    P.ppo_layernorm_backward(dy, x, ga, st, dx)
+    P.ppo_layernorm_backward(dy, x, ga, st, dxr, dres=dres)
+    for _ in range(5):
+        a, b, c, d = x.clone(), dy.clone(), dy.clone(), dres.clone()
+        P.ppo_layernorm_forward(a, ga, be, a)
+        P.ppo_layernorm_backward(b, x, ga, st, b)
+        P.ppo_layernorm_backward(c, x, ga, st, c, dres=dres)
+        P.ppo_layernorm_backward(dy, x, ga, st, d, dres=d)
+        assert torch.equal(a, y) and torch.equal(b, dx) and torch.equal(c, dxr) and torch.equal(d, dxr)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("M,D,pitch", [(700, 8200, None), (310, 16393, None), (1000, 4099, 4101)])
+def test_layernorm_of_long_rows_several_a_block(P, M, D, pitch, dtype):
+    """Rows that are read once per reduction; a block adds up several rows' parameter
+    gradients in its partial row."""
+    check_ln(P, M, D, dtype, pitch=pitch, seed=M)
+    check_ln(P, M, D, dtype, pitch=pitch, res=False, seed=M)
+
+
+def test_layernorm_past_32_bit_offsets_against_the_reference(P):
+    import torch
+    M, D = 540000, 4096                     # 2.2e9 elements
+    rows = torch.tensor([0, 1, M // 2, M - 2, M - 1], device="cuda")
+    x, dy = (torch.zeros(M, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    x[rows] = torch.randn(5, D, generator=g, device="cuda").to(torch.bfloat16)
+    dy[rows] = torch.randn(5, D, generator=g, device="cuda").to(torch.bfloat16)
+    ga, be = 1 + 0.2 * torch.randn(D, generator=g, device="cuda"), torch.randn(D, generator=g, device="cuda")
+    X, Z, st, dg, db = f64(x[rows]), f64(dy[rows]), out((M, 2)), out((D,)), out((D,))
+    work = out((P.ppo_layernorm_backward_workspace_bytes(M, D) // 4,))
+    y = torch.empty_like(x)
+    P.ppo_layernorm_forward(x, ga, be, y, stats=st)
+    P.ppo_layernorm_backward(dy, x, ga, st, dy, dgamma=dg, dbeta=db, work=work)      # in place
+    ry, mean, rstd = R.layernorm(X, f64(ga), f64(be), 1e-5)
+    rdx, rdg, rdb = R.layernorm_grad(Z, X, f64(ga), mean, rstd)
+    # as in check_ln: a row's values relative to its deviation are off by `lost`
+    lost = 16 * U32 * (np.sqrt(D) + 8) * (np.abs(X).mean(1) * rstd + 1)[:, None]
+    within(y[rows], ry, 2 * U16 * np.abs(ry) + lost * (np.abs(ry) + np.abs(f64(ga)) + np.abs(f64(be))), "y")
+    xh, q = np.abs((X - mean[:, None]) * rstd[:, None]), np.abs(Z * f64(ga))
+    size = rstd[:, None] * (q + q.mean(1, keepdims=True) + (xh + 1) * (q * (xh + 1)).mean(1, keepdims=True))
+    within(dy[rows], rdx, 2 * U16 * np.abs(rdx) + 2 * lost * (size + np.abs(rdx)), "dx")
+    n = 8 * U32 * (np.sqrt(5) + 8)
+    within(dg, rdg, n * (np.abs(Z) * xh).sum(0) + (np.abs(Z) * lost * (xh + 1)).sum(0), "dgamma")
+    within(db, rdb, n * np.abs(Z).sum(0), "dbeta")
+    want = be.to(torch.bfloat16)
+    assert bool((y[2:M // 2] == want).all()) and not bool(dy[2:M // 2].any())
+    assert bool((y[M // 2 + 1:M - 2] == want).all()) and not bool(dy[M // 2 + 1:M - 2].any())
