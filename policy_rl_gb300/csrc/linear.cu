@@ -102,18 +102,60 @@ __device__ __forceinline__ void finish4(const Epilogue& e, const Beside& x, floa
   put4<T>(e.out, i * e.ldo + j, n, vec, v);
 }
 
-// An fp32 product straight from its operands.  (The planes of an infinity, or of
-// what rounds to one in bf16, do not add up: their products hold NaN where the
-// product may not.)  NaN operands, whose sums are NaN from there on, stop early.
-__device__ __noinline__ float sum_again(const float* a, int64_t step, int64_t R) {
-  float v = 0.f;
-  for (int64_t r = 0; r < R && v == v; ++r) v += a[r * step];
-  return v;
+// Of a product of planes: where the sum of an element's parts is not finite, each part
+// that is not either is computed again, straight from the fp32 operands.  (The planes of
+// an infinity, or of what rounds to one in bf16, do not add up: their products hold NaN
+// where the product may not.)  Eight steps' loads are in flight: an infinity among
+// 1,000,000 rows of a weight gradient takes 18 ms, 2 s a step at a time over the
+// whole sum.  A part that has become NaN ends early.
+struct Again {
+  Product g;              // the fp32 operands
+  const float* part;
+  int64_t pitch;          // of the parts
+  int splits;
+  int64_t r_per_split;
+};
+__device__ __noinline__ float dot_again(const Again* __restrict__ p, int64_t i, int64_t j, int64_t at) {
+  constexpr int U = 8;
+  const int64_t sar = p->g.sar, sbr = p->g.sbr;
+  float sum = 0.f;
+  for (int s = 0; s < p->splits; ++s) {
+    float v = __ldcg(p->part + s * p->pitch + at);
+    if (!isfinite(v)) {
+      v = 0.f;
+      const int64_t r0 = s * p->r_per_split;
+      const float* a = static_cast<const float*>(p->g.A) + i * p->g.sai + r0 * sar;
+      const float* b = static_cast<const float*>(p->g.B) + j * p->g.sbj + r0 * sbr;
+      int64_t n = min(p->g.R - r0, p->r_per_split);
+      for (; n >= U && v == v; n -= U) {
+        float x[U], y[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u, a += sar, b += sbr) {
+          x[u] = __ldg(a);
+          y[u] = __ldg(b);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) v = fmaf(x[u], y[u], v);
+      }
+      for (; n > 0 && v == v; --n, a += sar, b += sbr) v = fmaf(__ldg(a), __ldg(b), v);
+    }
+    sum += v;
+  }
+  return sum;
 }
-__device__ __noinline__ float dot_again(const float* a, int64_t sar, const float* b, int64_t sbr,
-                                        int64_t R) {
+// Every eighth row's share of a column sum, from row w on.
+__device__ __noinline__ float sum_again(const float* a, int64_t step, int64_t R, int w) {
+  constexpr int U = 8, S = 8;
   float v = 0.f;
-  for (int64_t r = 0; r < R && v == v; ++r) v = fmaf(a[r * sar], b[r * sbr], v);
+  int64_t r = w;
+  for (; r + (U - 1) * S < R; r += U * S) {
+    float x[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) x[u] = __ldg(a + (r + u * S) * step);
+#pragma unroll
+    for (int u = 0; u < U; ++u) v += x[u];
+  }
+  for (; r < R; r += S) v += __ldg(a + r * step);
   return v;
 }
 
@@ -122,41 +164,71 @@ __device__ __noinline__ float dot_again(const float* a, int64_t sar, const float
 // kernel.  Bound by memory: 4,999 x 512 fp32 with residual and pre, three parts
 // (61 MB), 20 us.  PLANES: of a product of planes, g its fp32 operands.
 constexpr int kFinishThreads = 256;
-template <typename T, bool PLANES>
-__global__ void __launch_bounds__(kFinishThreads, 4)
-finish_kernel(const float* __restrict__ part, int splits, int64_t I, int64_t J, int64_t ldp,
-              const Epilogue e, int vec, const Product g) {
-  const int64_t n = I * ldp, per = ldp / 4, n4 = I * per;
-  bool waited = false;
+// This thread's pieces, one after another: f(row, column, columns that exist, piece).
+template <typename F>
+__device__ __forceinline__ void finish_pieces(int64_t I, int64_t J, int64_t ldp, F f) {
+  const int64_t per = ldp / 4, n4 = I * per;
   for (int64_t k = (int64_t)blockIdx.x * kFinishThreads + threadIdx.x; k < n4;
        k += (int64_t)gridDim.x * kFinishThreads) {
     // (a 64-bit division costs as much as the rest)
     const int64_t i = n4 < (1ll << 32) ? (int64_t)((uint32_t)k / (uint32_t)per) : k / per;
     const int64_t j = 4 * (k - i * per);
     const int cols = (int)min((int64_t)4, J - j);
+    if (cols > 0) f(i, j, cols, k);
+  }
+}
+// piece k of the partial products, summed; 0 in the columns that do not exist, whose
+// places hold anything
+__device__ __forceinline__ void add_parts(const float* part, int splits, int64_t n, int64_t k, int cols,
+                                          float (&v)[4]) {
+#pragma unroll 4
+  for (int s = 0; s < splits; ++s) {
+    const float4 t = __ldcg(reinterpret_cast<const float4*>(part + s * n) + k);
+    v[0] += t.x;
+    v[1] += t.y;
+    v[2] += t.z;
+    v[3] += t.w;
+  }
+#pragma unroll
+  for (int q = 1; q < 4; ++q) v[q] = q < cols ? v[q] : 0.f;
+}
+__device__ __forceinline__ bool finite4(const float (&v)[4]) {
+  return isfinite(v[0]) && isfinite(v[1]) && isfinite(v[2]) && isfinite(v[3]);
+}
+// The pieces that the kernel has left out.  (A pass of its own: with the call in the
+// kernel's loop that loop spilled, and a data gradient of 48,000 x 256 -> 1,397 took
+// 394 us, 351 before.)
+__device__ __noinline__ void finish_again(const Again* __restrict__ p, const Epilogue& e, int vec) {
+  const int64_t J = p->g.J, ldp = part_pitch(J);
+  finish_pieces(p->g.I, J, ldp, [&](int64_t i, int64_t j, int cols, int64_t k) {
+    float v[4] = {};
+    add_parts(p->part, p->splits, p->pitch, k, cols, v);
+    if (finite4(v)) return;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (q < cols && !isfinite(v[q])) v[q] = dot_again(p, i, j + q, 4 * k + q);
     Beside x;
-    if (cols > 0) beside4<T>(e, x, i, j, cols, vec);
+    beside4<float>(e, x, i, j, cols, vec);
+    finish4<float>(e, x, v, i, j, cols, vec);
+  });
+}
+template <typename T, bool PLANES>
+__global__ void __launch_bounds__(kFinishThreads, 4)
+finish_kernel(const float* __restrict__ part, int splits, int64_t I, int64_t J, int64_t ldp,
+              const __grid_constant__ Epilogue e, int vec, const __grid_constant__ Again again) {
+  bool waited = false, left = false;
+  finish_pieces(I, J, ldp, [&](int64_t i, int64_t j, int cols, int64_t k) {
+    Beside x;
+    beside4<T>(e, x, i, j, cols, vec);
     if (!waited) pdl_wait();      // for the partial products
     waited = true;
     float v[4] = {};
-#pragma unroll 4
-    for (int s = 0; s < splits; ++s) {
-      const float4 t = __ldcg(reinterpret_cast<const float4*>(part + s * n) + k);
-      v[0] += t.x;
-      v[1] += t.y;
-      v[2] += t.z;
-      v[3] += t.w;
-    }
-    if (PLANES && !(isfinite(v[0]) && isfinite(v[1]) && isfinite(v[2]) && isfinite(v[3]))) {
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        if (q < cols && !isfinite(v[q]))
-          v[q] = dot_again(static_cast<const float*>(g.A) + i * g.sai, g.sar,
-                           static_cast<const float*>(g.B) + (j + q) * g.sbj, g.sbr, g.R);
-    }
-    if (cols > 0) finish4<T>(e, x, v, i, j, cols, vec);
-  }
+    add_parts(part, splits, I * ldp, k, cols, v);
+    if (PLANES && !finite4(v)) left = true;
+    else finish4<T>(e, x, v, i, j, cols, vec);
+  });
   if (!waited) pdl_wait();
+  if (PLANES && left) finish_again(&again, e, vec);
 }
 
 // ---- a few rows ------------------------------------------------------------------------
@@ -443,10 +515,11 @@ int fours(const Epilogue& e) {
 
 template <typename T, bool PLANES = false>
 cudaError_t launch_finish(const float* part, int64_t splits, int64_t I, int64_t J, int64_t ldp,
-                          const Epilogue& e, cudaStream_t st, const Product& g = {}) {
+                          const Epilogue& e, cudaStream_t st, const Product& g = {},
+                          int64_t r_per_split = 0) {
   const int64_t blocks = std::min<int64_t>(cdiv(I * ldp / 4, kFinishThreads), 16 * kSms);
   return launch_pdl(finish_kernel<T, PLANES>, dim3((unsigned)blocks), dim3(kFinishThreads), 0, st, part,
-                    (int)splits, I, J, ldp, e, fours(e), g);
+                    (int)splits, I, J, ldp, e, fours(e), Again{g, part, I * ldp, (int)splits, r_per_split});
 }
 
 cudaError_t simt_product(const Product& g, const Epilogue& e, float* part, cudaStream_t st) {
@@ -580,12 +653,13 @@ size_t tc_part_bytes(int64_t I, int64_t J, int64_t R, bool must_split, int terms
 
 // dW from its partial products, four columns a thread, and db from the partial
 // column sums (the blocks after the first `wblocks`), all in a fixed order.
-// PLANES: of a product of planes, g its fp32 operands.
+// PLANES: of a product of planes.
 template <bool PLANES>
 __global__ void __launch_bounds__(kFinishThreads)
 finish_weight_kernel(const float* __restrict__ part, int splits, int64_t I, int64_t J, int64_t ldp,
                      float* __restrict__ dw, const float* __restrict__ sums, int64_t sum_rows,
-                     float* __restrict__ db, int accumulate, int wblocks, const Product g) {
+                     float* __restrict__ db, int accumulate, int wblocks,
+                     const __grid_constant__ Again again) {
   pdl_wait();
   if ((int)blockIdx.x < wblocks) {
     const int64_t n4 = I * ldp / 4, n = I * ldp;
@@ -607,9 +681,7 @@ finish_weight_kernel(const float* __restrict__ part, int splits, int64_t I, int6
       if (PLANES && !(isfinite(v.x) && isfinite(v.y) && isfinite(v.z) && isfinite(v.w))) {
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-          if (j + q < J && !isfinite(vv[q]))
-            vv[q] = dot_again(static_cast<const float*>(g.A) + i * g.sai, g.sar,
-                              static_cast<const float*>(g.B) + (j + q) * g.sbj, g.sbr, g.R);
+          if (j + q < J && !isfinite(vv[q])) vv[q] = dot_again(&again, i, j + q, 4 * k + q);
       }
       if (J % 4 == 0 && !accumulate) {
         *reinterpret_cast<float4*>(o) = make_float4(vv[0], vv[1], vv[2], vv[3]);
@@ -631,25 +703,38 @@ finish_weight_kernel(const float* __restrict__ part, int splits, int64_t I, int6
   }
   part_sum[w][lane] = t;
   __syncthreads();
-  if (w == 0 && c < I) {
-    float v = 0.f;
+  float v = 0.f;
 #pragma unroll
-    for (int q = 0; q < kFinishThreads / kWarp; ++q) v += part_sum[q][lane];
-    if (PLANES && !isfinite(v)) v = sum_again(static_cast<const float*>(g.A) + c * g.sai, g.sar, g.R);
-    db[c] = accumulate ? db[c] + v : v;
+  for (int q = 0; q < kFinishThreads / kWarp; ++q) v += part_sum[q][lane];
+  if (PLANES) {
+    // (the warps share a second look)
+    const bool mine = c < I && !isfinite(v);
+    if (__syncthreads_or(mine)) {
+      const Product& g = again.g;
+      part_sum[w][lane] =
+          mine ? sum_again(static_cast<const float*>(g.A) + c * g.sai, g.sar, g.R, w) : 0.f;
+      __syncthreads();
+      if (mine) {
+        v = 0.f;
+#pragma unroll
+        for (int q = 0; q < kFinishThreads / kWarp; ++q) v += part_sum[q][lane];
+      }
+    }
   }
+  if (w == 0 && c < I) db[c] = accumulate ? db[c] + v : v;
 }
 
 // (part nullptr: dW is there already)
 template <bool PLANES>
 cudaError_t launch_finish_weight(const float* part, int splits, const Product& g, const Epilogue& e,
-                                 const float* sums, int64_t sum_rows, float* db, cudaStream_t st) {
+                                 const float* sums, int64_t sum_rows, float* db, cudaStream_t st,
+                                 int64_t r_per_split = 0) {
   const int64_t ldp = part_pitch(g.J);
   const int wb = part ? (int)std::min<int64_t>(cdiv(g.I * ldp / 4, kFinishThreads), 8 * kSms) : 0;
   const int sb = db ? (int)cdiv(g.I, kWarp) : 0;
   return launch_pdl(finish_weight_kernel<PLANES>, dim3((unsigned)(wb + sb)), dim3(kFinishThreads), 0, st,
                     part, splits, g.I, g.J, ldp, static_cast<float*>(e.out), sums, sum_rows, db,
-                    e.accumulate, wb, g);
+                    e.accumulate, wb, Again{g, part, g.I * ldp, splits, r_per_split});
 }
 size_t sum_bytes(int64_t I, int64_t J, int64_t R, const TcPlan& plan) {
   const Product g{nullptr, 0, 0, nullptr, 0, 0, I, J, R};
@@ -698,9 +783,10 @@ cudaError_t planes_run(const Product& g, const Epilogue& e, float* db, char* wor
   x = tc_product(t, e, plan, part, sums, err, num_sms(), st, plane_rows(amn ? g.R : g.I),
                  plane_rows(bmn ? g.R : g.J));
   if (x != cudaSuccess) return x;
+  const int64_t r_per_split = (int64_t)plan.kt_per_split / kTerms * kSumStep;
   if (e.mode == kWeight)
-    return launch_finish_weight<true>(part, plan.splits, g, e, sums, tc_sum_rows(g, plan), db, st);
-  return launch_finish<float, true>(part, plan.splits, g.I, g.J, part_pitch(g.J), e, st, g);
+    return launch_finish_weight<true>(part, plan.splits, g, e, sums, tc_sum_rows(g, plan), db, st, r_per_split);
+  return launch_finish<float, true>(part, plan.splits, g.I, g.J, part_pitch(g.J), e, st, g, r_per_split);
 }
 size_t planes_need(int64_t ra, int64_t ca, int64_t rb, int64_t cb, int64_t I, int64_t J, int64_t R) {
   return planes_bytes(ra, ca) + planes_bytes(rb, cb) + 512 + tc_part_bytes(I, J, R, true, kTerms) +

@@ -36,6 +36,7 @@ struct Epilogue {
 // ---- tensor-core products (bf16, linear_tc.cu) ------------------------------------
 // A product whose rows (A(i, .), B(j, .), or for the weight gradient A(., r),
 // B(., r)) start on 16-byte boundaries.
+constexpr int kSumStep = 64;
 struct TcPlan {
   int cg;              // CTAs of an output tile: 1 (128 x 128) or 2 (256 x 256)
   int kt_per_split;    // 64-deep steps of the sum per split

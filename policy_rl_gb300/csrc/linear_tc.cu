@@ -62,7 +62,7 @@ using ppo::tc::drain_wait;
 using ppo::tc::wait_bar;
 
 constexpr uint64_t kWaitNs = 2000000000ull;
-constexpr int BM = 128, BK = 64;
+constexpr int BM = 128, BK = kSumStep;
 constexpr int kFirstEpi = 4;           // warps 0..3: producer, MMA, column sums
 constexpr int kBox = 4096;             // 32 rows x 128 bytes, 128-byte swizzle
 // The tensor cores truncate their fp32 sums: measured, 7.6e-5 relative after

@@ -313,3 +313,70 @@ def test_layernorm_past_32_bit_offsets_against_the_reference(P):
     want = be.to(torch.bfloat16)
     assert bool((y[2:M // 2] == want).all()) and not bool(dy[2:M // 2].any())
     assert bool((y[M // 2 + 1:M - 2] == want).all()) and not bool(dy[M // 2 + 1:M - 2].any())
+
+
+# ---- fp32 products by planes with elements that bf16 cannot hold ------------------------
+def test_f32_weight_gradient_infinities_in_many_slices_of_the_sum(P):
+    """Slices of a long sum are finished apart: infinities of one sign, of both signs
+    in one slice and in distant ones, infinity times zero, NaN, and large finite
+    values, each in its row of dW and its element of db alone."""
+    import torch
+    rng = np.random.default_rng(21)
+    M, N, K = 40000, 72, 68
+    dz, x = rng.normal(size=(M, N)), rng.normal(size=(M, K))
+    inf = np.inf
+    dz[11, 0] = dz[39990, 0] = inf                  # rows of dW: 0 .. 6
+    dz[11, 1], dz[39990, 1] = inf, -inf
+    dz[20000, 2], dz[20001, 2] = -inf, inf
+    dz[30000, 3], x[30000, 5] = inf, 0.0
+    dz[7, 4] = np.nan
+    dz[[9, 25000], 5], x[[9, 25000]] = 3.4e38, np.clip(x[[9, 25000]], -0.4, 0.4)
+    dz[39999, 6] = -inf
+    dz, x = dev(dz), dev(x)
+    dw, db = out((N, K)), out((N,))
+    work = torch.zeros(P.ppo_linear_workspace_bytes(M, N, K, x.dtype), dtype=torch.uint8, device="cuda")
+    P.ppo_linear_backward_weight(dz, x, dw, db=db, work=work)
+    P.ppo_work_status(work)
+    Z, X, W, B = f64(dz), f64(x), f64(dw), f64(db)
+    with np.errstate(invalid="ignore", over="ignore"):
+        rw, rb = Z.T @ X, Z.sum(0)
+        # (the product of an infinity and the rest, without what a library may do with it)
+        for n in (0, 1, 2, 3, 4, 6):
+            rw[n] = (Z[:, n, None] * X).sum(0)
+    special = np.arange(7)
+    for n in (0, 1, 2, 3, 4, 6):
+        assert np.array_equal(np.isnan(W[n]), np.isnan(rw[n])), n
+        ok = ~np.isnan(rw[n])
+        assert np.array_equal(W[n][ok], rw[n][ok]), n
+        assert B[n] == rb[n] or np.isnan(B[n]) and np.isnan(rb[n]), n
+    rest = np.setdiff1d(np.arange(N), special[[0, 1, 2, 3, 4, 6]])
+    assert (np.abs(W[rest] - rw[rest]) <= prod_bound("f32", Z[:, rest].T, X, M)).all()
+    # (6.8e38 leaves fp32's range in the sum of the column, not in its products)
+    assert B[5] == inf
+    rest = np.arange(7, N)
+    assert (np.abs(B[rest] - rb[rest]) <= 8 * U32 * (np.sqrt(M) + 8) * np.abs(Z[:, rest]).sum(0)).all()
+
+
+def test_f32_products_with_an_infinity_take_no_thousand_times_longer(P):
+    """One infinity in a gradient of 300,000 rows: its row of dW and its column sum are
+    computed again, which may take 100 times the product (0.4 ms), not 1,000."""
+    import torch
+    M, N, K = 300000, 64, 64
+    dz, x = torch.randn(M, N, device="cuda"), torch.randn(M, K, device="cuda")
+    dw, db = out((N, K)), out((N,))
+    work = torch.zeros(P.ppo_linear_workspace_bytes(M, N, K, x.dtype), dtype=torch.uint8, device="cuda")
+    a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+
+    def ms():
+        took = []
+        for _ in range(4):
+            a.record()
+            P.ppo_linear_backward_weight(dz, x, dw, db=db, work=work)
+            b.record()
+            torch.cuda.synchronize()
+            took.append(a.elapsed_time(b))
+        return min(took)
+    plain = ms()
+    dz[5, 7] = float("inf")
+    assert ms() < 100 * plain
+    assert bool(torch.isinf(dw[7]).all()) and bool(torch.isinf(db[7])) and int(torch.isfinite(dw).sum()) == (N - 1) * K
