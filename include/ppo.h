@@ -571,7 +571,9 @@ ppo_status ppo_set_collective(ppo_ctx *ctx, int32_t world, int32_t rank, ppo_col
  * parameters' gradients are fp32 whatever it is, and each result is rounded
  * to bf16 once.  NULL is allowed where "nullable" is said.  Outputs overlap
  * no input unless said.  Lengths below 1 are PPO_ERR_INVALID.  NaN and
- * infinities pass through as the formulas give them. */
+ * infinities pass through as the formulas give them, but for an infinite state
+ * of the scan, which may become NaN before it is cleared.  The order of every sum
+ * is fixed by types, sizes and pitches: results are deterministic. */
 typedef enum { PPO_DTYPE_F32 = 0, PPO_DTYPE_BF16 = 1 } ppo_dtype;
 
 /* Layer norm of the M rows of d_x: mean and 1/sqrt(var + eps) of each row
@@ -639,10 +641,16 @@ typedef enum {
  *   pre = x W^T + bias,   y = act(pre) + res.
  * d_bias fp32 [N], d_res [M][N], d_pre [M][N] (an output) nullable.  d_y may
  * be d_res (same pitch).  bf16 products run on the tensor cores with fp32
- * accumulation.  fp32 ones keep fp32's digits: as products of three bf16 planes
- * of each operand on the tensor cores from M N K = 2^26 on (weight gradients
- * 2^25), on the CUDA cores below.  Forward products of a few rows stream W through the CUDA cores.  M,
- * N, K are below 2^29, the product of any two at most 2^40.  d_work:
+ * accumulation, which truncates (7.6e-8 of the sum's size every 16 terms); weight
+ * gradients, and sums of more than 65,536 terms, are taken out of it piece by
+ * piece and added with rounding.  fp32 ones keep fp32's digits: as
+ * products of three bf16 planes of each operand on the tensor cores from M N K =
+ * 2^26 on (weight gradients 2^25), on the CUDA cores below.  (The planes hold 24
+ * bits of elements from 2^-100 or so on, fewer of smaller ones.  Infinities, and
+ * what bf16 rounds to one, come out right, but what they reach is computed again:
+ * one in a weight gradient of 1,000,000 rows takes 18 ms.)  Forward products of a
+ * few rows stream W through the CUDA cores.  M, N, K are below 2^29, the product
+ * of any two at most 2^40.  d_work:
  * ppo_linear_workspace_bytes of the same dtype, sizes and pitches (ldz: the
  * pitch of the [M][N] gradient of ppo_linear_backward_*; a pitch <= 0 stands
  * for the row's length).  Rows of bf16 operands that do not start on 16-byte
@@ -651,7 +659,8 @@ typedef enum {
  * serve any number of later calls in one stream's order.  Its first int32 is
  * set nonzero if a bounded device wait of a call gave up (the outputs of that
  * call are then unspecified): ppo_work_status synchronises `stream`, returns
- * PPO_ERR_TIMEOUT if it is set, and clears it. */
+ * PPO_ERR_TIMEOUT if it is set, and clears it (not inside a graph capture:
+ * PPO_ERR_CUDA). */
 ppo_status ppo_linear_workspace_bytes(int32_t dtype, int64_t M, int64_t N, int64_t K, int64_t ldx,
                                       int64_t ldw, int64_t ldz, size_t *bytes);
 ppo_status ppo_linear_forward(int32_t dtype, const void *d_x, int64_t ldx, const void *d_w,

