@@ -755,10 +755,14 @@ lin_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
                             : bias_slow(p.e.bias, c8 + 8 * i, J);
             }
           }
-          // `rows` rows of the box to where they belong (by TMA: after a fence)
+          // `rows` rows of the box to where they belong (by TMA: after a fence).  A TMA
+          // store ends on 16 bytes, not on the matrix's last column: a box that reaches
+          // past a width that is no multiple of 8 is stored by hand, or it would
+          // overwrite what follows the row.
+          const bool inside = col0 + PART <= J || (J & 7) == 0;
           auto leave = [&](uint8_t* from, const CUtensorMap* tm, bool tma, void* base, int64_t ld,
                            int r0, int rows) {
-            if (tma) {
+            if (tma && inside) {
               if (lane == 0 && r0 < I) tma_store_2d(tm, smem_u32(from), col0, r0);
             } else {
               box_store_slow(from, lane, base, ld, r0, col0, p.I, p.J, rows);

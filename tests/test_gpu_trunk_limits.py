@@ -380,3 +380,62 @@ def test_f32_products_with_an_infinity_take_no_thousand_times_longer(P):
     dz[5, 7] = float("inf")
     assert ms() < 100 * plain
     assert bool(torch.isinf(dw[7]).all()) and bool(torch.isinf(db[7])) and int(torch.isfinite(dw).sum()) == (N - 1) * K
+
+
+# ---- nothing but the outputs is written ------------------------------------------------
+@pytest.fixture
+def framed(monkeypatch):
+    """Outputs of the checks lie in larger buffers of NaN: before (`front` elements),
+    after and between their rows nothing may change."""
+    import torch
+    import test_gpu_trunk_ops as ops
+    frames = []
+
+    def framed_out(shape, dtype="f32", pitch=None):
+        front, pitch, rows = check.front, pitch or shape[-1], int(np.prod(shape[:-1]))
+        flat = torch.full((front + rows * pitch + 64,), float("nan"), dtype=tdt(dtype), device="cuda")
+        frames.append((flat, front, rows, pitch, shape[-1]))
+        return flat[front:-64].view(*shape[:-1], pitch)[..., :shape[-1]]
+
+    def check():
+        assert frames
+        for flat, front, rows, pitch, width in frames:
+            assert bool(flat[:front].isnan().all()) and bool(flat[-64:].isnan().all())
+            gap = flat[front:-64].view(rows, pitch)[:, width:]
+            assert bool(gap.isnan().all()), (rows, pitch, width, gap.isnan().logical_not().nonzero()[:3].tolist())
+    check.front = 64
+    monkeypatch.setattr(ops, "out", framed_out)
+    return check
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("pre,res,dres", [(False, False, False), (True, False, True), (False, True, False),
+                                          (True, True, True)])
+@pytest.mark.parametrize("M,N,K,pitch", [(50, 31, 21, (24, 24, 32)), (552, 6, 1, (8, 8, 8)), (300, 245, 335, (336, 336, 248)),
+                                         (700, 1003, 999, (1000, 1000, 1008)), (4220, 18, 270, (272, 272, 24)),
+                                         (260, 130, 71, (75, 73, 131))])
+def test_linear_writes_its_outputs_alone(P, framed, M, N, K, pitch, pre, res, dres, dtype):
+    """Rows that end inside 16 bytes, from 16-byte boundaries: what follows them in the
+    buffer (other columns of a wider matrix) stays."""
+    check_linear(P, M, N, K, dtype, act="gelu", pact="relu" if dres else "none", pre=pre, res=res, dres=dres,
+                 pitch=pitch, seed=M)
+    framed()
+
+
+@pytest.mark.parametrize("act,pact,res,dres,pre", [("relu", "relu", False, False, False), ("none", "none", False, True, False),
+                                                   ("gelu", "silu", True, True, True)])
+def test_linear_with_many_tiles_a_pair_writes_its_outputs_alone(P, framed, act, pact, res, dres, pre):
+    check_linear(P, 19500, 1001, 998, "bf16", act=act, pact=pact, res=res, dres=dres, pre=pre,
+                 pitch=(1000, 1000, 1008), seed=3)
+    framed()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_layernorm_and_scan_write_their_outputs_alone(P, framed, dtype):
+    framed.front = 0      # (check_ln looks between rows from the buffer's start on)
+    for M, D, pitch in [(19, 61, 64), (333, 1397, 1400), (70, 4099, 4104), (5000, 33, 35), (700, 8203, 8208), (9, 7, None)]:
+        check_ln(P, M, D, dtype, pitch=pitch, seed=D)
+    framed.front = 64
+    for T, N, H, pitch in [(1, 9, 61, 184), (7, 5, 33, 104), (140, 3, 61, 184), (1100, 2, 31, 96), (33, 4, 130, None)]:
+        check_scan(P, T, N, H, dtype, seed=T, pitch=pitch)
+    framed()
