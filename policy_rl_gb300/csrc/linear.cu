@@ -543,11 +543,12 @@ cudaError_t simt_product(const Product& g, const Epilogue& e, float* part, cudaS
 
 // ---- bf16 operands on 16-byte rows ---------------------------------------------------
 // TMA reads rows that start on 16-byte boundaries: others are copied once, with
-// a pitch rounded up to 8 elements.
+// a pitch rounded up to 8 elements.  (One row starts on the base's boundary, whatever
+// the pitch: callers give its length as well as its distance to a next row.)
 int64_t pitch8(int64_t cols) { return (cols + 7) / 8 * 8; }
 size_t packed_bytes(int64_t rows, int64_t cols, int64_t ld) {
   if (ld <= 0) ld = cols;
-  return ld % 8 ? (size_t)(rows * pitch8(cols) * 2 + 255) / 256 * 256 : 0;
+  return ld % 8 && rows > 1 ? (size_t)(rows * pitch8(cols) * 2 + 255) / 256 * 256 : 0;
 }
 constexpr int kPackThreads = 256;
 // A matrix that is copied, and the blocks that do it.  A product's two operands
@@ -578,6 +579,10 @@ __global__ void __launch_bounds__(kPackThreads) pack_rows_kernel(const Copy a, c
 Copy on_16_bytes(const void*& a, int64_t& ld, int64_t rows, int64_t cols, char*& work) {
   if (ld % 8 == 0) return Copy{};
   const int64_t pitch = pitch8(cols);
+  if (rows == 1) {
+    ld = pitch;
+    return Copy{};
+  }
   const Copy c{a, ld, rows, cols, pitch, rows, reinterpret_cast<uint4*>(work),
                (int)std::min<int64_t>(cdiv(rows * (pitch / 8), kPackThreads), 16 * kSms)};
   a = work;

@@ -439,3 +439,13 @@ def test_layernorm_and_scan_write_their_outputs_alone(P, framed, dtype):
     for T, N, H, pitch in [(1, 9, 61, 184), (7, 5, 33, 104), (140, 3, 61, 184), (1100, 2, 31, 96), (33, 4, 130, None)]:
         check_scan(P, T, N, H, dtype, seed=T, pitch=pitch)
     framed()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("M,N,K,pitch", [(1, 753, 21, (24, 24, 760)), (38, 1, 1889, (1896, 1896, 8)), (1, 1, 14, (16, 16, 8)),
+                                         (1, 468, 1152, (1152, 1152, 472)), (300, 1, 45, (48, 48, 8)),
+                                         (1, 244, 201, (208, 203, 246)), (1, 1397, 1001, None)])
+def test_linear_of_single_rows(P, framed, M, N, K, pitch, dtype):
+    """One row has no pitch of its own: the workspace of whichever is named is enough."""
+    check_linear(P, M, N, K, dtype, act="gelu", pact="silu", dres=True, pitch=pitch, seed=N)
+    framed()
