@@ -17,7 +17,10 @@
  * and the operators of a deeper recurrent trunk, forward and backward: layer
  * norm (ppo_layernorm_*), the gated linear recurrence over any length and
  * width (ppo_gated_scan_*), matrix products with bias, activation and residual
- * (ppo_linear_*).
+ * (ppo_linear_*), gated feed-forward layers (ppo_gated_linear_*); the
+ * log-probability, entropy and policy loss over any number of actions, forward
+ * and backward (ppo_action_*); and the norm of many gradient tensors, and their
+ * clipping (ppo_grad_norm, ppo_clip_grad_norm).
  *
  * Conventions shared by every entry point
  *  - Pointers named d_* are DEVICE pointers on the current CUDA device;
@@ -686,6 +689,110 @@ ppo_status ppo_linear_backward_weight(int32_t dtype, const void *d_dz, int64_t l
                                       float *d_dw, float *d_db, int32_t accumulate, void *d_work,
                                       size_t work_bytes, cudaStream_t stream);
 ppo_status ppo_work_status(void *d_work, cudaStream_t stream);
+
+/* Gated linear layer: two projections of x [M][K], the gate through its
+ * activation, and their product.  w [2N][K]: rows 0..N-1 the gate's, rows
+ * N..2N-1 the other's (bias fp32 [2N], nullable, likewise):
+ *   pre = x W^T + bias  [M][2N],   y = act(pre[:, 0..N-1]) * pre[:, N..2N-1]  [M][N].
+ * d_pre (nullable) keeps pre for the backward pass; y is computed before pre is
+ * rounded.  bf16 products run on the tensor cores, fp32 ones as in
+ * ppo_linear_forward (the same limits, with 2N for N).  d_work:
+ * ppo_gated_linear_workspace_bytes of the same dtype, sizes and pitches (J = 0:
+ * forward alone; a pitch <= 0 stands for the row's length), zeroed once, as
+ * for ppo_linear_*; ppo_work_status reads its status word. */
+ppo_status ppo_gated_linear_workspace_bytes(int32_t dtype, int64_t M, int64_t N, int64_t K, int64_t J,
+                                            int64_t ldx, int64_t ldw, int64_t lddz, int64_t ldw2,
+                                            size_t *bytes);
+ppo_status ppo_gated_linear_forward(int32_t dtype, const void *d_x, int64_t ldx, const void *d_w,
+                                    int64_t ldw, const float *d_bias, int32_t act, int64_t M,
+                                    int64_t N, int64_t K, void *d_y, int64_t ldy, void *d_pre,
+                                    int64_t ldpre, void *d_work, size_t work_bytes,
+                                    cudaStream_t stream);
+/* Gradient with respect to pre, from that of the layer that y goes into:
+ * dz [M][J], its weight w2 [J][N].  With g = pre[:, 0..N-1], u = pre[:, N..2N-1]:
+ *   d = dz W2,   dp = [ d u act'(g) | d act(g) ]  [M][2N],   y = act(g) u.
+ * d_y [M][N] (nullable): y once more, for the gradient of w2, so that the
+ * forward pass need not keep it.  The layer's own gradients are ppo_linear_*'s:
+ * dx = dp W by ppo_linear_backward_data, dW and dbias by
+ * ppo_linear_backward_weight.  d_dp may be d_pre (same pitch). */
+ppo_status ppo_gated_linear_backward_data(int32_t dtype, const void *d_dz, int64_t lddz,
+                                          const void *d_w2, int64_t ldw2, const void *d_pre,
+                                          int64_t ldpre, int32_t act, int64_t M, int64_t N,
+                                          int64_t J, void *d_dp, int64_t lddp, void *d_y,
+                                          int64_t ldy, void *d_work, size_t work_bytes,
+                                          cudaStream_t stream);
+
+/* ---- Policy over any number of actions ---------------------------------------
+ * One categorical head of V actions, V too large (or the head too far from the
+ * MLP) for ppo_minibatch_loss_grad: logits [M][V] of type dtype, pitch ld.
+ * d_mask (nullable): bytes [M][V], pitch ldm, 0 where the action is not
+ * allowed: such logits count as -inf whatever they hold.  With lp = log softmax
+ * of a row over its allowed actions,
+ *   logp = lp[action],   entropy = -sum exp(lp) lp.
+ * An action outside [0, V) marks a row without one: logp 0.  An action that is
+ * not allowed (or whose logit is -inf) has logp -inf; a row of which nothing is
+ * allowed has entropy 0.  Pointers need only their elements' alignment here.
+ * Statistics are fp32; V <= PPO_MAX_ACTIONS, M < 2^31 (PPO_ERR_UNSUPPORTED).
+ * NaN and infinities pass through as the formulas give them, but not from
+ * places that the mask covers. */
+enum { PPO_MAX_ACTIONS = 262144 };
+/* d_action int32 [M] (nullable when d_logp is); d_logp, d_entropy fp32 [M], nullable. */
+ppo_status ppo_action_logp(int32_t dtype, const void *d_logits, int64_t ld, int64_t M, int64_t V,
+                           const uint8_t *d_mask, int64_t ldm, const int32_t *d_action,
+                           float *d_logp, float *d_entropy, cudaStream_t stream);
+/* The clipped policy loss ("Teaching Mario to speedrun", sec. 6 "Don't move too
+ * far at once") with a KL term towards a reference policy, and its gradient:
+ *   x = logp - logp_old,   r = e^x,   A = d_adv,
+ *   pg = -min(r A, clip(r, 1 - clip_low, 1 + clip_high) A),
+ *   kl = e^y - y - 1,  y = logp_ref - logp    (0 when d_logp_ref is NULL),
+ *   loss = scale * sum over rows of w (pg + kl_coef kl - ent_coef entropy),
+ * w = d_weight[row] (1 when NULL).  kl is the estimate of KL(pi || ref) at the
+ * action taken.  d_dlogits [M][V] (pitch lddl, type dtype) receives dloss/dlogits:
+ *   scale w (c (1[j = action] - p_j) + ent_coef p_j (lp_j + entropy)),
+ *   c = -A r [r A <= clip(r) A] + kl_coef (1 - e^y);
+ * 0 where the mask covers.  It may be d_logits (same pitch).  Rows without an
+ * allowed action are left out: nothing of them is added, their gradients are 0, and
+ * what their logp_old, adv, logp_ref and weight hold does not matter.
+ * d_logp, d_entropy (nullable): as in ppo_action_logp.  d_stats (nullable) fp32
+ * [8]: scale * sum of w {pg + kl_coef kl - ent_coef entropy, pg, kl, entropy,
+ * [r < 1 - clip_low or r > 1 + clip_high], (r - 1) - x, 1}, then the number of
+ * rows left out.  d_work: ppo_action_loss_workspace_bytes() bytes (nullable
+ * without d_stats), 16-byte aligned. */
+ppo_status ppo_action_loss_workspace_bytes(size_t *bytes);
+ppo_status ppo_action_loss_grad(int32_t dtype, const void *d_logits, int64_t ld, int64_t M,
+                                int64_t V, const uint8_t *d_mask, int64_t ldm,
+                                const int32_t *d_action, const float *d_logp_old,
+                                const float *d_adv, const float *d_logp_ref,
+                                const float *d_weight, float scale, float clip_low,
+                                float clip_high, float kl_coef, float ent_coef, void *d_dlogits,
+                                int64_t lddl, float *d_logp, float *d_entropy, float *d_stats,
+                                void *d_work, size_t work_bytes, cudaStream_t stream);
+
+/* ---- Gradient norm of many tensors -------------------------------------------
+ * The 2-norm over all elements of n tensors, as ppo_adam_step takes it of a
+ * context's one buffer, and the tensors scaled by
+ *   f = min(1, max_norm / (norm + 1e-6))      (1 when max_norm <= 0).
+ * h_tensors (HOST, read during the call): device pointer (on its elements'
+ * alignment), elements (0 allowed) and type of each.  Squares are summed so that
+ * neither large nor small elements are lost: the norm is inf or 0 only if it is
+ * so in fp32.  A NaN makes norm and f NaN; an infinity makes f 0.
+ * ppo_clip_grad_norm writes f times each tensor, rounded once, to h_out's
+ * tensors (same counts and types, nullable: in place).  Tensors that are written
+ * overlap no other tensor of the call (PPO_ERR_INVALID), but an out tensor
+ * may be its own input.  d_norm fp32 [1] receives the norm before clipping.
+ * d_work: ppo_grad_norm_workspace_bytes(n) bytes, 16-byte aligned.  n < 2^20. */
+typedef struct {
+    void *d_data;
+    int64_t count;
+    int32_t dtype;     /* ppo_dtype */
+    int32_t reserved;  /* 0 */
+} ppo_tensor;
+ppo_status ppo_grad_norm_workspace_bytes(int64_t n, size_t *bytes);
+ppo_status ppo_grad_norm(const ppo_tensor *h_tensors, int64_t n, float *d_norm, void *d_work,
+                         size_t work_bytes, cudaStream_t stream);
+ppo_status ppo_clip_grad_norm(const ppo_tensor *h_tensors, const ppo_tensor *h_out, int64_t n,
+                              float max_norm, float *d_norm, void *d_work, size_t work_bytes,
+                              cudaStream_t stream);
 
 /* ---- Inspection and failure handling ----------------------------------------
  * Step trace of the whole update ("Teaching Mario to speedrun", sec. 6 "The

@@ -28,7 +28,10 @@ __all__ = [
     "ppo_layernorm_forward", "ppo_layernorm_backward_workspace_bytes", "ppo_layernorm_backward",
     "ppo_gated_scan_forward", "ppo_gated_scan_backward", "ppo_scan_blocks",
     "ppo_linear_workspace_bytes", "ppo_linear_forward", "ppo_linear_backward_data",
-    "ppo_linear_backward_weight", "ppo_work_status",
+    "ppo_linear_backward_weight", "ppo_work_status", "ppo_gated_linear_workspace_bytes",
+    "ppo_gated_linear_forward", "ppo_gated_linear_backward_data", "ppo_action_logp",
+    "ppo_action_loss_workspace_bytes", "ppo_action_loss_grad", "TensorList",
+    "ppo_grad_norm_workspace_bytes", "ppo_grad_norm", "ppo_clip_grad_norm",
     "library_path",
 ]
 
@@ -236,15 +239,17 @@ class RnnContext:
 # A call on a few rows takes the GPU some 3 us, so these wrappers are written
 # for little work per argument.
 _F32 = None        # torch.float32 (torch is imported by the caller's tensors)
+_I32S = _BYTES = ()
 _DTYPES: dict = {}
 _raw_stream = None
 _current_gpu = None
 
 
 def _bind_torch():
-    global _F32, _raw_stream, _current_gpu
+    global _F32, _I32S, _BYTES, _raw_stream, _current_gpu
     import torch
     _F32 = torch.float32
+    _I32S, _BYTES = (torch.int32,), (torch.bool, torch.uint8)
     _DTYPES.update({torch.float32: _abi.DTYPE_F32, torch.bfloat16: _abi.DTYPE_BF16})
     raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
     _raw_stream = raw or (lambda device: torch.cuda.current_stream(device).cuda_stream)
@@ -462,6 +467,191 @@ def ppo_work_status(work, stream=None) -> None:
     """Synchronises the stream; raises PPO_ERR_TIMEOUT if a bounded device wait
     of a ppo_linear_* call on this workspace gave up."""
     _abi.check(_lib().ppo_work_status(_ptr(work), _stream(stream)), "ppo_work_status")
+
+
+def ppo_gated_linear_workspace_bytes(M: int, N: int, K: int, dtype, J: int = 0, ldx: int = 0, ldw: int = 0,
+                                     lddz: int = 0, ldw2: int = 0) -> int:
+    """Bytes of workspace for a gated layer of x [M, K], w [2N, K] and, where J is
+    not 0, its backward pass from dz [M, J] through w2 [J, N] (allocate it zeroed;
+    pitches only where the rows are strided)."""
+    if _F32 is None:
+        _bind_torch()
+    n = ctypes.c_size_t()
+    _abi.check(_lib().ppo_gated_linear_workspace_bytes(_DTYPES.get(dtype, -1), M, N, K, J, ldx, ldw, lddz, ldw2,
+                                                       ctypes.byref(n)), "ppo_gated_linear_workspace_bytes")
+    return n.value
+
+
+def ppo_gated_linear_forward(x, w, y, bias=None, act=_abi.ACT_SILU, pre=None, work=None, stream=None) -> None:
+    """y [M, N] = act(gate) * up of x [M, K], the rows of w [2N, K] being the
+    gate's and then the other projection's, bias fp32 [2N] likewise; pre [M, 2N]
+    takes both (see ppo.h)."""
+    code, gpu = _kind(x)
+    dt = x.dtype
+    M, K = x.shape
+    N = y.shape[1]
+    px, ldx = _mat(x, dt, gpu, (M, K), "x")
+    pw, ldw = _mat(w, dt, gpu, (2 * N, K), "w")
+    py, ldy = _mat(y, dt, gpu, (M, N), "y")
+    pp, ldp = _mat(pre, dt, gpu, (M, 2 * N), "pre")
+    pk, wb = _work_of(work, gpu)
+    _check(_lib().ppo_gated_linear_forward(
+        code, px, ldx, pw, ldw, _vec(bias, gpu, (2 * N,), "bias"), act, M, N, K, py, ldy, pp, ldp, pk, wb,
+        _on(stream, gpu)), "ppo_gated_linear_forward")
+
+
+def ppo_gated_linear_backward_data(dz, w2, pre, dp, act=_abi.ACT_SILU, y=None, work=None, stream=None) -> None:
+    """dp [M, 2N], the gradient of pre [M, 2N], from dz [M, J] through w2 [J, N];
+    y [M, N] takes the layer's output once more (see ppo.h).  dp may be pre."""
+    code, gpu = _kind(dz)
+    dt = dz.dtype
+    M, J = dz.shape
+    N = w2.shape[1]
+    pd, ldd = _mat(dz, dt, gpu, (M, J), "dz")
+    pw, ldw = _mat(w2, dt, gpu, (J, N), "w2")
+    pp, ldp = _mat(pre, dt, gpu, (M, 2 * N), "pre")
+    po, ldo = _mat(dp, dt, gpu, (M, 2 * N), "dp")
+    py, ldy = _mat(y, dt, gpu, (M, N), "y")
+    pk, wb = _work_of(work, gpu)
+    _check(_lib().ppo_gated_linear_backward_data(
+        code, pd, ldd, pw, ldw, pp, ldp, act, M, N, J, po, ldo, py, ldy, pk, wb, _on(stream, gpu)),
+        "ppo_gated_linear_backward_data")
+
+
+# ---- policy over any number of actions --------------------------------------------
+def _of(t, dtypes, gpu, shape, name):
+    """Address of a contiguous argument of one of the types."""
+    if t is None:
+        return None
+    if t.dtype not in dtypes or t.shape != shape or t.get_device() != gpu or not t.is_contiguous():
+        raise ValueError(f"{name}: a contiguous tensor {tuple(shape)} of {dtypes[0]} on cuda:{gpu} is wanted, got "
+                         f"{tuple(t.shape)} of {t.dtype} on {t.device}")
+    return t.data_ptr()
+
+
+def _allowed(mask, gpu, shape):
+    """(address, pitch) of a mask of bytes."""
+    if mask is None:
+        return None, 0
+    if mask.dtype not in _BYTES:
+        raise ValueError(f"mask: torch.bool or torch.uint8 is wanted, got {mask.dtype}")
+    return _mat(mask, mask.dtype, gpu, shape, "mask")
+
+
+def ppo_action_logp(logits, action, logp=None, entropy=None, mask=None, stream=None) -> None:
+    """logp fp32 [M] of action int32 [M] and entropy fp32 [M] of the rows of
+    logits [M, V], over the actions where mask [M, V] (bool) is set (see ppo.h)."""
+    code, gpu = _kind(logits)
+    M, V = shape = logits.shape
+    pl, ld = _mat(logits, logits.dtype, gpu, shape, "logits")
+    pm, ldm = _allowed(mask, gpu, shape)
+    _check(_lib().ppo_action_logp(
+        code, pl, ld, M, V, pm, ldm, _of(action, _I32S, gpu, (M,), "action"), _vec(logp, gpu, (M,), "logp"),
+        _vec(entropy, gpu, (M,), "entropy"), _on(stream, gpu)), "ppo_action_logp")
+
+
+def ppo_action_loss_workspace_bytes() -> int:
+    n = ctypes.c_size_t()
+    _abi.check(_lib().ppo_action_loss_workspace_bytes(ctypes.byref(n)), "ppo_action_loss_workspace_bytes")
+    return n.value
+
+
+def ppo_action_loss_grad(logits, action, logp_old, adv, dlogits, scale, logp_ref=None, weight=None, mask=None,
+                         clip_low=0.2, clip_high=0.2, kl_coef=0.0, ent_coef=0.0, logp=None, entropy=None,
+                         stats=None, work=None, stream=None) -> None:
+    """dlogits [M, V], the gradient of the clipped policy loss with respect to
+    logits [M, V], for action int32 [M] and logp_old, adv, logp_ref, weight fp32
+    [M]; stats fp32 [8] takes the loss and its terms (see ppo.h).  dlogits may be
+    logits."""
+    code, gpu = _kind(logits)
+    dt = logits.dtype
+    M, V = shape = logits.shape
+    row = (M,)
+    pl, ld = _mat(logits, dt, gpu, shape, "logits")
+    pm, ldm = _allowed(mask, gpu, shape)
+    pd, ldd = _mat(dlogits, dt, gpu, shape, "dlogits")
+    pk, wb = _work_of(work, gpu)
+    _check(_lib().ppo_action_loss_grad(
+        code, pl, ld, M, V, pm, ldm, _of(action, _I32S, gpu, row, "action"),
+        _vec(logp_old, gpu, row, "logp_old"), _vec(adv, gpu, row, "adv"), _vec(logp_ref, gpu, row, "logp_ref"),
+        _vec(weight, gpu, row, "weight"), scale, clip_low, clip_high, kl_coef, ent_coef, pd, ldd,
+        _vec(logp, gpu, row, "logp"), _vec(entropy, gpu, row, "entropy"), _vec(stats, gpu, (8,), "stats"), pk, wb,
+        _on(stream, gpu)), "ppo_action_loss_grad")
+
+
+# ---- gradient norm of many tensors --------------------------------------------------
+class TensorList:
+    """The places of tensors on one GPU, as ppo_grad_norm and ppo_clip_grad_norm
+    take them (contiguous, float32 or bfloat16).  It keeps the tensors alive; a
+    program whose gradients stay where they are makes it once."""
+
+    def __init__(self, tensors):
+        if _F32 is None:
+            _bind_torch()
+        self.tensors = tuple(tensors)
+        self.gpu = self.tensors[0].get_device() if self.tensors else -1
+        self.array = (_abi.Tensor * max(1, len(self.tensors)))()
+        for k, t in enumerate(self.tensors):
+            code = _DTYPES.get(t.dtype)
+            if code is None:
+                raise ValueError(f"tensor {k}: float32 or bfloat16 is wanted, got {t.dtype}")
+            if t.get_device() != self.gpu or self.gpu < 0:
+                raise ValueError(f"tensor {k}: CUDA tensors of one GPU are wanted, got one on {t.device}")
+            if not t.is_contiguous():
+                raise ValueError(f"tensor {k}: must be contiguous")
+            self.array[k] = _abi.Tensor(t.data_ptr(), t.numel(), code, 0)
+
+    def __len__(self):
+        return len(self.tensors)
+
+
+def _listed(tensors):
+    return tensors if isinstance(tensors, TensorList) else TensorList(tensors)
+
+
+def ppo_grad_norm_workspace_bytes(tensors) -> int:
+    """Bytes of workspace for a TensorList, a sequence of tensors or their number."""
+    n = ctypes.c_size_t()
+    _abi.check(_lib().ppo_grad_norm_workspace_bytes(tensors if isinstance(tensors, int) else len(tensors),
+                                                    ctypes.byref(n)), "ppo_grad_norm_workspace_bytes")
+    return n.value
+
+
+def _list_gpu(norm, lists):
+    """The GPU of a call on lists of tensors."""
+    if _F32 is None:
+        _bind_torch()
+    gpu = norm.get_device()
+    if gpu < 0 or gpu != _current_gpu():
+        raise ValueError(f"norm is on {norm.device}, the current device is cuda:{_current_gpu()}")
+    for t in lists:
+        if len(t) and t.gpu != gpu:
+            raise ValueError(f"the tensors are on cuda:{t.gpu}, norm is on cuda:{gpu}")
+    return gpu
+
+
+def ppo_grad_norm(tensors, norm, work=None, stream=None) -> None:
+    """norm fp32 [1] = the 2-norm over all elements of the tensors (a TensorList or
+    a sequence; see ppo.h)."""
+    tensors = _listed(tensors)
+    gpu = _list_gpu(norm, (tensors,))
+    pk, wb = _work_of(work, gpu)
+    _check(_lib().ppo_grad_norm(tensors.array, len(tensors), _vec(norm, gpu, (1,), "norm"), pk, wb,
+                                _on(stream, gpu)), "ppo_grad_norm")
+
+
+def ppo_clip_grad_norm(tensors, max_norm, norm, out=None, work=None, stream=None) -> None:
+    """Scales the tensors, or writes them scaled to out's, by min(1, max_norm /
+    (norm + 1e-6)); norm fp32 [1] receives the norm before clipping (see ppo.h)."""
+    tensors = _listed(tensors)
+    out = None if out is None else _listed(out)
+    gpu = _list_gpu(norm, (tensors,) if out is None else (tensors, out))
+    if out is not None and len(out) != len(tensors):
+        raise ValueError(f"out: {len(tensors)} tensors are wanted, got {len(out)}")
+    pk, wb = _work_of(work, gpu)
+    _check(_lib().ppo_clip_grad_norm(tensors.array, None if out is None else out.array, len(tensors), max_norm,
+                                     _vec(norm, gpu, (1,), "norm"), pk, wb, _on(stream, gpu)),
+           "ppo_clip_grad_norm")
 
 
 # ---- context ------------------------------------------------------------------

@@ -27,11 +27,15 @@ SYMBOLS = (
     "ppo_set_wait_limit", "ppo_layernorm_forward", "ppo_layernorm_backward_workspace_bytes",
     "ppo_layernorm_backward", "ppo_gated_scan_forward", "ppo_gated_scan_backward",
     "ppo_linear_workspace_bytes", "ppo_linear_forward", "ppo_linear_backward_data",
-    "ppo_linear_backward_weight", "ppo_work_status",
+    "ppo_linear_backward_weight", "ppo_work_status", "ppo_gated_linear_workspace_bytes",
+    "ppo_gated_linear_forward", "ppo_gated_linear_backward_data", "ppo_action_logp",
+    "ppo_action_loss_workspace_bytes", "ppo_action_loss_grad", "ppo_grad_norm_workspace_bytes",
+    "ppo_grad_norm", "ppo_clip_grad_norm",
 )
 DTYPE_F32, DTYPE_BF16 = 0, 1
 ACT_NONE, ACT_TANH, ACT_RELU, ACT_SILU, ACT_GELU = -1, 0, 1, 2, 3
 SCAN_BLOCK = 128
+MAX_ACTIONS = 262144
 NUM_STAGES = 34
 NUM_KERNEL_STAGES = 25
 
@@ -71,6 +75,11 @@ class RnnConfig(ctypes.Structure):
         ("max_grad_norm", ctypes.c_float), ("beta1", ctypes.c_double),
         ("beta2", ctypes.c_double), ("adam_eps", ctypes.c_double),
     ]
+
+
+class Tensor(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("count", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
 
 
 _P = ctypes.c_void_p
@@ -170,6 +179,19 @@ def load(path: str = LIB_PATH):
         "ppo_linear_backward_weight": ([i32, _P, _I64, _P, _I64, _I64, _I64, _I64, _P, _P, i32, _P,
                                         _SZ, _P], ctypes.c_int),
         "ppo_work_status": ([_P, _P], ctypes.c_int),
+        "ppo_gated_linear_workspace_bytes": ([i32, _I64, _I64, _I64, _I64, _I64, _I64, _I64, _I64,
+                                              ctypes.POINTER(_SZ)], ctypes.c_int),
+        "ppo_gated_linear_forward": ([i32, _P, _I64, _P, _I64, _P, i32, _I64, _I64, _I64, _P, _I64,
+                                      _P, _I64, _P, _SZ, _P], ctypes.c_int),
+        "ppo_gated_linear_backward_data": ([i32, _P, _I64, _P, _I64, _P, _I64, i32, _I64, _I64,
+                                            _I64, _P, _I64, _P, _I64, _P, _SZ, _P], ctypes.c_int),
+        "ppo_action_logp": ([i32, _P, _I64, _I64, _I64, _P, _I64, _P, _P, _P, _P], ctypes.c_int),
+        "ppo_action_loss_workspace_bytes": ([ctypes.POINTER(_SZ)], ctypes.c_int),
+        "ppo_action_loss_grad": ([i32, _P, _I64, _I64, _I64, _P, _I64, _P, _P, _P, _P, _P, _F, _F,
+                                  _F, _F, _F, _P, _I64, _P, _P, _P, _P, _SZ, _P], ctypes.c_int),
+        "ppo_grad_norm_workspace_bytes": ([_I64, ctypes.POINTER(_SZ)], ctypes.c_int),
+        "ppo_grad_norm": ([_P, _I64, _P, _P, _SZ, _P], ctypes.c_int),
+        "ppo_clip_grad_norm": ([_P, _P, _I64, _F, _P, _P, _SZ, _P], ctypes.c_int),
     }
     for name, (args, res) in sig.items():
         fn = getattr(L, name)

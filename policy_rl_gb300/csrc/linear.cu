@@ -545,20 +545,14 @@ cudaError_t simt_product(const Product& g, const Epilogue& e, float* part, cudaS
 // TMA reads rows that start on 16-byte boundaries: others are copied once, with
 // a pitch rounded up to 8 elements.  (One row starts on the base's boundary, whatever
 // the pitch: callers give its length as well as its distance to a next row.)
+}  // namespace
 int64_t pitch8(int64_t cols) { return (cols + 7) / 8 * 8; }
 size_t packed_bytes(int64_t rows, int64_t cols, int64_t ld) {
   if (ld <= 0) ld = cols;
   return ld % 8 && rows > 1 ? (size_t)(rows * pitch8(cols) * 2 + 255) / 256 * 256 : 0;
 }
+namespace {
 constexpr int kPackThreads = 256;
-// A matrix that is copied, and the blocks that do it.  A product's two operands
-// take one launch (2,000 x 130 -> 250 forward: 15 us, 21 with a launch each).
-struct Copy {
-  const void* src;
-  int64_t ld, rows, cols, pitch, rows_pad;
-  uint4* dst;
-  int blocks;
-};
 __device__ __forceinline__ void copy_rows(const Copy& m, int block) {
   const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(m.src);
   const int64_t per = m.pitch / 8, n = m.rows * per, total = (m.rows - 1) * m.ld + m.cols;
@@ -575,7 +569,7 @@ __global__ void __launch_bounds__(kPackThreads) pack_rows_kernel(const Copy a, c
   if ((int)blockIdx.x < a.blocks) copy_rows(a, blockIdx.x);
   else copy_rows(b, blockIdx.x - a.blocks);
 }
-// the operand itself, or its copy in the workspace (advanced past it)
+}  // namespace
 Copy on_16_bytes(const void*& a, int64_t& ld, int64_t rows, int64_t cols, char*& work) {
   if (ld % 8 == 0) return Copy{};
   const int64_t pitch = pitch8(cols);
@@ -594,6 +588,7 @@ cudaError_t pack(const Copy& a, const Copy& b, cudaStream_t st) {
   if (a.blocks + b.blocks == 0) return cudaSuccess;
   return launch_pdl(pack_rows_kernel, dim3((unsigned)(a.blocks + b.blocks)), dim3(kPackThreads), 0, st, a, b);
 }
+namespace {
 
 // ---- fp32 operands as three bf16 planes ------------------------------------------------
 // x = x1 + x2 + x3 with bf16 x1 (x rounded), x2 (the rest rounded), x3: 24 bits
@@ -652,10 +647,12 @@ bool takes_planes(int mode, int64_t M, int64_t N, int64_t K) {
   return M * N * K >= (mode == kWeight ? 1ll << 25 : 1ll << 26);
 }
 
-size_t tc_part_bytes(int64_t I, int64_t J, int64_t R, bool must_split, int terms = 1) {
+}  // namespace
+size_t tc_part_bytes(int64_t I, int64_t J, int64_t R, bool must_split, int terms) {
   const TcPlan p = tc_plan(I, J, R, must_split, terms);
   return p.splits > 1 || must_split ? (size_t)p.splits * I * part_pitch(J) * 4 : 0;
 }
+namespace {
 
 // dW from its partial products, four columns a thread, and db from the partial
 // column sums (the blocks after the first `wblocks`), all in a fixed order.
@@ -844,6 +841,7 @@ cudaError_t run_f32(const Product& g, const Epilogue& e, int64_t M, int64_t N, i
   return column_sums(static_cast<const float*>(g.A), g.sar, M, N, db, e.accumulate, part, st);
 }
 
+}  // namespace
 bool sizes_ok(int64_t M, int64_t N, int64_t K) {
   // 32-bit TMA coordinates, of three planes too, and tile counts
   constexpr int64_t top = 1ll << 29;
@@ -851,7 +849,6 @@ bool sizes_ok(int64_t M, int64_t N, int64_t K) {
          M <= (1ll << 40) / K && N <= (1ll << 40) / K;
 }
 
-}  // namespace
 }  // namespace lin
 }  // namespace ppo
 

@@ -58,5 +58,24 @@ cudaError_t tc_product(const Product& g, const Epilogue& e, const TcPlan& plan, 
                        float* db_part, int* err, int sms, cudaStream_t st, int64_t plane_a = 0,
                        int64_t plane_b = 0);
 
+// ---- what other products share (linear.cu) ------------------------------------------
+// A matrix that is copied, and the blocks that do it.  A product's two operands
+// take one launch (2,000 x 130 -> 250 forward: 15 us, 21 with a launch each).
+struct Copy {
+  const void* src;
+  int64_t ld, rows, cols, pitch, rows_pad;
+  uint4* dst;
+  int blocks;
+};
+int64_t pitch8(int64_t cols);
+// Workspace of a bf16 operand's copy onto 16-byte rows (0 where it needs none).
+size_t packed_bytes(int64_t rows, int64_t cols, int64_t ld);
+// the operand itself, or its copy in the workspace (advanced past it)
+Copy on_16_bytes(const void*& a, int64_t& ld, int64_t rows, int64_t cols, char*& work);
+cudaError_t pack(const Copy& a, const Copy& b, cudaStream_t st);
+// Bytes of a product's partial products (0 where its tiles are finished at once).
+size_t tc_part_bytes(int64_t I, int64_t J, int64_t R, bool must_split, int terms = 1);
+bool sizes_ok(int64_t M, int64_t N, int64_t K);
+
 }  // namespace lin
 }  // namespace ppo
