@@ -6,19 +6,27 @@ A block takes the residual stream x [T, N, D] of a rollout through a gated scan
     x <- x + Wo . scan(Wp . layernorm(x) + bp) + bo
     x <- x + W2 . act(W1 . layernorm(x) + b1) + b2
 
+or, gated, act(Wg . n + bg) * (Wu . n + bu) of n = layernorm(x) instead of
+act(W1 . n + b1): W1 then holds the rows of Wg and, below them, Wu's.
+
 RecurrentTrunk holds the parameters, what the forward pass leaves for the
 backward pass, and the workspaces, all allocated once: forward() and backward()
 run whole rollouts, step() advances carried states by one acting step.  None of
 them allocates or synchronises, so each can be captured in a CUDA graph, and
 step() shares only the parameters with the other two, so that it may run on a
 stream of its own between two load_params().
+
+ActionHead is a head over any number of actions on the trunk's output, with the
+clipped policy loss; GradClip clips the gradients of both together.
 """
 import math
 
-from . import (_abi, ppo_gated_scan_backward, ppo_gated_scan_forward, ppo_layernorm_backward,
+from . import (TensorList, _abi, ppo_action_logp, ppo_action_loss_grad, ppo_action_loss_workspace_bytes,
+               ppo_clip_grad_norm, ppo_gated_linear_backward_data, ppo_gated_linear_forward,
+               ppo_gated_linear_workspace_bytes, ppo_gated_scan_backward, ppo_gated_scan_forward, ppo_layernorm_backward,
                ppo_layernorm_backward_workspace_bytes, ppo_layernorm_forward,
                ppo_linear_backward_data, ppo_linear_backward_weight, ppo_linear_forward,
-               ppo_linear_workspace_bytes, ppo_scan_blocks, ppo_work_status)
+               ppo_grad_norm_workspace_bytes, ppo_linear_workspace_bytes, ppo_scan_blocks, ppo_work_status)
 
 ACTIVATIONS = {"none": _abi.ACT_NONE, "tanh": _abi.ACT_TANH, "relu": _abi.ACT_RELU,
                "silu": _abi.ACT_SILU, "gelu": _abi.ACT_GELU}
@@ -28,21 +36,22 @@ class RecurrentTrunk:
     """`blocks` blocks for rollouts of T steps of N environments.
 
     params and grads map (block, name) to fp32 tensors: the layer norms' g1, c1,
-    g2, c2 [D], the matrices Wp [2H, D], Wo [D, H], W1 [F, D], W2 [D, F] and
-    their biases bp, bo, b1, b2.  The matrices enter the products in `dtype`:
+    g2, c2 [D], the matrices Wp [2H, D], Wo [D, H], W1 [F, D] ([2F, D] where
+    `gated`), W2 [D, F] and their biases bp, bo, b1, b2.  The matrices enter the products in `dtype`:
     call load_params() after changing params.
     """
 
     def __init__(self, T, N, width, hidden, inner, blocks=1, dtype=None, act="gelu", eps=1e-5,
-                 device="cuda", generator=None):
+                 device="cuda", generator=None, gated=False):
         import torch
         self.T, self.N, self.D, self.H, self.F, self.blocks = T, N, width, hidden, inner, blocks
         self.dtype = dtype or torch.bfloat16
-        self.act, self.eps = ACTIVATIONS[act], eps
+        self.act, self.eps, self.gated = ACTIVATIONS[act], eps, gated
         D, H, F, M = width, hidden, inner, T * N
         f32 = dict(dtype=torch.float32, device=device)
         own = dict(dtype=self.dtype, device=device)
-        shapes = {"Wp": (2 * H, D), "Wo": (D, H), "W1": (F, D), "W2": (D, F)}
+        F1 = 2 * F if gated else F          # what W1 gives
+        shapes = {"Wp": (2 * H, D), "Wo": (D, H), "W1": (F1, D), "W2": (D, F)}
         self.params, self.grads, self._w = {}, {}, {}
         for b in range(blocks):
             for name, (rows, cols) in shapes.items():
@@ -62,9 +71,13 @@ class RecurrentTrunk:
             n1=torch.empty(M, D, **own), s1=torch.empty(M, 2, **f32),
             p=torch.empty(T, N, 2 * H, **own), h=torch.empty(T, N, H, **own),
             carry=torch.empty(ppo_scan_blocks(T), N, H, **f32), xm=torch.empty(M, D, **own),
-            n2=torch.empty(M, D, **own), s2=torch.empty(M, 2, **f32), u=torch.empty(M, F, **own),
-            a=torch.empty(M, F, **own), y=torch.empty(M, D, **own)) for _ in range(blocks)]
-        self._du, self._dn = torch.empty(M, F, **own), torch.empty(M, D, **own)
+            n2=torch.empty(M, D, **own), s2=torch.empty(M, 2, **f32), u=torch.empty(M, F1, **own),
+            y=torch.empty(M, D, **own)) for _ in range(blocks)]
+        # (a gated layer's output is computed once more backward: one buffer for all)
+        a = torch.empty(M, F, **own) if gated else None
+        for k in self._kept:
+            k["a"] = a if gated else torch.empty(M, F, **own)
+        self._du, self._dn = torch.empty(M, F1, **own), torch.empty(M, D, **own)
         self._dh, self._dp = torch.empty(T, N, H, **own), torch.empty(T, N, 2 * H, **own)
         self._dxm, self._dx = torch.empty(M, D, **own), torch.empty(M, D, **own)
         # one acting step
@@ -76,6 +89,8 @@ class RecurrentTrunk:
         def workspace(rows):
             need = max(ppo_linear_workspace_bytes(rows, r, c, self.dtype, ldz=D | 1 if name == "W2" else 0)
                        for name, (r, c) in shapes.items())
+            if gated:
+                need = max(need, ppo_gated_linear_workspace_bytes(rows, F, D, self.dtype, J=D, lddz=D | 1))
             return torch.zeros(need, dtype=torch.uint8, device=device)
 
         self._work, self._act_work = workspace(M), workspace(N)
@@ -110,8 +125,11 @@ class RecurrentTrunk:
             ppo_linear_forward(k["h"].view(M, -1), W[b, "Wo"], k["xm"], P[b, "bo"], res=x, work=work,
                                stream=st)
             ppo_layernorm_forward(k["xm"], P[b, "g2"], P[b, "c2"], k["n2"], k["s2"], self.eps, st)
-            ppo_linear_forward(k["n2"], W[b, "W1"], k["a"], P[b, "b1"], self.act, pre=k["u"], work=work,
-                               stream=st)
+            if self.gated:
+                ppo_gated_linear_forward(k["n2"], W[b, "W1"], k["a"], P[b, "b1"], self.act, k["u"], work, st)
+            else:
+                ppo_linear_forward(k["n2"], W[b, "W1"], k["a"], P[b, "b1"], self.act, pre=k["u"], work=work,
+                                   stream=st)
             ppo_linear_forward(k["a"], W[b, "W2"], k["y"], P[b, "b2"], res=k["xm"], work=work, stream=st)
             x = k["y"]
         return x.view(self.T, self.N, D)
@@ -128,8 +146,11 @@ class RecurrentTrunk:
         for b in reversed(range(self.blocks)):
             k = self._kept[b]
             x = x0 if b == 0 else self._kept[b - 1]["y"]
+            if self.gated:
+                ppo_gated_linear_backward_data(dy, W[b, "W2"], k["u"], self._du, self.act, k["a"], work, st)
             ppo_linear_backward_weight(dy, k["a"], G[b, "W2"], G[b, "b2"], work=work, stream=st)
-            ppo_linear_backward_data(dy, W[b, "W2"], self._du, k["u"], self.act, work=work, stream=st)
+            if not self.gated:
+                ppo_linear_backward_data(dy, W[b, "W2"], self._du, k["u"], self.act, work=work, stream=st)
             ppo_linear_backward_weight(self._du, k["n2"], G[b, "W1"], G[b, "b1"], work=work, stream=st)
             ppo_linear_backward_data(self._du, W[b, "W1"], self._dn, work=work, stream=st)
             ppo_layernorm_backward(self._dn, k["xm"], P[b, "g2"], k["s2"], self._dxm, G[b, "g2"],
@@ -157,7 +178,10 @@ class RecurrentTrunk:
             ppo_gated_scan_forward(o["p"], o["h"], state[b], None, done, state[b], None, st)
             ppo_linear_forward(o["h"][0], W[b, "Wo"], o["xm"], P[b, "bo"], res=x, work=work, stream=st)
             ppo_layernorm_forward(o["xm"], P[b, "g2"], P[b, "c2"], o["n"], None, self.eps, st)
-            ppo_linear_forward(o["n"], W[b, "W1"], o["a"], P[b, "b1"], self.act, work=work, stream=st)
+            if self.gated:
+                ppo_gated_linear_forward(o["n"], W[b, "W1"], o["a"], P[b, "b1"], self.act, None, work, st)
+            else:
+                ppo_linear_forward(o["n"], W[b, "W1"], o["a"], P[b, "b1"], self.act, work=work, stream=st)
             ppo_linear_forward(o["a"], W[b, "W2"], o["y"], P[b, "b2"], res=o["xm"], work=work, stream=st)
             x = o["y"]
         return x
@@ -173,3 +197,78 @@ class RecurrentTrunk:
                 failed.append(e)
         if failed:
             raise failed[0]
+
+
+class ActionHead:
+    """Logits of V actions for `rows` rows [rows, D] of a trunk's output, and the
+    clipped policy loss over them.
+
+    params and grads map "W" [V, D] and "b" [V] to fp32 tensors; W enters the
+    products in `dtype` (call load_params() after changing params).  logits(),
+    logp() and loss_grad() share the head's buffers and belong on one stream; none
+    of them allocates or synchronises.
+    """
+
+    def __init__(self, rows, width, actions, dtype=None, device="cuda", generator=None):
+        import torch
+        self.M, self.D, self.V = rows, width, actions
+        self.dtype = dtype or torch.bfloat16
+        f32 = dict(dtype=torch.float32, device=device)
+        own = dict(dtype=self.dtype, device=device)
+        self.params = {"W": torch.randn(actions, width, generator=generator, **f32) * (0.1 / math.sqrt(width)),
+                       "b": torch.zeros(actions, **f32)}
+        self.grads = {k: torch.empty_like(v) for k, v in self.params.items()}
+        self._w = torch.empty(actions, width, **own)
+        # rows of logits on 16-byte boundaries, whatever V
+        pitch = (actions + 7) // 8 * 8
+        self._l = torch.zeros(rows, pitch, **own)[:, :actions]
+        self._dx = torch.empty(rows, width, **own)
+        self._work = torch.zeros(ppo_linear_workspace_bytes(rows, actions, width, self.dtype, ldz=pitch),
+                                 dtype=torch.uint8, device=device)
+        self._loss_work = torch.empty(ppo_action_loss_workspace_bytes(), dtype=torch.uint8, device=device)
+        self.load_params()
+
+    def load_params(self):
+        """Rounds W to the products' type."""
+        self._w.copy_(self.params["W"])
+
+    def logits(self, x, stream=None):
+        """The logits [rows, V] of x [rows, D]: the head's own buffer."""
+        ppo_linear_forward(x.reshape(self.M, self.D), self._w, self._l, self.params["b"], work=self._work,
+                           stream=stream)
+        return self._l
+
+    def logp(self, x, action, logp, entropy=None, mask=None, stream=None):
+        """logp and entropy fp32 [rows] of action int32 [rows], as in ppo_action_logp."""
+        ppo_action_logp(self.logits(x, stream), action, logp, entropy, mask, stream)
+
+    def loss_grad(self, x, action, logp_old, adv, scale, stream=None, **loss):
+        """The gradient of the policy loss with respect to x [.., D] (the head's own
+        buffer), grads of W and b; `loss` as in ppo_action_loss_grad."""
+        rows = x.reshape(self.M, self.D)
+        logits = self.logits(rows, stream)
+        ppo_action_loss_grad(logits, action, logp_old, adv, logits, scale, work=self._loss_work, stream=stream,
+                             **loss)
+        ppo_linear_backward_weight(logits, rows, self.grads["W"], self.grads["b"], work=self._work, stream=stream)
+        ppo_linear_backward_data(logits, self._w, self._dx, work=self._work, stream=stream)
+        return self._dx.view(x.shape)
+
+    def check(self, stream=None):
+        """Synchronises the stream; raises PpoError if a bounded device wait gave up."""
+        ppo_work_status(self._work, stream)
+
+
+class GradClip:
+    """Clips the gradients of several parts (a RecurrentTrunk, an ActionHead) to one
+    norm: clip(max_norm) scales them in place and leaves the norm in `norm`."""
+
+    def __init__(self, *parts):
+        import torch
+        self.grads = TensorList(g for part in parts for g in part.grads.values())
+        device = self.grads.tensors[0].device
+        self.norm = torch.zeros(1, dtype=torch.float32, device=device)
+        self._work = torch.empty(ppo_grad_norm_workspace_bytes(self.grads), dtype=torch.uint8, device=device)
+
+    def clip(self, max_norm, stream=None):
+        ppo_clip_grad_norm(self.grads, max_norm, self.norm, work=self._work, stream=stream)
+        return self.norm
