@@ -11,15 +11,17 @@
 #include <math_constants.h>
 
 #include "ops.cuh"
+#include "tc_ptx.cuh"
 
 namespace ppo {
 namespace {
 
 using namespace ops;
 
-constexpr int kRowThreads = 128;
+constexpr int kRowThreads = 128;     // block of the kernels that give a row to lanes of a warp
 constexpr int kMaxBlocks = 1216;     // blocks of a call: rows are walked by their stride
 constexpr int kTerms = 8;            // sums of d_stats
+constexpr int kMaxCluster = 8;
 
 struct ActionArgs {
   const void* l;
@@ -33,148 +35,501 @@ struct ActionArgs {
   void* dl;
   int64_t lddl;
   float *logp, *entropy;
-  double* part;                      // [blocks][kTerms]
+  float* part;                       // [kTerms][blocks]
 };
 
 // A row's statistics: maximum, sum of e^d, sum of e^d d.
 struct Stat {
   float m, s, t;
 };
-// (d = -inf of an action that is not allowed: e^d d is 0 there, not NaN)
-__device__ __forceinline__ float held(float d) { return fmaxf(d, -1e30f); }
 // maximum that the deviations are taken from: 0 in a row without any
 __device__ __forceinline__ float base_of(float m) { return m == -CUDART_INF_F ? 0.f : m; }
 
-// What a row's gradient and sums need beyond its logits.
+// What a row's gradient needs beyond its logits.
 struct RowTerms {
   float a0, a1, hot;       // gradient: e^d (a1 d + a0), + hot at the action
   bool kept;
 };
-// x: the logit of the row's action (-inf where it is not allowed); one thread.
-// Adds the row's terms to sums where they are wanted.
-__device__ __forceinline__ RowTerms row_terms(const ActionArgs& p, int64_t row, const Stat& st, float x,
-                                              bool has, double (&sums)[kTerms]) {
+// A row's own numbers, fetched ahead of its statistics (the same in all its threads).
+struct RowInput {
+  int a;                   // its action, -1: none
+  float x;                 // the action's logit, -inf where it is not allowed
+  float old, adv, ref, w;
+};
+// A thread's sums over rows, in shared memory (only a row's first thread has any),
+// compensated (Kahan): an add costs four fp32 operations, where one in 64 bits would
+// hold the FP64 units for 15 clocks.
+struct RowSums {
+  float2* at;              // [kTerms], `step` apart: sum and compensation
+  int step;
+  __device__ __forceinline__ void add(int i, float x) {
+    const float2 s = at[i * step];
+    const float y = x - s.y, t = s.x + y, r = (t - s.x) - y;
+    at[i * step] = make_float2(t, fabsf(t) < CUDART_INF_F ? r : 0.f);
+  }
+};
+
+// Every thread of a row takes its terms; `lead` writes what the row gives and adds it up.
+__device__ __forceinline__ RowTerms row_terms(const ActionArgs& p, int64_t row, const Stat& st, const RowInput& in,
+                                              bool lead, RowSums sums) {
   RowTerms r{0.f, 0.f, 0.f, false};
+  const bool has = in.a >= 0;
   const float base = base_of(st.m), logs = logf(st.s);
   const float H = st.s == 0.f ? 0.f : logs - st.t / st.s;
-  const float lp = has ? (x == -CUDART_INF_F ? x : (x - base) - logs) : 0.f;
-  if (p.logp) p.logp[row] = lp;
-  if (p.entropy) p.entropy[row] = H;
+  const float lp = has ? (in.x == -CUDART_INF_F ? in.x : (in.x - base) - logs) : 0.f;
+  if (lead) {
+    if (p.logp) p.logp[row] = lp;
+    if (p.entropy) p.entropy[row] = H;
+  }
   if (!p.dl) return r;
   if (!has || lp == -CUDART_INF_F) {
-    sums[7] += 1.0;
+    if (lead && p.part) sums.add(7, 1.f);
     return r;
   }
-  const float w = p.weight ? p.weight[row] : 1.f;
-  if (w == 0.f) return r;
-  const float A = p.adv[row], u = lp - p.old[row], ratio = expf(u);
-  const float s1 = ratio * A, s2 = fminf(fmaxf(ratio, p.lo), p.hi) * A;
+  if (in.w == 0.f) return r;
+  const float u = lp - in.old, ratio = expf(u);
+  const float s1 = ratio * in.adv, s2 = fminf(fmaxf(ratio, p.lo), p.hi) * in.adv;
   const float pg = s1 <= s2 ? -s1 : -s2;       // (NaN comes through s2)
   float c = s1 <= s2 ? -s1 : s1 != s1 ? s1 : 0.f, kl = 0.f;
   if (p.ref) {
-    const float y = p.ref[row] - lp, em = expm1f(y);
+    const float y = in.ref - lp, em = expm1f(y);
     kl = em - y;
     c -= p.kl * em;
   }
-  const float W = p.scale * w;
-  const double Wd = (double)p.scale * w;
-  sums[0] += Wd * ((double)pg + (double)p.kl * kl - (double)p.ent * H);
-  sums[1] += Wd * pg;
-  sums[2] += Wd * kl;
-  sums[3] += Wd * H;
-  sums[4] += ratio < p.lo || ratio > p.hi ? Wd : 0.0;
-  sums[5] += Wd * (expm1f(u) - u);
-  sums[6] += Wd;
+  const float W = p.scale * in.w;
+  if (lead && p.part) {
+    sums.add(0, W * (pg + p.kl * kl - p.ent * H));
+    sums.add(1, W * pg);
+    sums.add(2, W * kl);
+    sums.add(3, W * H);
+    sums.add(4, ratio < p.lo || ratio > p.hi ? W : 0.f);
+    sums.add(5, W * (expm1f(u) - u));
+    sums.add(6, W);
+  }
   r.kept = true;
   r.hot = W * c;
-  r.a1 = W * p.ent / st.s;
-  r.a0 = W * (p.ent * (H - logs) - c) / st.s;
+  const float k = W / st.s;
+  r.a1 = k * p.ent;
+  r.a0 = k * (p.ent * (H - logs) - c);
   return r;
 }
 
-// ---- a block for a row ---------------------------------------------------------------
-__device__ __forceinline__ float block_max(float v, float* s) {
+// ---- pieces of 16 bytes ------------------------------------------------------------------
+// A row is handled as the aligned 16-byte pieces that hold it; its first and last
+// piece may hold elements that are not its own, which count as -inf.
+template <typename T>
+struct Piece {
+  static constexpr int E = 16 / (int)sizeof(T);
+  static constexpr uint32_t kNone = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;     // -inf
+  uint32_t w[4];
+  __device__ __forceinline__ void none() {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-  if (threadIdx.x % kWarp == 0) s[threadIdx.x / kWarp] = v;
-  __syncthreads();
-  v = s[0];
-  for (int w = 1; w < kRowThreads / kWarp; ++w) v = fmaxf(v, s[w]);
-  __syncthreads();
-  return v;
+    for (int i = 0; i < 4; ++i) w[i] = kNone;
+  }
+  // element i becomes -inf
+  __device__ __forceinline__ void drop(int i) {
+    if constexpr (sizeof(T) == 2) w[i / 2] = i & 1 ? (w[i / 2] & 0xffffu) | 0xff800000u : (w[i / 2] & 0xffff0000u) | 0xff80u;
+    else w[i] = kNone;
+  }
+  __device__ __forceinline__ float2 pair(int i) const {      // elements 2 i, 2 i + 1
+    if constexpr (sizeof(T) == 2) return make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+    else return make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+  }
+  __device__ __forceinline__ void put(int i, float2 v) {
+    if constexpr (sizeof(T) == 2) w[i] = pack_bf16x2(v.x, v.y);
+    else {
+      w[2 * i] = __float_as_uint(v.x);
+      w[2 * i + 1] = __float_as_uint(v.y);
+    }
+  }
+  __device__ __forceinline__ float max() const {
+    if constexpr (sizeof(T) == 2) {
+      auto h = [&](int i) { return *reinterpret_cast<const __nv_bfloat162*>(&w[i]); };
+      const __nv_bfloat162 m = __hmax2(__hmax2(h(0), h(1)), __hmax2(h(2), h(3)));
+      return fmaxf(__low2float(m), __high2float(m));
+    } else {
+      auto f = [&](int i) { return __uint_as_float(w[i]); };
+      return fmaxf(fmaxf(f(0), f(1)), fmaxf(f(2), f(3)));
+    }
+  }
+};
+// (not through L1, and not as read-only data: the gradient may go to the same place)
+__device__ __forceinline__ void load16(const void* p, uint32_t (&w)[4]) {
+  asm volatile("ld.global.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+               : "l"(p));
 }
-__device__ __forceinline__ float block_sum(float v, float* s) {
-  v = warp_sum(v);
-  if (threadIdx.x % kWarp == 0) s[threadIdx.x / kWarp] = v;
-  __syncthreads();
-  v = 0.f;
-  for (int w = 0; w < kRowThreads / kWarp; ++w) v += s[w];
-  __syncthreads();
-  return v;
+__device__ __forceinline__ void store16(void* p, const uint32_t (&w)[4]) {
+  asm volatile("st.global.v4.b32 [%0], {%1, %2, %3, %4};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+               : "memory");
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kRowThreads) action_rows_kernel(const ActionArgs p) {
-  __shared__ float red[kRowThreads / kWarp];
-  __shared__ RowTerms terms;
-  double sums[kTerms] = {};
-  pdl_wait();
-  for (int64_t row = blockIdx.x; row < p.M; row += gridDim.x) {
-    const T* l = static_cast<const T*>(p.l) + row * p.ld;
-    const uint8_t* k = p.mask ? p.mask + row * p.ldm : nullptr;
-    auto at = [&](int j) { return k && !k[j] ? -CUDART_INF_F : (float)l[j]; };
-    const int a = p.action ? p.action[row] : -1;
-    const bool has = a >= 0 && a < p.V;
-    Stat st{-CUDART_INF_F, 0.f, 0.f};
-    for (int j = threadIdx.x; j < p.V; j += kRowThreads) st.m = fmaxf(st.m, at(j));
-    st.m = block_max(st.m, red);
-    const float base = base_of(st.m);
-    for (int j = threadIdx.x; j < p.V; j += kRowThreads) {
-      const float d = at(j) - base, e = __expf(d);
-      st.s += e;
-      st.t += e * held(d);
+// Bit i: element j + i of a row is allowed (i < E; the row's own elements alone are
+// looked at).  The aligned words that hold the bytes, where they lie inside the mask.
+template <int E>
+__device__ __forceinline__ uint32_t allowed(const uint8_t* row, int j, int V, const uint8_t* from,
+                                            const uint8_t* to) {
+  using Word = typename RawOf<E>::type;       // 4 or 8 bytes
+  const uint8_t* at = row + j;
+  const int sh = (int)(reinterpret_cast<uintptr_t>(at) & (E - 1));
+  const uint8_t* a = at - sh;
+  uint32_t bits = 0;
+  if (j >= 0 && j + E <= V && a >= from && a + 2 * E <= to) {
+    uint32_t b[4] = {};
+    const Word x = *reinterpret_cast<const Word*>(a);
+    memcpy(b, &x, E);
+    if (sh) {
+      const Word y = *reinterpret_cast<const Word*>(a + E);
+      memcpy(b + E / 4, &y, E);
     }
-    st.s = block_sum(st.s, red);
-    st.t = block_sum(st.t, red);
-    if (threadIdx.x == 0) terms = row_terms(p, row, st, has ? at(a) : 0.f, has, sums);
-    __syncthreads();
-    if (p.dl) {
-      const RowTerms r = terms;
-      T* o = static_cast<T*>(p.dl) + row * p.lddl;
-      for (int j = threadIdx.x; j < p.V; j += kRowThreads) {
-        const float x = at(j), d = x - base;
-        float g = __expf(d) * fmaf(r.a1, held(d), r.a0);
-        if (j == a) g += r.hot;
-        if (!r.kept || (k && !k[j])) g = 0.f;
-        round_to(g, o[j]);
+    if constexpr (E == 8) {
+      if (sh & 4) {
+        b[0] = b[1];
+        b[1] = b[2];
+        b[2] = b[3];
       }
     }
-    __syncthreads();
+    const int s = 8 * (sh & 3);
+#pragma unroll
+    for (int i = 0; i < E / 4; ++i) {
+      const uint32_t v = __funnelshift_r(b[i], b[i + 1], s);
+      // 0x80 in each byte that is not 0, then those bits side by side
+      const uint32_t nz = (((v & 0x7f7f7f7fu) + 0x7f7f7f7fu) | v) & 0x80808080u;
+      bits |= ((nz >> 7) * 0x10204080u >> 28) << (4 * i);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < E; ++i)
+      if (j + i >= 0 && j + i < V && at[i]) bits |= 1u << i;
   }
-  if (p.part && threadIdx.x == 0) {
-    for (int i = 0; i < kTerms; ++i) p.part[(int64_t)blockIdx.x * kTerms + i] = sums[i];
+  return bits;
+}
+
+// ---- reductions over a row's threads ---------------------------------------------------
+template <int G>
+__device__ __forceinline__ float lanes_max(float v) {
+  if constexpr (G == kWarp) {
+    // in the order of integers; no NaN comes here
+    const int b = __float_as_int(v), o = __reduce_max_sync(0xffffffffu, b >= 0 ? b : b ^ 0x7fffffff);
+    return __int_as_float(o >= 0 ? o : o ^ 0x7fffffff);
+  } else {
+#pragma unroll
+    for (int o = G / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+  }
+}
+template <int G>
+__device__ __forceinline__ float lanes_sum(float v) {
+#pragma unroll
+  for (int o = G / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {      // NaN where one is
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+constexpr float kLog2e = 1.4426950408889634f;
+// d and e^d of a pair: the difference is taken before the scaling, so that large
+// logits keep their digits
+__device__ __forceinline__ float2 exp_pair(float2 x, float base, float2& d) {
+  d = ptx::ffma2(x, make_float2(1.f, 1.f), make_float2(-base, -base));
+  d.x = max_nan(d.x, -1e30f);
+  d.y = max_nan(d.y, -1e30f);
+  float2 e = ptx::fmul2(d, make_float2(kLog2e, kLog2e));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(e.x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(e.y));
+  return e;
+}
+
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void put_remote(uint32_t addr, uint32_t rank, float a, float b, float c) {
+  asm volatile(
+      "{\n\t.reg .b32 r;\n\tmapa.shared::cluster.u32 r, %0, %1;\n\t"
+      "st.shared::cluster.v4.f32 [r], {%2, %3, %4, %4};\n\t}" ::"r"(addr),
+      "r"(rank), "f"(a), "f"(b), "f"(c)
+      : "memory");
+}
+
+// A row belongs to G threads (lanes of a warp, a block, or all blocks of a cluster),
+// each of which keeps up to GR of its 16-byte pieces in registers between the
+// statistics and the gradient, so that the row is read once.
+template <typename T, int G, int GR>
+__global__ void __launch_bounds__(G <= kWarp ? kRowThreads : G, G <= kWarp ? 8 : GR > 8 ? 1 : 1024 / G)
+action_kernel(const ActionArgs p) {
+  using P = Piece<T>;
+  constexpr int E = P::E;
+  constexpr bool kLanes = G <= kWarp;
+  constexpr int R = kLanes ? kRowThreads / G : 1;       // rows of a block at a time
+  constexpr int NW = kLanes ? 1 : G / kWarp;
+  __shared__ float4 entry[2][kLanes ? 1 : kMaxCluster * NW];
+  __shared__ float2 sum[kTerms][R];
+  const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp;
+  const int t = kLanes ? threadIdx.x % G : threadIdx.x;
+  const uint32_t cn = kLanes ? 1 : cluster_size(), cr = kLanes ? 0 : cluster_rank();
+  const int64_t stride = (int64_t)(gridDim.x / cn) * R;
+  const bool lead_thread = t == 0 && cr == 0;
+  const RowSums sums{&sum[0][kLanes ? threadIdx.x / G : 0], R};
+  if (t == 0) {
+    for (int i = 0; i < kTerms; ++i) sums.at[i * R] = make_float2(0.f, 0.f);
+  }
+  const uint8_t* mend = p.mask ? p.mask + (p.M - 1) * p.ldm + p.V : nullptr;
+  const char* lfrom = static_cast<const char*>(p.l);
+  const char* lto = lfrom + ((p.M - 1) * p.ld + p.V) * (int64_t)sizeof(T);
+  if (cn > 1) {        // the other blocks' shared memory is there
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  }
+  pdl_wait();
+  uint32_t par = 0;
+  for (int64_t row0 = (int64_t)(blockIdx.x / cn) * R; row0 < p.M; row0 += stride, par ^= 1) {
+    const int64_t mine = kLanes ? row0 + threadIdx.x / G : row0;
+    const bool active = mine < p.M;
+    const int64_t row = active ? mine : p.M - 1;
+    const char* la = lfrom + row * p.ld * (int64_t)sizeof(T);
+    const int off = (int)(reinterpret_cast<uintptr_t>(la) & 15) / (int)sizeof(T);
+    const char* lp = la - off * (int)sizeof(T);
+    const int nq = (off + p.V + E - 1) / E;
+    const uint8_t* mrow = p.mask ? p.mask + row * p.ldm : nullptr;
+    const int step = G * (int)cn, q0 = (int)cr * G + t;
+    P x[GR];
+#pragma unroll
+    for (int k = 0; k < GR; ++k) {
+      const int q = q0 + k * step;
+      x[k].none();
+      if (q < nq) {
+        const char* at = lp + (int64_t)q * 16;
+        if (at >= lfrom && at + 16 <= lto) {
+          load16(at, x[k].w);
+        } else {       // the matrix's first or last piece
+          const T* o = reinterpret_cast<const T*>(la);
+#pragma unroll
+          for (int i = 0; i < E; ++i) {
+            const int j = q * E + i - off;
+            if (j >= 0 && j < p.V) {
+              if constexpr (sizeof(T) == 2) {
+                const uint32_t b = __bfloat16_as_ushort(o[j]);
+                x[k].w[i / 2] = i & 1 ? (x[k].w[i / 2] & 0xffffu) | b << 16 : (x[k].w[i / 2] & 0xffff0000u) | b;
+              } else {
+                x[k].w[i] = __float_as_uint(o[j]);
+              }
+            }
+          }
+        }
+      }
+    }
+    RowInput in{-1, 0.f, 0.f, 0.f, 0.f, 1.f};
+    if (p.action) {
+      const int a = p.action[row];
+      if (a >= 0 && a < p.V) {
+        in.a = a;
+        in.x = mrow && !mrow[a] ? -CUDART_INF_F : (float)reinterpret_cast<const T*>(la)[a];
+      }
+    }
+    if (p.dl) {
+      in.old = p.old[row];
+      in.adv = p.adv[row];
+      if (p.ref) in.ref = p.ref[row];
+      if (p.weight) in.w = p.weight[row];
+    }
+#pragma unroll
+    for (int k = 0; k < GR; ++k) {
+      const int q = q0 + k * step;
+      if (mrow && q < nq) {
+        const uint32_t ok = allowed<E>(mrow, q * E - off, p.V, p.mask, mend);
+#pragma unroll
+        for (int i = 0; i < E; ++i)
+          if (!(ok >> i & 1)) x[k].drop(i);
+      } else if (q == 0 || q == nq - 1) {
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+          const int j = q * E + i - off;
+          if (j < 0 || j >= p.V) x[k].drop(i);
+        }
+      }
+    }
+    // statistics
+    Stat st{-CUDART_INF_F, 0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < GR; ++k) st.m = fmaxf(st.m, x[k].max());
+    st.m = lanes_max<kLanes ? G : kWarp>(st.m);
+    float2 s2 = make_float2(0.f, 0.f), t2 = make_float2(0.f, 0.f);
+    {
+      const float base = base_of(st.m);
+#pragma unroll
+      for (int k = 0; k < GR; ++k) {
+        if (q0 - t + k * step >= nq) break;       // (the same in all threads)
+#pragma unroll
+        for (int i = 0; i < E / 2; ++i) {
+          float2 d;
+          const float2 e = exp_pair(x[k].pair(i), base, d);
+          s2 = ptx::ffma2(e, make_float2(1.f, 1.f), s2);
+          t2 = ptx::ffma2(e, d, t2);
+        }
+      }
+    }
+    st.s = lanes_sum<kLanes ? G : kWarp>(s2.x + s2.y);
+    st.t = lanes_sum<kLanes ? G : kWarp>(t2.x + t2.y);
+    if constexpr (!kLanes) {
+      // every warp's statistics to every block of the row; then each warp joins them all
+      // (two sets in turn: a warp may still be reading the last row's)
+      if (lane < (int)cn) put_remote(ptx::smem_u32(&entry[par][cr * NW + warp]), lane, st.m, st.s, st.t);
+      if (cn > 1) {
+        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+      } else {
+        __syncthreads();
+      }
+      constexpr int PER = (kMaxCluster * NW + kWarp - 1) / kWarp;
+      float4 v[PER];
+      float m = -CUDART_INF_F;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        const int w = lane + i * kWarp;
+        v[i] = w < (int)cn * NW ? entry[par][w] : make_float4(-CUDART_INF_F, 0.f, 0.f, 0.f);
+        m = fmaxf(m, v[i].x);
+      }
+      m = lanes_max<kWarp>(m);
+      float s = 0.f, u = 0.f;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        // (a warp that saw nothing allowed counted from 0: its sums are 0, or NaN)
+        const bool none = v[i].x == -CUDART_INF_F;
+        const float d = none ? 0.f : max_nan(v[i].x - m, -1e30f), f = none ? 1.f : __expf(d);
+        s += f * v[i].y;
+        u += f * fmaf(v[i].y, d, v[i].z);
+      }
+      st.m = m;
+      st.s = lanes_sum<kWarp>(s);
+      st.t = lanes_sum<kWarp>(u);
+    }
+    const RowTerms r = row_terms(p, row, st, in, lead_thread && active, sums);
+    if (!p.dl || !active) continue;
+    // the gradient, over the logits' registers
+    const float base = base_of(st.m);
+    char* oa = static_cast<char*>(p.dl) + row * p.lddl * (int64_t)sizeof(T);
+    const bool same = (reinterpret_cast<uintptr_t>(oa) & 15) == (reinterpret_cast<uintptr_t>(la) & 15);
+    char* op = oa - off * (int)sizeof(T);
+    const int aq = in.a >= 0 ? (in.a + off) / E : -1, ai = (in.a + off) % E;
+#pragma unroll
+    for (int k = 0; k < GR; ++k) {
+      const int q = q0 + k * step;
+      if (q >= nq) break;
+      P g;
+#pragma unroll
+      for (int i = 0; i < E / 2; ++i) {
+        const float2 l = x[k].pair(i);
+        float2 d;
+        const float2 e = exp_pair(l, base, d);
+        float2 v = ptx::fmul2(e, ptx::ffma2(d, make_float2(r.a1, r.a1), make_float2(r.a0, r.a0)));
+        if (q == aq) {
+          v.x += ai == 2 * i ? r.hot : 0.f;
+          v.y += ai == 2 * i + 1 ? r.hot : 0.f;
+        }
+        if (!r.kept) v = make_float2(0.f, 0.f);
+        if (mrow) {       // (of a row that is NaN too)
+          v.x = l.x == -CUDART_INF_F ? 0.f : v.x;
+          v.y = l.y == -CUDART_INF_F ? 0.f : v.y;
+        }
+        g.put(i, v);
+      }
+      const int j0 = q * E - off;
+      if (same && j0 >= 0 && j0 + E <= p.V) {
+        store16(op + (int64_t)q * 16, g.w);
+      } else {
+        T* o = reinterpret_cast<T*>(oa);
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+          const int j = j0 + i;
+          if (j < 0 || j >= p.V) continue;
+          if constexpr (sizeof(T) == 2) o[j] = __ushort_as_bfloat16((uint16_t)(g.w[i / 2] >> (16 * (i & 1))));
+          else o[j] = __uint_as_float(g.w[i]);
+        }
+      }
+    }
+  }
+  if (!p.part) return;
+  // the block's sums, in order
+  __syncthreads();
+  if (threadIdx.x < kTerms) {
+    float v = 0.f;
+    for (int w = 0; w < R; ++w) v += sum[threadIdx.x][w].x;
+    p.part[(int64_t)threadIdx.x * gridDim.x + blockIdx.x] = v;
   }
 }
 
 // d_stats from the blocks' sums: a warp for each of them, in a fixed order.
 __global__ void __launch_bounds__(kTerms * kWarp)
-action_stats_kernel(const double* __restrict__ part, int blocks, float* __restrict__ stats) {
+action_stats_kernel(const float* __restrict__ part, int blocks, float* __restrict__ stats) {
   pdl_wait();
   const int i = threadIdx.x / kWarp, lane = threadIdx.x % kWarp;
-  double v = 0.0;
-  for (int b = lane; b < blocks; b += kWarp) v += part[(int64_t)b * kTerms + i];
+  float v[4] = {};
+  for (int b = lane; b < blocks; b += 4 * kWarp) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if (lane == 0) stats[i] = (float)v;
+    for (int u = 0; u < 4; ++u)
+      if (b + u * kWarp < blocks) v[u] += part[(int64_t)i * blocks + b + u * kWarp];
+  }
+  const float s = warp_sum((v[0] + v[1]) + (v[2] + v[3]));
+  if (lane == 0) stats[i] = s;
+}
+
+// ---- launch ------------------------------------------------------------------------------
+constexpr int kSms = 152;
+
+template <typename T, int G, int GR>
+cudaError_t go(const ActionArgs& p, int cn, float* stats, cudaStream_t st) {
+  constexpr int R = G <= kWarp ? kRowThreads / G : 1;
+  // two blocks of 512 threads an SM, or as many threads in smaller ones
+  constexpr int top = G <= kWarp ? kMaxBlocks : kSms * (GR > 8 ? 1 : 1024 / G);
+  const int64_t want = (p.M + R - 1) / R;
+  const int blocks = (int)std::min<int64_t>(want, top / cn) * cn;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)blocks);
+  cfg.blockDim = dim3(G <= kWarp ? kRowThreads : G);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)cn;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cn > 1 ? 2 : 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, action_kernel<T, G, GR>, p);
+  if (e != cudaSuccess || !stats) return e;
+  return launch_pdl(action_stats_kernel, dim3(1), dim3(kTerms * kWarp), 0, st, (const float*)p.part, blocks, stats);
 }
 
 template <typename T>
 cudaError_t run_rows(const ActionArgs& p, float* stats, cudaStream_t st) {
-  const int blocks = (int)std::min<int64_t>(p.M, kMaxBlocks);
-  cudaError_t e = launch_pdl(action_rows_kernel<T>, dim3((unsigned)blocks), dim3(kRowThreads), 0, st, p);
-  if (e != cudaSuccess || !stats) return e;
-  return launch_pdl(action_stats_kernel, dim3(1), dim3(kTerms * kWarp), 0, st, (const double*)p.part, blocks,
-                    stats);
+  constexpr int E = Piece<T>::E;
+  const bool aligned = al16(p.l) && p.ld % E == 0;
+  const int64_t nq = (p.V + E - 1) / E + (aligned ? 0 : 1);       // pieces of a row at most
+  if (nq <= 4) return go<T, 4, 1>(p, 1, stats, st);
+  if (nq <= 8) return go<T, 4, 2>(p, 1, stats, st);
+  if (nq <= 16) return go<T, 8, 2>(p, 1, stats, st);
+  if (nq <= 32) return go<T, 8, 4>(p, 1, stats, st);
+  if (nq <= 64) return go<T, 32, 2>(p, 1, stats, st);
+  if (nq <= 128) return go<T, 32, 4>(p, 1, stats, st);
+  if (nq <= 256) return go<T, 32, 8>(p, 1, stats, st);
+  if (nq <= 512) return go<T, 128, 4>(p, 1, stats, st);
+  // few rows: more blocks for each, down to two pieces a thread
+  const bool few = p.M < kSms;
+  if (nq <= 1024 && !few) return go<T, 128, 8>(p, 1, stats, st);
+  if (nq <= 2048 && !few) return go<T, 256, 8>(p, 1, stats, st);
+  int cn = 1;
+  while (cn < kMaxCluster && (nq > 4096 * cn || (p.M * cn * 2 <= kSms && nq > 1024 * cn))) cn *= 2;
+  return nq <= 4096 * cn ? go<T, 512, 8>(p, cn, stats, st) : go<T, 512, 16>(p, cn, stats, st);
 }
 cudaError_t run_any(int32_t dtype, const ActionArgs& p, float* stats, cudaStream_t st) {
   return dtype == PPO_DTYPE_F32 ? run_rows<float>(p, stats, st) : run_rows<__nv_bfloat16>(p, stats, st);
@@ -193,7 +548,7 @@ ppo_status rows_ok(int32_t dtype, const void* l, int64_t ld, int64_t M, int64_t 
     if (!on(r, 4)) return PPO_ERR_ALIGN;
   return PPO_OK;
 }
-constexpr size_t kActionWork = (size_t)kMaxBlocks * kTerms * sizeof(double);
+constexpr size_t kActionWork = (size_t)kMaxBlocks * kTerms * sizeof(float);
 
 }  // namespace
 }  // namespace ppo
@@ -268,7 +623,7 @@ ppo_status ppo_action_loss_grad(int32_t dtype, const void* logits, int64_t ld, i
   p.lddl = lddl;
   p.logp = logp;
   p.entropy = entropy;
-  p.part = stats ? static_cast<double*>(work) : nullptr;
+  p.part = stats ? static_cast<float*>(work) : nullptr;
   return ops::status_of(run_any(dtype, p, stats, st));
 }
 
