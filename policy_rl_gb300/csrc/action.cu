@@ -164,23 +164,31 @@ __device__ __forceinline__ void store16(void* p, const uint32_t (&w)[4]) {
                : "memory");
 }
 
-// Bit i: element j + i of a row is allowed (i < E; the row's own elements alone are
-// looked at).  The aligned words that hold the bytes, where they lie inside the mask.
-template <int E>
-__device__ __forceinline__ uint32_t allowed(const uint8_t* row, int j, int V, const uint8_t* from,
-                                            const uint8_t* to) {
+// PRMT with a sign selector (8 + byte): that byte's top bit, eight times
+__device__ __forceinline__ uint32_t spread(uint32_t v, uint32_t selector) {
+  uint32_t r;
+  asm("prmt.b32 %0, %1, %1, %2;" : "=r"(r) : "r"(v), "r"(selector));
+  return r;
+}
+// Elements of a piece that are not allowed become -inf: element i is the row's j + i.
+// Its mask bytes are taken as the aligned words that hold them where those lie inside
+// the mask's [from, to), else one by one.
+template <typename T>
+__device__ __forceinline__ void cover(Piece<T>& x, const uint8_t* row, int j, int V, const uint8_t* from,
+                                      const uint8_t* to) {
+  constexpr int E = Piece<T>::E;
   using Word = typename RawOf<E>::type;       // 4 or 8 bytes
   const uint8_t* at = row + j;
   const int sh = (int)(reinterpret_cast<uintptr_t>(at) & (E - 1));
   const uint8_t* a = at - sh;
-  uint32_t bits = 0;
+  uint32_t v[E / 4];
   if (j >= 0 && j + E <= V && a >= from && a + 2 * E <= to) {
-    uint32_t b[4] = {};
-    const Word x = *reinterpret_cast<const Word*>(a);
-    memcpy(b, &x, E);
+    uint32_t b[E / 4 + 1 + (E == 8)] = {};
+    const Word w0 = *reinterpret_cast<const Word*>(a);
+    memcpy(b, &w0, E);
     if (sh) {
-      const Word y = *reinterpret_cast<const Word*>(a + E);
-      memcpy(b + E / 4, &y, E);
+      const Word w1 = *reinterpret_cast<const Word*>(a + E);
+      memcpy(b + E / 4, &w1, E);
     }
     if constexpr (E == 8) {
       if (sh & 4) {
@@ -189,20 +197,35 @@ __device__ __forceinline__ uint32_t allowed(const uint8_t* row, int j, int V, co
         b[2] = b[3];
       }
     }
-    const int s = 8 * (sh & 3);
 #pragma unroll
-    for (int i = 0; i < E / 4; ++i) {
-      const uint32_t v = __funnelshift_r(b[i], b[i + 1], s);
-      // 0x80 in each byte that is not 0, then those bits side by side
-      const uint32_t nz = (((v & 0x7f7f7f7fu) + 0x7f7f7f7fu) | v) & 0x80808080u;
-      bits |= ((nz >> 7) * 0x10204080u >> 28) << (4 * i);
-    }
+    for (int i = 0; i < E / 4; ++i) v[i] = __funnelshift_r(b[i], b[i + 1], 8 * (sh & 3));
   } else {
 #pragma unroll
-    for (int i = 0; i < E; ++i)
-      if (j + i >= 0 && j + i < V && at[i]) bits |= 1u << i;
+    for (int i = 0; i < E / 4; ++i) {
+      v[i] = 0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int e = j + 4 * i + k;
+        if (e >= 0 && e < V && row[e]) v[i] |= 1u << (8 * k);
+      }
+    }
   }
-  return bits;
+#pragma unroll
+  for (int i = 0; i < E / 4; ++i) {
+    // the top bit of each byte that is not 0, spread over the element by PRMT's sign mode
+    const uint32_t nz = ((v[i] & 0x7f7f7f7fu) + 0x7f7f7f7fu) | v[i];
+    if constexpr (sizeof(T) == 2) {
+      const uint32_t m0 = spread(nz, 0x9988), m1 = spread(nz, 0xbbaa);
+      x.w[2 * i] = (x.w[2 * i] & m0) | (Piece<T>::kNone & ~m0);
+      x.w[2 * i + 1] = (x.w[2 * i + 1] & m1) | (Piece<T>::kNone & ~m1);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t m = spread(nz, 0x8888 + 0x1111 * k);
+        x.w[k] = (x.w[k] & m) | (Piece<T>::kNone & ~m);
+      }
+    }
+  }
 }
 
 // ---- reductions over a row's threads ---------------------------------------------------
@@ -234,12 +257,41 @@ constexpr float kLog2e = 1.4426950408889634f;
 // logits keep their digits
 __device__ __forceinline__ float2 exp_pair(float2 x, float base, float2& d) {
   d = ptx::ffma2(x, make_float2(1.f, 1.f), make_float2(-base, -base));
-  d.x = max_nan(d.x, -1e30f);
-  d.y = max_nan(d.y, -1e30f);
   float2 e = ptx::fmul2(d, make_float2(kLog2e, kLog2e));
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(e.x));
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(e.y));
   return e;
+}
+
+// Pieces are made safe for e^d d and e^d (a1 d + a0), which would be NaN at d = -inf:
+// nothing below kLow is left in them.  In a warp whose maximum m is ordinary that
+// is all; where it is not (from 1e25 on neighbouring floats are further apart than
+// exponentials reach: e^d is 1 at the maximum and 0 elsewhere) logits become 0 and
+// kLow, counted from m.
+constexpr float kLow = -1e30f, kWild = 1e25f;
+__device__ __forceinline__ bool is_wild(float m) { return !(fabsf(m) < kWild); }
+template <typename T>
+__device__ __forceinline__ void make_safe(Piece<T>& x) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (sizeof(T) == 2) {
+      constexpr uint32_t low = 0xf149f149u;      // -9.95e29, twice
+      asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(x.w[i]) : "r"(low));
+    } else {
+      x.w[i] = __float_as_uint(max_nan(__uint_as_float(x.w[i]), kLow));
+    }
+  }
+}
+template <typename T>
+__device__ __forceinline__ void make_safe_wild(Piece<T>& x, float m) {
+  const float at = m == CUDART_INF_F ? CUDART_NAN_F : m == -CUDART_INF_F ? kLow : 0.f;
+#pragma unroll
+  for (int i = 0; i < Piece<T>::E / 2; ++i) {
+    float2 v = x.pair(i);
+    v.x = v.x == m ? at : v.x != v.x ? v.x : kLow;
+    v.y = v.y == m ? at : v.y != v.y ? v.y : kLow;
+    x.put(i, v);
+  }
 }
 
 __device__ __forceinline__ uint32_t cluster_size() {
@@ -260,6 +312,12 @@ __device__ __forceinline__ void put_remote(uint32_t addr, uint32_t rank, float a
       : "memory");
 }
 
+// What the threads of a block's row take from its first warp.
+struct RowShared {
+  RowTerms r;
+  float m;
+};
+
 // A row belongs to G threads (lanes of a warp, a block, or all blocks of a cluster),
 // each of which keeps up to GR of its 16-byte pieces in registers between the
 // statistics and the gradient, so that the row is read once.
@@ -267,56 +325,58 @@ template <typename T, int G, int GR>
 __global__ void __launch_bounds__(G <= kWarp ? kRowThreads : G, G <= kWarp ? 8 : GR > 8 ? 1 : 1024 / G)
 action_kernel(const ActionArgs p) {
   using P = Piece<T>;
-  constexpr int E = P::E;
+  constexpr int E = P::E, ES = (int)sizeof(T);
   constexpr bool kLanes = G <= kWarp;
   constexpr int R = kLanes ? kRowThreads / G : 1;       // rows of a block at a time
   constexpr int NW = kLanes ? 1 : G / kWarp;
+  constexpr int L = kLanes ? G : kWarp;
   __shared__ float4 entry[2][kLanes ? 1 : kMaxCluster * NW];
+  __shared__ RowShared shared;
   __shared__ float2 sum[kTerms][R];
   const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp;
   const int t = kLanes ? threadIdx.x % G : threadIdx.x;
   const uint32_t cn = kLanes ? 1 : cluster_size(), cr = kLanes ? 0 : cluster_rank();
   const int64_t stride = (int64_t)(gridDim.x / cn) * R;
-  const bool lead_thread = t == 0 && cr == 0;
   const RowSums sums{&sum[0][kLanes ? threadIdx.x / G : 0], R};
   if (t == 0) {
     for (int i = 0; i < kTerms; ++i) sums.at[i * R] = make_float2(0.f, 0.f);
   }
   const uint8_t* mend = p.mask ? p.mask + (p.M - 1) * p.ldm + p.V : nullptr;
   const char* lfrom = static_cast<const char*>(p.l);
-  const char* lto = lfrom + ((p.M - 1) * p.ld + p.V) * (int64_t)sizeof(T);
+  const char* lto = lfrom + ((p.M - 1) * p.ld + p.V) * (int64_t)ES;
   if (cn > 1) {        // the other blocks' shared memory is there
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   }
   pdl_wait();
+  const int step = G * (int)cn, q0 = (int)cr * G + t;
   uint32_t par = 0;
   for (int64_t row0 = (int64_t)(blockIdx.x / cn) * R; row0 < p.M; row0 += stride, par ^= 1) {
     const int64_t mine = kLanes ? row0 + threadIdx.x / G : row0;
     const bool active = mine < p.M;
     const int64_t row = active ? mine : p.M - 1;
-    const char* la = lfrom + row * p.ld * (int64_t)sizeof(T);
-    const int off = (int)(reinterpret_cast<uintptr_t>(la) & 15) / (int)sizeof(T);
-    const char* lp = la - off * (int)sizeof(T);
+    const char* la = lfrom + row * p.ld * (int64_t)ES;
+    const int off = (int)(reinterpret_cast<uintptr_t>(la) & 15) / ES;
+    const char* lp = la - off * ES;
     const int nq = (off + p.V + E - 1) / E;
     const uint8_t* mrow = p.mask ? p.mask + row * p.ldm : nullptr;
-    const int step = G * (int)cn, q0 = (int)cr * G + t;
+    // every piece lies inside the matrix; or its first or last one does not
+    const bool inside = lp >= lfrom && lp + (int64_t)nq * 16 <= lto;
     P x[GR];
 #pragma unroll
     for (int k = 0; k < GR; ++k) {
       const int q = q0 + k * step;
       x[k].none();
       if (q < nq) {
-        const char* at = lp + (int64_t)q * 16;
-        if (at >= lfrom && at + 16 <= lto) {
-          load16(at, x[k].w);
-        } else {       // the matrix's first or last piece
+        if (inside || (q > 0 && q < nq - 1)) {
+          load16(lp + (int64_t)q * 16, x[k].w);
+        } else {
           const T* o = reinterpret_cast<const T*>(la);
 #pragma unroll
           for (int i = 0; i < E; ++i) {
             const int j = q * E + i - off;
             if (j >= 0 && j < p.V) {
-              if constexpr (sizeof(T) == 2) {
+              if constexpr (ES == 2) {
                 const uint32_t b = __bfloat16_as_ushort(o[j]);
                 x[k].w[i / 2] = i & 1 ? (x[k].w[i / 2] & 0xffffu) | b << 16 : (x[k].w[i / 2] & 0xffff0000u) | b;
               } else {
@@ -341,19 +401,22 @@ action_kernel(const ActionArgs p) {
       if (p.ref) in.ref = p.ref[row];
       if (p.weight) in.w = p.weight[row];
     }
+    if (mrow) {
 #pragma unroll
-    for (int k = 0; k < GR; ++k) {
-      const int q = q0 + k * step;
-      if (mrow && q < nq) {
-        const uint32_t ok = allowed<E>(mrow, q * E - off, p.V, p.mask, mend);
+      for (int k = 0; k < GR; ++k) {
+        const int q = q0 + k * step;
+        if (q < nq) cover(x[k], mrow, q * E - off, p.V, p.mask, mend);
+      }
+    } else if (off != 0 || (off + p.V) % E != 0) {
 #pragma unroll
-        for (int i = 0; i < E; ++i)
-          if (!(ok >> i & 1)) x[k].drop(i);
-      } else if (q == 0 || q == nq - 1) {
+      for (int k = 0; k < GR; ++k) {
+        const int q = q0 + k * step;
+        if (q == 0 || q == nq - 1) {
 #pragma unroll
-        for (int i = 0; i < E; ++i) {
-          const int j = q * E + i - off;
-          if (j < 0 || j >= p.V) x[k].drop(i);
+          for (int i = 0; i < E; ++i) {
+            const int j = q * E + i - off;
+            if (j < 0 || j >= p.V) x[k].drop(i);
+          }
         }
       }
     }
@@ -361,13 +424,22 @@ action_kernel(const ActionArgs p) {
     Stat st{-CUDART_INF_F, 0.f, 0.f};
 #pragma unroll
     for (int k = 0; k < GR; ++k) st.m = fmaxf(st.m, x[k].max());
-    st.m = lanes_max<kLanes ? G : kWarp>(st.m);
+    st.m = lanes_max<L>(st.m);
+    const float m0 = st.m;
+    const bool wild = is_wild(m0);
+    if (wild) {
+#pragma unroll
+      for (int k = 0; k < GR; ++k) make_safe_wild(x[k], m0);
+    } else {
+#pragma unroll
+      for (int k = 0; k < GR; ++k) make_safe(x[k]);
+    }
     float2 s2 = make_float2(0.f, 0.f), t2 = make_float2(0.f, 0.f);
     {
-      const float base = base_of(st.m);
+      const float base = wild ? 0.f : m0;
 #pragma unroll
       for (int k = 0; k < GR; ++k) {
-        if (q0 - t + k * step >= nq) break;       // (the same in all threads)
+        if (q0 - t + k * step >= nq) break;       // (the same in all the row's threads)
 #pragma unroll
         for (int i = 0; i < E / 2; ++i) {
           float2 d;
@@ -377,11 +449,14 @@ action_kernel(const ActionArgs p) {
         }
       }
     }
-    st.s = lanes_sum<kLanes ? G : kWarp>(s2.x + s2.y);
-    st.t = lanes_sum<kLanes ? G : kWarp>(t2.x + t2.y);
-    if constexpr (!kLanes) {
-      // every warp's statistics to every block of the row; then each warp joins them all
-      // (two sets in turn: a warp may still be reading the last row's)
+    st.s = lanes_sum<L>(s2.x + s2.y);
+    st.t = lanes_sum<L>(t2.x + t2.y);
+    RowTerms r;
+    if constexpr (kLanes) {
+      r = row_terms(p, row, st, in, t == 0 && active, sums);
+    } else {
+      // every warp's statistics to every block of the row; the first warp of each joins
+      // them and finds the row's terms for its block
       if (lane < (int)cn) put_remote(ptx::smem_u32(&entry[par][cr * NW + warp]), lane, st.m, st.s, st.t);
       if (cn > 1) {
         asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
@@ -389,37 +464,47 @@ action_kernel(const ActionArgs p) {
       } else {
         __syncthreads();
       }
-      constexpr int PER = (kMaxCluster * NW + kWarp - 1) / kWarp;
-      float4 v[PER];
-      float m = -CUDART_INF_F;
+      if (warp == 0) {
+        constexpr int PER = (kMaxCluster * NW + kWarp - 1) / kWarp;
+        float4 v[PER];
+        float m = -CUDART_INF_F;
 #pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        const int w = lane + i * kWarp;
-        v[i] = w < (int)cn * NW ? entry[par][w] : make_float4(-CUDART_INF_F, 0.f, 0.f, 0.f);
-        m = fmaxf(m, v[i].x);
-      }
-      m = lanes_max<kWarp>(m);
-      float s = 0.f, u = 0.f;
+        for (int i = 0; i < PER; ++i) {
+          const int w = lane + i * kWarp;
+          v[i] = w < (int)cn * NW ? entry[par][w] : make_float4(-CUDART_INF_F, 0.f, 0.f, 0.f);
+          m = fmaxf(m, v[i].x);
+        }
+        st.m = lanes_max<kWarp>(m);
+        float s = 0.f, u = 0.f;
 #pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        // (a warp that saw nothing allowed counted from 0: its sums are 0, or NaN)
-        const bool none = v[i].x == -CUDART_INF_F;
-        const float d = none ? 0.f : max_nan(v[i].x - m, -1e30f), f = none ? 1.f : __expf(d);
-        s += f * v[i].y;
-        u += f * fmaf(v[i].y, d, v[i].z);
+        for (int i = 0; i < PER; ++i) {
+          // (sums of a warp that saw nothing allowed are 0, or NaN)
+          const bool none = v[i].x == -CUDART_INF_F;
+          const float d = none ? 0.f : max_nan(v[i].x - st.m, kLow), f = none ? 1.f : __expf(d);
+          s += f * v[i].y;
+          u += f * fmaf(v[i].y, d, v[i].z);
+        }
+        st.s = lanes_sum<kWarp>(s);
+        st.t = lanes_sum<kWarp>(u);
+        r = row_terms(p, row, st, in, lane == 0 && cr == 0, sums);
+        if (lane == 0) shared = RowShared{r, st.m};
       }
-      st.m = m;
-      st.s = lanes_sum<kWarp>(s);
-      st.t = lanes_sum<kWarp>(u);
+      if (!p.dl) continue;       // (entry has two sets in turn)
+      __syncthreads();
+      r = shared.r;
+      st.m = shared.m;
     }
-    const RowTerms r = row_terms(p, row, st, in, lead_thread && active, sums);
     if (!p.dl || !active) continue;
     // the gradient, over the logits' registers
-    const float base = base_of(st.m);
-    char* oa = static_cast<char*>(p.dl) + row * p.lddl * (int64_t)sizeof(T);
+    char* oa = static_cast<char*>(p.dl) + row * p.lddl * (int64_t)ES;
+    T* o = reinterpret_cast<T*>(oa);
     const bool same = (reinterpret_cast<uintptr_t>(oa) & 15) == (reinterpret_cast<uintptr_t>(la) & 15);
-    char* op = oa - off * (int)sizeof(T);
-    const int aq = in.a >= 0 ? (in.a + off) / E : -1, ai = (in.a + off) % E;
+    char* op = oa - off * ES;
+    // (a wild warp's logits are counted from its own maximum)
+    const float base = fminf(wild ? st.m - m0 : st.m, -kLow);
+    if (!r.kept) r.a0 = r.a1 = 0.f;
+    // sums that are not finite: what the mask covers is 0 all the same
+    const bool odd = !(fabsf(r.a0) < CUDART_INF_F && fabsf(r.a1) < 1e7f);
 #pragma unroll
     for (int k = 0; k < GR; ++k) {
       const int q = q0 + k * step;
@@ -427,34 +512,39 @@ action_kernel(const ActionArgs p) {
       P g;
 #pragma unroll
       for (int i = 0; i < E / 2; ++i) {
-        const float2 l = x[k].pair(i);
         float2 d;
-        const float2 e = exp_pair(l, base, d);
-        float2 v = ptx::fmul2(e, ptx::ffma2(d, make_float2(r.a1, r.a1), make_float2(r.a0, r.a0)));
-        if (q == aq) {
-          v.x += ai == 2 * i ? r.hot : 0.f;
-          v.y += ai == 2 * i + 1 ? r.hot : 0.f;
+        const float2 e = exp_pair(x[k].pair(i), base, d);
+        g.put(i, ptx::fmul2(e, ptx::ffma2(d, make_float2(r.a1, r.a1), make_float2(r.a0, r.a0))));
+      }
+      if (odd || !r.kept) {
+#pragma unroll
+        for (int i = 0; i < E / 2; ++i) {
+          const float2 l = x[k].pair(i);
+          float2 v = g.pair(i);
+          v.x = !r.kept || l.x <= 0.9f * kLow ? 0.f : v.x;
+          v.y = !r.kept || l.y <= 0.9f * kLow ? 0.f : v.y;
+          g.put(i, v);
         }
-        if (!r.kept) v = make_float2(0.f, 0.f);
-        if (mrow) {       // (of a row that is NaN too)
-          v.x = l.x == -CUDART_INF_F ? 0.f : v.x;
-          v.y = l.y == -CUDART_INF_F ? 0.f : v.y;
-        }
-        g.put(i, v);
       }
       const int j0 = q * E - off;
       if (same && j0 >= 0 && j0 + E <= p.V) {
         store16(op + (int64_t)q * 16, g.w);
       } else {
-        T* o = reinterpret_cast<T*>(oa);
 #pragma unroll
         for (int i = 0; i < E; ++i) {
           const int j = j0 + i;
           if (j < 0 || j >= p.V) continue;
-          if constexpr (sizeof(T) == 2) o[j] = __ushort_as_bfloat16((uint16_t)(g.w[i / 2] >> (16 * (i & 1))));
+          if constexpr (ES == 2) o[j] = __ushort_as_bfloat16((uint16_t)(g.w[i / 2] >> (16 * (i & 1))));
           else o[j] = __uint_as_float(g.w[i]);
         }
       }
+    }
+    // the action's own element, stored again by the thread that has stored its piece
+    if (r.kept && ((in.a + off) / E - q0) % step == 0) {
+      float2 d;
+      const float b = base_of(st.m);
+      const float e = exp_pair(make_float2(in.x, in.x), b, d).x;
+      round_to(fmaf(e, fmaf(d.x, r.a1, r.a0), r.hot), o[in.a]);
     }
   }
   if (!p.part) return;
