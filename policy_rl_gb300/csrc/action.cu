@@ -1,12 +1,15 @@
 // action.cu -- the policy over any number of actions: log-probability and
 // entropy of a row of logits, and the clipped policy loss with its gradient.
 //
-// Of a row's logits l over the allowed actions, with m = max l and d = l - m:
-//   s = sum e^d,  t = sum e^d d,   logp_j = d_j - log s,   H = log s - t / s,
+// Of a row's logits l over the allowed actions, with m = max l, in powers of two
+// (k = log2 e, u = l k - m k):
+//   s = sum 2^u,  t = sum 2^u u,   logp_j = (u_j - log2 s) / k,   H = (log2 s - t / s) / k,
 // and with c and W the row's slope and weight (row_terms below) the gradient is
 //   W (c (1[j = a] - p_j) + ent p_j (logp_j + H))
-//     = e^(d_j) (A1 d_j + A0) + 1[j = a] W c,
-//   A1 = W ent / s,   A0 = W (ent (H - log s) - c) / s.
+//     = 2^(u_j) (A1 u_j + A0) + 1[j = a] W c,
+//   A1 = W ent / (k s),   A0 = W (ent (H - log2 s / k) - c) / s.
+// u is one fused multiply-add: m k is rounded once for the row, the same in every
+// use, so that its rounding cancels between 2^u, s and t.
 #include <algorithm>
 #include <math_constants.h>
 
@@ -38,22 +41,22 @@ struct ActionArgs {
   float* part;                       // [kTerms][blocks]
 };
 
-// A row's statistics: maximum, sum of e^d, sum of e^d d.
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+// A row's statistics: maximum, sum of 2^u, sum of 2^u u.
 struct Stat {
   float m, s, t;
 };
-// maximum that the deviations are taken from: 0 in a row without any
-__device__ __forceinline__ float base_of(float m) { return m == -CUDART_INF_F ? 0.f : m; }
 
 // What a row's gradient needs beyond its logits.
 struct RowTerms {
-  float a0, a1, hot;       // gradient: e^d (a1 d + a0), + hot at the action
+  float a0, a1, hot;       // gradient: 2^u (a1 u + a0), + hot at the action
   bool kept;
 };
 // A row's own numbers, fetched ahead of its statistics (the same in all its threads).
 struct RowInput {
   int a;                   // its action, -1: none
-  float x;                 // the action's logit, -inf where it is not allowed
+  float x, u;              // the action's logit, -inf where it is not allowed, and its u
   float old, adv, ref, w;
 };
 // A thread's sums over rows, in shared memory (only a row's first thread has any),
@@ -74,9 +77,9 @@ __device__ __forceinline__ RowTerms row_terms(const ActionArgs& p, int64_t row, 
                                               bool lead, RowSums sums) {
   RowTerms r{0.f, 0.f, 0.f, false};
   const bool has = in.a >= 0;
-  const float base = base_of(st.m), logs = logf(st.s);
-  const float H = st.s == 0.f ? 0.f : logs - st.t / st.s;
-  const float lp = has ? (in.x == -CUDART_INF_F ? in.x : (in.x - base) - logs) : 0.f;
+  const float logs = logf(st.s);
+  const float H = st.s == 0.f ? 0.f : logs - st.t / st.s * kLn2;
+  const float lp = has ? (in.x == -CUDART_INF_F ? in.x : in.u * kLn2 - logs) : 0.f;
   if (lead) {
     if (p.logp) p.logp[row] = lp;
     if (p.entropy) p.entropy[row] = H;
@@ -109,7 +112,7 @@ __device__ __forceinline__ RowTerms row_terms(const ActionArgs& p, int64_t row, 
   r.kept = true;
   r.hot = W * c;
   const float k = W / st.s;
-  r.a1 = k * p.ent;
+  r.a1 = k * p.ent * kLn2;
   r.a0 = k * (p.ent * (H - logs) - c);
   return r;
 }
@@ -153,12 +156,11 @@ struct Piece {
     }
   }
 };
-// (not through L1, and not as read-only data: the gradient may go to the same place)
-__device__ __forceinline__ void load16(const void* p, uint32_t (&w)[4]) {
-  asm volatile("ld.global.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-               : "l"(p));
+// 16 bytes into shared memory without registers; a thread waits for its own copies alone
+__device__ __forceinline__ void fetch16(uint32_t dst, const void* p) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(p) : "memory");
 }
+__device__ __forceinline__ void fetched() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 __device__ __forceinline__ void store16(void* p, const uint32_t (&w)[4]) {
   asm volatile("st.global.v4.b32 [%0], {%1, %2, %3, %4};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
                : "memory");
@@ -252,24 +254,23 @@ __device__ __forceinline__ float max_nan(float a, float b) {      // NaN where o
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
-constexpr float kLog2e = 1.4426950408889634f;
-// d and e^d of a pair: the difference is taken before the scaling, so that large
-// logits keep their digits
-__device__ __forceinline__ float2 exp_pair(float2 x, float base, float2& d) {
-  d = ptx::ffma2(x, make_float2(1.f, 1.f), make_float2(-base, -base));
-  float2 e = ptx::fmul2(d, make_float2(kLog2e, kLog2e));
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(e.x));
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(e.y));
+// u and 2^u of a pair, base = m k
+__device__ __forceinline__ float2 exp_pair(float2 x, float base, float2& u) {
+  u = ptx::ffma2(x, make_float2(kLog2e, kLog2e), make_float2(-base, -base));
+  float2 e;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(u.x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(u.y));
   return e;
 }
 
-// Pieces are made safe for e^d d and e^d (a1 d + a0), which would be NaN at d = -inf:
+// Pieces are made safe for 2^u u and 2^u (a1 u + a0), which would be NaN at u = -inf:
 // nothing below kLow is left in them.  In a warp whose maximum m is ordinary that
-// is all; where it is not (from 1e25 on neighbouring floats are further apart than
-// exponentials reach: e^d is 1 at the maximum and 0 elsewhere) logits become 0 and
-// kLow, counted from m.
-constexpr float kLow = -1e30f, kWild = 1e25f;
-__device__ __forceinline__ bool is_wild(float m) { return !(fabsf(m) < kWild); }
+// is all.  Past that m k's rounding would be felt, and the logits become their
+// distances from m: exact ones in fp32; in bf16, where neighbours are 2^8 apart from
+// 2^15 on, 0 at the maximum and kLow elsewhere (2^u is 1 and 0).
+constexpr float kLow = -1e30f;
+template <typename T>
+__device__ __forceinline__ bool is_wild(float m) { return !(fabsf(m) < (sizeof(T) == 2 ? 32768.f : 65536.f)); }
 template <typename T>
 __device__ __forceinline__ void make_safe(Piece<T>& x) {
 #pragma unroll
@@ -282,16 +283,25 @@ __device__ __forceinline__ void make_safe(Piece<T>& x) {
     }
   }
 }
+// a logit's distance from m (infinite m: NaN at +inf as the formula gives it, kLow at -inf)
+template <typename T>
+__device__ __forceinline__ float distance(float x, float m) {
+  if (m == -CUDART_INF_F) return x != x ? x : kLow;
+  if constexpr (sizeof(T) == 2) return x == m ? m - m : x != x ? x : kLow;
+  else return max_nan(x - m, kLow);
+}
 template <typename T>
 __device__ __forceinline__ void make_safe_wild(Piece<T>& x, float m) {
-  const float at = m == CUDART_INF_F ? CUDART_NAN_F : m == -CUDART_INF_F ? kLow : 0.f;
 #pragma unroll
   for (int i = 0; i < Piece<T>::E / 2; ++i) {
-    float2 v = x.pair(i);
-    v.x = v.x == m ? at : v.x != v.x ? v.x : kLow;
-    v.y = v.y == m ? at : v.y != v.y ? v.y : kLow;
-    x.put(i, v);
+    const float2 v = x.pair(i);
+    x.put(i, make_float2(distance<T>(v.x, m), distance<T>(v.y, m)));
   }
+}
+// m k of a row whose maximum is m, for the logits of a warp whose own is m0
+template <typename T>
+__device__ __forceinline__ float base_for(float m, float m0) {
+  return fminf(is_wild<T>(m0) ? m - m0 : m, -kLow) * kLog2e;
 }
 
 __device__ __forceinline__ uint32_t cluster_size() {
@@ -315,13 +325,14 @@ __device__ __forceinline__ void put_remote(uint32_t addr, uint32_t rank, float a
 // What the threads of a block's row take from its first warp.
 struct RowShared {
   RowTerms r;
-  float m;
+  float m, u;
 };
 
 // A row belongs to G threads (lanes of a warp, a block, or all blocks of a cluster),
 // each of which keeps up to GR of its 16-byte pieces in registers between the
-// statistics and the gradient, so that the row is read once.
-template <typename T, int G, int GR>
+// statistics and the gradient, so that the row is read once.  ON16: all rows, of
+// the gradient too, start on 16-byte boundaries.
+template <typename T, int G, int GR, bool ON16>
 __global__ void __launch_bounds__(G <= kWarp ? kRowThreads : G, G <= kWarp ? 8 : GR > 8 ? 1 : 1024 / G)
 action_kernel(const ActionArgs p) {
   using P = Piece<T>;
@@ -349,69 +360,113 @@ action_kernel(const ActionArgs p) {
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   }
   pdl_wait();
-  const int step = G * (int)cn, q0 = (int)cr * G + t;
-  uint32_t par = 0;
-  for (int64_t row0 = (int64_t)(blockIdx.x / cn) * R; row0 < p.M; row0 += stride, par ^= 1) {
-    const int64_t mine = kLanes ? row0 + threadIdx.x / G : row0;
-    const bool active = mine < p.M;
-    const int64_t row = active ? mine : p.M - 1;
-    const char* la = lfrom + row * p.ld * (int64_t)ES;
-    const int off = (int)(reinterpret_cast<uintptr_t>(la) & 15) / ES;
-    const char* lp = la - off * ES;
-    const int nq = (off + p.V + E - 1) / E;
-    const uint8_t* mrow = p.mask ? p.mask + row * p.ldm : nullptr;
-    // every piece lies inside the matrix; or its first or last one does not
-    const bool inside = lp >= lfrom && lp + (int64_t)nq * 16 <= lto;
-    P x[GR];
+  // a block of a cluster takes a run of the row's pieces
+  const int most = (p.V + E - 1) / E + (ON16 ? 0 : 1);
+  const int chunk = kLanes ? most : (most + (int)cn - 1) / (int)cn, q0 = (int)cr * chunk + t;
+  // where a row's pieces lie
+  struct Place {
+    const char* la;        // the row
+    const char* lp;        // its first piece
+    int off, nq;           // elements of another row in that; the end of the block's pieces
+    int from, to;          // the pieces that lie wholly in the matrix (ON16: in the row)
+    int last;              // the row's last piece
+  };
+  auto place = [&](int64_t row) {
+    Place w;
+    w.la = lfrom + row * p.ld * (int64_t)ES;
+    w.off = ON16 ? 0 : (int)(reinterpret_cast<uintptr_t>(w.la) & 15) / ES;
+    w.lp = w.la - w.off * ES;
+    const int n = (w.off + p.V + E - 1) / E;
+    w.last = n - 1;
+    w.nq = kLanes ? n : min(n, ((int)cr + 1) * chunk);
+    w.from = ON16 || w.lp >= lfrom ? 0 : 1;
+    w.to = ON16 ? p.V / E : w.lp + (int64_t)n * 16 <= lto ? n : n - 1;
+    return w;
+  };
+  auto row_of = [&](int64_t row0) { return min(kLanes ? row0 + threadIdx.x / G : row0, p.M - 1); };
+  auto action_of = [&](int64_t row) {
+    const int a = p.action ? p.action[row] : -1;
+    return a < p.V ? a : -1;
+  };
+  // A row's pieces on their way to this thread's places in shared memory, while the
+  // row before it is worked on.
+  extern __shared__ uint4 ahead[];
+  const uint32_t slot = ptx::smem_u32(&ahead[threadIdx.x]);
+  constexpr int kSlots = kLanes ? kRowThreads : G;
+  auto fetch = [&](const Place& w) {
+    const int to = min(w.nq, w.to);
 #pragma unroll
     for (int k = 0; k < GR; ++k) {
-      const int q = q0 + k * step;
-      x[k].none();
-      if (q < nq) {
-        if (inside || (q > 0 && q < nq - 1)) {
-          load16(lp + (int64_t)q * 16, x[k].w);
-        } else {
-          const T* o = reinterpret_cast<const T*>(la);
+      const int q = q0 + k * G;
+      if (q < to && (ON16 || q >= w.from)) fetch16(slot + k * kSlots * 16, w.lp + (int64_t)q * 16);
+    }
+  };
+  const int64_t first = (int64_t)(blockIdx.x / cn) * R;
+  int next_a = -1;
+  if (first < p.M) {
+    fetch(place(row_of(first)));
+    next_a = action_of(row_of(first));
+  }
+  uint32_t par = 0;
+  for (int64_t row0 = first; row0 < p.M; row0 += stride, par ^= 1) {
+    const int64_t row = row_of(row0);
+    const bool active = !kLanes || row0 + threadIdx.x / G < p.M;
+    const Place at = place(row);
+    const char* la = at.la;
+    const int off = at.off, nq = at.nq;
+    const uint8_t* mrow = p.mask ? p.mask + row * p.ldm : nullptr;
+    // (no branch waits for these)
+    RowInput in{next_a, 0.f, 0.f, 0.f, 0.f, 0.f, 1.f};
+    if (kLanes || warp == 0) {
+      const int a = max(in.a, 0);
+      in.x = (float)reinterpret_cast<const T*>(la)[a];
+      if (mrow) in.x = mrow[a] ? in.x : -CUDART_INF_F;
+      if (p.dl) {
+        in.old = p.old[row];
+        in.adv = p.adv[row];
+        if (p.ref) in.ref = p.ref[row];
+        if (p.weight) in.w = p.weight[row];
+      }
+    }
+    P x[GR];
+    fetched();
 #pragma unroll
-          for (int i = 0; i < E; ++i) {
-            const int j = q * E + i - off;
-            if (j >= 0 && j < p.V) {
-              if constexpr (ES == 2) {
-                const uint32_t b = __bfloat16_as_ushort(o[j]);
-                x[k].w[i / 2] = i & 1 ? (x[k].w[i / 2] & 0xffffu) | b << 16 : (x[k].w[i / 2] & 0xffff0000u) | b;
-              } else {
-                x[k].w[i] = __float_as_uint(o[j]);
-              }
+    for (int k = 0; k < GR; ++k) {
+      const int q = q0 + k * G;
+      x[k].none();
+      if (q < min(nq, at.to) && (ON16 || q >= at.from)) {
+        const uint4 v = ahead[k * kSlots + threadIdx.x];
+        x[k].w[0] = v.x;
+        x[k].w[1] = v.y;
+        x[k].w[2] = v.z;
+        x[k].w[3] = v.w;
+      } else if (q < nq) {
+        const T* o = reinterpret_cast<const T*>(la);
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+          const int j = q * E + i - off;
+          if (j >= 0 && j < p.V) {
+            if constexpr (ES == 2) {
+              const uint32_t b = __bfloat16_as_ushort(o[j]);
+              x[k].w[i / 2] = i & 1 ? (x[k].w[i / 2] & 0xffffu) | b << 16 : (x[k].w[i / 2] & 0xffff0000u) | b;
+            } else {
+              x[k].w[i] = __float_as_uint(o[j]);
             }
           }
         }
       }
     }
-    RowInput in{-1, 0.f, 0.f, 0.f, 0.f, 1.f};
-    if (p.action) {
-      const int a = p.action[row];
-      if (a >= 0 && a < p.V) {
-        in.a = a;
-        in.x = mrow && !mrow[a] ? -CUDART_INF_F : (float)reinterpret_cast<const T*>(la)[a];
-      }
-    }
-    if (p.dl) {
-      in.old = p.old[row];
-      in.adv = p.adv[row];
-      if (p.ref) in.ref = p.ref[row];
-      if (p.weight) in.w = p.weight[row];
-    }
     if (mrow) {
 #pragma unroll
       for (int k = 0; k < GR; ++k) {
-        const int q = q0 + k * step;
+        const int q = q0 + k * G;
         if (q < nq) cover(x[k], mrow, q * E - off, p.V, p.mask, mend);
       }
-    } else if (off != 0 || (off + p.V) % E != 0) {
+    } else if constexpr (!ON16) {
 #pragma unroll
       for (int k = 0; k < GR; ++k) {
-        const int q = q0 + k * step;
-        if (q == 0 || q == nq - 1) {
+        const int q = q0 + k * G;
+        if (q == 0 || q == at.last) {
 #pragma unroll
           for (int i = 0; i < E; ++i) {
             const int j = q * E + i - off;
@@ -424,9 +479,15 @@ action_kernel(const ActionArgs p) {
     Stat st{-CUDART_INF_F, 0.f, 0.f};
 #pragma unroll
     for (int k = 0; k < GR; ++k) st.m = fmaxf(st.m, x[k].max());
+    // (the pieces are in registers)
+    if (row0 + stride < p.M) {
+      const int64_t next = row_of(row0 + stride);
+      fetch(place(next));
+      next_a = action_of(next);
+    }
     st.m = lanes_max<L>(st.m);
     const float m0 = st.m;
-    const bool wild = is_wild(m0);
+    const bool wild = is_wild<T>(m0);
     if (wild) {
 #pragma unroll
       for (int k = 0; k < GR; ++k) make_safe_wild(x[k], m0);
@@ -436,23 +497,29 @@ action_kernel(const ActionArgs p) {
     }
     float2 s2 = make_float2(0.f, 0.f), t2 = make_float2(0.f, 0.f);
     {
-      const float base = wild ? 0.f : m0;
+      const float base = wild ? 0.f : m0 * kLog2e;
 #pragma unroll
       for (int k = 0; k < GR; ++k) {
-        if (q0 - t + k * step >= nq) break;       // (the same in all the row's threads)
+        if (q0 - t + k * G >= nq) break;       // (the same in all the row's threads)
 #pragma unroll
         for (int i = 0; i < E / 2; ++i) {
-          float2 d;
-          const float2 e = exp_pair(x[k].pair(i), base, d);
+          float2 u;
+          const float2 e = exp_pair(x[k].pair(i), base, u);
           s2 = ptx::ffma2(e, make_float2(1.f, 1.f), s2);
-          t2 = ptx::ffma2(e, d, t2);
+          t2 = ptx::ffma2(e, u, t2);
         }
       }
     }
     st.s = lanes_sum<L>(s2.x + s2.y);
     st.t = lanes_sum<L>(t2.x + t2.y);
+    // the action's u as the row's pieces have it
+    auto action_u = [&]() {
+      const bool far = is_wild<T>(st.m);
+      return fmaf(far ? max_nan(in.x - st.m, kLow) : in.x, kLog2e, far ? 0.f : -st.m * kLog2e);
+    };
     RowTerms r;
     if constexpr (kLanes) {
+      in.u = action_u();
       r = row_terms(p, row, st, in, t == 0 && active, sums);
     } else {
       // every warp's statistics to every block of the row; the first warp of each joins
@@ -475,48 +542,54 @@ action_kernel(const ActionArgs p) {
           m = fmaxf(m, v[i].x);
         }
         st.m = lanes_max<kWarp>(m);
-        float s = 0.f, u = 0.f;
+        float s = 0.f, w = 0.f;
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-          // (sums of a warp that saw nothing allowed are 0, or NaN)
-          const bool none = v[i].x == -CUDART_INF_F;
-          const float d = none ? 0.f : max_nan(v[i].x - st.m, kLow), f = none ? 1.f : __expf(d);
+          // A warp's sums, counted from its own maximum, by what its logits' u is off the
+          // row's: as the gradient will have it.  (Nothing allowed there: they are 0, or NaN.)
+          const float m1 = v[i].x;
+          const float from = is_wild<T>(m1) ? 0.f : m1 * kLog2e;
+          const float d = m1 == -CUDART_INF_F ? 0.f : max_nan(from - base_for<T>(st.m, m1), kLow);
+          float f;
+          asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(f) : "f"(d));
           s += f * v[i].y;
-          u += f * fmaf(v[i].y, d, v[i].z);
+          w += f * fmaf(v[i].y, d, v[i].z);
         }
         st.s = lanes_sum<kWarp>(s);
-        st.t = lanes_sum<kWarp>(u);
+        st.t = lanes_sum<kWarp>(w);
+        in.u = action_u();
         r = row_terms(p, row, st, in, lane == 0 && cr == 0, sums);
-        if (lane == 0) shared = RowShared{r, st.m};
+        if (lane == 0) shared = RowShared{r, st.m, in.u};
       }
       if (!p.dl) continue;       // (entry has two sets in turn)
       __syncthreads();
       r = shared.r;
       st.m = shared.m;
+      in.u = shared.u;
     }
     if (!p.dl || !active) continue;
     // the gradient, over the logits' registers
     char* oa = static_cast<char*>(p.dl) + row * p.lddl * (int64_t)ES;
     T* o = reinterpret_cast<T*>(oa);
-    const bool same = (reinterpret_cast<uintptr_t>(oa) & 15) == (reinterpret_cast<uintptr_t>(la) & 15);
+    const bool same = ON16 || (reinterpret_cast<uintptr_t>(oa) & 15) == (reinterpret_cast<uintptr_t>(la) & 15);
+    // the pieces that are the row's alone
+    const int whole0 = ON16 || off == 0 ? 0 : 1, whole1 = (off + p.V) / E;
     char* op = oa - off * ES;
-    // (a wild warp's logits are counted from its own maximum)
-    const float base = fminf(wild ? st.m - m0 : st.m, -kLow);
-    if (!r.kept) r.a0 = r.a1 = 0.f;
+    const float base = base_for<T>(st.m, m0);
     // sums that are not finite: what the mask covers is 0 all the same
-    const bool odd = !(fabsf(r.a0) < CUDART_INF_F && fabsf(r.a1) < 1e7f);
+    const bool odd = !r.kept || !(fabsf(r.a0) < CUDART_INF_F && fabsf(r.a1) < 1e7f);
 #pragma unroll
     for (int k = 0; k < GR; ++k) {
-      const int q = q0 + k * step;
+      const int q = q0 + k * G;
       if (q >= nq) break;
       P g;
 #pragma unroll
       for (int i = 0; i < E / 2; ++i) {
-        float2 d;
-        const float2 e = exp_pair(x[k].pair(i), base, d);
-        g.put(i, ptx::fmul2(e, ptx::ffma2(d, make_float2(r.a1, r.a1), make_float2(r.a0, r.a0))));
+        float2 u;
+        const float2 e = exp_pair(x[k].pair(i), base, u);
+        g.put(i, ptx::fmul2(e, ptx::ffma2(u, make_float2(r.a1, r.a1), make_float2(r.a0, r.a0))));
       }
-      if (odd || !r.kept) {
+      if (odd) {
 #pragma unroll
         for (int i = 0; i < E / 2; ++i) {
           const float2 l = x[k].pair(i);
@@ -526,13 +599,12 @@ action_kernel(const ActionArgs p) {
           g.put(i, v);
         }
       }
-      const int j0 = q * E - off;
-      if (same && j0 >= 0 && j0 + E <= p.V) {
+      if (same && q < whole1 && (ON16 || q >= whole0)) {
         store16(op + (int64_t)q * 16, g.w);
       } else {
 #pragma unroll
         for (int i = 0; i < E; ++i) {
-          const int j = j0 + i;
+          const int j = q * E - off + i;
           if (j < 0 || j >= p.V) continue;
           if constexpr (ES == 2) o[j] = __ushort_as_bfloat16((uint16_t)(g.w[i / 2] >> (16 * (i & 1))));
           else o[j] = __uint_as_float(g.w[i]);
@@ -540,11 +612,13 @@ action_kernel(const ActionArgs p) {
       }
     }
     // the action's own element, stored again by the thread that has stored its piece
-    if (r.kept && ((in.a + off) / E - q0) % step == 0) {
-      float2 d;
-      const float b = base_of(st.m);
-      const float e = exp_pair(make_float2(in.x, in.x), b, d).x;
-      round_to(fmaf(e, fmaf(d.x, r.a1, r.a0), r.hot), o[in.a]);
+    if (r.kept) {
+      const int q = (in.a + off) / E;
+      if (q < nq && q >= q0 && (q - q0) % G == 0) {
+        float e;
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(in.u));
+        round_to(fmaf(e, fmaf(in.u, r.a1, r.a0), r.hot), o[in.a]);
+      }
     }
   }
   if (!p.part) return;
@@ -575,16 +649,17 @@ action_stats_kernel(const float* __restrict__ part, int blocks, float* __restric
 // ---- launch ------------------------------------------------------------------------------
 constexpr int kSms = 152;
 
-template <typename T, int G, int GR>
-cudaError_t go(const ActionArgs& p, int cn, float* stats, cudaStream_t st) {
-  constexpr int R = G <= kWarp ? kRowThreads / G : 1;
+template <typename T, int G, int GR, bool ON16>
+cudaError_t launch(const ActionArgs& p, int cn, float* stats, cudaStream_t st) {
+  constexpr int R = G <= kWarp ? kRowThreads / G : 1, threads = G <= kWarp ? kRowThreads : G;
   // two blocks of 512 threads an SM, or as many threads in smaller ones
   constexpr int top = G <= kWarp ? kMaxBlocks : kSms * (GR > 8 ? 1 : 1024 / G);
   const int64_t want = (p.M + R - 1) / R;
   const int blocks = (int)std::min<int64_t>(want, top / cn) * cn;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)blocks);
-  cfg.blockDim = dim3(G <= kWarp ? kRowThreads : G);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = threads * GR * 16;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -595,16 +670,37 @@ cudaError_t go(const ActionArgs& p, int cn, float* stats, cudaStream_t st) {
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = cn > 1 ? 2 : 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, action_kernel<T, G, GR>, p);
+  cudaError_t e;
+  if constexpr (threads * GR * 16 > 48 * 1024) {
+    static thread_local int prepared = -1;   // the device whose shared-memory opt-in is made
+    int dev = 0;
+    e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (prepared != dev) {
+      e = cudaFuncSetAttribute(action_kernel<T, G, GR, ON16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               threads * GR * 16);
+      if (e != cudaSuccess) return e;
+      prepared = dev;
+    }
+  }
+  e = cudaLaunchKernelEx(&cfg, action_kernel<T, G, GR, ON16>, p);
   if (e != cudaSuccess || !stats) return e;
   return launch_pdl(action_stats_kernel, dim3(1), dim3(kTerms * kWarp), 0, st, (const float*)p.part, blocks, stats);
+}
+template <typename T, int G, int GR>
+cudaError_t go(const ActionArgs& p, int cn, float* stats, cudaStream_t st) {
+  constexpr int E = Piece<T>::E;
+  auto on16 = [](const void* m, int64_t ld) { return al16(m) && ld % E == 0; };
+  return on16(p.l, p.ld) && on16(p.dl, p.dl ? p.lddl : 0) ? launch<T, G, GR, true>(p, cn, stats, st)
+                                                          : launch<T, G, GR, false>(p, cn, stats, st);
 }
 
 template <typename T>
 cudaError_t run_rows(const ActionArgs& p, float* stats, cudaStream_t st) {
   constexpr int E = Piece<T>::E;
-  const bool aligned = al16(p.l) && p.ld % E == 0;
-  const int64_t nq = (p.V + E - 1) / E + (aligned ? 0 : 1);       // pieces of a row at most
+  // pieces of a row at most (the kernel for any rows counts one more than its longest has)
+  const bool on16 = al16(p.l) && p.ld % E == 0 && al16(p.dl) && p.lddl % E == 0;
+  const int64_t nq = (p.V + E - 1) / E + (on16 ? 0 : 1);
   if (nq <= 4) return go<T, 4, 1>(p, 1, stats, st);
   if (nq <= 8) return go<T, 4, 2>(p, 1, stats, st);
   if (nq <= 16) return go<T, 8, 2>(p, 1, stats, st);
