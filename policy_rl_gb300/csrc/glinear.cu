@@ -9,7 +9,7 @@
 // kernel finishes them: what it writes is rounded once, from fp32.
 #include <algorithm>
 
-#include "linear.h"
+#include "glinear.h"
 #include "ops.cuh"
 
 namespace ppo {
@@ -20,24 +20,6 @@ using namespace ops;
 
 constexpr int kThreads = 256;
 constexpr int kSms = 152;
-
-// What the sums of element (i, j) of the gated width go into.
-struct Gate {
-  int act;
-  const float* bias;       // [2N] (nullable)
-  const void* pre_in;      // backward: [M][2N]
-  int64_t ldin;
-  void* pre;               // forward: [M][2N] (nullable)
-  int64_t ldpre;
-  void* dp;                // backward: [M][2N]
-  int64_t lddp;
-  void* y;                 // [M][N] (backward: nullable)
-  int64_t ldy;
-  int64_t M, N;
-  const float* part;       // sums: [splits] of `stride` elements, pitch ldp
-  int64_t stride, ldp;
-  int splits;
-};
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads) gate_forward_kernel(const __grid_constant__ Gate g) {
@@ -196,8 +178,11 @@ ppo_status ppo_gated_linear_forward(int32_t dtype, const void* x, int64_t ldx, c
   char* free = static_cast<char*>(work) + glin::kCtrl;
   const lin::Copy ca = lin::on_16_bytes(x, ldx, M, K, free), cb = lin::on_16_bytes(w, ldw, 2 * N, K, free);
   cudaError_t err = lin::pack(ca, cb, st);
-  if (err == cudaSuccess)
-    err = glin::tc_sums({x, ldx, 1, w, ldw, 1, M, 2 * N, K}, lin::kForward, g, free, static_cast<int*>(work), st);
+  if (err != cudaSuccess) return status_of(err);
+  const lin::Product m{x, ldx, 1, w, ldw, 1, M, 2 * N, K};
+  if (const int pairs = glin::fused_pairs(false, M, N, K))
+    return status_of(glin::fused_forward(m, g, pairs, static_cast<int*>(work), ops::num_sms(), st));
+  err = glin::tc_sums(m, lin::kForward, g, free, static_cast<int*>(work), st);
   if (err == cudaSuccess) err = glin::finish_forward<__nv_bfloat16>(g, st);
   return status_of(err);
 }
@@ -237,8 +222,11 @@ ppo_status ppo_gated_linear_backward_data(int32_t dtype, const void* dz, int64_t
   char* free = static_cast<char*>(work) + glin::kCtrl;
   const lin::Copy ca = lin::on_16_bytes(dz, lddz, M, J, free), cb = lin::on_16_bytes(w2, ldw2, J, N, free);
   cudaError_t err = lin::pack(ca, cb, st);
-  if (err == cudaSuccess)
-    err = glin::tc_sums({dz, lddz, 1, w2, 1, ldw2, M, N, J}, lin::kData, g, free, static_cast<int*>(work), st);
+  if (err != cudaSuccess) return status_of(err);
+  const lin::Product m{dz, lddz, 1, w2, 1, ldw2, M, N, J};
+  if (const int pairs = glin::fused_pairs(true, M, N, J))
+    return status_of(glin::fused_backward(m, g, pairs, static_cast<int*>(work), ops::num_sms(), st));
+  err = glin::tc_sums(m, lin::kData, g, free, static_cast<int*>(work), st);
   if (err == cudaSuccess) err = glin::finish_backward<__nv_bfloat16>(g, st);
   return status_of(err);
 }
