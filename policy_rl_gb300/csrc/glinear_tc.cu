@@ -145,7 +145,7 @@ __device__ __forceinline__ void grad_all(int act, const float2 (&d)[8], uint32_t
 }
 
 // tmB: W (forward) or W2; tmG, tmU, tmY: boxes out; tmP, tmQ: gate and up in (backward)
-template <int CG, bool BACK>
+template <int CG, bool BACK, int SETS>
 __global__ void __launch_bounds__(Cfg<CG, BACK>::THREADS, 1)
 glin_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                const __grid_constant__ CUtensorMap tmG, const __grid_constant__ CUtensorMap tmU,
@@ -182,7 +182,7 @@ glin_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(tfull(a), 1);
-      mbar_init(tempty(a), CG * C::EW);
+      mbar_init(tempty(a), CG * C::EW / SETS);
     }
     mbar_init(drain, 1);
     for (int w = 0; w < C::EW; ++w) mbar_init(box_bar(w), 1);
@@ -291,23 +291,28 @@ glin_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
   } else {
     if constexpr (kShift) regs_inc<104>();
     const int q = warp & 3, we = warp - kFirstEpi;
-    // 64 columns of a tile a warp, forward 16 rows of them, backward 32 in two turns
-    constexpr int PARTS = C::GC / 64;
-    const int part = we / 4 % PARTS, half = BACK ? 0 : we / 4 / PARTS;
-    uint8_t* bg = boxes + we * 3 * kBox;
-    uint8_t* bu = bg + kBox;
-    uint8_t* by = bu + kBox;
+    // One set of warps reads every accumulator, or two sets one each.  64 columns of a tile
+    // a warp, 16 rows of them at a time.
+    constexpr int PARTS = C::GC / 64, TURNS = BACK ? 2 : SETS;
+    static_assert(C::EW / SETS * TURNS == 8 * PARTS, "warps of a tile");
+    const int set = SETS == 2 ? we / (C::EW / 2) : 0, ws = we - set * (C::EW / SETS);
+    const int part = ws / 4 % PARTS, half = TURNS == 2 ? 0 : ws / 4 / PARTS;
+    uint8_t* const bg = boxes + we * 3 * kBox;
+    uint8_t* const bu = bg + kBox;
+    uint8_t* const by = bu + kBox;
     const int I = p.I, J = p.J;
     auto row_of = [&](Tile x) { return (x.i * CG + (int)rank) * BM + q * 32 + 16 * half; };
     auto col_of = [&](Tile x) { return x.j * C::GC + part * 64; };
-    uint32_t n = 0, boxes_in = 0;
+    uint32_t n = 0;      // accumulators read
+    auto acc_of = [&](uint32_t k) { return SETS == 2 ? set : (int)(k & 1); };
+    auto phase_of = [&](uint32_t k) { return (SETS == 2 ? k : k >> 1) & 1; };
     // the accumulator's columns are read: the MMAs may overwrite them
     auto release = [&]() {
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
-        if constexpr (CG == 2) arrive_cluster(map_rank(tempty(n & 1), 0));
-        else mbar_arrive(tempty(n & 1));
+        if constexpr (CG == 2) arrive_cluster(map_rank(tempty(acc_of(n)), 0));
+        else mbar_arrive(tempty(acc_of(n)));
       }
     };
     // 16 rows of a box to where they belong (by TMA: after a fence).  A TMA store ends on
@@ -323,109 +328,128 @@ glin_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
         __syncwarp();
       }
     };
-    Tile x = first, soon = after(first), later = after(soon);
+    // this set's tiles
+    const int u0 = group + set * groups, step = SETS * groups;
+    auto next = [&](Tile y) { return SETS == 2 ? after(after(y)) : after(y); };
+    Tile x = set ? after(first) : first;
     bool ok = true;
     if constexpr (!BACK) {
-      for (int t = group; t < p.units; t += groups, x = after(x), ++n) {
-        if (!wait_bar(tfull(n & 1), (n >> 1) & 1, g)) break;
+      for (int t = u0; t < p.units; t += step, x = next(x), ++n) {
+        if (!wait_bar(tfull(acc_of(n)), phase_of(n), g)) break;
         tc_fence_after();
-        const uint32_t at = tmem + (uint32_t)((n & 1) * C::BN + part * 64) + ((uint32_t)(q * 32 + 16 * half) << 16);
-        const int row = row_of(x), col = col_of(x);
-        const bool there = row < I && col < J;
-        // (the boxes: the last stores have read them)
-        if (lane == 0) bulk_wait_read0();
-        __syncwarp();
+        const uint32_t at = tmem + (uint32_t)(acc_of(n) * C::BN + part * 64) + ((uint32_t)(q * 32 + 16 * half) << 16);
+        const int col = col_of(x);
+#pragma unroll 1
+        for (int hr = 0; hr < TURNS; ++hr) {
+          const int row = row_of(x) + 16 * hr;
+          const bool there = row < I && col < J;
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {      // 32 columns at a time
-          uint32_t rg[16], ru[16];
-          tmem_ld_16x32(at + (uint32_t)(32 * c), rg);
-          tmem_ld_16x32(at + (uint32_t)(C::GC + 32 * c), ru);
-          float2 b0[4], b1[4];
+          for (int c = 0; c < 2; ++c) {      // 32 columns at a time
+            uint32_t rg[16], ru[16];
+            tmem_ld_16x32(at + (uint32_t)(32 * c) + ((uint32_t)(16 * hr) << 16), rg);
+            tmem_ld_16x32(at + (uint32_t)(C::GC + 32 * c) + ((uint32_t)(16 * hr) << 16), ru);
+            float2 b0[4], b1[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int c8 = col + 32 * c + 8 * i + 2 * (lane & 3);
-            b0[i] = b1[i] = make_float2(0.f, 0.f);
-            if (p.bias && there) {
-              if (p.bias2 && col + 64 <= J) {
-                b0[i] = __ldg(reinterpret_cast<const float2*>(p.bias + c8));
-                b1[i] = __ldg(reinterpret_cast<const float2*>(p.bias + J + c8));
-              } else {
-                b0[i] = bias_slow(p.bias, c8, J);
-                b1[i] = bias_slow(p.bias + J, c8, J);
+            for (int i = 0; i < 4; ++i) {
+              const int c8 = col + 32 * c + 8 * i + 2 * (lane & 3);
+              b0[i] = b1[i] = make_float2(0.f, 0.f);
+              if (p.bias && there) {
+                if (p.bias2 && col + 64 <= J) {
+                  b0[i] = __ldg(reinterpret_cast<const float2*>(p.bias + c8));
+                  b1[i] = __ldg(reinterpret_cast<const float2*>(p.bias + J + c8));
+                } else {
+                  b0[i] = bias_slow(p.bias, c8, J);
+                  b1[i] = bias_slow(p.bias + J, c8, J);
+                }
               }
             }
-          }
-          tmem_wait16(rg);
-          tmem_wait16(ru);
-          if (c == 1) release();
-          if (!there) continue;
-          float2 vg[8], vu[8];      // [2 i + b]: column group i, row lane / 4 + 8 b
+            tmem_wait16(rg);
+            tmem_wait16(ru);
+            if (hr == TURNS - 1 && c == 1) release();
+            if (!there) continue;
+            float2 vg[8], vu[8];      // [2 i + b]: column group i, row lane / 4 + 8 b
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            vg[k] = ffma2(make_float2(__uint_as_float(rg[2 * k]), __uint_as_float(rg[2 * k + 1])), both(1.f), b0[k / 2]);
-            vu[k] = ffma2(make_float2(__uint_as_float(ru[2 * k]), __uint_as_float(ru[2 * k + 1])), both(1.f), b1[k / 2]);
-          }
-          auto put = [&](uint8_t* box, const float2 (&v)[8]) {
-#pragma unroll
-            for (int i = 0; i < 4; i += 2) {
-              uint32_t w[4];
-#pragma unroll
-              for (int j = 0; j < 4; ++j) w[j] = pack_bf16x2(v[2 * i + j].x, v[2 * i + j].y);
-              quad_put(box, lane, 4 * c + i, w);
+            for (int k = 0; k < 8; ++k) {
+              vg[k] = ffma2(make_float2(__uint_as_float(rg[2 * k]), __uint_as_float(rg[2 * k + 1])), both(1.f), b0[k / 2]);
+              vu[k] = ffma2(make_float2(__uint_as_float(ru[2 * k]), __uint_as_float(ru[2 * k + 1])), both(1.f), b1[k / 2]);
             }
-          };
-          if (p.both) {
-            put(bg, vg);
-            put(bu, vu);
-          }
-          act_all(p.act, vg);
+            auto pack = [&](const float2 (&v)[8], uint32_t (&w)[8]) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k) vg[k] = fmul2(vg[k], vu[k]);
-          put(by, vg);
-        }
-        if (there) {
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (p.both) {
-            leave(bg, &tmG, p.tma_both, p.both, p.ldboth, 0, row, col);
-            leave(bu, &tmU, p.tma_both, p.both, p.ldboth, J, row, col);
+              for (int k = 0; k < 8; ++k) w[k] = pack_bf16x2(v[k].x, v[k].y);
+            };
+            auto put = [&](uint8_t* box, const uint32_t (&w)[8]) {
+              quad_put(box, lane, 4 * c, w);
+              quad_put(box, lane, 4 * c + 2, w + 4);
+            };
+            uint32_t wg[8], wu[8], wy[8];
+            pack(vg, wg);
+            pack(vu, wu);
+            act_all(p.act, vg);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) vg[k] = fmul2(vg[k], vu[k]);
+            pack(vg, wy);
+            if (c == 0) {      // (the boxes: the last stores have read them)
+              if (lane == 0) bulk_wait_read0();
+              __syncwarp();
+            }
+            if (p.both) {
+              put(bg, wg);
+              put(bu, wu);
+            }
+            put(by, wy);
           }
-          leave(by, &tmY, p.tma_y, p.y, p.ldy, 0, row, col);
-          if (lane == 0) bulk_commit();
+          if (there) {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (p.both) {
+              leave(bg, &tmG, p.tma_both, p.both, p.ldboth, 0, row, col);
+              leave(bu, &tmU, p.tma_both, p.both, p.ldboth, J, row, col);
+            }
+            leave(by, &tmY, p.tma_y, p.y, p.ldy, 0, row, col);
+            if (lane == 0) bulk_commit();
+          }
         }
       }
     } else {
-      // the pre-activations of 16 rows from `row` on (lane 0; nothing off the matrix)
-      auto send = [&](int row, int col) {
-        if (row >= I || col >= J) return;
-        mbar_arrive_expect_tx(box_bar(we), 2 * kBox);
-        tma_load_2d(smem_u32(bg), &tmP, col, row, box_bar(we));
-        tma_load_2d(smem_u32(bu), &tmQ, col, row, box_bar(we));
+      // A tile is two turns of 16 rows.  Turns that are off the matrix have no boxes; the
+      // next one's pre-activations are sent when this one's results have left them.  (Not
+      // fetched to L2 earlier, nor into a second pair of boxes; the latter costs two stages
+      // of operands.  32,768 x 512 -> 2,048: 121 us; lines fetched a tile ahead 149 and two
+      // ahead 164; second boxes 138, and 152 with both.)
+      uint32_t sent = 0, in = 0;
+      Tile sx = x;             // the turn to be sent for next
+      int su = u0, sh = 0;
+      auto send_next = [&]() {
+        while (su < p.units) {
+          const int row = row_of(sx) + 16 * sh, col = col_of(sx);
+          if (++sh == 2) {
+            sh = 0;
+            su += step;
+            sx = next(sx);
+          }
+          if (row >= I || col >= J) continue;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(box_bar(we), 2 * kBox);
+            tma_load_2d(smem_u32(bg), &tmP, col, row, box_bar(we));
+            tma_load_2d(smem_u32(bu), &tmQ, col, row, box_bar(we));
+          }
+          ++sent;
+          return;
+        }
       };
-      // this thread's row of a tile's boxes, towards L2
-      auto ahead = [&](Tile y) {
-        const int row = row_of(y) + lane, col = col_of(y);
-        if (!p.tma_in || row >= I || col >= J) return;
-        const __nv_bfloat16* r = static_cast<const __nv_bfloat16*>(p.in) + (int64_t)row * p.ldin + col;
-        prefetch_l2(r);
-        prefetch_l2(r + J);
-      };
-      if (p.tma_in && lane == 0) send(row_of(x), col_of(x));
-      ahead(soon);
-      for (int t = group; t < p.units && ok; t += groups, x = soon, soon = later, later = after(later), ++n) {
-        if (!wait_bar(tfull(n & 1), (n >> 1) & 1, g)) break;
+      if (p.tma_in) send_next();
+      for (int t = u0; t < p.units && ok; t += step, x = next(x), ++n) {
+        if (!wait_bar(tfull(acc_of(n)), phase_of(n), g)) break;
         tc_fence_after();
-        const uint32_t at = tmem + (uint32_t)((n & 1) * C::BN + part * 64) + ((uint32_t)(q * 32) << 16);
+        const uint32_t at = tmem + (uint32_t)(acc_of(n) * C::BN + part * 64) + ((uint32_t)(q * 32) << 16);
         const int col = col_of(x);
-        ahead(later);
 #pragma unroll 1
         for (int hr = 0; hr < 2; ++hr) {
           const int row = row_of(x) + 16 * hr;
           const bool there = row < I && col < J;
           if (there) {
             if (p.tma_in) {
-              ok = wait_bar(box_bar(we), boxes_in & 1, g);
-              ++boxes_in;
+              ok = wait_bar(box_bar(we), in & 1, g);
             } else {
               if (lane == 0) bulk_wait_read0();
               __syncwarp();
@@ -435,6 +459,7 @@ glin_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
             }
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
+            if (p.tma_in) ++in;
           }
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
@@ -472,19 +497,13 @@ glin_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
             if (p.y) leave(by, &tmY, p.tma_y, p.y, p.ldy, 0, row, col);
             if (lane == 0) bulk_commit();
           }
-          // the boxes take the next 16 rows
-          if (lane == 0) {
-            bulk_wait_read0();
-            if (p.tma_in) {
-              if (hr == 0) send(row + 16, col);
-              else if (t + groups < p.units) send(row_of(soon), col_of(soon));
-            }
-          }
+          if (lane == 0) bulk_wait_read0();
+          if (p.tma_in && sent == in) send_next();
           __syncwarp();
         }
       }
       // boxes that were sent for but not used (after an abort)
-      if (p.tma_in && lane == 0 && *abort_flag) drain_wait(box_bar(we), boxes_in & 1, 1000000ull);
+      if (p.tma_in && lane == 0 && *abort_flag && sent != in) drain_wait(box_bar(we), in & 1, 1000000ull);
     }
     if (lane == 0) bulk_wait0();   // this warp's stores are complete before the CTA exits
   }
@@ -525,7 +544,7 @@ glin_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-template <int CG, bool BACK>
+template <int CG, bool BACK, int SETS>
 cudaError_t launch(const Product& m, const Gate& gate, int* err, int sms, cudaStream_t st) {
   using C = Cfg<CG, BACK>;
   const int64_t I = gate.M, J = gate.N;
@@ -571,7 +590,7 @@ cudaError_t launch(const Product& m, const Gate& gate, int* err, int sms, cudaSt
     box(&tq, second(p.in), p.ldin);
   }
   if (e != cudaSuccess) return e;
-  const auto kernel = glin_tc_kernel<CG, BACK>;
+  const auto kernel = glin_tc_kernel<CG, BACK, SETS>;
   static thread_local int prepared = -1;   // the device whose shared-memory opt-in is made
   int dev = 0;
   e = cudaGetDevice(&dev);
@@ -627,10 +646,15 @@ int fused_pairs(bool back, int64_t M, int64_t N, int64_t R) {
 }
 
 cudaError_t fused_forward(const Product& m, const Gate& g, int pairs, int* err, int sms, cudaStream_t st) {
-  return pairs == 2 ? launch<2, false>(m, g, err, sms, st) : launch<1, false>(m, g, err, sms, st);
+  // Two sets of epilogue warps where pre goes out too and there are tiles enough: while one
+  // waits (for TMEM, a fence, its stores) the other computes.  32,768 x 512 -> 2,048 with
+  // pre 121 us with one set and 109 with two, without 89 and 90; 2,048 x 512 -> 2,048 14.2 and 14.8.
+  if (pairs == 2 && g.pre && cdiv(g.M, 2 * BM) * cdiv(g.N, 128) >= 4 * (sms / 2))
+    return launch<2, false, 2>(m, g, err, sms, st);
+  return pairs == 2 ? launch<2, false, 1>(m, g, err, sms, st) : launch<1, false, 1>(m, g, err, sms, st);
 }
 cudaError_t fused_backward(const Product& m, const Gate& g, int pairs, int* err, int sms, cudaStream_t st) {
-  return pairs == 2 ? launch<2, true>(m, g, err, sms, st) : launch<1, true>(m, g, err, sms, st);
+  return pairs == 2 ? launch<2, true, 1>(m, g, err, sms, st) : launch<1, true, 1>(m, g, err, sms, st);
 }
 
 }  // namespace glin
