@@ -10,7 +10,9 @@
 #include <algorithm>
 
 #include "glinear.h"
+#include "lin_again.cuh"
 #include "ops.cuh"
+#include "tc_ptx.cuh"
 
 namespace ppo {
 namespace glin {
@@ -21,62 +23,277 @@ using namespace ops;
 constexpr int kThreads = 256;
 constexpr int kSms = 152;
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads) gate_forward_kernel(const __grid_constant__ Gate g) {
-  pdl_wait();
-  const int64_t n = g.M * g.N;
-  for (int64_t k = (int64_t)blockIdx.x * kThreads + threadIdx.x; k < n; k += (int64_t)gridDim.x * kThreads) {
-    const int64_t i = k / g.N, j = k - i * g.N;
-    float a = 0.f, u = 0.f;
-    for (int s = 0; s < g.splits; ++s) {
-      const float* p = g.part + s * g.stride + i * g.ldp + j;
-      a += __ldcg(p);
-      u += __ldcg(p + g.N);
-    }
-    if (g.bias) {
-      a += g.bias[j];
-      u += g.bias[g.N + j];
-    }
-    if (g.pre) {
-      T* o = static_cast<T*>(g.pre) + i * g.ldpre + j;
-      round_to(a, o[0]);
-      round_to(u, o[g.N]);
-    }
-    round_to(act_value<false>(g.act, a) * u, static_cast<T*>(g.y)[i * g.ldy + j]);
+// A block takes runs of kRun columns of a row, its threads one column in kThreads of them,
+// all loads first: rows may start anywhere.
+constexpr int kPer = 4, kRun = kPer * kThreads;
+
+// f(row, first column) of this block's runs
+template <typename F>
+__device__ __forceinline__ void each_run(int64_t M, int64_t N, F f) {
+  const int64_t per = (N + kRun - 1) / kRun, n = M * per;
+  for (int64_t k = blockIdx.x; k < n; k += gridDim.x) {
+    const int64_t i = k / per;
+    f(i, (k - i * per) * kRun + threadIdx.x);
   }
+}
+// The sums of a run's columns (past the last one, the last one's), `from` columns on.
+__device__ __forceinline__ void run_sums(const lin::PartialSums& s, int64_t i, const int64_t (&j)[kPer], int64_t from,
+                                         float (&v)[kPer]) {
+  const float* p = s.part + i * s.ldp + from;
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) v[e] = __ldcg(p + j[e]);
+  for (int k = 1; k < s.splits; ++k) {
+    p += s.stride;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) v[e] += __ldcg(p + j[e]);
+  }
+}
+__device__ __forceinline__ void run_columns(int64_t j0, int64_t N, int64_t (&j)[kPer]) {
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) j[e] = min(j0 + e * kThreads, N - 1);
+}
+// One sum, what is not finite of a product of planes looked at again.
+__device__ float sum_again(const lin::PartialSums& s, const lin::Again* again, int64_t i, int64_t j) {
+  const int64_t at = i * s.ldp + j;
+  float v = 0.f;
+  for (int k = 0; k < s.splits; ++k) v += __ldcg(s.part + k * s.stride + at);
+  return isfinite(v) ? v : lin::dot_again(again, i, j, at);
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) gate_backward_kernel(const __grid_constant__ Gate g) {
-  pdl_wait();
-  const int64_t n = g.M * g.N;
-  for (int64_t k = (int64_t)blockIdx.x * kThreads + threadIdx.x; k < n; k += (int64_t)gridDim.x * kThreads) {
-    const int64_t i = k / g.N, j = k - i * g.N;
-    float d = 0.f;
-    for (int s = 0; s < g.splits; ++s) d += __ldcg(g.part + s * g.stride + i * g.ldp + j);
-    const T* p = static_cast<const T*>(g.pre_in) + i * g.ldin + j;
-    const float a = (float)p[0], u = (float)p[g.N], v = act_value<false>(g.act, a);
-    T* o = static_cast<T*>(g.dp) + i * g.lddp + j;
-    round_to(d * u * act_slope<false>(g.act, a), o[0]);
-    round_to(d * v, o[g.N]);
-    if (g.y) round_to(v * u, static_cast<T*>(g.y)[i * g.ldy + j]);
+__device__ __forceinline__ void put_forward(const Gate& g, int64_t i, int64_t j, float a, float u) {
+  if (g.bias) {
+    a += g.bias[j];
+    u += g.bias[g.N + j];
   }
+  if (g.pre) {
+    T* o = static_cast<T*>(g.pre) + i * g.ldpre;
+    round_to(a, o[j]);
+    round_to(u, o[g.N + j]);
+  }
+  round_to(act_value<false>(g.act, a) * u, static_cast<T*>(g.y)[i * g.ldy + j]);
+}
+// The elements that the kernel has left out.  (A pass of its own: with the call in the
+// kernel's loop that loop spills, 106 us instead of 38.)
+__device__ __noinline__ void forward_again(const Gate& g, const lin::Again* again) {
+  each_run(g.M, g.N, [&](int64_t i, int64_t j0) {
+    for (int64_t j = j0; j < min(g.N, j0 + kRun); j += kThreads) {
+      float v[2] = {};
+      for (int c = 0; c < 2; ++c)
+        for (int k = 0; k < g.s.splits; ++k) v[c] += __ldcg(g.s.part + k * g.s.stride + i * g.s.ldp + c * g.N + j);
+      if (isfinite(v[0]) && isfinite(v[1])) continue;
+      put_forward<float>(g, i, j, sum_again(g.s, again, i, j), sum_again(g.s, again, i, g.N + j));
+    }
+  });
+}
+template <typename T, bool PLANES>
+__global__ void __launch_bounds__(kThreads)
+gate_forward_kernel(const __grid_constant__ Gate g, const __grid_constant__ lin::Again again) {
+  pdl_wait();
+  bool left = false;
+  each_run(g.M, g.N, [&](int64_t i, int64_t j0) {
+    int64_t j[kPer];
+    float a[kPer], u[kPer];
+    run_columns(j0, g.N, j);
+    run_sums(g.s, i, j, 0, a);
+    run_sums(g.s, i, j, g.N, u);
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) {
+      if (j0 + e * kThreads >= g.N) break;
+      if (PLANES && !(isfinite(a[e]) && isfinite(u[e]))) left = true;
+      else put_forward<T>(g, i, j[e], a[e], u[e]);
+    }
+  });
+  if (PLANES && left) forward_again(g, &again);
 }
 
-int blocks_for(int64_t n) { return (int)std::min<int64_t>((n + kThreads - 1) / kThreads, 16 * kSms); }
 template <typename T>
-cudaError_t finish_forward(const Gate& g, cudaStream_t st) {
-  return launch_pdl(gate_forward_kernel<T>, dim3((unsigned)blocks_for(g.M * g.N)), dim3(kThreads), 0, st, g);
+__device__ __forceinline__ void put_backward(const Gate& g, int64_t i, int64_t j, float d, float a, float u) {
+  T* o = static_cast<T*>(g.dp) + i * g.lddp;
+  const float v = act_value<false>(g.act, a);
+  round_to(d * u * act_slope<false>(g.act, a), o[j]);
+  round_to(d * v, o[g.N + j]);
+  if (g.y) round_to(v * u, static_cast<T*>(g.y)[i * g.ldy + j]);
 }
+__device__ __noinline__ void backward_again(const Gate& g, const lin::Again* again) {
+  each_run(g.M, g.N, [&](int64_t i, int64_t j0) {
+    for (int64_t j = j0; j < min(g.N, j0 + kRun); j += kThreads) {
+      float v = 0.f;
+      for (int k = 0; k < g.s.splits; ++k) v += __ldcg(g.s.part + k * g.s.stride + i * g.s.ldp + j);
+      if (isfinite(v)) continue;
+      const float* p = static_cast<const float*>(g.pre_in) + i * g.ldin;
+      put_backward<float>(g, i, j, sum_again(g.s, again, i, j), p[j], p[g.N + j]);
+    }
+  });
+}
+template <typename T, bool PLANES>
+__global__ void __launch_bounds__(kThreads)
+gate_backward_kernel(const __grid_constant__ Gate g, const __grid_constant__ lin::Again again) {
+  pdl_wait();
+  bool left = false;
+  each_run(g.M, g.N, [&](int64_t i, int64_t j0) {
+    const T* p = static_cast<const T*>(g.pre_in) + i * g.ldin;
+    int64_t j[kPer];
+    float d[kPer], a[kPer], u[kPer];
+    run_columns(j0, g.N, j);
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) {
+      a[e] = (float)p[j[e]];
+      u[e] = (float)p[g.N + j[e]];
+    }
+    run_sums(g.s, i, j, 0, d);
+    // (in place: what was read past the last column, of the last one, is not used)
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) {
+      if (j0 + e * kThreads >= g.N) break;
+      if (PLANES && !isfinite(d[e])) left = true;
+      else put_backward<T>(g, i, j[e], d[e], a[e], u[e]);
+    }
+  });
+  if (PLANES && left) backward_again(g, &again);
+}
+
+template <typename K>
+cudaError_t finish(K kernel, const Gate& g, const lin::Product& m, cudaStream_t st) {
+  const int64_t runs = g.M * ((g.N + kRun - 1) / kRun);
+  return launch_pdl(kernel, dim3((unsigned)std::min<int64_t>(runs, 8 * kSms)), dim3(kThreads), 0, st, g,
+                    lin::Again{m, g.s.part, g.s.stride, g.s.splits, g.s.r_per_split});
+}
+
+// ---- a few rows ------------------------------------------------------------------------
+// Forward of up to 8 rows: bound by reading W once, and for small W by the launch.  A
+// group of wk warps (1, 2 or 4, along the sum) takes one output column, every lane 16
+// bytes of both of its rows of W at a time and the same piece of the rows of x, which
+// stay in L1; the lanes' sums are then folded until a lane holds a row's gate and its
+// neighbour the other sum.  Rows off 16-byte boundaries go element by element.
+constexpr int kFewRows = 8;
+template <typename T, int MR>
+__global__ void __launch_bounds__(kThreads)
+gate_few_kernel(const __grid_constant__ lin::Product m, const __grid_constant__ Gate g, int vec, int wk) {
+  constexpr int A = 2 * MR, E = 16 / (int)sizeof(T);
+  constexpr int U = MR >= 4 ? 2 : 4;     // pieces of a W row in flight
+  __shared__ float sums[kThreads / kWarp][A];
+  pdl_wait();
+  const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp;
+  const int64_t j = (int64_t)blockIdx.x * (kThreads / kWarp / wk) + warp / wk;
+  const int64_t jj = min(j, g.N - 1);      // (columns and rows past the last one repeat it)
+  const T *x[MR], *w[2];
+#pragma unroll
+  for (int i = 0; i < MR; ++i) x[i] = static_cast<const T*>(m.A) + min((int64_t)i, g.M - 1) * m.sai;
+  w[0] = static_cast<const T*>(m.B) + jj * m.sbj;
+  w[1] = static_cast<const T*>(m.B) + (g.N + jj) * m.sbj;
+  float2 pair[A];      // [row][gate, up]: sums of even and odd elements
+#pragma unroll
+  for (int i = 0; i < A; ++i) pair[i] = make_float2(0.f, 0.f);
+  int64_t k = 0;
+  if (vec) {
+    const int64_t whole = m.R / E * E, step = (int64_t)wk * kWarp * E;
+    for (k = ((int64_t)(warp % wk) * kWarp + lane) * E; k < whole; k += U * step) {
+      Raw<T, E> rw[U][2];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+          rw[u][c] = k + u * step < whole ? __ldg(reinterpret_cast<const Raw<T, E>*>(w[c] + k + u * step))
+                                          : Raw<T, E>{};
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (k + u * step >= whole) break;
+        float fw[2][E];
+        to_f32<T, E>(rw[u][0], fw[0]);
+        to_f32<T, E>(rw[u][1], fw[1]);
+#pragma unroll
+        for (int i = 0; i < MR; ++i) {
+          float fx[E];
+          to_f32<T, E>(__ldg(reinterpret_cast<const Raw<T, E>*>(x[i] + k + u * step)), fx);
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int e = 0; e < E; e += 2)
+              pair[2 * i + c] = ptx::ffma2(make_float2(fx[e], fx[e + 1]), make_float2(fw[c][e], fw[c][e + 1]),
+                                           pair[2 * i + c]);
+        }
+      }
+    }
+    k = whole;
+  }
+  float acc[A];
+#pragma unroll
+  for (int i = 0; i < A; ++i) acc[i] = pair[i].x + pair[i].y;
+#pragma unroll 4
+  for (k += (int64_t)(warp % wk) * kWarp + lane; k < m.R; k += (int64_t)wk * kWarp) {
+    const float f0 = (float)w[0][k], f1 = (float)w[1][k];
+#pragma unroll
+    for (int i = 0; i < MR; ++i) {
+      const float f = (float)x[i][k];
+      acc[2 * i] = fmaf(f, f0, acc[2 * i]);
+      acc[2 * i + 1] = fmaf(f, f1, acc[2 * i + 1]);
+    }
+  }
+  // lanes fold their sums: each keeps half of them and takes the other lane's share of
+  // those, until one is left; `mine` is which
+  int mine = 0;
+#pragma unroll
+  for (int n = A, off = 16; off >= 1; off >>= 1) {
+    if (n > 1) {
+      n >>= 1;
+      const bool up = lane & off;
+      mine += up ? n : 0;
+#pragma unroll
+      for (int i = 0; i < n; ++i) {
+        const float give = up ? acc[i] : acc[i + n], keep = up ? acc[i + n] : acc[i];
+        acc[i] = keep + __shfl_xor_sync(0xffffffffu, give, off);
+      }
+    } else {
+      acc[0] += __shfl_xor_sync(0xffffffffu, acc[0], off);
+    }
+  }
+  constexpr int kNext = kWarp / A;       // from a row's gate to its other sum, in lanes
+  const bool holds = (lane & (kNext - 1)) == 0;
+  if (wk > 1) {
+    if (holds) sums[warp][mine] = acc[0];
+    __syncthreads();
+    if (warp % wk != 0) return;
+    acc[0] = 0.f;
+    for (int i = 0; i < wk; ++i) acc[0] += sums[warp + i][mine];
+  }
+  const int row = mine / 2, c = mine & 1;
+  float v = acc[0];
+  if (g.bias) v += g.bias[c * g.N + jj];
+  const float u = __shfl_xor_sync(0xffffffffu, v, kNext);
+  if (!holds || row >= g.M || j >= g.N) return;
+  if (g.pre) round_to(v, static_cast<T*>(g.pre)[row * g.ldpre + c * g.N + j]);
+  if (c == 0) round_to(act_value<false>(g.act, v) * u, static_cast<T*>(g.y)[row * g.ldy + j]);
+}
+
 template <typename T>
-cudaError_t finish_backward(const Gate& g, cudaStream_t st) {
-  return launch_pdl(gate_backward_kernel<T>, dim3((unsigned)blocks_for(g.M * g.N)), dim3(kThreads), 0, st, g);
+cudaError_t few(const lin::Product& m, const Gate& g, cudaStream_t st) {
+  constexpr int E = 16 / (int)sizeof(T);
+  const int vec = m.sai % E == 0 && m.sbj % E == 0;
+  // warps along the sum until there are 4,096
+  int wk = 1;
+  while (wk < 4 && g.N * wk < 4096 && m.R >= 4 * wk * kWarp * E) wk *= 2;
+  const int64_t per = kThreads / kWarp / wk;
+  auto go = [&](auto kernel) {
+    return launch_pdl(kernel, dim3((unsigned)((g.N + per - 1) / per)), dim3(kThreads), 0, st, m, g, vec, wk);
+  };
+  if (g.M <= 1) return go(gate_few_kernel<T, 1>);
+  if (g.M <= 2) return go(gate_few_kernel<T, 2>);
+  if (g.M <= 4) return go(gate_few_kernel<T, 4>);
+  return go(gate_few_kernel<T, kFewRows>);
+}
+constexpr int64_t kFewTop = 1ll << 22;
+template <typename T>
+bool takes_few(int64_t M, int64_t N, int64_t K) {
+  if (M <= 2 || (sizeof(T) == 4 && M <= kFewRows)) return true;
+  return M <= kFewRows && 2 * N * K <= (M <= 4 ? kFewTop : kFewTop / 2);
 }
 
 // ---- workspace ------------------------------------------------------------------------
-// The status word and its padding, then (bf16) the copies of operands off 16-byte
-// boundaries and the partial products, or (fp32) the sums and the product's own
-// workspace, whose status word is the call's.
+// The status word and its padding; then the copies of bf16 operands off 16-byte
+// boundaries, or fp32 operands' planes, and the partial products.  fp32 products that
+// take the CUDA cores: the product's own workspace, whose status word is the
+// call's, and the sums.
 constexpr size_t kCtrl = 256;
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
@@ -85,12 +302,17 @@ size_t linear_bytes(int64_t M, int64_t N, int64_t K) {
   return ppo_linear_workspace_bytes(PPO_DTYPE_F32, M, N, K, 0, 0, 0, &b) == PPO_OK ? up256(b) : 0;
 }
 size_t forward_bytes(int32_t dtype, int64_t M, int64_t N, int64_t K, int64_t ldx, int64_t ldw) {
-  if (dtype == PPO_DTYPE_F32) return linear_bytes(M, 2 * N, K) + (size_t)M * 2 * N * 4;
+  if (dtype == PPO_DTYPE_F32)
+    return lin::takes_planes(lin::kForward, M, 2 * N, K)
+               ? kCtrl + lin::planes_need(M, K, 2 * N, K, M, 2 * N, K)
+               : linear_bytes(M, 2 * N, K) + (size_t)M * 2 * N * 4;
   return kCtrl + lin::packed_bytes(M, K, ldx) + lin::packed_bytes(2 * N, K, ldw) +
          lin::tc_part_bytes(M, 2 * N, K, true);
 }
 size_t backward_bytes(int32_t dtype, int64_t M, int64_t N, int64_t J, int64_t lddz, int64_t ldw2) {
-  if (dtype == PPO_DTYPE_F32) return linear_bytes(M, J, N) + (size_t)M * N * 4;
+  if (dtype == PPO_DTYPE_F32)
+    return lin::takes_planes(lin::kData, M, J, N) ? kCtrl + lin::planes_need(M, J, J, N, M, N, J)
+                                                  : linear_bytes(M, J, N) + (size_t)M * N * 4;
   return kCtrl + lin::packed_bytes(M, J, lddz) + lin::packed_bytes(J, N, ldw2) +
          lin::tc_part_bytes(M, N, J, true);
 }
@@ -104,10 +326,8 @@ cudaError_t tc_sums(const lin::Product& p, int mode, Gate& g, char* work, int* e
   lin::Epilogue e{};
   e.mode = mode;
   e.act = PPO_ACT_NONE;
-  g.part = reinterpret_cast<float*>(work);
-  g.splits = plan.splits;
-  g.ldp = lin::part_pitch(p.J);
-  g.stride = p.I * g.ldp;
+  const int64_t ldp = lin::part_pitch(p.J);
+  g.s = lin::PartialSums{reinterpret_cast<float*>(work), plan.splits, p.I * ldp, ldp, 0};
   return lin::tc_product(p, e, plan, reinterpret_cast<float*>(work), nullptr, err, num_sms(), st);
 }
 
@@ -162,20 +382,31 @@ ppo_status ppo_gated_linear_forward(int32_t dtype, const void* x, int64_t ldx, c
   g.ldy = ldy;
   g.M = M;
   g.N = N;
-  if (dtype == PPO_DTYPE_F32) {
+  const lin::Product given{x, ldx, 1, w, ldw, 1, M, 2 * N, K};
+  char* free = static_cast<char*>(work) + glin::kCtrl;
+  if (dtype == PPO_DTYPE_F32 ? glin::takes_few<float>(M, N, K) : glin::takes_few<__nv_bfloat16>(M, N, K)) {
+    g.bias = bias;
+    g.pre = pre;
+    g.ldpre = ldpre;
+    return status_of(dtype == PPO_DTYPE_F32 ? glin::few<float>(given, g, st) : glin::few<__nv_bfloat16>(given, g, st));
+  }
+  if (dtype == PPO_DTYPE_F32 && !lin::takes_planes(lin::kForward, M, 2 * N, K)) {
+    // the sums go where pre does; without it, to the workspace
     const size_t own = glin::linear_bytes(M, 2 * N, K);
     float* sums = pre ? static_cast<float*>(pre) : reinterpret_cast<float*>(static_cast<char*>(work) + own);
-    g.part = sums;
-    g.ldp = pre ? ldpre : 2 * N;
-    g.splits = 1;
+    const int64_t ldp = pre ? ldpre : 2 * N;
+    g.s = lin::PartialSums{sums, 1, 0, ldp, 0};
     const ppo_status e = ppo_linear_forward(dtype, x, ldx, w, ldw, bias, PPO_ACT_NONE, nullptr, 0, M, 2 * N, K,
-                                            sums, g.ldp, nullptr, 0, work, own, st);
-    return e != PPO_OK ? e : status_of(glin::finish_forward<float>(g, st));
+                                            sums, ldp, nullptr, 0, work, own, st);
+    return e != PPO_OK ? e : status_of(glin::finish(glin::gate_forward_kernel<float, false>, g, given, st));
   }
   g.bias = bias;
   g.pre = pre;
   g.ldpre = ldpre;
-  char* free = static_cast<char*>(work) + glin::kCtrl;
+  if (dtype == PPO_DTYPE_F32) {
+    const cudaError_t e = lin::planes_sums(given, lin::kForward, free, static_cast<int*>(work), st, &g.s);
+    return status_of(e == cudaSuccess ? glin::finish(glin::gate_forward_kernel<float, true>, g, given, st) : e);
+  }
   const lin::Copy ca = lin::on_16_bytes(x, ldx, M, K, free), cb = lin::on_16_bytes(w, ldw, 2 * N, K, free);
   cudaError_t err = lin::pack(ca, cb, st);
   if (err != cudaSuccess) return status_of(err);
@@ -183,7 +414,7 @@ ppo_status ppo_gated_linear_forward(int32_t dtype, const void* x, int64_t ldx, c
   if (const int pairs = glin::fused_pairs(false, M, N, K))
     return status_of(glin::fused_forward(m, g, pairs, static_cast<int*>(work), ops::num_sms(), st));
   err = glin::tc_sums(m, lin::kForward, g, free, static_cast<int*>(work), st);
-  if (err == cudaSuccess) err = glin::finish_forward<__nv_bfloat16>(g, st);
+  if (err == cudaSuccess) err = glin::finish(glin::gate_forward_kernel<__nv_bfloat16, false>, g, m, st);
   return status_of(err);
 }
 
@@ -209,17 +440,20 @@ ppo_status ppo_gated_linear_backward_data(int32_t dtype, const void* dz, int64_t
   g.ldy = ldy;
   g.M = M;
   g.N = N;
-  if (dtype == PPO_DTYPE_F32) {
+  const lin::Product given{dz, lddz, 1, w2, 1, ldw2, M, N, J};
+  char* free = static_cast<char*>(work) + glin::kCtrl;
+  if (dtype == PPO_DTYPE_F32 && !lin::takes_planes(lin::kData, M, J, N)) {
     const size_t own = glin::linear_bytes(M, J, N);
     float* sums = reinterpret_cast<float*>(static_cast<char*>(work) + own);
-    g.part = sums;
-    g.ldp = N;
-    g.splits = 1;
+    g.s = lin::PartialSums{sums, 1, 0, N, 0};
     const ppo_status e = ppo_linear_backward_data(dtype, dz, lddz, w2, ldw2, nullptr, 0, PPO_ACT_NONE, nullptr,
                                                   0, M, J, N, sums, N, work, own, st);
-    return e != PPO_OK ? e : status_of(glin::finish_backward<float>(g, st));
+    return e != PPO_OK ? e : status_of(glin::finish(glin::gate_backward_kernel<float, false>, g, given, st));
   }
-  char* free = static_cast<char*>(work) + glin::kCtrl;
+  if (dtype == PPO_DTYPE_F32) {
+    const cudaError_t e = lin::planes_sums(given, lin::kData, free, static_cast<int*>(work), st, &g.s);
+    return status_of(e == cudaSuccess ? glin::finish(glin::gate_backward_kernel<float, true>, g, given, st) : e);
+  }
   const lin::Copy ca = lin::on_16_bytes(dz, lddz, M, J, free), cb = lin::on_16_bytes(w2, ldw2, J, N, free);
   cudaError_t err = lin::pack(ca, cb, st);
   if (err != cudaSuccess) return status_of(err);
@@ -227,7 +461,7 @@ ppo_status ppo_gated_linear_backward_data(int32_t dtype, const void* dz, int64_t
   if (const int pairs = glin::fused_pairs(true, M, N, J))
     return status_of(glin::fused_backward(m, g, pairs, static_cast<int*>(work), ops::num_sms(), st));
   err = glin::tc_sums(m, lin::kData, g, free, static_cast<int*>(work), st);
-  if (err == cudaSuccess) err = glin::finish_backward<__nv_bfloat16>(g, st);
+  if (err == cudaSuccess) err = glin::finish(glin::gate_backward_kernel<__nv_bfloat16, false>, g, m, st);
   return status_of(err);
 }
 

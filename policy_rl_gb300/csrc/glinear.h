@@ -19,9 +19,7 @@ struct Gate {
   void* y;                 // [M][N] (backward: nullable)
   int64_t ldy;
   int64_t M, N;
-  const float* part;       // sums: [splits] of `stride` elements, pitch ldp
-  int64_t stride, ldp;
-  int splits;
+  lin::PartialSums s;
 };
 
 // bf16 in one kernel (glinear_tc.cu), operands on 16-byte rows: A is x [M][R] or dz,

@@ -437,6 +437,14 @@ glin_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
           return;
         }
       };
+      // a turn's pre-activations towards L2, half a row a lane (where they come by hand)
+      auto ahead = [&](Tile y, int turn) {
+        const int row = row_of(y) + 16 * turn + (lane & 15), col = col_of(y);
+        if (row >= I || col >= J) return;
+        const __nv_bfloat16* r = static_cast<const __nv_bfloat16*>(p.in) + (int64_t)row * p.ldin + col + (lane & 16 ? J : 0);
+        prefetch_l2(r);
+        prefetch_l2(r + min(63, J - 1 - col));
+      };
       if (p.tma_in) send_next();
       for (int t = u0; t < p.units && ok; t += step, x = next(x), ++n) {
         if (!wait_bar(tfull(acc_of(n)), phase_of(n), g)) break;
@@ -455,6 +463,7 @@ glin_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
               __syncwarp();
               box_load_slow(bg, lane, p.in, p.ldin, row, col, I, J, 16);
               box_load_slow(bu, lane, p.in, p.ldin, row, J + col, I, 2 * (int64_t)J, 16);
+              ahead(hr == 0 ? x : next(x), hr ^ 1);
               __syncwarp();
             }
             ok = __all_sync(0xffffffffu, ok);
@@ -649,7 +658,8 @@ cudaError_t fused_forward(const Product& m, const Gate& g, int pairs, int* err, 
   // Two sets of epilogue warps where pre goes out too and there are tiles enough: while one
   // waits (for TMEM, a fence, its stores) the other computes.  32,768 x 512 -> 2,048 with
   // pre 121 us with one set and 109 with two, without 89 and 90; 2,048 x 512 -> 2,048 14.2 and 14.8.
-  if (pairs == 2 && g.pre && cdiv(g.M, 2 * BM) * cdiv(g.N, 128) >= 4 * (sms / 2))
+  // (of rows that TMA cannot store, one: 10,007 x 1,397 -> 1,001 82 us and 96.)
+  if (pairs == 2 && g.pre && ops::al16(g.pre) && g.ldpre % 8 == 0 && g.N % 8 == 0 && cdiv(g.M, 2 * BM) * cdiv(g.N, 128) >= 4 * (sms / 2))
     return launch<2, false, 2>(m, g, err, sms, st);
   return pairs == 2 ? launch<2, false, 1>(m, g, err, sms, st) : launch<1, false, 1>(m, g, err, sms, st);
 }

@@ -18,6 +18,7 @@
 
 #include <algorithm>
 
+#include "lin_again.cuh"
 #include "ops.cuh"
 #include "tc_ptx.cuh"
 
@@ -102,47 +103,6 @@ __device__ __forceinline__ void finish4(const Epilogue& e, const Beside& x, floa
   put4<T>(e.out, i * e.ldo + j, n, vec, v);
 }
 
-// Of a product of planes: where the sum of an element's parts is not finite, each part
-// that is not either is computed again, straight from the fp32 operands.  (The planes of
-// an infinity, or of what rounds to one in bf16, do not add up: their products hold NaN
-// where the product may not.)  Eight steps' loads are in flight: an infinity among
-// 1,000,000 rows of a weight gradient takes 18 ms, 2 s a step at a time over the
-// whole sum.  A part that has become NaN ends early.
-struct Again {
-  Product g;              // the fp32 operands
-  const float* part;
-  int64_t pitch;          // of the parts
-  int splits;
-  int64_t r_per_split;
-};
-__device__ __noinline__ float dot_again(const Again* __restrict__ p, int64_t i, int64_t j, int64_t at) {
-  constexpr int U = 8;
-  const int64_t sar = p->g.sar, sbr = p->g.sbr;
-  float sum = 0.f;
-  for (int s = 0; s < p->splits; ++s) {
-    float v = __ldcg(p->part + s * p->pitch + at);
-    if (!isfinite(v)) {
-      v = 0.f;
-      const int64_t r0 = s * p->r_per_split;
-      const float* a = static_cast<const float*>(p->g.A) + i * p->g.sai + r0 * sar;
-      const float* b = static_cast<const float*>(p->g.B) + j * p->g.sbj + r0 * sbr;
-      int64_t n = min(p->g.R - r0, p->r_per_split);
-      for (; n >= U && v == v; n -= U) {
-        float x[U], y[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u, a += sar, b += sbr) {
-          x[u] = __ldg(a);
-          y[u] = __ldg(b);
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) v = fmaf(x[u], y[u], v);
-      }
-      for (; n > 0 && v == v; --n, a += sar, b += sbr) v = fmaf(__ldg(a), __ldg(b), v);
-    }
-    sum += v;
-  }
-  return sum;
-}
 // Every eighth row's share of a column sum, from row w on.
 __device__ __noinline__ float sum_again(const float* a, int64_t step, int64_t R, int w) {
   constexpr int U = 8, S = 8;
@@ -643,9 +603,11 @@ __global__ void __launch_bounds__(kPackThreads) split_planes_kernel(const Copy a
 // instead of three (1,024 x 256 -> 256, 6.7e7 of them: 14.6 us forward, 12.5 and
 // 18.9 the gradients; 12.1, 11.9 and 12.7 by planes; 256 x 256 -> 256 7.8, 12.5 and
 // 16.9; 8.6, 13.0 and 11.7 by planes; 4,999 x 1,397 -> 512 230 to 460 and 67 to 77).
+}  // namespace
 bool takes_planes(int mode, int64_t M, int64_t N, int64_t K) {
   return M * N * K >= (mode == kWeight ? 1ll << 25 : 1ll << 26);
 }
+namespace {
 
 }  // namespace
 size_t tc_part_bytes(int64_t I, int64_t J, int64_t R, bool must_split, int terms) {
@@ -759,10 +721,10 @@ cudaError_t tc_run(const Product& g, const Epilogue& e, char* work, int* err, cu
   return launch_finish<__nv_bfloat16>(part, plan.splits, g.I, g.J, part_pitch(g.J), e, st);
 }
 
-// out = epilogue of an fp32 product, by planes.  A lies as rows of `ca`
-// elements (its own row or the sum's index), so does B.
-cudaError_t planes_run(const Product& g, const Epilogue& e, float* db, char* work, int* err,
-                       cudaStream_t st) {
+// The sums of an fp32 product, by planes, as partial products (and db's partial
+// column sums).  A lies as rows of `ca` elements (its own row or the sum's index), so does B.
+cudaError_t planes_product(const Product& g, const Epilogue& e, char* work, int* err, cudaStream_t st,
+                           bool with_sums, float** sums, PartialSums* out) {
   const bool amn = g.sai == 1 && e.mode == kWeight, bmn = e.mode != kForward;
   Product t = g;
   auto split = [&](const void*& a, int64_t ld, int64_t rows, int64_t cols, int64_t& pitch) {
@@ -780,22 +742,40 @@ cudaError_t planes_run(const Product& g, const Epilogue& e, float* db, char* wor
                              0, st, ca, cb);
   if (x != cudaSuccess) return x;
   const TcPlan plan = tc_plan(g.I, g.J, g.R, true, kTerms);
-  float* sums = db ? reinterpret_cast<float*>(work) : nullptr;
-  if (db) work += sum_bytes(g.I, g.J, g.R, plan);
+  *sums = with_sums ? reinterpret_cast<float*>(work) : nullptr;
+  if (with_sums) work += sum_bytes(g.I, g.J, g.R, plan);
   float* part = reinterpret_cast<float*>(work);
-  x = tc_product(t, e, plan, part, sums, err, num_sms(), st, plane_rows(amn ? g.R : g.I),
-                 plane_rows(bmn ? g.R : g.J));
+  const int64_t ldp = part_pitch(g.J);
+  *out = PartialSums{part, plan.splits, g.I * ldp, ldp, (int64_t)plan.kt_per_split / kTerms * kSumStep};
+  return tc_product(t, e, plan, part, *sums, err, num_sms(), st, plane_rows(amn ? g.R : g.I),
+                    plane_rows(bmn ? g.R : g.J));
+}
+// out = epilogue of an fp32 product, by planes.
+cudaError_t planes_run(const Product& g, const Epilogue& e, float* db, char* work, int* err,
+                       cudaStream_t st) {
+  float* sums;
+  PartialSums s;
+  const cudaError_t x = planes_product(g, e, work, err, st, db != nullptr, &sums, &s);
   if (x != cudaSuccess) return x;
-  const int64_t r_per_split = (int64_t)plan.kt_per_split / kTerms * kSumStep;
   if (e.mode == kWeight)
-    return launch_finish_weight<true>(part, plan.splits, g, e, sums, tc_sum_rows(g, plan), db, st, r_per_split);
-  return launch_finish<float, true>(part, plan.splits, g.I, g.J, part_pitch(g.J), e, st, g, r_per_split);
+    return launch_finish_weight<true>(s.part, s.splits, g, e, sums,
+                                      tc_sum_rows(g, tc_plan(g.I, g.J, g.R, true, kTerms)), db, st, s.r_per_split);
+  return launch_finish<float, true>(s.part, s.splits, g.I, g.J, s.ldp, e, st, g, s.r_per_split);
+}
+}  // namespace
+cudaError_t planes_sums(const Product& g, int mode, char* work, int* err, cudaStream_t st, PartialSums* out) {
+  Epilogue e{};
+  e.mode = mode;
+  e.act = PPO_ACT_NONE;
+  float* sums;
+  return planes_product(g, e, work, err, st, false, &sums, out);
 }
 size_t planes_need(int64_t ra, int64_t ca, int64_t rb, int64_t cb, int64_t I, int64_t J, int64_t R) {
   return planes_bytes(ra, ca) + planes_bytes(rb, cb) + 512 + tc_part_bytes(I, J, R, true, kTerms) +
          sum_bytes(I, J, R, tc_plan(I, J, R, true, kTerms));
 }
 
+namespace {
 // A gradient that is added to, or whose rows TMA cannot store, is finished from
 // partial products even where the sum is not split.
 bool must_finish(int64_t J, int accumulate) { return accumulate || J % 4; }

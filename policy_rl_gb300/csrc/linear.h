@@ -76,6 +76,18 @@ cudaError_t pack(const Copy& a, const Copy& b, cudaStream_t st);
 // Bytes of a product's partial products (0 where its tiles are finished at once).
 size_t tc_part_bytes(int64_t I, int64_t J, int64_t R, bool must_split, int terms = 1);
 bool sizes_ok(int64_t M, int64_t N, int64_t K);
+// Sums of a product in `splits` parts, `stride` apart, of rows of pitch ldp, each of
+// r_per_split terms.
+struct PartialSums {
+  const float* part;
+  int splits;
+  int64_t stride, ldp, r_per_split;
+};
+// Whether an fp32 product is taken by planes; its sums so (forward and data gradient), and
+// the workspace for operands of ra x ca and rb x cb.
+bool takes_planes(int mode, int64_t M, int64_t N, int64_t K);
+cudaError_t planes_sums(const Product& g, int mode, char* work, int* err, cudaStream_t st, PartialSums* out);
+size_t planes_need(int64_t ra, int64_t ca, int64_t rb, int64_t cb, int64_t I, int64_t J, int64_t R);
 
 }  // namespace lin
 }  // namespace ppo

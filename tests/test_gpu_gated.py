@@ -181,6 +181,44 @@ def test_special_values(P, M):
         assert torch.isnan(y2[:, 5]).all() and (~torch.isfinite(y2[:, 9])).all()
 
 
+def test_special_values_in_fp32_on_the_tensor_cores(P):
+    """The planes of an infinity do not add up: what it reaches is summed again."""
+    import torch
+    M, N, K = 1000, 512, 160
+    rng = np.random.default_rng(1)
+    x, w = dev(rng.normal(size=(M, K))), dev(rng.normal(size=(2 * N, K)) / 12)
+    dz, w2 = dev(rng.normal(size=(M, K))), dev(rng.normal(size=(K, N)) / 12)
+    pre = dev(rng.normal(size=(M, 2 * N)))
+    work = zeroed(P.ppo_gated_linear_workspace_bytes(M, N, K, x.dtype, J=K))
+    w[N + 9, 3] = float("inf")
+    w[40, 5] = 3.4e38           # bf16 rounds it to infinity
+    x[17, 5] = 0.0
+    w2[2, 33] = float("inf")
+    y, q, dp = out((M, N)), out((M, 2 * N)), out((M, 2 * N))
+    P.ppo_gated_linear_forward(x, w, y, None, CODES["relu"], q, work)
+    P.ppo_gated_linear_backward_data(dz, w2, pre, dp, CODES["relu"], None, work)
+    with np.errstate(invalid="ignore", over="ignore"):
+        r = f64(x) @ f64(w).T
+        d = f64(dz) @ f64(w2)
+    assert np.array_equal(np.sign(f64(q)[:, N + 9]), np.sign(r[:, N + 9])) and torch.isinf(q[:, N + 9]).all()
+    ok = np.abs(r[:, 40]) < 3e38
+    assert ok[17] and np.allclose(f64(q)[ok, 40], r[ok, 40], rtol=1e-5)
+    assert (np.isinf(f64(q)[:, 40]) == (np.abs(r[:, 40]) > 3.4028235e38)).all()
+    assert torch.isfinite(q[:, [c for c in range(2 * N) if c not in (40, N + 9)]]).all()
+    u = f64(pre)[:, N + 33]
+    g = f64(pre)[:, 33]
+    assert (np.isinf(f64(dp)[:, 33]) == ((g > 0) & (u != 0))).all() and not np.isfinite(f64(dp)[:, N + 33]).any()
+    assert np.array_equal(np.sign(f64(dp)[g > 0, N + 33]), np.sign(d[g > 0, 33]))
+
+
+def test_few_rows(P):
+    """One to eight rows: groups of warps along the sum, columns that do not fill a block."""
+    for M in range(1, 10):
+        for N, K in ((1, 3), (2, 2000), (37, 129), (300, 4096), (3000, 64)):
+            for dtype in ("f32", "bf16"):
+                check_forward(P, M, N, K, dtype, seed=M, pitches=(K + 1, None, N + 3, None) if N == 37 else (None,) * 4)
+
+
 def test_streams_graphs_and_determinism(P):
     import torch
     M, N, K = 300, 200, 96
