@@ -333,7 +333,7 @@ struct RowShared {
 // statistics and the gradient, so that the row is read once.  ON16: all rows, of
 // the gradient too, start on 16-byte boundaries.
 template <typename T, int G, int GR, bool ON16>
-__global__ void __launch_bounds__(G <= kWarp ? kRowThreads : G, G <= kWarp ? 8 : GR > 8 ? 1 : 1024 / G)
+__global__ void __launch_bounds__(G <= kWarp ? kRowThreads : G, G <= kWarp ? 8 : GR > 8 || G == 1024 ? 1 : 1024 / G)
 action_kernel(const ActionArgs p) {
   using P = Piece<T>;
   constexpr int E = P::E, ES = (int)sizeof(T);
@@ -701,6 +701,9 @@ cudaError_t run_rows(const ActionArgs& p, float* stats, cudaStream_t st) {
   // pieces of a row at most (the kernel for any rows counts one more than its longest has)
   const bool on16 = al16(p.l) && p.ld % E == 0 && al16(p.dl) && p.lddl % E == 0;
   const int64_t nq = (p.V + E - 1) / E + (on16 ? 0 : 1);
+  // (many rows: fewer threads for each, so that a row's terms cost fewer warps.  65,536 x
+  // 18 fp32 with a mask 13.4 us with four lanes, 10.3 with two; 4,096 x 18 4.2 and 4.7)
+  if (nq <= 8 && p.M >= 16384) return go<T, 2, 4>(p, 1, stats, st);
   if (nq <= 4) return go<T, 4, 1>(p, 1, stats, st);
   if (nq <= 8) return go<T, 4, 2>(p, 1, stats, st);
   if (nq <= 16) return go<T, 8, 2>(p, 1, stats, st);
@@ -713,6 +716,10 @@ cudaError_t run_rows(const ActionArgs& p, float* stats, cudaStream_t st) {
   const bool few = p.M < kSms;
   if (nq <= 1024 && !few) return go<T, 128, 8>(p, 1, stats, st);
   if (nq <= 2048 && !few) return go<T, 256, 8>(p, 1, stats, st);
+  // Long rows, many of them: clusters of as few blocks as hold one.  (4,096 x 131,072 bf16
+  // 672 us with four blocks of 512 threads, 518 with two of 1,024; but 1,001 x 50,257 66 and 70
+  // with two and one, 8,192 x 32,768 207 and 235 with one of either)
+  if (nq > 8192 && !few) return go<T, 1024, 8>(p, nq <= 16384 ? 2 : nq <= 32768 ? 4 : 8, stats, st);
   int cn = 1;
   while (cn < kMaxCluster && (nq > 4096 * cn || (p.M * cn * 2 <= kSms && nq > 1024 * cn))) cn *= 2;
   return nq <= 4096 * cn ? go<T, 512, 8>(p, cn, stats, st) : go<T, 512, 16>(p, cn, stats, st);
