@@ -25,15 +25,18 @@ constexpr int kSms = 152;
 
 // A block takes runs of kRun columns of a row, its threads one column in kThreads of them,
 // all loads first: rows may start anywhere.
-constexpr int kPer = 4, kRun = kPer * kThreads;
+constexpr int kPer = 2, kRun = kPer * kThreads;
 
-// f(row, first column) of this block's runs
+// f(row, this thread's first column, the run's end) of this block's runs, all of about
+// one length
 template <typename F>
 __device__ __forceinline__ void each_run(int64_t M, int64_t N, F f) {
   const int64_t per = (N + kRun - 1) / kRun, n = M * per;
+  const int64_t len = ((N + per - 1) / per + kWarp - 1) / kWarp * kWarp;
   for (int64_t k = blockIdx.x; k < n; k += gridDim.x) {
-    const int64_t i = k / per;
-    f(i, (k - i * per) * kRun + threadIdx.x);
+    const int64_t i = n < (1ll << 32) ? (int64_t)((uint32_t)k / (uint32_t)per) : k / per;
+    const int64_t j0 = (k - i * per) * len;
+    f(i, j0 + threadIdx.x, min(N, j0 + len));
   }
 }
 // The sums of a run's columns (past the last one, the last one's), `from` columns on.
@@ -76,8 +79,8 @@ __device__ __forceinline__ void put_forward(const Gate& g, int64_t i, int64_t j,
 // The elements that the kernel has left out.  (A pass of its own: with the call in the
 // kernel's loop that loop spills, 106 us instead of 38.)
 __device__ __noinline__ void forward_again(const Gate& g, const lin::Again* again) {
-  each_run(g.M, g.N, [&](int64_t i, int64_t j0) {
-    for (int64_t j = j0; j < min(g.N, j0 + kRun); j += kThreads) {
+  each_run(g.M, g.N, [&](int64_t i, int64_t j0, int64_t end) {
+    for (int64_t j = j0; j < end; j += kThreads) {
       float v[2] = {};
       for (int c = 0; c < 2; ++c)
         for (int k = 0; k < g.s.splits; ++k) v[c] += __ldcg(g.s.part + k * g.s.stride + i * g.s.ldp + c * g.N + j);
@@ -91,7 +94,7 @@ __global__ void __launch_bounds__(kThreads)
 gate_forward_kernel(const __grid_constant__ Gate g, const __grid_constant__ lin::Again again) {
   pdl_wait();
   bool left = false;
-  each_run(g.M, g.N, [&](int64_t i, int64_t j0) {
+  each_run(g.M, g.N, [&](int64_t i, int64_t j0, int64_t end) {
     int64_t j[kPer];
     float a[kPer], u[kPer];
     run_columns(j0, g.N, j);
@@ -99,7 +102,7 @@ gate_forward_kernel(const __grid_constant__ Gate g, const __grid_constant__ lin:
     run_sums(g.s, i, j, g.N, u);
 #pragma unroll
     for (int e = 0; e < kPer; ++e) {
-      if (j0 + e * kThreads >= g.N) break;
+      if (j0 + e * kThreads >= end) break;
       if (PLANES && !(isfinite(a[e]) && isfinite(u[e]))) left = true;
       else put_forward<T>(g, i, j[e], a[e], u[e]);
     }
@@ -116,8 +119,8 @@ __device__ __forceinline__ void put_backward(const Gate& g, int64_t i, int64_t j
   if (g.y) round_to(v * u, static_cast<T*>(g.y)[i * g.ldy + j]);
 }
 __device__ __noinline__ void backward_again(const Gate& g, const lin::Again* again) {
-  each_run(g.M, g.N, [&](int64_t i, int64_t j0) {
-    for (int64_t j = j0; j < min(g.N, j0 + kRun); j += kThreads) {
+  each_run(g.M, g.N, [&](int64_t i, int64_t j0, int64_t end) {
+    for (int64_t j = j0; j < end; j += kThreads) {
       float v = 0.f;
       for (int k = 0; k < g.s.splits; ++k) v += __ldcg(g.s.part + k * g.s.stride + i * g.s.ldp + j);
       if (isfinite(v)) continue;
@@ -131,7 +134,7 @@ __global__ void __launch_bounds__(kThreads)
 gate_backward_kernel(const __grid_constant__ Gate g, const __grid_constant__ lin::Again again) {
   pdl_wait();
   bool left = false;
-  each_run(g.M, g.N, [&](int64_t i, int64_t j0) {
+  each_run(g.M, g.N, [&](int64_t i, int64_t j0, int64_t end) {
     const T* p = static_cast<const T*>(g.pre_in) + i * g.ldin;
     int64_t j[kPer];
     float d[kPer], a[kPer], u[kPer];
@@ -145,7 +148,7 @@ gate_backward_kernel(const __grid_constant__ Gate g, const __grid_constant__ lin
     // (in place: what was read past the last column, of the last one, is not used)
 #pragma unroll
     for (int e = 0; e < kPer; ++e) {
-      if (j0 + e * kThreads >= g.N) break;
+      if (j0 + e * kThreads >= end) break;
       if (PLANES && !isfinite(d[e])) left = true;
       else put_backward<T>(g, i, j[e], d[e], a[e], u[e]);
     }
@@ -156,7 +159,7 @@ gate_backward_kernel(const __grid_constant__ Gate g, const __grid_constant__ lin
 template <typename K>
 cudaError_t finish(K kernel, const Gate& g, const lin::Product& m, cudaStream_t st) {
   const int64_t runs = g.M * ((g.N + kRun - 1) / kRun);
-  return launch_pdl(kernel, dim3((unsigned)std::min<int64_t>(runs, 8 * kSms)), dim3(kThreads), 0, st, g,
+  return launch_pdl(kernel, dim3((unsigned)std::min<int64_t>(runs, 16 * kSms)), dim3(kThreads), 0, st, g,
                     lin::Again{m, g.s.part, g.s.stride, g.s.splits, g.s.r_per_split});
 }
 
