@@ -6,7 +6,7 @@ shown, of those that the step allows.  One update per rollout: act, the clipped
 policy loss with a KL term towards the policy at the start, the gradients clipped
 to one norm, Adam.
 
-    python examples/recall_actions.py [--updates 40] [--actions 1000]
+    python examples/recall_actions.py [--updates 60] [--actions 16]
 """
 import argparse
 import os
@@ -21,8 +21,8 @@ from policy_rl_gb300.trunk import ActionHead, GradClip, RecurrentTrunk  # noqa: 
 
 def main(argv=None):
     ap = argparse.ArgumentParser()
-    ap.add_argument("--updates", type=int, default=40)
-    ap.add_argument("--actions", type=int, default=1000)
+    ap.add_argument("--updates", type=int, default=60)
+    ap.add_argument("--actions", type=int, default=16)
     ap.add_argument("--width", type=int, default=256)
     ap.add_argument("--T", type=int, default=32)
     ap.add_argument("--N", type=int, default=128)

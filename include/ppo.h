@@ -698,8 +698,8 @@ ppo_status ppo_work_status(void *d_work, cudaStream_t stream);
  * rounded.  bf16 products run on the tensor cores, fp32 ones as in
  * ppo_linear_forward (the same limits, with 2N for N).  d_work:
  * ppo_gated_linear_workspace_bytes of the same dtype, sizes and pitches (J = 0:
- * forward alone; a pitch <= 0 stands for the row's length), zeroed once, as
- * for ppo_linear_*; ppo_work_status reads its status word. */
+ * forward alone; a pitch <= 0 stands for the row's length), zeroed once, for one
+ * stream's calls, as for ppo_linear_*; ppo_work_status reads its status word. */
 ppo_status ppo_gated_linear_workspace_bytes(int32_t dtype, int64_t M, int64_t N, int64_t K, int64_t J,
                                             int64_t ldx, int64_t ldw, int64_t lddz, int64_t ldw2,
                                             size_t *bytes);
@@ -752,12 +752,15 @@ ppo_status ppo_action_logp(int32_t dtype, const void *d_logits, int64_t ld, int6
  *   c = -A r [r A <= clip(r) A] + kl_coef (1 - e^y);
  * 0 where the mask covers.  It may be d_logits (same pitch).  Rows without an
  * allowed action are left out: nothing of them is added, their gradients are 0, and
- * what their logp_old, adv, logp_ref and weight hold does not matter.
+ * what their logp_old, adv, logp_ref and weight hold does not matter; nor does it,
+ * weight aside, in a row of weight 0, whose gradient is 0 too.
  * d_logp, d_entropy (nullable): as in ppo_action_logp.  d_stats (nullable) fp32
  * [8]: scale * sum of w {pg + kl_coef kl - ent_coef entropy, pg, kl, entropy,
  * [r < 1 - clip_low or r > 1 + clip_high], (r - 1) - x, 1}, then the number of
  * rows left out.  d_work: ppo_action_loss_workspace_bytes() bytes (nullable
- * without d_stats), 16-byte aligned. */
+ * without d_stats), 16-byte aligned; calls that may overlap on the GPU (two streams, two
+ * graphs) want one each.  Deterministic: the order of a row's sums is fixed by
+ * types, sizes, pitches and the pointers' alignment.  Outputs overlap no input unless said. */
 ppo_status ppo_action_loss_workspace_bytes(size_t *bytes);
 ppo_status ppo_action_loss_grad(int32_t dtype, const void *d_logits, int64_t ld, int64_t M,
                                 int64_t V, const uint8_t *d_mask, int64_t ldm,
@@ -780,7 +783,8 @@ ppo_status ppo_action_loss_grad(int32_t dtype, const void *d_logits, int64_t ld,
  * tensors (same counts and types, nullable: in place).  Tensors that are written
  * overlap no other tensor of the call (PPO_ERR_INVALID), but an out tensor
  * may be its own input.  d_norm fp32 [1] receives the norm before clipping.
- * d_work: ppo_grad_norm_workspace_bytes(n) bytes, 16-byte aligned.  n < 2^20. */
+ * d_work: ppo_grad_norm_workspace_bytes(n) bytes, 16-byte aligned, one for each of
+ * calls that may overlap on the GPU.  n < 2^20.  Deterministic. */
 typedef struct {
     void *d_data;
     int64_t count;

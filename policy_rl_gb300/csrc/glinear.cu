@@ -5,8 +5,13 @@
 //   forward    pre = x W^T + b  [M][2N],  y = act(g) u,  g | u the halves of pre
 //   backward   d = dz W2  [M][N],  dp = [ d u act'(g) | d act(g) ],  y = act(g) u
 //
-// The products leave fp32 sums (partial ones where the sum is split), and one
-// kernel finishes them: what it writes is rounded once, from fp32.
+// bf16 products finish their tiles in the same kernel (glinear_tc.cu) where there are
+// tiles enough.  Others leave fp32 sums, partial ones where the sum is split, and one
+// kernel here finishes them: what it writes is rounded once, from fp32.  Forward
+// products of a few rows have a kernel of their own.
+// fp32, 4,999 x 512 -> 1,365 (floor 66 us as six bf16 products): forward planes 7 us, product
+// 71, gate 38 (a third of it the second run of a row: 30 since runs have one length);
+// backward 7, 51 and 36.  33 rows of 4,096 -> 4,096 bf16: product 16, gate 4, 10 by W's bytes.
 #include <algorithm>
 
 #include "glinear.h"
@@ -305,19 +310,21 @@ size_t linear_bytes(int64_t M, int64_t N, int64_t K) {
   return ppo_linear_workspace_bytes(PPO_DTYPE_F32, M, N, K, 0, 0, 0, &b) == PPO_OK ? up256(b) : 0;
 }
 size_t forward_bytes(int32_t dtype, int64_t M, int64_t N, int64_t K, int64_t ldx, int64_t ldw) {
+  if (dtype == PPO_DTYPE_F32 && takes_few<float>(M, N, K)) return kCtrl;
   if (dtype == PPO_DTYPE_F32)
     return lin::takes_planes(lin::kForward, M, 2 * N, K)
                ? kCtrl + lin::planes_need(M, K, 2 * N, K, M, 2 * N, K)
                : linear_bytes(M, 2 * N, K) + (size_t)M * 2 * N * 4;
+  if (takes_few<__nv_bfloat16>(M, N, K)) return kCtrl;
   return kCtrl + lin::packed_bytes(M, K, ldx) + lin::packed_bytes(2 * N, K, ldw) +
-         lin::tc_part_bytes(M, 2 * N, K, true);
+         (fused_pairs(false, M, N, K) ? 0 : lin::tc_part_bytes(M, 2 * N, K, true));
 }
 size_t backward_bytes(int32_t dtype, int64_t M, int64_t N, int64_t J, int64_t lddz, int64_t ldw2) {
   if (dtype == PPO_DTYPE_F32)
     return lin::takes_planes(lin::kData, M, J, N) ? kCtrl + lin::planes_need(M, J, J, N, M, N, J)
                                                   : linear_bytes(M, J, N) + (size_t)M * N * 4;
   return kCtrl + lin::packed_bytes(M, J, lddz) + lin::packed_bytes(J, N, ldw2) +
-         lin::tc_part_bytes(M, N, J, true);
+         (fused_pairs(true, M, N, J) ? 0 : lin::tc_part_bytes(M, N, J, true));
 }
 bool gated_sizes_ok(int64_t M, int64_t N, int64_t K) {
   return N >= 1 && N < (1ll << 28) && lin::sizes_ok(M, 2 * N, K);

@@ -81,7 +81,7 @@ struct Sum {
 template <typename T>
 __device__ __forceinline__ void add_squares(Sum& a, const uint4 (&x)[kPieces]) {
   const float v = piece_sum<T>(x, 1.f);
-  if (v == 0.f || (v > 0x1p-80f && v < 0x1p100f)) {
+  if (v == 0.f || (v > 0x1p-100f && v < 0x1p100f)) {
     const float y = v - a.c, t = a.s + y;
     a.c = (t - a.s) - y;
     a.s = t;

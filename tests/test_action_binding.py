@@ -163,6 +163,13 @@ def test_gated_refused(L):
     assert bwd(y=at(2), ldy=16) == ALIGN and need > 0
 
 
+def test_gated_workspaces_hold_no_sums_that_stay_in_their_tiles(L):
+    size = ctypes.c_size_t()
+    for M, N, K in ((32768, 2048, 512), (1, 2048, 512), (8192, 4096, 4096)):
+        assert L.ppo_gated_linear_workspace_bytes(1, M, N, K, 512, 0, 0, 0, 0, ctypes.byref(size)) == 0
+        assert size.value < 1 << 20, (M, N, K, size.value)
+
+
 def test_norms_refused(L):
     size = ctypes.c_size_t()
     for n in (-1, 1 << 20):

@@ -269,23 +269,39 @@ def test_offsets_past_32_bits(P):
     within(got[0], rg, b_g + (A.HALF["bf16"] + 4 * A.U) * np.abs(rg) + 1e-38, "dlogits")
 
 
-def test_streams_graphs_and_determinism(P):
+def test_an_infinite_ratio(P):
+    """r = inf: a good action's slope is 0, as its surrogate is flat; a bad one's infinite."""
     import torch
-    c = make(300, 3001, "bf16", 8, True)
+    l, g, st = dev(np.zeros((3, 4))), out((3, 4)), out((8,))
+    work = out((P.ppo_action_loss_workspace_bytes() // 4,))
+    for adv, good in ((1.0, True), (-1.0, False)):
+        P.ppo_action_loss_grad(l, ints([1, 2, 3]), dev([-200.0, 0.0, 0.0]), dev([adv, 0.0, 0.0]), g, 1.0, stats=st,
+                               work=work)
+        assert (g[1:] == 0).all()
+        if good:
+            assert (g[0] == 0).all() and abs(float(st[1]) + 1.2) < 1e-6
+        else:
+            assert not torch.isfinite(g[0]).all() and torch.isinf(st[1])
+
+
+@pytest.mark.parametrize("M,V", [(300, 3001), (40, 131072), (200, 70001), (900, 40)])
+def test_streams_graphs_and_determinism(P, M, V):
+    import torch
+    c = make(M, V, "bf16", 8, True)
     want = [t.clone() for t in run_loss(P, c, "bf16")]
     side = torch.cuda.Stream()
     a, old, adv, mask = ints(c["a"]), dev(c["old"]), dev(c["adv"]), flags(c["mask"])
     ref, w = dev(c["ref"]), dev(c["weight"])
-    g, st = out((300, 3001), "bf16"), out((8,))
+    g, st = out((M, V), "bf16"), out((8,))
     work = out((P.ppo_action_loss_workspace_bytes() // 4,))
     torch.cuda.synchronize()
     kw = dict(logp_ref=ref, weight=w, mask=mask, stats=st, work=work)
-    P.ppo_action_loss_grad(c["l"], a, old, adv, g, 1 / 300, stream=side, **kw)
+    P.ppo_action_loss_grad(c["l"], a, old, adv, g, 1 / M, stream=side, **kw)
     side.synchronize()
     assert torch.equal(g, want[0]) and torch.equal(st, want[3])
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
-        P.ppo_action_loss_grad(c["l"], a, old, adv, g, 1 / 300, **kw)
+        P.ppo_action_loss_grad(c["l"], a, old, adv, g, 1 / M, **kw)
     for _ in range(2):
         g.zero_(), st.zero_()
         graph.replay()
