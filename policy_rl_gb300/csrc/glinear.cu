@@ -8,10 +8,10 @@
 // bf16 products finish their tiles in the same kernel (glinear_tc.cu) where there are
 // tiles enough.  Others leave fp32 sums, partial ones where the sum is split, and one
 // kernel here finishes them: what it writes is rounded once, from fp32.  Forward
-// products of a few rows have a kernel of their own.
+// products of few rows have kernels of their own.
 // fp32, 4,999 x 512 -> 1,365 (floor 66 us as six bf16 products): forward planes 7 us, product
 // 71, gate 38 (a third of it the second run of a row: 30 since runs have one length);
-// backward 7, 51 and 36.  33 rows of 4,096 -> 4,096 bf16: product 16, gate 4, 10 by W's bytes.
+// backward 7, 51 and 36.  Up to 64 bf16 rows: glinear_skinny.cu.
 #include <algorithm>
 
 #include "glinear.h"
@@ -290,11 +290,15 @@ cudaError_t few(const lin::Product& m, const Gate& g, cudaStream_t st) {
   if (g.M <= 4) return go(gate_few_kernel<T, 4>);
   return go(gate_few_kernel<T, kFewRows>);
 }
-constexpr int64_t kFewTop = 1ll << 22;
+// bf16 in a graph, here / on the tensor cores: one row of 512 -> 2,048 2.7 us / 4.5, 3 rows
+// 3.2 / 4.5, 8 rows 4.5 / 4.6; of 4,096 -> 4,096, W not in L2, one row 18.2 / 14.9, two rows
+// 21.3 / 14.9.  Rows off 16-byte boundaries would have to be copied first for those.
+// (A pitch <= 0 stands for the row's length.)
 template <typename T>
-bool takes_few(int64_t M, int64_t N, int64_t K) {
-  if (M <= 2 || (sizeof(T) == 4 && M <= kFewRows)) return true;
-  return M <= kFewRows && 2 * N * K <= (M <= 4 ? kFewTop : kFewTop / 2);
+bool takes_few(int64_t M, int64_t N, int64_t K, int64_t ldx, int64_t ldw) {
+  if (sizeof(T) == 4 || M > kFewRows) return M <= kFewRows;
+  if (M <= 2 && ((ldx > 0 ? ldx : K) % 8 || (ldw > 0 ? ldw : K) % 8)) return true;
+  return 2 * N * K <= (M <= 4 ? 1ll << 22 : 1ll << 21);
 }
 
 // ---- workspace ------------------------------------------------------------------------
@@ -310,14 +314,14 @@ size_t linear_bytes(int64_t M, int64_t N, int64_t K) {
   return ppo_linear_workspace_bytes(PPO_DTYPE_F32, M, N, K, 0, 0, 0, &b) == PPO_OK ? up256(b) : 0;
 }
 size_t forward_bytes(int32_t dtype, int64_t M, int64_t N, int64_t K, int64_t ldx, int64_t ldw) {
-  if (dtype == PPO_DTYPE_F32 && takes_few<float>(M, N, K)) return kCtrl;
+  if (dtype == PPO_DTYPE_F32 && takes_few<float>(M, N, K, ldx, ldw)) return kCtrl;
   if (dtype == PPO_DTYPE_F32)
     return lin::takes_planes(lin::kForward, M, 2 * N, K)
                ? kCtrl + lin::planes_need(M, K, 2 * N, K, M, 2 * N, K)
                : linear_bytes(M, 2 * N, K) + (size_t)M * 2 * N * 4;
-  if (takes_few<__nv_bfloat16>(M, N, K)) return kCtrl;
+  if (takes_few<__nv_bfloat16>(M, N, K, ldx, ldw)) return kCtrl;
   return kCtrl + lin::packed_bytes(M, K, ldx) + lin::packed_bytes(2 * N, K, ldw) +
-         (fused_pairs(false, M, N, K) ? 0 : lin::tc_part_bytes(M, 2 * N, K, true));
+         (skinny_ctas(M, N, K) || fused_pairs(false, M, N, K) ? 0 : lin::tc_part_bytes(M, 2 * N, K, true));
 }
 size_t backward_bytes(int32_t dtype, int64_t M, int64_t N, int64_t J, int64_t lddz, int64_t ldw2) {
   if (dtype == PPO_DTYPE_F32)
@@ -394,7 +398,8 @@ ppo_status ppo_gated_linear_forward(int32_t dtype, const void* x, int64_t ldx, c
   g.N = N;
   const lin::Product given{x, ldx, 1, w, ldw, 1, M, 2 * N, K};
   char* free = static_cast<char*>(work) + glin::kCtrl;
-  if (dtype == PPO_DTYPE_F32 ? glin::takes_few<float>(M, N, K) : glin::takes_few<__nv_bfloat16>(M, N, K)) {
+  if (dtype == PPO_DTYPE_F32 ? glin::takes_few<float>(M, N, K, ldx, ldw)
+                             : glin::takes_few<__nv_bfloat16>(M, N, K, ldx, ldw)) {
     g.bias = bias;
     g.pre = pre;
     g.ldpre = ldpre;
@@ -421,6 +426,8 @@ ppo_status ppo_gated_linear_forward(int32_t dtype, const void* x, int64_t ldx, c
   cudaError_t err = lin::pack(ca, cb, st);
   if (err != cudaSuccess) return status_of(err);
   const lin::Product m{x, ldx, 1, w, ldw, 1, M, 2 * N, K};
+  if (const int ctas = glin::skinny_ctas(M, N, K))
+    return status_of(glin::skinny_forward(m, g, ctas, static_cast<int*>(work), st));
   if (const int pairs = glin::fused_pairs(false, M, N, K))
     return status_of(glin::fused_forward(m, g, pairs, static_cast<int*>(work), ops::num_sms(), st));
   err = glin::tc_sums(m, lin::kForward, g, free, static_cast<int*>(work), st);

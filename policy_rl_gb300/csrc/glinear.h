@@ -28,6 +28,10 @@ struct Gate {
 int fused_pairs(bool back, int64_t M, int64_t N, int64_t R);
 cudaError_t fused_forward(const lin::Product& m, const Gate& g, int pairs, int* err, int sms, cudaStream_t st);
 cudaError_t fused_backward(const lin::Product& m, const Gate& g, int pairs, int* err, int sms, cudaStream_t st);
+// bf16 forward of up to 64 rows (glinear_skinny.cu): CTAs that share a sum, 0 where it does
+// not apply.
+int skinny_ctas(int64_t M, int64_t N, int64_t R);
+cudaError_t skinny_forward(const lin::Product& m, const Gate& g, int ctas, int* err, cudaStream_t st);
 
 }  // namespace glin
 }  // namespace ppo
