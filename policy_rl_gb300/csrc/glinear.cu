@@ -9,9 +9,10 @@
 // tiles enough.  Others leave fp32 sums, partial ones where the sum is split, and one
 // kernel here finishes them: what it writes is rounded once, from fp32.  Forward
 // products of few rows have kernels of their own.
-// fp32, 4,999 x 512 -> 1,365 (floor 66 us as six bf16 products): forward planes 7 us, product
-// 71, gate 38 (a third of it the second run of a row: 30 since runs have one length);
-// backward 7, 51 and 36.  Up to 64 bf16 rows: glinear_skinny.cu.
+// fp32, 4,999 x 512 -> 1,365, forward with pre and backward with y: 204 us, floor 66 as six
+// bf16 products; of them the planes 14, the products 123, the gates 67 for the 300 MB
+// that they read and write (70 with a choice of activation for each element).  Up to 64
+// bf16 rows: glinear_skinny.cu.
 #include <algorithm>
 
 #include "glinear.h"
@@ -30,68 +31,127 @@ constexpr int kSms = 152;
 
 // A block takes runs of kRun columns of a row, its threads one column in kThreads of them,
 // all loads first: rows may start anywhere.
-constexpr int kPer = 2, kRun = kPer * kThreads;
+constexpr int kPer = 4, kRun = kPer * kThreads;
 
-// f(row, this thread's first column, the run's end) of this block's runs, all of about
-// one length
+// f(row, this thread's first column, how many of its columns there are) of this block's
+// runs, all of about one length
 template <typename F>
-__device__ __forceinline__ void each_run(int64_t M, int64_t N, F f) {
-  const int64_t per = (N + kRun - 1) / kRun, n = M * per;
-  const int64_t len = ((N + per - 1) / per + kWarp - 1) / kWarp * kWarp;
+__device__ __forceinline__ void each_run(const Gate& g, F f) {
+  const uint32_t per = (uint32_t)((g.N + kRun - 1) / kRun);
+  const int len = (int)((g.N + per - 1) / per + kWarp - 1) / kWarp * kWarp;
+  const int64_t n = g.M * per;
   for (int64_t k = blockIdx.x; k < n; k += gridDim.x) {
-    const int64_t i = n < (1ll << 32) ? (int64_t)((uint32_t)k / (uint32_t)per) : k / per;
-    const int64_t j0 = (k - i * per) * len;
-    f(i, j0 + threadIdx.x, min(N, j0 + len));
+    const int64_t i = n < (1ll << 32) ? (int64_t)((uint32_t)k / per) : k / per;
+    const int j0 = (int)(k - i * per) * len, j = j0 + (int)threadIdx.x, end = min((int)g.N, j0 + len);
+    if (j < end) f(i, j, (end - j + kThreads - 1) / kThreads);
   }
 }
-// The sums of a run's columns (past the last one, the last one's), `from` columns on.
-__device__ __forceinline__ void run_sums(const lin::PartialSums& s, int64_t i, const int64_t (&j)[kPer], int64_t from,
-                                         float (&v)[kPer]) {
-  const float* p = s.part + i * s.ldp + from;
+// kPer elements, kThreads apart, of which `count` are there
+template <typename T>
+__device__ __forceinline__ void run_load(const T* p, int count, float (&v)[kPer]) {
 #pragma unroll
-  for (int e = 0; e < kPer; ++e) v[e] = __ldcg(p + j[e]);
+  for (int e = 0; e < kPer; ++e) v[e] = e < count ? (float)p[e * kThreads] : 0.f;
+}
+template <typename T>
+__device__ __forceinline__ void run_store(T* p, int count, const float (&v)[kPer]) {
+#pragma unroll
+  for (int e = 0; e < kPer; ++e)
+    if (e < count) round_to(v[e], p[e * kThreads]);
+}
+__device__ __forceinline__ void run_sums(const lin::PartialSums& s, int64_t i, int64_t j, int count,
+                                         float (&v)[kPer]) {
+  const float* p = s.part + i * s.ldp + j;
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) v[e] = e < count ? __ldcg(p + e * kThreads) : 0.f;
   for (int k = 1; k < s.splits; ++k) {
     p += s.stride;
 #pragma unroll
-    for (int e = 0; e < kPer; ++e) v[e] += __ldcg(p + j[e]);
+    for (int e = 0; e < kPer; ++e) v[e] += e < count ? __ldcg(p + e * kThreads) : 0.f;
   }
 }
-__device__ __forceinline__ void run_columns(int64_t j0, int64_t N, int64_t (&j)[kPer]) {
+// What is not finite of a product of planes, looked at again.  (A pass of its own: with
+// the call in the kernel's loop that loop spills, 106 us instead of 38.)
+__device__ __forceinline__ bool run_finite(const float (&v)[kPer]) {
+  bool f = true;
 #pragma unroll
-  for (int e = 0; e < kPer; ++e) j[e] = min(j0 + e * kThreads, N - 1);
+  for (int e = 0; e < kPer; ++e) f = f && isfinite(v[e]);
+  return f;
 }
-// One sum, what is not finite of a product of planes looked at again.
-__device__ float sum_again(const lin::PartialSums& s, const lin::Again* again, int64_t i, int64_t j) {
-  const int64_t at = i * s.ldp + j;
-  float v = 0.f;
-  for (int k = 0; k < s.splits; ++k) v += __ldcg(s.part + k * s.stride + at);
-  return isfinite(v) ? v : lin::dot_again(again, i, j, at);
+__device__ __noinline__ void run_again(const lin::PartialSums& s, const lin::Again* again, int64_t i, int64_t j, int count,
+                                       float* v) {
+  for (int e = 0; e < count; ++e)
+    if (!isfinite(v[e])) v[e] = lin::dot_again(again, i, j + e * kThreads, i * s.ldp + j + e * kThreads);
+}
+
+// act(a), and its slope, of a run: the choice is made once
+template <int ACT>
+__device__ __forceinline__ void act_run(const float (&a)[kPer], float (&v)[kPer], float (&s)[kPer]) {
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) {
+    v[e] = act_value<false>(ACT, a[e]);
+    s[e] = act_slope<false>(ACT, a[e]);
+  }
+}
+__device__ __forceinline__ void act_run(int act, const float (&a)[kPer], float (&v)[kPer], float (&s)[kPer]) {
+  switch (act) {
+    case PPO_ACT_TANH: act_run<PPO_ACT_TANH>(a, v, s); break;
+    case PPO_ACT_RELU: act_run<PPO_ACT_RELU>(a, v, s); break;
+    case PPO_ACT_SILU: act_run<PPO_ACT_SILU>(a, v, s); break;
+    case PPO_ACT_GELU: act_run<PPO_ACT_GELU>(a, v, s); break;
+    default: act_run<PPO_ACT_NONE>(a, v, s); break;
+  }
 }
 
 template <typename T>
-__device__ __forceinline__ void put_forward(const Gate& g, int64_t i, int64_t j, float a, float u) {
+__device__ __forceinline__ void put_forward(const Gate& g, int64_t i, int j, int count, float (&a)[kPer],
+                                            float (&u)[kPer]) {
   if (g.bias) {
-    a += g.bias[j];
-    u += g.bias[g.N + j];
+    float b[kPer];
+    run_load(g.bias + j, count, b);
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) a[e] += b[e];
+    run_load(g.bias + g.N + j, count, b);
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) u[e] += b[e];
   }
   if (g.pre) {
-    T* o = static_cast<T*>(g.pre) + i * g.ldpre;
-    round_to(a, o[j]);
-    round_to(u, o[g.N + j]);
+    T* o = static_cast<T*>(g.pre) + i * g.ldpre + j;
+    run_store(o, count, a);
+    run_store(o + g.N, count, u);
   }
-  round_to(act_value<false>(g.act, a) * u, static_cast<T*>(g.y)[i * g.ldy + j]);
+  float v[kPer], s[kPer];
+  act_run(g.act, a, v, s);
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) v[e] *= u[e];
+  run_store(static_cast<T*>(g.y) + i * g.ldy + j, count, v);
 }
-// The elements that the kernel has left out.  (A pass of its own: with the call in the
-// kernel's loop that loop spills, 106 us instead of 38.)
+template <typename T>
+__device__ __forceinline__ void put_backward(const Gate& g, int64_t i, int j, int count, const float (&d)[kPer],
+                                             const float (&a)[kPer], const float (&u)[kPer]) {
+  float v[kPer], s[kPer], x[kPer];
+  act_run(g.act, a, v, s);
+  T* o = static_cast<T*>(g.dp) + i * g.lddp + j;
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) x[e] = d[e] * u[e] * s[e];
+  run_store(o, count, x);
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) x[e] = d[e] * v[e];
+  run_store(o + g.N, count, x);
+  if (!g.y) return;
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) x[e] = v[e] * u[e];
+  run_store(static_cast<T*>(g.y) + i * g.ldy + j, count, x);
+}
+
 __device__ __noinline__ void forward_again(const Gate& g, const lin::Again* again) {
-  each_run(g.M, g.N, [&](int64_t i, int64_t j0, int64_t end) {
-    for (int64_t j = j0; j < end; j += kThreads) {
-      float v[2] = {};
-      for (int c = 0; c < 2; ++c)
-        for (int k = 0; k < g.s.splits; ++k) v[c] += __ldcg(g.s.part + k * g.s.stride + i * g.s.ldp + c * g.N + j);
-      if (isfinite(v[0]) && isfinite(v[1])) continue;
-      put_forward<float>(g, i, j, sum_again(g.s, again, i, j), sum_again(g.s, again, i, g.N + j));
-    }
+  each_run(g, [&](int64_t i, int j, int count) {
+    float a[kPer], u[kPer];
+    run_sums(g.s, i, j, count, a);
+    run_sums(g.s, i, g.N + j, count, u);
+    if (run_finite(a) && run_finite(u)) return;
+    run_again(g.s, again, i, j, count, a);
+    run_again(g.s, again, i, g.N + j, count, u);
+    put_forward<float>(g, i, j, count, a, u);
   });
 }
 template <typename T, bool PLANES>
@@ -99,39 +159,26 @@ __global__ void __launch_bounds__(kThreads)
 gate_forward_kernel(const __grid_constant__ Gate g, const __grid_constant__ lin::Again again) {
   pdl_wait();
   bool left = false;
-  each_run(g.M, g.N, [&](int64_t i, int64_t j0, int64_t end) {
-    int64_t j[kPer];
+  each_run(g, [&](int64_t i, int j, int count) {
     float a[kPer], u[kPer];
-    run_columns(j0, g.N, j);
-    run_sums(g.s, i, j, 0, a);
-    run_sums(g.s, i, j, g.N, u);
-#pragma unroll
-    for (int e = 0; e < kPer; ++e) {
-      if (j0 + e * kThreads >= end) break;
-      if (PLANES && !(isfinite(a[e]) && isfinite(u[e]))) left = true;
-      else put_forward<T>(g, i, j[e], a[e], u[e]);
-    }
+    run_sums(g.s, i, j, count, a);
+    run_sums(g.s, i, g.N + j, count, u);
+    if (PLANES && !(run_finite(a) && run_finite(u))) left = true;
+    else put_forward<T>(g, i, j, count, a, u);
   });
   if (PLANES && left) forward_again(g, &again);
 }
 
-template <typename T>
-__device__ __forceinline__ void put_backward(const Gate& g, int64_t i, int64_t j, float d, float a, float u) {
-  T* o = static_cast<T*>(g.dp) + i * g.lddp;
-  const float v = act_value<false>(g.act, a);
-  round_to(d * u * act_slope<false>(g.act, a), o[j]);
-  round_to(d * v, o[g.N + j]);
-  if (g.y) round_to(v * u, static_cast<T*>(g.y)[i * g.ldy + j]);
-}
 __device__ __noinline__ void backward_again(const Gate& g, const lin::Again* again) {
-  each_run(g.M, g.N, [&](int64_t i, int64_t j0, int64_t end) {
-    for (int64_t j = j0; j < end; j += kThreads) {
-      float v = 0.f;
-      for (int k = 0; k < g.s.splits; ++k) v += __ldcg(g.s.part + k * g.s.stride + i * g.s.ldp + j);
-      if (isfinite(v)) continue;
-      const float* p = static_cast<const float*>(g.pre_in) + i * g.ldin;
-      put_backward<float>(g, i, j, sum_again(g.s, again, i, j), p[j], p[g.N + j]);
-    }
+  each_run(g, [&](int64_t i, int j, int count) {
+    float d[kPer], a[kPer], u[kPer];
+    run_sums(g.s, i, j, count, d);
+    if (run_finite(d)) return;
+    run_again(g.s, again, i, j, count, d);
+    const float* p = static_cast<const float*>(g.pre_in) + i * g.ldin + j;
+    run_load(p, count, a);
+    run_load(p + g.N, count, u);
+    put_backward<float>(g, i, j, count, d, a, u);
   });
 }
 template <typename T, bool PLANES>
@@ -139,24 +186,14 @@ __global__ void __launch_bounds__(kThreads)
 gate_backward_kernel(const __grid_constant__ Gate g, const __grid_constant__ lin::Again again) {
   pdl_wait();
   bool left = false;
-  each_run(g.M, g.N, [&](int64_t i, int64_t j0, int64_t end) {
-    const T* p = static_cast<const T*>(g.pre_in) + i * g.ldin;
-    int64_t j[kPer];
+  each_run(g, [&](int64_t i, int j, int count) {
+    const T* p = static_cast<const T*>(g.pre_in) + i * g.ldin + j;
     float d[kPer], a[kPer], u[kPer];
-    run_columns(j0, g.N, j);
-#pragma unroll
-    for (int e = 0; e < kPer; ++e) {
-      a[e] = (float)p[j[e]];
-      u[e] = (float)p[g.N + j[e]];
-    }
-    run_sums(g.s, i, j, 0, d);
-    // (in place: what was read past the last column, of the last one, is not used)
-#pragma unroll
-    for (int e = 0; e < kPer; ++e) {
-      if (j0 + e * kThreads >= end) break;
-      if (PLANES && !isfinite(d[e])) left = true;
-      else put_backward<T>(g, i, j[e], d[e], a[e], u[e]);
-    }
+    run_load(p, count, a);
+    run_load(p + g.N, count, u);
+    run_sums(g.s, i, j, count, d);
+    if (PLANES && !run_finite(d)) left = true;
+    else put_backward<T>(g, i, j, count, d, a, u);
   });
   if (PLANES && left) backward_again(g, &again);
 }
