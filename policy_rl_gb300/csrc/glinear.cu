@@ -10,7 +10,7 @@
 // kernel here finishes them: what it writes is rounded once, from fp32.  Forward
 // products of few rows have kernels of their own.
 // fp32, 4,999 x 512 -> 1,365, forward with pre and backward with y: 204 us, floor 66 as six
-// bf16 products; of them the planes 14, the products 123, the gates 67 for the 300 MB
+// bf16 products; of them the planes 14, the products 123, the gates 69 for the 300 MB
 // that they read and write (70 with a choice of activation for each element).  Up to 64
 // bf16 rows: glinear_skinny.cu.
 #include <algorithm>
