@@ -107,6 +107,22 @@ def test_loss_masked(P, M, V, dtype):
     check_loss(P, M, V, dtype, seed=M * 37 + V, masked=True)
 
 
+# rows enough that the kernels are chosen for throughput: blocks of 128, 256 and 512 threads, two
+# blocks a row, clusters of 2, 4 and 8 blocks of 1,024, two lanes a row
+@pytest.mark.parametrize("M,V,dtype,masked",
+                         [(160, 8000, "bf16", True), (700, 8001, "bf16", False), (161, 4000, "f32", True),
+                          (170, 12345, "bf16", True), (900, 16000, "bf16", False), (170, 8004, "f32", False),
+                          (333, 32768, "bf16", True), (320, 20011, "bf16", False), (160, 16383, "f32", True),
+                          (170, 50257, "bf16", True), (153, 65536, "bf16", False), (155, 20001, "f32", True),
+                          (160, 70001, "bf16", True), (160, 40000, "f32", False), (155, 140000, "bf16", True),
+                          (153, 70004, "f32", False), (153, 132001, "f32", True),
+                          (16385, 18, "f32", True), (20000, 31, "bf16", True), (16384, 8, "bf16", False),
+                          (40000, 3, "f32", True), (70001, 2, "bf16", False), (5000, 60, "bf16", True),
+                          (3001, 250, "f32", True), (2000, 1000, "bf16", True), (2500, 2040, "bf16", False)])
+def test_many_rows_of_every_length(P, M, V, dtype, masked):
+    check_loss(P, M, V, dtype, seed=M + V, masked=masked)
+
+
 @pytest.mark.parametrize("M", [1, 63, 1000, 5003])
 def test_many_rows(P, M):
     check_loss(P, M, 18, "f32", seed=M, masked=True)
@@ -160,6 +176,18 @@ def test_in_place(P, V, dtype):
     got = run_loss(P, c, dtype, in_place=True)
     for x, y in zip(want, got):
         assert torch.equal(torch.nan_to_num(x), torch.nan_to_num(y))
+
+
+@pytest.mark.parametrize("M,V", [(20000, 7), (3000, 121), (1000, 1001), (700, 8001), (400, 20001), (200, 50257),
+                                 (160, 70001)])
+def test_in_place_many_odd_rows(P, M, V):
+    """Neighbouring rows share 16 bytes at their ends, and are written while others are read."""
+    import torch
+    c = make(M, V, "bf16", V, False)
+    want = run_loss(P, c, "bf16")
+    got = run_loss(P, c, "bf16", in_place=True)
+    for x, y in zip(want, got):
+        assert torch.equal(x, y)
 
 
 @pytest.mark.parametrize("V", [18, 1000, 50257])
@@ -307,6 +335,24 @@ def test_streams_graphs_and_determinism(P, M, V):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(g, want[0]) and torch.equal(st, want[3])
+
+
+def test_two_streams_at_once(P):
+    """Calls that overlap, a workspace each."""
+    import torch
+    cs = [make(2000, 5001, "bf16", k, False) for k in range(2)]
+    want = [[t.clone() for t in run_loss(P, c, "bf16")] for c in cs]
+    streams = [torch.cuda.Stream() for _ in cs]
+    made = [(ints(c["a"]), dev(c["old"]), dev(c["adv"]), dev(c["ref"]), dev(c["weight"]), out((2000, 5001), "bf16"),
+             out((8,)), out((P.ppo_action_loss_workspace_bytes() // 4,))) for c in cs]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for c, s, (a, old, adv, ref, w, g, st, work) in zip(cs, streams, made):
+            P.ppo_action_loss_grad(c["l"], a, old, adv, g, 1 / 2000, logp_ref=ref, weight=w, stats=st, work=work,
+                                   stream=s)
+    torch.cuda.synchronize()
+    for (first, _, _, stats), m in zip(want, made):
+        assert torch.equal(first, m[5]) and torch.equal(stats, m[6])
 
 
 def test_refusals(P):

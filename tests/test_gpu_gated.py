@@ -109,6 +109,7 @@ def check_backward(P, M, N, J, dtype, act="silu", with_y=True, pitches=(None,) *
 # one row; few; odd; more than a tile; several tiles a CTA; sums that are split
 SIZES = [(1, 1, 1), (1, 512, 128), (1, 2048, 512), (2, 33, 70), (3, 7, 5), (4, 100, 1397), (8, 256, 256), (17, 40, 64), (33, 512, 512),
          (64, 65, 130), (100, 128, 64), (129, 127, 96), (128, 128, 64), (200, 300, 256), (300, 136, 1000), (513, 1001, 200),
+         (20, 3, 1), (64, 1, 9), (48, 129, 64), (49, 200, 4000),
          (1000, 64, 72), (2049, 520, 128), (70, 2048, 2048), (5000, 24, 40)]
 
 
@@ -219,9 +220,9 @@ def test_few_rows(P):
                 check_forward(P, M, N, K, dtype, seed=M, pitches=(K + 1, None, N + 3, None) if N == 37 else (None,) * 4)
 
 
-def test_streams_graphs_and_determinism(P):
+@pytest.mark.parametrize("M,N,K", [(300, 200, 96), (1, 200, 96), (33, 200, 1024), (64, 4000, 96), (4, 1024, 4096)])
+def test_streams_graphs_and_determinism(P, M, N, K):
     import torch
-    M, N, K = 300, 200, 96
     rng = np.random.default_rng(2)
     x, w = dev(rng.normal(size=(M, K)), "bf16"), dev(rng.normal(size=(2 * N, K)), "bf16")
     dz, w2 = dev(rng.normal(size=(M, K)), "bf16"), dev(rng.normal(size=(K, N)), "bf16")
