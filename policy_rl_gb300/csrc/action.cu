@@ -344,8 +344,9 @@ struct RowShared {
 // A row belongs to G threads (lanes of a warp, a block, or all blocks of a cluster),
 // each of which keeps up to GR of its 16-byte pieces in registers between the
 // statistics and the gradient, so that the row is read once.  ON16: all rows, of
-// the gradient too, start on 16-byte boundaries.
-template <typename T, int G, int GR, bool ON16>
+// the gradient too, start on 16-byte boundaries.  MASK: there may be a mask.  CLUSTER:
+// more than one block a row.  (Each of them at run time costs registers that the row needs.)
+template <typename T, int G, int GR, bool ON16, bool MASK, bool CLUSTER>
 __global__ void __launch_bounds__(G <= kWarp ? kRowThreads : G, G <= kWarp ? 8 : GR > 8 || G == 1024 ? 1 : 1024 / G)
 action_kernel(const ActionArgs p) {
   using P = Piece<T>;
@@ -354,18 +355,18 @@ action_kernel(const ActionArgs p) {
   constexpr int R = kLanes ? kRowThreads / G : 1;       // rows of a block at a time
   constexpr int NW = kLanes ? 1 : G / kWarp;
   constexpr int L = kLanes ? G : kWarp;
-  __shared__ float4 entry[2][kLanes ? 1 : kMaxCluster * NW];
+  __shared__ float4 entry[2][kLanes ? 1 : (CLUSTER ? kMaxCluster : 1) * NW];
   __shared__ RowShared shared;
   __shared__ float2 sum[kTerms][R];
   const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp;
   const int t = kLanes ? threadIdx.x % G : threadIdx.x;
-  const uint32_t cn = kLanes ? 1 : cluster_size(), cr = kLanes ? 0 : cluster_rank();
+  const uint32_t cn = CLUSTER ? cluster_size() : 1, cr = CLUSTER ? cluster_rank() : 0;
   const int64_t stride = (int64_t)(gridDim.x / cn) * R;
   const RowSums sums{&sum[0][kLanes ? threadIdx.x / G : 0], R};
   if (t == 0) {
     for (int i = 0; i < kTerms; ++i) sums.at[i * R] = make_float2(0.f, 0.f);
   }
-  const uint8_t* mend = p.mask ? p.mask + (p.M - 1) * p.ldm + p.V : nullptr;
+  const uint8_t* mend = MASK && p.mask ? p.mask + (p.M - 1) * p.ldm + p.V : nullptr;
   const char* lfrom = static_cast<const char*>(p.l);
   const char* lto = lfrom + ((p.M - 1) * p.ld + p.V) * (int64_t)ES;
   if (cn > 1) {        // the other blocks' shared memory is there
@@ -427,7 +428,7 @@ action_kernel(const ActionArgs p) {
     const Place at = place(row);
     const char* la = at.la;
     const int off = at.off, nq = at.nq;
-    const uint8_t* mrow = p.mask ? p.mask + row * p.ldm : nullptr;
+    const uint8_t* mrow = MASK && p.mask ? p.mask + row * p.ldm : nullptr;
     // (no branch waits for these)
     RowInput in{next_a, 0.f, 0.f, 0.f, 0.f, 0.f, 1.f};
     if (kLanes || warp == 0) {
@@ -545,28 +546,22 @@ action_kernel(const ActionArgs p) {
         __syncthreads();
       }
       if (warp == 0) {
-        constexpr int PER = (kMaxCluster * NW + kWarp - 1) / kWarp;
-        float4 v[PER];
+        // (read twice rather than kept: the row fills this warp's registers too)
+        const int n = (int)cn * NW;
         float m = -CUDART_INF_F;
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-          const int w = lane + i * kWarp;
-          v[i] = w < (int)cn * NW ? entry[par][w] : make_float4(-CUDART_INF_F, 0.f, 0.f, 0.f);
-          m = fmaxf(m, v[i].x);
-        }
+        for (int i = lane; i < n; i += kWarp) m = fmaxf(m, entry[par][i].x);
         st.m = lanes_max<kWarp>(m);
         float s = 0.f, w = 0.f;
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
+        for (int i = lane; i < n; i += kWarp) {
           // A warp's sums, counted from its own maximum, by what its logits' u is off the
           // row's: as the gradient will have it.  (Nothing allowed there: they are 0, or NaN.)
-          const float m1 = v[i].x;
-          const float from = is_wild<T>(m1) ? 0.f : m1 * kLog2e;
-          const float d = m1 == -CUDART_INF_F ? 0.f : max_nan(from - base_for<T>(st.m, m1), kLow);
+          const float4 v = entry[par][i];
+          const float from = is_wild<T>(v.x) ? 0.f : v.x * kLog2e;
+          const float d = v.x == -CUDART_INF_F ? 0.f : max_nan(from - base_for<T>(st.m, v.x), kLow);
           float f;
           asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(f) : "f"(d));
-          s += f * v[i].y;
-          w += f * fmaf(v[i].y, d, v[i].z);
+          s += f * v.y;
+          w += f * fmaf(v.y, d, v.z);
         }
         st.s = lanes_sum<kWarp>(s);
         st.t = lanes_sum<kWarp>(w);
@@ -662,7 +657,7 @@ action_stats_kernel(const float* __restrict__ part, int blocks, float* __restric
 // ---- launch ------------------------------------------------------------------------------
 constexpr int kSms = 152;
 
-template <typename T, int G, int GR, bool ON16>
+template <typename T, int G, int GR, bool ON16, bool MASK, bool CLUSTER>
 cudaError_t launch(const ActionArgs& p, int cn, float* stats, cudaStream_t st) {
   constexpr int R = G <= kWarp ? kRowThreads / G : 1, threads = G <= kWarp ? kRowThreads : G;
   // two blocks of 512 threads an SM, or as many threads in smaller ones
@@ -690,13 +685,13 @@ cudaError_t launch(const ActionArgs& p, int cn, float* stats, cudaStream_t st) {
     e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (prepared != dev) {
-      e = cudaFuncSetAttribute(action_kernel<T, G, GR, ON16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+      e = cudaFuncSetAttribute(action_kernel<T, G, GR, ON16, MASK, CLUSTER>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                threads * GR * 16);
       if (e != cudaSuccess) return e;
       prepared = dev;
     }
   }
-  e = cudaLaunchKernelEx(&cfg, action_kernel<T, G, GR, ON16>, p);
+  e = cudaLaunchKernelEx(&cfg, action_kernel<T, G, GR, ON16, MASK, CLUSTER>, p);
   if (e != cudaSuccess || !stats) return e;
   return launch_pdl(action_stats_kernel, dim3(1), dim3(kTerms * kWarp), 0, st, (const float*)p.part, blocks, stats);
 }
@@ -704,8 +699,23 @@ template <typename T, int G, int GR>
 cudaError_t go(const ActionArgs& p, int cn, float* stats, cudaStream_t st) {
   constexpr int E = Piece<T>::E;
   auto on16 = [](const void* m, int64_t ld) { return al16(m) && ld % E == 0; };
-  return on16(p.l, p.ld) && on16(p.dl, p.dl ? p.lddl : 0) ? launch<T, G, GR, true>(p, cn, stats, st)
-                                                          : launch<T, G, GR, false>(p, cn, stats, st);
+  const bool whole = on16(p.l, p.ld) && on16(p.dl, p.dl ? p.lddl : 0);
+  if constexpr (G >= 512) {
+    if (cn > 1)
+      return whole && !p.mask ? launch<T, G, GR, true, false, true>(p, cn, stats, st)
+             : whole          ? launch<T, G, GR, true, true, true>(p, cn, stats, st)
+             : !p.mask        ? launch<T, G, GR, false, false, true>(p, cn, stats, st)
+                              : launch<T, G, GR, false, true, true>(p, cn, stats, st);
+  }
+  if constexpr (G > kWarp && G < 1024 && GR <= 8) {
+    if (!p.mask)
+      return whole ? launch<T, G, GR, true, false, false>(p, 1, stats, st)
+                   : launch<T, G, GR, false, false, false>(p, 1, stats, st);
+  }
+  if constexpr (G < 1024 && GR <= 8)
+    return whole ? launch<T, G, GR, true, true, false>(p, 1, stats, st)
+                 : launch<T, G, GR, false, true, false>(p, 1, stats, st);
+  return cudaErrorInvalidValue;      // (such rows take a cluster)
 }
 
 template <typename T>
