@@ -431,7 +431,20 @@ action_kernel(const ActionArgs p) {
     const uint8_t* mrow = MASK && p.mask ? p.mask + row * p.ldm : nullptr;
     // (no branch waits for these)
     RowInput in{next_a, 0.f, 0.f, 0.f, 0.f, 0.f, 1.f};
-    if (kLanes || warp == 0) {
+    float one_of = 0.f;      // blocks: a lane of the first warp holds one of the row's numbers
+    if (!kLanes && warp == 0) {
+      const float* from = lane == 1 ? p.old : lane == 2 ? p.adv : lane == 3 ? p.ref : lane == 4 ? p.weight : nullptr;
+      if (lane == 0) {
+        const int a = max(next_a, 0);
+        one_of = (float)reinterpret_cast<const T*>(la)[a];
+        if (mrow) one_of = mrow[a] ? one_of : -CUDART_INF_F;
+      } else if (from) {
+        one_of = from[row];
+      } else if (lane == 4) {
+        one_of = 1.f;
+      }
+    }
+    if (kLanes) {
       const int a = max(in.a, 0);
       in.x = (float)reinterpret_cast<const T*>(la)[a];
       if (mrow) in.x = mrow[a] ? in.x : -CUDART_INF_F;
@@ -565,6 +578,11 @@ action_kernel(const ActionArgs p) {
         }
         st.s = lanes_sum<kWarp>(s);
         st.t = lanes_sum<kWarp>(w);
+        in.x = __shfl_sync(0xffffffffu, one_of, 0);
+        in.old = __shfl_sync(0xffffffffu, one_of, 1);
+        in.adv = __shfl_sync(0xffffffffu, one_of, 2);
+        in.ref = __shfl_sync(0xffffffffu, one_of, 3);
+        in.w = __shfl_sync(0xffffffffu, one_of, 4);
         in.u = action_u();
         r = row_terms(p, row, st, in, lane == 0 && cr == 0, sums);
         if (lane == 0) shared = RowShared{r, st.m, in.u};
