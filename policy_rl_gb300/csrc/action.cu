@@ -511,6 +511,13 @@ action_kernel(const ActionArgs p) {
       const int64_t next = row_of(row0 + stride);
       fetch(place(next));
       next_a = action_of(next);
+      if (MASK && !kLanes && mrow && threadIdx.x == 0) {
+        // this block's run of the next row's mask towards L2, in whole 16 bytes
+        const uint8_t* m = p.mask + next * p.ldm;
+        const uintptr_t a = (reinterpret_cast<uintptr_t>(m) + (int)cr * chunk * E + 15) & ~(uintptr_t)15;
+        const uintptr_t z = (reinterpret_cast<uintptr_t>(m) + min(p.V, ((int)cr + 1) * chunk * E)) & ~(uintptr_t)15;
+        if (a < z) ptx::bulk_prefetch_l2(reinterpret_cast<const void*>(a), (uint32_t)(z - a));
+      }
     }
     st.m = lanes_max<L>(st.m);
     const float m0 = st.m;
