@@ -12,16 +12,20 @@
 // use, so that its rounding cancels between 2^u, s and t.
 //
 // What bounds it: memory, the row read once and the gradient written once, and of bf16
-// rows as much the 17 instructions of an element (two exponentials among them), whose
-// warps wait at the row's reduction.  A row therefore stays in registers between the two,
-// 64 elements a thread, two blocks of 512 threads an SM; the next row comes meanwhile by
-// copies into shared memory.  Measured (of the copy rate): 8,192 x 32,768 bf16 212 us
-// (75 %), 8,192 x 16,384 fp32 175 (90 %), 1,001 x 50,257 bf16 with a mask 92 (41 %: rows off
-// 16-byte boundaries, two blocks a row, 30 instructions an element), 65,536 x 18 fp32
-// with a mask 10.3 in a graph (launch, one round of rows and the sums), one row of 131,072
-// bf16 6.4.  Left: the row kept in shared memory and more threads (217 to 252), blocks of
-// 1,024 threads for rows of 32,768 (235), the mask's bytes fetched ahead too (96; registers
-// spill).
+// rows as much the 17 instructions of an element, two exponentials among them.  A row
+// therefore stays in registers between its statistics and its gradient, 64 elements a
+// thread, two blocks of 512 threads an SM; the next row comes meanwhile by copies
+// into shared memory.  Registers are what it is made of: 20 bytes of spills less in the
+// kernel of 8,192 x 32,768 were worth 14 % (hence masks and clusters at compile time, a
+// row's own numbers one to a lane, joined statistics read twice).
+// Measured in a graph (of the copy rate): 8,192 x 32,768 bf16 183 us (87 %), with a mask 287
+// (69 %), 8,192 x 16,384 fp32 167 (95 %), 1,001 x 50,257 bf16 56 (53 %: one block an SM, rows
+// off 16-byte boundaries, seven rounds of 152 rows), with a mask 77, 65,536 x 18 fp32 with
+// a mask 10.3 (one round of rows, their terms, the sums), one row of 131,072 bf16 6.4.
+// Left: the row kept in shared memory and more threads (8,192 x 32,768 217 to 252), the mask's bytes
+// fetched into shared memory ahead (its L2 lines are: 1,001 x 50,257 98 without),
+// a cluster's statistics by copies that count on barriers of their own (4,096 x
+// 131,072 635).
 #include <algorithm>
 #include <math_constants.h>
 
@@ -732,12 +736,12 @@ cudaError_t go(const ActionArgs& p, int cn, float* stats, cudaStream_t st) {
              : !p.mask        ? launch<T, G, GR, false, false, true>(p, cn, stats, st)
                               : launch<T, G, GR, false, true, true>(p, cn, stats, st);
   }
-  if constexpr (G > kWarp && G < 1024 && GR <= 8) {
+  if constexpr (G > kWarp && GR <= 8) {
     if (!p.mask)
       return whole ? launch<T, G, GR, true, false, false>(p, 1, stats, st)
                    : launch<T, G, GR, false, false, false>(p, 1, stats, st);
   }
-  if constexpr (G < 1024 && GR <= 8)
+  if constexpr (GR <= 8)
     return whole ? launch<T, G, GR, true, true, false>(p, 1, stats, st)
                  : launch<T, G, GR, false, true, false>(p, 1, stats, st);
   return cudaErrorInvalidValue;      // (such rows take a cluster)
@@ -764,10 +768,11 @@ cudaError_t run_rows(const ActionArgs& p, float* stats, cudaStream_t st) {
   const bool few = p.M < kSms;
   if (nq <= 1024 && !few) return go<T, 128, 8>(p, 1, stats, st);
   if (nq <= 2048 && !few) return go<T, 256, 8>(p, 1, stats, st);
-  // Long rows, many of them: clusters of as few blocks as hold one.  (4,096 x 131,072 bf16
-  // 672 us with four blocks of 512 threads, 518 with two of 1,024; but 1,001 x 50,257 66 and 70
-  // with two and one, 8,192 x 32,768 207 and 235 with one of either)
-  if (nq > 8192 && !few) return go<T, 1024, 8>(p, nq <= 16384 ? 2 : nq <= 32768 ? 4 : 8, stats, st);
+  // Long rows, many of them: blocks of 1,024 threads, alone or in clusters of as few as hold
+  // one.  (1,001 x 50,257 bf16 56 us with one and 66 with two of 512, 4,000 x 32,000 fp32 162
+  // and 185, 4,096 x 131,072 434 with two and 672 with four of 512; but 8,192 x 32,768 255
+  // with one of 1,024 and 183 with one of 512, which leave room for two rows an SM)
+  if (nq > 4096 && !few) return go<T, 1024, 8>(p, nq <= 8192 ? 1 : nq <= 16384 ? 2 : nq <= 32768 ? 4 : 8, stats, st);
   int cn = 1;
   while (cn < kMaxCluster && (nq > 4096 * cn || (p.M * cn * 2 <= kSms && nq > 1024 * cn))) cn *= 2;
   return nq <= 4096 * cn ? go<T, 512, 8>(p, cn, stats, st) : go<T, 512, 16>(p, cn, stats, st);
