@@ -9,9 +9,10 @@
 // tiles enough.  Others leave fp32 sums, partial ones where the sum is split, and one
 // kernel here finishes them: what it writes is rounded once, from fp32.  Forward
 // products of few rows have kernels of their own.
-// fp32, 4,999 x 512 -> 1,365, forward with pre and backward with y: 204 us, floor 66 as six
-// bf16 products; of them the planes 14, the products 123, the gates 69 for the 300 MB
-// that they read and write (70 with a choice of activation for each element).  Up to 64
+// fp32, 4,999 x 512 -> 1,365, forward with pre and backward with y: 198 us, floor 66 as six
+// bf16 products; of them the planes 14, the products 123, the gates 60 for the 300 MB
+// that they read and write (75 with a choice of activation for each element and a division
+// for each run).  Up to 64
 // bf16 rows: glinear_skinny.cu.
 #include <algorithm>
 
@@ -34,16 +35,16 @@ constexpr int kSms = 152;
 constexpr int kPer = 4, kRun = kPer * kThreads;
 
 // f(row, this thread's first column, how many of its columns there are) of this block's
-// runs, all of about one length
+// runs, all of about one length: blocks along y take a row's runs, those along x the rows
 template <typename F>
 __device__ __forceinline__ void each_run(const Gate& g, F f) {
-  const uint32_t per = (uint32_t)((g.N + kRun - 1) / kRun);
+  const int per = (int)((g.N + kRun - 1) / kRun);
   const int len = (int)((g.N + per - 1) / per + kWarp - 1) / kWarp * kWarp;
-  const int64_t n = g.M * per;
-  for (int64_t k = blockIdx.x; k < n; k += gridDim.x) {
-    const int64_t i = n < (1ll << 32) ? (int64_t)((uint32_t)k / per) : k / per;
-    const int j0 = (int)(k - i * per) * len, j = j0 + (int)threadIdx.x, end = min((int)g.N, j0 + len);
-    if (j < end) f(i, j, (end - j + kThreads - 1) / kThreads);
+  for (int c = blockIdx.y; c < per; c += gridDim.y) {
+    const int j = c * len + (int)threadIdx.x, end = min((int)g.N, (c + 1) * len);
+    if (j >= end) continue;
+    const int count = (end - j + kThreads - 1) / kThreads;
+    for (int64_t i = blockIdx.x; i < g.M; i += gridDim.x) f(i, j, count);
   }
 }
 // kPer elements, kThreads apart, of which `count` are there
@@ -200,8 +201,9 @@ gate_backward_kernel(const __grid_constant__ Gate g, const __grid_constant__ lin
 
 template <typename K>
 cudaError_t finish(K kernel, const Gate& g, const lin::Product& m, cudaStream_t st) {
-  const int64_t runs = g.M * ((g.N + kRun - 1) / kRun);
-  return launch_pdl(kernel, dim3((unsigned)std::min<int64_t>(runs, 16 * kSms)), dim3(kThreads), 0, st, g,
+  const int64_t runs = std::min<int64_t>((g.N + kRun - 1) / kRun, 1024);
+  const int64_t rows = std::min<int64_t>(g.M, std::max<int64_t>(1, 16 * kSms / runs));
+  return launch_pdl(kernel, dim3((unsigned)rows, (unsigned)runs), dim3(kThreads), 0, st, g,
                     lin::Again{m, g.s.part, g.s.stride, g.s.splits, g.s.r_per_split});
 }
 
