@@ -9,9 +9,10 @@
 // across them; where they would overflow or lose digits, scaled by a power of two
 // (the ranges of Blue 1978, "A portable Fortran program to find the Euclidean norm
 // of a vector") and then in 64 bits.  64 bits throughout would be simpler, but a warp's
-// FP64 instruction takes 15 clocks of an SM: the reductions of 1,024 threads 10 us.  Every block leaves one partial sum, and the scaling kernel adds
-// them in a fixed order, so results do not depend on timing.  It walks the runs from
-// their other ends, so that it finds the last chunks in L2.  Both are bound by memory.
+// FP64 instruction takes 15 clocks of an SM: the reductions of 1,024 threads 10 us.
+// Every block leaves one partial sum, and the scaling kernel adds them in a fixed
+// order, so results do not depend on timing.  It walks the runs from their other
+// ends, so that it finds the last chunks in L2.  Both are bound by memory.
 // Measured: 500,000,000 elements in 300 tensors, bf16 and fp32 (1.42 GB), 659 us for norm
 // and clip, which move 4.27 GB: 96 % of the copy rate (element by element 1,256, pieces
 // without the chunk ahead 713; four blocks an SM spill and take 6 % longer).  100,000
