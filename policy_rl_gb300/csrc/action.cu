@@ -189,48 +189,46 @@ __device__ __forceinline__ uint32_t spread(uint32_t v, uint32_t selector) {
   asm("prmt.b32 %0, %1, %1, %2;" : "=r"(r) : "r"(v), "r"(selector));
   return r;
 }
-// Elements of a piece that are not allowed become -inf: element i is the row's j + i.
-// Its mask bytes are taken as the aligned words that hold them where those lie inside
-// the mask's [from, to), else one by one.
-template <typename T>
-__device__ __forceinline__ void cover(Piece<T>& x, const uint8_t* row, int j, int V, const uint8_t* from,
-                                      const uint8_t* to) {
-  constexpr int E = Piece<T>::E;
+// The mask bytes of a piece, four of them a word: E bytes from `sh` on in the two words
+// of E bytes at a.
+template <int E>
+__device__ __forceinline__ void mask_words(const uint8_t* a, int sh, uint32_t (&v)[E / 4]) {
   using Word = typename RawOf<E>::type;       // 4 or 8 bytes
-  const uint8_t* at = row + j;
-  const int sh = (int)(reinterpret_cast<uintptr_t>(at) & (E - 1));
-  const uint8_t* a = at - sh;
-  uint32_t v[E / 4];
-  if (j >= 0 && j + E <= V && a >= from && a + 2 * E <= to) {
-    uint32_t b[E / 4 + 1 + (E == 8)] = {};
-    const Word w0 = *reinterpret_cast<const Word*>(a);
-    memcpy(b, &w0, E);
-    if (sh) {
-      const Word w1 = *reinterpret_cast<const Word*>(a + E);
-      memcpy(b + E / 4, &w1, E);
-    }
-    if constexpr (E == 8) {
-      if (sh & 4) {
-        b[0] = b[1];
-        b[1] = b[2];
-        b[2] = b[3];
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < E / 4; ++i) v[i] = __funnelshift_r(b[i], b[i + 1], 8 * (sh & 3));
-  } else {
-#pragma unroll
-    for (int i = 0; i < E / 4; ++i) {
-      v[i] = 0;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int e = j + 4 * i + k;
-        if (e >= 0 && e < V && row[e]) v[i] |= 1u << (8 * k);
-      }
+  uint32_t b[E / 4 + 1 + (E == 8)] = {};
+  const Word w0 = *reinterpret_cast<const Word*>(a);
+  memcpy(b, &w0, E);
+  if (sh) {
+    const Word w1 = *reinterpret_cast<const Word*>(a + E);
+    memcpy(b + E / 4, &w1, E);
+  }
+  if constexpr (E == 8) {
+    if (sh & 4) {
+      b[0] = b[1];
+      b[1] = b[2];
+      b[2] = b[3];
     }
   }
 #pragma unroll
+  for (int i = 0; i < E / 4; ++i) v[i] = __funnelshift_r(b[i], b[i + 1], 8 * (sh & 3));
+}
+// The same one by one, for the mask's first and last: 0 where the row has none.
+template <int E>
+__device__ __forceinline__ void mask_bytes(const uint8_t* row, int j, int V, uint32_t (&v)[E / 4]) {
+#pragma unroll
   for (int i = 0; i < E / 4; ++i) {
+    v[i] = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int e = j + 4 * i + k;
+      if (e >= 0 && e < V && row[e]) v[i] |= 1u << (8 * k);
+    }
+  }
+}
+// Elements of a piece whose mask bytes are 0 become -inf.
+template <typename T>
+__device__ __forceinline__ void cover(Piece<T>& x, const uint32_t (&v)[Piece<T>::E / 4]) {
+#pragma unroll
+  for (int i = 0; i < Piece<T>::E / 4; ++i) {
     // the top bit of each byte that is not 0, spread over the element by PRMT's sign mode
     const uint32_t nz = ((v[i] & 0x7f7f7f7fu) + 0x7f7f7f7fu) | v[i];
     if constexpr (sizeof(T) == 2) {
@@ -487,13 +485,24 @@ action_kernel(const ActionArgs p) {
         }
       }
     }
-    if (mrow) {
+    if (MASK && mrow) {
+      // the aligned words that hold the row's bytes, two for each piece: all lie in the mask,
+      // or those of the first and last pieces may not
+      const uint8_t* mb = mrow - off;
+      const int sh = (int)(reinterpret_cast<uintptr_t>(mb) & (E - 1));
+      mb -= sh;
+      const bool all = mb >= p.mask && mb + (int64_t)(at.last + 2) * E <= mend;
 #pragma unroll
       for (int k = 0; k < GR; ++k) {
         const int q = q0 + k * G;
-        if (q < nq) cover(x[k], mrow, q * E - off, p.V, p.mask, mend);
+        if (q >= nq) break;
+        uint32_t v[E / 4];
+        if (all || (q > 0 && q + 1 < at.last)) mask_words<E>(mb + q * E, sh, v);
+        else mask_bytes<E>(mrow, q * E - off, p.V, v);
+        cover(x[k], v);
       }
-    } else if constexpr (!ON16) {
+    }
+    if constexpr (!ON16) {
 #pragma unroll
       for (int k = 0; k < GR; ++k) {
         const int q = q0 + k * G;
