@@ -765,6 +765,18 @@ cudaError_t run_rows(const ActionArgs& p, float* stats, cudaStream_t st) {
   // (many rows: fewer threads for each, so that a row's terms cost fewer warps.  65,536 x
   // 18 fp32 with a mask 13.4 us with four lanes, 10.3 with two; 4,096 x 18 4.2 and 4.7)
   if (nq <= 8 && p.M >= 16384) return go<T, 2, 4>(p, 1, stats, st);
+  // Rows enough that fewer threads for each still fill the GPU (ten warps an SM): eight pieces
+  // a thread.  (30,000 x 300 bf16 32 us with a warp a row, 18 with eight lanes; 100,000 x 100 29 and
+  // 21; 8,000 x 700 14.6 and 11.9 with 16; but 2,000 x 700 6.9 and 9.3)
+  if (nq > 8 && nq <= 128) {
+    const int lanes = nq <= 16 ? 2 : nq <= 32 ? 4 : nq <= 64 ? 8 : 16;
+    if (p.M * lanes >= 320 * kSms) {
+      if (lanes == 2) return go<T, 2, 8>(p, 1, stats, st);
+      if (lanes == 4) return go<T, 4, 8>(p, 1, stats, st);
+      if (lanes == 8) return go<T, 8, 8>(p, 1, stats, st);
+      return go<T, 16, 8>(p, 1, stats, st);
+    }
+  }
   if (nq <= 4) return go<T, 4, 1>(p, 1, stats, st);
   if (nq <= 8) return go<T, 4, 2>(p, 1, stats, st);
   if (nq <= 16) return go<T, 8, 2>(p, 1, stats, st);

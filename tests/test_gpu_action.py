@@ -118,6 +118,9 @@ def test_loss_masked(P, M, V, dtype):
                           (153, 70004, "f32", False), (153, 132001, "f32", True),
                           (16385, 18, "f32", True), (20000, 31, "bf16", True), (16384, 8, "bf16", False),
                           (40000, 3, "f32", True), (70001, 2, "bf16", False), (5000, 60, "bf16", True),
+                          (30001, 60, "bf16", True), (13001, 150, "bf16", True), (7000, 301, "bf16", False),
+                          (3300, 900, "bf16", True), (30000, 33, "f32", False), (14000, 100, "f32", True),
+                          (6500, 252, "f32", False), (3300, 500, "f32", True),
                           (3001, 250, "f32", True), (2000, 1000, "bf16", True), (2500, 2040, "bf16", False)])
 def test_many_rows_of_every_length(P, M, V, dtype, masked):
     check_loss(P, M, V, dtype, seed=M + V, masked=masked)
