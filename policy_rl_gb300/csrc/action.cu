@@ -18,8 +18,8 @@
 // into shared memory.  Registers are what it is made of: 20 bytes of spills less in the
 // kernel of 8,192 x 32,768 were worth 14 % (hence masks and clusters at compile time, a
 // row's own numbers one to a lane, joined statistics read twice).
-// Measured in a graph (of the copy rate): 8,192 x 32,768 bf16 183 us (87 %), with a mask 287
-// (69 %), 8,192 x 16,384 fp32 167 (95 %), 1,001 x 50,257 bf16 56 (53 %: one block an SM, rows
+// Measured in a graph (of the copy rate): 8,192 x 32,768 bf16 183 us (87 %), with a mask 271
+// (73 %), 8,192 x 16,384 fp32 167 (95 %), 1,001 x 50,257 bf16 56 (53 %: one block an SM, rows
 // off 16-byte boundaries, seven rounds of 152 rows), with a mask 77, 65,536 x 18 fp32 with
 // a mask 10.3 (one round of rows, their terms, the sums), one row of 131,072 bf16 6.4.
 // Left: the row kept in shared memory and more threads (8,192 x 32,768 217 to 252), the mask's bytes
