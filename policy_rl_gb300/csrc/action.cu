@@ -700,6 +700,9 @@ cudaError_t launch(const ActionArgs& p, int cn, float* stats, cudaStream_t st) {
   constexpr int R = G <= kWarp ? kRowThreads / G : 1, threads = G <= kWarp ? kRowThreads : G;
   // two blocks of 512 threads an SM, or as many threads in smaller ones
   constexpr int top = G <= kWarp ? kMaxBlocks : kSms * (GR > 8 ? 1 : 1024 / G);
+  // a block's run of a row's pieces, as the kernel counts it: no plan leaves any of them out
+  const int most = (p.V + Piece<T>::E - 1) / Piece<T>::E + (ON16 ? 0 : 1);
+  if ((most + cn - 1) / cn > G * GR) return cudaErrorInvalidValue;
   const int64_t want = (p.M + R - 1) / R;
   const int blocks = (int)std::min<int64_t>(want, top / cn) * cn;
   cudaLaunchConfig_t cfg = {};
@@ -785,6 +788,12 @@ cudaError_t run_rows(const ActionArgs& p, float* stats, cudaStream_t st) {
   if (nq <= 128) return go<T, 32, 4>(p, 1, stats, st);
   if (nq <= 256) return go<T, 32, 8>(p, 1, stats, st);
   if (nq <= 512) return go<T, 128, 4>(p, 1, stats, st);
+  // (a longest fp32 row off 16 bytes has a piece more than eight blocks of 8,192)
+  if constexpr (sizeof(T) == 4) {
+    if (nq > kMaxCluster * 8192)
+      return p.mask ? launch<T, 1024, 9, false, true, true>(p, kMaxCluster, stats, st)
+                    : launch<T, 1024, 9, false, false, true>(p, kMaxCluster, stats, st);
+  }
   // few rows: more blocks for each, down to two pieces a thread
   const bool few = p.M < kSms;
   if (nq <= 1024 && !few) return go<T, 128, 8>(p, 1, stats, st);
