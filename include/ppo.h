@@ -730,7 +730,8 @@ ppo_status ppo_gated_linear_backward_data(int32_t dtype, const void *d_dz, int64
  * of a row over its allowed actions,
  *   logp = lp[action],   entropy = -sum exp(lp) lp.
  * An action outside [0, V) marks a row without one: logp 0.  An action that is
- * not allowed (or whose logit is -inf) has logp -inf; a row of which nothing is
+ * not allowed (or whose logit is -inf) has logp -inf; any finite logit has a
+ * finite logp, fp32's lowest number at least.  A row of which nothing is
  * allowed has entropy 0.  Pointers need only their elements' alignment here.
  * Statistics are fp32; V <= PPO_MAX_ACTIONS, M < 2^31 (PPO_ERR_UNSUPPORTED).
  * NaN and infinities pass through as the formulas give them, but not from

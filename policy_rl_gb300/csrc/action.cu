@@ -27,6 +27,7 @@
 // a cluster's statistics by copies that count on barriers of their own (4,096 x
 // 131,072 635).
 #include <algorithm>
+#include <cfloat>
 #include <math_constants.h>
 
 #include "ops.cuh"
@@ -58,6 +59,7 @@ struct ActionArgs {
 };
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kLow = -1e30f;       // what stands for -inf in a row's pieces
 
 // A row's statistics: maximum, sum of 2^u, sum of 2^u u.
 struct Stat {
@@ -95,13 +97,16 @@ __device__ __forceinline__ RowTerms row_terms(const ActionArgs& p, int64_t row, 
   const bool has = in.a >= 0;
   const float logs = logf(st.s);
   const float H = st.s == 0.f ? 0.f : logs - st.t / st.s * kLn2;
-  const float lp = has ? (in.x == -CUDART_INF_F ? in.x : in.u * kLn2 - logs) : 0.f;
+  // (u ends at kLow, where p is 0 long since; a finite logit's logp does not)
+  const bool none = in.x == -CUDART_INF_F;
+  const float far = in.x - st.m, d = far < 0.5f * kLow ? fmaxf(far, -FLT_MAX) : in.u * kLn2;
+  const float lp = has ? (none ? in.x : d - logs) : 0.f;
   if (lead) {
     if (p.logp) p.logp[row] = lp;
     if (p.entropy) p.entropy[row] = H;
   }
   if (!p.dl) return r;
-  if (!has || lp == -CUDART_INF_F) {
+  if (!has || none) {
     if (lead && p.part) sums.add(7, 1.f);
     return r;
   }
@@ -283,7 +288,6 @@ __device__ __forceinline__ float2 exp_pair(float2 x, float base, float2& u) {
 // is all.  Past that m k's rounding would be felt, and the logits become their
 // distances from m: exact ones in fp32; in bf16, where neighbours are 2^8 apart from
 // 2^15 on, 0 at the maximum and kLow elsewhere (2^u is 1 and 0).
-constexpr float kLow = -1e30f;
 template <typename T>
 __device__ __forceinline__ bool is_wild(float m) { return !(fabsf(m) < (sizeof(T) == 2 ? 32768.f : 65536.f)); }
 template <typename T>
@@ -562,7 +566,7 @@ action_kernel(const ActionArgs p) {
     // the action's u as the row's pieces have it
     auto action_u = [&]() {
       const bool far = is_wild<T>(st.m);
-      return fmaf(far ? max_nan(in.x - st.m, kLow) : in.x, kLog2e, far ? 0.f : -st.m * kLog2e);
+      return fmaf(max_nan(far ? in.x - st.m : in.x, kLow), kLog2e, far ? 0.f : -st.m * kLog2e);
     };
     RowTerms r;
     if constexpr (kLanes) {

@@ -1,5 +1,5 @@
-"""Log-probability, entropy and policy loss at the limits of their plans: the longest rows.
-Bounds as in test_gpu_action.py."""
+"""Log-probability, entropy and policy loss at the limits of their plans: the longest rows,
+finite logits of the type's lowest value.  Bounds as in test_gpu_action.py."""
 import numpy as np
 import pytest
 
@@ -56,3 +56,49 @@ def test_the_longest_rows(P, V, pitch, out_pitch, times, masked):
     assert (room[0] == 7) and (room[1 + M * out_pitch:] == 7).all()
     if out_pitch > V:
         assert (torch.as_strided(room, (M, out_pitch - V), (out_pitch, 1), 1 + V) == 7).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("V", [5, 300, 1000, 5000, 20001, 131072])
+def test_an_action_of_the_lowest_logit(P, V, dtype):
+    """A finite logit counts, however low (masks are often made so): such an action's row is kept,
+    with a ratio of 0; logp is the logit less the row's log-sum, or the lowest number."""
+    import torch
+    low = torch.finfo(tdt(dtype)).min
+    rng = np.random.default_rng(V)
+    l = dev(rng.normal(size=(7, V)), dtype)
+    a = np.full(7, V - 2)
+    for i, x in enumerate((low, low, -2.5e38, -1e31, low, -5e29, low)):
+        l[i, V - 2] = x
+    l[1, 0] = 1e6                   # rows taken relative to their maximum
+    l[4, 0] = 2e38
+    l[5, 0] = 6e29
+    l[6, :] = low
+    l[6, V - 2] = low / 2
+    l64 = f64(l)
+    z = A.softmax_rows(l64, a)
+    want = np.maximum(z["logp"], -np.finfo(np.float32).max)
+    lp, H = out((7,)), out((7,))
+    P.ppo_action_logp(l, ints(a), logp=lp, entropy=H)
+    within(lp, want, 4 * A.U * np.abs(want) + z["b_logp"] * (np.abs(want) < 1), "logp")
+    within(H, z["H"], z["b_H"], "entropy")
+    # the loss: an advantage of 0 leaves the entropy's gradient, the same as for another action
+    zero, one = dev(np.zeros(7)), dev(np.ones(7))
+    other = ints([1] * 7)
+    got, st = [], out((8,))
+    work = out((P.ppo_action_loss_workspace_bytes() // 4,))
+    for act in (ints(a), other):
+        g = out((7, V), dtype)
+        P.ppo_action_loss_grad(l, act, zero, zero, g, 0.5, ent_coef=ENT, stats=st, work=work)
+        got.append(g)
+        assert float(st[7]) == 0 and float(st[6]) == 3.5
+        assert abs(float(st[3]) - 0.5 * z["H"].sum()) <= 0.5 * z["b_H"].sum() + 16 * A.U * z["H"].sum()
+    assert torch.isfinite(got[0]).all() and torch.equal(got[0], got[1])
+    # and an advantage that counts is multiplied by a ratio of 0 (row 6: of 1)
+    g = out((7, V), dtype)
+    P.ppo_action_loss_grad(l, ints(a), zero, one, g, 0.5, ent_coef=ENT, stats=st, work=work)
+    assert torch.equal(g[:6], got[0][:6])
+    # -inf alone means that there is no such action
+    l[0, V - 2] = float("-inf")
+    P.ppo_action_loss_grad(l, ints(a), zero, one, g, 0.5, ent_coef=ENT, stats=st, work=work)
+    assert float(st[7]) == 1 and (g[0] == 0).all()
