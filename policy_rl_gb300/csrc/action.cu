@@ -317,10 +317,13 @@ __device__ __forceinline__ void make_safe_wild(Piece<T>& x, float m) {
     x.put(i, make_float2(distance<T>(v.x, m), distance<T>(v.y, m)));
   }
 }
+// m k, rounded wherever it is used: fused into a sum it would keep what the other uses drop, by
+// which a warp's sums and its gradients would differ (0.3 % at m = 60,000)
+__device__ __forceinline__ float scaled(float m) { return __fmul_rn(m, kLog2e); }
 // m k of a row whose maximum is m, for the logits of a warp whose own is m0
 template <typename T>
 __device__ __forceinline__ float base_for(float m, float m0) {
-  return fminf(is_wild<T>(m0) ? m - m0 : m, -kLow) * kLog2e;
+  return scaled(fminf(is_wild<T>(m0) ? m - m0 : m, -kLow));
 }
 
 __device__ __forceinline__ uint32_t cluster_size() {
@@ -548,7 +551,7 @@ action_kernel(const ActionArgs p) {
     }
     float2 s2 = make_float2(0.f, 0.f), t2 = make_float2(0.f, 0.f);
     {
-      const float base = wild ? 0.f : m0 * kLog2e;
+      const float base = wild ? 0.f : scaled(m0);
 #pragma unroll
       for (int k = 0; k < GR; ++k) {
         if (q0 - t + k * G >= nq) break;       // (the same in all the row's threads)
@@ -566,7 +569,7 @@ action_kernel(const ActionArgs p) {
     // the action's u as the row's pieces have it
     auto action_u = [&]() {
       const bool far = is_wild<T>(st.m);
-      return fmaf(max_nan(far ? in.x - st.m : in.x, kLow), kLog2e, far ? 0.f : -st.m * kLog2e);
+      return fmaf(max_nan(far ? in.x - st.m : in.x, kLow), kLog2e, far ? 0.f : -scaled(st.m));
     };
     RowTerms r;
     if constexpr (kLanes) {
@@ -593,7 +596,7 @@ action_kernel(const ActionArgs p) {
           // A warp's sums, counted from its own maximum, by what its logits' u is off the
           // row's: as the gradient will have it.  (Nothing allowed there: they are 0, or NaN.)
           const float4 v = entry[par][i];
-          const float from = is_wild<T>(v.x) ? 0.f : v.x * kLog2e;
+          const float from = is_wild<T>(v.x) ? 0.f : scaled(v.x);
           const float d = v.x == -CUDART_INF_F ? 0.f : max_nan(from - base_for<T>(st.m, v.x), kLow);
           float f;
           asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(f) : "f"(d));

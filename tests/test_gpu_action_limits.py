@@ -1,5 +1,5 @@
 """Log-probability, entropy and policy loss at the limits of their plans: the longest rows,
-finite logits of the type's lowest value.  Bounds as in test_gpu_action.py."""
+logits far from 0, finite logits of the type's lowest value.  Bounds as in test_gpu_action.py."""
 import numpy as np
 import pytest
 
@@ -56,6 +56,38 @@ def test_the_longest_rows(P, V, pitch, out_pitch, times, masked):
     assert (room[0] == 7) and (room[1 + M * out_pitch:] == 7).all()
     if out_pitch > V:
         assert (torch.as_strided(room, (M, out_pitch - V), (out_pitch, 1), 1 + V) == 7).all()
+
+
+def far_rows(M, V, base, dtype, seed):
+    """Rows whose logits lie around `base`."""
+    rng = np.random.default_rng(seed)
+    return dev(base + 2 * rng.normal(size=(M, V)), dtype)
+
+
+def check_rows(P, l, dtype, seed, scale=0.25):
+    """The loss on l, with ratios as in make()."""
+    M, V = l.shape
+    c = make(M, V, dtype, seed, False)
+    c["a"] = np.random.default_rng(seed).integers(0, V, M)
+    c["a"][0] = int(f64(l)[0].argmax())
+    base = A.softmax_rows(f64(l), c["a"])["logp"]
+    c["old"] = (base - np.array([-0.5, -0.1, 0.02, 0.1, 0.5])[np.arange(M) % 5]).astype(np.float32)
+    c["ref"] = (base + 0.3 * np.random.default_rng(seed).normal(size=M)).astype(np.float32)
+    c["weight"] = np.ones(M, np.float32)
+    g = out((M, V), dtype)
+    close((g, *loss(P, l, g, c, scale)), c, f64(l), dtype, scale)
+
+
+# lanes of a warp, a warp, blocks of 128 to 1,024 threads, clusters
+LENGTHS = [(5, 9), (5, 300), (5, 1000), (5, 3000), (5, 9000), (3, 20001), (3, 70000), (2, 131072)]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("base", [100, -1000, 5000, -30000, 60000, -60000])
+@pytest.mark.parametrize("M,V", LENGTHS)
+def test_logits_around_a_large_number(P, M, V, base, dtype):
+    """What all logits share cancels, whichever warp a logit is in."""
+    check_rows(P, far_rows(M, V, base, dtype, V), dtype, V)
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
