@@ -320,10 +320,24 @@ __device__ __forceinline__ void make_safe_wild(Piece<T>& x, float m) {
 // m k, rounded wherever it is used: fused into a sum it would keep what the other uses drop, by
 // which a warp's sums and its gradients would differ (0.3 % at m = 60,000)
 __device__ __forceinline__ float scaled(float m) { return __fmul_rn(m, kLog2e); }
-// m k of a row whose maximum is m, for the logits of a warp whose own is m0
+// What that rounding drops of m k: distances from m, which are exact, are brought by it to what
+// the others count from, since both kinds meet in a row whose warps lie on either side of the
+// border.  (Not in bf16, where 2^u is 1 or 0 there; past 2^17 logits of the other kind are
+// so far off that their 2^u is 0.)
+template <typename T>
+__device__ __forceinline__ float dropped(float m) {
+  return sizeof(T) == 4 && fabsf(m) < 131072.f ? fmaf(m, kLog2e, -scaled(m)) : 0.f;
+}
+// what to take from a logit's k-fold (a wild warp's: from its distance's) for u, in a row
+// whose maximum is m and a warp whose own is m0
 template <typename T>
 __device__ __forceinline__ float base_for(float m, float m0) {
-  return scaled(fminf(is_wild<T>(m0) ? m - m0 : m, -kLow));
+  return is_wild<T>(m0) ? scaled(fminf(m - m0, -kLow)) - dropped<T>(m) : scaled(fminf(m, -kLow));
+}
+// the same of a warp's own maximum
+template <typename T>
+__device__ __forceinline__ float own_base(float m0) {
+  return is_wild<T>(m0) ? -dropped<T>(m0) : scaled(m0);
 }
 
 __device__ __forceinline__ uint32_t cluster_size() {
@@ -551,7 +565,7 @@ action_kernel(const ActionArgs p) {
     }
     float2 s2 = make_float2(0.f, 0.f), t2 = make_float2(0.f, 0.f);
     {
-      const float base = wild ? 0.f : scaled(m0);
+      const float base = own_base<T>(m0);
 #pragma unroll
       for (int k = 0; k < GR; ++k) {
         if (q0 - t + k * G >= nq) break;       // (the same in all the row's threads)
@@ -569,7 +583,7 @@ action_kernel(const ActionArgs p) {
     // the action's u as the row's pieces have it
     auto action_u = [&]() {
       const bool far = is_wild<T>(st.m);
-      return fmaf(max_nan(far ? in.x - st.m : in.x, kLow), kLog2e, far ? 0.f : -scaled(st.m));
+      return fmaf(max_nan(far ? in.x - st.m : in.x, kLow), kLog2e, -own_base<T>(st.m));
     };
     RowTerms r;
     if constexpr (kLanes) {
@@ -596,8 +610,7 @@ action_kernel(const ActionArgs p) {
           // A warp's sums, counted from its own maximum, by what its logits' u is off the
           // row's: as the gradient will have it.  (Nothing allowed there: they are 0, or NaN.)
           const float4 v = entry[par][i];
-          const float from = is_wild<T>(v.x) ? 0.f : scaled(v.x);
-          const float d = v.x == -CUDART_INF_F ? 0.f : max_nan(from - base_for<T>(st.m, v.x), kLow);
+          const float d = v.x == -CUDART_INF_F ? 0.f : max_nan(own_base<T>(v.x) - base_for<T>(st.m, v.x), kLow);
           float f;
           asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(f) : "f"(d));
           s += f * v.y;

@@ -1,5 +1,6 @@
 """Log-probability, entropy and policy loss at the limits of their plans: the longest rows,
-logits far from 0, finite logits of the type's lowest value.  Bounds as in test_gpu_action.py."""
+logits far from 0 on both sides of where they are taken relative to the maximum,
+finite logits of the type's lowest value.  Bounds as in test_gpu_action.py."""
 import numpy as np
 import pytest
 
@@ -88,6 +89,33 @@ LENGTHS = [(5, 9), (5, 300), (5, 1000), (5, 3000), (5, 9000), (3, 20001), (3, 70
 def test_logits_around_a_large_number(P, M, V, base, dtype):
     """What all logits share cancels, whichever warp a logit is in."""
     check_rows(P, far_rows(M, V, base, dtype, V), dtype, V)
+
+
+@pytest.mark.parametrize("base", [65536, -65536, 65540.5, -65531.5, 65900, 120000, -120000, 140000])
+@pytest.mark.parametrize("M,V", LENGTHS)
+def test_logits_around_the_border(P, M, V, base):
+    """Past |maximum| = 65,536 a warp takes fp32 logits relative to its own: rows of which
+    some warps do so and others do not."""
+    check_rows(P, far_rows(M, V, base, "f32", V), "f32", V)
+
+
+@pytest.mark.parametrize("top,rest", [(65537.25, 65533.0), (65536.0, 65535.5), (-65533.0, -65537.25), (65580.0, 65530.0)])
+@pytest.mark.parametrize("M,V", LENGTHS[3:] + [(160, 9000), (160, 40001)])
+def test_one_warp_across_the_border(P, M, V, top, rest):
+    """One logit of a row lies on the border's other side."""
+    import torch
+    rng = np.random.default_rng(V)
+    l = dev(rest + 0.25 * rng.integers(-1, 1, (min(M, 4), V)))
+    for i in range(l.shape[0]):
+        l[i, (i * 7919 + V // 3) % V] = top
+    check_rows(P, l.repeat(M // l.shape[0], 1) if M > 4 else l, "f32", V)
+
+
+@pytest.mark.parametrize("base", [32512, 32768, -32768, 33024])
+@pytest.mark.parametrize("M,V", [(5, 300), (5, 9000), (3, 20001), (2, 131072)])
+def test_bf16_logits_around_the_border(P, M, V, base):
+    rng = np.random.default_rng(V)
+    check_rows(P, dev(base + 128.0 * rng.integers(-2, 3, (M, V)), "bf16"), "bf16", V)
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
