@@ -82,7 +82,8 @@ struct Sum {
 template <typename T>
 __device__ __forceinline__ void add_squares(Sum& a, const uint4 (&x)[kPieces]) {
   const float v = piece_sum<T>(x, 1.f);
-  if (v == 0.f || (v > 0x1p-100f && v < 0x1p100f)) {
+  // (what is summed in fp32 stays in its range, however many tensors: 2^60 such sums)
+  if (v == 0.f || (v > 0x1p-100f && v < 0x1p64f)) {
     const float y = v - a.c, t = a.s + y;
     a.c = (t - a.s) - y;
     a.s = t;
