@@ -11,7 +11,7 @@
 // of a vector") and then in 64 bits.  64 bits throughout would be simpler, but a warp's
 // FP64 instruction takes 15 clocks of an SM: the reductions of 1,024 threads 10 us.
 // Every block leaves one partial sum, and the scaling kernel adds them in a fixed
-// order, so results do not depend on timing.  It walks the runs from their other
+// order, with compensation too, so results do not depend on timing.  It walks the runs from their other
 // ends, so that it finds the last chunks in L2.  Both are bound by memory.
 // Measured: 500,000,000 elements in 300 tensors, bf16 and fp32 (1.42 GB), 659 us for norm
 // and clip, which move 4.27 GB: 96 % of the copy rate (element by element 1,256, pieces
@@ -79,14 +79,17 @@ struct Sum {
   double odd;
   float s, c;
 };
+__device__ __forceinline__ void add_plain(Sum& a, float v) {
+  const float y = v - a.c, t = a.s + y;
+  a.c = (t - a.s) - y;
+  a.s = t;
+}
 template <typename T>
 __device__ __forceinline__ void add_squares(Sum& a, const uint4 (&x)[kPieces]) {
   const float v = piece_sum<T>(x, 1.f);
   // (what is summed in fp32 stays in its range, however many tensors: 2^60 such sums)
   if (v == 0.f || (v > 0x1p-100f && v < 0x1p64f)) {
-    const float y = v - a.c, t = a.s + y;
-    a.c = (t - a.s) - y;
-    a.s = t;
+    add_plain(a, v);
     if (v != 0.f) return;
     // (0, or too small to be squared)
   }
@@ -242,15 +245,24 @@ sumsq_kernel(const __grid_constant__ Table<N> t, Sum* __restrict__ part) {
   if (threadIdx.x == 0) part[blockIdx.x] = a;
 }
 
-// The norm from all partial sums, the same in every block.
-__device__ __forceinline__ float norm_of(const Sum* part, int parts) {
+// The sum of all partial sums, the same in every block.
+__device__ __forceinline__ Sum total_of(const Sum* part, int parts) {
   Sum a{};
   for (int i = threadIdx.x; i < parts; i += kThreads) {
     const Sum b = part[i];
     if (!plain(b)) a.odd += b.odd;
-    a.s += b.s;
+    add_plain(a, b.s);
   }
-  return root(block_total(a));
+  return block_total(a);
+}
+__device__ __forceinline__ float norm_of(const Sum* part, int parts) { return root(total_of(part, parts)); }
+
+// The partial sums of several tables become one, the first: the scaling kernels of all tables
+// read no other.
+__global__ void __launch_bounds__(kThreads) total_kernel(Sum* part, int parts) {
+  pdl_wait();
+  const Sum a = total_of(part, parts);      // (all threads have read theirs)
+  if (threadIdx.x == 0) part[0] = a;
 }
 
 __global__ void __launch_bounds__(kThreads)
@@ -329,6 +341,12 @@ cudaError_t run_table(const ppo_tensor* in, const ppo_tensor* out, int64_t n, in
     parts += blocks;
     return launch_pdl(sumsq_kernel<N>, dim3((unsigned)blocks), dim3(kThreads), 0, st, t, p);
   });
+  // From three tables on: each block would add up all tables' partial sums (10,000 tensors of 1,000
+  // floats, clipped, 343 us, 136 so; 1,300 26.5 and 23.7; but 700, two tables, 14.6 and 15.0)
+  if (e == cudaSuccess && scale && parts > 2 * kMaxBlocks) {
+    e = launch_pdl(total_kernel, dim3(1), dim3(kThreads), 0, st, part, parts);
+    parts = 1;
+  }
   bool wanted = true;      // the norm is still to be written
   if (e == cudaSuccess && scale)
     e = each_table<N>(in, out, n, [&](const Table<N>& t) {
