@@ -508,7 +508,7 @@ action_kernel(const ActionArgs p) {
     }
     if (MASK && mrow) {
       // the aligned words that hold the row's bytes, two for each piece: all lie in the mask,
-      // or those of the first and last pieces may not
+      // or those of the first two and last two pieces may not
       const uint8_t* mb = mrow - off;
       const int sh = (int)(reinterpret_cast<uintptr_t>(mb) & (E - 1));
       mb -= sh;
@@ -518,7 +518,7 @@ action_kernel(const ActionArgs p) {
         const int q = q0 + k * G;
         if (q >= nq) break;
         uint32_t v[E / 4];
-        if (all || (q > 0 && q + 1 < at.last)) mask_words<E>(mb + q * E, sh, v);
+        if (all || (q > 1 && q + 1 < at.last)) mask_words<E>(mb + q * E, sh, v);
         else mask_bytes<E>(mrow, q * E - off, p.V, v);
         cover(x[k], v);
       }

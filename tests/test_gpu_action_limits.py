@@ -162,3 +162,18 @@ def test_an_action_of_the_lowest_logit(P, V, dtype):
     l[0, V - 2] = float("-inf")
     P.ppo_action_loss_grad(l, ints(a), zero, one, g, 0.5, ent_coef=ENT, stats=st, work=work)
     assert float(st[7]) == 1 and (g[0] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("V", [11, 29, 301, 5003])
+def test_masks_inside_a_buffer(P, V, dtype):
+    """Masks that start anywhere, between bytes that say something else."""
+    import torch
+    M = 5
+    c = make(M, V, dtype, V, True)
+    for at in range(1, 10):
+        room = torch.full((M * V + 32,), at % 2, dtype=torch.uint8, device="cuda")
+        mask = room[at:at + M * V].view(M, V)
+        mask.copy_(flags(c["mask"]))
+        g = out((M, V), dtype, V + at % 3)
+        close((g, *loss(P, c["l"], g, c, 0.25, mask)), c, f64(c["l"]), dtype, 0.25)
