@@ -223,8 +223,9 @@ class ActionHead:
         pitch = (actions + 7) // 8 * 8
         self._l = torch.zeros(rows, pitch, **own)[:, :actions]
         self._dx = torch.empty(rows, width, **own)
-        self._work = torch.zeros(ppo_linear_workspace_bytes(rows, actions, width, self.dtype, ldz=pitch),
-                                 dtype=torch.uint8, device=device)
+        # (of x's rows at any pitch)
+        self._work = torch.zeros(ppo_linear_workspace_bytes(rows, actions, width, self.dtype, ldx=width | 1,
+                                                            ldz=pitch), dtype=torch.uint8, device=device)
         self._loss_work = torch.empty(ppo_action_loss_workspace_bytes(), dtype=torch.uint8, device=device)
         self.load_params()
 
