@@ -133,7 +133,7 @@ __device__ __forceinline__ void put_backward(const Gate& g, int64_t i, int j, in
   act_run(g.act, a, v, s);
   T* o = static_cast<T*>(g.dp) + i * g.lddp + j;
 #pragma unroll
-  for (int e = 0; e < kPer; ++e) x[e] = d[e] * u[e] * s[e];
+  for (int e = 0; e < kPer; ++e) x[e] = d[e] * s[e] * u[e];      // (d u may overflow where s is 0)
   run_store(o, count, x);
 #pragma unroll
   for (int e = 0; e < kPer; ++e) x[e] = d[e] * v[e];

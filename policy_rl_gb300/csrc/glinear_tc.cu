@@ -133,7 +133,8 @@ __device__ __forceinline__ void grad_all(const float2 (&d)[8], uint32_t (&g)[8],
     const float2 up = unpack_bf16x2(u[k]);
     float2 a, s;
     value_and_slope<ACT>(unpack_bf16x2(g[k]), a, s);
-    const float2 v = fmul2(a, up), dg = fmul2(fmul2(d[k], up), s), du = fmul2(d[k], a);
+    // (d u may overflow where the slope is 0)
+    const float2 v = fmul2(a, up), dg = fmul2(fmul2(d[k], s), up), du = fmul2(d[k], a);
     g[k] = pack_bf16x2(dg.x, dg.y);
     u[k] = pack_bf16x2(du.x, du.y);
     y[k] = pack_bf16x2(v.x, v.y);
