@@ -748,7 +748,7 @@ ppo_status ppo_action_logp(int32_t dtype, const void *d_logits, int64_t ld, int6
  *   kl = e^y - y - 1,  y = logp_ref - logp    (0 when d_logp_ref is NULL),
  *   loss = scale * sum over rows of w (pg + kl_coef kl - ent_coef entropy),
  * w = d_weight[row] (1 when NULL).  kl is the estimate of KL(pi || ref) at the
- * action taken.  d_dlogits [M][V] (pitch lddl, type dtype) receives dloss/dlogits:
+ * action taken; with a kl_coef of 0 it reaches d_stats alone, however large.  d_dlogits [M][V] (pitch lddl, type dtype) receives dloss/dlogits:
  *   scale w (c (1[j = action] - p_j) + ent_coef p_j (lp_j + entropy)),
  *   c = -A r [r A <= clip(r) A] + kl_coef (1 - e^y);
  * 0 where the mask covers.  It may be d_logits (same pitch).  Rows without an

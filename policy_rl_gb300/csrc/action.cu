@@ -119,11 +119,12 @@ __device__ __forceinline__ RowTerms row_terms(const ActionArgs& p, int64_t row, 
   if (p.ref) {
     const float y = in.ref - lp, em = expm1f(y);
     kl = em - y;
-    c -= p.kl * em;
+    // (a coefficient of 0 leaves out what fp32 may not hold: from y = 89 on)
+    if (p.kl != 0.f) c -= p.kl * em;
   }
   const float W = p.scale * in.w;
   if (lead && p.part) {
-    sums.add(0, W * (pg + p.kl * kl - p.ent * H));
+    sums.add(0, W * (pg + (p.kl != 0.f ? p.kl * kl : 0.f) - p.ent * H));
     sums.add(1, W * pg);
     sums.add(2, W * kl);
     sums.add(3, W * H);

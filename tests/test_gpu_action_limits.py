@@ -177,3 +177,25 @@ def test_masks_inside_a_buffer(P, V, dtype):
         mask.copy_(flags(c["mask"]))
         g = out((M, V), dtype, V + at % 3)
         close((g, *loss(P, c["l"], g, c, 0.25, mask)), c, f64(c["l"]), dtype, 0.25)
+
+
+@pytest.mark.parametrize("V", [5, 300, 5000, 131072])
+def test_a_reference_without_its_term(P, V):
+    """kl_coef = 0 with log-probabilities so far apart that e^y is no fp32 number: the KL estimate
+    says so, the loss and its gradient are those without a reference."""
+    import torch
+    M = 4
+    l = dev(np.random.default_rng(V).normal(size=(M, V)))
+    l[:, 1] = -120.0
+    a, adv, zero = ints([1] * M), dev([1.0, -1.0, 0.5, -2.0]), dev(np.zeros(M))
+    old, ref = torch.empty(M, device="cuda"), dev([0.0, -1.0, -100.0, -130.0])
+    P.ppo_action_logp(l, a, logp=old)
+    work = out((P.ppo_action_loss_workspace_bytes() // 4,))
+    got = []
+    for r in (None, ref):
+        g, st = out((M, V)), out((8,))
+        P.ppo_action_loss_grad(l, a, old, adv, g, 0.25, logp_ref=r, ent_coef=ENT, stats=st, work=work)
+        got.append((g, st))
+    assert torch.isfinite(got[1][0]).all() and torch.equal(got[0][0], got[1][0])
+    assert torch.equal(got[0][1][[0, 1, 3, 4, 5, 6, 7]], got[1][1][[0, 1, 3, 4, 5, 6, 7]])
+    assert torch.isinf(got[1][1][2])
