@@ -112,8 +112,10 @@ __device__ __forceinline__ RowTerms row_terms(const ActionArgs& p, int64_t row, 
   }
   if (in.w == 0.f) return r;
   const float u = lp - in.old, ratio = expf(u);
-  const float s1 = ratio * in.adv, s2 = fminf(fmaxf(ratio, p.lo), p.hi) * in.adv;
-  // (s1 alone is NaN where the ratio is, or is infinite beside an advantage of 0)
+  // (an advantage of 0 makes 0 of any ratio, of one past fp32's range too)
+  const float by = in.adv == 0.f && u < CUDART_INF_F ? 1.f : ratio;
+  const float s1 = by * in.adv, s2 = fminf(fmaxf(by, p.lo), p.hi) * in.adv;
+  // (s1 alone is NaN where the ratio is, or is e^inf beside an advantage of 0)
   const float pg = s1 <= s2 ? -s1 : s1 != s1 ? s1 : -s2;
   float c = s1 <= s2 ? -s1 : s1 != s1 ? s1 : 0.f, kl = 0.f;
   if (p.ref) {

@@ -199,3 +199,29 @@ def test_a_reference_without_its_term(P, V):
     assert torch.isfinite(got[1][0]).all() and torch.equal(got[0][0], got[1][0])
     assert torch.equal(got[0][1][[0, 1, 3, 4, 5, 6, 7]], got[1][1][[0, 1, 3, 4, 5, 6, 7]])
     assert torch.isinf(got[1][1][2])
+
+
+@pytest.mark.parametrize("clip_high", [0.2, float("inf")])
+@pytest.mark.parametrize("V", [5, 300, 5000, 131072])
+def test_an_advantage_of_zero(P, V, clip_high):
+    """It makes 0 of any ratio e^x, of those that are no fp32 number too: such rows have the entropy's
+    gradient alone.  An infinite x stays what the formula makes of it."""
+    import torch
+    M = 5
+    l = dev(np.random.default_rng(V).normal(size=(M, V)))
+    a, zero = ints([1] * M), dev(np.zeros(M))
+    work = out((P.ppo_action_loss_workspace_bytes() // 4,))
+    same, far = torch.empty(M, device="cuda"), dev([-100.0, -700.0, -1e9, -3e38, 1e9])
+    P.ppo_action_logp(l, a, logp=same)
+    got = []
+    for old in (same, far):
+        g, st = out((M, V)), out((8,))
+        P.ppo_action_loss_grad(l, a, old, zero, g, 0.25, clip_high=clip_high, ent_coef=ENT, stats=st, work=work)
+        got.append((g, st))
+    assert torch.isfinite(got[1][0]).all() and torch.equal(got[0][0], got[1][0])
+    assert torch.equal(got[0][1][[0, 1, 2, 3, 6, 7]], got[1][1][[0, 1, 2, 3, 6, 7]]) and float(got[1][1][1]) == 0
+    # (four ratios above every finite bound, one below)
+    assert float(got[1][1][4]) == (0.25 * 5 if clip_high < 1 else 0.25)
+    g = out((M, V))
+    P.ppo_action_loss_grad(l, a, dev([-np.inf, 0, 0, 0, 0]), zero, g, 0.25, ent_coef=ENT)
+    assert torch.isnan(g[0]).all() and torch.isfinite(g[1:]).all()
