@@ -77,17 +77,31 @@ struct RowInput {
   float x, u;              // the action's logit, -inf where it is not allowed, and its u
   float old, adv, ref, w;
 };
+// s.x: a sum, s.y: its compensation (none beside an infinity)
+__device__ __forceinline__ float2 add_kahan(float2 s, float x) {
+  const float y = x - s.y, t = s.x + y, r = (t - s.x) - y;
+  return make_float2(t, fabsf(t) < CUDART_INF_F ? r : 0.f);
+}
+// Two such sums as one, the rounding kept (the exact sum of two numbers of Knuth 1969, "The Art of
+// Computer Programming" 2)
+__device__ __forceinline__ float2 join_kahan(float2 a, float2 b) {
+  const float t = a.x + b.x, z = t - a.x, r = (a.x - (t - z)) + (b.x - z);
+  return make_float2(t, fabsf(t) < CUDART_INF_F ? (a.y + b.y) - r : 0.f);
+}
+// The sum of `n` lanes' next to one another, in each of them.
+__device__ __forceinline__ float2 lanes_kahan(float2 s, int n) {
+#pragma unroll
+  for (int o = n / 2; o > 0; o >>= 1)
+    s = join_kahan(s, make_float2(__shfl_xor_sync(0xffffffffu, s.x, o), __shfl_xor_sync(0xffffffffu, s.y, o)));
+  return s;
+}
 // A thread's sums over rows, in shared memory (only a row's first thread has any),
 // compensated (Kahan): an add costs four fp32 operations, where one in 64 bits would
 // hold the FP64 units for 15 clocks.
 struct RowSums {
   float2* at;              // [kTerms], `step` apart: sum and compensation
   int step;
-  __device__ __forceinline__ void add(int i, float x) {
-    const float2 s = at[i * step];
-    const float y = x - s.y, t = s.x + y, r = (t - s.x) - y;
-    at[i * step] = make_float2(t, fabsf(t) < CUDART_INF_F ? r : 0.f);
-  }
+  __device__ __forceinline__ void add(int i, float x) { at[i * step] = add_kahan(at[i * step], x); }
 };
 
 // Every thread of a row takes its terms; `lead` writes what the row gives and adds it up.
@@ -691,28 +705,44 @@ action_kernel(const ActionArgs p) {
     }
   }
   if (!p.part) return;
-  // the block's sums, in order
+  // the block's sums, in a fixed order: 16 threads to each of the terms (one thread that adds up to
+  // 64 of them loses 10 x 2^-24 of equal ones)
   __syncthreads();
-  if (threadIdx.x < kTerms) {
-    float v = 0.f;
-    for (int w = 0; w < R; ++w) v += sum[threadIdx.x][w].x;
-    p.part[(int64_t)threadIdx.x * gridDim.x + blockIdx.x] = v;
+  if constexpr (kLanes) {
+    constexpr int S = kRowThreads / kTerms;
+    const int term = threadIdx.x / S, w0 = threadIdx.x % S;
+    float2 v = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < R; w += S)
+      if (w + w0 < R) v = join_kahan(v, sum[term][w + w0]);
+    v = lanes_kahan(v, S);
+    if (w0 == 0) p.part[(int64_t)term * gridDim.x + blockIdx.x] = v.x - v.y;
+  } else if (threadIdx.x < kTerms) {
+    const float2 v = sum[threadIdx.x][0];
+    p.part[(int64_t)threadIdx.x * gridDim.x + blockIdx.x] = v.x - v.y;
   }
 }
 
-// d_stats from the blocks' sums: a warp for each of them, in a fixed order.
-__global__ void __launch_bounds__(kTerms * kWarp)
+// d_stats from the blocks' sums, in a fixed order: four warps for each of them, all loads at once.
+constexpr int kStatThreads = 128;
+__global__ void __launch_bounds__(kTerms * kStatThreads)
 action_stats_kernel(const float* __restrict__ part, int blocks, float* __restrict__ stats) {
+  constexpr int kPer = (kMaxBlocks + kStatThreads - 1) / kStatThreads, kWarps = kStatThreads / kWarp;
+  __shared__ float2 ws[kTerms][kWarps];
   pdl_wait();
-  const int i = threadIdx.x / kWarp, lane = threadIdx.x % kWarp;
-  float v[4] = {};
-  for (int b = lane; b < blocks; b += 4 * kWarp) {
+  const int i = threadIdx.x / kStatThreads, t = threadIdx.x % kStatThreads;
+  float x[kPer];
 #pragma unroll
-    for (int u = 0; u < 4; ++u)
-      if (b + u * kWarp < blocks) v[u] += part[(int64_t)i * blocks + b + u * kWarp];
-  }
-  const float s = warp_sum((v[0] + v[1]) + (v[2] + v[3]));
-  if (lane == 0) stats[i] = s;
+  for (int u = 0; u < kPer; ++u) x[u] = t + u * kStatThreads < blocks ? part[(int64_t)i * blocks + t + u * kStatThreads] : 0.f;
+  float2 s = make_float2(0.f, 0.f);
+#pragma unroll
+  for (int u = 0; u < kPer; ++u) s = add_kahan(s, x[u]);
+  s = lanes_kahan(s, kWarp);
+  if (t % kWarp == 0) ws[i][t / kWarp] = s;
+  __syncthreads();
+  if (threadIdx.x >= kTerms * kWarps) return;
+  s = lanes_kahan(ws[threadIdx.x / kWarps][threadIdx.x % kWarps], kWarps);
+  if (threadIdx.x % kWarps == 0) stats[threadIdx.x / kWarps] = s.x - s.y;
 }
 
 // ---- launch ------------------------------------------------------------------------------
@@ -757,7 +787,7 @@ cudaError_t launch(const ActionArgs& p, int cn, float* stats, cudaStream_t st) {
   }
   e = cudaLaunchKernelEx(&cfg, action_kernel<T, G, GR, ON16, MASK, CLUSTER>, p);
   if (e != cudaSuccess || !stats) return e;
-  return launch_pdl(action_stats_kernel, dim3(1), dim3(kTerms * kWarp), 0, st, (const float*)p.part, blocks, stats);
+  return launch_pdl(action_stats_kernel, dim3(1), dim3(kTerms * kStatThreads), 0, st, (const float*)p.part, blocks, stats);
 }
 template <typename T, int G, int GR>
 cudaError_t go(const ActionArgs& p, int cn, float* stats, cudaStream_t st) {

@@ -225,3 +225,25 @@ def test_an_advantage_of_zero(P, V, clip_high):
     g = out((M, V))
     P.ppo_action_loss_grad(l, a, dev([-np.inf, 0, 0, 0, 0]), zero, g, 0.25, ent_coef=ENT)
     assert torch.isnan(g[0]).all() and torch.isfinite(g[1:]).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("M,V", [(16452, 5), (65536, 5), (100003, 5), (300007, 2), (1000003, 3), (40000, 30), (70001, 60),
+                                 (9001, 300), (2003, 2000), (700, 9000)])
+def test_sums_over_many_equal_rows(P, M, V, dtype):
+    """Sums of equal terms, whose roundings do not cancel.  u = 2^-24: sums over a thread's rows and over
+    blocks are compensated, and joined with their roundings kept (2 u each, 1 where a block's and the
+    whole one are rounded): 6 u of a sum without signs; 8 u more for the terms' own products."""
+    l = dev(np.broadcast_to(np.linspace(-1, 1, V), (M, V)), dtype)
+    scale = np.float32(1.0 / M)
+    z = A.softmax_rows(f64(l[:1]), [0])
+    lp, H, st = out((M,)), out((M,)), out((8,))
+    work = out((P.ppo_action_loss_workspace_bytes() // 4,))
+    one = dev(np.ones(M))
+    old = dev(np.full(M, z["logp"][0] - 0.1))
+    P.ppo_action_loss_grad(l, ints(np.zeros(M)), old, one, out((M, V), dtype), scale, logp=lp, entropy=H, stats=st, work=work)
+    total = float(scale) * M
+    got = f64(st)
+    assert got[7] == 0 and got[4] == 0 and abs(got[6] - total) <= 6 * A.U * total, got[6] / total - 1
+    for k, term, own in ((3, z["H"][0], z["b_H"][0]), (1, -np.exp(float(z["logp"][0]) - f64(old)[0]), 2 * z["b_logp"][0])):
+        assert abs(got[k] - total * term) <= total * (own + 14 * A.U * abs(term)), (k, got[k], total * term)
