@@ -573,7 +573,9 @@ action_kernel(const ActionArgs p) {
     st.m = lanes_max<L>(st.m);
     const float m0 = st.m;
     const bool wild = is_wild<T>(m0);
+    float own = scaled(m0);      // own_base, of a wild warp after this
     if (wild) {
+      own = own_base<T>(m0);
 #pragma unroll
       for (int k = 0; k < GR; ++k) make_safe_wild(x[k], m0);
     } else {
@@ -581,18 +583,15 @@ action_kernel(const ActionArgs p) {
       for (int k = 0; k < GR; ++k) make_safe(x[k]);
     }
     float2 s2 = make_float2(0.f, 0.f), t2 = make_float2(0.f, 0.f);
-    {
-      const float base = own_base<T>(m0);
 #pragma unroll
-      for (int k = 0; k < GR; ++k) {
-        if (q0 - t + k * G >= nq) break;       // (the same in all the row's threads)
+    for (int k = 0; k < GR; ++k) {
+      if (q0 - t + k * G >= nq) break;       // (the same in all the row's threads)
 #pragma unroll
-        for (int i = 0; i < E / 2; ++i) {
-          float2 u;
-          const float2 e = exp_pair(x[k].pair(i), base, u);
-          s2 = ptx::ffma2(e, make_float2(1.f, 1.f), s2);
-          t2 = ptx::ffma2(e, u, t2);
-        }
+      for (int i = 0; i < E / 2; ++i) {
+        float2 u;
+        const float2 e = exp_pair(x[k].pair(i), own, u);
+        s2 = ptx::ffma2(e, make_float2(1.f, 1.f), s2);
+        t2 = ptx::ffma2(e, u, t2);
       }
     }
     st.s = lanes_sum<L>(s2.x + s2.y);
