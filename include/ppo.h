@@ -712,8 +712,9 @@ ppo_status ppo_gated_linear_forward(int32_t dtype, const void *d_x, int64_t ldx,
  * dz [M][J], its weight w2 [J][N].  With g = pre[:, 0..N-1], u = pre[:, N..2N-1]:
  *   d = dz W2,   dp = [ d u act'(g) | d act(g) ]  [M][2N],   y = act(g) u.
  * d_y [M][N] (nullable): y once more, for the gradient of w2, so that the
- * forward pass need not keep it.  The layer's own gradients are ppo_linear_*'s:
- * dx = dp W by ppo_linear_backward_data, dW and dbias by
+ * forward pass need not keep it; it is computed from pre as it was kept, in
+ * bf16 rounded, where the forward pass used the sums themselves.  The layer's own
+ * gradients are ppo_linear_*'s: dx = dp W by ppo_linear_backward_data, dW and dbias by
  * ppo_linear_backward_weight.  d_dp may be d_pre (same pitch). */
 ppo_status ppo_gated_linear_backward_data(int32_t dtype, const void *d_dz, int64_t lddz,
                                           const void *d_w2, int64_t ldw2, const void *d_pre,

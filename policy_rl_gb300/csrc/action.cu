@@ -12,20 +12,25 @@
 // use, so that its rounding cancels between 2^u, s and t.
 //
 // What bounds it: memory, the row read once and the gradient written once, and of bf16
-// rows as much the 17 instructions of an element, two exponentials among them.  A row
+// rows as much the 16 instructions of an element, two exponentials among them.  A row
 // therefore stays in registers between its statistics and its gradient, 64 elements a
 // thread, two blocks of 512 threads an SM; the next row comes meanwhile by copies
 // into shared memory.  Registers are what it is made of: 20 bytes of spills less in the
 // kernel of 8,192 x 32,768 were worth 14 % (hence masks and clusters at compile time, a
 // row's own numbers one to a lane, joined statistics read twice).
-// Measured in a graph (of the copy rate): 8,192 x 32,768 bf16 183 us (87 %), with a mask 271
-// (73 %), 8,192 x 16,384 fp32 167 (95 %), 1,001 x 50,257 bf16 56 (53 %: one block an SM, rows
+// Measured in a graph (of the copy rate): 8,192 x 32,768 bf16 182 us (87 %), with a mask 280
+// (71 %), 8,192 x 16,384 fp32 162 (98 %), 1,001 x 50,257 bf16 56 (53 %: one block an SM, rows
 // off 16-byte boundaries, seven rounds of 152 rows), with a mask 77, 65,536 x 18 fp32 with
-// a mask 10.3 (one round of rows, their terms, the sums), one row of 131,072 bf16 6.4.
-// Left: the row kept in shared memory and more threads (8,192 x 32,768 217 to 252), the mask's bytes
-// fetched into shared memory ahead (its L2 lines are: 1,001 x 50,257 98 without),
-// a cluster's statistics by copies that count on barriers of their own (4,096 x
-// 131,072 635).
+// a mask 8.1 (one round of rows, their terms, the sums), one row of 131,072 bf16 6.4 (forward
+// 4.6).  Forward alone 8,192 x 32,768 bf16 102 (78 %), with a mask 191 (62 %), 8,192 x 16,384
+// fp32 85 (93 %), 65,536 x 18 fp32 with a mask 4.2.  A gradient whose rows lie on other places of
+// 16 bytes than the logits' is stored by element: 8,192 x 32,768 bf16 from a pitch of 32,768 to
+// one of 32,769 883 us, to one of 32,776 178.
+// Left: the row kept in shared memory and more threads (8,192 x 32,768 217 to 252), a cluster's
+// statistics by copies that count on barriers of their own (4,096 x 131,072 635).  The mask's
+// L2 lines are fetched ahead (1,001 x 50,257 98 without), its bytes are not: in shared memory
+// they cost spills in a kernel that served rows with and without a mask, and have not been
+// tried since the two have kernels of their own.
 #include <algorithm>
 #include <cfloat>
 #include <math_constants.h>

@@ -331,7 +331,8 @@ cudaError_t few(const lin::Product& m, const Gate& g, cudaStream_t st) {
 }
 // bf16 in a graph, here / on the tensor cores: one row of 512 -> 2,048 2.7 us / 4.5, 3 rows
 // 3.2 / 4.5, 8 rows 4.5 / 4.6; of 4,096 -> 4,096, W not in L2, one row 18.2 / 14.9, two rows
-// 21.3 / 14.9.  Rows off 16-byte boundaries would have to be copied first for those.
+// 21.3 / 14.9.  Rows off 16-byte boundaries have to be copied first for those: of 1,397 -> 4,096
+// one row 18.2 here, 4 to 64 rows 15.1 to 17.4 with W copied (of 1,400 8.1 to 10.6).
 // (A pitch <= 0 stands for the row's length.)
 template <typename T>
 bool takes_few(int64_t M, int64_t N, int64_t K, int64_t ldx, int64_t ldw) {

@@ -5,8 +5,8 @@
 // the gate's W and the 64 of the other projection's for the same columns, its 16, 32,
 // 48 or 64 accumulator columns are x's rows, so that what it takes in by TMA is W and
 // little else (a tile of 128 rows of x would cost as much again, most of it
-// padding).  The sum is cut over the CTAs of a cluster, 1 to 8 of them, whatever fills
-// the GPU; each leaves its part in its shared memory, and after a cluster barrier each
+// padding).  The sum is cut over the 1, 2 or 4 CTAs of a cluster, whatever fills the
+// GPU; each leaves its part in its shared memory, and after a cluster barrier each
 // adds up its share of x's rows from all of them, in order, and finishes it: bias,
 // pre-activations, activation, product.
 //
